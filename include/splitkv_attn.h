@@ -118,7 +118,8 @@ const char* splitkv_last_error(void);
  * Read and clear the device error word of the current device (blocking: waits for all
  * work on the device).  *code = 0 if no kernel gave up a bounded wait, else a bitmask
  * (1: a consumer waited too long for a tile, 2: the loader waited too long for a free
- * stage, 4: a final drain waited too long).  Every wait in the kernels has a time limit.
+ * stage, 4: a final drain waited too long; 8: a position outside qk_norm_rope_append's
+ * tables).  Every wait in the kernels has a time limit.
  */
 skv_status splitkv_device_error(uint32_t* code);
 
@@ -370,6 +371,120 @@ skv_status gqa_decode_attn_passq(const skv_desc* desc, int32_t n_ranks, const vo
                                  const void* v_shards, const float* k_scale, const float* v_scale,
                                  const int32_t* shard_lens, void* out, float* lse, void* workspace,
                                  size_t workspace_bytes, void* stream);
+
+/*
+ * Ragged chunks of new tokens over a paged cache (no counterpart in the pages: what a server
+ * runs between them).  One packed batch holds every sequence's new tokens: prompt chunks of
+ * any length, proposed tokens, single decode tokens, side by side.  Both calls take the same
+ * three arrays, all in device memory and read by the kernels only, so that one captured graph
+ * serves any lengths:
+ *   cu_q       int32 [B + 1], non-decreasing, cu_q[0] >= 0: sequence b's new tokens are the
+ *              packed rows cu_q[b] .. cu_q[b + 1] (none allowed); rows at or past cu_q[B] and
+ *              before cu_q[0] belong to nobody and are left as they were
+ *   seq_lens   int32 [B]: tokens of sequence b in the cache, its new ones included
+ *   paged->block_table  as for the other paged calls
+ * Row i of sequence b with n new tokens sits at position seq_lens[b] - n + i.  The library clips
+ * what it reads: rows to [0, T), tokens to the max_blocks * block_len that a table row holds.
+ *
+ * A contiguous cache [B][Hkv][S][d] is the paged cache of one page per sequence (block_len = S,
+ * a multiple of 64; block_table[b] = b).
+ */
+
+/*
+ * attn_chunk_paged -- attention of every new token over its sequence's cached tokens, the new
+ * ones included (append them first).  The row at position p sees token t iff
+ *   t < seq_lens[b],  t <= p,  and  (window == 0  or  t > p - window  or  t < n_sink):
+ * causal, or with a sliding window of `window` tokens (the row's own counted) and the first
+ * n_sink tokens (sinks).  Pages whose tokens no row sees are not read: their table entries may
+ * be anything (a server hands back the pages behind the window).  Entries outside
+ * [0, num_blocks) read zeros.
+ *
+ *   q        bf16, packed [T][Hq][d] with desc->q_strides (token, head)
+ *   k_pages, v_pages, k_scale, v_scale  as for gqa_decode_attn_paged
+ *   out      bf16 [T][Hq][d] contiguous, 16-byte aligned;  lse  fp32 [T][Hq]: the natural log of
+ *            the softmax denominator, so that results merge (attn_merge_lse).  A row that sees
+ *            nothing (seq_lens[b] < n) gets out = 0, lse = -inf
+ *   workspace  attn_chunk_paged_workspace_size() bytes, 256-byte aligned
+ * desc->max_q_len bounds the sequences' new tokens (0: T): it chooses the kernel, the result
+ * does not depend on it.  Shapes: bf16 pages with d = 64 or 128, fp8-e4m3 pages with d = 128; any
+ * Hq multiple of Hkv.  A value that no row of a 64- or 128-token tile sees never counts, whatever
+ * it holds; a NaN or infinity in a V row that one row of a row tile sees may also reach the rows
+ * of that row tile that do not see it.
+ * Errors: SKV_EINVAL, SKV_EUNSUPPORTED and SKV_EWORKSPACE as for gqa_decode_attn_paged, and
+ * SKV_EINVAL for a softmax_scale that is not positive, a negative window or n_sink, and n_sink
+ * without a window.  T = 0 does nothing.
+ */
+typedef struct {
+  int32_t B;             /* sequences */
+  int32_t T;             /* packed rows */
+  int32_t Hq;            /* query heads, a multiple of Hkv */
+  int32_t Hkv;           /* KV heads */
+  int32_t d;             /* head dim of q, K and V */
+  int32_t window;        /* tokens that a row sees up to its own; 0: all */
+  int32_t n_sink;        /* first tokens seen besides the window */
+  int32_t max_q_len;     /* no sequence has more new tokens (0: T) */
+  float softmax_scale;   /* multiplies q.k, positive */
+  int32_t kv_dtype;      /* skv_kv_dtype */
+  int32_t scale_block;   /* fp8 only: tokens per scale block, a positive multiple of 64 */
+  int64_t q_strides[2];  /* q: element strides of (token, head); dim stride 1 */
+  int64_t k_strides[3];  /* k_pages: element strides of (page, KV head, token) */
+  int64_t v_strides[3];
+} skv_chunk_desc;
+
+skv_status attn_chunk_paged_workspace_size(const skv_chunk_desc* desc, const skv_paged* paged, size_t* bytes);
+skv_status attn_chunk_paged(const skv_chunk_desc* desc, const skv_paged* paged, const void* q, const void* k_pages,
+                            const void* v_pages, const float* k_scale, const float* v_scale, const int32_t* cu_q,
+                            const int32_t* seq_lens, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/*
+ * qk_norm_rope_append -- the new tokens on their way into the cache, in one pass: RMS norm of
+ * every query and key head, position rotation, queries to q_out, keys and values into their
+ * pages.  For a head x in R^d:
+ *   y = x * w / sqrt(mean(x^2) + eps)                                  (weight NULL: y = x)
+ *   (y_a, y_b) <- (y_a cos_j - y_b sin_j, y_b cos_j + y_a sin_j),  j < rot / 2,
+ *     (a, b) = (j, j + rot / 2), or (2j, 2j + 1) if interleaved      (rot = 0: no rotation)
+ * in fp32, rounded once at the store.
+ *
+ *   q, k, v    bf16, packed [T][H][d] with (token, head) strides, e.g. views of one fused
+ *              projection;  q_out bf16 with its own strides (q itself is allowed: in place)
+ *   q_weight, k_weight  [d] (stride 0) or one row per head (stride in elements), bf16 or fp32
+ *   cos, sin   fp32 [max_pos][rot / 2] contiguous
+ *   positions  int32 [T]: the rows of the tables, or NULL: each token's place in its sequence.
+ *              A position outside [0, max_pos) turns its token's queries and keys into NaN and
+ *              sets bit 8 of splitkv_device_error()
+ *   k_pages, v_pages  written at the token's place in its sequence, whatever `positions` says.
+ *              fp8: the code is e4m3(y / scale), saturated, by the scale that k_scale / v_scale
+ *              ([num_blocks][Hkv][block_len / scale_block]) hold for the block: scales are the
+ *              caller's (calibrated), never changed here; one that is not positive and finite
+ *              stores zeros.  A token whose place lies past max_blocks * block_len or before 0,
+ *              or whose table entry lies outside [0, num_blocks), is not stored (its query still
+ *              goes to q_out)
+ * Two rows that share a page row (a page listed for two sequences) must not be written by one
+ * call.  rot is a multiple of d / 8.  Shapes: as attn_chunk_paged.  Alignment: pointers 16 bytes,
+ * q / k / v / q_out strides multiples of 8 elements, page strides multiples of 16 bytes.
+ */
+typedef enum { SKV_WEIGHT_BF16 = 0, SKV_WEIGHT_FP32 = 1 } skv_weight_dtype;
+
+typedef struct {
+  int32_t B, T, Hq, Hkv, d;
+  int32_t rot;             /* rotated dims of each head, from the first; 0: none */
+  int32_t interleaved;     /* pairs (2j, 2j + 1) instead of (j, j + rot / 2) */
+  int32_t weight_dtype;    /* skv_weight_dtype of both weights */
+  int32_t kv_dtype;        /* skv_kv_dtype of the pages */
+  int32_t scale_block;     /* fp8 only */
+  float eps;
+  int64_t max_pos;         /* rows of cos and sin */
+  int64_t q_strides[2], k_strides[2], v_strides[2], q_out_strides[2];  /* (token, head) */
+  int64_t q_weight_stride, k_weight_stride;                            /* head; 0: shared */
+  int64_t k_page_strides[3], v_page_strides[3];                        /* (page, KV head, token) */
+} skv_append_desc;
+
+skv_status qk_norm_rope_append(const skv_append_desc* desc, const skv_paged* paged, const void* q, const void* k,
+                               const void* v, const void* q_weight, const void* k_weight, const float* cos,
+                               const float* sin, const int32_t* positions, const int32_t* cu_q,
+                               const int32_t* seq_lens, const float* k_scale, const float* v_scale, void* q_out,
+                               void* k_pages, void* v_pages, void* stream);
 
 #ifdef __cplusplus
 }

@@ -15,7 +15,11 @@ Entry points (same names as the C ABI):
   gqa_decode_attn(q, k_cache, v_cache, seq_lens, split_bounds, ...) -> (out, lse)
   gqa_decode_attn_noalloc(...) -> (out, lse)   (no workspace: the library's own scratch)
   gqa_decode_attn_passq(q, k_shards, v_shards, shard_lens, ...) -> (out, lse)
-plus the position-masked (_pos), paged (_paged) and pass-KV ring-step variants.
+plus the position-masked (_pos), paged (_paged) and pass-KV ring-step variants, and for
+ragged chunks of new tokens over a paged cache
+  qk_norm_rope_append(q, k, v, k_pages, v_pages, seq_lens, cu_q, block_table, ...) -> q_out
+  attn_chunk_paged(q, k_pages, v_pages, seq_lens, cu_q, block_table, ...) -> (out, lse)
+  (paged.chunk_step: both, from the fused projection's output)
 """
 
 import ctypes
@@ -33,6 +37,7 @@ LIB_PATH = os.path.join(_HERE, "libsplitkv_attn.so")
 
 SKV_OK, SKV_EINVAL, SKV_EUNSUPPORTED, SKV_ECUDA, SKV_EWORKSPACE = 0, -1, -2, -3, -4
 SKV_KV_BF16, SKV_KV_FP8_E4M3 = 0, 1
+SKV_WEIGHT_BF16, SKV_WEIGHT_FP32 = 0, 1
 _STATUS = {0: "SKV_OK", -1: "SKV_EINVAL", -2: "SKV_EUNSUPPORTED", -3: "SKV_ECUDA", -4: "SKV_EWORKSPACE"}
 
 # Every symbol declared in include/splitkv_attn.h.
@@ -57,6 +62,9 @@ EXPORTED_SYMBOLS = (
     "attn_ring_step",
     "gqa_decode_attn_passq_workspace_size",
     "gqa_decode_attn_passq",
+    "attn_chunk_paged_workspace_size",
+    "attn_chunk_paged",
+    "qk_norm_rope_append",
 )
 
 # Every symbol declared in include/splitkv_attn_selftest.h (hardware self-tests).
@@ -138,6 +146,13 @@ def _load():
     lib.gqa_decode_attn_passq_workspace_size.restype = I32
     lib.gqa_decode_attn_passq.argtypes = [D, I32, P, P, P, P, P, P, P, P, P, SZ, P]
     lib.gqa_decode_attn_passq.restype = I32
+    C, PG = ctypes.POINTER(SkvChunkDesc), ctypes.POINTER(SkvPaged)
+    lib.attn_chunk_paged_workspace_size.argtypes = [C, PG, ctypes.POINTER(SZ)]
+    lib.attn_chunk_paged_workspace_size.restype = I32
+    lib.attn_chunk_paged.argtypes = [C, PG] + [P] * 10 + [SZ, P]
+    lib.attn_chunk_paged.restype = I32
+    lib.qk_norm_rope_append.argtypes = [ctypes.POINTER(SkvAppendDesc), PG] + [P] * 16
+    lib.qk_norm_rope_append.restype = I32
     return lib
 
 
@@ -207,6 +222,33 @@ class SkvPaged(ctypes.Structure):
         ("max_blocks", ctypes.c_int32),
         ("num_blocks", ctypes.c_int64),
         ("block_table", ctypes.c_void_p),
+    ]
+
+
+class SkvChunkDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "Hq", "Hkv", "d", "window", "n_sink", "max_q_len")] + [
+        ("softmax_scale", ctypes.c_float),
+        ("kv_dtype", ctypes.c_int32),
+        ("scale_block", ctypes.c_int32),
+        ("q_strides", ctypes.c_int64 * 2),
+        ("k_strides", ctypes.c_int64 * 3),
+        ("v_strides", ctypes.c_int64 * 3),
+    ]
+
+
+class SkvAppendDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "Hq", "Hkv", "d", "rot", "interleaved", "weight_dtype",
+                                              "kv_dtype", "scale_block")] + [
+        ("eps", ctypes.c_float),
+        ("max_pos", ctypes.c_int64),
+        ("q_strides", ctypes.c_int64 * 2),
+        ("k_strides", ctypes.c_int64 * 2),
+        ("v_strides", ctypes.c_int64 * 2),
+        ("q_out_strides", ctypes.c_int64 * 2),
+        ("q_weight_stride", ctypes.c_int64),
+        ("k_weight_stride", ctypes.c_int64),
+        ("k_page_strides", ctypes.c_int64 * 3),
+        ("v_page_strides", ctypes.c_int64 * 3),
     ]
 
 
@@ -610,6 +652,135 @@ def gqa_decode_attn_passq(q, k_shards, v_shards, shard_lens, k_scale=None, v_sca
     return out, lse
 
 
+def _prep_chunk(d, q, k_pages, v_pages, seq_lens, cu_q, block_table, k_scale, v_scale, scale_block):
+    """What the two chunk calls share: q [T, Hq, d], pages [num_blocks, Hkv, block_len, d],
+    cu_q int32 [B + 1], seq_lens int32 [B], block_table int32 [B, max_blocks]; fills d's
+    common fields and returns the paged description."""
+    _require_cuda(k_pages, v_pages, seq_lens, cu_q, block_table, k_scale, v_scale)
+    _same_device(q.device, k_pages=k_pages, v_pages=v_pages, seq_lens=seq_lens, cu_q=cu_q, block_table=block_table,
+                 k_scale=k_scale, v_scale=v_scale)
+    if q.dim() != 3 or k_pages.dim() != 4 or v_pages.dim() != 4:
+        raise ValueError("q must be [T,Hq,d] and pages [num_blocks,Hkv,block_len,d]")
+    if q.dtype != torch.bfloat16:
+        raise ValueError("q must be bf16")
+    if q.stride(-1) != 1 or k_pages.stride(-1) != 1 or v_pages.stride(-1) != 1:
+        raise ValueError("the head dim must be unit-stride")
+    T, Hq, hd = q.shape
+    nb, Hkv, L, hd2 = k_pages.shape
+    if hd2 != hd or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
+        raise ValueError("q / k_pages / v_pages shapes or dtypes disagree")
+    if block_table.dtype != torch.int32 or not block_table.is_contiguous() or block_table.dim() != 2:
+        raise ValueError("block_table must be contiguous int32 [B, max_blocks]")
+    B = block_table.shape[0]
+    _check_lens(seq_lens, B, "seq_lens")
+    _check_lens(cu_q, B + 1, "cu_q")
+    d.B, d.T, d.Hq, d.Hkv, d.d = B, T, Hq, Hkv, hd
+    d.kv_dtype = _kv_dtype(k_pages)
+    d.scale_block = scale_block
+    if d.kv_dtype == SKV_KV_FP8_E4M3 and scale_block > 0:
+        _check_scales((k_scale, v_scale), (nb, Hkv, L // scale_block), "[num_blocks, Hkv, block_len / scale_block]")
+    for i in range(2):
+        d.q_strides[i] = q.stride(i)
+    pg = SkvPaged()
+    pg.block_len, pg.max_blocks, pg.num_blocks = L, block_table.shape[1], nb
+    pg.block_table = block_table.data_ptr()
+    return pg
+
+
+@_on_tensor_device
+def attn_chunk_paged(q, k_pages, v_pages, seq_lens, cu_q, block_table, max_q_len=None, window=0, n_sink=0,
+                     k_scale=None, v_scale=None, softmax_scale=None, scale_block=64, out=None, lse=None,
+                     workspace=None):
+    """Attention of ragged chunks of new tokens over a paged cache: q packed [T,Hq,d], rows
+    cu_q[b] .. cu_q[b+1] the last new tokens of sequence b's seq_lens[b] cached ones; causal, or
+    with a sliding window of ``window`` tokens and the first ``n_sink`` tokens.  max_q_len (the
+    longest chunk, if the caller knows it) chooses the kernel, not the result.  Returns (out
+    bf16 [T,Hq,d], lse fp32 [T,Hq]); rows of no sequence are left as they were."""
+    d = SkvChunkDesc()
+    pg = _prep_chunk(d, q, k_pages, v_pages, seq_lens, cu_q, block_table, k_scale, v_scale, scale_block)
+    d.window, d.n_sink, d.max_q_len = window, n_sink, max_q_len or 0
+    d.softmax_scale = softmax_scale if softmax_scale is not None else 1.0 / math.sqrt(d.d)
+    for i in range(3):
+        d.k_strides[i], d.v_strides[i] = k_pages.stride(i), v_pages.stride(i)
+    dev = q.device
+    out = _out(out, (d.T, d.Hq, d.d), torch.bfloat16, dev, "out")
+    lse = _out(lse, (d.T, d.Hq), torch.float32, dev, "lse")
+    nbytes = ctypes.c_size_t(0)
+    _check(_lib.attn_chunk_paged_workspace_size(ctypes.byref(d), ctypes.byref(pg), ctypes.byref(nbytes)))
+    if workspace is None:
+        # from torch's stream-ordered allocator at each call (in a capture: the graph's own
+        # pool), so that neither two streams nor two graphs share it
+        workspace, ws_bytes = torch.empty(nbytes.value, dtype=torch.uint8, device=dev), nbytes.value
+    else:
+        workspace, ws_bytes = _ws_arg(workspace, nbytes.value, dev)
+    _check(_lib.attn_chunk_paged(ctypes.byref(d), ctypes.byref(pg), _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale),
+                                 _ptr(v_scale), _ptr(cu_q), _ptr(seq_lens), _ptr(out), _ptr(lse), _ptr(workspace),
+                                 ws_bytes, _stream()))
+    return out, lse
+
+
+def _head_weight(w, heads, hd, dev, name):
+    """(pointer, head stride) of a norm weight [d] or [heads, d]."""
+    if w is None:
+        return None, 0
+    if w.device != dev or not w.is_contiguous() or tuple(w.shape) not in ((hd,), (heads, hd)):
+        raise ValueError(f"{name} must be a contiguous tensor [{hd}] or [{heads}, {hd}] on {dev}")
+    return w, hd if w.dim() == 2 else 0
+
+
+@_on_tensor_device
+def qk_norm_rope_append(q, k, v, k_pages, v_pages, seq_lens, cu_q, block_table, cos=None, sin=None, q_weight=None,
+                        k_weight=None, eps=1e-6, positions=None, interleaved=False, k_scale=None, v_scale=None,
+                        scale_block=64, q_out=None):
+    """The new tokens on their way into the cache: RMS norm of every query and key head
+    (weights [d] or [H,d], bf16 or fp32; None: no norm), rotation by the tables cos / sin fp32
+    [max_pos, rot/2] (None: none; halves, or interleaved pairs), keys and values into the pages
+    at each token's place in its sequence, queries to q_out (new, or the caller's strided bf16
+    [T,Hq,d], q itself included).  q / k / v are packed [T,H,d] views, e.g. of one fused
+    projection; positions int32 [T] replaces the place in the sequence as the tables' row; fp8
+    pages take codes by the scales already in k_scale / v_scale.  Returns q_out."""
+    d = SkvAppendDesc()
+    pg = _prep_chunk(d, q, k_pages, v_pages, seq_lens, cu_q, block_table, k_scale, v_scale, scale_block)
+    dev = q.device
+    _require_cuda(k, v, cos, sin, positions)
+    _same_device(dev, k=k, v=v, cos=cos, sin=sin, positions=positions, q_out=q_out)
+    for t, name in ((k, "k"), (v, "v")):
+        if t.dtype != torch.bfloat16 or tuple(t.shape) != (d.T, d.Hkv, d.d) or t.stride(-1) != 1:
+            raise ValueError(f"{name} must be bf16 [{d.T}, {d.Hkv}, {d.d}] with a unit-stride head dim")
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    if cos is not None:
+        for t, name in ((cos, "cos"), (sin, "sin")):
+            if t.dtype != torch.float32 or t.dim() != 2 or not t.is_contiguous() or t.shape != cos.shape:
+                raise ValueError(f"{name} must be contiguous float32 [max_pos, rot / 2]")
+        d.max_pos, d.rot = cos.shape[0], 2 * cos.shape[1]
+        if d.rot == 0:
+            raise ValueError("cos and sin have no columns: pass None for no rotation")
+    if positions is not None and (cos is None or positions.dtype != torch.int32 or not positions.is_contiguous()
+                                  or tuple(positions.shape) != (d.T,)):
+        raise ValueError(f"positions must be contiguous int32 of shape ({d.T},), with cos and sin")
+    qw, d.q_weight_stride = _head_weight(q_weight, d.Hq, d.d, dev, "q_weight")
+    kw, d.k_weight_stride = _head_weight(k_weight, d.Hkv, d.d, dev, "k_weight")
+    kinds = {w.dtype for w in (qw, kw) if w is not None}
+    if len(kinds) > 1 or not kinds <= {torch.bfloat16, torch.float32}:
+        raise ValueError("q_weight and k_weight must both be bf16 or both float32")
+    d.weight_dtype = SKV_WEIGHT_FP32 if kinds == {torch.float32} else SKV_WEIGHT_BF16
+    if q_out is None:
+        q_out = torch.empty((d.T, d.Hq, d.d), dtype=torch.bfloat16, device=dev)
+    elif q_out.dtype != torch.bfloat16 or q_out.shape != q.shape or q_out.stride(-1) != 1:
+        raise ValueError(f"q_out must be bf16 {tuple(q.shape)} with a unit-stride head dim")
+    d.eps = eps
+    d.interleaved = 1 if interleaved else 0
+    for i in range(2):
+        d.k_strides[i], d.v_strides[i], d.q_out_strides[i] = k.stride(i), v.stride(i), q_out.stride(i)
+    for i in range(3):
+        d.k_page_strides[i], d.v_page_strides[i] = k_pages.stride(i), v_pages.stride(i)
+    _check(_lib.qk_norm_rope_append(ctypes.byref(d), ctypes.byref(pg), _ptr(q), _ptr(k), _ptr(v), _ptr(qw), _ptr(kw),
+                                    _ptr(cos), _ptr(sin), _ptr(positions), _ptr(cu_q), _ptr(seq_lens), _ptr(k_scale),
+                                    _ptr(v_scale), _ptr(q_out), _ptr(k_pages), _ptr(v_pages), _stream()))
+    return q_out
+
+
 def kernel_timing(enable):
     """Start (True: clears the record) or stop recording the attention kernels' own device time."""
     _check(_lib.splitkv_kernel_timing(1 if enable else 0))
@@ -628,6 +799,8 @@ __all__ = [
     "kernel_timing_read",
     "attn_ring_step",
     "gqa_decode_attn_passq",
+    "qk_norm_rope_append",
+    "attn_chunk_paged",
     "attn_partial",
     "attn_partial_paged",
     "gqa_decode_attn_paged",
@@ -642,6 +815,9 @@ __all__ = [
     "version",
     "SplitKVError",
     "SkvDesc",
+    "SkvPaged",
+    "SkvChunkDesc",
+    "SkvAppendDesc",
     "LIB_PATH",
     "load_library",
     "EXPORTED_SYMBOLS",

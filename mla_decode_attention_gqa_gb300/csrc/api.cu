@@ -1015,3 +1015,241 @@ skv_status gqa_decode_attn_passq(const skv_desc* desc, int32_t n_ranks, const vo
 }
 
 }  // extern "C"
+
+// ------------------------------------------------------------------ ragged chunks over pages
+
+namespace {
+
+// A chunk call's shape as the description the shared checks and tensor maps take.
+skv_status chunk_desc(const skv_chunk_desc* c, const skv_paged* pg, skv_desc* d) {
+  if (!c) return fail(SKV_EINVAL, "desc is NULL");
+  if (!pg) return fail(SKV_EINVAL, "paged is NULL");
+  if (c->T < 0) return fail(SKV_EINVAL, "T must not be negative");
+  if (pg->max_blocks <= 0 || pg->block_len <= 0) return fail(SKV_EINVAL, "max_blocks and block_len must be positive");
+  std::memset(d, 0, sizeof(*d));
+  d->B = c->B;
+  d->Tq = 1;
+  d->Hq = c->Hq;
+  d->Hkv = c->Hkv;
+  d->dk = d->dv = c->d;
+  d->S_max = static_cast<int64_t>(pg->max_blocks) * pg->block_len;
+  d->softmax_scale = c->softmax_scale;
+  d->kv_dtype = c->kv_dtype;
+  d->scale_block = c->scale_block;
+  d->q_strides[1] = c->q_strides[0];
+  d->q_strides[2] = c->q_strides[1];
+  for (int i = 0; i < 3; ++i) {
+    d->k_strides[i] = c->k_strides[i];
+    d->v_strides[i] = c->v_strides[i];
+  }
+  skv_status st = validate(d, 1);
+  if (st != SKV_OK) return st;
+  return validate_paged(d, pg);
+}
+
+struct ChunkPlan {
+  GqaVariant variant;
+  int rows = 0;            // rows of a row tile
+  int64_t n_wave = 0;      // work items resident at once
+  int64_t n_target = 0;    // most items of sequences with several chunks
+  int64_t n_items = 0;     // blocks: an upper bound of the work items
+  int64_t part_rows = 0;   // an upper bound of the partial rows
+  size_t plan_bytes = 0, o_bytes = 0, lse_bytes = 0;
+};
+
+skv_status chunk_plan(const skv_chunk_desc* c, const skv_desc* d, ChunkPlan* pl) {
+  const int G = d->Hq / d->Hkv;
+  // the caller's bound on the chunk lengths chooses the row tile (results do not depend on it)
+  const int64_t longest = c->max_q_len > 0 ? std::min(c->max_q_len, c->T) : c->T;
+  const bool few = longest * G <= 16;
+  if (d->kv_dtype == SKV_KV_FP8_E4M3)
+    pl->variant = few ? GqaVariant::kFp8D128Decode : GqaVariant::kFp8D128Prefill;
+  else if (d->dk == 64)
+    pl->variant = few ? GqaVariant::kBf16D64Decode : GqaVariant::kBf16D64Prefill;
+  else
+    pl->variant = few ? GqaVariant::kBf16D128Decode : GqaVariant::kBf16D128Prefill;
+  const GqaLaunchInfo li = gqa_launch_info(pl->variant);
+  pl->rows = li.rows_per_cta;
+  pl->n_wave = static_cast<int64_t>(device_sm_count()) * li.ctas_per_sm;
+  pl->n_target = 4 * pl->n_wave;
+  const int64_t rows = static_cast<int64_t>(c->T) * G;
+  const int64_t row_tiles = rows / pl->rows + std::min(c->B, c->T);  // each sequence's last one may be short
+  pl->n_items = row_tiles * d->Hkv + pl->n_target;
+  if (pl->n_items >= (int64_t(1) << 31)) return fail(SKV_EINVAL, "T * Hq is too large for one call");
+  pl->part_rows = pl->n_target * std::min<int64_t>(pl->rows, rows);
+  pl->plan_bytes = align_up((3 * static_cast<size_t>(c->B) + 1) * 4, 256);
+  pl->o_bytes = align_up(static_cast<size_t>(pl->part_rows) * d->dv * 4, 256);
+  pl->lse_bytes = align_up(static_cast<size_t>(pl->part_rows) * 4, 256);
+  return SKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+skv_status attn_chunk_paged_workspace_size(const skv_chunk_desc* desc, const skv_paged* paged, size_t* bytes) {
+  if (!bytes) return fail(SKV_EINVAL, "bytes is NULL");
+  skv_desc d;
+  skv_status st = chunk_desc(desc, paged, &d);
+  if (st != SKV_OK) return st;
+  ChunkPlan pl;
+  if ((st = chunk_plan(desc, &d, &pl)) != SKV_OK) return st;
+  *bytes = desc->T == 0 ? 0 : pl.plan_bytes + pl.o_bytes + pl.lse_bytes;
+  return SKV_OK;
+}
+
+skv_status attn_chunk_paged(const skv_chunk_desc* desc, const skv_paged* paged, const void* q, const void* k_pages,
+                            const void* v_pages, const float* k_scale, const float* v_scale, const int32_t* cu_q,
+                            const int32_t* seq_lens, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  skv_desc d;
+  skv_status st = chunk_desc(desc, paged, &d);
+  if (st != SKV_OK) return st;
+  if (d.softmax_scale < 0.f) return fail(SKV_EINVAL, "softmax_scale must be positive");
+  if (desc->window < 0 || desc->n_sink < 0) return fail(SKV_EINVAL, "window and n_sink must not be negative");
+  if (desc->n_sink > 0 && desc->window == 0) return fail(SKV_EINVAL, "n_sink needs a window (window > 0)");
+  if (desc->T == 0) return SKV_OK;
+  if ((st = validate_ptrs(&d, q, k_pages, v_pages, k_scale, v_scale, seq_lens)) != SKV_OK) return st;
+  if (!cu_q || !aligned(cu_q, 4)) return fail(SKV_EINVAL, "cu_q NULL or misaligned");
+  if (!out || !lse) return fail(SKV_EINVAL, "out and lse must be non-NULL");
+  if (!aligned(out, 16) || !aligned(lse, 4)) return fail(SKV_EINVAL, "out must be 16-byte, lse 4-byte aligned");
+  ChunkPlan pl;
+  if ((st = chunk_plan(desc, &d, &pl)) != SKV_OK) return st;
+  if (!workspace || workspace_bytes < pl.plan_bytes + pl.o_bytes + pl.lse_bytes || !aligned(workspace, 256))
+    return fail(SKV_EWORKSPACE, "workspace missing, misaligned or smaller than attn_chunk_paged_workspace_size()");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  float* part_o = reinterpret_cast<float*>(ws + pl.plan_bytes);
+  float* part_lse = reinterpret_cast<float*>(ws + pl.plan_bytes + pl.o_bytes);
+  PartialParams p;
+  Plan unused;
+  st = fill_params(&p, &d, unused, q, k_scale, v_scale, seq_lens, nullptr, 1, 0, nullptr, nullptr, paged, part_o,
+                   part_lse, false);
+  if (st != SKV_OK) return st;
+  p.ck.cu_q = cu_q;
+  p.ck.seq_lens = seq_lens;
+  p.ck.B = d.B;
+  p.ck.T = desc->T;
+  p.ck.Hkv = d.Hkv;
+  p.ck.G = d.Hq / d.Hkv;
+  p.ck.cap = static_cast<int32_t>(d.S_max);
+  p.ck.window = desc->window;
+  p.ck.n_sink = desc->n_sink;
+  p.ck.rows = pl.rows;
+  p.ck.tile = kTileN;
+  p.ck.n_wave = static_cast<int32_t>(pl.n_wave);
+  p.ck.n_target = static_cast<int32_t>(pl.n_target);
+  p.ck.plan = reinterpret_cast<int32_t*>(ws);
+  p.ck.out = out;
+  p.ck.lse = lse;
+  CUtensorMap tmk, tmv;
+  if ((st = encode_kv_map(&tmk, k_pages, &d, d.k_strides, d.dk, kTileN, paged)) != SKV_OK) return st;
+  if ((st = encode_kv_map(&tmv, v_pages, &d, d.v_strides, d.dv, kTileN, paged)) != SKV_OK) return st;
+  cudaError_t e = timing_mark(false, s);
+  if (e == cudaSuccess) e = launch_gqa_chunk(pl.variant, p, tmk, tmv, pl.n_items, s);
+  if (e == cudaSuccess) e = timing_mark(true, s);
+  if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
+  // rows that can be in several chunks: no more than a partial row each
+  const int64_t rows = std::min<int64_t>(static_cast<int64_t>(desc->T) * d.Hq, pl.part_rows);
+  e = launch_chunk_merge(p.ck, d.dv, part_o, part_lse, rows, s);
+  if (e != cudaSuccess) return cuda_fail(e, "chunk merge launch");
+  return SKV_OK;
+}
+
+skv_status qk_norm_rope_append(const skv_append_desc* desc, const skv_paged* paged, const void* q, const void* k,
+                               const void* v, const void* q_weight, const void* k_weight, const float* cos,
+                               const float* sin, const int32_t* positions, const int32_t* cu_q,
+                               const int32_t* seq_lens, const float* k_scale, const float* v_scale, void* q_out,
+                               void* k_pages, void* v_pages, void* stream) {
+  if (!desc) return fail(SKV_EINVAL, "desc is NULL");
+  // the pages' description, checked as the attention calls check it
+  skv_chunk_desc c;
+  std::memset(&c, 0, sizeof(c));
+  c.B = desc->B;
+  c.T = desc->T;
+  c.Hq = desc->Hq;
+  c.Hkv = desc->Hkv;
+  c.d = desc->d;
+  c.softmax_scale = 1.f;
+  c.kv_dtype = desc->kv_dtype;
+  c.scale_block = desc->scale_block;
+  for (int i = 0; i < 2; ++i) c.q_strides[i] = desc->q_strides[i];
+  for (int i = 0; i < 3; ++i) {
+    c.k_strides[i] = desc->k_page_strides[i];
+    c.v_strides[i] = desc->v_page_strides[i];
+  }
+  skv_desc d;
+  skv_status st = chunk_desc(&c, paged, &d);
+  if (st != SKV_OK) return st;
+  for (int i = 0; i < 2; ++i) {
+    const int64_t all[3] = {desc->k_strides[i], desc->v_strides[i], desc->q_out_strides[i]};
+    for (int64_t x : all)
+      if (x < 0 || x % 8) return fail(SKV_EINVAL, "k, v and q_out strides must be non-negative multiples of 8 elements");
+  }
+  if (desc->q_out_strides[1] < desc->d && desc->Hq > 1)
+    return fail(SKV_EINVAL, "q_out head stride must cover a whole head row");
+  if (!std::isfinite(desc->eps) || desc->eps < 0.f) return fail(SKV_EINVAL, "eps must be finite and not negative");
+  const int step = desc->d / 8;  // a lane turns d / 16 values and its partner as many
+  if (desc->rot < 0 || desc->rot > desc->d || desc->rot % step) {
+    char buf[120];
+    snprintf(buf, sizeof buf, "rot must be a multiple of %d in [0, %d]", step, desc->d);
+    return fail(SKV_EINVAL, buf);
+  }
+  if (desc->rot > 0 && (!cos || !sin || desc->max_pos <= 0))
+    return fail(SKV_EINVAL, "a rotation needs cos and sin tables of at least one position");
+  if (!aligned(cos, 16) || !aligned(sin, 16) || !aligned(positions, 4))
+    return fail(SKV_EINVAL, "cos and sin must be 16-byte, positions 4-byte aligned");
+  if (desc->weight_dtype != SKV_WEIGHT_BF16 && desc->weight_dtype != SKV_WEIGHT_FP32)
+    return fail(SKV_EINVAL, "unknown weight_dtype");
+  if (!aligned(q_weight, 16) || !aligned(k_weight, 16)) return fail(SKV_EINVAL, "weights must be 16-byte aligned");
+  if (desc->q_weight_stride < 0 || desc->k_weight_stride < 0 || desc->q_weight_stride % 8 || desc->k_weight_stride % 8)
+    return fail(SKV_EINVAL, "weight strides must be non-negative multiples of 8 elements");
+  if (desc->T == 0) return SKV_OK;
+  if (!q || !k || !v || !q_out || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16))
+    return fail(SKV_EINVAL, "q, k, v and q_out must be non-NULL and 16-byte aligned");
+  if (!cu_q || !aligned(cu_q, 4)) return fail(SKV_EINVAL, "cu_q NULL or misaligned");
+  if ((st = validate_ptrs(&d, q, k_pages, v_pages, k_scale, v_scale, seq_lens)) != SKV_OK) return st;
+  AppendArgs a;
+  std::memset(&a, 0, sizeof(a));
+  cudaError_t e;
+  a.err = device_error_word(&e);
+  if (!a.err) return cuda_fail(e, "device error word");
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  a.q_st = desc->q_strides[0], a.q_sh = desc->q_strides[1];
+  a.k_st = desc->k_strides[0], a.k_sh = desc->k_strides[1];
+  a.v_st = desc->v_strides[0], a.v_sh = desc->v_strides[1];
+  a.o_st = desc->q_out_strides[0], a.o_sh = desc->q_out_strides[1];
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.q_weight_sh = desc->q_weight_stride;
+  a.k_weight_sh = desc->k_weight_stride;
+  a.weight_bf16 = desc->weight_dtype == SKV_WEIGHT_BF16 ? 1 : 0;
+  a.cos = cos;
+  a.sin = sin;
+  a.positions = positions;
+  a.max_pos = desc->max_pos;
+  a.cu_q = cu_q;
+  a.seq_lens = seq_lens;
+  a.block_table = paged->block_table;
+  a.k_pages = k_pages;
+  a.v_pages = v_pages;
+  a.kp_sb = d.k_strides[0], a.kp_sh = d.k_strides[1], a.kp_st = d.k_strides[2];
+  a.vp_sb = d.v_strides[0], a.vp_sh = d.v_strides[1], a.vp_st = d.v_strides[2];
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.num_blocks = paged->num_blocks;
+  a.B = d.B, a.T = desc->T, a.Hq = d.Hq, a.Hkv = d.Hkv, a.rot = desc->rot;
+  a.interleaved = desc->interleaved ? 1 : 0;
+  a.block_len = paged->block_len;
+  a.max_blocks = paged->max_blocks;
+  a.scale_block = d.kv_dtype == SKV_KV_FP8_E4M3 ? d.scale_block : kTileN;
+  a.eps = desc->eps;
+  e = launch_append(a, desc->d, d.kv_dtype == SKV_KV_FP8_E4M3, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "append launch");
+  return SKV_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,183 @@
+// Joins the partial rows of attention over ragged chunks (attn_chunk_paged): the rows of the
+// sequences whose KV tiles were dealt to several chunks.
+//
+// For every such row, with k partials (o_c, lse_c): m = max lse_c, w_c = exp(lse_c - m),
+// out = sum w_c o_c / sum w_c in bf16, lse = m + ln sum w_c; all partials empty: out = 0,
+// lse = -inf.  The work table (first row to merge, first partial row and k of each sequence)
+// was written by block 0 of the attention kernel before it.
+//
+// Bound by the partials' bytes, which are mostly still in L2; what counts is how many loads
+// are in flight.  A block takes 8 rows: one warp each while k <= 16 (all partials of a row in
+// two batches of 8 loads), else one row after the other with the partials dealt to the 8
+// warps, so that a single long sequence (hundreds of partials for a few rows) is not left to
+// a few warps.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include "skv_internal.h"
+
+namespace skv {
+
+namespace {
+
+constexpr int kRowsPerBlock = 8;
+constexpr int kWarpParts = 16;
+constexpr int kBatch = 8;
+
+// Running merge of one row's partials: this lane's 4 columns.
+struct Joined {
+  float m = -INFINITY, den = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+};
+
+// Partials first, first + step, .. below k; lse0 / o0: partial 0 of the row, `stride` rows apart.
+template <int D>
+__device__ __forceinline__ Joined join(const float* lse0, const float* o0, int64_t stride, int first, int step, int k,
+                                       int lane) {
+  Joined j;
+  for (int c = first + lane * step; c < k; c += 32 * step) j.m = fmaxf(j.m, lse0[c * stride]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) j.m = fmaxf(j.m, __shfl_xor_sync(0xffffffffu, j.m, o));
+  if (j.m == -INFINITY) return j;
+  for (int c0 = first; c0 < k; c0 += kBatch * step) {
+    float w[kBatch];
+    float4 x[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int c = c0 + u * step;
+      const float l = c < k ? lse0[c * stride] : -INFINITY;
+      w[u] = l == -INFINITY ? 0.f : __expf(l - j.m);  // an empty partial's o was never written
+      x[u] = (l != -INFINITY && 4 * lane < D) ? *reinterpret_cast<const float4*>(o0 + c * stride * D + 4 * lane)
+                                              : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      j.den += w[u];
+      j.acc.x += w[u] * x[u].x;
+      j.acc.y += w[u] * x[u].y;
+      j.acc.z += w[u] * x[u].z;
+      j.acc.w += w[u] * x[u].w;
+    }
+  }
+  return j;
+}
+
+template <int D>
+__device__ __forceinline__ void store_row(const ChunkArgs& a, int64_t row, const Joined& j, int lane) {
+  const float inv = j.den > 0.f ? 1.f / j.den : 0.f;
+  if (4 * lane < D) {
+    __nv_bfloat162 lo = __floats2bfloat162_rn(j.acc.x * inv, j.acc.y * inv);
+    __nv_bfloat162 hi = __floats2bfloat162_rn(j.acc.z * inv, j.acc.w * inv);
+    uint2 u;
+    u.x = *reinterpret_cast<uint32_t*>(&lo);
+    u.y = *reinterpret_cast<uint32_t*>(&hi);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * D + 4 * lane) = u;
+  }
+  if (lane == 0) a.lse[row] = j.den > 0.f ? j.m + logf(j.den) : -INFINITY;
+}
+
+template <int D>
+__global__ void __launch_bounds__(32 * kRowsPerBlock)
+    chunk_merge_kernel(const __grid_constant__ ChunkArgs a, const float* part_o, const float* part_lse) {
+  __shared__ int sm_parts[kRowsPerBlock], sm_n[kRowsPerBlock];
+  __shared__ int64_t sm_row[kRowsPerBlock], sm_part[kRowsPerBlock];
+  __shared__ float sm_m[kRowsPerBlock], sm_den[kRowsPerBlock];
+  __shared__ float4 sm_acc[kRowsPerBlock][D / 4];
+  // the attention kernel before it on the stream is complete and its writes are visible
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int Hq = a.Hkv * a.G;
+  const int rows = a.plan[3 * a.B];
+  for (int r0 = blockIdx.x * kRowsPerBlock; r0 < rows; r0 += gridDim.x * kRowsPerBlock) {
+    const int r = r0 + warp;
+    __syncthreads();  // the tables' earlier readers are done
+    if (lane == 0) {
+      int k = 0, n = 0;
+      int64_t row = 0, part = 0;
+      if (r < rows) {
+        int lo = 0, hi = a.B - 1;  // the last sequence whose first row is <= r
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (a.plan[3 * mid] <= r) lo = mid; else hi = mid - 1;
+        }
+        // sequences without rows to merge share the first row of the one after them
+        const int in = r - a.plan[3 * lo];
+        const int row0 = min(max(__ldg(a.cu_q + lo), 0), a.T);
+        n = max(min(max(__ldg(a.cu_q + lo + 1), 0), a.T) - row0, 0);
+        k = a.plan[3 * lo + 2];
+        row = static_cast<int64_t>(row0) * Hq + in;
+        part = static_cast<int64_t>(a.plan[3 * lo + 1]) + in;
+      }
+      sm_parts[warp] = k;
+      sm_n[warp] = n;
+      sm_row[warp] = row;
+      sm_part[warp] = part;
+    }
+    __syncthreads();
+    int most = 0;
+#pragma unroll
+    for (int w = 0; w < kRowsPerBlock; ++w) most = max(most, sm_parts[w]);
+    if (most <= kWarpParts) {
+      if (r < rows) {
+        const int64_t stride = static_cast<int64_t>(sm_n[warp]) * Hq;
+        const Joined j = join<D>(part_lse + sm_part[warp], part_o + sm_part[warp] * D, stride, 0, 1, sm_parts[warp], lane);
+        store_row<D>(a, sm_row[warp], j, lane);
+      }
+      continue;
+    }
+    for (int w = 0; w < kRowsPerBlock && r0 + w < rows; ++w) {
+      const int64_t stride = static_cast<int64_t>(sm_n[w]) * Hq;
+      const Joined j = join<D>(part_lse + sm_part[w], part_o + sm_part[w] * D, stride, warp, kRowsPerBlock, sm_parts[w],
+                               lane);
+      __syncthreads();  // the previous row's sums were read
+      if (lane == 0) {
+        sm_m[warp] = j.m;
+        sm_den[warp] = j.den;
+      }
+      if (4 * lane < D) sm_acc[warp][lane] = j.acc;
+      __syncthreads();
+      if (warp == w) {
+        Joined s;
+#pragma unroll
+        for (int v = 0; v < kRowsPerBlock; ++v) s.m = fmaxf(s.m, sm_m[v]);
+#pragma unroll
+        for (int v = 0; v < kRowsPerBlock; ++v) {
+          const float f = sm_m[v] == -INFINITY ? 0.f : __expf(sm_m[v] - s.m);
+          s.den += f * sm_den[v];
+          if (4 * lane < D) {
+            const float4 x = sm_acc[v][lane];
+            s.acc.x += f * x.x;
+            s.acc.y += f * x.y;
+            s.acc.z += f * x.z;
+            s.acc.w += f * x.w;
+          }
+        }
+        store_row<D>(a, sm_row[w], s, lane);
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_merge(const ChunkArgs& a, int32_t d, const float* part_o, const float* part_lse,
+                               int64_t max_rows, cudaStream_t stream) {
+  if (max_rows <= 0) return cudaSuccess;
+  // programmatic dependent launch, as the merge of equal splits (merge_lse.cu)
+  cudaLaunchConfig_t cfg = {};
+  // blocks beyond a few waves would only find the row count already passed
+  const int64_t blocks = (max_rows + kRowsPerBlock - 1) / kRowsPerBlock;
+  cfg.gridDim = dim3(static_cast<unsigned int>(blocks < 1216 ? blocks : 1216));
+  cfg.blockDim = dim3(32 * kRowsPerBlock);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (d == 64) return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<64>, a, part_o, part_lse);
+  return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<128>, a, part_o, part_lse);
+}
+
+}  // namespace skv

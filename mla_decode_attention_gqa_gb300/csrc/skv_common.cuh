@@ -18,6 +18,7 @@ enum DevError : unsigned int {
   kDevErrFullWait = 1u,   // a consumer gave up waiting for a TMA tile
   kDevErrEmptyWait = 2u,  // the producer gave up waiting for a free stage
   kDevErrDrainWait = 4u,  // the final drain of in-flight copies gave up
+  kDevErrPosition = 8u,   // a token's position lies outside the rotation tables
 };
 
 // Time limit of every spin-wait in the library's kernels, in SM clock cycles (the

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -26,6 +27,26 @@ cudaError_t once_per_device(std::atomic<uint64_t>& done, F&& set) {
   if (e == cudaSuccess && bit) done.fetch_or(bit, std::memory_order_acq_rel);
   return e;
 }
+
+// Parameters of attention over ragged chunks of new tokens (attn_chunk_paged; see
+// chunk_plan.cuh for the work decomposition).
+struct ChunkArgs {
+  const int32_t* cu_q;      // device [B + 1]: first packed row of each sequence
+  const int32_t* seq_lens;  // device [B]: cached tokens with the new ones
+  int32_t B, T, Hkv, G;
+  int32_t cap;      // tokens a block-table row can hold
+  int32_t window;   // tokens a row sees up to its own (0: all)
+  int32_t n_sink;   // first tokens seen besides the window
+  int32_t rows;     // rows (token, head of the group) of one row tile
+  int32_t tile;     // tokens of one KV tile
+  int32_t n_wave;   // work items resident at once
+  int32_t n_target; // most work items with several chunks per row tile
+  int32_t* plan;    // device [3 B + 1], written by block 0 for the merge
+  void* out;        // bf16 [T][Hq][d]
+  float* lse;       // fp32 [T][Hq]
+};
+// At most so many KV tiles for each resident work item are dealt out as a single wave.
+constexpr int kChunkShortTiles = 8;
 
 // Parameters of one split-KV partial-attention launch.
 //
@@ -66,6 +87,7 @@ struct PartialParams {
   int32_t ring_n;      // pass-Q ring: ranks (0: off) and query rows each rank owns; B then
   int32_t ring_bq;     //   counts ring_n * ring_n * ring_bq work rows (rank, step, slot)
   const int32_t* bounds;  // device [B][n_split + 1], or NULL: one split [0, S_max) per row
+  ChunkArgs ck;  // ragged chunks only: replaces Tq, bounds, n_split, n_chunk and m_tiles
 };
 
 #ifdef __CUDACC__
@@ -123,6 +145,42 @@ GqaLaunchInfo gqa_launch_info(GqaVariant v);
 
 cudaError_t launch_gqa_partial(GqaVariant v, const PartialParams& p, const CUtensorMap& tmk,
                                const CUtensorMap& tmv, int64_t n_items, cudaStream_t stream);
+// The same tiles over ragged chunks (p.ck): items with one chunk write p.ck.out / p.ck.lse,
+// the others partial rows to p.out_o / p.out_lse, which launch_chunk_merge joins.
+cudaError_t launch_gqa_chunk(GqaVariant v, const PartialParams& p, const CUtensorMap& tmk, const CUtensorMap& tmv,
+                             int64_t n_items, cudaStream_t stream);
+cudaError_t launch_chunk_merge(const ChunkArgs& a, int32_t d, const float* part_o, const float* part_lse,
+                               int64_t max_rows, cudaStream_t stream);
+
+// Norm, rotation and append of new tokens (see qk_norm_rope.cu).  Strides in elements.
+struct AppendArgs {
+  const __nv_bfloat16* q;  // [T][Hq][d]: token and head strides
+  const __nv_bfloat16* k;  // [T][Hkv][d]
+  const __nv_bfloat16* v;
+  __nv_bfloat16* q_out;
+  int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh, o_st, o_sh;
+  const void* q_weight;  // [d] (head stride 0) or [H][d]; NULL: no norm
+  const void* k_weight;
+  int64_t q_weight_sh, k_weight_sh;
+  const float* cos;  // [max_pos][rot / 2]
+  const float* sin;
+  const int32_t* positions;  // [T], or NULL: the token's place in its sequence
+  int64_t max_pos;
+  const int32_t* cu_q;         // [B + 1]
+  const int32_t* seq_lens;     // [B]
+  const int32_t* block_table;  // [B][max_blocks]
+  void* k_pages;
+  void* v_pages;
+  int64_t kp_sb, kp_sh, kp_st, vp_sb, vp_sh, vp_st;  // page, head, token
+  const float* k_scale;  // fp8: [num_blocks][Hkv][block_len / scale_block]
+  const float* v_scale;
+  int64_t num_blocks;
+  int32_t B, T, Hq, Hkv, rot, interleaved, weight_bf16;
+  int32_t block_len, max_blocks, scale_block;
+  float eps;
+  unsigned int* err;
+};
+cudaError_t launch_append(const AppendArgs& a, int32_t d, bool fp8, cudaStream_t stream);
 
 // MLA latent variant (dk = 576 latent+rope, dv = 512, one shared latent "head").
 // Tiles are 32 tokens; the tensor map's box is 64 elements x 32 tokens.

@@ -1,0 +1,184 @@
+"""What the chunk calls refuse, on the host and before any launch, through the C ABI and the
+binding; and the rotation tables."""
+
+import ctypes
+import math
+
+import pytest
+import torch
+
+import mla_decode_attention_gqa_gb300 as skv
+from mla_decode_attention_gqa_gb300 import paged
+
+FAKE = ctypes.c_void_p(0x10000)  # never dereferenced: validation fails first
+
+
+def _paged(**kw):
+    pg = skv.SkvPaged()
+    pg.block_len, pg.max_blocks, pg.num_blocks, pg.block_table = 64, 16, 100, 0x10000
+    for k, v in kw.items():
+        setattr(pg, k, v)
+    return pg
+
+
+def _set(d, kw):
+    for k, v in kw.items():
+        if isinstance(v, tuple):
+            for i, x in enumerate(v):
+                getattr(d, k)[i] = x
+        else:
+            setattr(d, k, v)
+    return d
+
+
+def _chunk(**kw):
+    d = skv.SkvChunkDesc()
+    base = dict(B=3, T=10, Hq=16, Hkv=4, d=128, softmax_scale=0.088, scale_block=64, q_strides=(16 * 128, 128),
+                k_strides=(4 * 64 * 128, 64 * 128, 128), v_strides=(4 * 64 * 128, 64 * 128, 128))
+    return _set(_set(d, base), kw)
+
+
+def _append(**kw):
+    d = skv.SkvAppendDesc()
+    base = dict(B=3, T=10, Hq=16, Hkv=4, d=128, rot=128, max_pos=1024, scale_block=64, eps=1e-6, q_strides=(24 * 128, 128),
+                k_strides=(24 * 128, 128), v_strides=(24 * 128, 128), q_out_strides=(16 * 128, 128),
+                k_page_strides=(4 * 64 * 128, 64 * 128, 128), v_page_strides=(4 * 64 * 128, 64 * 128, 128))
+    return _set(_set(d, base), kw)
+
+
+def _call_chunk(d, pg=None, ws_bytes=0, **ptr):
+    lib = skv.load_library()
+    p = dict(q=FAKE, k=FAKE, v=FAKE, ks=None, vs=None, cu=FAKE, seq=FAKE, out=FAKE, lse=FAKE, ws=None)
+    p.update(ptr)
+    return lib.attn_chunk_paged(ctypes.byref(d), ctypes.byref(pg or _paged()), p["q"], p["k"], p["v"], p["ks"], p["vs"],
+                                p["cu"], p["seq"], p["out"], p["lse"], p["ws"], ws_bytes, None)
+
+
+def _call_append(d, pg=None, **ptr):
+    lib = skv.load_library()
+    p = dict(q=FAKE, k=FAKE, v=FAKE, qw=FAKE, kw=FAKE, cos=FAKE, sin=FAKE, pos=None, cu=FAKE, seq=FAKE, ks=None, vs=None,
+             out=FAKE, kp=FAKE, vp=FAKE)
+    p.update(ptr)
+    return lib.qk_norm_rope_append(ctypes.byref(d), ctypes.byref(pg or _paged()), p["q"], p["k"], p["v"], p["qw"], p["kw"],
+                                   p["cos"], p["sin"], p["pos"], p["cu"], p["seq"], p["ks"], p["vs"], p["out"], p["kp"],
+                                   p["vp"], None)
+
+
+SHARED = [
+    (dict(B=0), skv.SKV_EINVAL),
+    (dict(T=-1), skv.SKV_EINVAL),
+    (dict(Hq=15), skv.SKV_EINVAL),
+    (dict(kv_dtype=5), skv.SKV_EINVAL),
+    (dict(kv_dtype=1, scale_block=32), skv.SKV_EINVAL),
+    (dict(kv_dtype=1, scale_block=128), skv.SKV_EINVAL),  # block_len 64
+    (dict(d=96), skv.SKV_EUNSUPPORTED),
+    (dict(kv_dtype=1, d=64), skv.SKV_EUNSUPPORTED),
+    (dict(q_strides=(16 * 128, 100)), skv.SKV_EINVAL),
+]
+
+
+@pytest.mark.parametrize("kw,status", SHARED + [
+    (dict(softmax_scale=math.inf), skv.SKV_EINVAL),
+    (dict(d=576, Hkv=1, k_strides=(64 * 576, 0, 576), v_strides=(64 * 576, 0, 576)), skv.SKV_EUNSUPPORTED),
+    (dict(softmax_scale=-0.1), skv.SKV_EINVAL),
+    (dict(softmax_scale=0.0), skv.SKV_EINVAL),
+    (dict(window=-1), skv.SKV_EINVAL),
+    (dict(window=5, n_sink=-1), skv.SKV_EINVAL),
+    (dict(n_sink=4), skv.SKV_EINVAL),
+    (dict(k_strides=(4 * 64 * 128, 64 * 128, 64)), skv.SKV_EINVAL),
+    (dict(v_strides=(4 * 64 * 128, 64 * 128, 132)), skv.SKV_EINVAL),
+    (dict(T=2 ** 31 - 1, Hq=64, Hkv=64), skv.SKV_EINVAL),  # more blocks than a grid has
+])
+def test_bad_chunk_descriptions(kw, status):
+    assert _call_chunk(_chunk(**kw)) == status
+    assert skv.last_error()
+
+
+@pytest.mark.parametrize("kw,status", SHARED + [
+    (dict(rot=130), skv.SKV_EINVAL),
+    (dict(rot=8), skv.SKV_EINVAL),
+    (dict(rot=-16), skv.SKV_EINVAL),
+    (dict(max_pos=0), skv.SKV_EINVAL),
+    (dict(eps=-1.0), skv.SKV_EINVAL),
+    (dict(eps=math.nan), skv.SKV_EINVAL),
+    (dict(weight_dtype=2), skv.SKV_EINVAL),
+    (dict(q_weight_stride=4), skv.SKV_EINVAL),
+    (dict(k_strides=(24 * 128, 130)), skv.SKV_EINVAL),
+    (dict(v_strides=(-8, 128)), skv.SKV_EINVAL),
+    (dict(q_out_strides=(16 * 128, 64)), skv.SKV_EINVAL),
+    (dict(k_page_strides=(4 * 64 * 128, 64 * 128, 120)), skv.SKV_EINVAL),
+])
+def test_bad_append_descriptions(kw, status):
+    assert _call_append(_append(**kw)) == status
+    assert skv.last_error()
+
+
+@pytest.mark.parametrize("kw", [dict(block_len=0), dict(block_len=96), dict(max_blocks=0), dict(num_blocks=0),
+                                dict(block_table=None), dict(block_table=0x10002), dict(max_blocks=2 ** 26)])
+def test_bad_pages(kw):
+    assert _call_chunk(_chunk(), _paged(**kw)) == skv.SKV_EINVAL
+    assert _call_append(_append(), _paged(**kw)) == skv.SKV_EINVAL
+
+
+def test_bad_pointers():
+    odd = ctypes.c_void_p(0x10008)
+    for name in ("q", "k", "v", "cu", "seq", "out", "lse"):
+        assert _call_chunk(_chunk(), **{name: None}) == skv.SKV_EINVAL
+    for name in ("q", "k", "v", "out"):
+        assert _call_chunk(_chunk(), **{name: odd}) == skv.SKV_EINVAL
+    for name in ("q", "k", "v", "cos", "sin", "cu", "seq", "out", "kp", "vp"):
+        assert _call_append(_append(), **{name: None}) == skv.SKV_EINVAL
+    for name in ("q", "k", "v", "qw", "kw", "cos", "sin", "out", "kp", "vp"):
+        assert _call_append(_append(), **{name: odd}) == skv.SKV_EINVAL
+    assert _call_append(_append(), pos=ctypes.c_void_p(0x10002)) == skv.SKV_EINVAL
+    assert _call_chunk(_chunk(kv_dtype=1)) == skv.SKV_EINVAL and "scale" in skv.last_error()
+    assert _call_append(_append(kv_dtype=1)) == skv.SKV_EINVAL and "scale" in skv.last_error()
+    assert _call_chunk(_chunk()) == skv.SKV_EWORKSPACE
+    assert _call_chunk(_chunk(), ws=ctypes.c_void_p(0x10010), ws_bytes=1 << 30) == skv.SKV_EWORKSPACE
+
+
+def test_no_rows_need_nothing():
+    n = ctypes.c_size_t(1)
+    lib = skv.load_library()
+    assert lib.attn_chunk_paged_workspace_size(ctypes.byref(_chunk(T=0)), ctypes.byref(_paged()), ctypes.byref(n)) == 0
+    assert n.value == 0
+    assert _call_chunk(_chunk(T=0), q=None, out=None) == skv.SKV_OK
+    assert _call_append(_append(T=0), q=None, out=None) == skv.SKV_OK
+    assert lib.attn_chunk_paged_workspace_size(ctypes.byref(_chunk()), ctypes.byref(_paged()), None) == skv.SKV_EINVAL
+    assert lib.attn_chunk_paged_workspace_size(None, ctypes.byref(_paged()), ctypes.byref(n)) == skv.SKV_EINVAL
+    assert lib.attn_chunk_paged_workspace_size(ctypes.byref(_chunk()), None, ctypes.byref(n)) == skv.SKV_EINVAL
+
+
+def test_the_workspace_does_not_grow_with_the_history():
+    """Partials are bounded by what fills the GPU, whatever the capacity of the tables."""
+    lib = skv.load_library()
+    sizes = []
+    for max_blocks in (1, 64, 1 << 20):
+        n = ctypes.c_size_t(0)
+        assert lib.attn_chunk_paged_workspace_size(ctypes.byref(_chunk(T=4096)), ctypes.byref(_paged(max_blocks=max_blocks)),
+                                                   ctypes.byref(n)) == 0
+        sizes.append(n.value)
+    assert len(set(sizes)) == 1 and 0 < sizes[0] < 1 << 28
+
+
+def test_cpu_tensors_are_refused():
+    z = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+    pages = torch.zeros(1, 2, 64, 64, dtype=torch.bfloat16)
+    i = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        skv.attn_chunk_paged(z, pages, pages, i[:1], i, i.view(1, 2))
+    with pytest.raises(ValueError, match="CUDA"):
+        skv.qk_norm_rope_append(z, z[:, :2], z[:, :2], pages, pages, i[:1], i, i.view(1, 2))
+
+
+def test_split_qkv_and_tables():
+    x = torch.arange(2 * 8 * 4).view(2, 32)
+    q, k, v = paged.split_qkv(x, 4, 2)
+    assert q.shape == (2, 4, 4) and k.shape == v.shape == (2, 2, 4)
+    assert torch.equal(torch.cat((q, k, v), 1).reshape(2, 32), x)
+    with pytest.raises(ValueError):
+        paged.split_qkv(x, 5, 1)
+    cos, sin = paged.rotation_tables(1000, 32)
+    assert cos.shape == sin.shape == (1000, 16) and cos.dtype == torch.float32
+    angle = 777 * 10000.0 ** (-2 * 5 / 32)
+    assert abs(cos[777, 5] - math.cos(angle)) <= 2 ** -24 and abs(sin[777, 5] - math.sin(angle)) <= 2 ** -24
