@@ -399,13 +399,14 @@ skv_status fill_params(PartialParams* p, const skv_desc* d, const Plan& pl, cons
   return SKV_OK;
 }
 
-// Query tensor map for the tensor-core kernel: dims (d, head, row, batch), box
-// (64, G, 128/G, 1) so that one box is a 128-row x 128-byte K-major tile.
-skv_status encode_q_map(CUtensorMap* map, const void* q, const skv_desc* d) {
+// Query tensor map for the tensor-core kernels: dims (d, head, row, batch), box
+// (64, G, 128/G, 1) so that one box is a 128-row x 128-byte K-major tile (box_heads > 0: that
+// many heads a box instead of the group's G).
+skv_status encode_q_map(CUtensorMap* map, const void* q, const skv_desc* d, int box_heads = 0) {
   cudaError_t e;
   auto encode = get_encode_fn(&e);
   if (!encode) return cuda_fail(e == cudaSuccess ? cudaErrorNotSupported : e, "cuTensorMapEncodeTiled lookup");
-  const int G = d->Hq / d->Hkv;
+  const int G = box_heads > 0 ? box_heads : d->Hq / d->Hkv;
   cuuint64_t gdim[4] = {static_cast<cuuint64_t>(d->dk), static_cast<cuuint64_t>(d->Hq),
                         static_cast<cuuint64_t>(d->Tq), static_cast<cuuint64_t>(d->B)};
   int64_t sh = d->q_strides[2] * 2, st = d->q_strides[1] * 2, sb = d->q_strides[0] * 2;
@@ -1044,11 +1045,27 @@ skv_status chunk_desc(const skv_chunk_desc* c, const skv_paged* pg, skv_desc* d)
   }
   skv_status st = validate(d, 1);
   if (st != SKV_OK) return st;
+  // a tensor map has no broadcast dimension, and a page that every entry shares cannot be written
+  if ((c->T > 1 && c->q_strides[0] == 0) || (c->Hq > 1 && c->q_strides[1] == 0))
+    return fail(SKV_EINVAL, "q strides must be positive");
+  for (const int64_t* s : {c->k_strides, c->v_strides})
+    if ((pg->num_blocks > 1 && s[0] == 0) || (c->Hkv > 1 && s[1] == 0))
+      return fail(SKV_EINVAL, "page and head strides of the pages must be positive");
   return validate_paged(d, pg);
 }
 
+// Rows of one token on the tensor-core kernel: the group padded to a power of two.
+int padded_group(int G) {
+  int r = 1;
+  while (r < G) r *= 2;
+  return r;
+}
+
 struct ChunkPlan {
-  GqaVariant variant;
+  bool tc = false;         // the tensor-core kernel
+  int group_rows = 1;      // rows of one token
+  int tile = kTileN;       // tokens of a KV tile
+  GqaVariant variant = GqaVariant::kBf16D128Decode;
   int rows = 0;            // rows of a row tile
   int64_t n_wave = 0;      // work items resident at once
   int64_t n_target = 0;    // most items of sequences with several chunks
@@ -1062,17 +1079,28 @@ skv_status chunk_plan(const skv_chunk_desc* c, const skv_desc* d, ChunkPlan* pl)
   // the caller's bound on the chunk lengths chooses the row tile (results do not depend on it)
   const int64_t longest = c->max_q_len > 0 ? std::min(c->max_q_len, c->T) : c->T;
   const bool few = longest * G <= 16;
+  pl->group_rows = G;
+  int per_sm = 1;
+  pl->tc = !few && d->kv_dtype == SKV_KV_BF16 && G <= 128;
   if (d->kv_dtype == SKV_KV_FP8_E4M3)
     pl->variant = few ? GqaVariant::kFp8D128Decode : GqaVariant::kFp8D128Prefill;
   else if (d->dk == 64)
     pl->variant = few ? GqaVariant::kBf16D64Decode : GqaVariant::kBf16D64Prefill;
   else
     pl->variant = few ? GqaVariant::kBf16D128Decode : GqaVariant::kBf16D128Prefill;
-  const GqaLaunchInfo li = gqa_launch_info(pl->variant);
-  pl->rows = li.rows_per_cta;
-  pl->n_wave = static_cast<int64_t>(device_sm_count()) * li.ctas_per_sm;
+  if (pl->tc) {
+    pl->group_rows = padded_group(G);
+    pl->rows = chunk_tc_rows();
+    pl->tile = chunk_tc_kv_tile();
+  } else {
+    const GqaLaunchInfo li = gqa_launch_info(pl->variant);
+    pl->rows = li.rows_per_cta;
+    per_sm = li.ctas_per_sm;
+  }
+  pl->n_wave = static_cast<int64_t>(device_sm_count()) * per_sm;
   pl->n_target = 4 * pl->n_wave;
-  const int64_t rows = static_cast<int64_t>(c->T) * G;
+  const int64_t rows = static_cast<int64_t>(c->T) * pl->group_rows;
+  if (rows + pl->rows >= (int64_t(1) << 31)) return fail(SKV_EINVAL, "T * Hq / Hkv is too large for one call");
   const int64_t row_tiles = rows / pl->rows + std::min(c->B, c->T);  // each sequence's last one may be short
   pl->n_items = row_tiles * d->Hkv + pl->n_target;
   if (pl->n_items >= (int64_t(1) << 31)) return fail(SKV_EINVAL, "T * Hq is too large for one call");
@@ -1135,18 +1163,28 @@ skv_status attn_chunk_paged(const skv_chunk_desc* desc, const skv_paged* paged, 
   p.ck.cap = static_cast<int32_t>(d.S_max);
   p.ck.window = desc->window;
   p.ck.n_sink = desc->n_sink;
+  p.ck.group_rows = pl.group_rows;
   p.ck.rows = pl.rows;
-  p.ck.tile = kTileN;
+  p.ck.tile = pl.tile;
   p.ck.n_wave = static_cast<int32_t>(pl.n_wave);
   p.ck.n_target = static_cast<int32_t>(pl.n_target);
   p.ck.plan = reinterpret_cast<int32_t*>(ws);
   p.ck.out = out;
   p.ck.lse = lse;
-  CUtensorMap tmk, tmv;
-  if ((st = encode_kv_map(&tmk, k_pages, &d, d.k_strides, d.dk, kTileN, paged)) != SKV_OK) return st;
-  if ((st = encode_kv_map(&tmv, v_pages, &d, d.v_strides, d.dv, kTileN, paged)) != SKV_OK) return st;
+  CUtensorMap tmq, tmk, tmv;
+  const int box = pl.tc ? chunk_tc_kv_box() : kTileN;
+  if ((st = encode_kv_map(&tmk, k_pages, &d, d.k_strides, d.dk, box, paged)) != SKV_OK) return st;
+  if ((st = encode_kv_map(&tmv, v_pages, &d, d.v_strides, d.dv, box, paged)) != SKV_OK) return st;
+  if (pl.tc) {
+    skv_desc dq = d;  // the packed rows as the query rows of one sequence
+    dq.B = 1;
+    dq.Tq = desc->T;
+    if ((st = encode_q_map(&tmq, q, &dq, pl.group_rows)) != SKV_OK) return st;
+  }
   cudaError_t e = timing_mark(false, s);
-  if (e == cudaSuccess) e = launch_gqa_chunk(pl.variant, p, tmk, tmv, pl.n_items, s);
+  if (e == cudaSuccess)
+    e = pl.tc ? launch_chunk_tc(p, d.dk, tmq, tmk, tmv, pl.n_items, s)
+              : launch_gqa_chunk(pl.variant, p, tmk, tmv, pl.n_items, s);
   if (e == cudaSuccess) e = timing_mark(true, s);
   if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
   // rows that can be in several chunks: no more than a partial row each

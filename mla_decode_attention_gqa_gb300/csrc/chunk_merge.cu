@@ -36,9 +36,15 @@ template <int D>
 __device__ __forceinline__ Joined join(const float* lse0, const float* o0, int64_t stride, int first, int step, int k,
                                        int lane) {
   Joined j;
-  for (int c = first + lane * step; c < k; c += 32 * step) j.m = fmaxf(j.m, lse0[c * stride]);
+  bool nan = false;  // a NaN partial makes the row NaN (fmaxf drops it)
+  for (int c = first + lane * step; c < k; c += 32 * step) {
+    const float l = lse0[c * stride];
+    nan = nan || l != l;
+    j.m = fmaxf(j.m, l);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) j.m = fmaxf(j.m, __shfl_xor_sync(0xffffffffu, j.m, o));
+  if (__any_sync(0xffffffffu, nan)) j.m = fmaxf(j.m, 0.f);
   if (j.m == -INFINITY) return j;
   for (int c0 = first; c0 < k; c0 += kBatch * step) {
     float w[kBatch];
@@ -65,7 +71,7 @@ __device__ __forceinline__ Joined join(const float* lse0, const float* o0, int64
 
 template <int D>
 __device__ __forceinline__ void store_row(const ChunkArgs& a, int64_t row, const Joined& j, int lane) {
-  const float inv = j.den > 0.f ? 1.f / j.den : 0.f;
+  const float inv = j.den != 0.f ? 1.f / j.den : 0.f;
   if (4 * lane < D) {
     __nv_bfloat162 lo = __floats2bfloat162_rn(j.acc.x * inv, j.acc.y * inv);
     __nv_bfloat162 hi = __floats2bfloat162_rn(j.acc.z * inv, j.acc.w * inv);
@@ -74,7 +80,7 @@ __device__ __forceinline__ void store_row(const ChunkArgs& a, int64_t row, const
     u.y = *reinterpret_cast<uint32_t*>(&hi);
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * D + 4 * lane) = u;
   }
-  if (lane == 0) a.lse[row] = j.den > 0.f ? j.m + logf(j.den) : -INFINITY;
+  if (lane == 0) a.lse[row] = j.den != 0.f ? j.m + logf(j.den) : -INFINITY;
 }
 
 template <int D>

@@ -3,8 +3,8 @@
 // call can be captured into a graph and replayed with other lengths.
 //
 // Sequence b has n = cu_q[b+1] - cu_q[b] new tokens, the last n of its m = seq_lens[b] cached
-// ones; row i sits at position m - n + i.  Its n * G rows per KV head are cut into row tiles
-// of R rows, and every row tile's KV tiles into k_b chunks:
+// ones; row i sits at position m - n + i.  Its rows of one KV head (n times the
+// group's G, or G padded to a power of two) are cut into row tiles of R rows, and every row tile's KV tiles into k_b chunks:
 //   W   = sum over b of (row tiles) * Hkv * (KV tiles of its last row tile)
 //   L   = max(1, ceil(W / n_target)),  k_b = max(1, floor((KV tiles) / L))
 // so the work items with k_b > 1 are at most W / L <= n_target, whatever the lengths are
@@ -64,8 +64,8 @@ __device__ __forceinline__ ChunkTiles chunk_tiles(int window, int n_sink, int ca
 
 // Row tiles per KV head and KV tiles of the last row tile (an upper bound of the others').
 __device__ __forceinline__ void chunk_extent(const ChunkArgs& a, int n, int m, int* row_tiles, int* kv_tiles) {
-  *row_tiles = static_cast<int>((static_cast<int64_t>(n) * a.G + a.rows - 1) / a.rows);
-  const int span = min(n, (a.rows + a.G - 1) / a.G + 1);
+  *row_tiles = static_cast<int>((static_cast<int64_t>(n) * a.group_rows + a.rows - 1) / a.rows);
+  const int span = min(n, (a.rows + a.group_rows - 1) / a.group_rows + 1);
   const ChunkTiles t = chunk_tiles(a.window, a.n_sink, a.cap, m - span, m - 1, a.tile);
   *kv_tiles = max(t.n, 1);
 }

@@ -646,6 +646,8 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
   const bool direct = CHUNK && ci.n_chunk == 1;  // the final rows, in bf16
   float* const lse_out = direct ? p.ck.lse : p.out_lse;
   const bool zero_empty = direct || (!CHUNK && p.zero_empty);
+  // a row that summed something; CHUNK: a NaN sum counts, so that NaN scores give a NaN row
+  auto some = [](float l) -> bool { return CHUNK ? l != 0.f : l > 0.f; };
   auto row_out = [&](int t_q, int h) -> int64_t {
     if constexpr (CHUNK)
       return direct ? (q_row0 + t_q) * p.Hq + h
@@ -663,10 +665,10 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
   };
 
   if constexpr (WN == 1) {
-    const float inv0 = lrun[0] > 0.f ? 1.f / lrun[0] : 0.f;
-    const float inv1 = lrun[1] > 0.f ? 1.f / lrun[1] : 0.f;
-    const bool w0 = v0 && (lrun[0] > 0.f || zero_empty);
-    const bool w1 = v1 && (lrun[1] > 0.f || zero_empty);
+    const float inv0 = some(lrun[0]) ? 1.f / lrun[0] : 0.f;
+    const float inv1 = some(lrun[1]) ? 1.f / lrun[1] : 0.f;
+    const bool w0 = v0 && (some(lrun[0]) || zero_empty);
+    const bool w1 = v1 && (some(lrun[1]) || zero_empty);
     if constexpr (!C::FP8) {
       const int64_t o0 = row_out(tq0, h0), o1 = row_out(tq1, h1);
 #pragma unroll
@@ -696,8 +698,8 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
       }
     }
     if (tq == 0) {
-      if (v0) lse_out[row_out(tq0, h0)] = lrun[0] > 0.f ? (mrun[0] + __log2f(lrun[0])) * kLn2 : -INFINITY;
-      if (v1) lse_out[row_out(tq1, h1)] = lrun[1] > 0.f ? (mrun[1] + __log2f(lrun[1])) * kLn2 : -INFINITY;
+      if (v0) lse_out[row_out(tq0, h0)] = some(lrun[0]) ? (mrun[0] + __log2f(lrun[0])) * kLn2 : -INFINITY;
+      if (v1) lse_out[row_out(tq1, h1)] = some(lrun[1]) ? (mrun[1] + __log2f(lrun[1])) * kLn2 : -INFINITY;
     }
   } else {
     constexpr int NCT = C::NCW * 32;
@@ -721,8 +723,11 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
       if (M != -INFINITY) {
 #pragma unroll
         for (int w = 0; w < WN; ++w) L += ml[(w * C::ROWS + lr) * 2 + 1] * fast_exp2(ml[(w * C::ROWS + lr) * 2] - M);
+      } else if constexpr (CHUNK) {
+#pragma unroll
+        for (int w = 0; w < WN; ++w) L += ml[(w * C::ROWS + lr) * 2 + 1];  // 0, or NaN
       }
-      f[r] = (L > 0.f) ? fast_exp2(mrun[r] - M) / L : 0.f;
+      f[r] = some(L) ? fast_exp2(mrun[r] - M) / L : 0.f;
     }
     float* obuf = reinterpret_cast<float*>(smem);  // [WN][ROWS][D]
     if constexpr (!C::FP8) {
@@ -763,10 +768,13 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
       if (M != -INFINITY) {
 #pragma unroll
         for (int w = 0; w < WN; ++w) L += ml[(w * C::ROWS + lr) * 2 + 1] * fast_exp2(ml[(w * C::ROWS + lr) * 2] - M);
+      } else if constexpr (CHUNK) {
+#pragma unroll
+        for (int w = 0; w < WN; ++w) L += ml[(w * C::ROWS + lr) * 2 + 1];  // 0, or NaN
       }
       const int t_q = m / p.G, h = g * p.G + m % p.G;
       const int64_t ro = row_out(t_q, h);
-      if (L > 0.f || zero_empty) {
+      if (some(L) || zero_empty) {
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < WN; ++w) {
@@ -782,7 +790,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
         else
           *reinterpret_cast<float4*>(p.out_o + ro * D + d) = acc;
       }
-      if (d == 0) lse_out[ro] = (L > 0.f) ? (M + __log2f(L)) * kLn2 : -INFINITY;
+      if (d == 0) lse_out[ro] = some(L) ? (M + __log2f(L)) * kLn2 : -INFINITY;
     }
   }
 }

@@ -37,6 +37,7 @@ struct ChunkArgs {
   int32_t cap;      // tokens a block-table row can hold
   int32_t window;   // tokens a row sees up to its own (0: all)
   int32_t n_sink;   // first tokens seen besides the window
+  int32_t group_rows;  // rows of one token: G, or G padded to a power of two
   int32_t rows;     // rows (token, head of the group) of one row tile
   int32_t tile;     // tokens of one KV tile
   int32_t n_wave;   // work items resident at once
@@ -149,6 +150,14 @@ cudaError_t launch_gqa_partial(GqaVariant v, const PartialParams& p, const CUten
 // the others partial rows to p.out_o / p.out_lse, which launch_chunk_merge joins.
 cudaError_t launch_gqa_chunk(GqaVariant v, const PartialParams& p, const CUtensorMap& tmk, const CUtensorMap& tmv,
                              int64_t n_items, cudaStream_t stream);
+// On the tensor cores (see chunk_tc.cu): bf16 pages, any G <= 128; tmq: q as (dim, head, packed
+// row) with 64 x group_rows x 128 / group_rows boxes, tmk / tmv: pages with chunk_tc_kv_box()
+// rows a box.
+int chunk_tc_rows();
+int chunk_tc_kv_tile();
+int chunk_tc_kv_box();
+cudaError_t launch_chunk_tc(const PartialParams& p, int32_t d, const CUtensorMap& tmq, const CUtensorMap& tmk,
+                            const CUtensorMap& tmv, int64_t n_items, cudaStream_t stream);
 cudaError_t launch_chunk_merge(const ChunkArgs& a, int32_t d, const float* part_o, const float* part_lse,
                                int64_t max_rows, cudaStream_t stream);
 

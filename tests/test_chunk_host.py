@@ -74,6 +74,8 @@ SHARED = [
     (dict(d=96), skv.SKV_EUNSUPPORTED),
     (dict(kv_dtype=1, d=64), skv.SKV_EUNSUPPORTED),
     (dict(q_strides=(16 * 128, 100)), skv.SKV_EINVAL),
+    (dict(q_strides=(0, 128)), skv.SKV_EINVAL),
+    (dict(q_strides=(16 * 128, 0)), skv.SKV_EINVAL),
 ]
 
 
@@ -87,7 +89,10 @@ SHARED = [
     (dict(n_sink=4), skv.SKV_EINVAL),
     (dict(k_strides=(4 * 64 * 128, 64 * 128, 64)), skv.SKV_EINVAL),
     (dict(v_strides=(4 * 64 * 128, 64 * 128, 132)), skv.SKV_EINVAL),
-    (dict(T=2 ** 31 - 1, Hq=64, Hkv=64), skv.SKV_EINVAL),  # more blocks than a grid has
+    (dict(v_strides=(0, 64 * 128, 128)), skv.SKV_EINVAL),
+    (dict(k_strides=(4 * 64 * 128, 0, 128)), skv.SKV_EINVAL),
+    (dict(T=2 ** 31 - 1), skv.SKV_EINVAL),  # more rows than 32 bits count
+    (dict(T=2 ** 30, Hq=512, Hkv=512), skv.SKV_EINVAL),  # more blocks than a grid has
 ])
 def test_bad_chunk_descriptions(kw, status):
     assert _call_chunk(_chunk(**kw)) == status

@@ -300,3 +300,32 @@ def test_no_rows_and_a_caller_workspace():
     with pytest.raises(skv.SplitKVError) as e:
         run(c, workspace=ws[:256])
     assert e.value.status == skv.SKV_EWORKSPACE
+
+
+@pytest.mark.parametrize("longest", [1, None])
+@pytest.mark.parametrize("kind,d", TYPES)
+def test_nan_that_is_seen_is_told(kind, d, longest):
+    """A NaN key makes every row that sees it NaN, through one chunk or many."""
+    n, m = ([1, 1, 1], [70, 40, 9000]) if longest == 1 else ([3, 2, 1], [70, 40, 9000])
+    c = R.make_case(n, m, 8, 2, d, fp8=kind == "fp8", seed=19, device=DEV)
+    for b, t in ((0, 5), (2, 8000)):
+        page = int(c["block_table"][b, t // 64])
+        c["k_pages"].view(torch.uint8 if kind == "fp8" else torch.int16)[page, 1, t % 64] = 0x7F if kind == "fp8" else 0x7FC0
+    out, lse = run(c, max_q_len=longest)
+    cu = c["cu_q"].tolist()
+    for b in range(3):
+        rows = slice(cu[b], cu[b + 1])
+        assert torch.isfinite(out[rows, :4]).all() and torch.isfinite(lse[rows, :4]).all()
+        hit = b != 1
+        assert torch.isnan(out[rows, 4:]).all() == hit and torch.isnan(lse[rows, 4:]).all() == hit
+        assert hit or torch.isfinite(out[rows]).all()
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 1), (7, 1), (100, 1), (128, 1), (136, 1)])
+@pytest.mark.parametrize("kind,d", TYPES)
+def test_head_groups(kind, d, Hq, Hkv):
+    """Groups padded to a power of two (fewer heads than a box among them), a group that fills a
+    query tile alone, and one larger than that."""
+    c = R.make_case([1, 9, 30], [200, 9, 150], Hq, Hkv, d, fp8=kind == "fp8", seed=Hq, device=DEV)
+    check(c)
+    check(c, window=40, n_sink=3)
