@@ -5,17 +5,18 @@
 // For every row (new token at position p, query head h of KV head g): s_u = scale q.k_u over
 // the visible tokens u (u <= p and u > p - window or u < n_sink), out = softmax(s) V, lse =
 // ln sum e^s.  One pass over the tokens with a running maximum; sums and O in fp32, P rounded
-// to bf16 for the product with V (2^-8 of each weight at most) and O normalised by the sum of the
-// rounded weights, so that the output stays a convex combination of V rows.
+// to bf16 for the product with V (2^-8 of each weight at most, as much as the output's own
+// rounding).  O is divided by the fp32 sum of the unrounded weights: summing the rounded ones as
+// well cost two more additions a pair of scores on the path that bounds the kernel.
 //
 // Bound by the tensor pipe for chunks of 128 and more rows (two 128 x 128 x D products per tile
 // of 128 tokens and 128 rows), by HBM for few rows.  Design (one CTA an SM, 384 threads):
 //   * rows of one KV head are (token, head of the group) pairs, the group padded to a power of
 //     two Gr, so that a 128-row tile is a TMA box of 128 / Gr tokens x Gr heads; every K/V byte
 //     is read once for the whole group;
-//   * warp 0 loads (Q once; K and V tiles of 128 tokens, each 64-token half from its own page,
-//     into separate K and V rings, since a K tile is free as soon as its scores are done and a
-//     V tile only after the softmax), warp 1 issues every MMA, warps 4-7 and 8-11 are two
+//   * warps 0 and 2 load (Q once; K and V tiles of 128 tokens, each 64-token half from its own
+//     page, into separate K and V rings, since a K tile is free as soon as its scores are done
+//     and a V tile only after the softmax), warp 1 issues every MMA, warps 4-7 and 8-11 are two
 //     softmax groups with one thread a row (the TMEM lane of its row: no shuffles);
 //   * pair mode (an item of more than 128 rows): group k serves query tile k, both read each
 //     K/V tile; MMA order PV0(i), S0(i+1), PV1(i), S1(i+1), so that one group works while the
@@ -62,8 +63,8 @@ struct TcCfg {
   static constexpr int OFF_K = 2 * TILE;
   static constexpr int OFF_V = OFF_K + NST * TILE;
   static constexpr int OFF_BAR = OFF_V + NST * TILE;
-  static constexpr int OFF_ML = OFF_BAR + 256;       // solo: group 1's (m, l, l of the rounded) per row
-  static constexpr int SMEM = 1024 + OFF_ML + kRowsTile * 12;
+  static constexpr int OFF_ML = OFF_BAR + 256;       // solo: group 1's (m, l) per row
+  static constexpr int SMEM = 1024 + OFF_ML + kRowsTile * 8;
   static_assert(SMEM <= 226 * 1024, "shared memory budget (the work search has some of its own)");
 };
 
@@ -138,52 +139,62 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = bars->tmem_base;
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer
-    if (lane == 0 && n_tiles > 0) {
-      tma_prefetch_desc(&tmq);
-      tma_prefetch_desc(&tmk);
-      tma_prefetch_desc(&tmv);
-      const int nq = pair ? 2 : 1;
-      mbar_arrive_expect_tx(&bars->q_full, nq * C::TILE);
-      for (int k = 0; k < nq; ++k)
-        for (int bx = 0; bx < NB; ++bx)
-          tma_4d(smem + k * C::TILE + bx * C::BOX, &tmq, &bars->q_full, bx * 64, it.g * G,
-                 it.row0 + (m0 + k * kRowsTile) / Gr, 0);
-      // pages of a tile's halves (a second half at or past the capacity holds no token: it
-      // takes the first one's page instead of an entry behind the table's row)
-      auto pages_of = [&](int i, int& a, int& c) {
+  if (warp == 0 || warp == 2) {
+    // ------------------------------------------------------------ TMA producers: 0 Q and K, 2 V
+    // A warp each, so that neither waits for the other's ring; the pages and rows of the next
+    // tile (four integer divisions and two dependent loads) are looked up behind this tile's
+    // copies, not between a freed stage and its refill, which bounds a two-stage ring.
+    if (n_tiles > 0) {
+      const bool is_k = warp == 0;
+      const CUtensorMap* map = is_k ? &tmk : &tmv;
+      uint64_t* full = is_k ? bars->k_full : bars->v_full;
+      uint64_t* empty = is_k ? bars->k_empty : bars->v_empty;
+      uint8_t* ring = smem + (is_k ? C::OFF_K : C::OFF_V);
+      if (tc::elect_one()) {
+        tma_prefetch_desc(map);
+        if (is_k) {
+          tma_prefetch_desc(&tmq);
+          const int nq = pair ? 2 : 1;
+          mbar_arrive_expect_tx(&bars->q_full, nq * C::TILE);
+          for (int k = 0; k < nq; ++k)
+            for (int bx = 0; bx < NB; ++bx)
+              tma_4d(smem + k * C::TILE + bx * C::BOX, &tmq, &bars->q_full, bx * 64, it.g * G,
+                     it.row0 + (m0 + k * kRowsTile) / Gr, 0);
+        }
+      }
+      __syncwarp();
+      int page[2], at[2];  // of a tile's two halves
+      auto look_up = [&](int i) {
         const int t = tile_token(i);
-        a = kv_page_of(p, it.b, t);
-        c = t + kHalf < p.ck.cap ? kv_page_of(p, it.b, t + kHalf) : a;
+        // a second half at or past the capacity holds no token: it takes the first one's page
+        // instead of an entry behind the table's row
+        const int t2 = t + kHalf < p.ck.cap ? t + kHalf : t;
+        at[0] = t % p.block_len;
+        at[1] = t2 % p.block_len;
+        page[0] = kv_page_of(p, it.b, t);
+        page[1] = kv_page_of(p, it.b, t2);
       };
-      auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int tok, const int (&page)[2]) {
-        mbar_arrive_expect_tx(bar, C::TILE);
-        for (int hf = 0; hf < 2; ++hf)
-          for (int bx = 0; bx < NB; ++bx)
-            tma_4d(dst + bx * C::BOX + hf * (C::BOX / 2), map, bar, bx * 64, (tok + hf * kHalf) % p.block_len, it.g,
-                   page[hf]);
-      };
-      int pg0, pg1, k_issued = 0, v_issued = 0;
-      pages_of(0, pg0, pg1);
+      look_up(0);
+      int issued = 0;
       for (int i = 0; i < n_tiles; ++i) {
         const int s = i % NST;
-        const uint32_t before = ((i / NST) - 1) & 1;
-        const int cur[2] = {pg0, pg1};
-        if (i + 1 < n_tiles) pages_of(i + 1, pg0, pg1);  // behind this tile's waits
-        if (i >= NST && !mbar_wait(&bars->k_empty[s], before, p.err, kDevErrEmptyWait)) break;
-        load(smem + C::OFF_K + s * C::TILE, &tmk, &bars->k_full[s], tile_token(i), cur);
-        k_issued = i + 1;
-        if (i >= NST && !mbar_wait(&bars->v_empty[s], before, p.err, kDevErrEmptyWait)) break;
-        load(smem + C::OFF_V + s * C::TILE, &tmv, &bars->v_full[s], tile_token(i), cur);
-        v_issued = i + 1;
+        if (i >= NST && !__all_sync(0xffffffffu, mbar_wait(&empty[s], ((i / NST) - 1) & 1, p.err, kDevErrEmptyWait))) break;
+        if (tc::elect_one()) {
+          mbar_arrive_expect_tx(&full[s], C::TILE);
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+            for (int bx = 0; bx < NB; ++bx)
+              tma_4d(ring + s * C::TILE + bx * C::BOX + hf * (C::BOX / 2), map, &full[s], bx * 64, at[hf], it.g, page[hf]);
+        }
+        __syncwarp();
+        issued = i + 1;
+        if (issued < n_tiles) look_up(issued);
       }
       // every issued copy lands before the CTA may exit
-      for (int i = max(0, k_issued - NST); i < k_issued; ++i)
-        if (!mbar_wait(&bars->k_full[i % NST], (i / NST) & 1, p.err, kDevErrDrainWait)) break;
-      for (int i = max(0, v_issued - NST); i < v_issued; ++i)
-        if (!mbar_wait(&bars->v_full[i % NST], (i / NST) & 1, p.err, kDevErrDrainWait)) break;
-      mbar_wait(&bars->q_full, 0, p.err, kDevErrDrainWait);
+      for (int i = max(0, issued - NST); i < issued; ++i)
+        if (!mbar_wait(&full[i % NST], (i / NST) & 1, p.err, kDevErrDrainWait)) break;
+      if (is_k) mbar_wait(&bars->q_full, 0, p.err, kDevErrDrainWait);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -332,8 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_col = t_lane + kColS + 128 * k;
     const uint32_t o_col = t_lane + kColO + 128 * k;
     const float sl = p.scale_log2;
-    // l_sum: fp32 sum of p (the lse's); l_pv: sum of the rounded p (O's)
-    float m_used = -INFINITY, l_sum = 0.f, l_pv = 0.f;
+    float m_used = -INFINITY, l_sum = 0.f;
     bool ok = true;
     const int first = pair ? 0 : k, step = pair ? 1 : 2;  // this group's tiles
 
@@ -351,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c_sink = min(max(sink_row - t0, 0), kTN);
         auto visible = [&](int col) -> bool { return static_cast<unsigned>(col - c_lo) < span || col < c_sink; };
         uint32_t pk[kTN / 2];
-        uint64_t ls[2] = {0ull, 0ull}, lr[2] = {0ull, 0ull};  // fp32 pair sums of p and of the rounded p
+        uint64_t ls[2] = {0ull, 0ull};  // fp32 pair sums of p
         const float base0 = (m_used == -INFINITY) ? 0.f : m_used;
         // masked: a compile-time flag, so that tiles that every row sees carry no test
         auto pass = [&](auto masked) {
@@ -375,7 +385,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
               ls[e & 1] = add_f32x2(ls[e & 1], p0, p1);
               pk[16 * cc + e] = pack_bf16(p0, p1);
-              lr[e & 1] = add_bf16x2_f32x2(lr[e & 1], pk[16 * cc + e]);
             }
           }
         };
@@ -427,12 +436,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc::tmem_wait_st();
             l_sum *= alpha;
-            l_pv *= alpha;
           }
           m_used = m_new;
           const float base = (m_used == -INFINITY) ? 0.f : m_used;
           ls[0] = ls[1] = 0ull;
-          lr[0] = lr[1] = 0ull;
 #pragma unroll 1
           for (int cc = 0; cc < kTN / 32; ++cc) {
             uint32_t r[2][16];
@@ -448,7 +455,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float p0 = fast_exp2(fmaf(v0, sl, -base)), p1 = fast_exp2(fmaf(v1, sl, -base));
               ls[e & 1] = add_f32x2(ls[e & 1], p0, p1);
               w[e] = pack_bf16(p0, p1);
-              lr[e & 1] = add_bf16x2_f32x2(lr[e & 1], w[e]);
             }
             tc::tmem_st16(s_col + 16 * cc, w);  // S columns 32 cc.. were read before P 16 cc.. is written
           }
@@ -463,7 +469,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc::tmem_wait_st();
         l_sum += sum_f32x2(ls[0]) + sum_f32x2(ls[1]);
-        l_pv += sum_f32x2(lr[0]) + sum_f32x2(lr[1]);
       }
       const bool inside = (t0 >= tl.lo && t0 + kTN <= tl.hi) || t0 + kTN <= tl.sinks;
       if (!inside && (k == 0 || !pair)) {
@@ -490,22 +495,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     // solo: the two groups' weights.  A group that summed nothing has l = 0 (its O may be
     // anything); a NaN among the scores keeps l NaN, and the row is NaN
     float a0 = 1.f, a1 = 0.f;
-    bool some0 = l_pv != 0.f, some1 = false;
+    bool some0 = l_sum != 0.f, some1 = false;
     if (!pair) {
       if (k == 1) {
-        ml[3 * row] = m_used;
-        ml[3 * row + 1] = l_sum;
-        ml[3 * row + 2] = l_pv;
+        ml[2 * row] = m_used;
+        ml[2 * row + 1] = l_sum;
       }
       asm volatile("bar.sync 1, 256;" ::: "memory");
       if (k == 0) {
-        const float m1 = ml[3 * row], l1 = ml[3 * row + 1], r1 = ml[3 * row + 2];
+        const float m1 = ml[2 * row], l1 = ml[2 * row + 1];
         const float mm = fmaxf(m_used, m1);
-        some1 = r1 != 0.f;
+        some1 = l1 != 0.f;
         a0 = some0 ? fast_exp2(m_used - mm) : 0.f;
         a1 = some1 ? fast_exp2(m1 - mm) : 0.f;
         l_sum = (some0 ? a0 * l_sum : 0.f) + (some1 ? a1 * l1 : 0.f);
-        l_pv = (some0 ? a0 * l_pv : 0.f) + (some1 ? a1 * r1 : 0.f);
         m_used = mm;
       }
     }
@@ -515,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && both) ok = mbar_wait(&bars->pv_done[1], (tiles_of(1) - 1) & 1, p.err, kDevErrFullWait);
       tc::fence_after_sync();
       const bool some = some0 || some1;
-      const float inv = some ? 1.f / l_pv : 0.f;
+      const float inv = some ? 1.f / l_sum : 0.f;
       a0 *= inv;
       a1 *= inv;
       constexpr float kLn2 = 0.6931471805599453f;
