@@ -1105,7 +1105,7 @@ skv_status chunk_plan(const skv_chunk_desc* c, const skv_desc* d, ChunkPlan* pl)
   pl->n_items = row_tiles * d->Hkv + pl->n_target;
   if (pl->n_items >= (int64_t(1) << 31)) return fail(SKV_EINVAL, "T * Hq is too large for one call");
   pl->part_rows = pl->n_target * std::min<int64_t>(pl->rows, rows);
-  pl->plan_bytes = align_up((3 * static_cast<size_t>(c->B) + 1) * 4, 256);
+  pl->plan_bytes = align_up((kPlanHead + kPlanRow * static_cast<size_t>(c->B)) * 4, 256);
   pl->o_bytes = align_up(static_cast<size_t>(pl->part_rows) * d->dv * 4, 256);
   pl->lse_bytes = align_up(static_cast<size_t>(pl->part_rows) * 4, 256);
   return SKV_OK;
@@ -1181,7 +1181,9 @@ skv_status attn_chunk_paged(const skv_chunk_desc* desc, const skv_paged* paged, 
     dq.Tq = desc->T;
     if ((st = encode_q_map(&tmq, q, &dq, pl.group_rows)) != SKV_OK) return st;
   }
-  cudaError_t e = timing_mark(false, s);
+  cudaError_t e = cudaSuccess;
+  if (pl.tc) e = launch_chunk_plan(p.ck, s);
+  if (e == cudaSuccess) e = timing_mark(false, s);
   if (e == cudaSuccess)
     e = pl.tc ? launch_chunk_tc(p, d.dk, tmq, tmk, tmv, pl.n_items, s)
               : launch_gqa_chunk(pl.variant, p, tmk, tmv, pl.n_items, s);

@@ -1,10 +1,11 @@
-// Joins the partial rows of attention over ragged chunks (attn_chunk_paged): the rows of the
+// The plan and the merge of attention over ragged chunks.
+//
+// The merge joins the partial rows of attention over ragged chunks (attn_chunk_paged): the rows of the
 // sequences whose KV tiles were dealt to several chunks.
 //
 // For every such row, with k partials (o_c, lse_c): m = max lse_c, w_c = exp(lse_c - m),
 // out = sum w_c o_c / sum w_c in bf16, lse = m + ln sum w_c; all partials empty: out = 0,
-// lse = -inf.  The work table (first row to merge, first partial row and k of each sequence)
-// was written by block 0 of the attention kernel before it.
+// lse = -inf.  Where they are stands in the plan (chunk_plan.cuh) of the call.
 //
 // Bound by the partials' bytes, which are mostly still in L2; what counts is how many loads
 // are in flight.  A block takes 8 rows: one warp each while k <= 16 (all partials of a row in
@@ -15,6 +16,7 @@
 #include <cuda_runtime.h>
 #include <math.h>
 
+#include "chunk_plan.cuh"
 #include "skv_internal.h"
 
 namespace skv {
@@ -94,7 +96,8 @@ __global__ void __launch_bounds__(32 * kRowsPerBlock)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int Hq = a.Hkv * a.G;
-  const int rows = a.plan[3 * a.B];
+  const int rows = __ldcg(a.plan + kPlanMerged);
+  const int32_t* plan = a.plan + kPlanHead;
   for (int r0 = blockIdx.x * kRowsPerBlock; r0 < rows; r0 += gridDim.x * kRowsPerBlock) {
     const int r = r0 + warp;
     __syncthreads();  // the tables' earlier readers are done
@@ -105,15 +108,15 @@ __global__ void __launch_bounds__(32 * kRowsPerBlock)
         int lo = 0, hi = a.B - 1;  // the last sequence whose first row is <= r
         while (lo < hi) {
           const int mid = (lo + hi + 1) >> 1;
-          if (a.plan[3 * mid] <= r) lo = mid; else hi = mid - 1;
+          if (__ldcg(plan + kPlanRow * mid + 1) <= r) lo = mid; else hi = mid - 1;
         }
         // sequences without rows to merge share the first row of the one after them
-        const int in = r - a.plan[3 * lo];
+        const int in = r - __ldcg(plan + kPlanRow * lo + 1);
         const int row0 = min(max(__ldg(a.cu_q + lo), 0), a.T);
         n = max(min(max(__ldg(a.cu_q + lo + 1), 0), a.T) - row0, 0);
-        k = a.plan[3 * lo + 2];
+        k = __ldcg(plan + kPlanRow * lo + 4);
         row = static_cast<int64_t>(row0) * Hq + in;
-        part = static_cast<int64_t>(a.plan[3 * lo + 1]) + in;
+        part = static_cast<int64_t>(__ldcg(plan + kPlanRow * lo + 2)) + in;
       }
       sm_parts[warp] = k;
       sm_n[warp] = n;
@@ -165,7 +168,31 @@ __global__ void __launch_bounds__(32 * kRowsPerBlock)
   }
 }
 
+constexpr int kPlanThreads = 512;
+
+// The plan of a call, for the persistent attention kernel and the merge after it.  One block:
+// two loads and two scans a sequence, a few microseconds, under which the next grid starts.
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_constant__ ChunkArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ int64_t sm_scan[2 * (kPlanThreads / 32)];
+  int64_t items, merged;
+  chunk_make_plan<kPlanThreads>(a, sm_scan, &items, &merged,
+                                [&](int b, int first, int rt, int k, int part_row, int merge_row) {
+                                  chunk_write_plan(a, b, first, rt, k, part_row, merge_row);
+                                });
+  if (threadIdx.x == 0) {
+    a.plan[kPlanItems] = static_cast<int>(items);
+    a.plan[kPlanMerged] = static_cast<int>(merged);
+    a.plan[kPlanNext] = 0;
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_chunk_plan(const ChunkArgs& a, cudaStream_t stream) {
+  chunk_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_chunk_merge(const ChunkArgs& a, int32_t d, const float* part_o, const float* part_lse,
                                int64_t max_rows, cudaStream_t stream) {

@@ -8,9 +8,12 @@
 //   W   = sum over b of (row tiles) * Hkv * (KV tiles of its last row tile)
 //   L   = max(1, ceil(W / n_target)),  k_b = max(1, floor((KV tiles) / L))
 // so the work items with k_b > 1 are at most W / L <= n_target, whatever the lengths are
-// (which bounds the workspace), and those with k_b = 1 at most Hkv * (row tiles).  Every
-// block finds its own item with one scan over the sequences (one pass of loads when B is at
-// most the block's threads), which costs less than a launch that would write a plan.
+// (which bounds the workspace), and those with k_b = 1 at most Hkv * (row tiles).
+//
+// The persistent tensor-core kernel takes its items from a plan that one small kernel wrote
+// before it; the other kernel's blocks, one item each, find theirs with a scan of their own
+// over the sequences (one pass of loads when B is at most the block's threads), and block 0
+// writes the plan for the merge.
 #pragma once
 
 #include "skv_internal.h"
@@ -70,6 +73,19 @@ __device__ __forceinline__ void chunk_extent(const ChunkArgs& a, int n, int m, i
   *kv_tiles = max(t.n, 1);
 }
 
+// The plan in device memory: [kPlanItems] work items, [kPlanMerged] rows to merge, [kPlanNext] the
+// next item to hand out, and for each sequence its first item, first row to merge, first partial
+// row, row tiles and chunks per row tile.
+__device__ __forceinline__ void chunk_write_plan(const ChunkArgs& a, int b, int first, int rt, int k, int part_row,
+                                                 int merge_row) {
+  int32_t* e = a.plan + kPlanHead + static_cast<int64_t>(kPlanRow) * b;
+  e[0] = first;
+  e[1] = merge_row;
+  e[2] = part_row;
+  e[3] = rt;
+  e[4] = k;
+}
+
 // Inclusive sums over the block's threads of x and y; total of both in *tx, *ty.
 template <int NT>
 __device__ __forceinline__ void chunk_block_scan(int64_t& x, int64_t& y, int64_t* tx, int64_t* ty, int64_t* sm) {
@@ -105,15 +121,13 @@ __device__ __forceinline__ void chunk_block_scan(int64_t& x, int64_t& y, int64_t
   *ty = sy;
 }
 
-// The block's work item; false if there are fewer items than blocks.  Block 0 also writes the
-// merge's table (see chunk_merge.cu).  Every thread of the block calls it.
-template <int NT>
-__device__ __forceinline__ bool chunk_find_item(const ChunkArgs& a, ChunkItem* item) {
-  __shared__ int64_t sm_scan[2 * (NT / 32)];
-  __shared__ ChunkItem sm_item;
-  __shared__ int sm_found;
+// The plan of one call, computed by all NT threads of a block: `visit(b, first item, row tiles,
+// chunks, first partial row, first row to merge)` for every sequence, totals in *items and
+// *merged.  A visitor must not synchronise.
+template <int NT, class F>
+__device__ __forceinline__ void chunk_make_plan(const ChunkArgs& a, int64_t* sm_scan, int64_t* items, int64_t* merged,
+                                                F&& visit) {
   const int tid = threadIdx.x;
-  if (tid == 0) sm_found = 0;
   int64_t w = 0, zero = 0, total, unused;
   for (int b = tid; b < a.B; b += NT) {
     int row0, n, m, rt, kt;
@@ -124,11 +138,8 @@ __device__ __forceinline__ bool chunk_find_item(const ChunkArgs& a, ChunkItem* i
   chunk_block_scan<NT>(w, zero, &total, &unused, sm_scan);
   const int64_t target = total <= a.n_wave * static_cast<int64_t>(kChunkShortTiles) ? a.n_wave : a.n_target;
   const int L = static_cast<int>(min(max((total + target - 1) / target, (int64_t)1), (int64_t)1 << 30));
-
-  const bool writes_plan = blockIdx.x == 0 && a.plan != nullptr;
   const int Hq = a.Hkv * a.G;
-  int64_t items = 0, parts = 0;  // of the sequences before this pass
-  int64_t merged = 0;            // rows to merge of the sequences before this pass
+  int64_t it0 = 0, part0 = 0, mr0 = 0;  // of the sequences before this pass
   for (int b0 = 0; b0 < a.B; b0 += NT) {
     const int b = b0 + tid;
     int row0 = 0, n = 0, m = 0, rt = 0, kt = 1, k = 1;
@@ -138,45 +149,78 @@ __device__ __forceinline__ bool chunk_find_item(const ChunkArgs& a, ChunkItem* i
       k = max(1, kt / L);
     }
     const int64_t mine = static_cast<int64_t>(rt) * a.Hkv * k;
-    const int64_t my_rows = k > 1 ? static_cast<int64_t>(n) * Hq : 0;
-    int64_t x = mine, y = my_rows * k, tx, ty;
+    const int64_t rows = k > 1 ? static_cast<int64_t>(n) * Hq : 0;
+    int64_t x = mine, y = rows * k, z = rows, tx, ty, tz;
     chunk_block_scan<NT>(x, y, &tx, &ty, sm_scan);
-    const int64_t first = items + x - mine, part0 = parts + y - my_rows * k;
-    if (b < a.B && blockIdx.x >= first && blockIdx.x < first + mine) {
-      int r = static_cast<int>(blockIdx.x - first);
-      ChunkItem it;
-      it.b = b;
-      it.n_chunk = k;
-      it.row0 = row0;
-      it.n = n;
-      it.m = m;
-      it.part_row = static_cast<int>(part0);
-      // later row tiles (which see more) first; a row tile's chunks and heads side by side
-      it.c = r % k;
-      r /= k;
-      it.g = r % a.Hkv;
-      it.mt = rt - 1 - r / a.Hkv;
-      sm_item = it;
+    chunk_block_scan<NT>(z, zero, &tz, &unused, sm_scan);
+    if (b < a.B)
+      visit(b, static_cast<int>(it0 + x - mine), rt, k, static_cast<int>(part0 + y - rows * k),
+            static_cast<int>(mr0 + z - rows));
+    it0 += tx;
+    part0 += ty;
+    mr0 += tz;
+    zero = 0;
+  }
+  *items = it0;
+  *merged = mr0;
+}
+
+// Item number r of sequence b: later row tiles (which see more) first; a row tile's chunks and
+// heads side by side.
+__device__ __forceinline__ ChunkItem chunk_item_of(const ChunkArgs& a, int b, int r, int rt, int k, int part_row) {
+  ChunkItem it;
+  it.b = b;
+  chunk_lengths(a, b, &it.row0, &it.n, &it.m);
+  it.n_chunk = k;
+  it.part_row = part_row;
+  it.c = r % k;
+  r /= k;
+  it.g = r % a.Hkv;
+  it.mt = rt - 1 - r / a.Hkv;
+  return it;
+}
+
+// The block's own work item by a scan of its own; false if there are fewer items than blocks.
+// Block 0 also writes the plan for the merge.  Every thread of the block calls it.
+template <int NT>
+__device__ __forceinline__ bool chunk_find_item(const ChunkArgs& a, ChunkItem* item) {
+  __shared__ int64_t sm_scan[2 * (NT / 32)];
+  __shared__ ChunkItem sm_item;
+  __shared__ int sm_found;
+  if (threadIdx.x == 0) sm_found = 0;
+  const bool writes = blockIdx.x == 0;
+  int64_t items, merged;
+  chunk_make_plan<NT>(a, sm_scan, &items, &merged, [&](int b, int first, int rt, int k, int part_row, int merge_row) {
+    const int r = static_cast<int>(blockIdx.x) - first;
+    if (r >= 0 && r < static_cast<int64_t>(rt) * a.Hkv * k) {
+      sm_item = chunk_item_of(a, b, r, rt, k, part_row);
       sm_found = 1;
     }
-    if (writes_plan) {  // uniform in the block
-      int64_t mx = my_rows, my = 0, tmx, tmy;
-      chunk_block_scan<NT>(mx, my, &tmx, &tmy, sm_scan);
-      if (b < a.B) {
-        a.plan[3 * b] = static_cast<int>(merged + mx - my_rows);  // first row to merge
-        a.plan[3 * b + 1] = static_cast<int>(part0);              // first partial row
-        a.plan[3 * b + 2] = k;
-      }
-      merged += tmx;
-    }
-    items += tx;
-    parts += ty;
-    if (!writes_plan && blockIdx.x < items) break;  // uniform in the block
-  }
-  if (writes_plan && tid == 0) a.plan[3 * a.B] = static_cast<int>(merged);
+    if (writes) chunk_write_plan(a, b, first, rt, k, part_row, merge_row);
+  });
+  if (writes && threadIdx.x == 0) a.plan[kPlanMerged] = static_cast<int>(merged);
   __syncthreads();
   *item = sm_item;
   return sm_found != 0;
+}
+
+// Work item `idx` from the written plan (idx < its number of items).  Warp-collective: a
+// 32-way search for the last sequence whose first item is <= idx (sequences without items
+// share the first item of the one after them).
+__device__ __forceinline__ ChunkItem chunk_item_at(const ChunkArgs& a, int idx) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = a.B;  // the answer lies in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int b = lo + lane * step;
+    const bool before = lane * step < n && __ldcg(a.plan + kPlanHead + static_cast<int64_t>(kPlanRow) * b) <= idx;
+    const int hits = __popc(__ballot_sync(0xffffffffu, before));  // >= 1: a prefix of the lanes
+    const int skip = max(hits - 1, 0) * step;
+    lo += skip;
+    n = min(step, n - skip);
+  }
+  const int32_t* e = a.plan + kPlanHead + static_cast<int64_t>(kPlanRow) * lo;
+  return chunk_item_of(a, lo, idx - __ldcg(e), __ldcg(e + 3), __ldcg(e + 4), __ldcg(e + 2));
 }
 
 #endif  // __CUDACC__

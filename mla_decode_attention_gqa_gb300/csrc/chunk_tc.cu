@@ -10,7 +10,8 @@
 // well cost two more additions a pair of scores on the path that bounds the kernel.
 //
 // Bound by the tensor pipe for chunks of 128 and more rows (two 128 x 128 x D products per tile
-// of 128 tokens and 128 rows), by HBM for few rows.  Design (one CTA an SM, 384 threads):
+// of 128 tokens and 128 rows), by HBM for few rows.  Design (one persistent CTA an SM, 384
+// threads; warp 3 hands the work items to the other warps through shared memory):
 //   * rows of one KV head are (token, head of the group) pairs, the group padded to a power of
 //     two Gr, so that a 128-row tile is a TMA box of 128 / Gr tokens x Gr heads; every K/V byte
 //     is read once for the whole group;
@@ -29,10 +30,11 @@
 //     MMAs from one thread complete in order, so when S_k(i+1) has landed PV_k(i) is done and
 //     O_k may be rescaled;
 //   * optimistic softmax: p = 2^(s - m) against the maximum so far; only a row's first visible
-//     tile, and a tile whose p sum passes 2^16, take the tile's maximum, rescale O and redo.
+//     tile, and (again) a tile whose p sum passes 2^16, take the tile's maximum and rescale O.
 #include <climits>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "chunk_plan.cuh"
@@ -48,6 +50,7 @@ constexpr int kTN = 128;        // tokens per K/V tile
 constexpr int kHalf = kTN / 2;  // tokens per TMA box: a page holds a multiple of 64
 constexpr int kRowsTile = 128;  // rows per query tile (MMA M)
 constexpr int kThreads = 12 * 32;
+constexpr int kItemReaders = 11;  // warps that read the work items: both loaders, the issuer, the softmax
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;    // S_k (P_k over its first 64 columns) at kColS + 128 k
 constexpr uint32_t kColO = 256;  // O_k at kColO + 128 k
@@ -64,17 +67,34 @@ struct TcCfg {
   static constexpr int OFF_V = OFF_K + NST * TILE;
   static constexpr int OFF_BAR = OFF_V + NST * TILE;
   static constexpr int OFF_ML = OFF_BAR + 256;       // solo: group 1's (m, l) per row
-  static constexpr int SMEM = 1024 + OFF_ML + kRowsTile * 8;
-  static_assert(SMEM <= 226 * 1024, "shared memory budget (the work search has some of its own)");
+  static constexpr int OFF_ITEM = OFF_ML + kRowsTile * 8;
+  static constexpr int SMEM = 1024 + OFF_ITEM + 256;
+  static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
 
 template <class C>
 struct TcBars {
-  uint64_t q_full;
+  uint64_t item_full[2], item_empty[2];
+  uint64_t q_full, q_empty;
   uint64_t k_full[C::NST], k_empty[C::NST];
   uint64_t v_full[C::NST], v_empty[C::NST];
   uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t ml_full, o1_free;  // solo: group 1's (m, l) are written; group 0 has read them and O1
   uint32_t tmem_base;
+};
+
+// What every role needs of a work item (written by the scheduling warp).
+struct TcItem {
+  ChunkItem it;
+  ChunkTiles tl;
+  int m0;       // first row of the row tile
+  int pair;     // more than 128 rows
+  int i0;       // first tile of the chunk in tl's run
+  int n_tiles;  // tiles of the chunk
+  __device__ __forceinline__ int token(int i) const {  // first token of the chunk's tile i
+    const int x = i0 + i;
+    return (x < tl.n_first ? x : tl.win + (x - tl.n_first)) * kTN;
+  }
 };
 
 __device__ __forceinline__ void tma_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2, int c3) {
@@ -88,6 +108,8 @@ __device__ __forceinline__ void tma_4d(void* dst, const CUtensorMap* map, uint64
 template <int V>
 using Int = std::integral_constant<int, V>;
 
+// One item after the other through all the roles: a role that is done with an item goes on to
+// the next, so that loads and first scores of one item run under the epilogue of the one before.
 template <class C>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_tc_kernel(const __grid_constant__ PartialParams p, const __grid_constant__ CUtensorMap tmq,
@@ -96,38 +118,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   TcBars<C>* bars = reinterpret_cast<TcBars<C>*>(smem + C::OFF_BAR);
+  TcItem* items = reinterpret_cast<TcItem*>(smem + C::OFF_ITEM);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  ChunkItem it;
-  if (!chunk_find_item<kThreads>(p.ck, &it)) return;
   const int G = p.ck.G, Gr = p.ck.group_rows;
-  const int rows_total = it.n * Gr;
-  const int m0 = it.mt * 2 * kRowsTile;
-  const int m_last = min(m0 + 2 * kRowsTile, rows_total) - 1;
-  const bool pair = m_last - m0 >= kRowsTile;
-  const int pos0 = it.m - it.n;  // position of the sequence's first row
-  const ChunkTiles tl = chunk_tiles(p.ck.window, p.ck.n_sink, p.ck.cap, pos0 + m0 / Gr, pos0 + m_last / Gr, kTN);
-  const int per_chunk = (tl.n + it.n_chunk - 1) / it.n_chunk;
-  const int i0 = min(it.c * per_chunk, tl.n);
-  const int n_tiles = min(per_chunk, tl.n - i0);
-  auto tile_token = [&](int i) -> int {  // first token of the chunk's tile i
-    const int x = i0 + i;
-    return (x < tl.n_first ? x : tl.win + (x - tl.n_first)) * kTN;
-  };
 
   if (threadIdx.x == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars->item_full[s], 1);
+      mbar_init(&bars->item_empty[s], kItemReaders);
+      mbar_init(&bars->s_full[s], 1);
+      mbar_init(&bars->p_full[s], kRowsTile);
+      mbar_init(&bars->pv_done[s], 1);
+    }
     mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_empty, 1);
     for (int s = 0; s < NST; ++s) {
       mbar_init(&bars->k_full[s], 1);
       mbar_init(&bars->k_empty[s], 1);
       mbar_init(&bars->v_full[s], 1);
       mbar_init(&bars->v_empty[s], 1);
     }
-    for (int k = 0; k < 2; ++k) {
-      mbar_init(&bars->s_full[k], 1);
-      mbar_init(&bars->p_full[k], kRowsTile);
-      mbar_init(&bars->pv_done[k], 1);
-    }
+    mbar_init(&bars->ml_full, kRowsTile);
+    mbar_init(&bars->o1_free, kRowsTile);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -139,243 +151,354 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_after_sync();
   const uint32_t tmem = bars->tmem_base;
 
-  if (warp == 0 || warp == 2) {
+  // Item r of this CTA has come (false: there is none, or a wait gave up) / is no longer read by
+  // this warp.  The whole warp calls them.
+  auto item_here = [&](int r) -> bool {
+    const int s = r & 1;
+    if (!__all_sync(0xffffffffu, mbar_wait(&bars->item_full[s], (r >> 1) & 1, p.err, kDevErrFullWait))) return false;
+    return items[s].it.b >= 0;
+  };
+  auto item_done = [&](int r) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->item_empty[r & 1]);
+  };
+  auto next_item = [&](int r, TcItem* out) -> bool {
+    if (!item_here(r)) return false;
+    *out = items[r & 1];
+    item_done(r);
+    return true;
+  };
+
+  if (warp == 3) {
+    // ------------------------------------------------------------ scheduler
+    // Items are handed out one by one (a counter that the plan kernel cleared), so that CTAs
+    // with light items take more; one item ahead of the other roles.
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan is written
+    const int total = __ldcg(p.ck.plan + kPlanItems);
+    for (int r = 0;; ++r) {
+      const int s = r & 1;
+      if (r >= 2 && !__all_sync(0xffffffffu, mbar_wait(&bars->item_empty[s], ((r >> 1) - 1) & 1, p.err, kDevErrEmptyWait)))
+        break;
+      int idx = blockIdx.x;
+      if (r > 0) {
+        if (lane == 0) idx = static_cast<int>(gridDim.x) + atomicAdd(p.ck.plan + kPlanNext, 1);
+        idx = __shfl_sync(0xffffffffu, idx, 0);
+      }
+      TcItem t;
+      t.it.b = -1;
+      if (idx < total) {
+        t.it = chunk_item_at(p.ck, idx);
+        t.m0 = t.it.mt * 2 * kRowsTile;
+        const int m_last = min(t.m0 + 2 * kRowsTile, t.it.n * Gr) - 1;
+        t.pair = m_last - t.m0 >= kRowsTile ? 1 : 0;
+        const int pos0 = t.it.m - t.it.n;
+        t.tl = chunk_tiles(p.ck.window, p.ck.n_sink, p.ck.cap, pos0 + t.m0 / Gr, pos0 + m_last / Gr, kTN);
+        const int per = (t.tl.n + t.it.n_chunk - 1) / t.it.n_chunk;
+        t.i0 = min(t.it.c * per, t.tl.n);
+        t.n_tiles = min(per, t.tl.n - t.i0);
+      }
+      if (lane == 0) {
+        items[s] = t;
+        mbar_arrive(&bars->item_full[s]);
+      }
+      __syncwarp();
+      if (t.it.b < 0) break;
+    }
+  } else if (warp == 0 || warp == 2) {
     // ------------------------------------------------------------ TMA producers: 0 Q and K, 2 V
     // A warp each, so that neither waits for the other's ring; the pages and rows of the next
     // tile (four integer divisions and two dependent loads) are looked up behind this tile's
     // copies, not between a freed stage and its refill, which bounds a two-stage ring.
-    if (n_tiles > 0) {
-      const bool is_k = warp == 0;
-      const CUtensorMap* map = is_k ? &tmk : &tmv;
-      uint64_t* full = is_k ? bars->k_full : bars->v_full;
-      uint64_t* empty = is_k ? bars->k_empty : bars->v_empty;
-      uint8_t* ring = smem + (is_k ? C::OFF_K : C::OFF_V);
-      if (tc::elect_one()) {
-        tma_prefetch_desc(map);
-        if (is_k) {
-          tma_prefetch_desc(&tmq);
-          const int nq = pair ? 2 : 1;
-          mbar_arrive_expect_tx(&bars->q_full, nq * C::TILE);
-          for (int k = 0; k < nq; ++k)
-            for (int bx = 0; bx < NB; ++bx)
-              tma_4d(smem + k * C::TILE + bx * C::BOX, &tmq, &bars->q_full, bx * 64, it.g * G,
-                     it.row0 + (m0 + k * kRowsTile) / Gr, 0);
-        }
-      }
-      __syncwarp();
+    const bool is_k = warp == 0;
+    const CUtensorMap* map = is_k ? &tmk : &tmv;
+    uint64_t* full = is_k ? bars->k_full : bars->v_full;
+    uint64_t* empty = is_k ? bars->k_empty : bars->v_empty;
+    uint8_t* ring = smem + (is_k ? C::OFF_K : C::OFF_V);
+    if (tc::elect_one()) {
+      tma_prefetch_desc(map);
+      if (is_k) tma_prefetch_desc(&tmq);
+    }
+    __syncwarp();
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.err, kDevErrEmptyWait));
+    };
+    TcItem t;
+    int done = 0, nq = 0;  // tiles and query tiles loaded so far
+    bool ok = true;
+    for (int r = 0; ok && next_item(r, &t); ++r) {
+      if (t.n_tiles == 0) continue;
       int page[2], at[2];  // of a tile's two halves
       auto look_up = [&](int i) {
-        const int t = tile_token(i);
+        const int a = t.token(i);
         // a second half at or past the capacity holds no token: it takes the first one's page
         // instead of an entry behind the table's row
-        const int t2 = t + kHalf < p.ck.cap ? t + kHalf : t;
-        at[0] = t % p.block_len;
-        at[1] = t2 % p.block_len;
-        page[0] = kv_page_of(p, it.b, t);
-        page[1] = kv_page_of(p, it.b, t2);
+        const int b = a + kHalf < p.ck.cap ? a + kHalf : a;
+        at[0] = a % p.block_len;
+        at[1] = b % p.block_len;
+        page[0] = kv_page_of(p, t.it.b, a);
+        page[1] = kv_page_of(p, t.it.b, b);
       };
       look_up(0);
-      int issued = 0;
-      for (int i = 0; i < n_tiles; ++i) {
-        const int s = i % NST;
-        if (i >= NST && !__all_sync(0xffffffffu, mbar_wait(&empty[s], ((i / NST) - 1) & 1, p.err, kDevErrEmptyWait))) break;
+      if (is_k) {
+        // the item before has no scores left to compute
+        if (nq > 0 && !wait_all(&bars->q_empty, (nq - 1) & 1)) break;
+        if (tc::elect_one()) {
+          mbar_arrive_expect_tx(&bars->q_full, (1 + t.pair) * C::TILE);
+          for (int k = 0; k <= t.pair; ++k)
+            for (int bx = 0; bx < NB; ++bx)
+              tma_4d(smem + k * C::TILE + bx * C::BOX, &tmq, &bars->q_full, bx * 64, t.it.g * G,
+                     t.it.row0 + (t.m0 + k * kRowsTile) / Gr, 0);
+        }
+        __syncwarp();
+        ++nq;
+      }
+      for (int i = 0; i < t.n_tiles; ++i) {
+        const int s = done % NST;
+        ok = done < NST || wait_all(&empty[s], ((done / NST) - 1) & 1);
+        if (!ok) break;
         if (tc::elect_one()) {
           mbar_arrive_expect_tx(&full[s], C::TILE);
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
             for (int bx = 0; bx < NB; ++bx)
-              tma_4d(ring + s * C::TILE + bx * C::BOX + hf * (C::BOX / 2), map, &full[s], bx * 64, at[hf], it.g, page[hf]);
+              tma_4d(ring + s * C::TILE + bx * C::BOX + hf * (C::BOX / 2), map, &full[s], bx * 64, at[hf], t.it.g,
+                     page[hf]);
         }
         __syncwarp();
-        issued = i + 1;
-        if (issued < n_tiles) look_up(issued);
+        ++done;
+        if (i + 1 < t.n_tiles) look_up(i + 1);
       }
-      // every issued copy lands before the CTA may exit
-      for (int i = max(0, issued - NST); i < issued; ++i)
-        if (!mbar_wait(&full[i % NST], (i / NST) & 1, p.err, kDevErrDrainWait)) break;
-      if (is_k) mbar_wait(&bars->q_full, 0, p.err, kDevErrDrainWait);
     }
+    // every issued copy lands before the CTA may exit
+    for (int i = max(0, done - NST); i < done; ++i)
+      if (!mbar_wait(&full[i % NST], (i / NST) & 1, p.err, kDevErrDrainWait)) break;
+    if (is_k && nq > 0) mbar_wait(&bars->q_full, (nq - 1) & 1, p.err, kDevErrDrainWait);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    // The whole warp waits, one elected lane issues; stages are compile-time constants (the
-    // loops are unrolled by the ring depth), so every operand is a constant offset.
-    if (n_tiles > 0) {
-      const uint32_t idesc_s = tc::idesc_f16(128, kTN, true, false, false);
-      const uint32_t idesc_pv = tc::idesc_f16(128, D, true, false, true);
-      const uint64_t qd = tc::smem_desc_sw128(smem_u32(smem), 16, 1024);
-      const uint64_t kd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
-      const uint64_t vd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_V), C::BOX, 1024);
-      auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-        return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.err, kDevErrFullWait));
-      };
-      auto issue_s = [&](int k, int q, int stage) {  // S_k = Q_q K^T
+    // The whole warp waits, one elected lane issues; a tile's stage is a compile-time constant,
+    // so every operand is a constant offset.
+    const uint32_t idesc_s = tc::idesc_f16(128, kTN, true, false, false);
+    const uint32_t idesc_pv = tc::idesc_f16(128, D, true, false, true);
+    const uint64_t qd = tc::smem_desc_sw128(smem_u32(smem), 16, 1024);
+    const uint64_t kd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
+    const uint64_t vd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_V), C::BOX, 1024);
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.err, kDevErrFullWait));
+    };
+    auto issue_s = [&](int k, int q, int stage) {  // S_k = Q_q K^T
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t in_box = (ks >> 2) * C::BOX + (ks & 3) * 32;
-          tc::mma_f16_ss(tmem + kColS + 128 * k, qd + static_cast<uint64_t>((q * C::TILE + in_box) >> 4),
-                         kd + static_cast<uint64_t>((stage * C::TILE + in_box) >> 4), idesc_s, ks > 0 ? 1u : 0u);
-        }
-      };
-      auto issue_pv = [&](int k, int stage, uint32_t acc0) {  // O_k += P_k V
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const uint32_t in_box = (ks >> 2) * C::BOX + (ks & 3) * 32;
+        tc::mma_f16_ss(tmem + kColS + 128 * k, qd + static_cast<uint64_t>((q * C::TILE + in_box) >> 4),
+                       kd + static_cast<uint64_t>((stage * C::TILE + in_box) >> 4), idesc_s, ks > 0 ? 1u : 0u);
+      }
+      tc::mma_commit(smem_u32(&bars->s_full[k]));
+    };
+    auto issue_pv = [&](int k, int stage, uint32_t acc0) {  // O_k += P_k V
 #pragma unroll
-        for (int ks = 0; ks < kTN / 16; ++ks)
-          tc::mma_f16_ts(tmem + kColO + 128 * k, tmem + kColS + 128 * k + ks * 8,
-                         vd + static_cast<uint64_t>((stage * C::TILE + ks * 2048) >> 4), idesc_pv, ks > 0 ? 1u : acc0);
-      };
-      bool ok = wait_all(&bars->q_full, 0);
-      if (pair) {
-        // tile i in stage ST: PV0(i), S0(i+1), PV1(i), S1(i+1)
-        auto tile = [&](auto st, int i) {
-          constexpr int ST = decltype(st)::value, NX = (ST + 1) % NST;
-          ok = wait_all(&bars->p_full[0], i & 1) && wait_all(&bars->v_full[ST], (i / NST) & 1);
-          if (!ok) return;
-          tc::fence_after_sync();
+      for (int ks = 0; ks < kTN / 16; ++ks)
+        tc::mma_f16_ts(tmem + kColO + 128 * k, tmem + kColS + 128 * k + ks * 8,
+                       vd + static_cast<uint64_t>((stage * C::TILE + ks * 2048) >> 4), idesc_pv, ks > 0 ? 1u : acc0);
+      tc::mma_commit(smem_u32(&bars->pv_done[k]));
+    };
+    // runs fn with tile number x's stage as a constant
+    auto at_stage = [&](int x, auto&& fn) {
+      const int s = x % NST;
+      if (s == 0) fn(Int<0>{});
+      if (s == 1) fn(Int<1>{});
+      if constexpr (NST == 4) {
+        if (s == 2) fn(Int<2>{});
+        if (s == 3) fn(Int<3>{});
+      }
+    };
+    TcItem t;
+    int base = 0, nq = 0;          // tiles and query tiles of the items before
+    uint32_t np[2] = {0u, 0u};     // tiles of each softmax group so far
+    bool ok = true;
+    for (int r = 0; ok && next_item(r, &t); ++r) {
+      const int n = t.n_tiles;
+      if (n == 0) continue;
+      ok = wait_all(&bars->q_full, nq & 1);
+      if (!ok) break;
+      ++nq;
+      // scores of tile x (both groups, or group x & 1 in solo mode); the last ones free Q
+      if (t.pair) {
+        // tile i: PV0(i), S0(i+1), PV1(i), S1(i+1)
+        ok = wait_all(&bars->k_full[base % NST], (base / NST) & 1);
+        if (!ok) break;
+        tc::fence_after_sync();
+        at_stage(base, [&](auto st) {
+          constexpr int ST = decltype(st)::value;
           if (tc::elect_one()) {
-            issue_pv(0, ST, i > 0 ? 1u : 0u);
-            tc::mma_commit(smem_u32(&bars->pv_done[0]));
+            issue_s(0, 0, ST);
+            issue_s(1, 1, ST);
+            tc::mma_commit(smem_u32(&bars->k_empty[ST]));
+            if (n == 1) tc::mma_commit(smem_u32(&bars->q_empty));
           }
           __syncwarp();
-          const bool more = i + 1 < n_tiles;
+        });
+        auto tile = [&](auto st, int i) {
+          constexpr int ST = decltype(st)::value, NX = (ST + 1) % NST;
+          const int x = base + i;
+          ok = wait_all(&bars->p_full[0], np[0] & 1) && wait_all(&bars->v_full[ST], (x / NST) & 1);
+          if (!ok) return;
+          ++np[0];
+          tc::fence_after_sync();
+          if (tc::elect_one()) issue_pv(0, ST, i > 0 ? 1u : 0u);
+          __syncwarp();
+          const bool more = i + 1 < n;
           if (more) {
-            ok = wait_all(&bars->k_full[NX], ((i + 1) / NST) & 1);
+            ok = wait_all(&bars->k_full[NX], ((x + 1) / NST) & 1);
             if (!ok) return;
             tc::fence_after_sync();
-            if (tc::elect_one()) {
-              issue_s(0, 0, NX);
-              tc::mma_commit(smem_u32(&bars->s_full[0]));
-            }
+            if (tc::elect_one()) issue_s(0, 0, NX);
             __syncwarp();
           }
-          ok = wait_all(&bars->p_full[1], i & 1);
+          ok = wait_all(&bars->p_full[1], np[1] & 1);
           if (!ok) return;
+          ++np[1];
           tc::fence_after_sync();
           if (tc::elect_one()) {
             issue_pv(1, ST, i > 0 ? 1u : 0u);
-            tc::mma_commit(smem_u32(&bars->pv_done[1]));
             tc::mma_commit(smem_u32(&bars->v_empty[ST]));
             if (more) {
               issue_s(1, 1, NX);
-              tc::mma_commit(smem_u32(&bars->s_full[1]));
               tc::mma_commit(smem_u32(&bars->k_empty[NX]));
+              if (i + 2 == n) tc::mma_commit(smem_u32(&bars->q_empty));
             }
           }
           __syncwarp();
         };
-        ok = ok && wait_all(&bars->k_full[0], 0);
-        if (ok) {
-          tc::fence_after_sync();
-          if (tc::elect_one()) {
-            issue_s(0, 0, 0);
-            tc::mma_commit(smem_u32(&bars->s_full[0]));
-            issue_s(1, 1, 0);
-            tc::mma_commit(smem_u32(&bars->s_full[1]));
-            tc::mma_commit(smem_u32(&bars->k_empty[0]));
+        // unrolled by the ring depth, entered at the stage that the items before left
+        int i = 0;
+        const int enter = base % NST;
+        for (bool first = true; ok && i < n; first = false) {
+          if (!first || enter <= 0) {
+            tile(Int<0>{}, i);
+            if (!ok || ++i >= n) break;
           }
-          __syncwarp();
-        }
-        for (int i = 0; i < n_tiles && ok; i += NST) {
-          tile(Int<0>{}, i);
-          if (ok && i + 1 < n_tiles) tile(Int<1>{}, i + 1);
+          if (!first || enter <= 1) {
+            tile(Int<1>{}, i);
+            if (!ok || ++i >= n) break;
+          }
           if constexpr (NST == 4) {
-            if (ok && i + 2 < n_tiles) tile(Int<2>{}, i + 2);
-            if (ok && i + 3 < n_tiles) tile(Int<3>{}, i + 3);
+            if (!first || enter <= 2) {
+              tile(Int<2>{}, i);
+              if (!ok || ++i >= n) break;
+            }
+            tile(Int<3>{}, i);
+            ++i;
           }
         }
       } else {
-        // tile i in stage ST belongs to group i & 1: PV(i), then S(i + 2)
-        auto scores = [&](auto st, int i) {
-          constexpr int ST = decltype(st)::value;
-          ok = wait_all(&bars->k_full[ST], (i / NST) & 1);
-          if (!ok) return;
-          tc::fence_after_sync();
-          if (tc::elect_one()) {
-            issue_s(ST & 1, 0, ST);
-            tc::mma_commit(smem_u32(&bars->s_full[ST & 1]));
-            tc::mma_commit(smem_u32(&bars->k_empty[ST]));
-          }
-          __syncwarp();
+        // tile i belongs to group i & 1: PV(i), then S(i + 2)
+        auto scores = [&](int i) {
+          at_stage(base + i, [&](auto st) {
+            constexpr int ST = decltype(st)::value;
+            ok = wait_all(&bars->k_full[ST], ((base + i) / NST) & 1);
+            if (!ok) return;
+            tc::fence_after_sync();
+            if (tc::elect_one()) {
+              if (i & 1)
+                issue_s(1, 0, ST);
+              else
+                issue_s(0, 0, ST);
+              tc::mma_commit(smem_u32(&bars->k_empty[ST]));
+              if (i + 1 == n) tc::mma_commit(smem_u32(&bars->q_empty));
+            }
+            __syncwarp();
+          });
         };
-        auto tile = [&](auto st, int i) {
-          constexpr int ST = decltype(st)::value, K = ST & 1;
-          ok = wait_all(&bars->p_full[K], (i >> 1) & 1) && wait_all(&bars->v_full[ST], (i / NST) & 1);
-          if (!ok) return;
-          tc::fence_after_sync();
-          if (tc::elect_one()) {
-            issue_pv(K, ST, i > 1 ? 1u : 0u);
-            tc::mma_commit(smem_u32(&bars->pv_done[K]));
-            tc::mma_commit(smem_u32(&bars->v_empty[ST]));
-          }
-          __syncwarp();
-          if (i + 2 < n_tiles) scores(Int<(ST + 2) % NST>{}, i + 2);
-        };
-        if (ok) scores(Int<0>{}, 0);
-        if (ok && n_tiles > 1) scores(Int<1>{}, 1);
-        for (int i = 0; i < n_tiles && ok; i += NST) {
-          tile(Int<0>{}, i);
-          if (ok && i + 1 < n_tiles) tile(Int<1>{}, i + 1);
-          if constexpr (NST == 4) {
-            if (ok && i + 2 < n_tiles) tile(Int<2>{}, i + 2);
-            if (ok && i + 3 < n_tiles) tile(Int<3>{}, i + 3);
-          }
+        scores(0);
+        if (ok && n > 1) scores(1);
+        for (int i = 0; i < n && ok; ++i) {
+          at_stage(base + i, [&](auto st) {
+            constexpr int ST = decltype(st)::value;
+            const int k = i & 1;
+            ok = wait_all(&bars->p_full[k], np[k] & 1) && wait_all(&bars->v_full[ST], ((base + i) / NST) & 1);
+            if (!ok) return;
+            ++np[k];
+            tc::fence_after_sync();
+            if (tc::elect_one()) {
+              if (k)
+                issue_pv(1, ST, i > 1 ? 1u : 0u);
+              else
+                issue_pv(0, ST, i > 1 ? 1u : 0u);
+              tc::mma_commit(smem_u32(&bars->v_empty[ST]));
+            }
+            __syncwarp();
+          });
+          if (ok && i + 2 < n) scores(i + 2);
         }
       }
+      base += n;
     }
-  } else if (warp >= 4) {
+  } else {
     // ------------------------------------------------------------ softmax groups
     const int k = (warp - 4) >> 2;
     const int lgrp = warp & 3;         // TMEM lane group of this warp
     const int row = lgrp * 32 + lane;  // row inside the query tile
-    const int m = m0 + (pair ? k * kRowsTile : 0) + row;
-    const int t_q = m / Gr, hg = m % Gr;
-    const bool valid = m < rows_total && hg < G;
-    const int pos = pos0 + t_q;
-    // visible tokens of this row: [lo_row, hi_row) and [0, sink_row)
-    const int hi_row = valid ? min(max(pos + 1, 0), p.ck.cap) : 0;
-    const int lo_row = (valid && p.ck.window > 0 && pos >= p.ck.window) ? pos - p.ck.window + 1 : 0;
-    const int sink_row = min(p.ck.n_sink, hi_row);
-    const bool active = __any_sync(0xffffffffu, valid);  // some row of this warp exists
-    const int hi_min = __reduce_min_sync(0xffffffffu, valid ? hi_row : INT_MAX);
-    const int hi_max = __reduce_max_sync(0xffffffffu, hi_row);
-    const int lo_max = __reduce_max_sync(0xffffffffu, lo_row);
-    const int sink_min = __reduce_min_sync(0xffffffffu, valid ? sink_row : INT_MAX);
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(lgrp * 32) << 16);
     const uint32_t s_col = t_lane + kColS + 128 * k;
     const uint32_t o_col = t_lane + kColO + 128 * k;
     const float sl = p.scale_log2;
-    float m_used = -INFINITY, l_sum = 0.f;
+    float* ml = reinterpret_cast<float*>(smem + C::OFF_ML);
+    int base = 0;              // tiles of the items before
+    uint32_t np = 0, np1 = 0;  // tiles of this group, and of group 1, so far
+    uint32_t n_solo = 0;
     bool ok = true;
-    const int first = pair ? 0 : k, step = pair ? 1 : 2;  // this group's tiles
+    for (int r = 0; ok && item_here(r); ++r) {
+      const TcItem& t = items[r & 1];  // read in place: registers are short here
+      const int rows_total = t.it.n * Gr, pos0 = t.it.m - t.it.n;
+      const bool pair = t.pair != 0;
+      const int m = t.m0 + (pair ? k * kRowsTile : 0) + row;
+      const int t_q = m / Gr, hg = m % Gr;
+      const bool valid = m < rows_total && hg < G;
+      const int pos = pos0 + t_q;
+      // visible tokens of this row: [lo_row, hi_row) and [0, sink_row)
+      const int hi_row = valid ? min(max(pos + 1, 0), p.ck.cap) : 0;
+      const int lo_row = (valid && p.ck.window > 0 && pos >= p.ck.window) ? pos - p.ck.window + 1 : 0;
+      const int sink_row = min(p.ck.n_sink, hi_row);
+      const bool active = __any_sync(0xffffffffu, valid);  // some row of this warp exists
+      const int hi_min = __reduce_min_sync(0xffffffffu, valid ? hi_row : INT_MAX);
+      const int hi_max = __reduce_max_sync(0xffffffffu, hi_row);
+      const int lo_max = __reduce_max_sync(0xffffffffu, lo_row);
+      const int lo_min = __reduce_min_sync(0xffffffffu, valid ? lo_row : INT_MAX);
+      const int sink_min = __reduce_min_sync(0xffffffffu, valid ? sink_row : INT_MAX);
+      const int sink_max = __reduce_max_sync(0xffffffffu, sink_row);
+      float m_used = -INFINITY, l_sum = 0.f;
+      const int step = pair ? 1 : 2;  // this group's tiles: all, or every other
 
-    int j = 0;  // tiles done
-    for (int i = first; i < n_tiles; i += step, ++j) {
-      const int t0 = tile_token(i);
-      ok = mbar_wait(&bars->s_full[k], j & 1, p.err, kDevErrFullWait);
-      if (!ok) break;
-      tc::fence_after_sync();
-      if (active) {
-        const bool none = hi_max <= t0;  // no row of the warp reaches this tile
-        const bool need_mask = hi_min < t0 + kTN || (t0 < lo_max && t0 + kTN > sink_min);
-        const int c_lo = min(max(lo_row - t0, 0), kTN);
-        const unsigned span = static_cast<unsigned>(max(min(max(hi_row - t0, 0), kTN) - c_lo, 0));
-        const int c_sink = min(max(sink_row - t0, 0), kTN);
-        auto visible = [&](int col) -> bool { return static_cast<unsigned>(col - c_lo) < span || col < c_sink; };
-        uint32_t pk[kTN / 2];
-        uint64_t ls[2] = {0ull, 0ull};  // fp32 pair sums of p
-        const float base0 = (m_used == -INFINITY) ? 0.f : m_used;
-        // masked: a compile-time flag, so that tiles that every row sees carry no test
-        auto pass = [&](auto masked) {
-#pragma unroll
-          for (int cc = 0; cc < kTN / 32; ++cc) {
-            uint32_t r[2][16];
-            tc::tmem_ld16(s_col + 32 * cc, r[0]);
-            tc::tmem_ld16(s_col + 32 * cc + 16, r[1]);
+      int j = 0;  // tiles of the item done
+      for (int i = pair ? 0 : k; i < t.n_tiles; i += step, ++j) {
+        const int t0 = t.token(i);
+        ok = mbar_wait(&bars->s_full[k], np & 1, p.err, kDevErrFullWait);
+        if (!ok) break;
+        ++np;
+        tc::fence_after_sync();
+        if (active) {
+          const bool need_mask = hi_min < t0 + kTN || (t0 < lo_max && t0 + kTN > sink_min);
+          const int c_lo = min(max(lo_row - t0, 0), kTN);
+          const unsigned span = static_cast<unsigned>(max(min(max(hi_row - t0, 0), kTN) - c_lo, 0));
+          const int c_sink = min(max(sink_row - t0, 0), kTN);
+          auto visible = [&](int col) -> bool { return static_cast<unsigned>(col - c_lo) < span || col < c_sink; };
+          const bool row_vis = valid && (!need_mask || span > 0u || c_sink > 0);
+          uint32_t pk[kTN / 2];
+          uint64_t ls[2];  // fp32 pair sums of p
+          // 32 columns from TMEM as packed P.  masked: a compile-time flag, so that columns that
+          // every row sees carry no test
+          auto columns = [&](auto masked, auto chunk, float base0) {
+            constexpr int cc = decltype(chunk)::value;
+            uint32_t x[2][16];
+            tc::tmem_ld16(s_col + 32 * cc, x[0]);
+            tc::tmem_ld16(s_col + 32 * cc + 16, x[1]);
             tc::tmem_wait_ld();
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const int col = 32 * cc + 2 * e;
-              float v0 = __uint_as_float(r[e >> 3][(2 * e) & 15]);
-              float v1 = __uint_as_float(r[e >> 3][(2 * e + 1) & 15]);
+              float v0 = __uint_as_float(x[e >> 3][(2 * e) & 15]);
+              float v1 = __uint_as_float(x[e >> 3][(2 * e + 1) & 15]);
               if constexpr (decltype(masked)::value) {
                 v0 = visible(col) ? v0 : -INFINITY;
                 v1 = visible(col + 1) ? v1 : -INFINITY;
@@ -386,79 +509,89 @@ __global__ void __launch_bounds__(kThreads, 1)
               ls[e & 1] = add_f32x2(ls[e & 1], p0, p1);
               pk[16 * cc + e] = pack_bf16(p0, p1);
             }
-          }
-        };
-        if (none) {
+          };
+          // What the warp's rows see of 32 columns: 0 nothing, 2 all of them, 1 some.  The rows of a
+          // warp are few tokens, so at most two of a tile's four chunks are mixed at an edge.
+          auto sees = [&](int cc) -> int {
+            const int a = t0 + 32 * cc, b = a + 32;
+            if (hi_max <= a || (lo_min >= b && sink_max <= a)) return 0;
+            return (hi_min >= b && (lo_max <= a || sink_min >= b)) ? 2 : 1;
+          };
+          auto edge_columns = [&](auto chunk, float base0) {
+            constexpr int cc = decltype(chunk)::value;
+            const int mode = sees(cc);
+            if (mode == 2) {
+              columns(std::false_type{}, chunk, base0);
+            } else if (mode == 1) {
+              columns(std::true_type{}, chunk, base0);
+            } else {
 #pragma unroll
-          for (int e = 0; e < kTN / 2; ++e) pk[e] = 0u;
-        } else if (need_mask) {
-          pass(std::true_type{});
-        } else {
-          pass(std::false_type{});
-        }
-        const float tile_sum = sum_f32x2(ls[0]) + sum_f32x2(ls[1]);
-        const bool row_vis = valid && !none && (!need_mask || span > 0u || c_sink > 0);
-        const bool need = row_vis && (m_used == -INFINITY || !(tile_sum <= kTileSumLimit));
-        if (__any_sync(0xffffffffu, need)) {
-          // the tile's true maximum, O and l rescaled to it, and this tile's P again from S
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-          for (int cc = 0; cc < kTN / 32; ++cc) {
-            uint32_t r[2][16];
-            tc::tmem_ld16(s_col + 32 * cc, r[0]);
-            tc::tmem_ld16(s_col + 32 * cc + 16, r[1]);
-            tc::tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int col = 32 * cc + 2 * e;
-              const float v0 = visible(col) ? __uint_as_float(r[e >> 3][(2 * e) & 15]) : -INFINITY;
-              const float v1 = visible(col + 1) ? __uint_as_float(r[e >> 3][(2 * e + 1) & 15]) : -INFINITY;
-              mx[e & 3] = fmax3(mx[e & 3], v0, v1);
+              for (int e = 0; e < 16; ++e) pk[16 * cc + e] = 0u;
             }
-          }
-          const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;  // sl > 0
-          const float m_new = need ? fmaxf(m_used, tmax) : m_used;
-          if (j > 0) {
-            // PV_k of this group's tile before ran before these scores: O_k is final here
-            const float alpha = need ? fast_exp2(m_used - ((m_new == -INFINITY) ? 0.f : m_new)) : 1.f;
+          };
+          // a row's first visible tile, or one whose p sum passed the limit, takes the tile's
+          // true maximum first and rescales O and l to it
+          bool need = row_vis && m_used == -INFINITY;
+          for (bool again = false;; again = true) {
+            if (__any_sync(0xffffffffu, need)) {
+              float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-            for (int c = 0; c < D / 16; c += 2) {
-              uint32_t r[2][16];
-              tc::tmem_ld16(o_col + 16 * c, r[0]);
-              tc::tmem_ld16(o_col + 16 * (c + 1), r[1]);
-              tc::tmem_wait_ld();
+              for (int cc = 0; cc < kTN / 32; ++cc) {
+                const int mode = need_mask ? sees(cc) : 2;
+                if (mode == 0) continue;
+                uint32_t x[2][16];
+                tc::tmem_ld16(s_col + 32 * cc, x[0]);
+                tc::tmem_ld16(s_col + 32 * cc + 16, x[1]);
+                tc::tmem_wait_ld();
+                if (mode == 1) {
 #pragma unroll
-              for (int h2 = 0; h2 < 2; ++h2)
+                  for (int e = 0; e < 32; ++e)
+                    if (!visible(32 * cc + e)) x[e >> 4][e & 15] = __float_as_uint(-INFINITY);
+                }
 #pragma unroll
-                for (int e = 0; e < 16; ++e) r[h2][e] = __float_as_uint(__uint_as_float(r[h2][e]) * alpha);
-              tc::tmem_st16(o_col + 16 * c, r[0]);
-              tc::tmem_st16(o_col + 16 * (c + 1), r[1]);
-            }
-            tc::tmem_wait_st();
-            l_sum *= alpha;
-          }
-          m_used = m_new;
-          const float base = (m_used == -INFINITY) ? 0.f : m_used;
-          ls[0] = ls[1] = 0ull;
+                for (int e = 0; e < 16; ++e)
+                  mx[e & 3] = fmax3(mx[e & 3], __uint_as_float(x[e >> 3][(2 * e) & 15]),
+                                    __uint_as_float(x[e >> 3][(2 * e + 1) & 15]));
+              }
+              const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;  // sl > 0
+              const float m_new = need ? fmaxf(m_used, tmax) : m_used;
+              // PV_k of this group's tile before ran before these scores: O_k is final here
+              if (__any_sync(0xffffffffu, need && m_used != -INFINITY)) {
+                const float alpha = (need && m_used != -INFINITY) ? fast_exp2(m_used - m_new) : 1.f;
 #pragma unroll 1
-          for (int cc = 0; cc < kTN / 32; ++cc) {
-            uint32_t r[2][16];
-            tc::tmem_ld16(s_col + 32 * cc, r[0]);
-            tc::tmem_ld16(s_col + 32 * cc + 16, r[1]);
-            tc::tmem_wait_ld();
-            uint32_t w[16];
+                for (int c = 0; c < D / 16; c += 2) {
+                  uint32_t x[2][16];
+                  tc::tmem_ld16(o_col + 16 * c, x[0]);
+                  tc::tmem_ld16(o_col + 16 * (c + 1), x[1]);
+                  tc::tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int col = 32 * cc + 2 * e;
-              const float v0 = visible(col) ? __uint_as_float(r[e >> 3][(2 * e) & 15]) : -INFINITY;
-              const float v1 = visible(col + 1) ? __uint_as_float(r[e >> 3][(2 * e + 1) & 15]) : -INFINITY;
-              const float p0 = fast_exp2(fmaf(v0, sl, -base)), p1 = fast_exp2(fmaf(v1, sl, -base));
-              ls[e & 1] = add_f32x2(ls[e & 1], p0, p1);
-              w[e] = pack_bf16(p0, p1);
+                  for (int h2 = 0; h2 < 2; ++h2)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) x[h2][e] = __float_as_uint(__uint_as_float(x[h2][e]) * alpha);
+                  tc::tmem_st16(o_col + 16 * c, x[0]);
+                  tc::tmem_st16(o_col + 16 * (c + 1), x[1]);
+                }
+                tc::tmem_wait_st();
+                l_sum *= alpha;
+              }
+              m_used = m_new;
             }
-            tc::tmem_st16(s_col + 16 * cc, w);  // S columns 32 cc.. were read before P 16 cc.. is written
+            ls[0] = ls[1] = 0ull;
+            const float base0 = (m_used == -INFINITY) ? 0.f : m_used;
+            if (need_mask) {
+              edge_columns(Int<0>{}, base0);
+              edge_columns(Int<1>{}, base0);
+              edge_columns(Int<2>{}, base0);
+              edge_columns(Int<3>{}, base0);
+            } else {
+              columns(std::false_type{}, Int<0>{}, base0);
+              columns(std::false_type{}, Int<1>{}, base0);
+              columns(std::false_type{}, Int<2>{}, base0);
+              columns(std::false_type{}, Int<3>{}, base0);
+            }
+            need = row_vis && !(sum_f32x2(ls[0]) + sum_f32x2(ls[1]) <= kTileSumLimit);
+            if (again || !__any_sync(0xffffffffu, need)) break;
           }
-        } else {
 #pragma unroll
           for (int cc = 0; cc < kTN / 32; ++cc) {
             uint32_t w[16];
@@ -466,43 +599,51 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 16; ++e) w[e] = pk[16 * cc + e];
             tc::tmem_st16(s_col + 16 * cc, w);
           }
+          tc::tmem_wait_st();
+          l_sum += sum_f32x2(ls[0]) + sum_f32x2(ls[1]);
         }
-        tc::tmem_wait_st();
-        l_sum += sum_f32x2(ls[0]) + sum_f32x2(ls[1]);
-      }
-      const bool inside = (t0 >= tl.lo && t0 + kTN <= tl.hi) || t0 + kTN <= tl.sinks;
-      if (!inside && (k == 0 || !pair)) {
-        // tokens that no row of the item sees may hold anything: zero their V rows, so that p = 0
-        // really counts nothing
-        const int s = i % NST;
-        mbar_wait(&bars->v_full[s], (i / NST) & 1, p.err, kDevErrFullWait);
-        const int tok = t0 + row;
-        if (!((tok >= tl.lo && tok < tl.hi) || tok < tl.sinks)) {
-          uint8_t* vt = smem + C::OFF_V + s * C::TILE + row * 128;
-          for (int bx = 0; bx < NB; ++bx)
-            for (int cc = 0; cc < 8; ++cc)
-              *reinterpret_cast<uint4*>(vt + bx * C::BOX + cc * 16) = make_uint4(0u, 0u, 0u, 0u);
+        const bool inside = (t0 >= t.tl.lo && t0 + kTN <= t.tl.hi) || t0 + kTN <= t.tl.sinks;
+        if (!inside && (k == 0 || !pair)) {
+          // tokens that no row of the item sees may hold anything: zero their V rows, so that
+          // p = 0 really counts nothing
+          const int x = base + i, s = x % NST;
+          mbar_wait(&bars->v_full[s], (x / NST) & 1, p.err, kDevErrFullWait);
+          const int tok = t0 + row;
+          if (!((tok >= t.tl.lo && tok < t.tl.hi) || tok < t.tl.sinks)) {
+            uint8_t* vt = smem + C::OFF_V + s * C::TILE + row * 128;
+            for (int bx = 0; bx < NB; ++bx)
+              for (int cc = 0; cc < 8; ++cc)
+                *reinterpret_cast<uint4*>(vt + bx * C::BOX + cc * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
         }
-        fence_proxy_async_smem();
+        tc::fence_before_sync();
+        mbar_arrive(&bars->p_full[k]);
       }
-      tc::fence_before_sync();
-      mbar_arrive(&bars->p_full[k]);
-    }
+      base += t.n_tiles;
+      const int tiles1 = pair ? t.n_tiles : t.n_tiles / 2;  // group 1's
+      np1 += tiles1;
+      if (!ok) break;
 
-    // ---- epilogue: O / l and lse
-    auto tiles_of = [&](int kk) { return pair ? n_tiles : (n_tiles + 1 - kk) / 2; };
-    float* ml = reinterpret_cast<float*>(smem + C::OFF_ML);
-    // solo: the two groups' weights.  A group that summed nothing has l = 0 (its O may be
-    // anything); a NaN among the scores keeps l NaN, and the row is NaN
-    float a0 = 1.f, a1 = 0.f;
-    bool some0 = l_sum != 0.f, some1 = false;
-    if (!pair) {
-      if (k == 1) {
-        ml[2 * row] = m_used;
-        ml[2 * row + 1] = l_sum;
-      }
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (k == 0) {
+      // ---- epilogue: O / l and lse
+      // solo: the two groups' weights.  A group that summed nothing has l = 0 (its O may be
+      // anything); a NaN among the scores keeps l NaN, and the row is NaN
+      float a0 = 1.f, a1 = 0.f;
+      bool some0 = l_sum != 0.f, some1 = false;
+      if (!pair) {
+        if (k == 1) {
+          ml[2 * row] = m_used;
+          ml[2 * row + 1] = l_sum;
+          mbar_arrive(&bars->ml_full);
+          // O1 and (m, l) are read before the next item changes them
+          ok = mbar_wait(&bars->o1_free, n_solo & 1, p.err, kDevErrEmptyWait);
+          ++n_solo;
+          tc::fence_after_sync();
+          item_done(r);
+          continue;
+        }
+        ok = mbar_wait(&bars->ml_full, n_solo & 1, p.err, kDevErrFullWait);
+        ++n_solo;
         const float m1 = ml[2 * row], l1 = ml[2 * row + 1];
         const float mm = fmaxf(m_used, m1);
         some1 = l1 != 0.f;
@@ -511,11 +652,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         l_sum = (some0 ? a0 * l_sum : 0.f) + (some1 ? a1 * l1 : 0.f);
         m_used = mm;
       }
-    }
-    if (pair || k == 0) {
-      if (ok && tiles_of(k) > 0) ok = mbar_wait(&bars->pv_done[k], (tiles_of(k) - 1) & 1, p.err, kDevErrFullWait);
-      const bool both = !pair && tiles_of(1) > 0;
-      if (ok && both) ok = mbar_wait(&bars->pv_done[1], (tiles_of(1) - 1) & 1, p.err, kDevErrFullWait);
+      if (ok && j > 0) ok = mbar_wait(&bars->pv_done[k], (np - 1) & 1, p.err, kDevErrFullWait);
+      const bool both = !pair && tiles1 > 0;
+      if (ok && both) ok = mbar_wait(&bars->pv_done[1], (np1 - 1) & 1, p.err, kDevErrFullWait);
       tc::fence_after_sync();
       const bool some = some0 || some1;
       const float inv = some ? 1.f / l_sum : 0.f;
@@ -523,24 +662,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       a1 *= inv;
       constexpr float kLn2 = 0.6931471805599453f;
       const float lse = some ? (m_used + __log2f(l_sum)) * kLn2 : -INFINITY;
-      const bool direct = it.n_chunk == 1;
-      const int h = it.g * G + hg;
-      const int64_t orow = direct ? (static_cast<int64_t>(it.row0) + t_q) * p.Hq + h
-                                  : it.part_row + (static_cast<int64_t>(it.c) * it.n + t_q) * p.Hq + h;
+      const bool direct = t.it.n_chunk == 1;
+      const int h = t.it.g * G + hg;
+      const int64_t orow = direct ? (static_cast<int64_t>(t.it.row0) + t_q) * p.Hq + h
+                                  : t.it.part_row + (static_cast<int64_t>(t.it.c) * t.it.n + t_q) * p.Hq + h;
       // an empty partial's o is never read
       const bool write_o = valid && (direct || some);
       if (active) {
 #pragma unroll 2
         for (int c = 0; c < D / 16; ++c) {
-          uint32_t r[16], r1[16];
-          if (n_tiles > 0) tc::tmem_ld16(o_col + 16 * c, r);
-          if (both) tc::tmem_ld16(o_col + 128 + 16 * c, r1);
+          uint32_t x0[16], x1[16];
+          if (t.n_tiles > 0) tc::tmem_ld16(o_col + 16 * c, x0);
+          if (both) tc::tmem_ld16(o_col + 128 + 16 * c, x1);
           tc::tmem_wait_ld();
           float x[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            x[e] = some0 ? __uint_as_float(r[e]) * a0 : 0.f;
-            if (some1) x[e] = fmaf(__uint_as_float(r1[e]), a1, x[e]);
+            x[e] = some0 ? __uint_as_float(x0[e]) * a0 : 0.f;
+            if (some1) x[e] = fmaf(__uint_as_float(x1[e]), a1, x[e]);
           }
           if (write_o) {
             if (direct) {
@@ -559,6 +698,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (valid) (direct ? p.ck.lse : p.out_lse)[orow] = lse;
+      // (the next tile's p_full arrival orders these TMEM reads before the next PV writes O)
+      tc::fence_before_sync();
+      if (!pair) mbar_arrive(&bars->o1_free);
+      item_done(r);
     }
   }
 
@@ -576,8 +719,18 @@ cudaError_t launch_cfg(const PartialParams& p, const CUtensorMap& tmq, const CUt
   });
   if (e0 != cudaSuccess) return e0;
   if (n_items <= 0) return cudaSuccess;
-  chunk_tc_kernel<C><<<static_cast<unsigned int>(n_items), kThreads, C::SMEM, stream>>>(p, tmq, tmk, tmv);
-  return cudaGetLastError();
+  // a programmatic dependent of the plan kernel: its CTAs set themselves up meanwhile
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned int>(std::min<int64_t>(n_items, p.ck.n_wave)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, chunk_tc_kernel<C>, p, tmq, tmk, tmv);
 }
 
 }  // namespace

@@ -42,10 +42,12 @@ struct ChunkArgs {
   int32_t tile;     // tokens of one KV tile
   int32_t n_wave;   // work items resident at once
   int32_t n_target; // most work items with several chunks per row tile
-  int32_t* plan;    // device [3 B + 1], written by block 0 for the merge
+  int32_t* plan;    // device [kPlanHead + kPlanRow B] (chunk_plan.cuh)
   void* out;        // bf16 [T][Hq][d]
   float* lse;       // fp32 [T][Hq]
 };
+// The plan's words (see chunk_plan.cuh).
+enum ChunkPlanWord : int { kPlanItems = 0, kPlanMerged = 1, kPlanNext = 2, kPlanHead = 4, kPlanRow = 5 };
 // At most so many KV tiles for each resident work item are dealt out as a single wave.
 constexpr int kChunkShortTiles = 8;
 
@@ -153,6 +155,8 @@ cudaError_t launch_gqa_chunk(GqaVariant v, const PartialParams& p, const CUtenso
 // On the tensor cores (see chunk_tc.cu): bf16 pages, any G <= 128; tmq: q as (dim, head, packed
 // row) with 64 x group_rows x 128 / group_rows boxes, tmk / tmv: pages with chunk_tc_kv_box()
 // rows a box.
+// launch_chunk_plan, directly before it on the stream, writes the plan that it takes its items from.
+cudaError_t launch_chunk_plan(const ChunkArgs& a, cudaStream_t stream);
 int chunk_tc_rows();
 int chunk_tc_kv_tile();
 int chunk_tc_kv_box();
