@@ -1081,7 +1081,7 @@ skv_status chunk_plan(const skv_chunk_desc* c, const skv_desc* d, ChunkPlan* pl)
   const bool few = longest * G <= 16;
   pl->group_rows = G;
   int per_sm = 1;
-  pl->tc = !few && d->kv_dtype == SKV_KV_BF16 && G <= 128;
+  pl->tc = !few && G <= 128;
   if (d->kv_dtype == SKV_KV_FP8_E4M3)
     pl->variant = few ? GqaVariant::kFp8D128Decode : GqaVariant::kFp8D128Prefill;
   else if (d->dk == 64)
@@ -1185,7 +1185,7 @@ skv_status attn_chunk_paged(const skv_chunk_desc* desc, const skv_paged* paged, 
   if (pl.tc) e = launch_chunk_plan(p.ck, s);
   if (e == cudaSuccess) e = timing_mark(false, s);
   if (e == cudaSuccess)
-    e = pl.tc ? launch_chunk_tc(p, d.dk, tmq, tmk, tmv, pl.n_items, s)
+    e = pl.tc ? launch_chunk_tc(p, d.dk, d.kv_dtype == SKV_KV_FP8_E4M3, tmq, tmk, tmv, pl.n_items, s)
               : launch_gqa_chunk(pl.variant, p, tmk, tmv, pl.n_items, s);
   if (e == cudaSuccess) e = timing_mark(true, s);
   if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");

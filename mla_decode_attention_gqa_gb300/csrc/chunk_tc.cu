@@ -1,6 +1,6 @@
 // Tensor-core (tcgen05) attention of ragged chunks of new tokens over a paged cache
 // (attn_chunk_paged): prompt chunks, proposed tokens and decode tokens of one packed batch,
-// causal or with a sliding window and sinks; bf16 pages.
+// causal or with a sliding window and sinks; bf16 pages, or fp8-e4m3 pages with block scales.
 //
 // For every row (new token at position p, query head h of KV head g): s_u = scale q.k_u over
 // the visible tokens u (u <= p and u > p - window or u < n_sink), out = softmax(s) V, lse =
@@ -29,6 +29,9 @@
 //   * TMEM: S0 | S1 | O0 | O1; P in bf16 over its S, read from TMEM as the A operand of P V.
 //     MMAs from one thread complete in order, so when S_k(i+1) has landed PV_k(i) is done and
 //     O_k may be rescaled;
+//   * fp8: tiles of codes land beside the rings and four converter warps widen them into the bf16
+//     rings (exact; 16 KB a tile from HBM, the products as for bf16); the K block scale goes into
+//     the score's scale, the V block scale into p before its rounding;
 //   * optimistic softmax: p = 2^(s - m) against the maximum so far; only a row's first visible
 //     tile, and (again) a tile whose p sum passes 2^16, take the tile's maximum and rescale O.
 #include <climits>
@@ -49,28 +52,38 @@ namespace {
 constexpr int kTN = 128;        // tokens per K/V tile
 constexpr int kHalf = kTN / 2;  // tokens per TMA box: a page holds a multiple of 64
 constexpr int kRowsTile = 128;  // rows per query tile (MMA M)
-constexpr int kThreads = 12 * 32;
-constexpr int kItemReaders = 11;  // warps that read the work items: both loaders, the issuer, the softmax
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;    // S_k (P_k over its first 64 columns) at kColS + 128 k
 constexpr uint32_t kColO = 256;  // O_k at kColO + 128 k
 constexpr float kTileSumLimit = 65536.0f;
 
-template <int D_>
+template <int D_, bool FP8_>
 struct TcCfg {
   static constexpr int D = D_;
-  static constexpr int NB = D / 64;                  // 128-byte boxes of a row
+  static constexpr bool FP8 = FP8_;
+  static constexpr int THREADS = (FP8 ? 16 : 12) * 32;
+  static constexpr int READERS = FP8 ? 15 : 11;      // warps that read the work items
+  static constexpr int NB = D / 64;                  // 128-byte boxes of a row of 16-bit values
   static constexpr int NST = D == 64 ? 4 : 2;        // ring depth, tiles
   static constexpr int BOX = kTN * 128;              // one box column of a tile: 128 rows x 128 bytes
-  static constexpr int TILE = NB * BOX;              // a Q, K or V tile of 128 rows
+  static constexpr int TILE = NB * BOX;              // a Q, K or V tile of 128 rows in bf16
+  static constexpr int TILE8 = FP8 ? kTN * 128 : 0;  // a K or V tile of e4m3 codes as it lands
+  static constexpr int LOAD = FP8 ? TILE8 : TILE;    // bytes of one loaded tile
+  static constexpr int LOAD_BOXES = FP8 ? 1 : NB;
+  static constexpr int LOAD_BOX_ELEMS = FP8 ? 128 : 64;
   static constexpr int OFF_K = 2 * TILE;
   static constexpr int OFF_V = OFF_K + NST * TILE;
-  static constexpr int OFF_BAR = OFF_V + NST * TILE;
-  static constexpr int OFF_ML = OFF_BAR + 256;       // solo: group 1's (m, l) per row
+  static constexpr int OFF_K8 = OFF_V + NST * TILE;
+  static constexpr int OFF_V8 = OFF_K8 + TILE8;
+  static constexpr int OFF_BAR = OFF_V8 + TILE8;
+  static constexpr int OFF_ML = OFF_BAR + 512;       // solo: group 1's (m, l) per row
   static constexpr int OFF_ITEM = OFF_ML + kRowsTile * 8;
   static constexpr int SMEM = 1024 + OFF_ITEM + 256;
+  static_assert(!FP8 || D == 128, "e4m3 rows are one 128-byte box");
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
+
+constexpr int kScaleSlots = 8;  // tiles whose fp8 scales are held (see the loader)
 
 template <class C>
 struct TcBars {
@@ -80,6 +93,9 @@ struct TcBars {
   uint64_t v_full[C::NST], v_empty[C::NST];
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t ml_full, o1_free;  // solo: group 1's (m, l) are written; group 0 has read them and O1
+  // fp8: codes have landed / are converted; a tile's scales are written
+  uint64_t k8_full, k8_empty, v8_full, v8_empty, sc_full[kScaleSlots];
+  float4 scales[kScaleSlots];  // K and V scale of a tile's first half, then of its second
   uint32_t tmem_base;
 };
 
@@ -108,10 +124,35 @@ __device__ __forceinline__ void tma_4d(void* dst, const CUtensorMap* map, uint64
 template <int V>
 using Int = std::integral_constant<int, V>;
 
+// Four e4m3 codes to bf16, exactly.  A code's exponent and mantissa bits moved to a bf16's are
+// the value times 2^(7 - 127) (a subnormal code becomes the subnormal bf16 of that product), so
+// one packed multiplication by 2^120 gives the value: five operations a pair, where conversions
+// by way of fp16 and fp32 take four of the slower conversion pipe's.  NaN codes come out as
+// +-480 and are told by bit 7 of a byte of `odd`.
+__device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t& lo, uint32_t& hi, uint32_t& odd) {
+  odd |= (w & 0x7F7F7F7Fu) + 0x01010101u;
+  const __nv_bfloat162 k = __halves2bfloat162(__ushort_as_bfloat16(0x7B80), __ushort_as_bfloat16(0x7B80));  // 2^120
+  const uint32_t a = prmt(w, 0u, 0x1404u), b = prmt(w, 0u, 0x3424u);  // codes in the high bytes
+  uint32_t x = ((a >> 4) & 0x07F007F0u) | (a & 0x80008000u);
+  uint32_t y = ((b >> 4) & 0x07F007F0u) | (b & 0x80008000u);
+  __nv_bfloat162 u = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&x), k);
+  __nv_bfloat162 v = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&y), k);
+  lo = *reinterpret_cast<uint32_t*>(&u);
+  hi = *reinterpret_cast<uint32_t*>(&v);
+}
+
+// (x0, x1) * s for a pair in one packed instruction.
+__device__ __forceinline__ void mul_pair(float& x0, float& x1, float s) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\tmul.rn.f32x2 a, a, b;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(s));
+}
+
 // One item after the other through all the roles: a role that is done with an item goes on to
 // the next, so that loads and first scores of one item run under the epilogue of the one before.
 template <class C>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(C::THREADS, 1)
     chunk_tc_kernel(const __grid_constant__ PartialParams p, const __grid_constant__ CUtensorMap tmq,
                     const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
   constexpr int D = C::D, NST = C::NST, NB = C::NB;
@@ -125,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars->item_full[s], 1);
-      mbar_init(&bars->item_empty[s], kItemReaders);
+      mbar_init(&bars->item_empty[s], C::READERS);
       mbar_init(&bars->s_full[s], 1);
       mbar_init(&bars->p_full[s], kRowsTile);
       mbar_init(&bars->pv_done[s], 1);
@@ -133,11 +174,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 1);
     for (int s = 0; s < NST; ++s) {
-      mbar_init(&bars->k_full[s], 1);
+      mbar_init(&bars->k_full[s], C::FP8 ? 128 : 1);
       mbar_init(&bars->k_empty[s], 1);
-      mbar_init(&bars->v_full[s], 1);
+      mbar_init(&bars->v_full[s], C::FP8 ? 128 : 1);
       mbar_init(&bars->v_empty[s], 1);
     }
+    mbar_init(&bars->k8_full, 1);
+    mbar_init(&bars->k8_empty, 128);
+    mbar_init(&bars->v8_full, 1);
+    mbar_init(&bars->v8_empty, 128);
+    for (int s = 0; s < kScaleSlots; ++s) mbar_init(&bars->sc_full[s], 1);
     mbar_init(&bars->ml_full, kRowsTile);
     mbar_init(&bars->o1_free, kRowsTile);
     fence_mbar_init();
@@ -169,6 +215,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     return true;
   };
 
+  // fp8: the launch's 512 threads x 128 registers as 128 x (104 + 72 + 168 + 168)
+  if (warp < 4) {
+    if constexpr (C::FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
   if (warp == 3) {
     // ------------------------------------------------------------ scheduler
     // Items are handed out one by one (a counter that the plan kernel cleared), so that CTAs
@@ -204,16 +253,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (t.it.b < 0) break;
     }
-  } else if (warp == 0 || warp == 2) {
+  } else if (warp != 1) {
     // ------------------------------------------------------------ TMA producers: 0 Q and K, 2 V
     // A warp each, so that neither waits for the other's ring; the pages and rows of the next
     // tile (four integer divisions and two dependent loads) are looked up behind this tile's
     // copies, not between a freed stage and its refill, which bounds a two-stage ring.
     const bool is_k = warp == 0;
     const CUtensorMap* map = is_k ? &tmk : &tmv;
-    uint64_t* full = is_k ? bars->k_full : bars->v_full;
-    uint64_t* empty = is_k ? bars->k_empty : bars->v_empty;
-    uint8_t* ring = smem + (is_k ? C::OFF_K : C::OFF_V);
+    // fp8: the codes land in one buffer each for K and V, from which the converter warps fill
+    // the rings
+    constexpr int NL = C::FP8 ? 1 : NST;
+    uint64_t* full = C::FP8 ? (is_k ? &bars->k8_full : &bars->v8_full) : (is_k ? bars->k_full : bars->v_full);
+    uint64_t* empty = C::FP8 ? (is_k ? &bars->k8_empty : &bars->v8_empty) : (is_k ? bars->k_empty : bars->v_empty);
+    uint8_t* ring = smem + (C::FP8 ? (is_k ? C::OFF_K8 : C::OFF_V8) : (is_k ? C::OFF_K : C::OFF_V));
     if (tc::elect_one()) {
       tma_prefetch_desc(map);
       if (is_k) tma_prefetch_desc(&tmq);
@@ -228,6 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int r = 0; ok && next_item(r, &t); ++r) {
       if (t.n_tiles == 0) continue;
       int page[2], at[2];  // of a tile's two halves
+      float scale = 0.f;   // fp8: lanes 0-3 of the K loader
       auto look_up = [&](int i) {
         const int a = t.token(i);
         // a second half at or past the capacity holds no token: it takes the first one's page
@@ -237,6 +290,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         at[1] = b % p.block_len;
         page[0] = kv_page_of(p, t.it.b, a);
         page[1] = kv_page_of(p, t.it.b, b);
+        if constexpr (C::FP8) {
+          // the scales of both halves, a lane each (K, V, K, V).  Halves in which no row sees a token,
+          // and pages outside the cache, take 0: their scales may be anything
+          const int hf = (lane >> 1) & 1, tok = a + hf * kHalf, pg = page[hf];
+          const bool seen = (tok < t.tl.hi && tok + kHalf > t.tl.lo) || tok < t.tl.sinks;
+          scale = 0.f;
+          if (is_k && lane < 4 && seen && pg >= 0 && pg < p.num_blocks) {
+            const int per = p.block_len / p.scale_block;
+            const int64_t x = (static_cast<int64_t>(pg) * p.Hkv + t.it.g) * per + at[hf] / p.scale_block;
+            scale = __ldg(((lane & 1) ? p.v_scale : p.k_scale) + x);
+          }
+        }
       };
       look_up(0);
       if (is_k) {
@@ -253,28 +318,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++nq;
       }
       for (int i = 0; i < t.n_tiles; ++i) {
-        const int s = done % NST;
-        ok = done < NST || wait_all(&empty[s], ((done / NST) - 1) & 1);
+        const int s = done % NL;
+        ok = done < NL || wait_all(&empty[s], ((done / NL) - 1) & 1);
         if (!ok) break;
         if (tc::elect_one()) {
-          mbar_arrive_expect_tx(&full[s], C::TILE);
+          mbar_arrive_expect_tx(&full[s], C::LOAD);
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-            for (int bx = 0; bx < NB; ++bx)
-              tma_4d(ring + s * C::TILE + bx * C::BOX + hf * (C::BOX / 2), map, &full[s], bx * 64, at[hf], t.it.g,
-                     page[hf]);
+            for (int bx = 0; bx < C::LOAD_BOXES; ++bx)
+              tma_4d(ring + s * C::LOAD + bx * C::BOX + hf * (C::BOX / 2), map, &full[s], bx * C::LOAD_BOX_ELEMS, at[hf],
+                     t.it.g, page[hf]);
         }
         __syncwarp();
+        if constexpr (C::FP8) {
+          if (is_k) {
+            // slot of tile x again at x + 8: its codes follow those of x + 5 into a ring stage that the
+            // scores of x + 5 left, which were issued after P V of x: the softmax of x is done
+            const int sl = done % kScaleSlots;
+            if (lane < 4) reinterpret_cast<float*>(&bars->scales[sl])[lane] = scale;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->sc_full[sl]);
+          }
+        }
         ++done;
         if (i + 1 < t.n_tiles) look_up(i + 1);
       }
     }
     // every issued copy lands before the CTA may exit
-    for (int i = max(0, done - NST); i < done; ++i)
-      if (!mbar_wait(&full[i % NST], (i / NST) & 1, p.err, kDevErrDrainWait)) break;
+    for (int i = max(0, done - NL); i < done; ++i)
+      if (!mbar_wait(&full[i % NL], (i / NL) & 1, p.err, kDevErrDrainWait)) break;
     if (is_k && nq > 0) mbar_wait(&bars->q_full, (nq - 1) & 1, p.err, kDevErrDrainWait);
-  } else if (warp == 1) {
+  } else {
     // ------------------------------------------------------------ MMA issuer
     // The whole warp waits, one elected lane issues; a tile's stage is a compile-time constant,
     // so every operand is a constant offset.
@@ -434,15 +509,74 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       base += n;
     }
+  }
+  } else if (warp >= 12) {  // (fp8 only: no such warps otherwise)
+    // ------------------------------------------------------------ fp8: codes to bf16 tiles
+    if constexpr (C::FP8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    // One thread a token row: 16 codes of a 16-byte chunk become the 32 bytes of two chunks of
+    // the 128-byte-swizzled bf16 tile (both sides conflict-free: eight rows, eight chunks).
+    const int row = (warp - 12) * 32 + lane;
+    auto convert = [&](const uint8_t* from, uint8_t* to) {
+      uint32_t odd = 0u;  // bit 7 of a byte: a NaN code among the row's
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const uint4 u = *reinterpret_cast<const uint4*>(from + row * 128 + ((c ^ (row & 7)) << 4));
+        uint8_t* d = to + (c >> 2) * C::BOX + row * 128;
+        const int d0 = 2 * (c & 3);
+        uint4 lo, hi;
+        e4m3x4_to_bf16(u.x, lo.x, lo.y, odd);
+        e4m3x4_to_bf16(u.y, lo.z, lo.w, odd);
+        e4m3x4_to_bf16(u.z, hi.x, hi.y, odd);
+        e4m3x4_to_bf16(u.w, hi.z, hi.w, odd);
+        *reinterpret_cast<uint4*>(d + ((d0 ^ (row & 7)) << 4)) = lo;
+        *reinterpret_cast<uint4*>(d + (((d0 + 1) ^ (row & 7)) << 4)) = hi;
+      }
+      if (odd & 0x80808080u) {  // rare: put the NaNs in
+        for (int x = 0; x < 128; ++x) {
+          const uint8_t code = from[row * 128 + (((x >> 4) ^ (row & 7)) << 4) + (x & 15)];
+          if ((code & 0x7Fu) == 0x7Fu) {
+            const int b = 2 * (x & 63);
+            *reinterpret_cast<uint16_t*>(to + (x >> 6) * C::BOX + row * 128 + (((b >> 4) ^ (row & 7)) << 4) + (b & 15)) =
+                0x7FC0u;
+          }
+        }
+      }
+    };
+    int done = 0;
+    bool ok = true;
+    auto tile = [&](uint64_t* landed, uint64_t* taken, uint64_t* full, uint64_t* empty, const uint8_t* from, uint8_t* to) {
+      ok = mbar_wait(landed, done & 1, p.err, kDevErrFullWait) &&
+           (done < NST || mbar_wait(empty, ((done / NST) - 1) & 1, p.err, kDevErrEmptyWait));
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      convert(from, to);
+      fence_proxy_async_smem();
+      mbar_arrive(full);
+      mbar_arrive(taken);
+    };
+    for (int r = 0; ok && item_here(r); ++r) {
+      const int n = items[r & 1].n_tiles;
+      item_done(r);
+      for (int i = 0; i < n && ok; ++i, ++done) {
+        const int s = done % NST;
+        tile(&bars->k8_full, &bars->k8_empty, &bars->k_full[s], &bars->k_empty[s], smem + C::OFF_K8,
+             smem + C::OFF_K + s * C::TILE);
+        if (ok)
+          tile(&bars->v8_full, &bars->v8_empty, &bars->v_full[s], &bars->v_empty[s], smem + C::OFF_V8,
+               smem + C::OFF_V + s * C::TILE);
+      }
+    }
+    }
   } else {
     // ------------------------------------------------------------ softmax groups
+    if constexpr (C::FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     const int k = (warp - 4) >> 2;
     const int lgrp = warp & 3;         // TMEM lane group of this warp
     const int row = lgrp * 32 + lane;  // row inside the query tile
     const uint32_t t_lane = tmem + (static_cast<uint32_t>(lgrp * 32) << 16);
     const uint32_t s_col = t_lane + kColS + 128 * k;
     const uint32_t o_col = t_lane + kColO + 128 * k;
-    const float sl = p.scale_log2;
     float* ml = reinterpret_cast<float*>(smem + C::OFF_ML);
     int base = 0;              // tiles of the items before
     uint32_t np = 0, np1 = 0;  // tiles of this group, and of group 1, so far
@@ -484,6 +618,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int c_sink = min(max(sink_row - t0, 0), kTN);
           auto visible = [&](int col) -> bool { return static_cast<unsigned>(col - c_lo) < span || col < c_sink; };
           const bool row_vis = valid && (!need_mask || span > 0u || c_sink > 0);
+          // score scale (base 2) and V scale of the tile's halves
+          float sl[2] = {p.scale_log2, p.scale_log2}, vs[2] = {1.f, 1.f};
+          if constexpr (C::FP8) {
+            const int x = base + i;
+            ok = mbar_wait(&bars->sc_full[x % kScaleSlots], (x / kScaleSlots) & 1, p.err, kDevErrFullWait);
+            const float4 sc = bars->scales[x % kScaleSlots];
+            sl[0] *= sc.x, vs[0] = sc.y, sl[1] *= sc.z, vs[1] = sc.w;
+          }
           uint32_t pk[kTN / 2];
           uint64_t ls[2];  // fp32 pair sums of p
           // 32 columns from TMEM as packed P.  masked: a compile-time flag, so that columns that
@@ -497,16 +639,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const int col = 32 * cc + 2 * e;
-              float v0 = __uint_as_float(x[e >> 3][(2 * e) & 15]);
-              float v1 = __uint_as_float(x[e >> 3][(2 * e + 1) & 15]);
-              if constexpr (decltype(masked)::value) {
-                v0 = visible(col) ? v0 : -INFINITY;
-                v1 = visible(col + 1) ? v1 : -INFINITY;
-              }
+              const float v0 = __uint_as_float(x[e >> 3][(2 * e) & 15]);
+              const float v1 = __uint_as_float(x[e >> 3][(2 * e + 1) & 15]);
               float a0, a1;
-              fma_pair(v0, v1, sl, -base0, a0, a1);
-              const float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
+              fma_pair(v0, v1, sl[cc >> 1], -base0, a0, a1);
+              if constexpr (decltype(masked)::value) {
+                a0 = visible(col) ? a0 : -INFINITY;
+                a1 = visible(col + 1) ? a1 : -INFINITY;
+              }
+              float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
               ls[e & 1] = add_f32x2(ls[e & 1], p0, p1);
+              if constexpr (C::FP8) mul_pair(p0, p1, vs[cc >> 1]);  // V = code * scale
               pk[16 * cc + e] = pack_bf16(p0, p1);
             }
           };
@@ -543,6 +686,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::tmem_ld16(s_col + 32 * cc, x[0]);
                 tc::tmem_ld16(s_col + 32 * cc + 16, x[1]);
                 tc::tmem_wait_ld();
+                const float s2 = cc < 2 ? sl[0] : sl[1];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) x[e >> 4][e & 15] = __float_as_uint(__uint_as_float(x[e >> 4][e & 15]) * s2);
                 if (mode == 1) {
 #pragma unroll
                   for (int e = 0; e < 32; ++e)
@@ -553,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   mx[e & 3] = fmax3(mx[e & 3], __uint_as_float(x[e >> 3][(2 * e) & 15]),
                                     __uint_as_float(x[e >> 3][(2 * e + 1) & 15]));
               }
-              const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;  // sl > 0
+              const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
               const float m_new = need ? fmaxf(m_used, tmax) : m_used;
               // PV_k of this group's tile before ran before these scores: O_k is final here
               if (__any_sync(0xffffffffu, need && m_used != -INFINITY)) {
@@ -722,7 +868,7 @@ cudaError_t launch_cfg(const PartialParams& p, const CUtensorMap& tmq, const CUt
   // a programmatic dependent of the plan kernel: its CTAs set themselves up meanwhile
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned int>(std::min<int64_t>(n_items, p.ck.n_wave)));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -739,10 +885,11 @@ int chunk_tc_rows() { return 2 * kRowsTile; }
 int chunk_tc_kv_tile() { return kTN; }
 int chunk_tc_kv_box() { return kHalf; }
 
-cudaError_t launch_chunk_tc(const PartialParams& p, int32_t d, const CUtensorMap& tmq, const CUtensorMap& tmk,
+cudaError_t launch_chunk_tc(const PartialParams& p, int32_t d, bool fp8, const CUtensorMap& tmq, const CUtensorMap& tmk,
                             const CUtensorMap& tmv, int64_t n_items, cudaStream_t stream) {
-  if (d == 64) return launch_cfg<TcCfg<64>>(p, tmq, tmk, tmv, n_items, stream);
-  return launch_cfg<TcCfg<128>>(p, tmq, tmk, tmv, n_items, stream);
+  if (fp8) return launch_cfg<TcCfg<128, true>>(p, tmq, tmk, tmv, n_items, stream);
+  if (d == 64) return launch_cfg<TcCfg<64, false>>(p, tmq, tmk, tmv, n_items, stream);
+  return launch_cfg<TcCfg<128, false>>(p, tmq, tmk, tmv, n_items, stream);
 }
 
 }  // namespace skv

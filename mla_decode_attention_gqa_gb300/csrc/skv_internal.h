@@ -152,7 +152,7 @@ cudaError_t launch_gqa_partial(GqaVariant v, const PartialParams& p, const CUten
 // the others partial rows to p.out_o / p.out_lse, which launch_chunk_merge joins.
 cudaError_t launch_gqa_chunk(GqaVariant v, const PartialParams& p, const CUtensorMap& tmk, const CUtensorMap& tmv,
                              int64_t n_items, cudaStream_t stream);
-// On the tensor cores (see chunk_tc.cu): bf16 pages, any G <= 128; tmq: q as (dim, head, packed
+// On the tensor cores (see chunk_tc.cu), any G <= 128; tmq: q as (dim, head, packed
 // row) with 64 x group_rows x 128 / group_rows boxes, tmk / tmv: pages with chunk_tc_kv_box()
 // rows a box.
 // launch_chunk_plan, directly before it on the stream, writes the plan that it takes its items from.
@@ -160,8 +160,8 @@ cudaError_t launch_chunk_plan(const ChunkArgs& a, cudaStream_t stream);
 int chunk_tc_rows();
 int chunk_tc_kv_tile();
 int chunk_tc_kv_box();
-cudaError_t launch_chunk_tc(const PartialParams& p, int32_t d, const CUtensorMap& tmq, const CUtensorMap& tmk,
-                            const CUtensorMap& tmv, int64_t n_items, cudaStream_t stream);
+cudaError_t launch_chunk_tc(const PartialParams& p, int32_t d, bool fp8, const CUtensorMap& tmq,
+                            const CUtensorMap& tmk, const CUtensorMap& tmv, int64_t n_items, cudaStream_t stream);
 cudaError_t launch_chunk_merge(const ChunkArgs& a, int32_t d, const float* part_o, const float* part_lse,
                                int64_t max_rows, cudaStream_t stream);
 

@@ -329,3 +329,49 @@ def test_head_groups(kind, d, Hq, Hkv):
     c = R.make_case([1, 9, 30], [200, 9, 150], Hq, Hkv, d, fp8=kind == "fp8", seed=Hq, device=DEV)
     check(c)
     check(c, window=40, n_sink=3)
+
+
+@pytest.mark.parametrize("longest", [1, None])
+def test_every_e4m3_code(longest):
+    """Each code as a key element against a one-hot query: the lse of a row that sees only that
+    token is the score itself; and as a value: its product is the output."""
+    d, L = 128, 64
+    codes = torch.tensor([c for c in range(256) if c & 0x7F != 0x7F], dtype=torch.uint8)
+    n = len(codes)
+    k = torch.zeros(n, 1, L, d, dtype=torch.uint8)
+    k[:, 0, 0, 77] = codes
+    v = torch.zeros(n, 1, L, d, dtype=torch.uint8)
+    v[:, 0, 0] = codes[:, None]
+    value = codes.view(R.E4M3).double()
+    # sequences of two tokens that see only their own (window 1): rows at position 0 and 1
+    q = torch.zeros(2 * n, 1, d, dtype=torch.bfloat16)
+    q[:, :, 77] = 1.0
+    scale = torch.full((n, 1, 1), 0.25)
+    c = dict(q=q.to(DEV), k_pages=k.view(R.E4M3).to(DEV), v_pages=v.view(R.E4M3).to(DEV), k_scale=scale.to(DEV),
+             v_scale=scale.to(DEV), block_table=torch.arange(n, dtype=torch.int32, device=DEV).view(n, 1),
+             seq_lens=torch.full((n,), 2, dtype=torch.int32, device=DEV),
+             cu_q=torch.arange(n + 1, dtype=torch.int32, device=DEV) * 2)
+    out, lse = run(c, window=1, max_q_len=longest, softmax_scale=1.0)
+    got_lse, got = lse[0::2, 0].cpu().double(), out[0::2, 0].cpu().double()
+    want = value * 0.25
+    assert (got_lse - want).abs().max() <= 112 * 2.0 ** -22  # the base-2 scaling there and back
+    assert ((got - want[:, None]).abs() <= 2.0 ** -8 * want.abs()[:, None]).all()
+    assert (lse[1::2].abs() <= 1e-6).all() and (out[1::2] == 0).all()
+
+
+def test_scales_of_blocks_that_nobody_sees():
+    """NaN scales of blocks without a visible token, in pages that are read for others."""
+    c = R.make_case([1, 40, 1], [70, 450, 700], 8, 2, 128, block_len=192, fp8=True, seed=24, device=DEV)
+    for window, n_sink in ((0, 0), (100, 3)):
+        x = dict(c, k_scale=c["k_scale"].clone(), v_scale=c["v_scale"].clone())
+        seen = torch.zeros(c["k_scale"].shape[0], 3, dtype=torch.bool)
+        table = c["block_table"].tolist()
+        for b, (n, m) in enumerate(((1, 70), (40, 450), (1, 700))):
+            for t in range(m):
+                if not window or t > m - n - window or t < n_sink:
+                    seen[table[b][t // 192], t % 192 // 64] = True
+        for s in ("k_scale", "v_scale"):
+            x[s].transpose(1, 2)[~seen.to(DEV)] = math.nan
+        for longest in (1, None):
+            out, lse = run(x, window, n_sink, max_q_len=longest)
+            R.check_attention(c, out, lse, window, n_sink)
