@@ -165,7 +165,9 @@ class _LazyLib:
     def __getattr__(self, name):
         if _LazyLib._handle is None:
             _LazyLib._handle = _load()
-        return getattr(_LazyLib._handle, name)
+        fn = getattr(_LazyLib._handle, name)
+        setattr(self, name, fn)  # later uses find it directly
+        return fn
 
 
 _lib = _LazyLib()
@@ -269,6 +271,8 @@ def _on_tensor_device(fn):
         t = args[0] if args else kw.get(first)
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise ValueError("split-KV attention runs on CUDA tensors only (no CPU path)")
+        if t.device.index == torch.cuda.current_device():
+            return fn(*args, **kw)
         with torch.cuda.device(t.device):
             return fn(*args, **kw)
 
@@ -652,39 +656,34 @@ def gqa_decode_attn_passq(q, k_shards, v_shards, shard_lens, k_scale=None, v_sca
     return out, lse
 
 
-def _prep_chunk(d, q, k_pages, v_pages, seq_lens, cu_q, block_table, k_scale, v_scale, scale_block):
+def _check_chunk(q, k_pages, v_pages, seq_lens, cu_q, block_table, k_scale, v_scale, scale_block):
     """What the two chunk calls share: q [T, Hq, d], pages [num_blocks, Hkv, block_len, d],
-    cu_q int32 [B + 1], seq_lens int32 [B], block_table int32 [B, max_blocks]; fills d's
-    common fields and returns the paged description."""
-    _require_cuda(k_pages, v_pages, seq_lens, cu_q, block_table, k_scale, v_scale)
-    _same_device(q.device, k_pages=k_pages, v_pages=v_pages, seq_lens=seq_lens, cu_q=cu_q, block_table=block_table,
-                 k_scale=k_scale, v_scale=v_scale)
+    cu_q int32 [B + 1], seq_lens int32 [B], block_table int32 [B, max_blocks].  Returns
+    (B, T, Hq, Hkv, d, KV dtype, paged description)."""
+    dev = q.device
+    for t in (k_pages, v_pages, seq_lens, cu_q, block_table, k_scale, v_scale):
+        if t is not None and t.device != dev:
+            _require_cuda(t)
+            _same_device(dev, **{"a tensor": t})
     if q.dim() != 3 or k_pages.dim() != 4 or v_pages.dim() != 4:
         raise ValueError("q must be [T,Hq,d] and pages [num_blocks,Hkv,block_len,d]")
     if q.dtype != torch.bfloat16:
         raise ValueError("q must be bf16")
-    if q.stride(-1) != 1 or k_pages.stride(-1) != 1 or v_pages.stride(-1) != 1:
+    if q.stride(2) != 1 or k_pages.stride(3) != 1 or v_pages.stride(3) != 1:
         raise ValueError("the head dim must be unit-stride")
     T, Hq, hd = q.shape
     nb, Hkv, L, hd2 = k_pages.shape
     if hd2 != hd or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
         raise ValueError("q / k_pages / v_pages shapes or dtypes disagree")
-    if block_table.dtype != torch.int32 or not block_table.is_contiguous() or block_table.dim() != 2:
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or not block_table.is_contiguous():
         raise ValueError("block_table must be contiguous int32 [B, max_blocks]")
-    B = block_table.shape[0]
+    B, max_blocks = block_table.shape
     _check_lens(seq_lens, B, "seq_lens")
     _check_lens(cu_q, B + 1, "cu_q")
-    d.B, d.T, d.Hq, d.Hkv, d.d = B, T, Hq, Hkv, hd
-    d.kv_dtype = _kv_dtype(k_pages)
-    d.scale_block = scale_block
-    if d.kv_dtype == SKV_KV_FP8_E4M3 and scale_block > 0:
+    kv = _kv_dtype(k_pages)
+    if kv == SKV_KV_FP8_E4M3 and scale_block > 0:
         _check_scales((k_scale, v_scale), (nb, Hkv, L // scale_block), "[num_blocks, Hkv, block_len / scale_block]")
-    for i in range(2):
-        d.q_strides[i] = q.stride(i)
-    pg = SkvPaged()
-    pg.block_len, pg.max_blocks, pg.num_blocks = L, block_table.shape[1], nb
-    pg.block_table = block_table.data_ptr()
-    return pg
+    return B, T, Hq, Hkv, hd, kv, SkvPaged(L, max_blocks, nb, block_table.data_ptr())
 
 
 @_on_tensor_device
@@ -696,36 +695,45 @@ def attn_chunk_paged(q, k_pages, v_pages, seq_lens, cu_q, block_table, max_q_len
     with a sliding window of ``window`` tokens and the first ``n_sink`` tokens.  max_q_len (the
     longest chunk, if the caller knows it) chooses the kernel, not the result.  Returns (out
     bf16 [T,Hq,d], lse fp32 [T,Hq]); rows of no sequence are left as they were."""
-    d = SkvChunkDesc()
-    pg = _prep_chunk(d, q, k_pages, v_pages, seq_lens, cu_q, block_table, k_scale, v_scale, scale_block)
-    d.window, d.n_sink, d.max_q_len = window, n_sink, max_q_len or 0
-    d.softmax_scale = softmax_scale if softmax_scale is not None else 1.0 / math.sqrt(d.d)
-    for i in range(3):
-        d.k_strides[i], d.v_strides[i] = k_pages.stride(i), v_pages.stride(i)
+    B, T, Hq, Hkv, hd, kv, pg = _check_chunk(q, k_pages, v_pages, seq_lens, cu_q, block_table, k_scale, v_scale,
+                                             scale_block)
+    d = SkvChunkDesc(B, T, Hq, Hkv, hd, window, n_sink, max_q_len or 0,
+                     1.0 / math.sqrt(hd) if softmax_scale is None else softmax_scale, kv, scale_block,
+                     q.stride()[:2], k_pages.stride()[:3], v_pages.stride()[:3])
     dev = q.device
-    out = _out(out, (d.T, d.Hq, d.d), torch.bfloat16, dev, "out")
-    lse = _out(lse, (d.T, d.Hq), torch.float32, dev, "lse")
-    nbytes = ctypes.c_size_t(0)
-    _check(_lib.attn_chunk_paged_workspace_size(ctypes.byref(d), ctypes.byref(pg), ctypes.byref(nbytes)))
+    out = _out(out, (T, Hq, hd), torch.bfloat16, dev, "out")
+    lse = _out(lse, (T, Hq), torch.float32, dev, "lse")
+    n = ctypes.c_size_t(0)
+    _check(_lib.attn_chunk_paged_workspace_size(d, pg, n))
     if workspace is None:
         # from torch's stream-ordered allocator at each call (in a capture: the graph's own
         # pool), so that neither two streams nor two graphs share it
-        workspace, ws_bytes = torch.empty(nbytes.value, dtype=torch.uint8, device=dev), nbytes.value
+        workspace, ws_bytes = torch.empty(n.value, dtype=torch.uint8, device=dev), n.value
     else:
-        workspace, ws_bytes = _ws_arg(workspace, nbytes.value, dev)
-    _check(_lib.attn_chunk_paged(ctypes.byref(d), ctypes.byref(pg), _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale),
-                                 _ptr(v_scale), _ptr(cu_q), _ptr(seq_lens), _ptr(out), _ptr(lse), _ptr(workspace),
-                                 ws_bytes, _stream()))
+        workspace, ws_bytes = _ws_arg(workspace, n.value, dev)
+    _check(_lib.attn_chunk_paged(d, pg, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _addr(k_scale),
+                                 _addr(v_scale), cu_q.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                                 workspace.data_ptr(), ws_bytes, _raw_stream(dev)))
     return out, lse
 
 
-def _head_weight(w, heads, hd, dev, name):
-    """(pointer, head stride) of a norm weight [d] or [heads, d]."""
+def _raw_stream(dev):
+    """The current stream of the (current) device as an integer, without the Stream object that
+    torch.cuda.current_stream() makes (6 us of a 35 us call)."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _head_stride(w, heads, hd, dev, name):
+    """Head stride of a norm weight [d] or [heads, d]."""
     if w is None:
-        return None, 0
+        return 0
     if w.device != dev or not w.is_contiguous() or tuple(w.shape) not in ((hd,), (heads, hd)):
         raise ValueError(f"{name} must be a contiguous tensor [{hd}] or [{heads}, {hd}] on {dev}")
-    return w, hd if w.dim() == 2 else 0
+    return hd if w.dim() == 2 else 0
 
 
 @_on_tensor_device
@@ -739,45 +747,45 @@ def qk_norm_rope_append(q, k, v, k_pages, v_pages, seq_lens, cu_q, block_table, 
     [T,Hq,d], q itself included).  q / k / v are packed [T,H,d] views, e.g. of one fused
     projection; positions int32 [T] replaces the place in the sequence as the tables' row; fp8
     pages take codes by the scales already in k_scale / v_scale.  Returns q_out."""
-    d = SkvAppendDesc()
-    pg = _prep_chunk(d, q, k_pages, v_pages, seq_lens, cu_q, block_table, k_scale, v_scale, scale_block)
+    B, T, Hq, Hkv, hd, kv, pg = _check_chunk(q, k_pages, v_pages, seq_lens, cu_q, block_table, k_scale, v_scale,
+                                             scale_block)
     dev = q.device
-    _require_cuda(k, v, cos, sin, positions)
-    _same_device(dev, k=k, v=v, cos=cos, sin=sin, positions=positions, q_out=q_out)
+    for t in (k, v, cos, sin, positions, q_out):
+        if t is not None and t.device != dev:
+            _require_cuda(t)
+            _same_device(dev, **{"a tensor": t})
     for t, name in ((k, "k"), (v, "v")):
-        if t.dtype != torch.bfloat16 or tuple(t.shape) != (d.T, d.Hkv, d.d) or t.stride(-1) != 1:
-            raise ValueError(f"{name} must be bf16 [{d.T}, {d.Hkv}, {d.d}] with a unit-stride head dim")
+        if t.dtype != torch.bfloat16 or tuple(t.shape) != (T, Hkv, hd) or t.stride(2) != 1:
+            raise ValueError(f"{name} must be bf16 [{T}, {Hkv}, {hd}] with a unit-stride head dim")
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin go together")
+    max_pos = rot = 0
     if cos is not None:
         for t, name in ((cos, "cos"), (sin, "sin")):
             if t.dtype != torch.float32 or t.dim() != 2 or not t.is_contiguous() or t.shape != cos.shape:
                 raise ValueError(f"{name} must be contiguous float32 [max_pos, rot / 2]")
-        d.max_pos, d.rot = cos.shape[0], 2 * cos.shape[1]
-        if d.rot == 0:
+        max_pos, rot = cos.shape[0], 2 * cos.shape[1]
+        if rot == 0:
             raise ValueError("cos and sin have no columns: pass None for no rotation")
     if positions is not None and (cos is None or positions.dtype != torch.int32 or not positions.is_contiguous()
-                                  or tuple(positions.shape) != (d.T,)):
-        raise ValueError(f"positions must be contiguous int32 of shape ({d.T},), with cos and sin")
-    qw, d.q_weight_stride = _head_weight(q_weight, d.Hq, d.d, dev, "q_weight")
-    kw, d.k_weight_stride = _head_weight(k_weight, d.Hkv, d.d, dev, "k_weight")
-    kinds = {w.dtype for w in (qw, kw) if w is not None}
+                                  or tuple(positions.shape) != (T,)):
+        raise ValueError(f"positions must be contiguous int32 of shape ({T},), with cos and sin")
+    q_ws, k_ws = _head_stride(q_weight, Hq, hd, dev, "q_weight"), _head_stride(k_weight, Hkv, hd, dev, "k_weight")
+    kinds = {w.dtype for w in (q_weight, k_weight) if w is not None}
     if len(kinds) > 1 or not kinds <= {torch.bfloat16, torch.float32}:
         raise ValueError("q_weight and k_weight must both be bf16 or both float32")
-    d.weight_dtype = SKV_WEIGHT_FP32 if kinds == {torch.float32} else SKV_WEIGHT_BF16
     if q_out is None:
-        q_out = torch.empty((d.T, d.Hq, d.d), dtype=torch.bfloat16, device=dev)
-    elif q_out.dtype != torch.bfloat16 or q_out.shape != q.shape or q_out.stride(-1) != 1:
+        q_out = torch.empty((T, Hq, hd), dtype=torch.bfloat16, device=dev)
+    elif q_out.dtype != torch.bfloat16 or q_out.shape != q.shape or q_out.stride(2) != 1:
         raise ValueError(f"q_out must be bf16 {tuple(q.shape)} with a unit-stride head dim")
-    d.eps = eps
-    d.interleaved = 1 if interleaved else 0
-    for i in range(2):
-        d.k_strides[i], d.v_strides[i], d.q_out_strides[i] = k.stride(i), v.stride(i), q_out.stride(i)
-    for i in range(3):
-        d.k_page_strides[i], d.v_page_strides[i] = k_pages.stride(i), v_pages.stride(i)
-    _check(_lib.qk_norm_rope_append(ctypes.byref(d), ctypes.byref(pg), _ptr(q), _ptr(k), _ptr(v), _ptr(qw), _ptr(kw),
-                                    _ptr(cos), _ptr(sin), _ptr(positions), _ptr(cu_q), _ptr(seq_lens), _ptr(k_scale),
-                                    _ptr(v_scale), _ptr(q_out), _ptr(k_pages), _ptr(v_pages), _stream()))
+    d = SkvAppendDesc(B, T, Hq, Hkv, hd, rot, 1 if interleaved else 0,
+                      SKV_WEIGHT_FP32 if torch.float32 in kinds else SKV_WEIGHT_BF16, kv, scale_block, eps, max_pos,
+                      q.stride()[:2], k.stride()[:2], v.stride()[:2], q_out.stride()[:2], q_ws, k_ws,
+                      k_pages.stride()[:3], v_pages.stride()[:3])
+    _check(_lib.qk_norm_rope_append(d, pg, q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(q_weight), _addr(k_weight),
+                                    _addr(cos), _addr(sin), _addr(positions), cu_q.data_ptr(), seq_lens.data_ptr(),
+                                    _addr(k_scale), _addr(v_scale), q_out.data_ptr(), k_pages.data_ptr(),
+                                    v_pages.data_ptr(), _raw_stream(dev)))
     return q_out
 
 

@@ -1189,6 +1189,7 @@ skv_status attn_chunk_paged(const skv_chunk_desc* desc, const skv_paged* paged, 
               : launch_gqa_chunk(pl.variant, p, tmk, tmv, pl.n_items, s);
   if (e == cudaSuccess) e = timing_mark(true, s);
   if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
+  if (d.S_max <= pl.tile) return SKV_OK;  // one KV tile at most: never several chunks
   // rows that can be in several chunks: no more than a partial row each
   const int64_t rows = std::min<int64_t>(static_cast<int64_t>(desc->T) * d.Hq, pl.part_rows);
   e = launch_chunk_merge(p.ck, d.dv, part_o, part_lse, rows, s);
@@ -1244,6 +1245,9 @@ skv_status qk_norm_rope_append(const skv_append_desc* desc, const skv_paged* pag
   if (!aligned(q_weight, 16) || !aligned(k_weight, 16)) return fail(SKV_EINVAL, "weights must be 16-byte aligned");
   if (desc->q_weight_stride < 0 || desc->k_weight_stride < 0 || desc->q_weight_stride % 8 || desc->k_weight_stride % 8)
     return fail(SKV_EINVAL, "weight strides must be non-negative multiples of 8 elements");
+  if (static_cast<int64_t>(desc->T) * (static_cast<int64_t>(desc->Hq) + 2 * static_cast<int64_t>(desc->Hkv)) >= (int64_t(1) << 31))
+    return fail(SKV_EINVAL, "T * (Hq + 2 Hkv) is too large for one call");
+  if (desc->Hq + 2 * static_cast<int64_t>(desc->Hkv) > 65535) return fail(SKV_EINVAL, "Hq + 2 Hkv must be below 65536");
   if (desc->T == 0) return SKV_OK;
   if (!q || !k || !v || !q_out || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16))
     return fail(SKV_EINVAL, "q, k, v and q_out must be non-NULL and 16-byte aligned");

@@ -9,11 +9,15 @@
 //   likewise without norm and rotation.  Everything between the loads and the one rounding at
 //   the store is in fp32.
 //
-// Bound by HBM: each input is read once and each output written once.  16 lanes hold one head
-// (d / 16 values each: 16 or 8 bytes a load), so the mean of squares is four shuffles and the
-// rotation's partner value one shuffle; a 16-lane group keeps its token's cosines and sines in
-// registers over kHeads heads, whose loads are all issued before the first is used.
+// Bound by HBM (each input is read once and each output written once), and closely behind it by
+// the instructions: 8 lanes hold one head, as two chunks of d / 16 values that the rotation
+// pairs, so that it needs no exchange between lanes, the sum of squares is three shuffles for four
+// heads, and the arithmetic runs on packed pairs.  A block takes a run of (token, head) pairs: the
+// chains token -> sequence -> position -> page and table row of its tokens run side by side under
+// the first loads, and every group keeps kAhead heads' loads in flight.
 #include <cuda_runtime.h>
+
+#include <algorithm>
 
 #include "skv_common.cuh"
 #include "skv_internal.h"
@@ -23,12 +27,40 @@ namespace skv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kGroups = kThreads / 16;  // 16-lane groups of a block
+constexpr int kGroups = kThreads / 8;  // heads a block works on at once
+constexpr int kAhead = 3;              // heads in flight in a group (4 spill: 72 -> 82 us for 4096 x 144 heads)
+constexpr int kMaxSteps = 16;          // heads that a group works off in turn (8: 73, 16: 68, 64: 74 us)
+constexpr int kMaxTokens = 64;         // tokens a block's run may touch
 
-// This lane's E values of a head row as floats.
-template <int E>
-__device__ __forceinline__ void load_row(const __nv_bfloat16* p, uint32_t (&w)[E / 2]) {
-  if constexpr (E == 8) {
+// ---- two fp32 values in one 64-bit register (packed round-to-nearest operations)
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t swap2(uint64_t v) {
+  float x, y;
+  unpack2(v, x, y);
+  return pack2(y, x);
+}
+
+// H bf16 values as packed words.
+template <int H>
+__device__ __forceinline__ void load_chunk(const __nv_bfloat16* p, uint32_t* w) {
+  if constexpr (H == 8) {
     const uint4 u = *reinterpret_cast<const uint4*>(p);
     w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
   } else {
@@ -36,218 +68,321 @@ __device__ __forceinline__ void load_row(const __nv_bfloat16* p, uint32_t (&w)[E
     w[0] = u.x, w[1] = u.y;
   }
 }
-
-template <int E>
-__device__ __forceinline__ void store_bf16(__nv_bfloat16* p, const float (&x)[E]) {
-  if constexpr (E == 8)
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                                              pack_bf16(x[6], x[7]));
+template <int H>
+__device__ __forceinline__ void store_chunk(__nv_bfloat16* p, const uint32_t* w) {
+  if constexpr (H == 8)
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
   else
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
 }
 
 // e4m3 codes of x / scale, saturated at +-448; a scale that is not a positive number stores
-// zeros (the value that such a block stands for).
-template <int E>
-__device__ __forceinline__ void store_e4m3(uint8_t* p, const float (&x)[E], float scale) {
-  uint32_t w[E / 4];
-  const bool ok = scale > 0.f && scale <= 3.402823466e38f;
+// zeros (the value that such a block stands for).  A product with the reciprocal where that is
+// finite (off by 2^-23 of the quotient before the rounding to 2^-4), else a division.
+template <int H>
+__device__ __forceinline__ void store_e4m3(uint8_t* p, const uint64_t* x, float scale) {
+  const bool ok = scale > 0.f && scale <= 3.402823466e38f, tiny = scale < 1.1754944e-38f;
+  const float inv = ok && !tiny ? __frcp_rn(scale) : 0.f;
+  uint32_t w[H / 4];
 #pragma unroll
-  for (int i = 0; i < E / 4; ++i) {
+  for (int i = 0; i < H / 4; ++i) {
     uint32_t codes = 0;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const float2 v = ok ? make_float2(__fdiv_rn(x[4 * i + 2 * j], scale), __fdiv_rn(x[4 * i + 2 * j + 1], scale))
-                          : make_float2(0.f, 0.f);
-      codes |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3)) << (16 * j);
+      float u, v;
+      unpack2(x[2 * i + j], u, v);
+      float2 z = make_float2(u * inv, v * inv);
+      if (ok && tiny) z = make_float2(__fdiv_rn(u, scale), __fdiv_rn(v, scale));
+      if (!ok) z = make_float2(0.f, 0.f);
+      codes |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(z, __NV_SATFINITE, __NV_E4M3)) << (16 * j);
     }
     w[i] = codes;
   }
-  if constexpr (E == 8)
+  if constexpr (H == 8)
     *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
   else
     *reinterpret_cast<uint32_t*>(p) = w[0];
 }
 
-template <int E, bool BF16>
-__device__ __forceinline__ void load_weight(const void* w, int64_t at, float (&x)[E]) {
-  if constexpr (BF16) {
-    uint32_t u[E / 2];
-    load_row<E>(static_cast<const __nv_bfloat16*>(w) + at, u);
+// H norm weights as packed pairs.
+template <int H>
+__device__ __forceinline__ void load_weight(const void* w, bool bf16, int64_t at, uint64_t* x) {
+  if (bf16) {
+    uint32_t u[H / 2];
+    load_chunk<H>(static_cast<const __nv_bfloat16*>(w) + at, u);
 #pragma unroll
-    for (int i = 0; i < E / 2; ++i) x[2 * i] = bf16_lo(u[i]), x[2 * i + 1] = bf16_hi(u[i]);
+    for (int i = 0; i < H / 2; ++i) x[i] = pack2(bf16_lo(u[i]), bf16_hi(u[i]));
   } else {
 #pragma unroll
-    for (int i = 0; i < E; i += 4) {
-      const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(w) + at + i);
-      x[i] = u.x, x[i + 1] = u.y, x[i + 2] = u.z, x[i + 3] = u.w;
+    for (int i = 0; i < H; i += 4) {
+      const float4 u = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + at + i));
+      x[i / 2] = pack2(u.x, u.y);
+      x[i / 2 + 1] = pack2(u.z, u.w);
     }
   }
 }
 
-// Sequence of packed row `row`: the b with cu_q[b] <= row < cu_q[b + 1], or -1.
+// Sequence of packed row `row`: the last b with cu_q[b] <= row, if row < cu_q[b + 1]; else -1.
+// Warp-collective: a 32-way search.
 __device__ __forceinline__ int sequence_of(const int32_t* cu_q, int B, int row) {
-  int lo = 0, hi = B;  // the number of sequences whose rows begin at or before `row`
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(cu_q + mid) <= row) lo = mid + 1; else hi = mid;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = B;  // the answer lies in [lo, lo + n), or before lo = 0
+  while (true) {
+    const int step = (n + 31) / 32;
+    const bool before = lane * step < n && __ldg(cu_q + lo + lane * step) <= row;
+    const int hits = __popc(__ballot_sync(0xffffffffu, before));
+    if (hits == 0) return -1;  // before the first sequence
+    lo += (hits - 1) * step;
+    n = min(step, n - (hits - 1) * step);
+    if (step == 1) break;
   }
-  return (lo > 0 && row < __ldg(cu_q + lo)) ? lo - 1 : -1;
+  return row < __ldg(cu_q + lo + 1) ? lo : -1;
 }
 
-// FP8: e4m3 pages; HEADS: heads that one 16-lane group works off.
-template <int D, bool FP8, int HEADS>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a) {
-  constexpr int E = D / 16;
-  const int l16 = threadIdx.x & 15;
+// Where a token goes (written by one warp, read by the block).
+struct Place {
+  int64_t page;   // its page (< 0: its K and V are dropped)
+  int64_t table;  // row of cos and sin; < 0: no such row
+  int at;         // row in the page
+  int live;       // a row of some sequence
+};
+
+// INTER: pairs (2j, 2j + 1) instead of (j, j + rot / 2).
+template <int D, bool FP8, bool INTER>
+__global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_constant__ AppendArgs a) {
+  constexpr int H = D / 16;  // values of a chunk
+  __shared__ Place places[kMaxTokens];
+  const int warp = threadIdx.x >> 5, l8 = threadIdx.x & 7;
   const int n_heads = a.Hq + 2 * a.Hkv;  // queries, keys, values
-  const int parts = (n_heads + HEADS - 1) / HEADS;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kGroups + (threadIdx.x >> 4);
-  const int64_t n_units = static_cast<int64_t>(a.T) * parts;
-  // every lane stays to the end: the shuffles below take whole warps
-  const bool live = unit < n_units;
-  const int row = live ? static_cast<int>(unit / parts) : 0;
-  const int h0 = live ? static_cast<int>(unit % parts) * HEADS : n_heads;
+  const uint32_t pair0 = blockIdx.x * static_cast<uint32_t>(a.steps * kGroups);
+  const int t0 = static_cast<int>(pair0 / n_heads);  // first token of the block's run
+  const uint32_t n_pairs = static_cast<uint32_t>(a.T) * n_heads;
+  const uint32_t last = min(pair0 + static_cast<uint32_t>(a.steps * kGroups), n_pairs) - 1;
+  const int tokens = static_cast<int>(last / n_heads) - t0 + 1;
 
-  // all loads of the group's heads first
-  uint32_t raw[HEADS][E / 2];
-#pragma unroll
-  for (int i = 0; i < HEADS; ++i) {
-    const int h = h0 + i;
-    const __nv_bfloat16* p = nullptr;
-    if (h < a.Hq)
-      p = a.q + row * a.q_st + h * a.q_sh;
-    else if (h < a.Hq + a.Hkv)
-      p = a.k + row * a.k_st + (h - a.Hq) * a.k_sh;
-    else if (h < n_heads)
-      p = a.v + row * a.v_st + (h - a.Hq - a.Hkv) * a.v_sh;
-    if (p) {
-      load_row<E>(p + l16 * E, raw[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < E / 2; ++j) raw[i][j] = 0u;
+  // this lane's two chunks.  Halves: values f.. and their partners; behind the rotated dims the
+  // rest is split in two the same way.  Interleaved: pairs lie inside a chunk
+  const int half = a.rot >> 1, f = l8 * H;
+  const bool in_rot = f < half;
+  const int c0 = INTER || in_rot ? f : a.rot + f - half;
+  const int c1 = INTER ? D / 2 + f : in_rot ? f + half : a.rot + (D - a.rot) / 2 + f - half;
+  const bool turn0 = INTER ? c0 < a.rot : in_rot, turn1 = INTER ? c1 < a.rot : in_rot;
+
+  // The steps of a group are 32 pairs apart.  Its input pointer moves by a constant when q, k and
+  // v are the heads of one fused projection, and is computed anew otherwise; so does q_out's.
+  int ft = 0;  // token and head of the next fetch
+  int fh = static_cast<int>(pair0 - static_cast<uint32_t>(t0) * n_heads) + (threadIdx.x >> 3);
+  while (fh >= n_heads) fh -= n_heads, ++ft;
+  auto input = [&]() -> const __nv_bfloat16* {
+    const int64_t row = t0 + ft;
+    if (fh < a.Hq) return a.q + row * a.q_st + fh * a.q_sh;
+    if (fh < a.Hq + a.Hkv) return a.k + row * a.k_st + (fh - a.Hq) * a.k_sh;
+    return a.v + row * a.v_st + (fh - a.Hq - a.Hkv) * a.v_sh;
+  };
+  const __nv_bfloat16* in = input();
+  const int64_t in_step = kGroups * a.q_sh, in_wrap = a.q_st - n_heads * a.q_sh;
+  const int64_t out_step = kGroups * a.o_sh, out_wrap = a.o_st - n_heads * a.o_sh;
+
+  uint32_t raw[kAhead][H];
+  int who[kAhead];  // token << 16 | head of what is in flight
+  auto fetch = [&](uint32_t (&w)[H], int& id) {
+    id = (ft << 16) | fh;
+    if (t0 + ft < a.T) {
+      load_chunk<H>(in + c0, w);
+      load_chunk<H>(in + c1, w + H / 2);
     }
+    fh += kGroups;
+    in += in_step;
+    while (fh >= n_heads) fh -= n_heads, ++ft, in += in_wrap;
+    if (!a.fused) in = input();
+  };
+  __nv_bfloat16* out = a.q_out + (t0 + static_cast<int64_t>(ft)) * a.o_st + fh * a.o_sh;  // of the next step
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) {
+#pragma unroll
+    for (int j = 0; j < H; ++j) raw[u][j] = 0u;
+    who[u] = 0;
+    if (u < a.steps) fetch(raw[u], who[u]);
   }
 
-  const int b = live ? sequence_of(a.cu_q, a.B, row) : -1;
-  int64_t pos = -1;  // logical position in the sequence
-  if (b >= 0) pos = static_cast<int64_t>(__ldg(a.seq_lens + b)) - __ldg(a.cu_q + b + 1) + row;
-  // page row of the new token (page < 0: its K and V are dropped)
-  int64_t page = -1;
-  int at = 0;
-  if (b >= 0 && h0 + HEADS > a.Hq && pos >= 0 && pos < static_cast<int64_t>(a.max_blocks) * a.block_len) {
-    page = __ldg(a.block_table + static_cast<int64_t>(b) * a.max_blocks + pos / a.block_len);
-    at = static_cast<int>(pos % a.block_len);
-    if (page >= a.num_blocks) page = -1;
+  for (int t = warp; t < tokens; t += kThreads / 32) {
+    const int row = t0 + t;
+    const int b = sequence_of(a.cu_q, a.B, row);
+    Place pl;
+    pl.live = b >= 0;
+    pl.page = pl.table = -1;
+    pl.at = 0;
+    if (b >= 0) {
+      // place in the sequence
+      const int64_t pos = static_cast<int64_t>(__ldg(a.seq_lens + b)) - __ldg(a.cu_q + b + 1) + row;
+      if (pos >= 0 && pos < static_cast<int64_t>(a.max_blocks) * a.block_len) {
+        const int block = static_cast<int>(pos) / a.block_len;  // the capacity is below 2^31
+        pl.page = __ldg(a.block_table + static_cast<int64_t>(b) * a.max_blocks + block);
+        pl.at = static_cast<int>(pos) - block * a.block_len;
+        if (pl.page >= a.num_blocks) pl.page = -1;
+      }
+      pl.table = a.positions ? __ldg(a.positions + row) : pos;
+      if (pl.table >= a.max_pos) pl.table = -1;
+      if (a.rot > 0 && pl.table < 0 && (threadIdx.x & 31) == 0)
+        atomicOr(a.err + kErrCode, static_cast<unsigned int>(kDevErrPosition));
+    }
+    if ((threadIdx.x & 31) == 0) places[t] = pl;
   }
-  // the rotation of this lane's values
-  float cs[E], sn[E];
-  const int d0 = l16 * E, half = a.rot >> 1;
-  const bool turns = d0 < a.rot;  // rot is a multiple of 2 E: a lane turns all its values or none
-  // interleaved pairs lie inside the lane; halves lie half / E lanes apart
-  const bool upper = d0 >= half;
-  const int partner = a.interleaved || !turns ? l16 : l16 + (upper ? -half / E : half / E);
+  __syncthreads();
+
+  Place pl;
+  pl.live = 0;
+  int have_t = -1, have_w = -1;  // token of the place and rotation, kind of the weights held
+  // halves: cs, sn, -sn of the chunk's values; interleaved: (c, c) and (-s, s) of its pairs
+  uint64_t cs[H], sn[H], wt[H];
 #pragma unroll
-  for (int j = 0; j < E; ++j) cs[j] = 1.f, sn[j] = 0.f;
-  if (turns && b >= 0 && h0 < a.Hq + a.Hkv) {
-    const int64_t rp = a.positions ? __ldg(a.positions + row) : pos;
-    if (rp >= 0 && rp < a.max_pos) {
-      const float* c = a.cos + rp * half;
-      const float* s = a.sin + rp * half;
-      if (a.interleaved) {
+  for (int j = 0; j < H; ++j) cs[j] = sn[j] = wt[j] = 0ull;
+  auto step = [&](uint32_t (&w)[H], int& id) {
+    uint32_t r[H];
 #pragma unroll
-        for (int j = 0; j < E; ++j) {
-          cs[j] = __ldg(c + d0 / 2 + j / 2);
-          sn[j] = __ldg(s + d0 / 2 + j / 2);
-        }
-      } else {
-        const int j0 = upper ? d0 - half : d0;
+    for (int j = 0; j < H; ++j) r[j] = w[j];
+    const int t = id >> 16, h = id & 0xFFFF;
+    __nv_bfloat16* const o_q = out;
+    out += out_step;
+    for (int x = h + kGroups; x >= n_heads; x -= n_heads) out += out_wrap;
+    fetch(w, id);
+    const bool here = t < tokens;
+    if (here && t != have_t) {  // a new token
+      have_t = t;
+      pl = places[t];
+      if ((turn0 || turn1) && pl.live) {
+        const float nan = __int_as_float(0x7fc00000);
+        const float* c = a.cos + pl.table * half;
+        const float* s = a.sin + pl.table * half;
+        if constexpr (INTER) {
 #pragma unroll
-        for (int j = 0; j < E; j += 4) {
-          const float4 c4 = __ldg(reinterpret_cast<const float4*>(c + j0 + j));
-          const float4 s4 = __ldg(reinterpret_cast<const float4*>(s + j0 + j));
-          cs[j] = c4.x, cs[j + 1] = c4.y, cs[j + 2] = c4.z, cs[j + 3] = c4.w;
-          sn[j] = s4.x, sn[j + 1] = s4.y, sn[j + 2] = s4.z, sn[j + 3] = s4.w;
+          for (int j = 0; j < H; ++j) {
+            const bool turn = j < H / 2 ? turn0 : turn1;
+            const int at = (j < H / 2 ? c0 + 2 * j : c1 + 2 * (j - H / 2)) / 2;
+            float x = 1.f, y = 0.f;
+            if (turn) x = pl.table >= 0 ? __ldg(c + at) : nan, y = pl.table >= 0 ? __ldg(s + at) : nan;
+            cs[j] = pack2(x, x);
+            sn[j] = pack2(-y, y);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < H / 4; ++j) {
+            float4 x = make_float4(nan, nan, nan, nan), y = x;
+            if (pl.table >= 0) {
+              x = __ldg(reinterpret_cast<const float4*>(c + f + 4 * j));
+              y = __ldg(reinterpret_cast<const float4*>(s + f + 4 * j));
+            }
+            cs[2 * j] = pack2(x.x, x.y);
+            cs[2 * j + 1] = pack2(x.z, x.w);
+            sn[2 * j] = pack2(y.x, y.y);
+            sn[2 * j + 1] = pack2(y.z, y.w);
+            sn[H / 2 + 2 * j] = pack2(-y.x, -y.y);
+            sn[H / 2 + 2 * j + 1] = pack2(-y.z, -y.w);
+          }
         }
       }
-    } else {  // no such row of the tables: NaN, and the host is told
-#pragma unroll
-      for (int j = 0; j < E; ++j) cs[j] = sn[j] = __int_as_float(0x7fc00000);
-      if (l16 == 0) atomicOr(a.err + kErrCode, static_cast<unsigned int>(kDevErrPosition));
     }
-  }
-  const int64_t weight_at = d0;
-
-#pragma unroll
-  for (int i = 0; i < HEADS; ++i) {
-    const int h = h0 + i;
     const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
-    float x[E];
+    uint64_t x[H];  // chunk 0, chunk 1
 #pragma unroll
-    for (int j = 0; j < E / 2; ++j) x[2 * j] = bf16_lo(raw[i][j]), x[2 * j + 1] = bf16_hi(raw[i][j]);
-    // the 16-lane sum of squares and the partner's values: whole warps, values included (their
-    // results are not used), so that no lane of a warp is missing
-    float ss = 0.f;
+    for (int j = 0; j < H; ++j) x[j] = pack2(bf16_lo(r[j]), bf16_hi(r[j]));
+    // the sum of squares over the 8 lanes: whole warps, values included (unused there)
+    uint64_t acc = 0ull;
 #pragma unroll
-    for (int j = 0; j < E; ++j) ss = fmaf(x[j], x[j], ss);
+    for (int j = 0; j < H; ++j) acc = fma2(x[j], x[j], acc);
+    float ss = sum_f32x2(acc);
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const void* wp = is_q ? a.q_weight : a.k_weight;
-    if (!is_v && wp) {
-      const float inv = rsqrtf(ss * (1.f / D) + a.eps);
-      float w[E];
-      const int64_t wa = weight_at + (is_q ? h * a.q_weight_sh : (h - a.Hq) * a.k_weight_sh);
-      if (a.weight_bf16)
-        load_weight<E, true>(wp, wa, w);
-      else
-        load_weight<E, false>(wp, wa, w);
+    for (int o = 4; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (!here || !pl.live) return;  // (no shuffle below)
+    if (!is_v) {
+      const void* wp = is_q ? a.q_weight : a.k_weight;
+      const int64_t w_sh = is_q ? a.q_weight_sh : a.k_weight_sh;
+      float inv = 1.f;
+      if (wp) {
+        if (w_sh != 0 || have_w != (is_q ? 0 : 1)) {
+          const int64_t at = (is_q ? h : h - a.Hq) * w_sh;
+          load_weight<H>(wp, a.weight_bf16 != 0, at + c0, wt);
+          load_weight<H>(wp, a.weight_bf16 != 0, at + c1, wt + H / 2);
+          have_w = is_q ? 0 : 1;
+        }
+        inv = rsqrtf(ss * (1.f / D) + a.eps);
 #pragma unroll
-      for (int j = 0; j < E; ++j) x[j] = x[j] * inv * w[j];
-    }
-    float y[E];
+        for (int j = 0; j < H; ++j) x[j] = mul2(x[j], wt[j]);
+      }
+      if constexpr (INTER) {
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-      const float other = __shfl_sync(0xffffffffu, x[j], partner, 16);
-      if (!turns || is_v) {
-        y[j] = x[j];
-      } else if (a.interleaved) {
-        y[j] = (j & 1) ? fmaf(x[j], cs[j], x[j ^ 1] * sn[j]) : fmaf(x[j], cs[j], -x[j ^ 1] * sn[j]);
-      } else {
-        y[j] = upper ? fmaf(x[j], cs[j], other * sn[j]) : fmaf(x[j], cs[j], -other * sn[j]);
+        for (int j = 0; j < H; ++j)
+          if (j < H / 2 ? turn0 : turn1) x[j] = fma2(x[j], cs[j], mul2(swap2(x[j]), sn[j]));
+      } else if (turn0) {
+#pragma unroll
+        for (int j = 0; j < H / 2; ++j) {
+          const uint64_t u = x[j], v = x[H / 2 + j];
+          x[j] = fma2(u, cs[j], mul2(v, sn[H / 2 + j]));
+          x[H / 2 + j] = fma2(v, cs[j], mul2(u, sn[j]));
+        }
+      }
+      const uint64_t inv2 = pack2(inv, inv);
+#pragma unroll
+      for (int j = 0; j < H; ++j) x[j] = mul2(x[j], inv2);
+      if (is_q || !FP8) {
+#pragma unroll
+        for (int j = 0; j < H; ++j) {
+          float u, v;
+          unpack2(x[j], u, v);
+          r[j] = pack_bf16(u, v);
+        }
       }
     }
-    if (b < 0 || h >= n_heads) continue;  // (no shuffle below)
     if (is_q) {
-      store_bf16<E>(a.q_out + row * a.o_st + h * a.o_sh + d0, y);
-    } else if (page >= 0) {
+      store_chunk<H>(o_q + c0, r);
+      store_chunk<H>(o_q + c1, r + H / 2);
+    } else if (pl.page >= 0) {
       const int g = h - a.Hq - (is_v ? a.Hkv : 0);
-      const int64_t to = page * (is_v ? a.vp_sb : a.kp_sb) + g * (is_v ? a.vp_sh : a.kp_sh) +
-                         at * (is_v ? a.vp_st : a.kp_st) + d0;
+      const int64_t to =
+          pl.page * (is_v ? a.vp_sb : a.kp_sb) + g * (is_v ? a.vp_sh : a.kp_sh) + pl.at * (is_v ? a.vp_st : a.kp_st);
       if constexpr (FP8) {
         const int per = a.block_len / a.scale_block;
-        const float sc = __ldg((is_v ? a.v_scale : a.k_scale) + (page * a.Hkv + g) * per + at / a.scale_block);
-        store_e4m3<E>(static_cast<uint8_t*>(is_v ? a.v_pages : a.k_pages) + to, y, sc);
+        const float scale = __ldg((is_v ? a.v_scale : a.k_scale) + (pl.page * a.Hkv + g) * per + pl.at / a.scale_block);
+        uint8_t* o = static_cast<uint8_t*>(is_v ? a.v_pages : a.k_pages) + to;
+        store_e4m3<H>(o + c0, x, scale);
+        store_e4m3<H>(o + c1, x + H / 2, scale);
       } else {
-        store_bf16<E>(static_cast<__nv_bfloat16*>(is_v ? a.v_pages : a.k_pages) + to, y);
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(is_v ? a.v_pages : a.k_pages) + to;
+        store_chunk<H>(o + c0, r);
+        store_chunk<H>(o + c1, r + H / 2);
       }
     }
+  };
+  for (int n = 0; n < a.steps; n += kAhead) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (n + u < a.steps) step(raw[u], who[u]);  // the same for every lane of the block
   }
 }
 
-template <int D, bool FP8, int HEADS>
-cudaError_t launch(const AppendArgs& a, cudaStream_t stream) {
-  const int64_t parts = (a.Hq + 2 * a.Hkv + HEADS - 1) / HEADS;
-  const int64_t blocks = (a.T * parts + kGroups - 1) / kGroups;
-  if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-  append_kernel<D, FP8, HEADS><<<static_cast<unsigned int>(blocks), kThreads, 0, stream>>>(a);
+template <int D, bool FP8>
+cudaError_t launch(AppendArgs a, cudaStream_t stream) {
+  const int64_t n_heads = a.Hq + 2 * a.Hkv, pairs = a.T * n_heads;
+  // Steps of 32 heads a block: several waves of two blocks an SM (the looks-up of a block's
+  // tokens, about 2 us, should run under other blocks' traffic), one step where there is little
+  int64_t steps = std::min<int64_t>(kMaxSteps, std::max<int64_t>(1, pairs / (kGroups * 3 * 304)));
+  steps = std::min<int64_t>(steps, (kMaxTokens - 2) * n_heads / kGroups);  // tokens that a run touches
+  a.steps = static_cast<int>(steps);
+  a.fused = a.k_st == a.q_st && a.v_st == a.q_st && a.k_sh == a.q_sh && a.v_sh == a.q_sh && a.k == a.q + a.Hq * a.q_sh &&
+            a.v == a.k + a.Hkv * a.q_sh;
+  const unsigned int blocks = static_cast<unsigned int>((pairs + steps * kGroups - 1) / (steps * kGroups));
+  if (a.interleaved)
+    append_kernel<D, FP8, true><<<blocks, kThreads, 0, stream>>>(a);
+  else
+    append_kernel<D, FP8, false><<<blocks, kThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_append(const AppendArgs& a, int32_t d, bool fp8, cudaStream_t stream) {
-  if (d == 64) return launch<64, false, 4>(a, stream);
-  return fp8 ? launch<128, true, 4>(a, stream) : launch<128, false, 4>(a, stream);
+  if (d == 64) return launch<64, false>(a, stream);
+  return fp8 ? launch<128, true>(a, stream) : launch<128, false>(a, stream);
 }
 
 }  // namespace skv
