@@ -29,11 +29,14 @@
 //   * TMEM: S0 | S1 | O0 | O1; P in bf16 over its S, read from TMEM as the A operand of P V.
 //     MMAs from one thread complete in order, so when S_k(i+1) has landed PV_k(i) is done and
 //     O_k may be rescaled;
-//   * fp8: tiles of codes land beside the rings and four converter warps widen them into the bf16
-//     rings (exact; 16 KB a tile from HBM, the products as for bf16); the K block scale goes into
-//     the score's scale, the V block scale into p before its rounding;
+//   * fp8: four converter warps split Q into two e4m3 parts (see split_q), so that Q K^T runs on the
+//     K codes as they land, two 8-bit products at twice the rate, and widen the V codes to bf16
+//     (exact) for P V; the K block scale goes into the score's scale, the V block scale into p
+//     before its rounding.  Widening K as well made the converters the bound (554 us against the
+//     ragged prompts' 3 x 1500);
 //   * optimistic softmax: p = 2^(s - m) against the maximum so far; only a row's first visible
-//     tile, and (again) a tile whose p sum passes 2^16, take the tile's maximum and rescale O.
+//     tile takes a maximum (of 32 columns) beforehand, and a tile whose p sum passes 2^16 its true
+//     one, with O rescaled, and its p again.
 #include <climits>
 #include <cuda_runtime.h>
 
@@ -66,19 +69,20 @@ struct TcCfg {
   static constexpr int NB = D / 64;                  // 128-byte boxes of a row of 16-bit values
   static constexpr int NST = D == 64 ? 4 : 2;        // ring depth, tiles
   static constexpr int BOX = kTN * 128;              // one box column of a tile: 128 rows x 128 bytes
-  static constexpr int TILE = NB * BOX;              // a Q, K or V tile of 128 rows in bf16
-  static constexpr int TILE8 = FP8 ? kTN * 128 : 0;  // a K or V tile of e4m3 codes as it lands
-  static constexpr int LOAD = FP8 ? TILE8 : TILE;    // bytes of one loaded tile
+  static constexpr int TILE = NB * BOX;              // a Q or V tile of 128 rows in bf16
+  static constexpr int LOAD = FP8 ? BOX : TILE;      // a K or V tile as it lands
   static constexpr int LOAD_BOXES = FP8 ? 1 : NB;
   static constexpr int LOAD_BOX_ELEMS = FP8 ? 128 : 64;
   static constexpr int OFF_K = 2 * TILE;
-  static constexpr int OFF_V = OFF_K + NST * TILE;
-  static constexpr int OFF_K8 = OFF_V + NST * TILE;
-  static constexpr int OFF_V8 = OFF_K8 + TILE8;
-  static constexpr int OFF_BAR = OFF_V8 + TILE8;
+  static constexpr int OFF_V = OFF_K + NST * LOAD;
+  static constexpr int OFF_V8 = OFF_V + NST * TILE;  // fp8: the V codes' ring
+  static constexpr int OFF_BAR = OFF_V8 + (FP8 ? NST * LOAD : 0);
   static constexpr int OFF_ML = OFF_BAR + 512;       // solo: group 1's (m, l) per row
   static constexpr int OFF_ITEM = OFF_ML + kRowsTile * 8;
-  static constexpr int SMEM = 1024 + OFF_ITEM + 256;
+  static constexpr int OFF_QS = OFF_ITEM + 256;      // fp8: Q's row scales [item & 1][query tile][row]
+  static constexpr int OFF_OUT = OFF_QS + (FP8 ? 4 * kRowsTile * 4 : 0);  // 64 bytes of each output row
+  static constexpr int OFF_ROW = OFF_OUT + 2 * kRowsTile * 64;            // what each softmax thread's row sees
+  static constexpr int SMEM = 1024 + OFF_ROW + 2 * kRowsTile * 16;
   static_assert(!FP8 || D == 128, "e4m3 rows are one 128-byte box");
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
@@ -93,8 +97,8 @@ struct TcBars {
   uint64_t v_full[C::NST], v_empty[C::NST];
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t ml_full, o1_free;  // solo: group 1's (m, l) are written; group 0 has read them and O1
-  // fp8: codes have landed / are converted; a tile's scales are written
-  uint64_t k8_full, k8_empty, v8_full, v8_empty, sc_full[kScaleSlots];
+  // fp8: V codes have landed / are converted; Q is split (item & 1); a tile's scales are written
+  uint64_t v8_full[C::NST], v8_empty[C::NST], q8_full[2], sc_full[kScaleSlots];
   float4 scales[kScaleSlots];  // K and V scale of a tile's first half, then of its second
   uint32_t tmem_base;
 };
@@ -141,12 +145,117 @@ __device__ __forceinline__ void e4m3x4_to_bf16(uint32_t w, uint32_t& lo, uint32_
   hi = *reinterpret_cast<uint32_t*>(&v);
 }
 
+__device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t at) {
+  uint4 u;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(at) : "memory");
+  return u;
+}
+
 // (x0, x1) * s for a pair in one packed instruction.
 __device__ __forceinline__ void mul_pair(float& x0, float& x1, float s) {
   asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\tmul.rn.f32x2 a, a, b;\n\t"
       "mov.b64 {%0, %1}, a;\n\t}"
       : "+f"(x0), "+f"(x1)
       : "f"(s));
+}
+
+// An edge tile: the scores that this thread's row does not see (row: its end, the start of its
+// window, the end of its sinks) become `out` in tensor memory, out0 in the first 64 columns, so that
+// the passes over the scores carry no test.  hi_min, lo_max, sink_min: columns that the whole warp
+// sees are left alone.  (A function of its own, as store_rows is: inlined, their registers spilled
+// into the loop over the tiles, which then took 1.6 us a tile instead of 1.4.)
+__device__ __noinline__ void hide_scores(uint32_t s_col, int t0, int4 row, int hi_min, int lo_max, int sink_min,
+                                         float out0, float out1) {
+#pragma unroll 1
+  for (int c = 0; c < kTN; c += 32) {
+    const int a = t0 + c, b = a + 32;
+    if (hi_min >= b && (lo_max <= a || sink_min >= b)) continue;  // all see all
+    uint32_t x[2][16];
+    tc::tmem_ld16(s_col + c, x[0]);
+    tc::tmem_ld16(s_col + c + 16, x[1]);
+    const uint32_t out = __float_as_uint(c < 64 ? out0 : out1);
+    uint32_t seen[2];  // bit e: column 16 h + e is seen
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int f = a + 16 * h;
+      const int hi = min(max(row.x - f, 0), 16), lo = min(max(row.y - f, 0), 16), sink = min(max(row.z - f, 0), 16);
+      seen[h] = ((1u << hi) - 1u) & ((0xFFFFu << lo) | ((1u << sink) - 1u));
+    }
+    tc::tmem_wait_ld();
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[h][e] = ((seen[h] >> e) & 1u) ? x[h][e] : out;
+    tc::tmem_st16(s_col + c, x[0]);
+    tc::tmem_st16(s_col + c + 16, x[1]);
+  }
+  tc::tmem_wait_st();
+}
+
+// The warp's 32 output rows (orow: this lane's; bit r of write: row r exists) from tensor memory:
+// w0 O_k, plus w1 O_1 where both groups worked for the row, as bf16 or fp32.  64 bytes of every row
+// at a time go through shared memory, so that a store instruction covers 8 rows x 64 bytes instead
+// of 16 bytes of 32 rows.
+template <int D>
+__device__ __noinline__ void store_rows(uint32_t o_col, bool has0, bool has1, float w0, bool some0, float w1, bool some1,
+                                        unsigned write, int64_t orow, void* out, bool bf16, uint32_t stage) {
+  const int lane = threadIdx.x & 31;
+  const int row_bytes = bf16 ? D * 2 : D * 4;
+  uint8_t* to[4];  // this lane's stores: 16 bytes of rows lane / 4 + 8 i
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    to[i] = static_cast<uint8_t*>(out) + __shfl_sync(0xffffffffu, orow, 8 * i + (lane >> 2)) * row_bytes + (lane & 3) * 16;
+  // piece q of row r lies at q ^ ((r >> 1) & 3): no bank serves two rows at once
+  const uint32_t at_w = stage + lane * 64, swz_w = (lane >> 1) & 3;
+  const uint32_t at_r = stage + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);
+  auto put = [&](const uint32_t* w, int off) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) st_shared_v4(at_w + ((q ^ swz_w) << 4), w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint4 u = ld_shared_v4(at_r + 512 * i);
+      if ((write >> (8 * i + (lane >> 2))) & 1u) *reinterpret_cast<uint4*>(to[i] + off) = u;
+    }
+    __syncwarp();
+  };
+#pragma unroll 1
+  for (int c = 0; c < D; c += 32) {
+    uint32_t x[2][16], w[16];
+    if (has0) {
+      tc::tmem_ld16(o_col + c, x[0]);
+      tc::tmem_ld16(o_col + c + 16, x[1]);
+    }
+    if (has1) {
+      uint32_t y[2][16];
+      tc::tmem_ld16(o_col + 128 + c, y[0]);
+      tc::tmem_ld16(o_col + 128 + c + 16, y[1]);
+      tc::tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 32; ++e) {
+        float v = some0 ? __uint_as_float(x[e >> 4][e & 15]) * w0 : 0.f;
+        if (some1) v = fmaf(__uint_as_float(y[e >> 4][e & 15]), w1, v);
+        x[e >> 4][e & 15] = __float_as_uint(v);
+      }
+    } else {
+      tc::tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        x[e >> 4][e & 15] = some0 ? __float_as_uint(__uint_as_float(x[e >> 4][e & 15]) * w0) : 0u;
+    }
+    if (bf16) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        w[e] = pack_bf16(__uint_as_float(x[e >> 3][(2 * e) & 15]), __uint_as_float(x[e >> 3][(2 * e + 1) & 15]));
+      put(w, 2 * c);
+    } else {
+      put(x[0], 4 * c);
+      put(x[1], 4 * c + 64);
+    }
+  }
 }
 
 // One item after the other through all the roles: a role that is done with an item goes on to
@@ -174,15 +283,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 1);
     for (int s = 0; s < NST; ++s) {
-      mbar_init(&bars->k_full[s], C::FP8 ? 128 : 1);
+      mbar_init(&bars->k_full[s], 1);
       mbar_init(&bars->k_empty[s], 1);
       mbar_init(&bars->v_full[s], C::FP8 ? 128 : 1);
       mbar_init(&bars->v_empty[s], 1);
+      mbar_init(&bars->v8_full[s], 1);
+      mbar_init(&bars->v8_empty[s], 128);
     }
-    mbar_init(&bars->k8_full, 1);
-    mbar_init(&bars->k8_empty, 128);
-    mbar_init(&bars->v8_full, 1);
-    mbar_init(&bars->v8_empty, 128);
+    mbar_init(&bars->q8_full[0], 128);
+    mbar_init(&bars->q8_full[1], 128);
     for (int s = 0; s < kScaleSlots; ++s) mbar_init(&bars->sc_full[s], 1);
     mbar_init(&bars->ml_full, kRowsTile);
     mbar_init(&bars->o1_free, kRowsTile);
@@ -215,9 +324,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     return true;
   };
 
-  // fp8: the launch's 512 threads x 128 registers as 128 x (104 + 72 + 168 + 168)
+  // fp8: the launch's 512 threads x 128 registers as 128 x (104 + 88 + 160 + 160)
   if (warp < 4) {
-    if constexpr (C::FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
   if (warp == 3) {
     // ------------------------------------------------------------ scheduler
     // Items are handed out one by one (a counter that the plan kernel cleared), so that CTAs
@@ -260,12 +369,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // copies, not between a freed stage and its refill, which bounds a two-stage ring.
     const bool is_k = warp == 0;
     const CUtensorMap* map = is_k ? &tmk : &tmv;
-    // fp8: the codes land in one buffer each for K and V, from which the converter warps fill
-    // the rings
-    constexpr int NL = C::FP8 ? 1 : NST;
-    uint64_t* full = C::FP8 ? (is_k ? &bars->k8_full : &bars->v8_full) : (is_k ? bars->k_full : bars->v_full);
-    uint64_t* empty = C::FP8 ? (is_k ? &bars->k8_empty : &bars->v8_empty) : (is_k ? bars->k_empty : bars->v_empty);
-    uint8_t* ring = smem + (C::FP8 ? (is_k ? C::OFF_K8 : C::OFF_V8) : (is_k ? C::OFF_K : C::OFF_V));
+    // (fp8: K codes go to the products as they are, V codes to a ring of their own, from which
+    // the converter warps fill V's)
+    uint64_t* full = is_k ? bars->k_full : C::FP8 ? bars->v8_full : bars->v_full;
+    uint64_t* empty = is_k ? bars->k_empty : C::FP8 ? bars->v8_empty : bars->v_empty;
+    uint8_t* ring = smem + (is_k ? C::OFF_K : C::FP8 ? C::OFF_V8 : C::OFF_V);
     if (tc::elect_one()) {
       tma_prefetch_desc(map);
       if (is_k) tma_prefetch_desc(&tmq);
@@ -318,8 +426,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         ++nq;
       }
       for (int i = 0; i < t.n_tiles; ++i) {
-        const int s = done % NL;
-        ok = done < NL || wait_all(&empty[s], ((done / NL) - 1) & 1);
+        const int s = done % NST;
+        ok = done < NST || wait_all(&empty[s], ((done / NST) - 1) & 1);
         if (!ok) break;
         if (tc::elect_one()) {
           mbar_arrive_expect_tx(&full[s], C::LOAD);
@@ -333,8 +441,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         __syncwarp();
         if constexpr (C::FP8) {
           if (is_k) {
-            // slot of tile x again at x + 8: its codes follow those of x + 5 into a ring stage that the
-            // scores of x + 5 left, which were issued after P V of x: the softmax of x is done
+            // slot of tile x again at x + 8: its codes take a stage that the scores of x + 8 - NST left,
+            // which were issued after P V of x: the softmax of x is done
             const int sl = done % kScaleSlots;
             if (lane < 4) reinterpret_cast<float*>(&bars->scales[sl])[lane] = scale;
             __syncwarp();
@@ -346,35 +454,52 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       }
     }
     // every issued copy lands before the CTA may exit
-    for (int i = max(0, done - NL); i < done; ++i)
-      if (!mbar_wait(&full[i % NL], (i / NL) & 1, p.err, kDevErrDrainWait)) break;
+    for (int i = max(0, done - NST); i < done; ++i)
+      if (!mbar_wait(&full[i % NST], (i / NST) & 1, p.err, kDevErrDrainWait)) break;
     if (is_k && nq > 0) mbar_wait(&bars->q_full, (nq - 1) & 1, p.err, kDevErrDrainWait);
   } else {
     // ------------------------------------------------------------ MMA issuer
     // The whole warp waits, one elected lane issues; a tile's stage is a compile-time constant,
     // so every operand is a constant offset.
-    const uint32_t idesc_s = tc::idesc_f16(128, kTN, true, false, false);
+    // (format 0 of kind::f8f6f4 is e4m3, as 0 of kind::f16 is fp16)
+    const uint32_t idesc_s = tc::idesc_f16(128, kTN, !C::FP8, false, false);
     const uint32_t idesc_pv = tc::idesc_f16(128, D, true, false, true);
     const uint64_t qd = tc::smem_desc_sw128(smem_u32(smem), 16, 1024);
     const uint64_t kd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
     const uint64_t vd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_V), C::BOX, 1024);
+    // A descriptor at a constant offset, by one 32-bit addition where it is used: kept as they are
+    // over the loops, the 64-bit sums of every product take more registers than the warp has (the
+    // address field ends in the low word, shared memory ends below its 18 bits)
+    auto low_of = [](uint64_t d) -> uint32_t {
+      uint32_t lo = static_cast<uint32_t>(d);
+      asm volatile("" : "+r"(lo));
+      return lo;
+    };
+    auto at = [](uint64_t d, uint32_t lo, uint32_t bytes) -> uint64_t {
+      return (d & 0xFFFFFFFF00000000ull) | (lo + (bytes >> 4));
+    };
     auto wait_all = [&](uint64_t* bar, uint32_t parity) {
       return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.err, kDevErrFullWait));
     };
     auto issue_s = [&](int k, int q, int stage) {  // S_k = Q_q K^T
+      const uint32_t ql = low_of(qd), kl = low_of(kd);
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         const uint32_t in_box = (ks >> 2) * C::BOX + (ks & 3) * 32;
-        tc::mma_f16_ss(tmem + kColS + 128 * k, qd + static_cast<uint64_t>((q * C::TILE + in_box) >> 4),
-                       kd + static_cast<uint64_t>((stage * C::TILE + in_box) >> 4), idesc_s, ks > 0 ? 1u : 0u);
+        const uint64_t qa = at(qd, ql, q * C::TILE + in_box);
+        if constexpr (C::FP8)  // the large parts of Q over 4 steps of 32 codes, then the small ones
+          tc::mma_f8_ss(tmem + kColS + 128 * k, qa, at(kd, kl, stage * C::LOAD + (ks & 3) * 32), idesc_s, ks > 0 ? 1u : 0u);
+        else
+          tc::mma_f16_ss(tmem + kColS + 128 * k, qa, at(kd, kl, stage * C::LOAD + in_box), idesc_s, ks > 0 ? 1u : 0u);
       }
       tc::mma_commit(smem_u32(&bars->s_full[k]));
     };
     auto issue_pv = [&](int k, int stage, uint32_t acc0) {  // O_k += P_k V
+      const uint32_t vl = low_of(vd);
 #pragma unroll
       for (int ks = 0; ks < kTN / 16; ++ks)
-        tc::mma_f16_ts(tmem + kColO + 128 * k, tmem + kColS + 128 * k + ks * 8,
-                       vd + static_cast<uint64_t>((stage * C::TILE + ks * 2048) >> 4), idesc_pv, ks > 0 ? 1u : acc0);
+        tc::mma_f16_ts(tmem + kColO + 128 * k, tmem + kColS + 128 * k + ks * 8, at(vd, vl, stage * C::TILE + ks * 2048),
+                       idesc_pv, ks > 0 ? 1u : acc0);
       tc::mma_commit(smem_u32(&bars->pv_done[k]));
     };
     // runs fn with tile number x's stage as a constant
@@ -394,7 +519,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     for (int r = 0; ok && next_item(r, &t); ++r) {
       const int n = t.n_tiles;
       if (n == 0) continue;
-      ok = wait_all(&bars->q_full, nq & 1);
+      ok = C::FP8 ? wait_all(&bars->q8_full[nq & 1], (nq >> 1) & 1) : wait_all(&bars->q_full, nq & 1);
       if (!ok) break;
       ++nq;
       // scores of tile x (both groups, or group x & 1 in solo mode); the last ones free Q
@@ -416,20 +541,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         auto tile = [&](auto st, int i) {
           constexpr int ST = decltype(st)::value, NX = (ST + 1) % NST;
           const int x = base + i;
-          ok = wait_all(&bars->p_full[0], np[0] & 1) && wait_all(&bars->v_full[ST], (x / NST) & 1);
+          const bool more = i + 1 < n;
+          // tiles first, the softmax last: a wait costs 100 cycles and more even for what is there
+          ok = wait_all(&bars->v_full[ST], (x / NST) & 1) && (!more || wait_all(&bars->k_full[NX], ((x + 1) / NST) & 1)) &&
+               wait_all(&bars->p_full[0], np[0] & 1);
           if (!ok) return;
           ++np[0];
           tc::fence_after_sync();
-          if (tc::elect_one()) issue_pv(0, ST, i > 0 ? 1u : 0u);
-          __syncwarp();
-          const bool more = i + 1 < n;
-          if (more) {
-            ok = wait_all(&bars->k_full[NX], ((x + 1) / NST) & 1);
-            if (!ok) return;
-            tc::fence_after_sync();
-            if (tc::elect_one()) issue_s(0, 0, NX);
-            __syncwarp();
+          if (tc::elect_one()) {
+            issue_pv(0, ST, i > 0 ? 1u : 0u);
+            if (more) issue_s(0, 0, NX);
           }
+          __syncwarp();
           ok = wait_all(&bars->p_full[1], np[1] & 1);
           if (!ok) return;
           ++np[1];
@@ -511,15 +634,87 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
   }
   } else if (warp >= 12) {  // (fp8 only: no such warps otherwise)
-    // ------------------------------------------------------------ fp8: codes to bf16 tiles
+    // ------------------------------------------------------------ fp8: Q split, V codes to bf16
     if constexpr (C::FP8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    const int row = (warp - 12) * 32 + lane;
+    // Q for the products with e4m3 keys: a row times the power of two that puts its largest
+    // magnitude in [2^7, 2^8) is the sum of two e4m3 values, the rounded one and the rest.  A bf16
+    // value's 8 bits are 4 and 4, so the sum is exact down to 2^-10 of the row's largest and off
+    // by 2^-18 of it at most below.  The rounded parts (128 bytes) go over the row's first 64
+    // values, the rests over its last 64, each after what it overwrites was read.
+    auto split_q = [&](uint8_t* q) -> float {
+      auto chunk = [&](int c) {
+        return reinterpret_cast<uint4*>(q + (c >> 3) * C::BOX + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+      };
+      uint32_t most = 0u;  // magnitudes order as their bits; a NaN is above infinity
+#pragma unroll 4
+      for (int c = 0; c < 16; ++c) {
+        const uint4 u = *chunk(c);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) most = max(most, max((w[j] << 16) & 0x7FFF0000u, w[j] & 0x7FFF0000u));
+      }
+      const bool finite = most < 0x7F800000u;
+      const int e = most == 0u ? 0 : min(max(static_cast<int>(most >> 23) - 127 - 7, -126), 126);
+      const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      // a pair's codes: the rounded values in the low halves of hi, the rests' in those of lo
+      auto split = [&](uint32_t w, uint32_t& hi, uint32_t& lo) {
+        const float x = bf16_lo(w) * down, y = bf16_hi(w) * down;
+        const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t back = e4m3x2_to_f16x2(h);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
+        hi = h;
+        lo = __nv_cvt_float2_to_fp8x2(make_float2(x - f.x, y - f.y), __NV_SATFINITE, __NV_E4M3);
+      };
+      auto split_chunk = [&](const uint4& u, uint32_t* hi, uint32_t* lo) {  // 8 values: 2 words each
+        uint32_t h0, h1, h2, h3, l0, l1, l2, l3;
+        split(u.x, h0, l0);
+        split(u.y, h1, l1);
+        split(u.z, h2, l2);
+        split(u.w, h3, l3);
+        hi[0] = h0 | (h1 << 16), hi[1] = h2 | (h3 << 16);
+        lo[0] = l0 | (l1 << 16), lo[1] = l2 | (l3 << 16);
+      };
+      uint32_t lo[16];  // the rests of the values read so far and not yet written
+#pragma unroll
+      for (int c = 0; c < 8; c += 2) {  // first 64 values
+        uint32_t hi[4];
+        const uint4 u = *chunk(c), v = *chunk(c + 1);
+        split_chunk(u, hi, lo + 2 * c);
+        split_chunk(v, hi + 2, lo + 2 * c + 2);
+        *chunk(c / 2) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      }
+#pragma unroll
+      for (int c = 0; c < 8; c += 4) {  // last 64, four chunks read before two of them are written
+        uint32_t hi[8], rest[8];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const uint4 u = *chunk(8 + c + d);
+          split_chunk(u, hi + 2 * d, rest + 2 * d);
+        }
+        *chunk(4 + c / 2) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *chunk(5 + c / 2) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+        if (c == 0) {  // chunks 8 .. 11 are read: the first values' rests; these rests wait in their place
+#pragma unroll
+          for (int d = 0; d < 4; ++d) *chunk(8 + d) = make_uint4(lo[4 * d], lo[4 * d + 1], lo[4 * d + 2], lo[4 * d + 3]);
+#pragma unroll
+          for (int d = 0; d < 8; ++d) lo[d] = rest[d];
+        } else {  // chunks 12 .. 15 are read
+          *chunk(12) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          *chunk(13) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+          *chunk(14) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+          *chunk(15) = make_uint4(rest[4], rest[5], rest[6], rest[7]);
+        }
+      }
+      // an infinity or a NaN in the row makes its scores NaN
+      return finite ? __uint_as_float(static_cast<uint32_t>(127 + e) << 23) : __int_as_float(0x7fc00000);
+    };
     // One thread a token row: 16 codes of a 16-byte chunk become the 32 bytes of two chunks of
     // the 128-byte-swizzled bf16 tile (both sides conflict-free: eight rows, eight chunks).
-    const int row = (warp - 12) * 32 + lane;
     auto convert = [&](const uint8_t* from, uint8_t* to) {
       uint32_t odd = 0u;  // bit 7 of a byte: a NaN code among the row's
-#pragma unroll
+#pragma unroll 4
       for (int c = 0; c < 8; ++c) {
         const uint4 u = *reinterpret_cast<const uint4*>(from + row * 128 + ((c ^ (row & 7)) << 4));
         uint8_t* d = to + (c >> 2) * C::BOX + row * 128;
@@ -543,34 +738,38 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
       }
     };
-    int done = 0;
+    int done = 0, nq = 0;  // tiles and query tiles so far
     bool ok = true;
-    auto tile = [&](uint64_t* landed, uint64_t* taken, uint64_t* full, uint64_t* empty, const uint8_t* from, uint8_t* to) {
-      ok = mbar_wait(landed, done & 1, p.err, kDevErrFullWait) &&
-           (done < NST || mbar_wait(empty, ((done / NST) - 1) & 1, p.err, kDevErrEmptyWait));
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return;
-      convert(from, to);
-      fence_proxy_async_smem();
-      mbar_arrive(full);
-      mbar_arrive(taken);
-    };
     for (int r = 0; ok && item_here(r); ++r) {
-      const int n = items[r & 1].n_tiles;
+      const int n = items[r & 1].n_tiles, pair = items[r & 1].pair;
       item_done(r);
+      if (n == 0) continue;
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_full, nq & 1, p.err, kDevErrFullWait));
+      if (!ok) break;
+      float* qs = reinterpret_cast<float*>(smem + C::OFF_QS) + (nq & 1) * 2 * kRowsTile;
+      for (int k = 0; k <= pair; ++k) qs[k * kRowsTile + row] = split_q(smem + k * C::TILE);
+      fence_proxy_async_smem();
+      mbar_arrive(&bars->q8_full[nq & 1]);
+      ++nq;
       for (int i = 0; i < n && ok; ++i, ++done) {
         const int s = done % NST;
-        tile(&bars->k8_full, &bars->k8_empty, &bars->k_full[s], &bars->k_empty[s], smem + C::OFF_K8,
-             smem + C::OFF_K + s * C::TILE);
-        if (ok)
-          tile(&bars->v8_full, &bars->v8_empty, &bars->v_full[s], &bars->v_empty[s], smem + C::OFF_V8,
-               smem + C::OFF_V + s * C::TILE);
+        ok = mbar_wait(&bars->v8_full[s], (done / NST) & 1, p.err, kDevErrFullWait) &&
+             (done < NST || mbar_wait(&bars->v_empty[s], ((done / NST) - 1) & 1, p.err, kDevErrEmptyWait));
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        convert(smem + C::OFF_V8 + s * C::LOAD, smem + C::OFF_V + s * C::TILE);
+        fence_proxy_async_smem();
+        mbar_arrive(&bars->v_full[s]);
+        mbar_arrive(&bars->v8_empty[s]);
       }
     }
     }
   } else {
     // ------------------------------------------------------------ softmax groups
-    if constexpr (C::FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    if constexpr (C::FP8)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     const int k = (warp - 4) >> 2;
     const int lgrp = warp & 3;         // TMEM lane group of this warp
     const int row = lgrp * 32 + lane;  // row inside the query tile
@@ -578,30 +777,35 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const uint32_t s_col = t_lane + kColS + 128 * k;
     const uint32_t o_col = t_lane + kColO + 128 * k;
     float* ml = reinterpret_cast<float*>(smem + C::OFF_ML);
+    int4* mine = reinterpret_cast<int4*>(smem + C::OFF_ROW) + k * kRowsTile + row;
     int base = 0;              // tiles of the items before
     uint32_t np = 0, np1 = 0;  // tiles of this group, and of group 1, so far
-    uint32_t n_solo = 0;
+    uint32_t n_solo = 0, nq = 0;  // solo items, items with tiles so far
     bool ok = true;
     for (int r = 0; ok && item_here(r); ++r) {
       const TcItem& t = items[r & 1];  // read in place: registers are short here
-      const int rows_total = t.it.n * Gr, pos0 = t.it.m - t.it.n;
       const bool pair = t.pair != 0;
-      const int m = t.m0 + (pair ? k * kRowsTile : 0) + row;
-      const int t_q = m / Gr, hg = m % Gr;
-      const bool valid = m < rows_total && hg < G;
-      const int pos = pos0 + t_q;
-      // visible tokens of this row: [lo_row, hi_row) and [0, sink_row)
-      const int hi_row = valid ? min(max(pos + 1, 0), p.ck.cap) : 0;
-      const int lo_row = (valid && p.ck.window > 0 && pos >= p.ck.window) ? pos - p.ck.window + 1 : 0;
-      const int sink_row = min(p.ck.n_sink, hi_row);
-      const bool active = __any_sync(0xffffffffu, valid);  // some row of this warp exists
-      const int hi_min = __reduce_min_sync(0xffffffffu, valid ? hi_row : INT_MAX);
-      const int hi_max = __reduce_max_sync(0xffffffffu, hi_row);
-      const int lo_max = __reduce_max_sync(0xffffffffu, lo_row);
-      const int lo_min = __reduce_min_sync(0xffffffffu, valid ? lo_row : INT_MAX);
-      const int sink_min = __reduce_min_sync(0xffffffffu, valid ? sink_row : INT_MAX);
-      const int sink_max = __reduce_max_sync(0xffffffffu, sink_row);
+      // What only edge tiles and the epilogue need waits in shared memory: the registers are full
+      // of scores and weights.
+      bool active;                  // some row of this warp exists
+      int hi_min, lo_max, sink_min;  // a tile in [lo_max, hi_min) (or below sink_min) every row sees
+      {
+        const int m = t.m0 + (pair ? k * kRowsTile : 0) + row;
+        const int t_q = m / Gr, hg = m % Gr;
+        const bool valid = m < t.it.n * Gr && hg < G;
+        const int pos = t.it.m - t.it.n + t_q;
+        // visible tokens of this row: [lo_row, hi_row) and [0, sink_row)
+        const int hi_row = valid ? min(max(pos + 1, 0), p.ck.cap) : 0;
+        const int lo_row = (valid && p.ck.window > 0 && pos >= p.ck.window) ? pos - p.ck.window + 1 : 0;
+        const int sink_row = min(p.ck.n_sink, hi_row);
+        active = __any_sync(0xffffffffu, valid);
+        hi_min = __reduce_min_sync(0xffffffffu, valid ? hi_row : INT_MAX);
+        lo_max = __reduce_max_sync(0xffffffffu, lo_row);
+        sink_min = __reduce_min_sync(0xffffffffu, valid ? sink_row : INT_MAX);
+        *mine = make_int4(hi_row, lo_row, sink_row, valid ? 1 : 0);
+      }
       float m_used = -INFINITY, l_sum = 0.f;
+      float q_scale = 0.f;  // fp8: the score scale times the row's own
       const int step = pair ? 1 : 2;  // this group's tiles: all, or every other
 
       int j = 0;  // tiles of the item done
@@ -612,138 +816,134 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         ++np;
         tc::fence_after_sync();
         if (active) {
-          const bool need_mask = hi_min < t0 + kTN || (t0 < lo_max && t0 + kTN > sink_min);
-          const int c_lo = min(max(lo_row - t0, 0), kTN);
-          const unsigned span = static_cast<unsigned>(max(min(max(hi_row - t0, 0), kTN) - c_lo, 0));
-          const int c_sink = min(max(sink_row - t0, 0), kTN);
-          auto visible = [&](int col) -> bool { return static_cast<unsigned>(col - c_lo) < span || col < c_sink; };
-          const bool row_vis = valid && (!need_mask || span > 0u || c_sink > 0);
+          const bool edge = hi_min < t0 + kTN || (t0 < lo_max && t0 + kTN > sink_min);
           // score scale (base 2) and V scale of the tile's halves
           float sl[2] = {p.scale_log2, p.scale_log2}, vs[2] = {1.f, 1.f};
           if constexpr (C::FP8) {
             const int x = base + i;
             ok = mbar_wait(&bars->sc_full[x % kScaleSlots], (x / kScaleSlots) & 1, p.err, kDevErrFullWait);
             const float4 sc = bars->scales[x % kScaleSlots];
-            sl[0] *= sc.x, vs[0] = sc.y, sl[1] *= sc.z, vs[1] = sc.w;
+            if (j == 0) {
+              // the row's own scale.  (Q of the item after the next one is split only after the
+              // next one's last scores, which follow this item's last P V)
+              ok = ok && mbar_wait(&bars->q8_full[nq & 1], (nq >> 1) & 1, p.err, kDevErrFullWait);
+              q_scale = p.scale_log2 *
+                        reinterpret_cast<const float*>(smem + C::OFF_QS)[((nq & 1) * 2 + (pair ? k : 0)) * kRowsTile + row];
+            }
+            sl[0] = q_scale * sc.x, vs[0] = sc.y, sl[1] = q_scale * sc.z, vs[1] = sc.w;
           }
-          uint32_t pk[kTN / 2];
-          uint64_t ls[2];  // fp32 pair sums of p
-          // 32 columns from TMEM as packed P.  masked: a compile-time flag, so that columns that
-          // every row sees carry no test
-          auto columns = [&](auto masked, auto chunk, float base0) {
-            constexpr int cc = decltype(chunk)::value;
+          if constexpr (C::FP8) {  // a masked score is an infinity that the scale makes -inf
+            sl[0] = sl[0] == 0.f ? 1e-37f : sl[0];
+            sl[1] = sl[1] == 0.f ? 1e-37f : sl[1];
+          }
+          if (edge) {
+            const float inf = -INFINITY;  // after the scale
+            hide_scores(s_col, t0, *mine, hi_min, lo_max, sink_min, C::FP8 && sl[0] < 0.f ? -inf : inf,
+                        C::FP8 && sl[1] < 0.f ? -inf : inf);
+          }
+          // the largest score (scaled) of 32 columns from TMEM
+          auto largest = [&](int cc) -> float {
             uint32_t x[2][16];
             tc::tmem_ld16(s_col + 32 * cc, x[0]);
             tc::tmem_ld16(s_col + 32 * cc + 16, x[1]);
             tc::tmem_wait_ld();
+            const float s2 = cc < 2 ? sl[0] : sl[1];
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const int col = 32 * cc + 2 * e;
-              const float v0 = __uint_as_float(x[e >> 3][(2 * e) & 15]);
-              const float v1 = __uint_as_float(x[e >> 3][(2 * e + 1) & 15]);
-              float a0, a1;
-              fma_pair(v0, v1, sl[cc >> 1], -base0, a0, a1);
-              if constexpr (decltype(masked)::value) {
-                a0 = visible(col) ? a0 : -INFINITY;
-                a1 = visible(col + 1) ? a1 : -INFINITY;
-              }
-              float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
-              ls[e & 1] = add_f32x2(ls[e & 1], p0, p1);
-              if constexpr (C::FP8) mul_pair(p0, p1, vs[cc >> 1]);  // V = code * scale
-              pk[16 * cc + e] = pack_bf16(p0, p1);
+              float u = __uint_as_float(x[e >> 3][(2 * e) & 15]), v = __uint_as_float(x[e >> 3][(2 * e + 1) & 15]);
+              if constexpr (C::FP8) u *= s2, v *= s2;  // (a scale may be negative)
+              m4[e & 3] = fmax3(m4[e & 3], u, v);
             }
+            const float m1 = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+            return C::FP8 ? m1 : m1 * s2;
           };
-          // What the warp's rows see of 32 columns: 0 nothing, 2 all of them, 1 some.  The rows of a
-          // warp are few tokens, so at most two of a tile's four chunks are mixed at an edge.
-          auto sees = [&](int cc) -> int {
-            const int a = t0 + 32 * cc, b = a + 32;
-            if (hi_max <= a || (lo_min >= b && sink_max <= a)) return 0;
-            return (hi_min >= b && (lo_max <= a || sink_min >= b)) ? 2 : 1;
-          };
-          auto edge_columns = [&](auto chunk, float base0) {
-            constexpr int cc = decltype(chunk)::value;
-            const int mode = sees(cc);
-            if (mode == 2) {
-              columns(std::false_type{}, chunk, base0);
-            } else if (mode == 1) {
-              columns(std::true_type{}, chunk, base0);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) pk[16 * cc + e] = 0u;
-            }
-          };
-          // a row's first visible tile, or one whose p sum passed the limit, takes the tile's
-          // true maximum first and rescales O and l to it
-          bool need = row_vis && m_used == -INFINITY;
-          for (bool again = false;; again = true) {
-            if (__any_sync(0xffffffffu, need)) {
-              float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          // A row's first visible tile starts from the maximum of the first 32 columns that it sees
+          // (the limit on the p sum allows that to be 2^16 short).  Rows that do not exist go along
+          // where no mask tells them apart
+          if (__any_sync(0xffffffffu, m_used == -INFINITY)) {
+            float mx = -INFINITY;
 #pragma unroll 1
-              for (int cc = 0; cc < kTN / 32; ++cc) {
-                const int mode = need_mask ? sees(cc) : 2;
-                if (mode == 0) continue;
-                uint32_t x[2][16];
-                tc::tmem_ld16(s_col + 32 * cc, x[0]);
-                tc::tmem_ld16(s_col + 32 * cc + 16, x[1]);
-                tc::tmem_wait_ld();
-                const float s2 = cc < 2 ? sl[0] : sl[1];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) x[e >> 4][e & 15] = __float_as_uint(__uint_as_float(x[e >> 4][e & 15]) * s2);
-                if (mode == 1) {
-#pragma unroll
-                  for (int e = 0; e < 32; ++e)
-                    if (!visible(32 * cc + e)) x[e >> 4][e & 15] = __float_as_uint(-INFINITY);
-                }
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                  mx[e & 3] = fmax3(mx[e & 3], __uint_as_float(x[e >> 3][(2 * e) & 15]),
-                                    __uint_as_float(x[e >> 3][(2 * e + 1) & 15]));
-              }
-              const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-              const float m_new = need ? fmaxf(m_used, tmax) : m_used;
-              // PV_k of this group's tile before ran before these scores: O_k is final here
-              if (__any_sync(0xffffffffu, need && m_used != -INFINITY)) {
-                const float alpha = (need && m_used != -INFINITY) ? fast_exp2(m_used - m_new) : 1.f;
-#pragma unroll 1
-                for (int c = 0; c < D / 16; c += 2) {
-                  uint32_t x[2][16];
-                  tc::tmem_ld16(o_col + 16 * c, x[0]);
-                  tc::tmem_ld16(o_col + 16 * (c + 1), x[1]);
-                  tc::tmem_wait_ld();
-#pragma unroll
-                  for (int h2 = 0; h2 < 2; ++h2)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) x[h2][e] = __float_as_uint(__uint_as_float(x[h2][e]) * alpha);
-                  tc::tmem_st16(o_col + 16 * c, x[0]);
-                  tc::tmem_st16(o_col + 16 * (c + 1), x[1]);
-                }
-                tc::tmem_wait_st();
-                l_sum *= alpha;
-              }
-              m_used = m_new;
+            for (int cc = 0; cc < kTN / 32; ++cc) {
+              mx = fmaxf(mx, largest(cc));
+              if (!__any_sync(0xffffffffu, m_used == -INFINITY && mx == -INFINITY)) break;
             }
-            ls[0] = ls[1] = 0ull;
-            const float base0 = (m_used == -INFINITY) ? 0.f : m_used;
-            if (need_mask) {
-              edge_columns(Int<0>{}, base0);
-              edge_columns(Int<1>{}, base0);
-              edge_columns(Int<2>{}, base0);
-              edge_columns(Int<3>{}, base0);
-            } else {
-              columns(std::false_type{}, Int<0>{}, base0);
-              columns(std::false_type{}, Int<1>{}, base0);
-              columns(std::false_type{}, Int<2>{}, base0);
-              columns(std::false_type{}, Int<3>{}, base0);
-            }
-            need = row_vis && !(sum_f32x2(ls[0]) + sum_f32x2(ls[1]) <= kTileSumLimit);
-            if (again || !__any_sync(0xffffffffu, need)) break;
+            if (m_used == -INFINITY) m_used = mx;
           }
+          uint32_t pk[kTN / 2];
+          uint64_t ls[2] = {0ull, 0ull};  // fp32 pair sums of p
+          {
+            const float base0 = (m_used == -INFINITY) ? 0.f : m_used;
 #pragma unroll
-          for (int cc = 0; cc < kTN / 32; ++cc) {
-            uint32_t w[16];
+            for (int cc = 0; cc < kTN / 32; ++cc) {
+              uint32_t x[2][16];
+              tc::tmem_ld16(s_col + 32 * cc, x[0]);
+              tc::tmem_ld16(s_col + 32 * cc + 16, x[1]);
+              tc::tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = pk[16 * cc + e];
-            tc::tmem_st16(s_col + 16 * cc, w);
+              for (int e = 0; e < 16; ++e) {
+                float a0, a1;
+                fma_pair(__uint_as_float(x[e >> 3][(2 * e) & 15]), __uint_as_float(x[e >> 3][(2 * e + 1) & 15]),
+                         sl[cc >> 1], -base0, a0, a1);
+                float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
+                ls[e & 1] = add_f32x2(ls[e & 1], p0, p1);
+                if constexpr (C::FP8) mul_pair(p0, p1, vs[cc >> 1]);  // V = code * scale
+                pk[16 * cc + e] = pack_bf16(p0, p1);
+              }
+            }
+          }
+          const bool need = !(sum_f32x2(ls[0]) + sum_f32x2(ls[1]) <= kTileSumLimit);
+          if (__any_sync(0xffffffffu, need)) {
+            // rare: O and l rescaled to the tile's true maximum, and its P again
+            float mx = m_used;
+#pragma unroll 1
+            for (int cc = 0; cc < kTN / 32; ++cc) mx = fmaxf(mx, largest(cc));
+            const float m_new = need ? mx : m_used;
+            // PV_k of this group's tile before ran before these scores: O_k is final here
+            const float alpha = (need && l_sum != 0.f) ? fast_exp2(m_used - m_new) : 1.f;
+            if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+              for (int c = 0; c < D / 16; ++c) {
+                uint32_t x[16];
+                tc::tmem_ld16(o_col + 16 * c, x);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * alpha);
+                tc::tmem_st16(o_col + 16 * c, x);
+              }
+              tc::tmem_wait_st();
+              l_sum *= alpha;
+            }
+            m_used = m_new;
+            const float base0 = (m_used == -INFINITY) ? 0.f : m_used;
+            ls[0] = ls[1] = 0ull;
+#pragma unroll 1
+            for (int cc = 0; cc < kTN / 32; ++cc) {
+              uint32_t x[2][16], w[16];
+              tc::tmem_ld16(s_col + 32 * cc, x[0]);
+              tc::tmem_ld16(s_col + 32 * cc + 16, x[1]);
+              tc::tmem_wait_ld();
+              const float s2 = cc < 2 ? sl[0] : sl[1], v2 = cc < 2 ? vs[0] : vs[1];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                float a0, a1;
+                fma_pair(__uint_as_float(x[e >> 3][(2 * e) & 15]), __uint_as_float(x[e >> 3][(2 * e + 1) & 15]), s2, -base0,
+                         a0, a1);
+                float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
+                ls[e & 1] = add_f32x2(ls[e & 1], p0, p1);
+                if constexpr (C::FP8) mul_pair(p0, p1, v2);
+                w[e] = pack_bf16(p0, p1);
+              }
+              tc::tmem_st16(s_col + 16 * cc, w);  // S columns 32 cc.. were read before P 16 cc.. is written
+            }
+          } else {
+#pragma unroll
+            for (int cc = 0; cc < kTN / 32; ++cc) {
+              uint32_t w[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) w[e] = pk[16 * cc + e];
+              tc::tmem_st16(s_col + 16 * cc, w);
+            }
           }
           tc::tmem_wait_st();
           l_sum += sum_f32x2(ls[0]) + sum_f32x2(ls[1]);
@@ -767,6 +967,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         mbar_arrive(&bars->p_full[k]);
       }
       base += t.n_tiles;
+      if (t.n_tiles > 0) ++nq;
       const int tiles1 = pair ? t.n_tiles : t.n_tiles / 2;  // group 1's
       np1 += tiles1;
       if (!ok) break;
@@ -809,39 +1010,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       constexpr float kLn2 = 0.6931471805599453f;
       const float lse = some ? (m_used + __log2f(l_sum)) * kLn2 : -INFINITY;
       const bool direct = t.it.n_chunk == 1;
-      const int h = t.it.g * G + hg;
+      const bool valid = mine->w != 0;
+      const int m = t.m0 + (pair ? k * kRowsTile : 0) + row;
+      const int t_q = m / Gr, h = t.it.g * G + m % Gr;
       const int64_t orow = direct ? (static_cast<int64_t>(t.it.row0) + t_q) * p.Hq + h
                                   : t.it.part_row + (static_cast<int64_t>(t.it.c) * t.it.n + t_q) * p.Hq + h;
       // an empty partial's o is never read
-      const bool write_o = valid && (direct || some);
-      if (active) {
-#pragma unroll 2
-        for (int c = 0; c < D / 16; ++c) {
-          uint32_t x0[16], x1[16];
-          if (t.n_tiles > 0) tc::tmem_ld16(o_col + 16 * c, x0);
-          if (both) tc::tmem_ld16(o_col + 128 + 16 * c, x1);
-          tc::tmem_wait_ld();
-          float x[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            x[e] = some0 ? __uint_as_float(x0[e]) * a0 : 0.f;
-            if (some1) x[e] = fmaf(__uint_as_float(x1[e]), a1, x[e]);
-          }
-          if (write_o) {
-            if (direct) {
-              __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.ck.out) + orow * D + 16 * c;
-              *reinterpret_cast<uint4*>(o) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
-                                                        pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-              *reinterpret_cast<uint4*>(o + 8) = make_uint4(pack_bf16(x[8], x[9]), pack_bf16(x[10], x[11]),
-                                                            pack_bf16(x[12], x[13]), pack_bf16(x[14], x[15]));
-            } else {
-              float* o = p.out_o + orow * D + 16 * c;
-#pragma unroll
-              for (int e = 0; e < 16; e += 4)
-                *reinterpret_cast<float4*>(o + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-            }
-          }
-        }
+      const unsigned write_o = __ballot_sync(0xffffffffu, valid && (direct || some));
+      if (write_o != 0u) {
+        store_rows<D>(o_col, t.n_tiles > 0, both, some0 ? a0 : 0.f, some0, some1 ? a1 : 0.f, some1, write_o, orow,
+                      direct ? p.ck.out : p.out_o, direct, smem_u32(smem + C::OFF_OUT + (warp - 4) * (32 * 64)));
       }
       if (valid) (direct ? p.ck.lse : p.out_lse)[orow] = lse;
       // (the next tile's p_full arrival orders these TMEM reads before the next PV writes O)

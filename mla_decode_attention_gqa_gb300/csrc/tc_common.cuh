@@ -86,6 +86,18 @@ __device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uin
       : "memory");
 }
 
+// The same with 8-bit operands (kind::f8f6f4; a K step is 32 elements, 32 bytes): the
+// instruction descriptor's A and B formats are 0 for e4m3.
+__device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // MMA with the A operand in tensor memory: D(tmem) (+)= A(tmem) * B(smem desc).  A holds
 // one row per TMEM lane and two 16-bit elements per 32-bit column (element 2c in the low
 // half of column c), so a K step of 16 elements spans 8 columns.
