@@ -195,6 +195,91 @@ __device__ __noinline__ void hide_scores(uint32_t s_col, int t0, int4 row, int h
   tc::tmem_wait_st();
 }
 
+// The largest score (scaled) of 32 columns in tensor memory.
+template <bool FP8>
+__device__ __forceinline__ float largest(uint32_t s_col, float scale) {
+  uint32_t x[2][16];
+  tc::tmem_ld16(s_col, x[0]);
+  tc::tmem_ld16(s_col + 16, x[1]);
+  tc::tmem_wait_ld();
+  float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    float u = __uint_as_float(x[e >> 3][(2 * e) & 15]), v = __uint_as_float(x[e >> 3][(2 * e + 1) & 15]);
+    if constexpr (FP8) u *= scale, v *= scale;  // (a block scale may be negative)
+    m4[e & 3] = fmax3(m4[e & 3], u, v);
+  }
+  const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+  return FP8 ? m : m * scale;
+}
+
+// A row's first visible tile (m = -inf) starts from the maximum of the first 32 columns that it
+// sees: the limit on the p sum allows that to be 2^16 short.  Rows that do not exist go along where
+// no mask tells them apart.
+template <bool FP8>
+__device__ __noinline__ float first_max(uint32_t s_col, float m, float scale0, float scale1) {
+  float mx = -INFINITY;
+#pragma unroll 1
+  for (int cc = 0; cc < kTN / 32; ++cc) {
+    mx = fmaxf(mx, largest<FP8>(s_col + 32 * cc, cc < 2 ? scale0 : scale1));
+    if (!__any_sync(0xffffffffu, m == -INFINITY && mx == -INFINITY)) break;
+  }
+  return m == -INFINITY ? mx : m;
+}
+
+// A tile in which the p sum of some row of the warp (need) passed the limit: O and l rescaled to
+// the tile's true maximum, and its P again.  PV of the group's tile before ran before these scores,
+// so O is final.  l comes back with the tile's sum.
+struct Redone {
+  float m, l;
+};
+template <int D, bool FP8>
+__device__ __noinline__ Redone redo_tile(uint32_t s_col, uint32_t o_col, bool need, float m, float l, float scale0,
+                                         float scale1, float v0, float v1) {
+  float mx = m;
+#pragma unroll 1
+  for (int cc = 0; cc < kTN / 32; ++cc) mx = fmaxf(mx, largest<FP8>(s_col + 32 * cc, cc < 2 ? scale0 : scale1));
+  const float m_new = need ? mx : m;
+  const float alpha = (need && l != 0.f) ? fast_exp2(m - m_new) : 1.f;
+  if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+    for (int c = 0; c < D; c += 16) {
+      uint32_t x[16];
+      tc::tmem_ld16(o_col + c, x);
+      tc::tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * alpha);
+      tc::tmem_st16(o_col + c, x);
+    }
+    tc::tmem_wait_st();
+    l *= alpha;
+  }
+  const float base = (m_new == -INFINITY) ? 0.f : m_new;
+  uint64_t ls[2] = {0ull, 0ull};
+#pragma unroll 1
+  for (int cc = 0; cc < kTN / 32; ++cc) {
+    uint32_t x[2][16], w[16];
+    tc::tmem_ld16(s_col + 32 * cc, x[0]);
+    tc::tmem_ld16(s_col + 32 * cc + 16, x[1]);
+    tc::tmem_wait_ld();
+    const float s2 = cc < 2 ? scale0 : scale1, v2 = cc < 2 ? v0 : v1;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      float a0, a1;
+      fma_pair(__uint_as_float(x[e >> 3][(2 * e) & 15]), __uint_as_float(x[e >> 3][(2 * e + 1) & 15]), s2, -base, a0, a1);
+      float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
+      ls[e & 1] = add_f32x2(ls[e & 1], p0, p1);
+      if constexpr (FP8) mul_pair(p0, p1, v2);
+      w[e] = pack_bf16(p0, p1);
+    }
+    tc::tmem_st16(s_col + 16 * cc, w);  // S columns 32 cc.. were read before P 16 cc.. is written
+  }
+  Redone r;
+  r.m = m_new;
+  r.l = l + sum_f32x2(ls[0]) + sum_f32x2(ls[1]);
+  return r;
+}
+
 // The warp's 32 output rows (orow: this lane's; bit r of write: row r exists) from tensor memory:
 // w0 O_k, plus w1 O_1 where both groups worked for the row, as bf16 or fp32.  64 bytes of every row
 // at a time go through shared memory, so that a store instruction covers 8 rows x 64 bytes instead
@@ -841,35 +926,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             hide_scores(s_col, t0, *mine, hi_min, lo_max, sink_min, C::FP8 && sl[0] < 0.f ? -inf : inf,
                         C::FP8 && sl[1] < 0.f ? -inf : inf);
           }
-          // the largest score (scaled) of 32 columns from TMEM
-          auto largest = [&](int cc) -> float {
-            uint32_t x[2][16];
-            tc::tmem_ld16(s_col + 32 * cc, x[0]);
-            tc::tmem_ld16(s_col + 32 * cc + 16, x[1]);
-            tc::tmem_wait_ld();
-            const float s2 = cc < 2 ? sl[0] : sl[1];
-            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float u = __uint_as_float(x[e >> 3][(2 * e) & 15]), v = __uint_as_float(x[e >> 3][(2 * e + 1) & 15]);
-              if constexpr (C::FP8) u *= s2, v *= s2;  // (a scale may be negative)
-              m4[e & 3] = fmax3(m4[e & 3], u, v);
-            }
-            const float m1 = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-            return C::FP8 ? m1 : m1 * s2;
-          };
-          // A row's first visible tile starts from the maximum of the first 32 columns that it sees
-          // (the limit on the p sum allows that to be 2^16 short).  Rows that do not exist go along
-          // where no mask tells them apart
-          if (__any_sync(0xffffffffu, m_used == -INFINITY)) {
-            float mx = -INFINITY;
-#pragma unroll 1
-            for (int cc = 0; cc < kTN / 32; ++cc) {
-              mx = fmaxf(mx, largest(cc));
-              if (!__any_sync(0xffffffffu, m_used == -INFINITY && mx == -INFINITY)) break;
-            }
-            if (m_used == -INFINITY) m_used = mx;
-          }
+          if (__any_sync(0xffffffffu, m_used == -INFINITY)) m_used = first_max<C::FP8>(s_col, m_used, sl[0], sl[1]);
           uint32_t pk[kTN / 2];
           uint64_t ls[2] = {0ull, 0ull};  // fp32 pair sums of p
           {
@@ -894,49 +951,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
           const bool need = !(sum_f32x2(ls[0]) + sum_f32x2(ls[1]) <= kTileSumLimit);
           if (__any_sync(0xffffffffu, need)) {
-            // rare: O and l rescaled to the tile's true maximum, and its P again
-            float mx = m_used;
-#pragma unroll 1
-            for (int cc = 0; cc < kTN / 32; ++cc) mx = fmaxf(mx, largest(cc));
-            const float m_new = need ? mx : m_used;
-            // PV_k of this group's tile before ran before these scores: O_k is final here
-            const float alpha = (need && l_sum != 0.f) ? fast_exp2(m_used - m_new) : 1.f;
-            if (__any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll 1
-              for (int c = 0; c < D / 16; ++c) {
-                uint32_t x[16];
-                tc::tmem_ld16(o_col + 16 * c, x);
-                tc::tmem_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * alpha);
-                tc::tmem_st16(o_col + 16 * c, x);
-              }
-              tc::tmem_wait_st();
-              l_sum *= alpha;
-            }
-            m_used = m_new;
-            const float base0 = (m_used == -INFINITY) ? 0.f : m_used;
-            ls[0] = ls[1] = 0ull;
-#pragma unroll 1
-            for (int cc = 0; cc < kTN / 32; ++cc) {
-              uint32_t x[2][16], w[16];
-              tc::tmem_ld16(s_col + 32 * cc, x[0]);
-              tc::tmem_ld16(s_col + 32 * cc + 16, x[1]);
-              tc::tmem_wait_ld();
-              const float s2 = cc < 2 ? sl[0] : sl[1], v2 = cc < 2 ? vs[0] : vs[1];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                float a0, a1;
-                fma_pair(__uint_as_float(x[e >> 3][(2 * e) & 15]), __uint_as_float(x[e >> 3][(2 * e + 1) & 15]), s2, -base0,
-                         a0, a1);
-                float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
-                ls[e & 1] = add_f32x2(ls[e & 1], p0, p1);
-                if constexpr (C::FP8) mul_pair(p0, p1, v2);
-                w[e] = pack_bf16(p0, p1);
-              }
-              tc::tmem_st16(s_col + 16 * cc, w);  // S columns 32 cc.. were read before P 16 cc.. is written
-            }
+            const Redone again = redo_tile<D, C::FP8>(s_col, o_col, need, m_used, l_sum, sl[0], sl[1], vs[0], vs[1]);
+            m_used = again.m;
+            l_sum = again.l;
           } else {
+            l_sum += sum_f32x2(ls[0]) + sum_f32x2(ls[1]);
 #pragma unroll
             for (int cc = 0; cc < kTN / 32; ++cc) {
               uint32_t w[16];
@@ -946,7 +965,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
           }
           tc::tmem_wait_st();
-          l_sum += sum_f32x2(ls[0]) + sum_f32x2(ls[1]);
         }
         const bool inside = (t0 >= t.tl.lo && t0 + kTN <= t.tl.hi) || t0 + kTN <= t.tl.sinks;
         if (!inside && (k == 0 || !pair)) {
