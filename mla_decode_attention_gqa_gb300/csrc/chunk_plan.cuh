@@ -42,8 +42,8 @@ __device__ __forceinline__ void chunk_lengths(const ChunkArgs& a, int b, int* ro
   *m = __ldg(a.seq_lens + b);
 }
 
-// Token tiles seen by the rows at positions [p0, p1] of a sequence with `cap` tokens at most:
-// the tiles below n_first hold the sinks, then come the tiles from win on; tile i of the
+// Blocks of kTileN tokens seen by the rows at positions [p0, p1] of a sequence with `cap` tokens
+// at most: those below n_first hold the sinks, then come the ones from win on; block i of the
 // item is i < n_first ? i : win + (i - n_first).  lo / hi: the window's token range (of all
 // the rows together); sinks: the first tokens seen besides it.
 struct ChunkTiles {
@@ -51,7 +51,8 @@ struct ChunkTiles {
   int n_first, win, n;
 };
 
-__device__ __forceinline__ ChunkTiles chunk_tiles(int window, int n_sink, int cap, int p0, int p1, int tile) {
+__device__ __forceinline__ ChunkTiles chunk_tiles(int window, int n_sink, int cap, int p0, int p1) {
+  constexpr int tile = kTileN;
   ChunkTiles t;
   t.hi = min(max(p1 + 1, 0), cap);
   t.lo = (window > 0 && p0 >= window) ? p0 - window + 1 : 0;
@@ -60,7 +61,7 @@ __device__ __forceinline__ ChunkTiles chunk_tiles(int window, int n_sink, int ca
   t.n_first = t.lo > 0 ? (t.sinks + tile - 1) / tile : 0;
   t.win = t.lo / tile;
   const int end = (t.hi + tile - 1) / tile;
-  if (t.lo > 0 && t.n_first > t.win) t.n_first = t.win;  // a tile of both is the window's
+  if (t.lo > 0 && t.n_first > t.win) t.n_first = t.win;  // a block of both is the window's
   t.n = t.n_first + max(end - t.win, 0);
   return t;
 }
@@ -69,8 +70,9 @@ __device__ __forceinline__ ChunkTiles chunk_tiles(int window, int n_sink, int ca
 __device__ __forceinline__ void chunk_extent(const ChunkArgs& a, int n, int m, int* row_tiles, int* kv_tiles) {
   *row_tiles = static_cast<int>((static_cast<int64_t>(n) * a.group_rows + a.rows - 1) / a.rows);
   const int span = min(n, (a.rows + a.group_rows - 1) / a.group_rows + 1);
-  const ChunkTiles t = chunk_tiles(a.window, a.n_sink, a.cap, m - span, m - 1, a.tile);
-  *kv_tiles = max(t.n, 1);
+  const ChunkTiles t = chunk_tiles(a.window, a.n_sink, a.cap, m - span, m - 1);
+  const int per = a.tile / kTileN;
+  *kv_tiles = max((t.n + per - 1) / per, 1);
 }
 
 // The plan in device memory: [kPlanItems] work items, [kPlanMerged] rows to merge, [kPlanNext] the

@@ -83,6 +83,7 @@ struct TcCfg {
   static constexpr int OFF_OUT = OFF_QS + (FP8 ? 4 * kRowsTile * 4 : 0);  // 64 bytes of each output row
   static constexpr int OFF_ROW = OFF_OUT + 2 * kRowsTile * 64;            // what each softmax thread's row sees
   static constexpr int SMEM = 1024 + OFF_ROW + 2 * kRowsTile * 16;
+  static_assert(kHalf == kTileN, "the plan counts in halves");
   static_assert(!FP8 || D == 128, "e4m3 rows are one 128-byte box");
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
@@ -109,11 +110,13 @@ struct TcItem {
   ChunkTiles tl;
   int m0;       // first row of the row tile
   int pair;     // more than 128 rows
-  int i0;       // first tile of the chunk in tl's run
-  int n_tiles;  // tiles of the chunk
-  __device__ __forceinline__ int token(int i) const {  // first token of the chunk's tile i
-    const int x = i0 + i;
-    return (x < tl.n_first ? x : tl.win + (x - tl.n_first)) * kTN;
+  int h0;       // first half of the chunk in tl's run
+  int n_tiles;  // tiles of the chunk, two halves each
+  // First token of the chunk's half h: tile i is the halves 2 i and 2 i + 1, which need not follow
+  // one another (sinks and window; the last one may lie behind the run: no row sees its tokens).
+  __device__ __forceinline__ int token(int h) const {
+    const int x = h0 + h;
+    return (x < tl.n_first ? x : tl.win + (x - tl.n_first)) * kHalf;
   }
 };
 
@@ -163,20 +166,20 @@ __device__ __forceinline__ void mul_pair(float& x0, float& x1, float s) {
 }
 
 // An edge tile: the scores that this thread's row does not see (row: its end, the start of its
-// window, the end of its sinks) become `out` in tensor memory, out0 in the first 64 columns, so that
+// window, the end of its sinks) become out0 (first half) or out1 in tensor memory, so that
 // the passes over the scores carry no test.  hi_min, lo_max, sink_min: columns that the whole warp
 // sees are left alone.  (A function of its own, as store_rows is: inlined, their registers spilled
 // into the loop over the tiles, which then took 1.6 us a tile instead of 1.4.)
-__device__ __noinline__ void hide_scores(uint32_t s_col, int t0, int4 row, int hi_min, int lo_max, int sink_min,
+__device__ __noinline__ void hide_scores(uint32_t s_col, int ta, int tb, int4 row, int hi_min, int lo_max, int sink_min,
                                          float out0, float out1) {
 #pragma unroll 1
   for (int c = 0; c < kTN; c += 32) {
-    const int a = t0 + c, b = a + 32;
+    const int a = c < kHalf ? ta + c : tb + c - kHalf, b = a + 32;
     if (hi_min >= b && (lo_max <= a || sink_min >= b)) continue;  // all see all
     uint32_t x[2][16];
     tc::tmem_ld16(s_col + c, x[0]);
     tc::tmem_ld16(s_col + c + 16, x[1]);
-    const uint32_t out = __float_as_uint(c < 64 ? out0 : out1);
+    const uint32_t out = __float_as_uint(c < kHalf ? out0 : out1);
     uint32_t seen[2];  // bit e: column 16 h + e is seen
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -435,10 +438,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int m_last = min(t.m0 + 2 * kRowsTile, t.it.n * Gr) - 1;
         t.pair = m_last - t.m0 >= kRowsTile ? 1 : 0;
         const int pos0 = t.it.m - t.it.n;
-        t.tl = chunk_tiles(p.ck.window, p.ck.n_sink, p.ck.cap, pos0 + t.m0 / Gr, pos0 + m_last / Gr, kTN);
-        const int per = (t.tl.n + t.it.n_chunk - 1) / t.it.n_chunk;
-        t.i0 = min(t.it.c * per, t.tl.n);
-        t.n_tiles = min(per, t.tl.n - t.i0);
+        t.tl = chunk_tiles(p.ck.window, p.ck.n_sink, p.ck.cap, pos0 + t.m0 / Gr, pos0 + m_last / Gr);
+        const int tiles = (t.tl.n + 1) / 2, per = (tiles + t.it.n_chunk - 1) / t.it.n_chunk;
+        const int i0 = min(t.it.c * per, tiles);
+        t.h0 = 2 * i0;
+        t.n_tiles = min(per, tiles - i0);
       }
       if (lane == 0) {
         items[s] = t;
@@ -475,10 +479,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       int page[2], at[2];  // of a tile's two halves
       float scale = 0.f;   // fp8: lanes 0-3 of the K loader
       auto look_up = [&](int i) {
-        const int a = t.token(i);
+        const int first[2] = {t.token(2 * i), t.token(2 * i + 1)};
         // a second half at or past the capacity holds no token: it takes the first one's page
         // instead of an entry behind the table's row
-        const int b = a + kHalf < p.ck.cap ? a + kHalf : a;
+        const int a = first[0], b = first[1] < p.ck.cap ? first[1] : a;
         at[0] = a % p.block_len;
         at[1] = b % p.block_len;
         page[0] = kv_page_of(p, t.it.b, a);
@@ -486,7 +490,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if constexpr (C::FP8) {
           // the scales of both halves, a lane each (K, V, K, V).  Halves in which no row sees a token,
           // and pages outside the cache, take 0: their scales may be anything
-          const int hf = (lane >> 1) & 1, tok = a + hf * kHalf, pg = page[hf];
+          const int hf = (lane >> 1) & 1, tok = first[hf], pg = page[hf];
           const bool seen = (tok < t.tl.hi && tok + kHalf > t.tl.lo) || tok < t.tl.sinks;
           scale = 0.f;
           if (is_k && lane < 4 && seen && pg >= 0 && pg < p.num_blocks) {
@@ -895,13 +899,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
       int j = 0;  // tiles of the item done
       for (int i = pair ? 0 : k; i < t.n_tiles; i += step, ++j) {
-        const int t0 = t.token(i);
+        const int ta = t.token(2 * i), tb = t.token(2 * i + 1);  // the halves' first tokens
         ok = mbar_wait(&bars->s_full[k], np & 1, p.err, kDevErrFullWait);
         if (!ok) break;
         ++np;
         tc::fence_after_sync();
         if (active) {
-          const bool edge = hi_min < t0 + kTN || (t0 < lo_max && t0 + kTN > sink_min);
+          auto all_see = [&](int a) { return hi_min >= a + kHalf && (lo_max <= a || sink_min >= a + kHalf); };
+          const bool edge = !all_see(ta) || !all_see(tb);
           // score scale (base 2) and V scale of the tile's halves
           float sl[2] = {p.scale_log2, p.scale_log2}, vs[2] = {1.f, 1.f};
           if constexpr (C::FP8) {
@@ -923,7 +928,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
           if (edge) {
             const float inf = -INFINITY;  // after the scale
-            hide_scores(s_col, t0, *mine, hi_min, lo_max, sink_min, C::FP8 && sl[0] < 0.f ? -inf : inf,
+            hide_scores(s_col, ta, tb, *mine, hi_min, lo_max, sink_min, C::FP8 && sl[0] < 0.f ? -inf : inf,
                         C::FP8 && sl[1] < 0.f ? -inf : inf);
           }
           if (__any_sync(0xffffffffu, m_used == -INFINITY)) m_used = first_max<C::FP8>(s_col, m_used, sl[0], sl[1]);
@@ -966,18 +971,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
           tc::tmem_wait_st();
         }
-        const bool inside = (t0 >= t.tl.lo && t0 + kTN <= t.tl.hi) || t0 + kTN <= t.tl.sinks;
-        if (!inside && (k == 0 || !pair)) {
+        auto inside = [&](int a) { return (a >= t.tl.lo && a + kHalf <= t.tl.hi) || a + kHalf <= t.tl.sinks; };
+        if ((k == 0 || !pair) && !(inside(ta) && inside(tb))) {
           // tokens that no row of the item sees may hold anything: zero their V rows, so that
           // p = 0 really counts nothing
           const int x = base + i, s = x % NST;
           mbar_wait(&bars->v_full[s], (x / NST) & 1, p.err, kDevErrFullWait);
-          const int tok = t0 + row;
-          if (!((tok >= t.tl.lo && tok < t.tl.hi) || tok < t.tl.sinks)) {
-            uint8_t* vt = smem + C::OFF_V + s * C::TILE + row * 128;
-            for (int bx = 0; bx < NB; ++bx)
-              for (int cc = 0; cc < 8; ++cc)
-                *reinterpret_cast<uint4*>(vt + bx * C::BOX + cc * 16) = make_uint4(0u, 0u, 0u, 0u);
+          for (int y = row >> 3; y < kTN; y += 16) {  // 8 threads a row
+            const int tok = y < kHalf ? ta + y : tb + y - kHalf;
+            if (!((tok >= t.tl.lo && tok < t.tl.hi) || tok < t.tl.sinks)) {
+              uint8_t* vt = smem + C::OFF_V + s * C::TILE + y * 128 + (row & 7) * 16;
+              for (int bx = 0; bx < NB; ++bx) *reinterpret_cast<uint4*>(vt + bx * C::BOX) = make_uint4(0u, 0u, 0u, 0u);
+            }
           }
           fence_proxy_async_smem();
         }

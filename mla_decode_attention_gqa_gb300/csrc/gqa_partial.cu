@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
     causal_offset = ci.m - ci.n;
     const int m_last = min(m0 + C::ROWS, rows_total) - 1;
     const ChunkTiles t = chunk_tiles(p.ck.window, p.ck.n_sink, p.ck.cap, ci.m - ci.n + m0 / p.G,
-                                     ci.m - ci.n + m_last / p.G, TN);
+                                     ci.m - ci.n + m_last / p.G);
     const int ct = (t.n + ci.n_chunk - 1) / ci.n_chunk;
     const int i0 = min(c * ct, t.n);
     n_tiles = min(ct, t.n - i0);
