@@ -412,9 +412,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     return true;
   };
 
-  // fp8: the launch's 512 threads x 128 registers as 128 x (104 + 88 + 160 + 160)
+  // fp8: the launch's 512 threads x 128 registers as 128 x (88 + 72 + 176 + 176)
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if constexpr (C::FP8)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    else
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
   if (warp == 3) {
     // ------------------------------------------------------------ scheduler
     // Items are handed out one by one (a counter that the plan kernel cleared), so that CTAs
@@ -725,7 +728,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   } else if (warp >= 12) {  // (fp8 only: no such warps otherwise)
     // ------------------------------------------------------------ fp8: Q split, V codes to bf16
     if constexpr (C::FP8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     const int row = (warp - 12) * 32 + lane;
     // Q for the products with e4m3 keys: a row times the power of two that puts its largest
     // magnitude in [2^7, 2^8) is the sum of two e4m3 values, the rounded one and the rest.  A bf16
@@ -856,7 +859,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   } else {
     // ------------------------------------------------------------ softmax groups
     if constexpr (C::FP8)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     else
       asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     const int k = (warp - 4) >> 2;
