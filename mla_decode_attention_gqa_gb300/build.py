@@ -19,7 +19,7 @@ LIB_PATH = os.path.join(HERE, LIB_NAME)
 BUILD_DIR = os.path.join(HERE, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "gqa_partial.cu", "mla_partial.cu", "merge_lse.cu", "umma_selftest.cu", "attn_tc.cu", "mla_tc.cu",
-           "chunk_tc.cu", "chunk_merge.cu", "qk_norm_rope.cu"]
+           "chunk_tc.cu", "chunk_rows.cu", "chunk_merge.cu", "qk_norm_rope.cu"]
 
 
 def _nvcc():

@@ -1064,47 +1064,33 @@ int padded_group(int G) {
 struct ChunkPlan {
   bool tc = false;         // the tensor-core kernel
   int group_rows = 1;      // rows of one token
-  int tile = kTileN;       // tokens of a KV tile
-  GqaVariant variant = GqaVariant::kBf16D128Decode;
   int rows = 0;            // rows of a row tile
-  int64_t n_wave = 0;      // work items resident at once
-  int64_t n_target = 0;    // most items of sequences with several chunks
-  int64_t n_items = 0;     // blocks: an upper bound of the work items
+  int tile = kTileN;       // tokens of a KV tile
+  int64_t n_wave = 0;      // CTAs resident at once
+  int64_t n_target = 0;    // tensor cores: most items of sequences with several chunks
+  int64_t n_items = 0;     // tensor cores: an upper bound of the work items
   int64_t part_rows = 0;   // an upper bound of the partial rows
   size_t plan_bytes = 0, o_bytes = 0, lse_bytes = 0;
 };
 
 skv_status chunk_plan(const skv_chunk_desc* c, const skv_desc* d, ChunkPlan* pl) {
   const int G = d->Hq / d->Hkv;
-  // the caller's bound on the chunk lengths chooses the row tile (results do not depend on it)
+  // The caller's bound on the chunk lengths chooses the kernel (results do not depend on it): up
+  // to 16 rows of a KV head fill an mma.sync tile, where the tensor cores' 128 are mostly padding
+  // (decode of 64 sequences, 64 / 8 heads: RATIO); a group above 128 heads has no query tile there.
   const int64_t longest = c->max_q_len > 0 ? std::min(c->max_q_len, c->T) : c->T;
-  const bool few = longest * G <= 16;
-  pl->group_rows = G;
-  int per_sm = 1;
-  pl->tc = !few && G <= 128;
-  if (d->kv_dtype == SKV_KV_FP8_E4M3)
-    pl->variant = few ? GqaVariant::kFp8D128Decode : GqaVariant::kFp8D128Prefill;
-  else if (d->dk == 64)
-    pl->variant = few ? GqaVariant::kBf16D64Decode : GqaVariant::kBf16D64Prefill;
-  else
-    pl->variant = few ? GqaVariant::kBf16D128Decode : GqaVariant::kBf16D128Prefill;
-  if (pl->tc) {
-    pl->group_rows = padded_group(G);
-    pl->rows = chunk_tc_rows();
-    pl->tile = chunk_tc_kv_tile();
-  } else {
-    const GqaLaunchInfo li = gqa_launch_info(pl->variant);
-    pl->rows = li.rows_per_cta;
-    per_sm = li.ctas_per_sm;
-  }
-  pl->n_wave = static_cast<int64_t>(device_sm_count()) * per_sm;
+  pl->tc = longest * G > 16 && G <= 128;
+  pl->group_rows = pl->tc ? padded_group(G) : G;
+  pl->rows = pl->tc ? chunk_tc_rows() : chunk_rows_per_tile();
+  pl->tile = pl->tc ? chunk_tc_kv_tile() : kTileN;
+  pl->n_wave = static_cast<int64_t>(device_sm_count()) * (pl->tc ? 1 : chunk_rows_ctas_per_sm());
   pl->n_target = 4 * pl->n_wave;
   const int64_t rows = static_cast<int64_t>(c->T) * pl->group_rows;
   if (rows + pl->rows >= (int64_t(1) << 31)) return fail(SKV_EINVAL, "T * Hq / Hkv is too large for one call");
   const int64_t row_tiles = rows / pl->rows + std::min(c->B, c->T);  // each sequence's last one may be short
   pl->n_items = row_tiles * d->Hkv + pl->n_target;
   if (pl->n_items >= (int64_t(1) << 31)) return fail(SKV_EINVAL, "T * Hq is too large for one call");
-  pl->part_rows = pl->n_target * std::min<int64_t>(pl->rows, rows);
+  pl->part_rows = pl->tc ? pl->n_target * std::min<int64_t>(pl->rows, rows) : 2 * pl->n_wave * pl->rows;
   pl->plan_bytes = align_up((kPlanHead + kPlanRow * static_cast<size_t>(c->B)) * 4, 256);
   pl->o_bytes = align_up(static_cast<size_t>(pl->part_rows) * d->dv * 4, 256);
   pl->lse_bytes = align_up(static_cast<size_t>(pl->part_rows) * 4, 256);
@@ -1186,13 +1172,14 @@ skv_status attn_chunk_paged(const skv_chunk_desc* desc, const skv_paged* paged, 
   if (e == cudaSuccess) e = timing_mark(false, s);
   if (e == cudaSuccess)
     e = pl.tc ? launch_chunk_tc(p, d.dk, d.kv_dtype == SKV_KV_FP8_E4M3, tmq, tmk, tmv, pl.n_items, s)
-              : launch_gqa_chunk(pl.variant, p, tmk, tmv, pl.n_items, s);
+              : launch_chunk_rows(p, d.dk, d.kv_dtype == SKV_KV_FP8_E4M3, tmk, tmv, s);
   if (e == cudaSuccess) e = timing_mark(true, s);
   if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
   if (d.S_max <= pl.tile) return SKV_OK;  // one KV tile at most: never several chunks
   // rows that can be in several chunks: no more than a partial row each
   const int64_t rows = std::min<int64_t>(static_cast<int64_t>(desc->T) * d.Hq, pl.part_rows);
-  e = launch_chunk_merge(p.ck, d.dv, part_o, part_lse, rows, s);
+  e = pl.tc ? launch_chunk_merge(p.ck, d.dv, part_o, part_lse, rows, s)
+            : launch_chunk_runs_merge(p.ck, d.dv, part_o, part_lse, s);
   if (e != cudaSuccess) return cuda_fail(e, "chunk merge launch");
   return SKV_OK;
 }

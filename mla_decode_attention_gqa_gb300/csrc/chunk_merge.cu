@@ -33,14 +33,14 @@ struct Joined {
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 };
 
-// Partials first, first + step, .. below k; lse0 / o0: partial 0 of the row, `stride` rows apart.
-template <int D>
-__device__ __forceinline__ Joined join(const float* lse0, const float* o0, int64_t stride, int first, int step, int k,
+// Partials first, first + step, .. below k of one row; at(c): the row of partial c.
+template <int D, class At>
+__device__ __forceinline__ Joined join(const float* part_o, const float* part_lse, At&& at, int first, int step, int k,
                                        int lane) {
   Joined j;
   bool nan = false;  // a NaN partial makes the row NaN (fmaxf drops it)
   for (int c = first + lane * step; c < k; c += 32 * step) {
-    const float l = lse0[c * stride];
+    const float l = part_lse[at(c)];
     nan = nan || l != l;
     j.m = fmaxf(j.m, l);
   }
@@ -54,9 +54,9 @@ __device__ __forceinline__ Joined join(const float* lse0, const float* o0, int64
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       const int c = c0 + u * step;
-      const float l = c < k ? lse0[c * stride] : -INFINITY;
+      const float l = c < k ? part_lse[at(c)] : -INFINITY;
       w[u] = l == -INFINITY ? 0.f : __expf(l - j.m);  // an empty partial's o was never written
-      x[u] = (l != -INFINITY && 4 * lane < D) ? *reinterpret_cast<const float4*>(o0 + c * stride * D + 4 * lane)
+      x[u] = (l != -INFINITY && 4 * lane < D) ? *reinterpret_cast<const float4*>(part_o + at(c) * D + 4 * lane)
                                               : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 #pragma unroll
@@ -85,13 +85,50 @@ __device__ __forceinline__ void store_row(const ChunkArgs& a, int64_t row, const
   if (lane == 0) a.lse[row] = j.den != 0.f ? j.m + logf(j.den) : -INFINITY;
 }
 
+// One row's partials dealt to the block's warps.
+template <int D>
+struct BlockJoin {
+  float m[kRowsPerBlock], den[kRowsPerBlock];
+  float4 acc[kRowsPerBlock][D / 4];
+};
+template <int D, class At>
+__device__ __forceinline__ void join_by_block(const ChunkArgs& a, BlockJoin<D>& sm, const float* part_o,
+                                              const float* part_lse, At&& at, int k, int64_t row) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Joined j = join<D>(part_o, part_lse, at, warp, kRowsPerBlock, k, lane);
+  __syncthreads();  // the sums before were read
+  if (lane == 0) {
+    sm.m[warp] = j.m;
+    sm.den[warp] = j.den;
+  }
+  if (4 * lane < D) sm.acc[warp][lane] = j.acc;
+  __syncthreads();
+  if (warp == 0) {
+    Joined s;
+#pragma unroll
+    for (int v = 0; v < kRowsPerBlock; ++v) s.m = fmaxf(s.m, sm.m[v]);
+#pragma unroll
+    for (int v = 0; v < kRowsPerBlock; ++v) {
+      const float f = sm.m[v] == -INFINITY ? 0.f : __expf(sm.m[v] - s.m);
+      s.den += f * sm.den[v];
+      if (4 * lane < D) {
+        const float4 x = sm.acc[v][lane];
+        s.acc.x += f * x.x;
+        s.acc.y += f * x.y;
+        s.acc.z += f * x.z;
+        s.acc.w += f * x.w;
+      }
+    }
+    store_row<D>(a, row, s, lane);
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(32 * kRowsPerBlock)
     chunk_merge_kernel(const __grid_constant__ ChunkArgs a, const float* part_o, const float* part_lse) {
   __shared__ int sm_parts[kRowsPerBlock], sm_n[kRowsPerBlock];
   __shared__ int64_t sm_row[kRowsPerBlock], sm_part[kRowsPerBlock];
-  __shared__ float sm_m[kRowsPerBlock], sm_den[kRowsPerBlock];
-  __shared__ float4 sm_acc[kRowsPerBlock][D / 4];
+  __shared__ BlockJoin<D> sm_join;
   // the attention kernel before it on the stream is complete and its writes are visible
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -127,44 +164,58 @@ __global__ void __launch_bounds__(32 * kRowsPerBlock)
     int most = 0;
 #pragma unroll
     for (int w = 0; w < kRowsPerBlock; ++w) most = max(most, sm_parts[w]);
+    auto at = [&](int w) {
+      const int64_t first = sm_part[w], stride = static_cast<int64_t>(sm_n[w]) * Hq;
+      return [first, stride](int c) -> int64_t { return first + c * stride; };
+    };
     if (most <= kWarpParts) {
-      if (r < rows) {
-        const int64_t stride = static_cast<int64_t>(sm_n[warp]) * Hq;
-        const Joined j = join<D>(part_lse + sm_part[warp], part_o + sm_part[warp] * D, stride, 0, 1, sm_parts[warp], lane);
-        store_row<D>(a, sm_row[warp], j, lane);
-      }
-      continue;
+      if (r < rows) store_row<D>(a, sm_row[warp], join<D>(part_o, part_lse, at(warp), 0, 1, sm_parts[warp], lane), lane);
+    } else {
+      for (int w = 0; w < kRowsPerBlock && r0 + w < rows; ++w)
+        join_by_block<D>(a, sm_join, part_o, part_lse, at(w), sm_parts[w], sm_row[w]);
     }
-    for (int w = 0; w < kRowsPerBlock && r0 + w < rows; ++w) {
-      const int64_t stride = static_cast<int64_t>(sm_n[w]) * Hq;
-      const Joined j = join<D>(part_lse + sm_part[w], part_o + sm_part[w] * D, stride, warp, kRowsPerBlock, sm_parts[w],
-                               lane);
-      __syncthreads();  // the previous row's sums were read
-      if (lane == 0) {
-        sm_m[warp] = j.m;
-        sm_den[warp] = j.den;
-      }
-      if (4 * lane < D) sm_acc[warp][lane] = j.acc;
-      __syncthreads();
-      if (warp == w) {
-        Joined s;
-#pragma unroll
-        for (int v = 0; v < kRowsPerBlock; ++v) s.m = fmaxf(s.m, sm_m[v]);
-#pragma unroll
-        for (int v = 0; v < kRowsPerBlock; ++v) {
-          const float f = sm_m[v] == -INFINITY ? 0.f : __expf(sm_m[v] - s.m);
-          s.den += f * sm_den[v];
-          if (4 * lane < D) {
-            const float4 x = sm_acc[v][lane];
-            s.acc.x += f * x.x;
-            s.acc.y += f * x.y;
-            s.acc.z += f * x.z;
-            s.acc.w += f * x.w;
-          }
-        }
-        store_row<D>(a, sm_row[w], s, lane);
-      }
-    }
+  }
+}
+
+// The merge after the kernel for few rows: block c looks at the border between the runs of CTAs
+// c - 1 and c.  If it lies inside an item, that item's partials are those of the CTAs whose
+// runs reach into it, and the blocks of all its borders share its rows.
+template <int D>
+__global__ void __launch_bounds__(32 * kRowsPerBlock)
+    chunk_runs_merge_kernel(const __grid_constant__ ChunkArgs a, const float* part_o, const float* part_lse) {
+  __shared__ BlockJoin<D> sm_join;
+  const int c = blockIdx.x + 1;
+  ChunkRuns runs;
+  ChunkShare sh;
+  // (reads lengths only: under the attention kernel's end)
+  const bool any = chunk_find_runs<32 * kRowsPerBlock>(a, a.n_wave, c, &runs, &sh);
+  int tile = 0;
+  const int64_t item = any ? runs.seek(a, &tile) : 0;
+  // the attention kernel before it on the stream is complete and its writes are visible (also where
+  // there is nothing to do: what comes after this grid may rely on both)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (tile == 0) return;
+  const int64_t u0 = runs.u - tile;  // the item's first tile
+  const int c0 = sh.owner(u0), c1 = sh.owner(u0 + runs.kt - 1);
+  const int k = c1 - c0 + 1, borders = c1 - c0, mine = c - c0 - 1;
+  const int first = sh.start(c0) == u0 ? 2 * c0 : 2 * c0 + 1;  // c0's run begins with the item, or ends in it
+  const int mt = runs.rt - 1 - static_cast<int>(item / a.Hkv), g = static_cast<int>(item % a.Hkv);
+  const int m0 = mt * a.rows, rows = min(a.rows, runs.n * a.G - m0);
+  auto out_row = [&](int r) -> int64_t {
+    const int m = m0 + r;
+    return (static_cast<int64_t>(runs.row0) + m / a.G) * (a.Hkv * a.G) + g * a.G + m % a.G;
+  };
+  auto at = [&](int r) {
+    const int64_t p0 = static_cast<int64_t>(first) * a.rows + r, p1 = static_cast<int64_t>(2 * c0) * a.rows + r;
+    const int64_t step = 2 * a.rows;
+    return [p0, p1, step](int i) -> int64_t { return i == 0 ? p0 : p1 + i * step; };
+  };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (k <= kWarpParts) {
+    for (int r = mine * kRowsPerBlock + warp; r < rows; r += borders * kRowsPerBlock)
+      store_row<D>(a, out_row(r), join<D>(part_o, part_lse, at(r), 0, 1, k, lane), lane);
+  } else {
+    for (int r = mine; r < rows; r += borders) join_by_block<D>(a, sm_join, part_o, part_lse, at(r), k, out_row(r));
   }
 }
 
@@ -192,6 +243,22 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
 cudaError_t launch_chunk_plan(const ChunkArgs& a, cudaStream_t stream) {
   chunk_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
   return cudaGetLastError();
+}
+
+cudaError_t launch_chunk_runs_merge(const ChunkArgs& a, int32_t d, const float* part_o, const float* part_lse,
+                                    cudaStream_t stream) {
+  if (a.n_wave <= 1) return cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned int>(a.n_wave - 1));
+  cfg.blockDim = dim3(32 * kRowsPerBlock);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (d == 64) return cudaLaunchKernelEx(&cfg, chunk_runs_merge_kernel<64>, a, part_o, part_lse);
+  return cudaLaunchKernelEx(&cfg, chunk_runs_merge_kernel<128>, a, part_o, part_lse);
 }
 
 cudaError_t launch_chunk_merge(const ChunkArgs& a, int32_t d, const float* part_o, const float* part_lse,

@@ -11,9 +11,9 @@
 // (which bounds the workspace), and those with k_b = 1 at most Hkv * (row tiles).
 //
 // The persistent tensor-core kernel takes its items from a plan that one small kernel wrote
-// before it; the other kernel's blocks, one item each, find theirs with a scan of their own
-// over the sequences (one pass of loads when B is at most the block's threads), and block 0
-// writes the plan for the merge.
+// before it.  The kernel for few rows cuts the work into equal runs instead, which every CTA
+// finds with a scan of its own over the sequences (one pass of loads when B is at most the block's
+// threads).
 #pragma once
 
 #include "skv_internal.h"
@@ -66,13 +66,20 @@ __device__ __forceinline__ ChunkTiles chunk_tiles(int window, int n_sink, int ca
   return t;
 }
 
-// Row tiles per KV head and KV tiles of the last row tile (an upper bound of the others').
+// Row tiles per KV head, and KV tiles of the row tile that has most: the last one; with a window, an
+// earlier one may touch a block more than the last, so there the bound is of their length alone.
 __device__ __forceinline__ void chunk_extent(const ChunkArgs& a, int n, int m, int* row_tiles, int* kv_tiles) {
   *row_tiles = static_cast<int>((static_cast<int64_t>(n) * a.group_rows + a.rows - 1) / a.rows);
   const int span = min(n, (a.rows + a.group_rows - 1) / a.group_rows + 1);
   const ChunkTiles t = chunk_tiles(a.window, a.n_sink, a.cap, m - span, m - 1);
+  int blocks = t.n;
+  if (a.window > 0 && *row_tiles > 1) {
+    const int64_t seen = static_cast<int64_t>(a.window) - 1 + span;  // tokens of a row tile's window
+    const int64_t most = (seen + 2 * kTileN - 2) / kTileN + (a.n_sink + static_cast<int64_t>(kTileN) - 1) / kTileN;
+    blocks = static_cast<int>(min(most, (static_cast<int64_t>(t.hi) + kTileN - 1) / kTileN));
+  }
   const int per = a.tile / kTileN;
-  *kv_tiles = max((t.n + per - 1) / per, 1);
+  *kv_tiles = max((blocks + per - 1) / per, 1);
 }
 
 // The plan in device memory: [kPlanItems] work items, [kPlanMerged] rows to merge, [kPlanNext] the
@@ -182,30 +189,6 @@ __device__ __forceinline__ ChunkItem chunk_item_of(const ChunkArgs& a, int b, in
   return it;
 }
 
-// The block's own work item by a scan of its own; false if there are fewer items than blocks.
-// Block 0 also writes the plan for the merge.  Every thread of the block calls it.
-template <int NT>
-__device__ __forceinline__ bool chunk_find_item(const ChunkArgs& a, ChunkItem* item) {
-  __shared__ int64_t sm_scan[2 * (NT / 32)];
-  __shared__ ChunkItem sm_item;
-  __shared__ int sm_found;
-  if (threadIdx.x == 0) sm_found = 0;
-  const bool writes = blockIdx.x == 0;
-  int64_t items, merged;
-  chunk_make_plan<NT>(a, sm_scan, &items, &merged, [&](int b, int first, int rt, int k, int part_row, int merge_row) {
-    const int r = static_cast<int>(blockIdx.x) - first;
-    if (r >= 0 && r < static_cast<int64_t>(rt) * a.Hkv * k) {
-      sm_item = chunk_item_of(a, b, r, rt, k, part_row);
-      sm_found = 1;
-    }
-    if (writes) chunk_write_plan(a, b, first, rt, k, part_row, merge_row);
-  });
-  if (writes && threadIdx.x == 0) a.plan[kPlanMerged] = static_cast<int>(merged);
-  __syncthreads();
-  *item = sm_item;
-  return sm_found != 0;
-}
-
 // Work item `idx` from the written plan (idx < its number of items).  Warp-collective: a
 // 32-way search for the last sequence whose first item is <= idx (sequences without items
 // share the first item of the one after them).
@@ -223,6 +206,124 @@ __device__ __forceinline__ ChunkItem chunk_item_at(const ChunkArgs& a, int idx) 
   }
   const int32_t* e = a.plan + kPlanHead + static_cast<int64_t>(kPlanRow) * lo;
   return chunk_item_of(a, lo, idx - __ldcg(e), __ldcg(e + 3), __ldcg(e + 4), __ldcg(e + 2));
+}
+
+// ---- equal runs (the kernel for few rows): all items' KV tiles in one line -- sequence after
+// sequence, in each the items (row tile, KV head), in each its tiles -- cut into n equal runs.
+
+// How U tiles are shared by n CTAs: the first r take q + 1, the others q.
+struct ChunkShare {
+  int64_t q;
+  int r, n;
+  __device__ __forceinline__ int64_t start(int c) const { return q * c + min(c, r); }
+  __device__ __forceinline__ int owner(int64_t u) const {
+    const int64_t head = (q + 1) * r;
+    return static_cast<int>(u < head ? u / (q + 1) : r + (u - head) / q);
+  }
+};
+
+// The part of one item that lies in a run.
+struct ChunkPiece {
+  int b, g, mt;
+  int row0, n, m;   // first packed row, new tokens, cached tokens with them
+  ChunkTiles tl;
+  int i0, n_tiles;  // its blocks in tl's run
+  int slot;         // the partial's number, two of each CTA; < 0: the whole item, final
+  __device__ __forceinline__ int token(int i) const {  // first token of tile i
+    const int x = i0 + i;
+    return (x < tl.n_first ? x : tl.win + (x - tl.n_first)) * kTileN;
+  }
+};
+
+// A CTA's run, piece by piece.
+struct ChunkRuns {
+  int64_t u, end;  // tiles left
+  int64_t first;   // first tile of sequence b
+  int cta, b, row0, n, m, rt, kt;
+  bool head;
+  __device__ __forceinline__ void load(const ChunkArgs& a) {
+    chunk_lengths(a, b, &row0, &n, &m);
+    chunk_extent(a, n, m, &rt, &kt);
+  }
+  // u's sequence, item and tile in it
+  __device__ __forceinline__ int64_t seek(const ChunkArgs& a, int* tile) {
+    while (u - first >= static_cast<int64_t>(rt) * a.Hkv * kt) {  // (u < end: there is such a sequence)
+      first += static_cast<int64_t>(rt) * a.Hkv * kt;
+      ++b;
+      load(a);
+    }
+    *tile = static_cast<int>((u - first) % kt);
+    return (u - first) / kt;
+  }
+  __device__ __forceinline__ bool next(const ChunkArgs& a, ChunkPiece* pc) {
+    if (u >= end) return false;
+    int s;
+    const int64_t item = seek(a, &s);
+    const int e = static_cast<int>(min(static_cast<int64_t>(kt), s + (end - u)));
+    pc->b = b, pc->row0 = row0, pc->n = n, pc->m = m;
+    pc->mt = rt - 1 - static_cast<int>(item / a.Hkv);
+    pc->g = static_cast<int>(item % a.Hkv);
+    const int m0 = pc->mt * a.rows, m_last = min(m0 + a.rows, n * a.group_rows) - 1;
+    pc->tl = chunk_tiles(a.window, a.n_sink, a.cap, m - n + m0 / a.group_rows, m - n + m_last / a.group_rows);
+    pc->i0 = min(s, pc->tl.n);
+    pc->n_tiles = min(e, pc->tl.n) - pc->i0;  // (an earlier row tile may see fewer than kt)
+    pc->slot = (s == 0 && e == kt) ? -1 : 2 * cta + (head ? 0 : 1);
+    head = false;
+    u += e - s;
+    return true;
+  }
+};
+
+// Run `cta` of at most n_cta; false if there is none.  Every thread of the block calls it.
+template <int NT>
+__device__ __forceinline__ bool chunk_find_runs(const ChunkArgs& a, int n_cta, int cta, ChunkRuns* runs,
+                                                ChunkShare* share = nullptr) {
+  __shared__ int64_t sm_scan[2 * (NT / 32)];
+  __shared__ int64_t sm_first;
+  __shared__ int sm_b;
+  const int tid = threadIdx.x;
+  int64_t w = 0, zero = 0, total, unused;
+  for (int b = tid; b < a.B; b += NT) {
+    int row0, n, m, rt, kt;
+    chunk_lengths(a, b, &row0, &n, &m);
+    chunk_extent(a, n, m, &rt, &kt);
+    w += static_cast<int64_t>(rt) * a.Hkv * kt;
+  }
+  chunk_block_scan<NT>(w, zero, &total, &unused, sm_scan);
+  ChunkShare sh;
+  sh.n = static_cast<int>(min(static_cast<int64_t>(n_cta), max(total / kChunkMinTiles, (int64_t)1)));
+  sh.q = total / sh.n;
+  sh.r = static_cast<int>(total % sh.n);
+  if (share) *share = sh;
+  if (cta >= sh.n || total == 0) return false;  // uniform in the block
+  const int64_t u = sh.start(cta);
+  int64_t before = 0;
+  for (int b0 = 0; b0 < a.B && before <= u; b0 += NT) {  // uniform in the block
+    const int b = b0 + tid;
+    int row0, n, m, rt = 0, kt = 1;
+    if (b < a.B) {
+      chunk_lengths(a, b, &row0, &n, &m);
+      chunk_extent(a, n, m, &rt, &kt);
+    }
+    const int64_t mine = static_cast<int64_t>(rt) * a.Hkv * kt;
+    int64_t x = mine, y = 0, tx, ty;
+    chunk_block_scan<NT>(x, y, &tx, &ty, sm_scan);
+    const int64_t first = before + x - mine;
+    if (b < a.B && u >= first && u < first + mine) {
+      sm_first = first;
+      sm_b = b;
+    }
+    before += tx;
+  }
+  __syncthreads();
+  runs->u = u;
+  runs->end = sh.start(cta + 1);
+  runs->first = sm_first;
+  runs->cta = cta;
+  runs->b = sm_b;
+  runs->head = true;
+  runs->load(a);
+  return true;
 }
 
 #endif  // __CUDACC__

@@ -40,7 +40,6 @@
 
 #include <type_traits>
 
-#include "chunk_plan.cuh"
 #include "skv_common.cuh"
 #include "skv_internal.h"
 
@@ -152,11 +151,10 @@ __device__ __forceinline__ int64_t ring_out_slot(const PartialParams& p) {
 }
 
 // PAGED: K/V live in pages with a block table; POS: the causal rule comes from position
-// arrays; RING: a pass-Q ring's work rows (never with PAGED or POS); CHUNK: ragged chunks of
-// new tokens (p.ck), with a window and sinks (only with PAGED).  Separate
+// arrays; RING: a pass-Q ring's work rows (never with PAGED or POS).  Separate
 // instantiations, so the plain kernels carry none of that code (a runtime test of the
 // first two cost the fp8 decode 4 %, of the third 1.3 %).
-template <class C, bool PAGED, bool POS, bool RING, bool CHUNK>
+template <class C, bool PAGED, bool POS, bool RING>
 __global__ void __launch_bounds__(C::THREADS, C::MINB)
     gqa_partial_kernel(const __grid_constant__ PartialParams p, const __grid_constant__ CUtensorMap tmk,
                        const __grid_constant__ CUtensorMap tmv) {
@@ -172,73 +170,37 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // ---- work item
-  int mt, c, j = 0, g, b;
-  ChunkItem ci{};  // CHUNK only
-  if constexpr (CHUNK) {
-    if (!chunk_find_item<C::THREADS>(p.ck, &ci)) return;
-    mt = ci.mt, c = ci.c, g = ci.g, b = ci.b;
-  } else {
-    int64_t item = blockIdx.x;
-    mt = static_cast<int>(item % p.m_tiles);
-    item /= p.m_tiles;
-    c = static_cast<int>(item % p.n_chunk);
-    item /= p.n_chunk;
-    j = static_cast<int>(item % p.n_split);
-    item /= p.n_split;
-    g = static_cast<int>(item % p.Hkv);
-    b = static_cast<int>(item / p.Hkv);
-  }
+  int64_t item = blockIdx.x;
+  const int mt = static_cast<int>(item % p.m_tiles);
+  item /= p.m_tiles;
+  const int c = static_cast<int>(item % p.n_chunk);
+  item /= p.n_chunk;
+  const int j = static_cast<int>(item % p.n_split);
+  item /= p.n_split;
+  const int g = static_cast<int>(item % p.Hkv);
+  const int b = static_cast<int>(item / p.Hkv);
 
   // bq: query row; bkv: KV row (sequence) of the cache
   int bq = b, bkv = b;
   if constexpr (RING) ring_rows(p, b, &bq, &bkv);
 
+  const int seq_len = p.seq_lens[bkv];
+  int lo, hi, win_lo, win_hi;
+  split_range(p, bkv, j, j + 1, seq_len, &lo, &hi);
+  chunk_window(p, lo, hi, c, &win_lo, &win_hi);
   static_assert(TN == kTileN, "chunks are cut in whole tiles");
-  int r_lo, r_hi, rows_total;
+  int r_lo = max(lo, win_lo);
+  int r_hi = min(hi, win_hi);
+  const int rows_total = p.Tq * p.G;
   const int m0 = mt * C::ROWS;
-  int64_t q_row0 = 0;        // packed row of the sequence's first query row (CHUNK)
-  int64_t causal_offset;     // position of query row 0
-  int tile_begin, n_tiles;
-  int n_first = 0, sinks = 0;  // CHUNK: the item's tiles that hold only sinks, sink tokens
-  if constexpr (CHUNK) {
-    // [r_lo, r_hi): the window's tokens; the item's tiles are i < n_first ? tile_0 + i :
-    // tile_begin + (i - n_first) (see ChunkTiles), cut into the chunk's run below
-    rows_total = ci.n * p.G;
-    q_row0 = ci.row0;
-    causal_offset = ci.m - ci.n;
-    const int m_last = min(m0 + C::ROWS, rows_total) - 1;
-    const ChunkTiles t = chunk_tiles(p.ck.window, p.ck.n_sink, p.ck.cap, ci.m - ci.n + m0 / p.G,
-                                     ci.m - ci.n + m_last / p.G);
-    const int ct = (t.n + ci.n_chunk - 1) / ci.n_chunk;
-    const int i0 = min(c * ct, t.n);
-    n_tiles = min(ct, t.n - i0);
-    r_lo = t.lo, r_hi = t.hi, sinks = t.sinks;
-    // tile i of the chunk is i < n_first ? i0 + i : tile_begin + i
-    n_first = max(t.n_first - i0, 0);
-    tile_begin = t.win + i0 - t.n_first;
-    c = i0;  // first tile of the sinks' run
-  } else {
-    const int seq_len = p.seq_lens[bkv];
-    int lo, hi, win_lo, win_hi;
-    split_range(p, bkv, j, j + 1, seq_len, &lo, &hi);
-    chunk_window(p, lo, hi, c, &win_lo, &win_hi);
-    r_lo = max(lo, win_lo);
-    r_hi = min(hi, win_hi);
-    rows_total = p.Tq * p.G;
-    causal_offset = p.causal_offset;
-    const int m_last = min(m0 + C::ROWS, rows_total) - 1;
+  const int m_last = min(m0 + C::ROWS, rows_total) - 1;
+  {
     // no row of this tile sees a token past causal_offset + (its query row)
     const int64_t horizon = p.causal_offset + m_last / p.G;
     if (horizon < static_cast<int64_t>(r_hi) - 1) r_hi = static_cast<int>(max(horizon + 1, (int64_t)r_lo));
-    tile_begin = r_lo / TN;
-    n_tiles = (r_hi > r_lo) ? ((r_hi + TN - 1) / TN - tile_begin) : 0;
   }
-  auto tile_token = [&](int i) -> int {  // first token of the item's tile i
-    if constexpr (CHUNK) {
-      if (i < n_first) return (c + i) * TN;
-    }
-    return (tile_begin + i) * TN;
-  };
+  const int tile_begin = r_lo / TN;
+  const int n_tiles = (r_hi > r_lo) ? ((r_hi + TN - 1) / TN - tile_begin) : 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NFULL; ++s) mbar_init(&full[s], 1);
@@ -255,7 +217,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
       const uint64_t pol = l2_policy_evict_first();
       // paged cache: the next tile's page is read one tile ahead, behind the stage wait
       int page_next = bkv;
-      if constexpr (PAGED) page_next = kv_page_of(p, bkv, tile_token(0));
+      if constexpr (PAGED) page_next = kv_page_of(p, bkv, tile_begin * TN);
       int issued = 0;
       for (int i = 0; i < n_tiles; ++i) {
         const int s = i % NSTAGE;
@@ -264,12 +226,12 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
         mbar_arrive_expect_tx(fb, C::STAGE_BYTES);
         uint8_t* ks = smem + s * C::STAGE_BYTES;
         uint8_t* vs = ks + C::TILE_BYTES;
-        const int tok = tile_token(i);
+        const int tok = (tile_begin + i) * TN;
         const int outer = page_next;  // page (paged) or sequence
         int row = tok;
         if constexpr (PAGED) {
           row = tok % p.block_len;
-          if (i + 1 < n_tiles) page_next = kv_page_of(p, bkv, tile_token(i + 1));
+          if (i + 1 < n_tiles) page_next = kv_page_of(p, bkv, tok + TN);
         }
 #pragma unroll
         for (int bx = 0; bx < C::NBOX; ++bx) {
@@ -294,17 +256,8 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
   const bool v0 = mrow0 < rows_total, v1 = mrow1 < rows_total;
   const int tq0 = v0 ? mrow0 / p.G : 0, tq1 = v1 ? mrow1 / p.G : 0;
   const int h0 = g * p.G + (v0 ? mrow0 % p.G : 0), h1 = g * p.G + (v1 ? mrow1 % p.G : 0);
-  const int64_t hz0 = causal_offset + tq0, hz1 = causal_offset + tq1;
-  const int64_t hz_min = causal_offset + (m0 + wm * 16) / p.G;
-  // CHUNK: first token of each row's window; the warp's last row has the highest
-  int wl0 = 0, wl1 = 0, wl_max = 0;
-  if constexpr (CHUNK) {
-    auto window_lo = [&](int64_t pos) -> int {
-      return p.ck.window > 0 && pos >= p.ck.window ? static_cast<int>(pos) - p.ck.window + 1 : 0;
-    };
-    wl0 = window_lo(hz0), wl1 = window_lo(hz1);
-    wl_max = window_lo(causal_offset + min(m0 + wm * 16 + 15, rows_total - 1) / p.G);
-  }
+  const int64_t hz0 = p.causal_offset + tq0, hz1 = p.causal_offset + tq1;
+  const int64_t hz_min = p.causal_offset + (m0 + wm * 16) / p.G;
   // tokens stored out of sequence order: visible iff k_pos[t] <= q_pos[row]
   const int32_t* kpos_b = POS ? p.k_pos + static_cast<int64_t>(bkv) * p.S_max : nullptr;
   const int qp0 = POS ? __ldg(p.q_pos + bq * p.Tq + tq0) : 0;
@@ -319,10 +272,8 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
   // has no register to spare for it).
   {
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q);
-    // (CHUNK: packed rows; b's stride then does not exist)
-    const int64_t qb = CHUNK ? q_row0 * p.q_st : bq * p.q_sb;
-    const __nv_bfloat16* q0 = q + qb + tq0 * p.q_st + h0 * p.q_sh;
-    const __nv_bfloat16* q1 = q + qb + tq1 * p.q_st + h1 * p.q_sh;
+    const __nv_bfloat16* q0 = q + bq * p.q_sb + tq0 * p.q_st + h0 * p.q_sh;
+    const __nv_bfloat16* q1 = q + bq * p.q_sb + tq1 * p.q_st + h1 * p.q_sh;
     float qsc = 1.f;  // 2^-qe
     if constexpr (C::FP8) {
       float amax = 0.f;
@@ -399,7 +350,7 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
 
   for (int i = wn; i < n_tiles; i += WN) {
     const int s = i % NSTAGE;
-    const int t0 = tile_token(i);
+    const int t0 = (tile_begin + i) * TN;
     float ksc = 1.f, vsc = 1.f;
     if constexpr (C::FP8) {
       if constexpr (!PAGED) {
@@ -475,13 +426,8 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
     // ---- scale, mask, online softmax (fp8: the q scaling undone here)
     float sl = p.scale_log2;
     if constexpr (C::FP8) sl = *reinterpret_cast<volatile const float*>(qscale + wm) * ksc;
-    // CHUNK: every token of a step below the sinks' end is seen too
-    const bool in_range = ((t0s >= r_lo) && (t0s + NS <= r_hi)) || (CHUNK && t0s + NS <= sinks);
-    bool need_mask = POS || !in_range || (static_cast<int64_t>(t0s) + NS - 1 > hz_min);
-    if constexpr (CHUNK) need_mask = need_mask || (t0s < wl_max && t0s + NS > sinks);
-    auto in_item = [&](int tok) -> bool {  // a token that some row of the item sees
-      return (tok >= r_lo && tok < r_hi) || (CHUNK && tok < sinks);
-    };
+    const bool in_range = (t0s >= r_lo) && (t0s + NS <= r_hi);
+    const bool need_mask = POS || !in_range || (static_cast<int64_t>(t0s) + NS - 1 > hz_min);
     float tmax[2] = {-INFINITY, -INFINITY};
     // fp8: one instantiation per mask mode (need_mask is warp-uniform; written as one loop
     // with the test inside, the compiler evaluated it on every tile, and the fp8 decode does
@@ -497,8 +443,6 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
             const int tok = t0s + 8 * nt + 2 * tq + (e & 1);
             const int64_t hz = (e < 2) ? hz0 : hz1;
             bool ok = tok >= r_lo && tok < r_hi && static_cast<int64_t>(tok) <= hz;
-            if constexpr (CHUNK)
-              ok = tok < r_hi && static_cast<int64_t>(tok) <= hz && (tok >= ((e < 2) ? wl0 : wl1) || tok < sinks);
             if constexpr (POS) ok = ok && __ldg(kpos_b + tok) <= ((e < 2) ? qp0 : qp1);
             x = ok ? x : -INFINITY;
           }
@@ -577,8 +521,8 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
         uint32_t mlo = 0xFFFFFFFFu, mhi = 0xFFFFFFFFu;
         if constexpr (decltype(vmasked)::value) {
           const int ta = t0s + 16 * kk + 2 * tq, tb2 = ta + 8;
-          mlo = half_mask(in_item(ta), in_item(ta + 1));
-          mhi = half_mask(in_item(tb2), in_item(tb2 + 1));
+          mlo = half_mask(ta >= r_lo && ta < r_hi, ta + 1 >= r_lo && ta + 1 < r_hi);
+          mhi = half_mask(tb2 >= r_lo && tb2 < r_hi, tb2 + 1 >= r_lo && tb2 + 1 < r_hi);
         }
 #pragma unroll
         for (int dp = 0; dp < D / 16; ++dp) {
@@ -601,8 +545,8 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
         uint32_t m0 = 0xFFFFFFFFu, m1 = 0xFFFFFFFFu;
         if constexpr (decltype(vmasked)::value) {
           const int ta = t0s + 16 * kk + 2 * tq, tb2 = ta + 8;
-          m0 = half_mask(in_item(ta), in_item(ta + 1));
-          m1 = half_mask(in_item(tb2), in_item(tb2 + 1));
+          m0 = half_mask(ta >= r_lo && ta < r_hi, ta + 1 >= r_lo && ta + 1 < r_hi);
+          m1 = half_mask(tb2 >= r_lo && tb2 < r_hi, tb2 + 1 >= r_lo && tb2 + 1 < r_hi);
         }
         const uint32_t b00 = pa[kk][0], b01 = pa[kk][2], b10 = pa[kk][1], b11 = pa[kk][3];
 #pragma unroll
@@ -638,44 +582,26 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
     lrun[r] += __shfl_xor_sync(0xffffffffu, lrun[r], 2);
   }
   constexpr float kLn2 = 0.6931471805599453f;
-  int64_t oslot = 0;
+  int64_t oslot;
   if constexpr (RING)
     oslot = ring_out_slot(p);
-  else if constexpr (!CHUNK)
+  else
     oslot = static_cast<int64_t>(j * p.n_chunk + c) * p.B + b;
-  const bool direct = CHUNK && ci.n_chunk == 1;  // the final rows, in bf16
-  float* const lse_out = direct ? p.ck.lse : p.out_lse;
-  const bool zero_empty = direct || (!CHUNK && p.zero_empty);
-  // a row that summed something; CHUNK: a NaN sum counts, so that NaN scores give a NaN row
-  auto some = [](float l) -> bool { return CHUNK ? l != 0.f : l > 0.f; };
-  auto row_out = [&](int t_q, int h) -> int64_t {
-    if constexpr (CHUNK)
-      return direct ? (q_row0 + t_q) * p.Hq + h
-                    : ci.part_row + (static_cast<int64_t>(ci.c) * ci.n + t_q) * p.Hq + h;
-    return (oslot * p.Tq + t_q) * p.Hq + h;
-  };
-  auto store2 = [&](int64_t row, int d, float x, float y) {  // two columns of output row `row`
-    if constexpr (CHUNK) {
-      if (direct) {
-        *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.ck.out) + row * D + d) = pack_bf16(x, y);
-        return;
-      }
-    }
-    *reinterpret_cast<float2*>(p.out_o + row * D + d) = make_float2(x, y);
-  };
+  auto row_out = [&](int t_q, int h) -> int64_t { return (oslot * p.Tq + t_q) * p.Hq + h; };
 
   if constexpr (WN == 1) {
-    const float inv0 = some(lrun[0]) ? 1.f / lrun[0] : 0.f;
-    const float inv1 = some(lrun[1]) ? 1.f / lrun[1] : 0.f;
-    const bool w0 = v0 && (some(lrun[0]) || zero_empty);
-    const bool w1 = v1 && (some(lrun[1]) || zero_empty);
+    const float inv0 = lrun[0] > 0.f ? 1.f / lrun[0] : 0.f;
+    const float inv1 = lrun[1] > 0.f ? 1.f / lrun[1] : 0.f;
+    const bool w0 = v0 && (lrun[0] > 0.f || p.zero_empty);
+    const bool w1 = v1 && (lrun[1] > 0.f || p.zero_empty);
     if constexpr (!C::FP8) {
-      const int64_t o0 = row_out(tq0, h0), o1 = row_out(tq1, h1);
+      float* o0 = p.out_o + row_out(tq0, h0) * D;
+      float* o1 = p.out_o + row_out(tq1, h1) * D;
 #pragma unroll
       for (int nt = 0; nt < D / 8; ++nt) {
         const int d = 8 * nt + 2 * tq;
-        if (w0) store2(o0, d, o[nt][0] * inv0, o[nt][1] * inv0);
-        if (w1) store2(o1, d, o[nt][2] * inv1, o[nt][3] * inv1);
+        if (w0) *reinterpret_cast<float2*>(o0 + d) = make_float2(o[nt][0] * inv0, o[nt][1] * inv0);
+        if (w1) *reinterpret_cast<float2*>(o1 + d) = make_float2(o[nt][2] * inv1, o[nt][3] * inv1);
       }
     } else {
       // O^T: this thread holds rows (8n + 2tq + {0,1}) at dv 16c + 2gq + {0,1}
@@ -688,18 +614,18 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
           const bool wr = __shfl_sync(0xffffffffu, (n ? w1 : w0) ? 1 : 0, src) != 0;
           const int tq_r = __shfl_sync(0xffffffffu, n ? tq1 : tq0, src);
           const int h_r = __shfl_sync(0xffffffffu, n ? h1 : h0, src);
-          const int64_t orow = row_out(tq_r, h_r);
+          float* orow = p.out_o + row_out(tq_r, h_r) * D;
 #pragma unroll
           for (int c = 0; c < D / 16; ++c) {
             const float* ov = o[2 * c + n];
-            if (wr) store2(orow, 16 * c + 2 * gq, ov[e] * inv, ov[2 + e] * inv);
+            if (wr) *reinterpret_cast<float2*>(orow + 16 * c + 2 * gq) = make_float2(ov[e] * inv, ov[2 + e] * inv);
           }
         }
       }
     }
     if (tq == 0) {
-      if (v0) lse_out[row_out(tq0, h0)] = some(lrun[0]) ? (mrun[0] + __log2f(lrun[0])) * kLn2 : -INFINITY;
-      if (v1) lse_out[row_out(tq1, h1)] = some(lrun[1]) ? (mrun[1] + __log2f(lrun[1])) * kLn2 : -INFINITY;
+      if (v0) p.out_lse[row_out(tq0, h0)] = lrun[0] > 0.f ? (mrun[0] + __log2f(lrun[0])) * kLn2 : -INFINITY;
+      if (v1) p.out_lse[row_out(tq1, h1)] = lrun[1] > 0.f ? (mrun[1] + __log2f(lrun[1])) * kLn2 : -INFINITY;
     }
   } else {
     constexpr int NCT = C::NCW * 32;
@@ -723,11 +649,8 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
       if (M != -INFINITY) {
 #pragma unroll
         for (int w = 0; w < WN; ++w) L += ml[(w * C::ROWS + lr) * 2 + 1] * fast_exp2(ml[(w * C::ROWS + lr) * 2] - M);
-      } else if constexpr (CHUNK) {
-#pragma unroll
-        for (int w = 0; w < WN; ++w) L += ml[(w * C::ROWS + lr) * 2 + 1];  // 0, or NaN
       }
-      f[r] = some(L) ? fast_exp2(mrun[r] - M) / L : 0.f;
+      f[r] = (L > 0.f) ? fast_exp2(mrun[r] - M) / L : 0.f;
     }
     float* obuf = reinterpret_cast<float*>(smem);  // [WN][ROWS][D]
     if constexpr (!C::FP8) {
@@ -768,13 +691,10 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
       if (M != -INFINITY) {
 #pragma unroll
         for (int w = 0; w < WN; ++w) L += ml[(w * C::ROWS + lr) * 2 + 1] * fast_exp2(ml[(w * C::ROWS + lr) * 2] - M);
-      } else if constexpr (CHUNK) {
-#pragma unroll
-        for (int w = 0; w < WN; ++w) L += ml[(w * C::ROWS + lr) * 2 + 1];  // 0, or NaN
       }
       const int t_q = m / p.G, h = g * p.G + m % p.G;
       const int64_t ro = row_out(t_q, h);
-      if (some(L) || zero_empty) {
+      if (L > 0.f || p.zero_empty) {
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < WN; ++w) {
@@ -784,13 +704,9 @@ __global__ void __launch_bounds__(C::THREADS, C::MINB)
           acc.z += x.z;
           acc.w += x.w;
         }
-        if (direct)
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.ck.out) + ro * D + d) =
-              make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
-        else
-          *reinterpret_cast<float4*>(p.out_o + ro * D + d) = acc;
+        *reinterpret_cast<float4*>(p.out_o + ro * D + d) = acc;
       }
-      if (d == 0) lse_out[ro] = some(L) ? (M + __log2f(L)) * kLn2 : -INFINITY;
+      if (d == 0) p.out_lse[ro] = (L > 0.f) ? (M + __log2f(L)) * kLn2 : -INFINITY;
     }
   }
 }
@@ -812,11 +728,11 @@ cudaError_t launch_cfg(const PartialParams& p, const CUtensorMap& tmk, const CUt
                        cudaStream_t stream) {
   static std::atomic<uint64_t> attr_done{0};  // per variant, per device
   cudaError_t e0 = once_per_device(attr_done, [] {
-    const void* fns[5] = {reinterpret_cast<const void*>(gqa_partial_kernel<C, false, false, false, false>),
-                          reinterpret_cast<const void*>(gqa_partial_kernel<C, true, false, false, false>),
-                          reinterpret_cast<const void*>(gqa_partial_kernel<C, false, true, false, false>),
-                          reinterpret_cast<const void*>(gqa_partial_kernel<C, true, true, false, false>),
-                          reinterpret_cast<const void*>(gqa_partial_kernel<C, false, false, true, false>)};
+    const void* fns[5] = {reinterpret_cast<const void*>(gqa_partial_kernel<C, false, false, false>),
+                          reinterpret_cast<const void*>(gqa_partial_kernel<C, true, false, false>),
+                          reinterpret_cast<const void*>(gqa_partial_kernel<C, false, true, false>),
+                          reinterpret_cast<const void*>(gqa_partial_kernel<C, true, true, false>),
+                          reinterpret_cast<const void*>(gqa_partial_kernel<C, false, false, true>)};
     for (const void* f : fns) {
       cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
       if (e != cudaSuccess) return e;
@@ -828,31 +744,16 @@ cudaError_t launch_cfg(const PartialParams& p, const CUtensorMap& tmk, const CUt
   const unsigned int grid = static_cast<unsigned int>(n_items);
   if (p.ring_n > 0) {
     if (p.block_table || p.k_pos) return cudaErrorInvalidValue;  // no such instantiation
-    gqa_partial_kernel<C, false, false, true, false><<<grid, C::THREADS, C::SMEM, stream>>>(p, tmk, tmv);
+    gqa_partial_kernel<C, false, false, true><<<grid, C::THREADS, C::SMEM, stream>>>(p, tmk, tmv);
   } else if (p.block_table && p.k_pos) {
-    gqa_partial_kernel<C, true, true, false, false><<<grid, C::THREADS, C::SMEM, stream>>>(p, tmk, tmv);
+    gqa_partial_kernel<C, true, true, false><<<grid, C::THREADS, C::SMEM, stream>>>(p, tmk, tmv);
   } else if (p.block_table) {
-    gqa_partial_kernel<C, true, false, false, false><<<grid, C::THREADS, C::SMEM, stream>>>(p, tmk, tmv);
+    gqa_partial_kernel<C, true, false, false><<<grid, C::THREADS, C::SMEM, stream>>>(p, tmk, tmv);
   } else if (p.k_pos) {
-    gqa_partial_kernel<C, false, true, false, false><<<grid, C::THREADS, C::SMEM, stream>>>(p, tmk, tmv);
+    gqa_partial_kernel<C, false, true, false><<<grid, C::THREADS, C::SMEM, stream>>>(p, tmk, tmv);
   } else {
-    gqa_partial_kernel<C, false, false, false, false><<<grid, C::THREADS, C::SMEM, stream>>>(p, tmk, tmv);
+    gqa_partial_kernel<C, false, false, false><<<grid, C::THREADS, C::SMEM, stream>>>(p, tmk, tmv);
   }
-  return cudaGetLastError();
-}
-
-template <class C>
-cudaError_t launch_chunk_cfg(const PartialParams& p, const CUtensorMap& tmk, const CUtensorMap& tmv, int64_t n_items,
-                             cudaStream_t stream) {
-  static std::atomic<uint64_t> attr_done{0};  // per variant, per device
-  cudaError_t e0 = once_per_device(attr_done, [] {
-    return cudaFuncSetAttribute(gqa_partial_kernel<C, true, false, false, true>,
-                                cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-  });
-  if (e0 != cudaSuccess) return e0;
-  if (n_items <= 0) return cudaSuccess;
-  gqa_partial_kernel<C, true, false, false, true>
-      <<<static_cast<unsigned int>(n_items), C::THREADS, C::SMEM, stream>>>(p, tmk, tmv);
   return cudaGetLastError();
 }
 
@@ -879,19 +780,6 @@ cudaError_t launch_gqa_partial(GqaVariant v, const PartialParams& p, const CUten
     case GqaVariant::kBf16D64Prefill: return launch_cfg<CfgBf16D64Pre>(p, tmk, tmv, n_items, stream);
     case GqaVariant::kBf16D128Prefill: return launch_cfg<CfgBf16D128Pre>(p, tmk, tmv, n_items, stream);
     case GqaVariant::kFp8D128Prefill: return launch_cfg<CfgFp8D128Pre>(p, tmk, tmv, n_items, stream);
-  }
-  return cudaErrorInvalidValue;
-}
-
-cudaError_t launch_gqa_chunk(GqaVariant v, const PartialParams& p, const CUtensorMap& tmk, const CUtensorMap& tmv,
-                             int64_t n_items, cudaStream_t stream) {
-  switch (v) {
-    case GqaVariant::kBf16D64Decode: return launch_chunk_cfg<CfgBf16D64Dec>(p, tmk, tmv, n_items, stream);
-    case GqaVariant::kBf16D128Decode: return launch_chunk_cfg<CfgBf16D128Dec>(p, tmk, tmv, n_items, stream);
-    case GqaVariant::kFp8D128Decode: return launch_chunk_cfg<CfgFp8D128Dec>(p, tmk, tmv, n_items, stream);
-    case GqaVariant::kBf16D64Prefill: return launch_chunk_cfg<CfgBf16D64Pre>(p, tmk, tmv, n_items, stream);
-    case GqaVariant::kBf16D128Prefill: return launch_chunk_cfg<CfgBf16D128Pre>(p, tmk, tmv, n_items, stream);
-    case GqaVariant::kFp8D128Prefill: return launch_chunk_cfg<CfgFp8D128Pre>(p, tmk, tmv, n_items, stream);
   }
   return cudaErrorInvalidValue;
 }

@@ -40,7 +40,7 @@ struct ChunkArgs {
   int32_t group_rows;  // rows of one token: G, or G padded to a power of two
   int32_t rows;     // rows (token, head of the group) of one row tile
   int32_t tile;     // tokens of one KV tile
-  int32_t n_wave;   // work items resident at once
+  int32_t n_wave;   // CTAs resident at once
   int32_t n_target; // most work items with several chunks per row tile
   int32_t* plan;    // device [kPlanHead + kPlanRow B] (chunk_plan.cuh)
   void* out;        // bf16 [T][Hq][d]
@@ -50,6 +50,8 @@ struct ChunkArgs {
 enum ChunkPlanWord : int { kPlanItems = 0, kPlanMerged = 1, kPlanNext = 2, kPlanHead = 4, kPlanRow = 5 };
 // At most so many KV tiles for each resident work item are dealt out as a single wave.
 constexpr int kChunkShortTiles = 8;
+// A run of the kernel for few rows has at least so many KV tiles.
+constexpr int kChunkMinTiles = 2;
 
 // Parameters of one split-KV partial-attention launch.
 //
@@ -148,10 +150,16 @@ GqaLaunchInfo gqa_launch_info(GqaVariant v);
 
 cudaError_t launch_gqa_partial(GqaVariant v, const PartialParams& p, const CUtensorMap& tmk,
                                const CUtensorMap& tmv, int64_t n_items, cudaStream_t stream);
-// The same tiles over ragged chunks (p.ck): items with one chunk write p.ck.out / p.ck.lse,
-// the others partial rows to p.out_o / p.out_lse, which launch_chunk_merge joins.
-cudaError_t launch_gqa_chunk(GqaVariant v, const PartialParams& p, const CUtensorMap& tmk, const CUtensorMap& tmv,
-                             int64_t n_items, cudaStream_t stream);
+// Ragged chunks of new tokens (p.ck): items in one piece write p.ck.out / p.ck.lse, the others
+// partial rows to p.out_o / p.out_lse, which the merge of the kernel joins.
+// Few rows (see chunk_rows.cu): n_wave CTAs, two partials of chunk_rows_per_tile() rows each;
+// tmk / tmv: pages with kTileN rows a box.
+int chunk_rows_per_tile();
+int chunk_rows_ctas_per_sm();
+cudaError_t launch_chunk_rows(const PartialParams& p, int32_t d, bool fp8, const CUtensorMap& tmk, const CUtensorMap& tmv,
+                              cudaStream_t stream);
+cudaError_t launch_chunk_runs_merge(const ChunkArgs& a, int32_t d, const float* part_o, const float* part_lse,
+                                    cudaStream_t stream);
 // On the tensor cores (see chunk_tc.cu), any G <= 128; tmq: q as (dim, head, packed
 // row) with 64 x group_rows x 128 / group_rows boxes, tmk / tmv: pages with chunk_tc_kv_box()
 // rows a box.

@@ -210,8 +210,10 @@ def test_the_kernel_choice_does_not_change_the_result():
             for longest in (1, 3, None):
                 check(c, max_q_len=longest)
             # a bound that is too small is only a worse choice
-            c = R.make_case([1, 60, 1], [900, 64, 333], 2 * G, 2, d, fp8=kind == "fp8", seed=15, device=DEV)
+            c = R.make_case([1, 60, 1, 90], [900, 64, 333, 700], 2 * G, 2, d, fp8=kind == "fp8", seed=15, device=DEV)
             check(c, max_q_len=1)
+            for window, n_sink in ((1, 0), (63, 2), (70, 65), (129, 0), (500, 130)):
+                check(c, window, n_sink, max_q_len=1)
 
 
 @pytest.mark.parametrize("kind,d", TYPES)
@@ -375,3 +377,23 @@ def test_scales_of_blocks_that_nobody_sees():
         for longest in (1, None):
             out, lse = run(x, window, n_sink, max_q_len=longest)
             R.check_attention(c, out, lse, window, n_sink)
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e-6, 1e4, 1e30])
+@pytest.mark.parametrize("longest", [1, None])
+def test_fp8_scales_of_any_size(longest, size):
+    """Tiny and huge V scales, and blocks that differ by many powers of ten: the weights keep
+    their bits."""
+    c = R.make_case([1, 5], [700, 300], 8, 2, 128, fp8=True, seed=25, device=DEV)
+    c["v_scale"] *= size
+    for spread in (False, True):
+        if spread:
+            g = torch.Generator().manual_seed(2)
+            c["v_scale"] *= 10.0 ** torch.randint(-6, 1, c["v_scale"].shape, generator=g).to(DEV)
+        out, lse = run(c, max_q_len=longest)
+        ro, rl, total = R.attend(c)
+        out = out.cpu().double()
+        big = total > 1e-36  # (bf16 and fp32 sums end at 2^-126)
+        tol = 2.0 ** -8 * (total + ro.abs()) + 2.0 ** -12 * total
+        assert ((out - ro).abs() <= tol)[big].all() and torch.isfinite(out).all()
+        assert (lse.cpu().double() - rl).abs().max() <= 2.5e-4
