@@ -701,8 +701,14 @@ def attn_chunk_paged(q, k_pages, v_pages, seq_lens, cu_q, block_table, max_q_len
                      1.0 / math.sqrt(hd) if softmax_scale is None else softmax_scale, kv, scale_block,
                      q.stride()[:2], k_pages.stride()[:3], v_pages.stride()[:3])
     dev = q.device
-    out = _out(out, (T, Hq, hd), torch.bfloat16, dev, "out")
-    lse = _out(lse, (T, Hq), torch.float32, dev, "lse")
+    if out is None:
+        out = torch.empty((T, Hq, hd), dtype=torch.bfloat16, device=dev)
+    else:
+        _out(out, (T, Hq, hd), torch.bfloat16, dev, "out")
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    else:
+        _out(lse, (T, Hq), torch.float32, dev, "lse")
     n = ctypes.c_size_t(0)
     _check(_lib.attn_chunk_paged_workspace_size(d, pg, n))
     if workspace is None:

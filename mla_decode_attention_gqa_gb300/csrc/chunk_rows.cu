@@ -51,7 +51,8 @@ struct RowsCfg {
   static constexpr int OFF_ML = OFF_O + kRows * D * 4;         // (m, l) of each warp's rows
   static constexpr int OFF_QF = OFF_ML + WN * kRows * 2 * 4;   // fp8: q fragments
   static constexpr int OFF_BAR = OFF_QF + (FP8 ? (D / 16) * 32 * 16 : 0);
-  static constexpr int SMEM = 1024 + OFF_BAR + 256;
+  static constexpr int OFF_RUN = OFF_BAR + 256;                // each consumer warp's run and piece
+  static constexpr int SMEM = 1024 + OFF_RUN + WN * 192;
   static_assert((NFULL + NSTAGE) * 8 + 8 <= 256, "barriers and the q scale");
   static_assert(2 * (SMEM + 1536) <= 227 * 1024, "two CTAs an SM");
 };
@@ -136,23 +137,32 @@ __global__ void __launch_bounds__(C::THREADS, 2)
   const int gq = lane >> 2, tq = lane & 3;
   float* ml = reinterpret_cast<float*>(smem + C::OFF_ML);
   uint4* qfrag = reinterpret_cast<uint4*>(smem + C::OFF_QF);
+  // the run and its piece wait in shared memory: the registers are full of scores and O
+  static_assert(sizeof(ChunkRuns) <= 64 && sizeof(ChunkPiece) <= 128, "a warp's place");
+  ChunkRuns* run = reinterpret_cast<ChunkRuns*>(smem + C::OFF_RUN + warp * 192);
+  ChunkPiece& pc = *reinterpret_cast<ChunkPiece*>(smem + C::OFF_RUN + warp * 192 + 64);
+  if (lane == 0) *run = runs;
+  auto next_piece = [&]() -> bool {
+    __syncwarp();  // the piece's readers are done
+    bool more = false;
+    if (lane == 0) more = run->next(p.ck, &pc);
+    more = __any_sync(0xffffffffu, more);
+    __syncwarp();  // lane 0's stores
+    return more;
+  };
   int x0 = 0;  // tiles of the pieces before
-  ChunkPiece pc;
-  while (runs.next(p.ck, &pc)) {
+  while (next_piece()) {
     const int rows_total = pc.n * p.G;
     const int mrow0 = pc.mt * kRows + gq, mrow1 = mrow0 + 8;
     const bool v0 = mrow0 < rows_total, v1 = mrow1 < rows_total;
     const int tq0 = v0 ? mrow0 / p.G : 0, tq1 = v1 ? mrow1 / p.G : 0;
     const int h0 = pc.g * p.G + (v0 ? mrow0 % p.G : 0), h1 = pc.g * p.G + (v1 ? mrow1 % p.G : 0);
     // visible tokens of a row: [wl, hz] and below the sinks' end; all below the item's end
-    const int64_t pos0 = static_cast<int64_t>(pc.m) - pc.n;
-    const int64_t hz0 = pos0 + tq0, hz1 = pos0 + tq1, hz_min = pos0 + pc.mt * kRows / p.G;
-    auto window_lo = [&](int64_t pos) -> int {
-      return p.ck.window > 0 && pos >= p.ck.window ? static_cast<int>(pos) - p.ck.window + 1 : 0;
-    };
+    const int pos0 = pc.m - pc.n;
+    const int hz0 = pos0 + tq0, hz1 = pos0 + tq1, hz_min = pos0 + pc.mt * kRows / p.G;
+    auto window_lo = [&](int pos) -> int { return p.ck.window > 0 && pos >= p.ck.window ? pos - p.ck.window + 1 : 0; };
     const int wl0 = window_lo(hz0), wl1 = window_lo(hz1);
     const int wl_max = window_lo(pos0 + min(pc.mt * kRows + kRows - 1, rows_total - 1) / p.G);
-    const int r_lo = pc.tl.lo, r_hi = pc.tl.hi, sinks = pc.tl.sinks;
 
     // ---- Q fragments (A operand, 16 rows x D): registers for bf16, shared memory for fp8
     uint32_t qa[C::FP8 ? 1 : D / 16][4];
@@ -282,9 +292,9 @@ __global__ void __launch_bounds__(C::THREADS, 2)
       float sl = p.scale_log2;
       if constexpr (C::FP8) sl = *reinterpret_cast<volatile const float*>(q_scale) * ksc;
       // tokens of this tile that some row of the item sees / that every row of it sees
+      const int r_lo = pc.tl.lo, r_hi = pc.tl.hi, sinks = pc.tl.sinks;
       const bool in_range = (t0 >= r_lo && t0 + TN <= r_hi) || t0 + TN <= sinks;
-      const bool need_mask =
-          !in_range || static_cast<int64_t>(t0) + TN - 1 > hz_min || (t0 < wl_max && t0 + TN > sinks);
+      const bool need_mask = !in_range || t0 + TN - 1 > hz_min || (t0 < wl_max && t0 + TN > sinks);
       auto in_item = [&](int tok) -> bool { return (tok >= r_lo && tok < r_hi) || tok < sinks; };
       float tmax[2] = {-INFINITY, -INFINITY};
       // an instantiation per mask mode: most tiles carry no test
@@ -296,7 +306,7 @@ __global__ void __launch_bounds__(C::THREADS, 2)
             float y = sc[nt][e] * sl;
             if constexpr (decltype(masked)::value) {
               const int tok = t0 + 8 * nt + 2 * tq + (e & 1);
-              const bool seen = tok < r_hi && static_cast<int64_t>(tok) <= ((e < 2) ? hz0 : hz1) &&
+              const bool seen = tok < r_hi && tok <= ((e < 2) ? hz0 : hz1) &&
                                 (tok >= ((e < 2) ? wl0 : wl1) || tok < sinks);
               y = seen ? y : -INFINITY;
             }
@@ -536,7 +546,7 @@ __global__ void __launch_bounds__(C::THREADS, 2)
 
 using CfgBf16D64 = RowsCfg<false, 64, 4, 6>;
 using CfgBf16D128 = RowsCfg<false, 128, 3, 3>;
-using CfgFp8D128 = RowsCfg<true, 128, 4, 5>;
+using CfgFp8D128 = RowsCfg<true, 128, 4, 6>;
 
 template <class C>
 cudaError_t launch_cfg(const PartialParams& p, const CUtensorMap& tmk, const CUtensorMap& tmv, cudaStream_t stream) {
