@@ -9,12 +9,14 @@
 //   likewise without norm and rotation.  Everything between the loads and the one rounding at
 //   the store is in fp32.
 //
-// Bound by HBM (each input is read once and each output written once), and closely behind it by
-// the instructions: 8 lanes hold one head, as two chunks of d / 16 values that the rotation
-// pairs, so that it needs no exchange between lanes, the sum of squares is three shuffles for four
-// heads, and the arithmetic runs on packed pairs.  A block takes a run of (token, head) pairs: the
-// chains token -> sequence -> position -> page and table row of its tokens run side by side under
-// the first loads, and every group keeps kAhead heads' loads in flight.
+// Bound by HBM: each input is read once and each output written once.  A warp copies the heads by
+// bulk copies into a ring, 32 heads a stage, so that 40 KB a CTA are on their way whatever the
+// others wait for (heads loaded to registers ahead of their use: 68 us for 4096 tokens of
+// 128 + 16 heads, this way 58: 5.2 TB/s of the 6.8 that a copy reaches).  8 lanes take one head, as two chunks of d / 16 values
+// that the rotation pairs, so that it needs no exchange between lanes, the sum of squares is
+// three shuffles for four heads, and the arithmetic runs on packed pairs.  The chains token ->
+// sequence -> position -> page and table row of a CTA's tokens run side by side under the first
+// copies.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -26,11 +28,12 @@ namespace skv {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kGroups = kThreads / 8;  // heads a block works on at once
-constexpr int kAhead = 3;              // heads in flight in a group (4 spill: 72 -> 82 us for 4096 x 144 heads)
-constexpr int kMaxSteps = 16;          // heads that a group works off in turn (8: 73, 16: 68, 64: 74 us)
-constexpr int kMaxTokens = 64;         // tokens a block's run may touch
+constexpr int kWarps = 8;              // consumer warps
+constexpr int kThreads = kWarps * 32 + 32;
+constexpr int kGroups = kWarps * 4;    // heads of a stage
+constexpr int kStages = 5;               // 40 KB (static shared memory ends at 48)
+constexpr int kCtas = 2 * 152;         // CTAs of a large call: two an SM
+constexpr int kMaxTokens = 64;         // tokens a CTA's run may touch
 
 // ---- two fp32 values in one 64-bit register (packed round-to-nearest operations)
 __device__ __forceinline__ uint64_t pack2(float x, float y) {
@@ -55,6 +58,14 @@ __device__ __forceinline__ uint64_t swap2(uint64_t v) {
   float x, y;
   unpack2(v, x, y);
   return pack2(y, x);
+}
+
+// Untiled bulk copy (16-byte aligned addresses, a multiple of 16 bytes) completing on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
 
 // H bf16 values as packed words.
@@ -151,14 +162,63 @@ struct Place {
 template <int D, bool FP8, bool INTER>
 __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int H = D / 16;  // values of a chunk
+  constexpr uint32_t kRowBytes = D * 2;
+  __shared__ __align__(128) uint8_t ring[kStages][kGroups * kRowBytes];
+  __shared__ uint64_t full[kStages], empty[kStages];
   __shared__ Place places[kMaxTokens];
-  const int warp = threadIdx.x >> 5, l8 = threadIdx.x & 7;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l8 = threadIdx.x & 7;
   const int n_heads = a.Hq + 2 * a.Hkv;  // queries, keys, values
-  const uint32_t pair0 = blockIdx.x * static_cast<uint32_t>(a.steps * kGroups);
-  const int t0 = static_cast<int>(pair0 / n_heads);  // first token of the block's run
+  // this CTA's run of (token, head) pairs
   const uint32_t n_pairs = static_cast<uint32_t>(a.T) * n_heads;
-  const uint32_t last = min(pair0 + static_cast<uint32_t>(a.steps * kGroups), n_pairs) - 1;
-  const int tokens = static_cast<int>(last / n_heads) - t0 + 1;
+  const uint32_t pair0 = blockIdx.x * static_cast<uint32_t>(a.steps * kGroups);
+  const uint32_t pair1 = min(pair0 + static_cast<uint32_t>(a.steps * kGroups), n_pairs);
+  const int steps = static_cast<int>((pair1 - pair0 + kGroups - 1) / kGroups);
+  const int t0 = static_cast<int>(pair0 / n_heads);  // first token of the run
+  const int tokens = static_cast<int>((pair1 - 1) / n_heads) - t0 + 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], kWarps);
+    }
+    fence_mbar_init();
+  }
+  __syncthreads();
+
+  // (token, head) of this lane's (producer) or group's (consumer) pair; a stage on: kGroups pairs
+  int t = 0, h = static_cast<int>(pair0 - static_cast<uint32_t>(t0) * n_heads) + (warp == kWarps ? lane : threadIdx.x >> 3);
+  while (h >= n_heads) h -= n_heads, ++t;
+  auto advance = [&]() {
+    h += kGroups;
+    while (h >= n_heads) h -= n_heads, ++t;
+  };
+
+  if (warp == kWarps) {
+    // ------------------------------------------------------------ the copies
+    int done = 0;
+    for (int n = 0; n < steps; ++n, advance()) {
+      const int s = n % kStages;
+      const int valid = static_cast<int>(min(pair1 - pair0 - static_cast<uint32_t>(n * kGroups), static_cast<uint32_t>(kGroups)));
+      if (n >= kStages && !__all_sync(0xffffffffu, mbar_wait(&empty[s], ((n / kStages) - 1) & 1, a.err, kDevErrEmptyWait))) break;
+      if (lane == 0) mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(valid) * kRowBytes);
+      __syncwarp();
+      // a copy for each head; heads of one projection in a row go in one
+      const bool starts = a.fused ? lane == 0 || h == 0 : true;
+      if (lane < valid && starts) {
+        const int64_t row = t0 + t;
+        const __nv_bfloat16* from = h < a.Hq           ? a.q + row * a.q_st + h * a.q_sh
+                                    : h < a.Hq + a.Hkv ? a.k + row * a.k_st + (h - a.Hq) * a.k_sh
+                                                       : a.v + row * a.v_st + (h - a.Hq - a.Hkv) * a.v_sh;
+        const int heads = a.fused ? min(valid - lane, n_heads - h) : 1;
+        bulk_load(&ring[s][lane * kRowBytes], from, heads * kRowBytes, &full[s]);
+      }
+      done = n + 1;
+    }
+    // every copy lands before the CTA may exit
+    for (int n = max(0, done - kStages); n < done; ++n)
+      if (!mbar_wait(&full[n % kStages], (n / kStages) & 1, a.err, kDevErrDrainWait)) break;
+    return;
+  }
 
   // this lane's two chunks.  Halves: values f.. and their partners; behind the rotated dims the
   // rest is split in two the same way.  Interleaved: pairs lie inside a chunk
@@ -168,45 +228,8 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
   const int c1 = INTER ? D / 2 + f : in_rot ? f + half : a.rot + (D - a.rot) / 2 + f - half;
   const bool turn0 = INTER ? c0 < a.rot : in_rot, turn1 = INTER ? c1 < a.rot : in_rot;
 
-  // The steps of a group are 32 pairs apart.  Its input pointer moves by a constant when q, k and
-  // v are the heads of one fused projection, and is computed anew otherwise; so does q_out's.
-  int ft = 0;  // token and head of the next fetch
-  int fh = static_cast<int>(pair0 - static_cast<uint32_t>(t0) * n_heads) + (threadIdx.x >> 3);
-  while (fh >= n_heads) fh -= n_heads, ++ft;
-  auto input = [&]() -> const __nv_bfloat16* {
-    const int64_t row = t0 + ft;
-    if (fh < a.Hq) return a.q + row * a.q_st + fh * a.q_sh;
-    if (fh < a.Hq + a.Hkv) return a.k + row * a.k_st + (fh - a.Hq) * a.k_sh;
-    return a.v + row * a.v_st + (fh - a.Hq - a.Hkv) * a.v_sh;
-  };
-  const __nv_bfloat16* in = input();
-  const int64_t in_step = kGroups * a.q_sh, in_wrap = a.q_st - n_heads * a.q_sh;
-  const int64_t out_step = kGroups * a.o_sh, out_wrap = a.o_st - n_heads * a.o_sh;
-
-  uint32_t raw[kAhead][H];
-  int who[kAhead];  // token << 16 | head of what is in flight
-  auto fetch = [&](uint32_t (&w)[H], int& id) {
-    id = (ft << 16) | fh;
-    if (t0 + ft < a.T) {
-      load_chunk<H>(in + c0, w);
-      load_chunk<H>(in + c1, w + H / 2);
-    }
-    fh += kGroups;
-    in += in_step;
-    while (fh >= n_heads) fh -= n_heads, ++ft, in += in_wrap;
-    if (!a.fused) in = input();
-  };
-  __nv_bfloat16* out = a.q_out + (t0 + static_cast<int64_t>(ft)) * a.o_st + fh * a.o_sh;  // of the next step
-#pragma unroll
-  for (int u = 0; u < kAhead; ++u) {
-#pragma unroll
-    for (int j = 0; j < H; ++j) raw[u][j] = 0u;
-    who[u] = 0;
-    if (u < a.steps) fetch(raw[u], who[u]);
-  }
-
-  for (int t = warp; t < tokens; t += kThreads / 32) {
-    const int row = t0 + t;
+  for (int i = warp; i < tokens; i += kWarps) {
+    const int row = t0 + i;
     const int b = sequence_of(a.cu_q, a.B, row);
     Place pl;
     pl.live = b >= 0;
@@ -223,12 +246,12 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
       }
       pl.table = a.positions ? __ldg(a.positions + row) : pos;
       if (pl.table >= a.max_pos) pl.table = -1;
-      if (a.rot > 0 && pl.table < 0 && (threadIdx.x & 31) == 0)
+      if (a.rot > 0 && pl.table < 0 && lane == 0)
         atomicOr(a.err + kErrCode, static_cast<unsigned int>(kDevErrPosition));
     }
-    if ((threadIdx.x & 31) == 0) places[t] = pl;
+    if (lane == 0) places[i] = pl;
   }
-  __syncthreads();
+  asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");  // (the copying warp goes its own way)
 
   Place pl;
   pl.live = 0;
@@ -237,16 +260,18 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
   uint64_t cs[H], sn[H], wt[H];
 #pragma unroll
   for (int j = 0; j < H; ++j) cs[j] = sn[j] = wt[j] = 0ull;
-  auto step = [&](uint32_t (&w)[H], int& id) {
+  for (int n = 0; n < steps; ++n, advance()) {
+    const int s = n % kStages;
+    if (!__all_sync(0xffffffffu, mbar_wait(&full[s], (n / kStages) & 1, a.err, kDevErrFullWait))) break;
     uint32_t r[H];
-#pragma unroll
-    for (int j = 0; j < H; ++j) r[j] = w[j];
-    const int t = id >> 16, h = id & 0xFFFF;
-    __nv_bfloat16* const o_q = out;
-    out += out_step;
-    for (int x = h + kGroups; x >= n_heads; x -= n_heads) out += out_wrap;
-    fetch(w, id);
-    const bool here = t < tokens;
+    {
+      const uint8_t* row = &ring[s][(threadIdx.x >> 3) * kRowBytes];
+      load_chunk<H>(reinterpret_cast<const __nv_bfloat16*>(row) + c0, r);
+      load_chunk<H>(reinterpret_cast<const __nv_bfloat16*>(row) + c1, r + H / 2);
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[s]);
+    const bool here = pair0 + static_cast<uint32_t>(n * kGroups + (threadIdx.x >> 3)) < pair1;
     if (here && t != have_t) {  // a new token
       have_t = t;
       pl = places[t];
@@ -293,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
     float ss = sum_f32x2(acc);
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (!here || !pl.live) return;  // (no shuffle below)
+    if (!here || !pl.live) continue;  // (no shuffle below)
     if (!is_v) {
       const void* wp = is_q ? a.q_weight : a.k_weight;
       const int64_t w_sh = is_q ? a.q_weight_sh : a.k_weight_sh;
@@ -334,8 +359,9 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
       }
     }
     if (is_q) {
-      store_chunk<H>(o_q + c0, r);
-      store_chunk<H>(o_q + c1, r + H / 2);
+      __nv_bfloat16* o = a.q_out + (t0 + static_cast<int64_t>(t)) * a.o_st + h * a.o_sh;
+      store_chunk<H>(o + c0, r);
+      store_chunk<H>(o + c1, r + H / 2);
     } else if (pl.page >= 0) {
       const int g = h - a.Hq - (is_v ? a.Hkv : 0);
       const int64_t to =
@@ -352,24 +378,18 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
         store_chunk<H>(o + c1, r + H / 2);
       }
     }
-  };
-  for (int n = 0; n < a.steps; n += kAhead) {
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-      if (n + u < a.steps) step(raw[u], who[u]);  // the same for every lane of the block
   }
 }
 
 template <int D, bool FP8>
 cudaError_t launch(AppendArgs a, cudaStream_t stream) {
   const int64_t n_heads = a.Hq + 2 * a.Hkv, pairs = a.T * n_heads;
-  // Steps of 32 heads a block: several waves of two blocks an SM (the looks-up of a block's
-  // tokens, about 2 us, should run under other blocks' traffic), one step where there is little
-  int64_t steps = std::min<int64_t>(kMaxSteps, std::max<int64_t>(1, pairs / (kGroups * 3 * 304)));
-  steps = std::min<int64_t>(steps, (kMaxTokens - 2) * n_heads / kGroups);  // tokens that a run touches
+  // equal runs for two CTAs an SM, of one stage at least; a run touches kMaxTokens tokens at most
+  int64_t steps = (pairs + kGroups * kCtas - 1) / (kGroups * kCtas);
+  steps = std::min<int64_t>(steps, std::max<int64_t>(1, (kMaxTokens - 2) * n_heads / kGroups));
   a.steps = static_cast<int>(steps);
-  a.fused = a.k_st == a.q_st && a.v_st == a.q_st && a.k_sh == a.q_sh && a.v_sh == a.q_sh && a.k == a.q + a.Hq * a.q_sh &&
-            a.v == a.k + a.Hkv * a.q_sh;
+  a.fused = a.q_sh == D && a.k_st == a.q_st && a.v_st == a.q_st && a.k_sh == D && a.v_sh == D && a.k == a.q + a.Hq * D &&
+            a.v == a.k + a.Hkv * D;
   const unsigned int blocks = static_cast<unsigned int>((pairs + steps * kGroups - 1) / (steps * kGroups));
   if (a.interleaved)
     append_kernel<D, FP8, true><<<blocks, kThreads, 0, stream>>>(a);

@@ -198,8 +198,8 @@ struct AppendArgs {
   int64_t num_blocks;
   int32_t B, T, Hq, Hkv, rot, interleaved, weight_bf16;
   int32_t block_len, max_blocks, scale_block;
-  int32_t steps;  // heads that each group of a block works off, and whether q, k and v are the
-  int32_t fused;  //   heads of one projection (the launcher's)
+  int32_t steps;  // stages of 32 heads of a CTA's run, and whether a token's q, k and v heads lie in
+  int32_t fused;  //   a row in memory (the launcher's)
   float eps;
   unsigned int* err;
 };
