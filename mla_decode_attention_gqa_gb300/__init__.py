@@ -305,7 +305,7 @@ def _ws_arg(workspace, nbytes, dev):
 
 
 def _check_lens(t, n, name):
-    if t.dtype != torch.int32 or not t.is_contiguous() or tuple(t.shape) != (n,):
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.shape != (n,):
         raise ValueError(f"{name} must be contiguous int32 of shape ({n},)")
 
 
@@ -656,15 +656,23 @@ def gqa_decode_attn_passq(q, k_shards, v_shards, shard_lens, k_scale=None, v_sca
     return out, lse
 
 
+def _elsewhere(q, *ts):
+    """Raises: some tensor of the call is not on q's device."""
+    for t in ts:
+        if t is not None:
+            _require_cuda(t)
+            _same_device(q.device, **{"a tensor": t})
+
+
 def _check_chunk(q, k_pages, v_pages, seq_lens, cu_q, block_table, k_scale, v_scale, scale_block):
     """What the two chunk calls share: q [T, Hq, d], pages [num_blocks, Hkv, block_len, d],
     cu_q int32 [B + 1], seq_lens int32 [B], block_table int32 [B, max_blocks].  Returns
-    (B, T, Hq, Hkv, d, KV dtype, paged description)."""
-    dev = q.device
-    for t in (k_pages, v_pages, seq_lens, cu_q, block_table, k_scale, v_scale):
-        if t is not None and t.device != dev:
-            _require_cuda(t)
-            _same_device(dev, **{"a tensor": t})
+    (B, T, Hq, Hkv, d, KV dtype, paged description).  (Host time counts in a decode step: plain
+    comparisons, no loops over the tensors.)"""
+    i = q.get_device()
+    if not (i == k_pages.get_device() == v_pages.get_device() == seq_lens.get_device() == cu_q.get_device()
+            == block_table.get_device()):
+        _elsewhere(q, k_pages, v_pages, seq_lens, cu_q, block_table)
     if q.dim() != 3 or k_pages.dim() != 4 or v_pages.dim() != 4:
         raise ValueError("q must be [T,Hq,d] and pages [num_blocks,Hkv,block_len,d]")
     if q.dtype != torch.bfloat16:
@@ -681,8 +689,10 @@ def _check_chunk(q, k_pages, v_pages, seq_lens, cu_q, block_table, k_scale, v_sc
     _check_lens(seq_lens, B, "seq_lens")
     _check_lens(cu_q, B + 1, "cu_q")
     kv = _kv_dtype(k_pages)
-    if kv == SKV_KV_FP8_E4M3 and scale_block > 0:
-        _check_scales((k_scale, v_scale), (nb, Hkv, L // scale_block), "[num_blocks, Hkv, block_len / scale_block]")
+    if kv == SKV_KV_FP8_E4M3:
+        _elsewhere(q, k_scale, v_scale)
+        if scale_block > 0:
+            _check_scales((k_scale, v_scale), (nb, Hkv, L // scale_block), "[num_blocks, Hkv, block_len / scale_block]")
     return B, T, Hq, Hkv, hd, kv, SkvPaged(L, max_blocks, nb, block_table.data_ptr())
 
 
@@ -737,7 +747,7 @@ def _head_stride(w, heads, hd, dev, name):
     """Head stride of a norm weight [d] or [heads, d]."""
     if w is None:
         return 0
-    if w.device != dev or not w.is_contiguous() or tuple(w.shape) not in ((hd,), (heads, hd)):
+    if w.device != dev or not w.is_contiguous() or (w.shape != (hd,) and w.shape != (heads, hd)):
         raise ValueError(f"{name} must be a contiguous tensor [{hd}] or [{heads}, {hd}] on {dev}")
     return hd if w.dim() == 2 else 0
 
@@ -756,36 +766,40 @@ def qk_norm_rope_append(q, k, v, k_pages, v_pages, seq_lens, cu_q, block_table, 
     B, T, Hq, Hkv, hd, kv, pg = _check_chunk(q, k_pages, v_pages, seq_lens, cu_q, block_table, k_scale, v_scale,
                                              scale_block)
     dev = q.device
-    for t in (k, v, cos, sin, positions, q_out):
-        if t is not None and t.device != dev:
-            _require_cuda(t)
-            _same_device(dev, **{"a tensor": t})
-    for t, name in ((k, "k"), (v, "v")):
-        if t.dtype != torch.bfloat16 or tuple(t.shape) != (T, Hkv, hd) or t.stride(2) != 1:
-            raise ValueError(f"{name} must be bf16 [{T}, {Hkv}, {hd}] with a unit-stride head dim")
+    i = q.get_device()
+    if not i == k.get_device() == v.get_device():
+        _elsewhere(q, k, v)
+    bf16 = torch.bfloat16
+    if k.dtype != bf16 or v.dtype != bf16 or k.shape != (T, Hkv, hd) or v.shape != k.shape or k.stride(2) != 1 \
+            or v.stride(2) != 1:
+        raise ValueError(f"k and v must be bf16 [{T}, {Hkv}, {hd}] with a unit-stride head dim")
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin go together")
     max_pos = rot = 0
     if cos is not None:
-        for t, name in ((cos, "cos"), (sin, "sin")):
-            if t.dtype != torch.float32 or t.dim() != 2 or not t.is_contiguous() or t.shape != cos.shape:
-                raise ValueError(f"{name} must be contiguous float32 [max_pos, rot / 2]")
+        if not i == cos.get_device() == sin.get_device():
+            _elsewhere(q, cos, sin)
+        if cos.dtype != torch.float32 or sin.dtype != torch.float32 or cos.dim() != 2 or sin.shape != cos.shape \
+                or not cos.is_contiguous() or not sin.is_contiguous():
+            raise ValueError("cos and sin must be contiguous float32 [max_pos, rot / 2]")
         max_pos, rot = cos.shape[0], 2 * cos.shape[1]
         if rot == 0:
             raise ValueError("cos and sin have no columns: pass None for no rotation")
-    if positions is not None and (cos is None or positions.dtype != torch.int32 or not positions.is_contiguous()
-                                  or tuple(positions.shape) != (T,)):
-        raise ValueError(f"positions must be contiguous int32 of shape ({T},), with cos and sin")
+    if positions is not None:
+        _elsewhere(q, positions)
+        if cos is None or positions.dtype != torch.int32 or not positions.is_contiguous() or positions.shape != (T,):
+            raise ValueError(f"positions must be contiguous int32 of shape ({T},), with cos and sin")
     q_ws, k_ws = _head_stride(q_weight, Hq, hd, dev, "q_weight"), _head_stride(k_weight, Hkv, hd, dev, "k_weight")
-    kinds = {w.dtype for w in (q_weight, k_weight) if w is not None}
-    if len(kinds) > 1 or not kinds <= {torch.bfloat16, torch.float32}:
+    w = q_weight if q_weight is not None else k_weight
+    wdtype = bf16 if w is None else w.dtype
+    if wdtype not in (bf16, torch.float32) or (k_weight is not None and k_weight.dtype != wdtype):
         raise ValueError("q_weight and k_weight must both be bf16 or both float32")
     if q_out is None:
         q_out = torch.empty((T, Hq, hd), dtype=torch.bfloat16, device=dev)
-    elif q_out.dtype != torch.bfloat16 or q_out.shape != q.shape or q_out.stride(2) != 1:
-        raise ValueError(f"q_out must be bf16 {tuple(q.shape)} with a unit-stride head dim")
+    elif q_out.device != dev or q_out.dtype != bf16 or q_out.shape != q.shape or q_out.stride(2) != 1:
+        raise ValueError(f"q_out must be bf16 {tuple(q.shape)} on {dev} with a unit-stride head dim")
     d = SkvAppendDesc(B, T, Hq, Hkv, hd, rot, 1 if interleaved else 0,
-                      SKV_WEIGHT_FP32 if torch.float32 in kinds else SKV_WEIGHT_BF16, kv, scale_block, eps, max_pos,
+                      SKV_WEIGHT_BF16 if wdtype == bf16 else SKV_WEIGHT_FP32, kv, scale_block, eps, max_pos,
                       q.stride()[:2], k.stride()[:2], v.stride()[:2], q_out.stride()[:2], q_ws, k_ws,
                       k_pages.stride()[:3], v_pages.stride()[:3])
     _check(_lib.qk_norm_rope_append(d, pg, q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(q_weight), _addr(k_weight),
