@@ -1,7 +1,7 @@
-// The plan and the merge of attention over ragged chunks.
+// The plan and the merge of attention over ragged chunks (attn_chunk_paged).
 //
-// The merge joins the partial rows of attention over ragged chunks (attn_chunk_paged): the rows of the
-// sequences whose KV tiles were dealt to several chunks.
+// The merge joins partial rows: those of sequences whose KV tiles were dealt to several chunks
+// (chunk_tc), or of items that a run's end cut (chunk_rows).
 //
 // For every such row, with k partials (o_c, lse_c): m = max lse_c, w_c = exp(lse_c - m),
 // out = sum w_c o_c / sum w_c in bf16, lse = m + ln sum w_c; all partials empty: out = 0,

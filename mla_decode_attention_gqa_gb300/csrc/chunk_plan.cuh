@@ -3,8 +3,9 @@
 // call can be captured into a graph and replayed with other lengths.
 //
 // Sequence b has n = cu_q[b+1] - cu_q[b] new tokens, the last n of its m = seq_lens[b] cached
-// ones; row i sits at position m - n + i.  Its rows of one KV head (n times the
-// group's G, or G padded to a power of two) are cut into row tiles of R rows, and every row tile's KV tiles into k_b chunks:
+// ones; row i sits at position m - n + i.  Its rows of one KV head (n times the group's G, or G
+// padded to a power of two) are cut into row tiles of R rows.  For the tensor-core kernel every row
+// tile's KV tiles are cut into k_b chunks:
 //   W   = sum over b of (row tiles) * Hkv * (KV tiles of its last row tile)
 //   L   = max(1, ceil(W / n_target)),  k_b = max(1, floor((KV tiles) / L))
 // so the work items with k_b > 1 are at most W / L <= n_target, whatever the lengths are

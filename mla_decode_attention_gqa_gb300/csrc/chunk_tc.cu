@@ -32,8 +32,8 @@
 //   * fp8: four converter warps split Q into two e4m3 parts (see split_q), so that Q K^T runs on the
 //     K codes as they land, two 8-bit products at twice the rate, and widen the V codes to bf16
 //     (exact) for P V; the K block scale goes into the score's scale, the V block scale into p
-//     before its rounding.  Widening K as well made the converters the bound (554 us against the
-//     ragged prompts' 3 x 1500);
+//     before its rounding.  (Widening K as well made the converters the bound: 554 us for ragged
+//     prompts over an fp8 cache that take 329 this way);
 //   * optimistic softmax: p = 2^(s - m) against the maximum so far; only a row's first visible
 //     tile takes a maximum (of 32 columns) beforehand, and a tile whose p sum passes 2^16 its true
 //     one, with O rescaled, and its p again.
@@ -418,443 +418,443 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     else
       asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-  if (warp == 3) {
-    // ------------------------------------------------------------ scheduler
-    // Items are handed out one by one (a counter that the plan kernel cleared), so that CTAs
-    // with light items take more; one item ahead of the other roles.
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan is written
-    const int total = __ldcg(p.ck.plan + kPlanItems);
-    for (int r = 0;; ++r) {
-      const int s = r & 1;
-      if (r >= 2 && !__all_sync(0xffffffffu, mbar_wait(&bars->item_empty[s], ((r >> 1) - 1) & 1, p.err, kDevErrEmptyWait)))
-        break;
-      int idx = blockIdx.x;
-      if (r > 0) {
-        if (lane == 0) idx = static_cast<int>(gridDim.x) + atomicAdd(p.ck.plan + kPlanNext, 1);
-        idx = __shfl_sync(0xffffffffu, idx, 0);
+    if (warp == 3) {
+      // ------------------------------------------------------------ scheduler
+      // Items are handed out one by one (a counter that the plan kernel cleared), so that CTAs
+      // with light items take more; one item ahead of the other roles.
+      asm volatile("griddepcontrol.wait;" ::: "memory");  // the plan is written
+      const int total = __ldcg(p.ck.plan + kPlanItems);
+      for (int r = 0;; ++r) {
+        const int s = r & 1;
+        if (r >= 2 && !__all_sync(0xffffffffu, mbar_wait(&bars->item_empty[s], ((r >> 1) - 1) & 1, p.err, kDevErrEmptyWait)))
+          break;
+        int idx = blockIdx.x;
+        if (r > 0) {
+          if (lane == 0) idx = static_cast<int>(gridDim.x) + atomicAdd(p.ck.plan + kPlanNext, 1);
+          idx = __shfl_sync(0xffffffffu, idx, 0);
+        }
+        TcItem t;
+        t.it.b = -1;
+        if (idx < total) {
+          t.it = chunk_item_at(p.ck, idx);
+          t.m0 = t.it.mt * 2 * kRowsTile;
+          const int m_last = min(t.m0 + 2 * kRowsTile, t.it.n * Gr) - 1;
+          t.pair = m_last - t.m0 >= kRowsTile ? 1 : 0;
+          const int pos0 = t.it.m - t.it.n;
+          t.tl = chunk_tiles(p.ck.window, p.ck.n_sink, p.ck.cap, pos0 + t.m0 / Gr, pos0 + m_last / Gr);
+          const int tiles = (t.tl.n + 1) / 2, per = (tiles + t.it.n_chunk - 1) / t.it.n_chunk;
+          const int i0 = min(t.it.c * per, tiles);
+          t.h0 = 2 * i0;
+          t.n_tiles = min(per, tiles - i0);
+        }
+        if (lane == 0) {
+          items[s] = t;
+          mbar_arrive(&bars->item_full[s]);
+        }
+        __syncwarp();
+        if (t.it.b < 0) break;
       }
-      TcItem t;
-      t.it.b = -1;
-      if (idx < total) {
-        t.it = chunk_item_at(p.ck, idx);
-        t.m0 = t.it.mt * 2 * kRowsTile;
-        const int m_last = min(t.m0 + 2 * kRowsTile, t.it.n * Gr) - 1;
-        t.pair = m_last - t.m0 >= kRowsTile ? 1 : 0;
-        const int pos0 = t.it.m - t.it.n;
-        t.tl = chunk_tiles(p.ck.window, p.ck.n_sink, p.ck.cap, pos0 + t.m0 / Gr, pos0 + m_last / Gr);
-        const int tiles = (t.tl.n + 1) / 2, per = (tiles + t.it.n_chunk - 1) / t.it.n_chunk;
-        const int i0 = min(t.it.c * per, tiles);
-        t.h0 = 2 * i0;
-        t.n_tiles = min(per, tiles - i0);
-      }
-      if (lane == 0) {
-        items[s] = t;
-        mbar_arrive(&bars->item_full[s]);
+    } else if (warp != 1) {
+      // ------------------------------------------------------------ TMA producers: 0 Q and K, 2 V
+      // A warp each, so that neither waits for the other's ring; the pages and rows of the next
+      // tile (four integer divisions and two dependent loads) are looked up behind this tile's
+      // copies, not between a freed stage and its refill, which bounds a two-stage ring.
+      const bool is_k = warp == 0;
+      const CUtensorMap* map = is_k ? &tmk : &tmv;
+      // (fp8: K codes go to the products as they are, V codes to a ring of their own, from which
+      // the converter warps fill V's)
+      uint64_t* full = is_k ? bars->k_full : C::FP8 ? bars->v8_full : bars->v_full;
+      uint64_t* empty = is_k ? bars->k_empty : C::FP8 ? bars->v8_empty : bars->v_empty;
+      uint8_t* ring = smem + (is_k ? C::OFF_K : C::FP8 ? C::OFF_V8 : C::OFF_V);
+      if (tc::elect_one()) {
+        tma_prefetch_desc(map);
+        if (is_k) tma_prefetch_desc(&tmq);
       }
       __syncwarp();
-      if (t.it.b < 0) break;
-    }
-  } else if (warp != 1) {
-    // ------------------------------------------------------------ TMA producers: 0 Q and K, 2 V
-    // A warp each, so that neither waits for the other's ring; the pages and rows of the next
-    // tile (four integer divisions and two dependent loads) are looked up behind this tile's
-    // copies, not between a freed stage and its refill, which bounds a two-stage ring.
-    const bool is_k = warp == 0;
-    const CUtensorMap* map = is_k ? &tmk : &tmv;
-    // (fp8: K codes go to the products as they are, V codes to a ring of their own, from which
-    // the converter warps fill V's)
-    uint64_t* full = is_k ? bars->k_full : C::FP8 ? bars->v8_full : bars->v_full;
-    uint64_t* empty = is_k ? bars->k_empty : C::FP8 ? bars->v8_empty : bars->v_empty;
-    uint8_t* ring = smem + (is_k ? C::OFF_K : C::FP8 ? C::OFF_V8 : C::OFF_V);
-    if (tc::elect_one()) {
-      tma_prefetch_desc(map);
-      if (is_k) tma_prefetch_desc(&tmq);
-    }
-    __syncwarp();
-    auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.err, kDevErrEmptyWait));
-    };
-    TcItem t;
-    int done = 0, nq = 0;  // tiles and query tiles loaded so far
-    bool ok = true;
-    for (int r = 0; ok && next_item(r, &t); ++r) {
-      if (t.n_tiles == 0) continue;
-      int page[2], at[2];  // of a tile's two halves
-      float scale = 0.f;   // fp8: lanes 0-3 of the K loader
-      auto look_up = [&](int i) {
-        const int first[2] = {t.token(2 * i), t.token(2 * i + 1)};
-        // a second half at or past the capacity holds no token: it takes the first one's page
-        // instead of an entry behind the table's row
-        const int a = first[0], b = first[1] < p.ck.cap ? first[1] : a;
-        at[0] = a % p.block_len;
-        at[1] = b % p.block_len;
-        page[0] = kv_page_of(p, t.it.b, a);
-        page[1] = kv_page_of(p, t.it.b, b);
-        if constexpr (C::FP8) {
-          // the scales of both halves, a lane each (K, V, K, V).  Halves in which no row sees a token,
-          // and pages outside the cache, take 0: their scales may be anything
-          const int hf = (lane >> 1) & 1, tok = first[hf], pg = page[hf];
-          const bool seen = (tok < t.tl.hi && tok + kHalf > t.tl.lo) || tok < t.tl.sinks;
-          scale = 0.f;
-          if (is_k && lane < 4 && seen && pg >= 0 && pg < p.num_blocks) {
-            const int per = p.block_len / p.scale_block;
-            const int64_t x = (static_cast<int64_t>(pg) * p.Hkv + t.it.g) * per + at[hf] / p.scale_block;
-            scale = __ldg(((lane & 1) ? p.v_scale : p.k_scale) + x);
+      auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.err, kDevErrEmptyWait));
+      };
+      TcItem t;
+      int done = 0, nq = 0;  // tiles and query tiles loaded so far
+      bool ok = true;
+      for (int r = 0; ok && next_item(r, &t); ++r) {
+        if (t.n_tiles == 0) continue;
+        int page[2], at[2];  // of a tile's two halves
+        float scale = 0.f;   // fp8: lanes 0-3 of the K loader
+        auto look_up = [&](int i) {
+          const int first[2] = {t.token(2 * i), t.token(2 * i + 1)};
+          // a second half at or past the capacity holds no token: it takes the first one's page
+          // instead of an entry behind the table's row
+          const int a = first[0], b = first[1] < p.ck.cap ? first[1] : a;
+          at[0] = a % p.block_len;
+          at[1] = b % p.block_len;
+          page[0] = kv_page_of(p, t.it.b, a);
+          page[1] = kv_page_of(p, t.it.b, b);
+          if constexpr (C::FP8) {
+            // the scales of both halves, a lane each (K, V, K, V).  Halves in which no row sees a token,
+            // and pages outside the cache, take 0: their scales may be anything
+            const int hf = (lane >> 1) & 1, tok = first[hf], pg = page[hf];
+            const bool seen = (tok < t.tl.hi && tok + kHalf > t.tl.lo) || tok < t.tl.sinks;
+            scale = 0.f;
+            if (is_k && lane < 4 && seen && pg >= 0 && pg < p.num_blocks) {
+              const int per = p.block_len / p.scale_block;
+              const int64_t x = (static_cast<int64_t>(pg) * p.Hkv + t.it.g) * per + at[hf] / p.scale_block;
+              scale = __ldg(((lane & 1) ? p.v_scale : p.k_scale) + x);
+            }
           }
+        };
+        look_up(0);
+        if (is_k) {
+          // the item before has no scores left to compute
+          if (nq > 0 && !wait_all(&bars->q_empty, (nq - 1) & 1)) break;
+          if (tc::elect_one()) {
+            mbar_arrive_expect_tx(&bars->q_full, (1 + t.pair) * C::TILE);
+            for (int k = 0; k <= t.pair; ++k)
+              for (int bx = 0; bx < NB; ++bx)
+                tma_4d(smem + k * C::TILE + bx * C::BOX, &tmq, &bars->q_full, bx * 64, t.it.g * G,
+                       t.it.row0 + (t.m0 + k * kRowsTile) / Gr, 0);
+          }
+          __syncwarp();
+          ++nq;
+        }
+        for (int i = 0; i < t.n_tiles; ++i) {
+          const int s = done % NST;
+          ok = done < NST || wait_all(&empty[s], ((done / NST) - 1) & 1);
+          if (!ok) break;
+          if (tc::elect_one()) {
+            mbar_arrive_expect_tx(&full[s], C::LOAD);
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+              for (int bx = 0; bx < C::LOAD_BOXES; ++bx)
+                tma_4d(ring + s * C::LOAD + bx * C::BOX + hf * (C::BOX / 2), map, &full[s], bx * C::LOAD_BOX_ELEMS, at[hf],
+                       t.it.g, page[hf]);
+          }
+          __syncwarp();
+          if constexpr (C::FP8) {
+            if (is_k) {
+              // slot of tile x again at x + 8: its codes take a stage that the scores of x + 8 - NST left,
+              // which were issued after P V of x: the softmax of x is done
+              const int sl = done % kScaleSlots;
+              if (lane < 4) reinterpret_cast<float*>(&bars->scales[sl])[lane] = scale;
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars->sc_full[sl]);
+            }
+          }
+          ++done;
+          if (i + 1 < t.n_tiles) look_up(i + 1);
+        }
+      }
+      // every issued copy lands before the CTA may exit
+      for (int i = max(0, done - NST); i < done; ++i)
+        if (!mbar_wait(&full[i % NST], (i / NST) & 1, p.err, kDevErrDrainWait)) break;
+      if (is_k && nq > 0) mbar_wait(&bars->q_full, (nq - 1) & 1, p.err, kDevErrDrainWait);
+    } else {
+      // ------------------------------------------------------------ MMA issuer
+      // The whole warp waits, one elected lane issues; a tile's stage is a compile-time constant,
+      // so every operand is a constant offset.
+      // (format 0 of kind::f8f6f4 is e4m3, as 0 of kind::f16 is fp16)
+      const uint32_t idesc_s = tc::idesc_f16(128, kTN, !C::FP8, false, false);
+      const uint32_t idesc_pv = tc::idesc_f16(128, D, true, false, true);
+      const uint64_t qd = tc::smem_desc_sw128(smem_u32(smem), 16, 1024);
+      const uint64_t kd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
+      const uint64_t vd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_V), C::BOX, 1024);
+      // A descriptor at a constant offset, by one 32-bit addition where it is used: kept as they are
+      // over the loops, the 64-bit sums of every product take more registers than the warp has (the
+      // address field ends in the low word, shared memory ends below its 18 bits)
+      auto low_of = [](uint64_t d) -> uint32_t {
+        uint32_t lo = static_cast<uint32_t>(d);
+        asm volatile("" : "+r"(lo));
+        return lo;
+      };
+      auto at = [](uint64_t d, uint32_t lo, uint32_t bytes) -> uint64_t {
+        return (d & 0xFFFFFFFF00000000ull) | (lo + (bytes >> 4));
+      };
+      auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.err, kDevErrFullWait));
+      };
+      auto issue_s = [&](int k, int q, int stage) {  // S_k = Q_q K^T
+        const uint32_t ql = low_of(qd), kl = low_of(kd);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t in_box = (ks >> 2) * C::BOX + (ks & 3) * 32;
+          const uint64_t qa = at(qd, ql, q * C::TILE + in_box);
+          if constexpr (C::FP8)  // the large parts of Q over 4 steps of 32 codes, then the small ones
+            tc::mma_f8_ss(tmem + kColS + 128 * k, qa, at(kd, kl, stage * C::LOAD + (ks & 3) * 32), idesc_s, ks > 0 ? 1u : 0u);
+          else
+            tc::mma_f16_ss(tmem + kColS + 128 * k, qa, at(kd, kl, stage * C::LOAD + in_box), idesc_s, ks > 0 ? 1u : 0u);
+        }
+        tc::mma_commit(smem_u32(&bars->s_full[k]));
+      };
+      auto issue_pv = [&](int k, int stage, uint32_t acc0) {  // O_k += P_k V
+        const uint32_t vl = low_of(vd);
+#pragma unroll
+        for (int ks = 0; ks < kTN / 16; ++ks)
+          tc::mma_f16_ts(tmem + kColO + 128 * k, tmem + kColS + 128 * k + ks * 8, at(vd, vl, stage * C::TILE + ks * 2048),
+                         idesc_pv, ks > 0 ? 1u : acc0);
+        tc::mma_commit(smem_u32(&bars->pv_done[k]));
+      };
+      // runs fn with tile number x's stage as a constant
+      auto at_stage = [&](int x, auto&& fn) {
+        const int s = x % NST;
+        if (s == 0) fn(Int<0>{});
+        if (s == 1) fn(Int<1>{});
+        if constexpr (NST == 4) {
+          if (s == 2) fn(Int<2>{});
+          if (s == 3) fn(Int<3>{});
         }
       };
-      look_up(0);
-      if (is_k) {
-        // the item before has no scores left to compute
-        if (nq > 0 && !wait_all(&bars->q_empty, (nq - 1) & 1)) break;
-        if (tc::elect_one()) {
-          mbar_arrive_expect_tx(&bars->q_full, (1 + t.pair) * C::TILE);
-          for (int k = 0; k <= t.pair; ++k)
-            for (int bx = 0; bx < NB; ++bx)
-              tma_4d(smem + k * C::TILE + bx * C::BOX, &tmq, &bars->q_full, bx * 64, t.it.g * G,
-                     t.it.row0 + (t.m0 + k * kRowsTile) / Gr, 0);
-        }
-        __syncwarp();
+      TcItem t;
+      int base = 0, nq = 0;          // tiles and query tiles of the items before
+      uint32_t np[2] = {0u, 0u};     // tiles of each softmax group so far
+      bool ok = true;
+      for (int r = 0; ok && next_item(r, &t); ++r) {
+        const int n = t.n_tiles;
+        if (n == 0) continue;
+        ok = C::FP8 ? wait_all(&bars->q8_full[nq & 1], (nq >> 1) & 1) : wait_all(&bars->q_full, nq & 1);
+        if (!ok) break;
         ++nq;
-      }
-      for (int i = 0; i < t.n_tiles; ++i) {
-        const int s = done % NST;
-        ok = done < NST || wait_all(&empty[s], ((done / NST) - 1) & 1);
-        if (!ok) break;
-        if (tc::elect_one()) {
-          mbar_arrive_expect_tx(&full[s], C::LOAD);
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-            for (int bx = 0; bx < C::LOAD_BOXES; ++bx)
-              tma_4d(ring + s * C::LOAD + bx * C::BOX + hf * (C::BOX / 2), map, &full[s], bx * C::LOAD_BOX_ELEMS, at[hf],
-                     t.it.g, page[hf]);
-        }
-        __syncwarp();
-        if constexpr (C::FP8) {
-          if (is_k) {
-            // slot of tile x again at x + 8: its codes take a stage that the scores of x + 8 - NST left,
-            // which were issued after P V of x: the softmax of x is done
-            const int sl = done % kScaleSlots;
-            if (lane < 4) reinterpret_cast<float*>(&bars->scales[sl])[lane] = scale;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->sc_full[sl]);
-          }
-        }
-        ++done;
-        if (i + 1 < t.n_tiles) look_up(i + 1);
-      }
-    }
-    // every issued copy lands before the CTA may exit
-    for (int i = max(0, done - NST); i < done; ++i)
-      if (!mbar_wait(&full[i % NST], (i / NST) & 1, p.err, kDevErrDrainWait)) break;
-    if (is_k && nq > 0) mbar_wait(&bars->q_full, (nq - 1) & 1, p.err, kDevErrDrainWait);
-  } else {
-    // ------------------------------------------------------------ MMA issuer
-    // The whole warp waits, one elected lane issues; a tile's stage is a compile-time constant,
-    // so every operand is a constant offset.
-    // (format 0 of kind::f8f6f4 is e4m3, as 0 of kind::f16 is fp16)
-    const uint32_t idesc_s = tc::idesc_f16(128, kTN, !C::FP8, false, false);
-    const uint32_t idesc_pv = tc::idesc_f16(128, D, true, false, true);
-    const uint64_t qd = tc::smem_desc_sw128(smem_u32(smem), 16, 1024);
-    const uint64_t kd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
-    const uint64_t vd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_V), C::BOX, 1024);
-    // A descriptor at a constant offset, by one 32-bit addition where it is used: kept as they are
-    // over the loops, the 64-bit sums of every product take more registers than the warp has (the
-    // address field ends in the low word, shared memory ends below its 18 bits)
-    auto low_of = [](uint64_t d) -> uint32_t {
-      uint32_t lo = static_cast<uint32_t>(d);
-      asm volatile("" : "+r"(lo));
-      return lo;
-    };
-    auto at = [](uint64_t d, uint32_t lo, uint32_t bytes) -> uint64_t {
-      return (d & 0xFFFFFFFF00000000ull) | (lo + (bytes >> 4));
-    };
-    auto wait_all = [&](uint64_t* bar, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.err, kDevErrFullWait));
-    };
-    auto issue_s = [&](int k, int q, int stage) {  // S_k = Q_q K^T
-      const uint32_t ql = low_of(qd), kl = low_of(kd);
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
-        const uint32_t in_box = (ks >> 2) * C::BOX + (ks & 3) * 32;
-        const uint64_t qa = at(qd, ql, q * C::TILE + in_box);
-        if constexpr (C::FP8)  // the large parts of Q over 4 steps of 32 codes, then the small ones
-          tc::mma_f8_ss(tmem + kColS + 128 * k, qa, at(kd, kl, stage * C::LOAD + (ks & 3) * 32), idesc_s, ks > 0 ? 1u : 0u);
-        else
-          tc::mma_f16_ss(tmem + kColS + 128 * k, qa, at(kd, kl, stage * C::LOAD + in_box), idesc_s, ks > 0 ? 1u : 0u);
-      }
-      tc::mma_commit(smem_u32(&bars->s_full[k]));
-    };
-    auto issue_pv = [&](int k, int stage, uint32_t acc0) {  // O_k += P_k V
-      const uint32_t vl = low_of(vd);
-#pragma unroll
-      for (int ks = 0; ks < kTN / 16; ++ks)
-        tc::mma_f16_ts(tmem + kColO + 128 * k, tmem + kColS + 128 * k + ks * 8, at(vd, vl, stage * C::TILE + ks * 2048),
-                       idesc_pv, ks > 0 ? 1u : acc0);
-      tc::mma_commit(smem_u32(&bars->pv_done[k]));
-    };
-    // runs fn with tile number x's stage as a constant
-    auto at_stage = [&](int x, auto&& fn) {
-      const int s = x % NST;
-      if (s == 0) fn(Int<0>{});
-      if (s == 1) fn(Int<1>{});
-      if constexpr (NST == 4) {
-        if (s == 2) fn(Int<2>{});
-        if (s == 3) fn(Int<3>{});
-      }
-    };
-    TcItem t;
-    int base = 0, nq = 0;          // tiles and query tiles of the items before
-    uint32_t np[2] = {0u, 0u};     // tiles of each softmax group so far
-    bool ok = true;
-    for (int r = 0; ok && next_item(r, &t); ++r) {
-      const int n = t.n_tiles;
-      if (n == 0) continue;
-      ok = C::FP8 ? wait_all(&bars->q8_full[nq & 1], (nq >> 1) & 1) : wait_all(&bars->q_full, nq & 1);
-      if (!ok) break;
-      ++nq;
-      // scores of tile x (both groups, or group x & 1 in solo mode); the last ones free Q
-      if (t.pair) {
-        // tile i: PV0(i), S0(i+1), PV1(i), S1(i+1)
-        ok = wait_all(&bars->k_full[base % NST], (base / NST) & 1);
-        if (!ok) break;
-        tc::fence_after_sync();
-        at_stage(base, [&](auto st) {
-          constexpr int ST = decltype(st)::value;
-          if (tc::elect_one()) {
-            issue_s(0, 0, ST);
-            issue_s(1, 1, ST);
-            tc::mma_commit(smem_u32(&bars->k_empty[ST]));
-            if (n == 1) tc::mma_commit(smem_u32(&bars->q_empty));
-          }
-          __syncwarp();
-        });
-        auto tile = [&](auto st, int i) {
-          constexpr int ST = decltype(st)::value, NX = (ST + 1) % NST;
-          const int x = base + i;
-          const bool more = i + 1 < n;
-          // tiles first, the softmax last: a wait costs 100 cycles and more even for what is there
-          ok = wait_all(&bars->v_full[ST], (x / NST) & 1) && (!more || wait_all(&bars->k_full[NX], ((x + 1) / NST) & 1)) &&
-               wait_all(&bars->p_full[0], np[0] & 1);
-          if (!ok) return;
-          ++np[0];
+        // scores of tile x (both groups, or group x & 1 in solo mode); the last ones free Q
+        if (t.pair) {
+          // tile i: PV0(i), S0(i+1), PV1(i), S1(i+1)
+          ok = wait_all(&bars->k_full[base % NST], (base / NST) & 1);
+          if (!ok) break;
           tc::fence_after_sync();
-          if (tc::elect_one()) {
-            issue_pv(0, ST, i > 0 ? 1u : 0u);
-            if (more) issue_s(0, 0, NX);
-          }
-          __syncwarp();
-          ok = wait_all(&bars->p_full[1], np[1] & 1);
-          if (!ok) return;
-          ++np[1];
-          tc::fence_after_sync();
-          if (tc::elect_one()) {
-            issue_pv(1, ST, i > 0 ? 1u : 0u);
-            tc::mma_commit(smem_u32(&bars->v_empty[ST]));
-            if (more) {
-              issue_s(1, 1, NX);
-              tc::mma_commit(smem_u32(&bars->k_empty[NX]));
-              if (i + 2 == n) tc::mma_commit(smem_u32(&bars->q_empty));
+          at_stage(base, [&](auto st) {
+            constexpr int ST = decltype(st)::value;
+            if (tc::elect_one()) {
+              issue_s(0, 0, ST);
+              issue_s(1, 1, ST);
+              tc::mma_commit(smem_u32(&bars->k_empty[ST]));
+              if (n == 1) tc::mma_commit(smem_u32(&bars->q_empty));
             }
-          }
-          __syncwarp();
-        };
-        // unrolled by the ring depth, entered at the stage that the items before left
-        int i = 0;
-        const int enter = base % NST;
-        for (bool first = true; ok && i < n; first = false) {
-          if (!first || enter <= 0) {
-            tile(Int<0>{}, i);
-            if (!ok || ++i >= n) break;
-          }
-          if (!first || enter <= 1) {
-            tile(Int<1>{}, i);
-            if (!ok || ++i >= n) break;
-          }
-          if constexpr (NST == 4) {
-            if (!first || enter <= 2) {
-              tile(Int<2>{}, i);
+            __syncwarp();
+          });
+          auto tile = [&](auto st, int i) {
+            constexpr int ST = decltype(st)::value, NX = (ST + 1) % NST;
+            const int x = base + i;
+            const bool more = i + 1 < n;
+            // tiles first, the softmax last: a wait costs 100 cycles and more even for what is there
+            ok = wait_all(&bars->v_full[ST], (x / NST) & 1) && (!more || wait_all(&bars->k_full[NX], ((x + 1) / NST) & 1)) &&
+                 wait_all(&bars->p_full[0], np[0] & 1);
+            if (!ok) return;
+            ++np[0];
+            tc::fence_after_sync();
+            if (tc::elect_one()) {
+              issue_pv(0, ST, i > 0 ? 1u : 0u);
+              if (more) issue_s(0, 0, NX);
+            }
+            __syncwarp();
+            ok = wait_all(&bars->p_full[1], np[1] & 1);
+            if (!ok) return;
+            ++np[1];
+            tc::fence_after_sync();
+            if (tc::elect_one()) {
+              issue_pv(1, ST, i > 0 ? 1u : 0u);
+              tc::mma_commit(smem_u32(&bars->v_empty[ST]));
+              if (more) {
+                issue_s(1, 1, NX);
+                tc::mma_commit(smem_u32(&bars->k_empty[NX]));
+                if (i + 2 == n) tc::mma_commit(smem_u32(&bars->q_empty));
+              }
+            }
+            __syncwarp();
+          };
+          // unrolled by the ring depth, entered at the stage that the items before left
+          int i = 0;
+          const int enter = base % NST;
+          for (bool first = true; ok && i < n; first = false) {
+            if (!first || enter <= 0) {
+              tile(Int<0>{}, i);
               if (!ok || ++i >= n) break;
             }
-            tile(Int<3>{}, i);
-            ++i;
+            if (!first || enter <= 1) {
+              tile(Int<1>{}, i);
+              if (!ok || ++i >= n) break;
+            }
+            if constexpr (NST == 4) {
+              if (!first || enter <= 2) {
+                tile(Int<2>{}, i);
+                if (!ok || ++i >= n) break;
+              }
+              tile(Int<3>{}, i);
+              ++i;
+            }
+          }
+        } else {
+          // tile i belongs to group i & 1: PV(i), then S(i + 2)
+          auto scores = [&](int i) {
+            at_stage(base + i, [&](auto st) {
+              constexpr int ST = decltype(st)::value;
+              ok = wait_all(&bars->k_full[ST], ((base + i) / NST) & 1);
+              if (!ok) return;
+              tc::fence_after_sync();
+              if (tc::elect_one()) {
+                if (i & 1)
+                  issue_s(1, 0, ST);
+                else
+                  issue_s(0, 0, ST);
+                tc::mma_commit(smem_u32(&bars->k_empty[ST]));
+                if (i + 1 == n) tc::mma_commit(smem_u32(&bars->q_empty));
+              }
+              __syncwarp();
+            });
+          };
+          scores(0);
+          if (ok && n > 1) scores(1);
+          for (int i = 0; i < n && ok; ++i) {
+            at_stage(base + i, [&](auto st) {
+              constexpr int ST = decltype(st)::value;
+              const int k = i & 1;
+              ok = wait_all(&bars->p_full[k], np[k] & 1) && wait_all(&bars->v_full[ST], ((base + i) / NST) & 1);
+              if (!ok) return;
+              ++np[k];
+              tc::fence_after_sync();
+              if (tc::elect_one()) {
+                if (k)
+                  issue_pv(1, ST, i > 1 ? 1u : 0u);
+                else
+                  issue_pv(0, ST, i > 1 ? 1u : 0u);
+                tc::mma_commit(smem_u32(&bars->v_empty[ST]));
+              }
+              __syncwarp();
+            });
+            if (ok && i + 2 < n) scores(i + 2);
           }
         }
-      } else {
-        // tile i belongs to group i & 1: PV(i), then S(i + 2)
-        auto scores = [&](int i) {
-          at_stage(base + i, [&](auto st) {
-            constexpr int ST = decltype(st)::value;
-            ok = wait_all(&bars->k_full[ST], ((base + i) / NST) & 1);
-            if (!ok) return;
-            tc::fence_after_sync();
-            if (tc::elect_one()) {
-              if (i & 1)
-                issue_s(1, 0, ST);
-              else
-                issue_s(0, 0, ST);
-              tc::mma_commit(smem_u32(&bars->k_empty[ST]));
-              if (i + 1 == n) tc::mma_commit(smem_u32(&bars->q_empty));
-            }
-            __syncwarp();
-          });
-        };
-        scores(0);
-        if (ok && n > 1) scores(1);
-        for (int i = 0; i < n && ok; ++i) {
-          at_stage(base + i, [&](auto st) {
-            constexpr int ST = decltype(st)::value;
-            const int k = i & 1;
-            ok = wait_all(&bars->p_full[k], np[k] & 1) && wait_all(&bars->v_full[ST], ((base + i) / NST) & 1);
-            if (!ok) return;
-            ++np[k];
-            tc::fence_after_sync();
-            if (tc::elect_one()) {
-              if (k)
-                issue_pv(1, ST, i > 1 ? 1u : 0u);
-              else
-                issue_pv(0, ST, i > 1 ? 1u : 0u);
-              tc::mma_commit(smem_u32(&bars->v_empty[ST]));
-            }
-            __syncwarp();
-          });
-          if (ok && i + 2 < n) scores(i + 2);
-        }
+        base += n;
       }
-      base += n;
     }
-  }
   } else if (warp >= 12) {  // (fp8 only: no such warps otherwise)
     // ------------------------------------------------------------ fp8: Q split, V codes to bf16
     if constexpr (C::FP8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    const int row = (warp - 12) * 32 + lane;
-    // Q for the products with e4m3 keys: a row times the power of two that puts its largest
-    // magnitude in [2^7, 2^8) is the sum of two e4m3 values, the rounded one and the rest.  A bf16
-    // value's 8 bits are 4 and 4, so the sum is exact down to 2^-10 of the row's largest and off
-    // by 2^-18 of it at most below.  The rounded parts (128 bytes) go over the row's first 64
-    // values, the rests over its last 64, each after what it overwrites was read.
-    auto split_q = [&](uint8_t* q) -> float {
-      auto chunk = [&](int c) {
-        return reinterpret_cast<uint4*>(q + (c >> 3) * C::BOX + row * 128 + (((c & 7) ^ (row & 7)) << 4));
-      };
-      uint32_t most = 0u;  // magnitudes order as their bits; a NaN is above infinity
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+      const int row = (warp - 12) * 32 + lane;
+      // Q for the products with e4m3 keys: a row times the power of two that puts its largest
+      // magnitude in [2^7, 2^8) is the sum of two e4m3 values, the rounded one and the rest.  A bf16
+      // value's 8 bits are 4 and 4, so the sum is exact down to 2^-10 of the row's largest and off
+      // by 2^-18 of it at most below.  The rounded parts (128 bytes) go over the row's first 64
+      // values, the rests over its last 64, each after what it overwrites was read.
+      auto split_q = [&](uint8_t* q) -> float {
+        auto chunk = [&](int c) {
+          return reinterpret_cast<uint4*>(q + (c >> 3) * C::BOX + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+        };
+        uint32_t most = 0u;  // magnitudes order as their bits; a NaN is above infinity
 #pragma unroll 4
-      for (int c = 0; c < 16; ++c) {
-        const uint4 u = *chunk(c);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        for (int c = 0; c < 16; ++c) {
+          const uint4 u = *chunk(c);
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) most = max(most, max((w[j] << 16) & 0x7FFF0000u, w[j] & 0x7FFF0000u));
-      }
-      const bool finite = most < 0x7F800000u;
-      const int e = most == 0u ? 0 : min(max(static_cast<int>(most >> 23) - 127 - 7, -126), 126);
-      const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-      // a pair's codes: the rounded values in the low halves of hi, the rests' in those of lo
-      auto split = [&](uint32_t w, uint32_t& hi, uint32_t& lo) {
-        const float x = bf16_lo(w) * down, y = bf16_hi(w) * down;
-        const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t back = e4m3x2_to_f16x2(h);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
-        hi = h;
-        lo = __nv_cvt_float2_to_fp8x2(make_float2(x - f.x, y - f.y), __NV_SATFINITE, __NV_E4M3);
-      };
-      auto split_chunk = [&](const uint4& u, uint32_t* hi, uint32_t* lo) {  // 8 values: 2 words each
-        uint32_t h0, h1, h2, h3, l0, l1, l2, l3;
-        split(u.x, h0, l0);
-        split(u.y, h1, l1);
-        split(u.z, h2, l2);
-        split(u.w, h3, l3);
-        hi[0] = h0 | (h1 << 16), hi[1] = h2 | (h3 << 16);
-        lo[0] = l0 | (l1 << 16), lo[1] = l2 | (l3 << 16);
-      };
-      uint32_t lo[16];  // the rests of the values read so far and not yet written
-#pragma unroll
-      for (int c = 0; c < 8; c += 2) {  // first 64 values
-        uint32_t hi[4];
-        const uint4 u = *chunk(c), v = *chunk(c + 1);
-        split_chunk(u, hi, lo + 2 * c);
-        split_chunk(v, hi + 2, lo + 2 * c + 2);
-        *chunk(c / 2) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      }
-#pragma unroll
-      for (int c = 0; c < 8; c += 4) {  // last 64, four chunks read before two of them are written
-        uint32_t hi[8], rest[8];
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          const uint4 u = *chunk(8 + c + d);
-          split_chunk(u, hi + 2 * d, rest + 2 * d);
+          for (int j = 0; j < 4; ++j) most = max(most, max((w[j] << 16) & 0x7FFF0000u, w[j] & 0x7FFF0000u));
         }
-        *chunk(4 + c / 2) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *chunk(5 + c / 2) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-        if (c == 0) {  // chunks 8 .. 11 are read: the first values' rests; these rests wait in their place
+        const bool finite = most < 0x7F800000u;
+        const int e = most == 0u ? 0 : min(max(static_cast<int>(most >> 23) - 127 - 7, -126), 126);
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        // a pair's codes: the rounded values in the low halves of hi, the rests' in those of lo
+        auto split = [&](uint32_t w, uint32_t& hi, uint32_t& lo) {
+          const float x = bf16_lo(w) * down, y = bf16_hi(w) * down;
+          const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+          const uint32_t back = e4m3x2_to_f16x2(h);
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back));
+          hi = h;
+          lo = __nv_cvt_float2_to_fp8x2(make_float2(x - f.x, y - f.y), __NV_SATFINITE, __NV_E4M3);
+        };
+        auto split_chunk = [&](const uint4& u, uint32_t* hi, uint32_t* lo) {  // 8 values: 2 words each
+          uint32_t h0, h1, h2, h3, l0, l1, l2, l3;
+          split(u.x, h0, l0);
+          split(u.y, h1, l1);
+          split(u.z, h2, l2);
+          split(u.w, h3, l3);
+          hi[0] = h0 | (h1 << 16), hi[1] = h2 | (h3 << 16);
+          lo[0] = l0 | (l1 << 16), lo[1] = l2 | (l3 << 16);
+        };
+        uint32_t lo[16];  // the rests of the values read so far and not yet written
 #pragma unroll
-          for (int d = 0; d < 4; ++d) *chunk(8 + d) = make_uint4(lo[4 * d], lo[4 * d + 1], lo[4 * d + 2], lo[4 * d + 3]);
-#pragma unroll
-          for (int d = 0; d < 8; ++d) lo[d] = rest[d];
-        } else {  // chunks 12 .. 15 are read
-          *chunk(12) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          *chunk(13) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
-          *chunk(14) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
-          *chunk(15) = make_uint4(rest[4], rest[5], rest[6], rest[7]);
+        for (int c = 0; c < 8; c += 2) {  // first 64 values
+          uint32_t hi[4];
+          const uint4 u = *chunk(c), v = *chunk(c + 1);
+          split_chunk(u, hi, lo + 2 * c);
+          split_chunk(v, hi + 2, lo + 2 * c + 2);
+          *chunk(c / 2) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         }
-      }
-      // an infinity or a NaN in the row makes its scores NaN
-      return finite ? __uint_as_float(static_cast<uint32_t>(127 + e) << 23) : __int_as_float(0x7fc00000);
-    };
-    // One thread a token row: 16 codes of a 16-byte chunk become the 32 bytes of two chunks of
-    // the 128-byte-swizzled bf16 tile (both sides conflict-free: eight rows, eight chunks).
-    auto convert = [&](const uint8_t* from, uint8_t* to) {
-      uint32_t odd = 0u;  // bit 7 of a byte: a NaN code among the row's
-#pragma unroll 4
-      for (int c = 0; c < 8; ++c) {
-        const uint4 u = *reinterpret_cast<const uint4*>(from + row * 128 + ((c ^ (row & 7)) << 4));
-        uint8_t* d = to + (c >> 2) * C::BOX + row * 128;
-        const int d0 = 2 * (c & 3);
-        uint4 lo, hi;
-        e4m3x4_to_bf16(u.x, lo.x, lo.y, odd);
-        e4m3x4_to_bf16(u.y, lo.z, lo.w, odd);
-        e4m3x4_to_bf16(u.z, hi.x, hi.y, odd);
-        e4m3x4_to_bf16(u.w, hi.z, hi.w, odd);
-        *reinterpret_cast<uint4*>(d + ((d0 ^ (row & 7)) << 4)) = lo;
-        *reinterpret_cast<uint4*>(d + (((d0 + 1) ^ (row & 7)) << 4)) = hi;
-      }
-      if (odd & 0x80808080u) {  // rare: put the NaNs in
-        for (int x = 0; x < 128; ++x) {
-          const uint8_t code = from[row * 128 + (((x >> 4) ^ (row & 7)) << 4) + (x & 15)];
-          if ((code & 0x7Fu) == 0x7Fu) {
-            const int b = 2 * (x & 63);
-            *reinterpret_cast<uint16_t*>(to + (x >> 6) * C::BOX + row * 128 + (((b >> 4) ^ (row & 7)) << 4) + (b & 15)) =
-                0x7FC0u;
+#pragma unroll
+        for (int c = 0; c < 8; c += 4) {  // last 64, four chunks read before two of them are written
+          uint32_t hi[8], rest[8];
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            const uint4 u = *chunk(8 + c + d);
+            split_chunk(u, hi + 2 * d, rest + 2 * d);
+          }
+          *chunk(4 + c / 2) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *chunk(5 + c / 2) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+          if (c == 0) {  // chunks 8 .. 11 are read: the first values' rests; these rests wait in their place
+#pragma unroll
+            for (int d = 0; d < 4; ++d) *chunk(8 + d) = make_uint4(lo[4 * d], lo[4 * d + 1], lo[4 * d + 2], lo[4 * d + 3]);
+#pragma unroll
+            for (int d = 0; d < 8; ++d) lo[d] = rest[d];
+          } else {  // chunks 12 .. 15 are read
+            *chunk(12) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            *chunk(13) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+            *chunk(14) = make_uint4(rest[0], rest[1], rest[2], rest[3]);
+            *chunk(15) = make_uint4(rest[4], rest[5], rest[6], rest[7]);
           }
         }
-      }
-    };
-    int done = 0, nq = 0;  // tiles and query tiles so far
-    bool ok = true;
-    for (int r = 0; ok && item_here(r); ++r) {
-      const int n = items[r & 1].n_tiles, pair = items[r & 1].pair;
-      item_done(r);
-      if (n == 0) continue;
-      ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_full, nq & 1, p.err, kDevErrFullWait));
-      if (!ok) break;
-      float* qs = reinterpret_cast<float*>(smem + C::OFF_QS) + (nq & 1) * 2 * kRowsTile;
-      for (int k = 0; k <= pair; ++k) qs[k * kRowsTile + row] = split_q(smem + k * C::TILE);
-      fence_proxy_async_smem();
-      mbar_arrive(&bars->q8_full[nq & 1]);
-      ++nq;
-      for (int i = 0; i < n && ok; ++i, ++done) {
-        const int s = done % NST;
-        ok = mbar_wait(&bars->v8_full[s], (done / NST) & 1, p.err, kDevErrFullWait) &&
-             (done < NST || mbar_wait(&bars->v_empty[s], ((done / NST) - 1) & 1, p.err, kDevErrEmptyWait));
-        ok = __all_sync(0xffffffffu, ok);
+        // an infinity or a NaN in the row makes its scores NaN
+        return finite ? __uint_as_float(static_cast<uint32_t>(127 + e) << 23) : __int_as_float(0x7fc00000);
+      };
+      // One thread a token row: 16 codes of a 16-byte chunk become the 32 bytes of two chunks of
+      // the 128-byte-swizzled bf16 tile (both sides conflict-free: eight rows, eight chunks).
+      auto convert = [&](const uint8_t* from, uint8_t* to) {
+        uint32_t odd = 0u;  // bit 7 of a byte: a NaN code among the row's
+#pragma unroll 4
+        for (int c = 0; c < 8; ++c) {
+          const uint4 u = *reinterpret_cast<const uint4*>(from + row * 128 + ((c ^ (row & 7)) << 4));
+          uint8_t* d = to + (c >> 2) * C::BOX + row * 128;
+          const int d0 = 2 * (c & 3);
+          uint4 lo, hi;
+          e4m3x4_to_bf16(u.x, lo.x, lo.y, odd);
+          e4m3x4_to_bf16(u.y, lo.z, lo.w, odd);
+          e4m3x4_to_bf16(u.z, hi.x, hi.y, odd);
+          e4m3x4_to_bf16(u.w, hi.z, hi.w, odd);
+          *reinterpret_cast<uint4*>(d + ((d0 ^ (row & 7)) << 4)) = lo;
+          *reinterpret_cast<uint4*>(d + (((d0 + 1) ^ (row & 7)) << 4)) = hi;
+        }
+        if (odd & 0x80808080u) {  // rare: put the NaNs in
+          for (int x = 0; x < 128; ++x) {
+            const uint8_t code = from[row * 128 + (((x >> 4) ^ (row & 7)) << 4) + (x & 15)];
+            if ((code & 0x7Fu) == 0x7Fu) {
+              const int b = 2 * (x & 63);
+              *reinterpret_cast<uint16_t*>(to + (x >> 6) * C::BOX + row * 128 + (((b >> 4) ^ (row & 7)) << 4) + (b & 15)) =
+                  0x7FC0u;
+            }
+          }
+        }
+      };
+      int done = 0, nq = 0;  // tiles and query tiles so far
+      bool ok = true;
+      for (int r = 0; ok && item_here(r); ++r) {
+        const int n = items[r & 1].n_tiles, pair = items[r & 1].pair;
+        item_done(r);
+        if (n == 0) continue;
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_full, nq & 1, p.err, kDevErrFullWait));
         if (!ok) break;
-        convert(smem + C::OFF_V8 + s * C::LOAD, smem + C::OFF_V + s * C::TILE);
+        float* qs = reinterpret_cast<float*>(smem + C::OFF_QS) + (nq & 1) * 2 * kRowsTile;
+        for (int k = 0; k <= pair; ++k) qs[k * kRowsTile + row] = split_q(smem + k * C::TILE);
         fence_proxy_async_smem();
-        mbar_arrive(&bars->v_full[s]);
-        mbar_arrive(&bars->v8_empty[s]);
+        mbar_arrive(&bars->q8_full[nq & 1]);
+        ++nq;
+        for (int i = 0; i < n && ok; ++i, ++done) {
+          const int s = done % NST;
+          ok = mbar_wait(&bars->v8_full[s], (done / NST) & 1, p.err, kDevErrFullWait) &&
+               (done < NST || mbar_wait(&bars->v_empty[s], ((done / NST) - 1) & 1, p.err, kDevErrEmptyWait));
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          convert(smem + C::OFF_V8 + s * C::LOAD, smem + C::OFF_V + s * C::TILE);
+          fence_proxy_async_smem();
+          mbar_arrive(&bars->v_full[s]);
+          mbar_arrive(&bars->v8_empty[s]);
+        }
       }
-    }
     }
   } else {
     // ------------------------------------------------------------ softmax groups

@@ -12,11 +12,11 @@
 // Bound by HBM: each input is read once and each output written once.  A warp copies the heads by
 // bulk copies into a ring, 32 heads a stage, so that 40 KB a CTA are on their way whatever the
 // others wait for (heads loaded to registers ahead of their use: 68 us for 4096 tokens of
-// 128 + 16 heads, this way 58: 5.2 TB/s of the 6.8 that a copy reaches).  8 lanes take one head, as two chunks of d / 16 values
-// that the rotation pairs, so that it needs no exchange between lanes, the sum of squares is
-// three shuffles for four heads, and the arithmetic runs on packed pairs.  The chains token ->
-// sequence -> position -> page and table row of a CTA's tokens run side by side under the first
-// copies.
+// 128 + 16 heads, this way 58: 5.2 TB/s of the 6.8 that a copy reaches).  8 lanes take one head, as
+// two chunks of d / 16 values that the rotation pairs, so that it needs no exchange between lanes,
+// the sum of squares is three shuffles for four heads, and the arithmetic runs on packed pairs.
+// The chains token -> sequence -> position -> page and table row of a CTA's tokens run side by side
+// under the first copies.
 #include <cuda_runtime.h>
 
 #include <algorithm>
