@@ -77,7 +77,7 @@ struct TcCfg {
   static constexpr int OFF_V = OFF_K + NST * LOAD;
   static constexpr int OFF_V8 = OFF_V + NST * TILE;  // fp8: the V codes' ring
   static constexpr int OFF_BAR = OFF_V8 + (FP8 ? NST * LOAD : 0);
-  static constexpr int OFF_ML = OFF_BAR + 512;       // solo: group 1's (m, l) per row
+  static constexpr int OFF_ML = OFF_BAR + 768;       // solo: group 1's (m, l) per row
   static constexpr int OFF_ITEM = OFF_ML + kRowsTile * 8;
   static constexpr int OFF_QS = OFF_ITEM + 256;      // fp8: Q's row scales [item & 1][query tile][row]
   static constexpr int OFF_OUT = OFF_QS + (FP8 ? 4 * kRowsTile * 4 : 0);  // 64 bytes of each output row
@@ -353,6 +353,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     chunk_tc_kernel(const __grid_constant__ PartialParams p, const __grid_constant__ CUtensorMap tmq,
                     const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
   constexpr int D = C::D, NST = C::NST, NB = C::NB;
+  static_assert(sizeof(TcBars<C>) <= C::OFF_ML - C::OFF_BAR, "barriers");
+  static_assert(2 * sizeof(TcItem) <= C::OFF_QS - C::OFF_ITEM, "items");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   TcBars<C>* bars = reinterpret_cast<TcBars<C>*>(smem + C::OFF_BAR);
