@@ -31,9 +31,10 @@ namespace {
 constexpr int kWarps = 8;              // consumer warps
 constexpr int kThreads = kWarps * 32 + 32;
 constexpr int kGroups = kWarps * 4;    // heads of a stage
-constexpr int kStages = 5;               // 40 KB (static shared memory ends at 48)
+constexpr int kStages = 5;             // 40 KB for heads of 128
 constexpr int kCtas = 2 * 152;         // CTAs of a large call: two an SM
-constexpr int kMaxTokens = 64;         // tokens a CTA's run may touch
+constexpr int kMaxTokens = 64;         // tokens a CTA's run may touch: 8 a warp
+constexpr int kScaleHeads = 16;        // KV heads whose scales wait in shared memory
 
 // ---- two fp32 values in one 64-bit register (packed round-to-nearest operations)
 __device__ __forceinline__ uint64_t pack2(float x, float y) {
@@ -134,18 +135,15 @@ __device__ __forceinline__ void load_weight(const void* w, bool bf16, int64_t at
 }
 
 // Sequence of packed row `row`: the last b with cu_q[b] <= row, if row < cu_q[b + 1]; else -1.
-// Warp-collective: a 32-way search.
 __device__ __forceinline__ int sequence_of(const int32_t* cu_q, int B, int row) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, n = B;  // the answer lies in [lo, lo + n), or before lo = 0
-  while (true) {
-    const int step = (n + 31) / 32;
-    const bool before = lane * step < n && __ldg(cu_q + lo + lane * step) <= row;
-    const int hits = __popc(__ballot_sync(0xffffffffu, before));
-    if (hits == 0) return -1;  // before the first sequence
-    lo += (hits - 1) * step;
-    n = min(step, n - (hits - 1) * step);
-    if (step == 1) break;
+  if (__ldg(cu_q) > row) return -1;
+  int lo = 0;
+  for (int n = B; n > 1;) {
+    const int half = n >> 1;
+    if (__ldg(cu_q + lo + half) <= row)
+      lo += half, n -= half;
+    else
+      n = half;
   }
   return row < __ldg(cu_q + lo + 1) ? lo : -1;
 }
@@ -163,9 +161,13 @@ template <int D, bool FP8, bool INTER>
 __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int H = D / 16;  // values of a chunk
   constexpr uint32_t kRowBytes = D * 2;
-  __shared__ __align__(128) uint8_t ring[kStages][kGroups * kRowBytes];
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint8_t(*ring)[kGroups * kRowBytes] = reinterpret_cast<uint8_t(*)[kGroups * kRowBytes]>(smem);
   __shared__ uint64_t full[kStages], empty[kStages];
   __shared__ Place places[kMaxTokens];
+  // of each token of the run: its rows of cos and sin, then (fp8) the scales of its block
+  float* turns = reinterpret_cast<float*>(smem + kStages * kGroups * kRowBytes);
+  float* scales = turns + a.run_tokens * a.rot;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l8 = threadIdx.x & 7;
   const int n_heads = a.Hq + 2 * a.Hkv;  // queries, keys, values
   // this CTA's run of (token, head) pairs
@@ -228,28 +230,50 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
   const int c1 = INTER ? D / 2 + f : in_rot ? f + half : a.rot + (D - a.rot) / 2 + f - half;
   const bool turn0 = INTER ? c0 < a.rot : in_rot, turn1 = INTER ? c1 < a.rot : in_rot;
 
-  for (int i = warp; i < tokens; i += kWarps) {
-    const int row = t0 + i;
-    const int b = sequence_of(a.cu_q, a.B, row);
+  // Places: a lane for each token, so that the chains of loads of all tokens run side by side
+  {
+    const int i = warp + kWarps * lane, row = t0 + i;
+    const bool mine = lane < kMaxTokens / kWarps && i < tokens;
     Place pl;
-    pl.live = b >= 0;
     pl.page = pl.table = -1;
     pl.at = 0;
+    const int b = mine ? sequence_of(a.cu_q, a.B, row) : -1;
+    pl.live = b >= 0;
     if (b >= 0) {
       // place in the sequence
       const int64_t pos = static_cast<int64_t>(__ldg(a.seq_lens + b)) - __ldg(a.cu_q + b + 1) + row;
+      pl.table = a.positions ? __ldg(a.positions + row) : pos;
       if (pos >= 0 && pos < static_cast<int64_t>(a.max_blocks) * a.block_len) {
         const int block = static_cast<int>(pos) / a.block_len;  // the capacity is below 2^31
         pl.page = __ldg(a.block_table + static_cast<int64_t>(b) * a.max_blocks + block);
         pl.at = static_cast<int>(pos) - block * a.block_len;
         if (pl.page >= a.num_blocks) pl.page = -1;
       }
-      pl.table = a.positions ? __ldg(a.positions + row) : pos;
       if (pl.table >= a.max_pos) pl.table = -1;
-      if (a.rot > 0 && pl.table < 0 && lane == 0)
-        atomicOr(a.err + kErrCode, static_cast<unsigned int>(kDevErrPosition));
+      if (a.rot > 0 && pl.table < 0) atomicOr(a.err + kErrCode, static_cast<unsigned int>(kDevErrPosition));
     }
-    if (lane == 0) places[i] = pl;
+    if (mine) places[i] = pl;
+    // lanes 0 .. 15: the row of cos, 16 .. 31: of sin
+    const int n_mine = (tokens - warp + kWarps - 1) / kWarps, per = half >> 2, c4 = lane & 15;
+    const float* table = lane < 16 ? a.cos : a.sin;
+    const float nan = __int_as_float(0x7fc00000);
+#pragma unroll 4
+    for (int x = 0; x < n_mine; ++x) {
+      const int64_t at = __shfl_sync(0xffffffffu, pl.table, x);
+      const bool live = __shfl_sync(0xffffffffu, pl.live, x) != 0;
+      if (live && c4 < per) {
+        float4 u = make_float4(nan, nan, nan, nan);
+        if (at >= 0) u = __ldg(reinterpret_cast<const float4*>(table + at * half) + c4);
+        reinterpret_cast<float4*>(turns + (warp + kWarps * x) * a.rot + (lane >> 4) * half)[c4] = u;
+      }
+      if constexpr (FP8) {
+        const int64_t page = __shfl_sync(0xffffffffu, pl.page, x);
+        const int block = __shfl_sync(0xffffffffu, pl.at, x) / a.scale_block;
+        if (page >= 0 && a.Hkv <= kScaleHeads && c4 < a.Hkv)
+          scales[(warp + kWarps * x) * 2 * kScaleHeads + lane] =
+              __ldg((lane < 16 ? a.k_scale : a.v_scale) + (page * a.Hkv + c4) * (a.block_len / a.scale_block) + block);
+      }
+    }
   }
   asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");  // (the copying warp goes its own way)
 
@@ -276,27 +300,23 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
       have_t = t;
       pl = places[t];
       if ((turn0 || turn1) && pl.live) {
-        const float nan = __int_as_float(0x7fc00000);
-        const float* c = a.cos + pl.table * half;
-        const float* s = a.sin + pl.table * half;
+        const float* c = turns + t * a.rot;
+        const float* s = c + half;
         if constexpr (INTER) {
 #pragma unroll
           for (int j = 0; j < H; ++j) {
             const bool turn = j < H / 2 ? turn0 : turn1;
             const int at = (j < H / 2 ? c0 + 2 * j : c1 + 2 * (j - H / 2)) / 2;
             float x = 1.f, y = 0.f;
-            if (turn) x = pl.table >= 0 ? __ldg(c + at) : nan, y = pl.table >= 0 ? __ldg(s + at) : nan;
+            if (turn) x = c[at], y = s[at];
             cs[j] = pack2(x, x);
             sn[j] = pack2(-y, y);
           }
         } else {
 #pragma unroll
           for (int j = 0; j < H / 4; ++j) {
-            float4 x = make_float4(nan, nan, nan, nan), y = x;
-            if (pl.table >= 0) {
-              x = __ldg(reinterpret_cast<const float4*>(c + f + 4 * j));
-              y = __ldg(reinterpret_cast<const float4*>(s + f + 4 * j));
-            }
+            const float4 x = *reinterpret_cast<const float4*>(c + f + 4 * j);
+            const float4 y = *reinterpret_cast<const float4*>(s + f + 4 * j);
             cs[2 * j] = pack2(x.x, x.y);
             cs[2 * j + 1] = pack2(x.z, x.w);
             sn[2 * j] = pack2(y.x, y.y);
@@ -367,8 +387,12 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
       const int64_t to =
           pl.page * (is_v ? a.vp_sb : a.kp_sb) + g * (is_v ? a.vp_sh : a.kp_sh) + pl.at * (is_v ? a.vp_st : a.kp_st);
       if constexpr (FP8) {
-        const int per = a.block_len / a.scale_block;
-        const float scale = __ldg((is_v ? a.v_scale : a.k_scale) + (pl.page * a.Hkv + g) * per + pl.at / a.scale_block);
+        float scale;
+        if (a.Hkv <= kScaleHeads)
+          scale = scales[(2 * t + is_v) * kScaleHeads + g];
+        else
+          scale = __ldg((is_v ? a.v_scale : a.k_scale) + (pl.page * a.Hkv + g) * (a.block_len / a.scale_block) +
+                        pl.at / a.scale_block);
         uint8_t* o = static_cast<uint8_t*>(is_v ? a.v_pages : a.k_pages) + to;
         store_e4m3<H>(o + c0, x, scale);
         store_e4m3<H>(o + c1, x + H / 2, scale);
@@ -391,10 +415,24 @@ cudaError_t launch(AppendArgs a, cudaStream_t stream) {
   a.fused = a.q_sh == D && a.k_st == a.q_st && a.v_st == a.q_st && a.k_sh == D && a.v_sh == D && a.k == a.q + a.Hq * D &&
             a.v == a.k + a.Hkv * D;
   const unsigned int blocks = static_cast<unsigned int>((pairs + steps * kGroups - 1) / (steps * kGroups));
+  a.run_tokens = static_cast<int>((steps * kGroups + n_heads - 2) / n_heads + 1);
+  const auto bytes = [](int tokens, int rot) {
+    return kStages * kGroups * D * 2 + tokens * (rot + (FP8 ? 2 * kScaleHeads : 0)) * 4;
+  };
+  static std::atomic<uint64_t> attr_done{0};
+  cudaError_t e = once_per_device(attr_done, [&] {
+    cudaError_t x = cudaFuncSetAttribute(append_kernel<D, FP8, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         bytes(kMaxTokens, D));
+    if (x != cudaSuccess) return x;
+    return cudaFuncSetAttribute(append_kernel<D, FP8, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                bytes(kMaxTokens, D));
+  });
+  if (e != cudaSuccess) return e;
+  const size_t smem = bytes(a.run_tokens, a.rot);
   if (a.interleaved)
-    append_kernel<D, FP8, true><<<blocks, kThreads, 0, stream>>>(a);
+    append_kernel<D, FP8, true><<<blocks, kThreads, smem, stream>>>(a);
   else
-    append_kernel<D, FP8, false><<<blocks, kThreads, 0, stream>>>(a);
+    append_kernel<D, FP8, false><<<blocks, kThreads, smem, stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -199,7 +199,8 @@ struct AppendArgs {
   int32_t B, T, Hq, Hkv, rot, interleaved, weight_bf16;
   int32_t block_len, max_blocks, scale_block;
   int32_t steps;  // stages of 32 heads of a CTA's run, and whether a token's q, k and v heads lie in
-  int32_t fused;  //   a row in memory (the launcher's)
+  int32_t fused;  //   a row in memory; most tokens a run touches (the launcher sets them)
+  int32_t run_tokens;
   float eps;
   unsigned int* err;
 };
