@@ -12,11 +12,12 @@
 // Bound by HBM: each input is read once and each output written once.  A warp copies the heads by
 // bulk copies into a ring, 32 heads a stage, so that 40 KB a CTA are on their way whatever the
 // others wait for (heads loaded to registers ahead of their use: 68 us for 4096 tokens of
-// 128 + 16 heads, this way 58: 5.2 TB/s of the 6.8 that a copy reaches).  8 lanes take one head, as
+// 128 + 16 heads, this way 53: 5.7 TB/s of the 6.8 that a copy reaches).  8 lanes take one head, as
 // two chunks of d / 16 values that the rotation pairs, so that it needs no exchange between lanes,
 // the sum of squares is three shuffles for four heads, and the arithmetic runs on packed pairs.
-// The chains token -> sequence -> position -> page and table row of a CTA's tokens run side by side
-// under the first copies.
+// The chains token -> sequence -> position -> page and table row of all tokens of a CTA's run go
+// side by side, a lane each, under the first copies, and leave the run's rotations and scales in
+// shared memory (looked up by each head's lanes at a new token: 58 us).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -32,7 +33,10 @@ constexpr int kWarps = 8;              // consumer warps
 constexpr int kThreads = kWarps * 32 + 32;
 constexpr int kGroups = kWarps * 4;    // heads of a stage
 constexpr int kStages = 5;             // 40 KB for heads of 128
-constexpr int kCtas = 2 * 152;         // CTAs of a large call: two an SM
+// CTAs an SM.  bf16: two, a token's rotation held in registers while its heads pass (4096 tokens of
+// 128 + 16 heads 53 us; three CTAs that read it from shared memory for each head 56).  fp8: three,
+// whose warps hide the conversions (6800 tokens of 64 + 16 heads 62 us against 70).
+constexpr int ctas_per_sm(bool fp8) { return fp8 ? 3 : 2; }
 constexpr int kMaxTokens = 64;         // tokens a CTA's run may touch: 8 a warp
 constexpr int kScaleHeads = 16;        // KV heads whose scales wait in shared memory
 
@@ -158,16 +162,17 @@ struct Place {
 
 // INTER: pairs (2j, 2j + 1) instead of (j, j + rot / 2).
 template <int D, bool FP8, bool INTER>
-__global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(FP8)) append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int H = D / 16;  // values of a chunk
   constexpr uint32_t kRowBytes = D * 2;
+  constexpr bool kHoldTurns = !FP8;
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t(*ring)[kGroups * kRowBytes] = reinterpret_cast<uint8_t(*)[kGroups * kRowBytes]>(smem);
   __shared__ uint64_t full[kStages], empty[kStages];
   __shared__ Place places[kMaxTokens];
-  // of each token of the run: its rows of cos and sin, then (fp8) the scales of its block
+  // of each token of the run: its rows of cos, sin and -sin, then (fp8) the scales of its block
   float* turns = reinterpret_cast<float*>(smem + kStages * kGroups * kRowBytes);
-  float* scales = turns + a.run_tokens * a.rot;
+  float* scales = turns + a.run_tokens * 3 * (a.rot >> 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l8 = threadIdx.x & 7;
   const int n_heads = a.Hq + 2 * a.Hkv;  // queries, keys, values
   // this CTA's run of (token, head) pairs
@@ -264,7 +269,9 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
       if (live && c4 < per) {
         float4 u = make_float4(nan, nan, nan, nan);
         if (at >= 0) u = __ldg(reinterpret_cast<const float4*>(table + at * half) + c4);
-        reinterpret_cast<float4*>(turns + (warp + kWarps * x) * a.rot + (lane >> 4) * half)[c4] = u;
+        float4* to = reinterpret_cast<float4*>(turns + (warp + kWarps * x) * 3 * half) + c4;
+        to[(lane >> 4) * per] = u;
+        if (lane >= 16) to[2 * per] = make_float4(-u.x, -u.y, -u.z, -u.w);
       }
       if constexpr (FP8) {
         const int64_t page = __shfl_sync(0xffffffffu, pl.page, x);
@@ -279,11 +286,33 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
 
   Place pl;
   pl.live = 0;
-  int have_t = -1, have_w = -1;  // token of the place and rotation, kind of the weights held
+  int have_t = -1, have_w = -1;  // token of the place, kind of the weights held
   // halves: cs, sn, -sn of the chunk's values; interleaved: (c, c) and (-s, s) of its pairs
-  uint64_t cs[H], sn[H], wt[H];
+  uint64_t held_c[H], held_s[H], wt[H];
 #pragma unroll
-  for (int j = 0; j < H; ++j) cs[j] = sn[j] = wt[j] = 0ull;
+  for (int j = 0; j < H; ++j) held_c[j] = held_s[j] = wt[j] = 0ull;
+  auto load_turns = [&](uint64_t(&cs)[H], uint64_t(&sn)[H]) {
+    const float* c = turns + t * 3 * half;  // cos, sin, -sin
+    if constexpr (INTER) {
+#pragma unroll
+      for (int j = 0; j < H; ++j)
+        if (j < H / 2 ? turn0 : turn1) {
+          const float* at = c + (j < H / 2 ? c0 + 2 * j : c1 + 2 * (j - H / 2)) / 2;
+          cs[j] = pack2(at[0], at[0]);
+          sn[j] = pack2(at[2 * half], at[half]);
+        }
+    } else if (turn0) {
+#pragma unroll
+      for (int j = 0; j < H / 2; j += 2) {
+        const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(c + f + 2 * j);
+        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(c + half + f + 2 * j);
+        const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(c + 2 * half + f + 2 * j);
+        cs[j] = u.x, cs[j + 1] = u.y;
+        sn[j] = v.x, sn[j + 1] = v.y;
+        sn[H / 2 + j] = w.x, sn[H / 2 + j + 1] = w.y;
+      }
+    }
+  };
   for (int n = 0; n < steps; ++n, advance()) {
     const int s = n % kStages;
     if (!__all_sync(0xffffffffu, mbar_wait(&full[s], (n / kStages) & 1, a.err, kDevErrFullWait))) break;
@@ -299,33 +328,8 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
     if (here && t != have_t) {  // a new token
       have_t = t;
       pl = places[t];
-      if ((turn0 || turn1) && pl.live) {
-        const float* c = turns + t * a.rot;
-        const float* s = c + half;
-        if constexpr (INTER) {
-#pragma unroll
-          for (int j = 0; j < H; ++j) {
-            const bool turn = j < H / 2 ? turn0 : turn1;
-            const int at = (j < H / 2 ? c0 + 2 * j : c1 + 2 * (j - H / 2)) / 2;
-            float x = 1.f, y = 0.f;
-            if (turn) x = c[at], y = s[at];
-            cs[j] = pack2(x, x);
-            sn[j] = pack2(-y, y);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < H / 4; ++j) {
-            const float4 x = *reinterpret_cast<const float4*>(c + f + 4 * j);
-            const float4 y = *reinterpret_cast<const float4*>(s + f + 4 * j);
-            cs[2 * j] = pack2(x.x, x.y);
-            cs[2 * j + 1] = pack2(x.z, x.w);
-            sn[2 * j] = pack2(y.x, y.y);
-            sn[2 * j + 1] = pack2(y.z, y.w);
-            sn[H / 2 + 2 * j] = pack2(-y.x, -y.y);
-            sn[H / 2 + 2 * j + 1] = pack2(-y.z, -y.w);
-          }
-        }
-      }
+      if constexpr (kHoldTurns)
+        if (pl.live) load_turns(held_c, held_s);
     }
     const bool is_q = h < a.Hq, is_v = h >= a.Hq + a.Hkv;
     uint64_t x[H];  // chunk 0, chunk 1
@@ -354,17 +358,26 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
 #pragma unroll
         for (int j = 0; j < H; ++j) x[j] = mul2(x[j], wt[j]);
       }
-      if constexpr (INTER) {
+      auto rotate = [&](const uint64_t(&cs)[H], const uint64_t(&sn)[H]) {
+        if constexpr (INTER) {
 #pragma unroll
-        for (int j = 0; j < H; ++j)
-          if (j < H / 2 ? turn0 : turn1) x[j] = fma2(x[j], cs[j], mul2(swap2(x[j]), sn[j]));
-      } else if (turn0) {
+          for (int j = 0; j < H; ++j)
+            if (j < H / 2 ? turn0 : turn1) x[j] = fma2(x[j], cs[j], mul2(swap2(x[j]), sn[j]));
+        } else if (turn0) {
 #pragma unroll
-        for (int j = 0; j < H / 2; ++j) {
-          const uint64_t u = x[j], v = x[H / 2 + j];
-          x[j] = fma2(u, cs[j], mul2(v, sn[H / 2 + j]));
-          x[H / 2 + j] = fma2(v, cs[j], mul2(u, sn[j]));
+          for (int j = 0; j < H / 2; ++j) {
+            const uint64_t u = x[j], v = x[H / 2 + j];
+            x[j] = fma2(u, cs[j], mul2(v, sn[H / 2 + j]));
+            x[H / 2 + j] = fma2(v, cs[j], mul2(u, sn[j]));
+          }
         }
+      };
+      if constexpr (kHoldTurns) {
+        rotate(held_c, held_s);
+      } else {
+        uint64_t cs[H], sn[H];
+        load_turns(cs, sn);
+        rotate(cs, sn);
       }
       const uint64_t inv2 = pack2(inv, inv);
 #pragma unroll
@@ -408,8 +421,9 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
 template <int D, bool FP8>
 cudaError_t launch(AppendArgs a, cudaStream_t stream) {
   const int64_t n_heads = a.Hq + 2 * a.Hkv, pairs = a.T * n_heads;
-  // equal runs for two CTAs an SM, of one stage at least; a run touches kMaxTokens tokens at most
-  int64_t steps = (pairs + kGroups * kCtas - 1) / (kGroups * kCtas);
+  // equal runs for the CTAs that are resident at once, of one stage at least; a run touches kMaxTokens tokens at most
+  constexpr int64_t kRuns = 152 * ctas_per_sm(FP8);
+  int64_t steps = (pairs + kGroups * kRuns - 1) / (kGroups * kRuns);
   steps = std::min<int64_t>(steps, std::max<int64_t>(1, (kMaxTokens - 2) * n_heads / kGroups));
   a.steps = static_cast<int>(steps);
   a.fused = a.q_sh == D && a.k_st == a.q_st && a.v_st == a.q_st && a.k_sh == D && a.v_sh == D && a.k == a.q + a.Hq * D &&
@@ -417,7 +431,7 @@ cudaError_t launch(AppendArgs a, cudaStream_t stream) {
   const unsigned int blocks = static_cast<unsigned int>((pairs + steps * kGroups - 1) / (steps * kGroups));
   a.run_tokens = static_cast<int>((steps * kGroups + n_heads - 2) / n_heads + 1);
   const auto bytes = [](int tokens, int rot) {
-    return kStages * kGroups * D * 2 + tokens * (rot + (FP8 ? 2 * kScaleHeads : 0)) * 4;
+    return kStages * kGroups * D * 2 + tokens * (rot / 2 * 3 + (FP8 ? 2 * kScaleHeads : 0)) * 4;
   };
   static std::atomic<uint64_t> attr_done{0};
   cudaError_t e = once_per_device(attr_done, [&] {
