@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   TcBars<C>* bars = reinterpret_cast<TcBars<C>*>(smem + C::OFF_BAR);
   TcItem* items = reinterpret_cast<TcItem*>(smem + C::OFF_ITEM);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int G = p.ck.G, Gr = p.ck.group_rows;
+  const int G = p.ck.G, Gr = p.ck.group_rows, gr_bits = 31 - __clz(Gr);  // (Gr is a power of two)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           const int m_last = min(t.m0 + 2 * kRowsTile, t.it.n * Gr) - 1;
           t.pair = m_last - t.m0 >= kRowsTile ? 1 : 0;
           const int pos0 = t.it.m - t.it.n;
-          t.tl = chunk_tiles(p.ck.window, p.ck.n_sink, p.ck.cap, pos0 + t.m0 / Gr, pos0 + m_last / Gr);
+          t.tl = chunk_tiles(p.ck.window, p.ck.n_sink, p.ck.cap, pos0 + (t.m0 >> gr_bits), pos0 + (m_last >> gr_bits));
           const int tiles = (t.tl.n + 1) / 2, per = (tiles + t.it.n_chunk - 1) / t.it.n_chunk;
           const int i0 = min(t.it.c * per, tiles);
           t.h0 = 2 * i0;
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             for (int k = 0; k <= t.pair; ++k)
               for (int bx = 0; bx < NB; ++bx)
                 tma_4d(smem + k * C::TILE + bx * C::BOX, &tmq, &bars->q_full, bx * 64, t.it.g * G,
-                       t.it.row0 + (t.m0 + k * kRowsTile) / Gr, 0);
+                       t.it.row0 + ((t.m0 + k * kRowsTile) >> gr_bits), 0);
           }
           __syncwarp();
           ++nq;
@@ -885,7 +885,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       int hi_min, lo_max, sink_min;  // a tile in [lo_max, hi_min) (or below sink_min) every row sees
       {
         const int m = t.m0 + (pair ? k * kRowsTile : 0) + row;
-        const int t_q = m / Gr, hg = m % Gr;
+        const int t_q = m >> gr_bits, hg = m & (Gr - 1);
         const bool valid = m < t.it.n * Gr && hg < G;
         const int pos = t.it.m - t.it.n + t_q;
         // visible tokens of this row: [lo_row, hi_row) and [0, sink_row)
@@ -1040,7 +1040,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const bool direct = t.it.n_chunk == 1;
       const bool valid = mine->w != 0;
       const int m = t.m0 + (pair ? k * kRowsTile : 0) + row;
-      const int t_q = m / Gr, h = t.it.g * G + m % Gr;
+      const int t_q = m >> gr_bits, h = t.it.g * G + (m & (Gr - 1));
       const int64_t orow = direct ? (static_cast<int64_t>(t.it.row0) + t_q) * p.Hq + h
                                   : t.it.part_row + (static_cast<int64_t>(t.it.c) * t.it.n + t_q) * p.Hq + h;
       // an empty partial's o is never read
