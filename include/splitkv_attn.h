@@ -408,8 +408,11 @@ skv_status gqa_decode_attn_passq(const skv_desc* desc, int32_t n_ranks, const vo
  * desc->max_q_len bounds the sequences' new tokens (0: T): it chooses the kernel, the result
  * does not depend on it.  Shapes: bf16 pages with d = 64 or 128, fp8-e4m3 pages with d = 128; any
  * Hq multiple of Hkv.  A value that no row of a 64- or 128-token tile sees never counts, whatever
- * it holds; a NaN or infinity in a V row that one row of a row tile sees may also reach the rows
- * of that row tile that do not see it.
+ * it holds; a NaN or infinity in a V row, or in the scales of a block, that one row of a row tile
+ * sees may also reach the rows of that row tile that do not see it.
+ * Rounding: scores, sums and the weighted sum in fp32; the softmax weights once, to bf16 (fp8
+ * pages: weight times V scale, to bf16, or with few rows to fp16), the output to bf16.  fp8 codes
+ * are exact; of q what lies below 2^-18 of its row's largest magnitude may be lost with fp8 pages.
  * Errors: SKV_EINVAL, SKV_EUNSUPPORTED and SKV_EWORKSPACE as for gqa_decode_attn_paged, and
  * SKV_EINVAL for a softmax_scale that is not positive, a negative window or n_sink, and n_sink
  * without a window.  T = 0 does nothing.

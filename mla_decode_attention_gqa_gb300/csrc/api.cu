@@ -1045,6 +1045,8 @@ skv_status chunk_desc(const skv_chunk_desc* c, const skv_paged* pg, skv_desc* d)
   }
   skv_status st = validate(d, 1);
   if (st != SKV_OK) return st;
+  // (the kernels count in 32 bits up to a tile past the last token)
+  if (d->S_max > (int64_t(1) << 31) - 4096) return fail(SKV_EINVAL, "max_blocks * block_len is too large");
   // a tensor map has no broadcast dimension, and a page that every entry shares cannot be written
   if ((c->T > 1 && c->q_strides[0] == 0) || (c->Hq > 1 && c->q_strides[1] == 0))
     return fail(SKV_EINVAL, "q strides must be positive");

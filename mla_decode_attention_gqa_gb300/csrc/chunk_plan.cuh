@@ -40,7 +40,7 @@ __device__ __forceinline__ void chunk_lengths(const ChunkArgs& a, int b, int* ro
   const int lo = min(max(__ldg(a.cu_q + b), 0), a.T), hi = min(max(__ldg(a.cu_q + b + 1), 0), a.T);
   *row0 = lo;
   *n = max(hi - lo, 0);
-  *m = __ldg(a.seq_lens + b);
+  *m = max(__ldg(a.seq_lens + b), 0);
 }
 
 // Blocks of kTileN tokens seen by the rows at positions [p0, p1] of a sequence with `cap` tokens

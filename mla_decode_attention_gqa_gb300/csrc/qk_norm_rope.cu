@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(FP8)) append_kernel(cons
     pl.live = b >= 0;
     if (b >= 0) {
       // place in the sequence
-      const int64_t pos = static_cast<int64_t>(__ldg(a.seq_lens + b)) - __ldg(a.cu_q + b + 1) + row;
+      const int64_t pos = static_cast<int64_t>(max(__ldg(a.seq_lens + b), 0)) - min(__ldg(a.cu_q + b + 1), a.T) + row;
       pl.table = a.positions ? __ldg(a.positions + row) : pos;
       if (pos >= 0 && pos < static_cast<int64_t>(a.max_blocks) * a.block_len) {
         const int block = static_cast<int>(pos) / a.block_len;  // the capacity is below 2^31

@@ -119,7 +119,8 @@ def test_bad_append_descriptions(kw, status):
 
 
 @pytest.mark.parametrize("kw", [dict(block_len=0), dict(block_len=96), dict(max_blocks=0), dict(num_blocks=0),
-                                dict(block_table=None), dict(block_table=0x10002), dict(max_blocks=2 ** 26)])
+                                dict(block_table=None), dict(block_table=0x10002), dict(max_blocks=2 ** 26),
+                                dict(max_blocks=2 ** 25 - 1)])  # a tile past the last token leaves 32 bits
 def test_bad_pages(kw):
     assert _call_chunk(_chunk(), _paged(**kw)) == skv.SKV_EINVAL
     assert _call_append(_append(), _paged(**kw)) == skv.SKV_EINVAL

@@ -158,6 +158,31 @@ def test_rows_of_no_sequence_are_left_alone():
     assert (out[:1] == 7).all() and (out[23:] == 7).all()
 
 
+def test_rows_past_the_batch_are_clipped():
+    """A last sequence said to reach past the packed rows has those that exist, in both calls."""
+    n, m, Hq, Hkv, d = [3, 6], [90, 130], 8, 2, 128
+    c = make(n, m, Hq, Hkv, d, seed=13)
+    far = dict(c, k_pages=c["k_pages"].clone(), v_pages=c["v_pages"].clone(), cu_q=c["cu_q"].clone())
+    far["cu_q"][-1] += 7
+    want, got = append(c, Hq, Hkv), append(far, Hq, Hkv)
+    assert torch.equal(got, want)
+    assert torch.equal(far["k_pages"], c["k_pages"]) and torch.equal(far["v_pages"], c["v_pages"])
+    for x in (0, 1):  # either kernel
+        a, b = (skv.attn_chunk_paged(want, y["k_pages"], y["v_pages"], y["seq_lens"], y["cu_q"], y["block_table"],
+                                     max_q_len=x) for y in (c, far))
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("kind,d", TYPES)
+@pytest.mark.parametrize("n,m,Hq,Hkv", [
+    ([1500, 0, 700], [1500, 3, 900], 1, 1),    # as many tokens a CTA as there can be
+    ([2, 5, 1], [2, 64, 129], 40, 20),         # more KV heads than have their scales looked up early
+    ([0, 1, 0, 2] * 80, [3, 70, 0, 2] * 80, 4, 2),
+])
+def test_head_counts_and_batches(kind, d, n, m, Hq, Hkv):
+    go(make(n, m, Hq, Hkv, d, fp8=kind == "fp8", seed=14), Hq, Hkv)
+
+
 def test_in_place_and_strided_outputs():
     c = make(N, M, 8, 2, 128, seed=9)
     want = append(c, 8, 2)
