@@ -1079,14 +1079,15 @@ skv_status chunk_plan(const skv_chunk_desc* c, const skv_desc* d, ChunkPlan* pl)
   const int G = d->Hq / d->Hkv;
   // The caller's bound on the chunk lengths chooses the kernel (results do not depend on it): up
   // to 16 rows of a KV head fill an mma.sync tile, where the tensor cores' 128 are mostly padding
-  // (decode of 64 sequences, 64 / 8 heads: 377 us against 457, fp8 224 against 491); a group above
+  // (decode of 64 sequences, 64 / 8 heads: 377 us against 457, fp8 224 against 491), up to 32 two
+  // (24 sequences of 5 rows, 40 / 8 heads: 93 us against 115, fp8 92 against 154); a group above
   // 128 heads has no query tile there.
   const int64_t longest = c->max_q_len > 0 ? std::min(c->max_q_len, c->T) : c->T;
-  pl->tc = longest * G > 16 && G <= 128;
+  pl->tc = longest * G > 32 && G <= 128;
   pl->group_rows = pl->tc ? padded_group(G) : G;
-  pl->rows = pl->tc ? chunk_tc_rows() : chunk_rows_per_tile();
+  pl->rows = pl->tc ? chunk_tc_rows() : longest * G <= 16 ? 16 : 32;
   pl->tile = pl->tc ? chunk_tc_kv_tile() : kTileN;
-  pl->n_wave = static_cast<int64_t>(device_sm_count()) * (pl->tc ? 1 : chunk_rows_ctas_per_sm());
+  pl->n_wave = static_cast<int64_t>(device_sm_count()) * (pl->tc ? 1 : chunk_rows_ctas_per_sm(pl->rows));
   pl->n_target = 4 * pl->n_wave;
   const int64_t rows = static_cast<int64_t>(c->T) * pl->group_rows;
   if (rows + pl->rows >= (int64_t(1) << 31)) return fail(SKV_EINVAL, "T * Hq / Hkv is too large for one call");
@@ -1157,6 +1158,8 @@ skv_status attn_chunk_paged(const skv_chunk_desc* desc, const skv_paged* paged, 
   p.ck.tile = pl.tile;
   p.ck.n_wave = static_cast<int32_t>(pl.n_wave);
   p.ck.n_target = static_cast<int32_t>(pl.n_target);
+  // (with one KV tile at most no item is ever cut, and nothing merged)
+  p.ck.start = d.S_max <= pl.tile ? 0 : kChunkStart * (d.dk == 64 || d.kv_dtype == SKV_KV_FP8_E4M3 ? 2 : 1);
   p.ck.plan = reinterpret_cast<int32_t*>(ws);
   p.ck.out = out;
   p.ck.lse = lse;

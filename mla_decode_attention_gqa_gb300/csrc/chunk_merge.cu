@@ -189,18 +189,16 @@ __global__ void __launch_bounds__(32 * kRowsPerBlock)
   ChunkShare sh;
   // (reads lengths only: under the attention kernel's end)
   const bool any = chunk_find_runs<32 * kRowsPerBlock>(a, a.n_wave, c, &runs, &sh);
-  int tile = 0;
-  const int64_t item = any ? runs.seek(a, &tile) : 0;
+  const int tile = any ? runs.s : 0;
   // the attention kernel before it on the stream is complete and its writes are visible (also where
   // there is nothing to do: what comes after this grid may rely on both)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (tile == 0) return;
-  const int64_t u0 = runs.u - tile;  // the item's first tile
+  const int64_t u0 = sh.start(c) - tile;  // the item's first tile
   const int c0 = sh.owner(u0), c1 = sh.owner(u0 + runs.kt - 1);
   const int k = c1 - c0 + 1, borders = c1 - c0, mine = c - c0 - 1;
   const int first = sh.start(c0) == u0 ? 2 * c0 : 2 * c0 + 1;  // c0's run begins with the item, or ends in it
-  const int mt = runs.rt - 1 - static_cast<int>(item / a.Hkv), g = static_cast<int>(item % a.Hkv);
-  const int m0 = mt * a.rows, rows = min(a.rows, runs.n * a.G - m0);
+  const int g = runs.g, m0 = runs.mt * a.rows, rows = min(a.rows, runs.n * a.G - m0);
   auto out_row = [&](int r) -> int64_t {
     const int m = m0 + r;
     return (static_cast<int64_t>(runs.row0) + m / a.G) * (a.Hkv * a.G) + g * a.G + m % a.G;

@@ -210,7 +210,9 @@ __device__ __forceinline__ ChunkItem chunk_item_at(const ChunkArgs& a, int idx) 
 }
 
 // ---- equal runs (the kernel for few rows): all items' KV tiles in one line -- sequence after
-// sequence, in each the items (row tile, KV head), in each its tiles -- cut into n equal runs.
+// sequence, in each the items (row tile, KV head), in each its tiles -- cut into n equal runs.  An
+// item counts `start` tiles more than it has, ahead of them: what its rows' loads and the
+// join of the warps take (without, a CTA with many short items took half as long again).
 
 // How U tiles are shared by n CTAs: the first r take q + 1, the others q.
 struct ChunkShare {
@@ -236,41 +238,51 @@ struct ChunkPiece {
   }
 };
 
-// A CTA's run, piece by piece.
+// A CTA's run, piece by piece.  (The divisions are done once, by find: a piece begins where the one
+// before ends.)
 struct ChunkRuns {
-  int64_t u, end;  // tiles left
-  int64_t first;   // first tile of sequence b
-  int cta, b, row0, n, m, rt, kt;
+  int64_t left;  // tiles left
+  int cta, b, row0, n, m, rt, kt;  // kt: with the start
+  int g, mt, s;  // the next piece's item, and its first tile there
   bool head;
   __device__ __forceinline__ void load(const ChunkArgs& a) {
     chunk_lengths(a, b, &row0, &n, &m);
     chunk_extent(a, n, m, &rt, &kt);
+    kt += a.start;
   }
-  // u's sequence, item and tile in it
-  __device__ __forceinline__ int64_t seek(const ChunkArgs& a, int* tile) {
-    while (u - first >= static_cast<int64_t>(rt) * a.Hkv * kt) {  // (u < end: there is such a sequence)
-      first += static_cast<int64_t>(rt) * a.Hkv * kt;
-      ++b;
-      load(a);
-    }
-    *tile = static_cast<int>((u - first) % kt);
-    return (u - first) / kt;
+  // Tiles [at, at + count) of those from sequence `seq` on (which holds the first of them).
+  __device__ __forceinline__ void find(const ChunkArgs& a, int c, int seq, int64_t at, int64_t count) {
+    cta = c;
+    b = seq;
+    left = count;
+    head = true;
+    load(a);
+    const int64_t item = at / kt;
+    s = static_cast<int>(at - item * kt);
+    const int r = static_cast<int>(item / a.Hkv);
+    g = static_cast<int>(item - static_cast<int64_t>(r) * a.Hkv);
+    mt = rt - 1 - r;
   }
   __device__ __forceinline__ bool next(const ChunkArgs& a, ChunkPiece* pc) {
-    if (u >= end) return false;
-    int s;
-    const int64_t item = seek(a, &s);
-    const int e = static_cast<int>(min(static_cast<int64_t>(kt), s + (end - u)));
+    if (left <= 0) return false;
+    while (mt < 0) {  // (tiles are left: there is such a sequence)
+      ++b;
+      load(a);
+      mt = rt - 1;
+    }
+    const int e = static_cast<int>(min(static_cast<int64_t>(kt), s + left));
     pc->b = b, pc->row0 = row0, pc->n = n, pc->m = m;
-    pc->mt = rt - 1 - static_cast<int>(item / a.Hkv);
-    pc->g = static_cast<int>(item % a.Hkv);
-    const int m0 = pc->mt * a.rows, m_last = min(m0 + a.rows, n * a.group_rows) - 1;
+    pc->mt = mt;
+    pc->g = g;
+    const int m0 = mt * a.rows, m_last = min(m0 + a.rows, n * a.group_rows) - 1;
     pc->tl = chunk_tiles(a.window, a.n_sink, a.cap, m - n + m0 / a.group_rows, m - n + m_last / a.group_rows);
-    pc->i0 = min(s, pc->tl.n);
-    pc->n_tiles = min(e, pc->tl.n) - pc->i0;  // (an earlier row tile may see fewer than kt)
+    pc->i0 = min(max(s - a.start, 0), pc->tl.n);
+    pc->n_tiles = min(max(e - a.start, 0), pc->tl.n) - pc->i0;  // (an earlier row tile may see fewer than kt)
     pc->slot = (s == 0 && e == kt) ? -1 : 2 * cta + (head ? 0 : 1);
     head = false;
-    u += e - s;
+    left -= e - s;
+    s = 0;
+    if (++g == a.Hkv) g = 0, --mt;
     return true;
   }
 };
@@ -288,7 +300,7 @@ __device__ __forceinline__ bool chunk_find_runs(const ChunkArgs& a, int n_cta, i
     int row0, n, m, rt, kt;
     chunk_lengths(a, b, &row0, &n, &m);
     chunk_extent(a, n, m, &rt, &kt);
-    w += static_cast<int64_t>(rt) * a.Hkv * kt;
+    w += static_cast<int64_t>(rt) * a.Hkv * (kt + a.start);
   }
   chunk_block_scan<NT>(w, zero, &total, &unused, sm_scan);
   ChunkShare sh;
@@ -306,7 +318,7 @@ __device__ __forceinline__ bool chunk_find_runs(const ChunkArgs& a, int n_cta, i
       chunk_lengths(a, b, &row0, &n, &m);
       chunk_extent(a, n, m, &rt, &kt);
     }
-    const int64_t mine = static_cast<int64_t>(rt) * a.Hkv * kt;
+    const int64_t mine = static_cast<int64_t>(rt) * a.Hkv * (kt + a.start);
     int64_t x = mine, y = 0, tx, ty;
     chunk_block_scan<NT>(x, y, &tx, &ty, sm_scan);
     const int64_t first = before + x - mine;
@@ -317,13 +329,7 @@ __device__ __forceinline__ bool chunk_find_runs(const ChunkArgs& a, int n_cta, i
     before += tx;
   }
   __syncthreads();
-  runs->u = u;
-  runs->end = sh.start(cta + 1);
-  runs->first = sm_first;
-  runs->cta = cta;
-  runs->b = sm_b;
-  runs->head = true;
-  runs->load(a);
+  runs->find(a, cta, sm_b, u - sm_first, sh.start(cta + 1) - u);
   return true;
 }
 

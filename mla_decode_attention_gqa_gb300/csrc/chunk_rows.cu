@@ -1,6 +1,6 @@
 // Attention of few new tokens over a paged cache (attn_chunk_paged): decode steps and proposed
-// tokens, 16 rows (new token, head of the group) of a KV head at a time, causal or with a sliding
-// window and sinks; bf16 pages, or fp8-e4m3 pages with block scales.
+// tokens, 16 or 32 rows (new token, head of the group) of a KV head at a time, causal or with a
+// sliding window and sinks; bf16 pages, or fp8-e4m3 pages with block scales.
 //
 // For every row (new token at position p, query head h of KV head g): s_u = scale q.k_u over the
 // visible tokens u (u <= p and u > p - window or u < n_sink), out = softmax(s) V, lse = ln sum e^s,
@@ -8,14 +8,16 @@
 // product with V: to bf16 (2^-8 of each weight), or times the V block scale to fp16 (2^-11).
 //
 // Bound by HBM: each K/V byte is read once for the whole group.  A warp loads K and V tiles of 64
-// tokens by TMA into a ring; 3 or 4 warps take the tiles in turn (16 x 64 scores on mma.sync
-// tiles: tcgen05's 128 rows would be mostly padding) and join their (m, l, O) at the end.
+// tokens by TMA into a ring; 3 to 5 warps take the tiles in turn (16 x 64 scores on mma.sync
+// tiles: tcgen05's 128 rows would be mostly padding) and join their (m, l, O) at the end.  For 17 to
+// 32 rows a second set of warps takes the same tiles for the other 16: one CTA an SM with twice the
+// ring, where two row tiles would read the pages twice.
 //
 // Work: the KV tiles of all items (sequence, row tile, KV head) in one line, cut into as many equal
-// runs as CTAs are resident, two an SM: every CTA streams the same number of tiles and starts
-// once, where chunks of equal length per sequence left a part of a wave empty and started four
-// times (decode of 64 sequences of 4096 to 16384 tokens, 64 / 8 heads: 404 us, in equal runs 377 us: the
-// rate of a plain copy).
+// runs as CTAs are resident: every CTA streams the same number of tiles (an item's start counted as
+// some, kChunkStart) and starts once, where chunks of equal length per sequence left a part of a
+// wave empty and started four times (decode of 64 sequences of 4096 to 16384 tokens, 64 / 8 heads:
+// 404 us, in equal runs 374: the rate of a plain copy).
 // A run may begin and end inside an item: those two pieces go out as partial rows, at most
 // two a CTA, which chunk_runs_merge joins; the items between are final.
 #include <cuda_runtime.h>
@@ -28,13 +30,16 @@ namespace skv {
 
 namespace {
 
-constexpr int kRows = 16;
+constexpr int kRows = 16;  // rows of a warp
 
-template <bool FP8_, int D_, int WN_, int NSTAGE_>
+template <bool FP8_, int D_, int WM_, int WN_, int NSTAGE_>
 struct RowsCfg {
   static constexpr bool FP8 = FP8_;
   static constexpr int D = D_;
-  static constexpr int WN = WN_;          // consumer warps
+  static constexpr int WM = WM_;          // sets of 16 rows, which share the tiles
+  static constexpr int WN = WN_;          // consumer warps of a set
+  static constexpr int ROWS = WM * kRows;
+  static constexpr int CTAS = WM == 1 ? 2 : 1;  // an SM
   static constexpr int NSTAGE = NSTAGE_;  // tiles in the ring
   static constexpr int TN = kTileN;
   static constexpr int ESZ = FP8 ? 1 : 2;
@@ -43,19 +48,19 @@ struct RowsCfg {
   static constexpr int BOX_BYTES = TN * 128;
   static constexpr int TILE = NBOX * BOX_BYTES;
   static constexpr int STAGE = 2 * TILE;
-  static constexpr int THREADS = (WN + 1) * 32;
-  // Full barriers are per consumer warp, DW of them each: a warp's wait is then always for the
+  static constexpr int THREADS = (WM * WN + 1) * 32;
+  // Full barriers are per consumer warp (of each set), DW of them each: a warp's wait is then always for the
   // phase after the one it saw last, whatever the other warps' tiles do
   static constexpr int DW = (NSTAGE + WN - 1) / WN;
   static constexpr int NFULL = WN * DW;
-  static constexpr int OFF_O = NSTAGE * STAGE;                 // one warp's O, to be joined
-  static constexpr int OFF_ML = OFF_O + kRows * D * 4;         // (m, l) of each warp's rows
-  static constexpr int OFF_QF = OFF_ML + WN * kRows * 2 * 4;   // fp8: q fragments
-  static constexpr int OFF_BAR = OFF_QF + (FP8 ? (D / 16) * 32 * 16 : 0);
+  static constexpr int OFF_O = NSTAGE * STAGE;                 // one warp's O of each set, to be joined
+  static constexpr int OFF_ML = OFF_O + ROWS * D * 4;          // (m, l) of each warp's rows
+  static constexpr int OFF_QF = OFF_ML + WN * ROWS * 2 * 4;    // fp8: q fragments
+  static constexpr int OFF_BAR = OFF_QF + (FP8 ? WM * (D / 16) * 32 * 16 : 0);
   static constexpr int OFF_RUN = OFF_BAR + 256;                // each consumer warp's run and piece
-  static constexpr int SMEM = 1024 + OFF_RUN + WN * 192;
-  static_assert((NFULL + NSTAGE) * 8 + 8 <= 256, "barriers and the q scale");
-  static_assert(2 * (SMEM + 1536) <= 227 * 1024, "two CTAs an SM");
+  static constexpr int SMEM = 1024 + OFF_RUN + WM * WN * 192;
+  static_assert((NFULL + NSTAGE) * 8 + WM * 4 <= 256, "barriers and the q scales");
+  static_assert(CTAS * (SMEM + 1536) <= 227 * 1024, "CTAs an SM");
 };
 
 template <class C>
@@ -74,12 +79,15 @@ __device__ __forceinline__ uint32_t half_mask(bool lo, bool hi) {
   return (lo ? 0x0000FFFFu : 0u) | (hi ? 0xFFFF0000u : 0u);
 }
 template <class C>
-__device__ __forceinline__ void consumers_sync() {
-  asm volatile("bar.sync 1, %0;" ::"n"(C::WN * 32) : "memory");
+__device__ __forceinline__ void consumers_sync(int set) {  // the consumer warps of a set
+  if (C::WM == 1 || set == 0)
+    asm volatile("bar.sync 1, %0;" ::"n"(C::WN * 32) : "memory");
+  else
+    asm volatile("bar.sync 2, %0;" ::"n"(C::WN * 32) : "memory");
 }
 
 template <class C>
-__global__ void __launch_bounds__(C::THREADS, 2)
+__global__ void __launch_bounds__(C::THREADS, C::CTAS)
     chunk_rows_kernel(const __grid_constant__ PartialParams p, const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv) {
   constexpr int D = C::D, TN = C::TN, NSTAGE = C::NSTAGE, WN = C::WN;
@@ -87,57 +95,71 @@ __global__ void __launch_bounds__(C::THREADS, 2)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* empty = full + C::NFULL;
-  float* q_scale = reinterpret_cast<float*>(empty + NSTAGE);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NFULL; ++s) mbar_init(&full[s], 1);
-    for (int s = 0; s < NSTAGE; ++s) mbar_init(&empty[s], 1);
+    for (int s = 0; s < NSTAGE; ++s) mbar_init(&empty[s], C::WM);
     fence_mbar_init();
   }
   ChunkRuns runs;  // (synchronises the block)
   if (!chunk_find_runs<C::THREADS>(p.ck, gridDim.x, blockIdx.x, &runs)) return;
 
-  if (warp == WN) {
+  if (warp == C::WM * WN) {
     // ------------------------------------------------------------ producer warp
+    // Pages and rows of 32 tiles at a time, a lane each: one tile's look-up after the other took as
+    // long as a tile of codes
     if (lane == 0) {
       tma_prefetch_desc(&tmk);
       tma_prefetch_desc(&tmv);
-      const uint64_t pol = l2_policy_evict_first();
-      int x = 0;  // tiles loaded
-      ChunkPiece pc;
-      bool ok = true;
-      while (ok && runs.next(p.ck, &pc)) {
-        // the next tile's page is read one tile ahead, behind the stage wait
-        int page = pc.n_tiles > 0 ? kv_page_of(p, pc.b, pc.token(0)) : 0;
-        for (int i = 0; i < pc.n_tiles; ++i, ++x) {
+    }
+    const uint64_t pol = l2_policy_evict_first();
+    int x = 0;  // tiles loaded
+    ChunkPiece pc;
+    bool ok = true;
+    while (ok && runs.next(p.ck, &pc)) {
+      for (int i0 = 0; ok && i0 < pc.n_tiles; i0 += 32) {
+        int pages = 0, rows = 0;
+        if (i0 + lane < pc.n_tiles) {
+          const int t = pc.token(i0 + lane);
+          pages = kv_page_of(p, pc.b, t);
+          rows = t % p.block_len;
+        }
+        const int n = min(32, pc.n_tiles - i0);
+        for (int i = 0; i < n; ++i) {
+          const int page = __shfl_sync(0xffffffffu, pages, i), row = __shfl_sync(0xffffffffu, rows, i);
           const int s = x % NSTAGE;
-          ok = x < NSTAGE || mbar_wait(&empty[s], ((x / NSTAGE) - 1) & 1, p.err, kDevErrEmptyWait);
-          if (!ok) break;
-          uint64_t* fb = &full[full_slot<C>(x)];
-          mbar_arrive_expect_tx(fb, C::STAGE);
-          uint8_t* ks = smem + s * C::STAGE;
-          const int row = pc.token(i) % p.block_len, from = page;
-          if (i + 1 < pc.n_tiles) page = kv_page_of(p, pc.b, pc.token(i + 1));
+          if (lane == 0) {
+            ok = x < NSTAGE || mbar_wait(&empty[s], ((x / NSTAGE) - 1) & 1, p.err, kDevErrEmptyWait);
+            if (ok) {
+              uint64_t* fb = &full[full_slot<C>(x)];
+              mbar_arrive_expect_tx(fb, C::STAGE);
+              uint8_t* ks = smem + s * C::STAGE;
 #pragma unroll
-          for (int bx = 0; bx < C::NBOX; ++bx) {
-            tma_load_4d(ks + bx * C::BOX_BYTES, &tmk, fb, bx * C::BOX_ELEMS, row, pc.g, from, pol);
-            tma_load_4d(ks + C::TILE + bx * C::BOX_BYTES, &tmv, fb, bx * C::BOX_ELEMS, row, pc.g, from, pol);
+              for (int bx = 0; bx < C::NBOX; ++bx) {
+                tma_load_4d(ks + bx * C::BOX_BYTES, &tmk, fb, bx * C::BOX_ELEMS, row, pc.g, page, pol);
+                tma_load_4d(ks + C::TILE + bx * C::BOX_BYTES, &tmv, fb, bx * C::BOX_ELEMS, row, pc.g, page, pol);
+              }
+            }
           }
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          if (!ok) break;
+          ++x;
         }
       }
-      // every issued copy lands before the CTA may exit
-      for (int y = max(0, x - NSTAGE); y < x; ++y)
-        if (!mbar_wait(&full[full_slot<C>(y)], full_parity<C>(y), p.err, kDevErrDrainWait)) break;
     }
+    // every issued copy lands before the CTA may exit
+    for (int y = max(0, x - NSTAGE); y < x; ++y)
+      if (!mbar_wait(&full[full_slot<C>(y)], full_parity<C>(y), p.err, kDevErrDrainWait)) break;
     return;
   }
 
   // -------------------------------------------------------------- consumer warps
-  const int wn = warp;
+  const int wm = C::WM == 1 ? 0 : warp / WN, wn = warp - wm * WN;
   const int gq = lane >> 2, tq = lane & 3;
-  float* ml = reinterpret_cast<float*>(smem + C::OFF_ML);
-  uint4* qfrag = reinterpret_cast<uint4*>(smem + C::OFF_QF);
+  float* ml = reinterpret_cast<float*>(smem + C::OFF_ML) + wm * WN * kRows * 2;
+  uint4* qfrag = reinterpret_cast<uint4*>(smem + C::OFF_QF) + wm * (D / 16) * 32;
+  float* q_scale = reinterpret_cast<float*>(empty + NSTAGE) + wm;
   // the run and its piece wait in shared memory: the registers are full of scores and O
   static_assert(sizeof(ChunkRuns) <= 64 && sizeof(ChunkPiece) <= 128, "a warp's place");
   ChunkRuns* run = reinterpret_cast<ChunkRuns*>(smem + C::OFF_RUN + warp * 192);
@@ -154,16 +176,18 @@ __global__ void __launch_bounds__(C::THREADS, 2)
   int x0 = 0;  // tiles of the pieces before
   while (next_piece()) {
     const int rows_total = pc.n * p.G;
-    const int mrow0 = pc.mt * kRows + gq, mrow1 = mrow0 + 8;
+    const int mset = pc.mt * C::ROWS + wm * kRows;  // this set's first row
+    const int mrow0 = mset + gq, mrow1 = mrow0 + 8;
     const bool v0 = mrow0 < rows_total, v1 = mrow1 < rows_total;
     const int tq0 = v0 ? mrow0 / p.G : 0, tq1 = v1 ? mrow1 / p.G : 0;
     const int h0 = pc.g * p.G + (v0 ? mrow0 % p.G : 0), h1 = pc.g * p.G + (v1 ? mrow1 % p.G : 0);
     // visible tokens of a row: [wl, hz] and below the sinks' end; all below the item's end
     const int pos0 = pc.m - pc.n;
-    const int hz0 = pos0 + tq0, hz1 = pos0 + tq1, hz_min = pos0 + pc.mt * kRows / p.G;
+    const int hz0 = pos0 + tq0, hz1 = pos0 + tq1, hz_min = pos0 + mset / p.G;
     auto window_lo = [&](int pos) -> int { return p.ck.window > 0 && pos >= p.ck.window ? pos - p.ck.window + 1 : 0; };
     const int wl0 = window_lo(hz0), wl1 = window_lo(hz1);
-    const int wl_max = window_lo(pos0 + min(pc.mt * kRows + kRows - 1, rows_total - 1) / p.G);
+    const int wl_max = window_lo(pos0 + min(mset + kRows - 1, rows_total - 1) / p.G);
+    const bool idle = C::WM > 1 && mset >= rows_total;  // a set without rows only passes the tiles on
 
     // ---- Q fragments (A operand, 16 rows x D): registers for bf16, shared memory for fp8
     uint32_t qa[C::FP8 ? 1 : D / 16][4];
@@ -184,7 +208,7 @@ __global__ void __launch_bounds__(C::THREADS, 2)
         // The 16 rows times the power of two that puts their largest magnitude in [2^14, 2^15)
         // convert to fp16 without overflow, exactly for every element within 2^-29 of the largest;
         // the power goes back into the score scale
-        consumers_sync<C>();  // the fragments' readers of the piece before are done
+        consumers_sync<C>(wm);  // the fragments' readers of the piece before are done
         if (wn == 0) {
           uint2 u[2][D / 16];
           uint32_t most = 0u;  // magnitudes order as their bits
@@ -212,7 +236,7 @@ __global__ void __launch_bounds__(C::THREADS, 2)
                                                pack_f16(bf16_lo(u[0][ks].y) * down, bf16_hi(u[0][ks].y) * down),
                                                pack_f16(bf16_lo(u[1][ks].y) * down, bf16_hi(u[1][ks].y) * down));
         }
-        consumers_sync<C>();
+        consumers_sync<C>(wm);
       }
     }
 
@@ -242,6 +266,11 @@ __global__ void __launch_bounds__(C::THREADS, 2)
         }
       }
       if (!mbar_wait(&full[full_slot<C>(x)], full_parity<C>(x), p.err, kDevErrFullWait)) break;
+      if (idle) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[s]);
+        continue;
+      }
       const uint32_t kbase = smem_u32(smem + s * C::STAGE);
       const uint32_t vbase = kbase + C::TILE;
       const int mi = lane >> 3;
@@ -449,7 +478,7 @@ __global__ void __launch_bounds__(C::THREADS, 2)
         ml[(wn * kRows + gq + 8 * r) * 2 + 1] = lrun[r];
       }
     }
-    consumers_sync<C>();
+    consumers_sync<C>(wm);
     float M[2], L[2], f[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -476,14 +505,14 @@ __global__ void __launch_bounds__(C::THREADS, 2)
     for (int i2 = 0; i2 < D / 8; ++i2)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[i2][e] *= C::FP8 ? fr[2 * (i2 & 1) + (e & 1)] : fr[e];
-    float4* obuf = reinterpret_cast<float4*>(smem + C::OFF_O);
+    float4* obuf = reinterpret_cast<float4*>(smem + C::OFF_O) + wm * (D / 8) * 32;
 #pragma unroll 1
     for (int w = 1; w < WN; ++w) {
       if (wn == w) {
 #pragma unroll
         for (int i2 = 0; i2 < D / 8; ++i2) obuf[i2 * 32 + lane] = make_float4(o[i2][0], o[i2][1], o[i2][2], o[i2][3]);
       }
-      consumers_sync<C>();
+      consumers_sync<C>(wm);
       if (wn == 0) {
 #pragma unroll
         for (int i2 = 0; i2 < D / 8; ++i2) {
@@ -491,7 +520,7 @@ __global__ void __launch_bounds__(C::THREADS, 2)
           o[i2][0] += y.x, o[i2][1] += y.y, o[i2][2] += y.z, o[i2][3] += y.w;
         }
       }
-      consumers_sync<C>();
+      consumers_sync<C>(wm);
     }
 
     // ---- the first warp stores: final rows in bf16, or a partial (an empty one's o is never read)
@@ -499,7 +528,7 @@ __global__ void __launch_bounds__(C::THREADS, 2)
       constexpr float kLn2 = 0.6931471805599453f;
       const bool direct = pc.slot < 0;
       const int64_t row_a = direct ? (pc.row0 + static_cast<int64_t>(tq0)) * p.Hq + h0
-                                   : static_cast<int64_t>(pc.slot) * kRows + gq;
+                                   : static_cast<int64_t>(pc.slot) * C::ROWS + wm * kRows + gq;
       const int64_t row_b = direct ? (pc.row0 + static_cast<int64_t>(tq1)) * p.Hq + h1 : row_a + 8;
       auto store2 = [&](int64_t row, int d, float y0, float y1) {
         if (direct)
@@ -545,9 +574,14 @@ __global__ void __launch_bounds__(C::THREADS, 2)
   }
 }
 
-using CfgBf16D64 = RowsCfg<false, 64, 4, 6>;
-using CfgBf16D128 = RowsCfg<false, 128, 3, 3>;
-using CfgFp8D128 = RowsCfg<true, 128, 4, 6>;
+// (two sets with bf16 heads of 128: 5 warps a set have 168 registers each, too few: 126 us for 24
+// sequences of 5 rows, 40 / 8 heads, where 3 warps of 233 take 117; the other two fit, fp8 159 -> 137)
+template <int WM>
+using CfgBf16D64 = RowsCfg<false, 64, WM, WM == 1 ? 4 : 5, WM == 1 ? 6 : 12>;
+template <int WM>
+using CfgBf16D128 = RowsCfg<false, 128, WM, 3, WM == 1 ? 3 : 6>;
+template <int WM>
+using CfgFp8D128 = RowsCfg<true, 128, WM, WM == 1 ? 4 : 5, WM == 1 ? 6 : 12>;
 
 template <class C>
 cudaError_t launch_cfg(const PartialParams& p, const CUtensorMap& tmk, const CUtensorMap& tmv, cudaStream_t stream) {
@@ -560,16 +594,21 @@ cudaError_t launch_cfg(const PartialParams& p, const CUtensorMap& tmk, const CUt
   return cudaGetLastError();
 }
 
+template <int WM>
+cudaError_t launch_sets(const PartialParams& p, int32_t d, bool fp8, const CUtensorMap& tmk, const CUtensorMap& tmv,
+                        cudaStream_t stream) {
+  if (fp8) return launch_cfg<CfgFp8D128<WM>>(p, tmk, tmv, stream);
+  if (d == 64) return launch_cfg<CfgBf16D64<WM>>(p, tmk, tmv, stream);
+  return launch_cfg<CfgBf16D128<WM>>(p, tmk, tmv, stream);
+}
+
 }  // namespace
 
-int chunk_rows_per_tile() { return kRows; }
-int chunk_rows_ctas_per_sm() { return 2; }
+int chunk_rows_ctas_per_sm(int rows) { return rows == kRows ? 2 : 1; }
 
 cudaError_t launch_chunk_rows(const PartialParams& p, int32_t d, bool fp8, const CUtensorMap& tmk, const CUtensorMap& tmv,
                               cudaStream_t stream) {
-  if (fp8) return launch_cfg<CfgFp8D128>(p, tmk, tmv, stream);
-  if (d == 64) return launch_cfg<CfgBf16D64>(p, tmk, tmv, stream);
-  return launch_cfg<CfgBf16D128>(p, tmk, tmv, stream);
+  return p.ck.rows == kRows ? launch_sets<1>(p, d, fp8, tmk, tmv, stream) : launch_sets<2>(p, d, fp8, tmk, tmv, stream);
 }
 
 }  // namespace skv

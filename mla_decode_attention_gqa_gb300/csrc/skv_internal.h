@@ -42,6 +42,7 @@ struct ChunkArgs {
   int32_t tile;     // tokens of one KV tile
   int32_t n_wave;   // CTAs resident at once
   int32_t n_target; // most work items with several chunks per row tile
+  int32_t start;    // few rows: tiles that an item counts besides its own (chunk_plan.cuh)
   int32_t* plan;    // device [kPlanHead + kPlanRow B] (chunk_plan.cuh)
   void* out;        // bf16 [T][Hq][d]
   float* lse;       // fp32 [T][Hq]
@@ -52,6 +53,10 @@ enum ChunkPlanWord : int { kPlanItems = 0, kPlanMerged = 1, kPlanNext = 2, kPlan
 constexpr int kChunkShortTiles = 8;
 // A run of the kernel for few rows has at least so many KV tiles.
 constexpr int kChunkMinTiles = 2;
+// Tiles of 16 KB of K and as much of V that the start and the end of an item are worth (24 ragged
+// sequences of 5 rows, 40 / 8 heads: counted as nothing 117 us, as 3 tiles 95, 5 to 8 92, 14 93; fp8
+// 138, 98, 92, 103).
+constexpr int kChunkStart = 5;
 
 // Parameters of one split-KV partial-attention launch.
 //
@@ -152,10 +157,9 @@ cudaError_t launch_gqa_partial(GqaVariant v, const PartialParams& p, const CUten
                                const CUtensorMap& tmv, int64_t n_items, cudaStream_t stream);
 // Ragged chunks of new tokens (p.ck): items in one piece write p.ck.out / p.ck.lse, the others
 // partial rows to p.out_o / p.out_lse, which the merge of the kernel joins.
-// Few rows (see chunk_rows.cu): n_wave CTAs, two partials of chunk_rows_per_tile() rows each;
+// Few rows (see chunk_rows.cu): row tiles of 16 or 32, n_wave CTAs, two partials of a row tile each;
 // tmk / tmv: pages with kTileN rows a box.
-int chunk_rows_per_tile();
-int chunk_rows_ctas_per_sm();
+int chunk_rows_ctas_per_sm(int rows);
 cudaError_t launch_chunk_rows(const PartialParams& p, int32_t d, bool fp8, const CUtensorMap& tmk, const CUtensorMap& tmv,
                               cudaStream_t stream);
 cudaError_t launch_chunk_runs_merge(const ChunkArgs& a, int32_t d, const float* part_o, const float* part_lse,

@@ -216,6 +216,16 @@ def test_the_kernel_choice_does_not_change_the_result():
                 check(c, window, n_sink, max_q_len=1)
 
 
+@pytest.mark.parametrize("window,n_sink", [(0, 0), (1, 0), (70, 5), (700, 66)])
+@pytest.mark.parametrize("Hq,Hkv,longest", [(40, 8, 5), (8, 2, 8), (17, 1, 1), (32, 1, 1), (3, 1, 10), (9, 3, 6)])
+@pytest.mark.parametrize("kind,d", TYPES)
+def test_two_sets_of_rows(kind, d, Hq, Hkv, longest, window, n_sink):
+    """17 to 32 rows of a KV head, beside sequences of fewer (one set idle), of none and of more."""
+    for seed, n, m in ((17, [longest, 1, 0, longest, 2], [1500, 1, 9, longest, 130]),
+                       (18, [1, 43, longest, 20], [900, 64, 5000, 333])):
+        check(R.make_case(n, m, Hq, Hkv, d, fp8=kind == "fp8", seed=seed, device=DEV), window, n_sink, max_q_len=longest)
+
+
 @pytest.mark.parametrize("kind,d", TYPES)
 def test_a_captured_graph_follows_the_lengths(kind, d):
     """One graph replayed for other lengths, chunk borders and tables, eager calls in between."""
