@@ -126,6 +126,18 @@ def test_bad_pages(kw):
     assert _call_append(_append(), _paged(**kw)) == skv.SKV_EINVAL
 
 
+@pytest.mark.parametrize("kind,fields", [(skv.SkvChunkDesc, skv._CHUNK_FIELDS), (skv.SkvAppendDesc, skv._APPEND_FIELDS)])
+def test_descriptions_from_their_fields(kind, fields):
+    flat = [x for _, t in kind._fields_ for x in [t._type_ if issubclass(t, ctypes.Array) else t] * getattr(t, "_length_", 1)]
+    values = [0.5 if t is ctypes.c_float else i + 1 for i, t in enumerate(flat)]
+    d = skv._described(kind, fields, *values)
+    got = [x for n, t in kind._fields_ for x in (list(getattr(d, n)) if issubclass(t, ctypes.Array) else [getattr(d, n)])]
+    assert got == values
+    for bad in (1 << 40, 1.5, None):
+        with pytest.raises(ValueError):
+            skv._described(kind, fields, bad, *values[1:])
+
+
 def test_bad_pointers():
     odd = ctypes.c_void_p(0x10008)
     for name in ("q", "k", "v", "cu", "seq", "out", "lse"):
