@@ -25,6 +25,7 @@
 #include "chunk_plan.cuh"
 #include "skv_common.cuh"
 #include "skv_internal.h"
+#include "warp_wait.cuh"
 
 namespace skv {
 
@@ -174,6 +175,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     return more;
   };
   int x0 = 0;  // tiles of the pieces before
+  // A warp that gave up a wait takes no further tile, but goes on through the pieces, since the
+  // others of its set count on it at their barriers
+  WarpWait wait(p.err);
   while (next_piece()) {
     const int rows_total = pc.n * p.G;
     const int mset = pc.mt * C::ROWS + wm * kRows;  // this set's first row
@@ -265,7 +269,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           vsc = __ldg(p.v_scale + idx);
         }
       }
-      if (!mbar_wait(&full[full_slot<C>(x)], full_parity<C>(x), p.err, kDevErrFullWait)) break;
+      if (!wait(&full[full_slot<C>(x)], full_parity<C>(x), kDevErrFullWait)) break;
       if (idle) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[s]);

@@ -47,6 +47,7 @@
 #include "skv_common.cuh"
 #include "skv_internal.h"
 #include "tc_common.cuh"
+#include "warp_wait.cuh"
 
 namespace skv {
 
@@ -875,8 +876,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     int base = 0;              // tiles of the items before
     uint32_t np = 0, np1 = 0;  // tiles of this group, and of group 1, so far
     uint32_t n_solo = 0, nq = 0;  // solo items, items with tiles so far
-    bool ok = true;
-    for (int r = 0; ok && item_here(r); ++r) {
+    WarpWait wait(p.err);
+    for (int r = 0; wait.ok && item_here(r); ++r) {
       const TcItem& t = items[r & 1];  // read in place: registers are short here
       const bool pair = t.pair != 0;
       // What only edge tiles and the epilogue need waits in shared memory: the registers are full
@@ -905,8 +906,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       int j = 0;  // tiles of the item done
       for (int i = pair ? 0 : k; i < t.n_tiles; i += step, ++j) {
         const int ta = t.token(2 * i), tb = t.token(2 * i + 1);  // the halves' first tokens
-        ok = mbar_wait(&bars->s_full[k], np & 1, p.err, kDevErrFullWait);
-        if (!ok) break;
+        if (!wait(&bars->s_full[k], np & 1, kDevErrFullWait)) break;
         ++np;
         tc::fence_after_sync();
         if (active) {
@@ -916,12 +916,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           float sl[2] = {p.scale_log2, p.scale_log2}, vs[2] = {1.f, 1.f};
           if constexpr (C::FP8) {
             const int x = base + i;
-            ok = mbar_wait(&bars->sc_full[x % kScaleSlots], (x / kScaleSlots) & 1, p.err, kDevErrFullWait);
+            if (!wait(&bars->sc_full[x % kScaleSlots], (x / kScaleSlots) & 1, kDevErrFullWait)) break;
             const float4 sc = bars->scales[x % kScaleSlots];
             if (j == 0) {
               // the row's own scale.  (Q of the item after the next one is split only after the
               // next one's last scores, which follow this item's last P V)
-              ok = ok && mbar_wait(&bars->q8_full[nq & 1], (nq >> 1) & 1, p.err, kDevErrFullWait);
+              if (!wait(&bars->q8_full[nq & 1], (nq >> 1) & 1, kDevErrFullWait)) break;
               q_scale = p.scale_log2 *
                         reinterpret_cast<const float*>(smem + C::OFF_QS)[((nq & 1) * 2 + (pair ? k : 0)) * kRowsTile + row];
             }
@@ -981,7 +981,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           // tokens that no row of the item sees may hold anything: zero their V rows, so that
           // p = 0 really counts nothing
           const int x = base + i, s = x % NST;
-          mbar_wait(&bars->v_full[s], (x / NST) & 1, p.err, kDevErrFullWait);
+          if (!wait(&bars->v_full[s], (x / NST) & 1, kDevErrFullWait)) break;
           for (int y = row >> 3; y < kTN; y += 16) {  // 8 threads a row
             const int tok = y < kHalf ? ta + y : tb + y - kHalf;
             if (!((tok >= t.tl.lo && tok < t.tl.hi) || tok < t.tl.sinks)) {
@@ -998,7 +998,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       if (t.n_tiles > 0) ++nq;
       const int tiles1 = pair ? t.n_tiles : t.n_tiles / 2;  // group 1's
       np1 += tiles1;
-      if (!ok) break;
+      if (!wait.ok) break;
 
       // ---- epilogue: O / l and lse
       // solo: the two groups' weights.  A group that summed nothing has l = 0 (its O may be
@@ -1011,13 +1011,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           ml[2 * row + 1] = l_sum;
           mbar_arrive(&bars->ml_full);
           // O1 and (m, l) are read before the next item changes them
-          ok = mbar_wait(&bars->o1_free, n_solo & 1, p.err, kDevErrEmptyWait);
+          if (!wait(&bars->o1_free, n_solo & 1, kDevErrEmptyWait)) break;
           ++n_solo;
           tc::fence_after_sync();
           item_done(r);
           continue;
         }
-        ok = mbar_wait(&bars->ml_full, n_solo & 1, p.err, kDevErrFullWait);
+        if (!wait(&bars->ml_full, n_solo & 1, kDevErrFullWait)) break;
         ++n_solo;
         const float m1 = ml[2 * row], l1 = ml[2 * row + 1];
         const float mm = fmaxf(m_used, m1);
@@ -1027,9 +1027,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         l_sum = (some0 ? a0 * l_sum : 0.f) + (some1 ? a1 * l1 : 0.f);
         m_used = mm;
       }
-      if (ok && j > 0) ok = mbar_wait(&bars->pv_done[k], (np - 1) & 1, p.err, kDevErrFullWait);
+      if (j > 0 && !wait(&bars->pv_done[k], (np - 1) & 1, kDevErrFullWait)) break;
       const bool both = !pair && tiles1 > 0;
-      if (ok && both) ok = mbar_wait(&bars->pv_done[1], (np1 - 1) & 1, p.err, kDevErrFullWait);
+      if (both && !wait(&bars->pv_done[1], (np1 - 1) & 1, kDevErrFullWait)) break;
       tc::fence_after_sync();
       const bool some = some0 || some1;
       const float inv = some ? 1.f / l_sum : 0.f;
