@@ -249,9 +249,13 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     float mrun[2] = {-INFINITY, -INFINITY};
     float lrun[2] = {0.f, 0.f};
-    // fp8: O is held times 2^-ve, ve the largest exponent of the V scales so far, so that p times a
-    // scale of any size keeps fp16's 11 bits
-    int ve = -200;
+    // fp8: p times the V scale goes to fp16, whose 11 bits hold from 2^-14 to 2^16, so each row has a
+    // power of two, up, by which its weights and its O are multiplied: the largest weight of a tile lies
+    // between 2^4 and 2^15 then, and what is above 2^-28 of it (2^-18 where it lies lowest) keeps its
+    // bits, however far apart the scales and the scores of the row's tiles are
+    constexpr int kMostUp = 124;  // (2^-kMostUp is a normal number)
+    float up[2];
+    up[0] = up[1] = __uint_as_float(static_cast<uint32_t>(127 + kMostUp) << 23);
 
     // this warp's tiles: those whose number in the CTA is wn modulo WN
     for (int i = (wn + WN - x0 % WN) % WN; i < pc.n_tiles; i += WN) {
@@ -353,31 +357,69 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         scale_mask(std::true_type{});
       else
         scale_mask(std::false_type{});
-      float base[2], alpha[2];
-      float grow = 1.f;  // fp8: 2^(old - new) of ve
-      if constexpr (C::FP8) {
-        const int e = vsc == 0.f ? -200 : static_cast<int>((__float_as_uint(vsc) >> 23) & 0xFFu) - 127;
-        if (e > ve) {
-          grow = ve == -200 ? 0.f : exp2f(static_cast<float>(ve - e));
-          ve = e;
-        }
-        // |vsc| in units of 2^ve, below 2; in two factors, since 2^-ve may be subnormal
-        const int half_e = -ve / 2;
-        vsc = vsc * __uint_as_float(static_cast<uint32_t>(127 + half_e) << 23) *
-              __uint_as_float(static_cast<uint32_t>(127 - ve - half_e) << 23);
-      }
+      float base[2], alpha[2], fall[2], vs[2] = {1.f, 1.f};
+      bool other = false;  // fp8: a row's largest weight leaves its range
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         tmax[r] = fmaxf(tmax[r], __shfl_xor_sync(0xffffffffu, tmax[r], 1));
         tmax[r] = fmaxf(tmax[r], __shfl_xor_sync(0xffffffffu, tmax[r], 2));
         const float mnew = fmaxf(mrun[r], tmax[r]);
         base[r] = (mnew == -INFINITY) ? 0.f : mnew;
-        alpha[r] = fast_exp2(mrun[r] - base[r]);  // 0 when mrun = -inf
+        fall[r] = mrun[r] - base[r];
+        alpha[r] = fast_exp2(fall[r]);  // 0 when mrun = -inf
         mrun[r] = mnew;
         lrun[r] *= alpha[r];
-        alpha[r] *= grow;
+        if constexpr (C::FP8) {
+          vs[r] = vsc * up[r];
+          const float most = fabsf(vs[r]) * fast_exp2(tmax[r] - base[r]);
+          other = other || !(most >= 16.f && most <= 32768.f);
+        }
       }
-      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {  // a row max (or ve) moved
+      if constexpr (C::FP8) {
+        if (__any_sync(0xffffffffu, other)) {
+          // log2 of a row's largest weight in this tile (below 2^-100 of its scale it is nothing), and of up
+          const int e = static_cast<int>((__float_as_uint(vsc) >> 23) & 0xFFu) - 127;
+          float most[2];
+          int was[2], to[2];
+          bool lower = false;
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            most[r] = static_cast<float>(e) + fmaxf(tmax[r] - base[r], -100.f);
+            was[r] = static_cast<int>(__float_as_uint(up[r]) >> 23) - 127;
+            to[r] = min(14 - static_cast<int>(ceilf(most[r])), kMostUp);
+            // (a row that sees nothing here keeps its power; its weights are zeros, whatever the scale)
+            if (tmax[r] == -INFINITY || vsc == 0.f || (to[r] >= was[r] && to[r] <= was[r] + 8)) to[r] = was[r];
+            lower = lower || to[r] > was[r];
+          }
+          if (__any_sync(0xffffffffu, lower)) {
+            // O grows with its power, up to 2^100: the largest of each row's O (a thread's columns are rows
+            // 2tq, 2tq+1 (+8); the other lanes of the same rows hold other dims)
+            float big[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+            for (int i2 = 0; i2 < D / 8; ++i2)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) big[i2 & 1][q & 1] = fmaxf(big[i2 & 1][q & 1], fabsf(o[i2][q]));
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+#pragma unroll
+              for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int w = 4; w < 32; w <<= 1) big[r][q] = fmaxf(big[r][q], __shfl_xor_sync(0xffffffffu, big[r][q], w));
+              const float even = __shfl_sync(0xffffffffu, big[r][0], gq >> 1), odd = __shfl_sync(0xffffffffu, big[r][1], gq >> 1);
+              const float x = (gq & 1) ? odd : even;
+              const float room = 100.f - (static_cast<float>(static_cast<int>(__float_as_uint(x) >> 23) - 126) + fall[r]);
+              if (to[r] > was[r] && x > 0.f) to[r] = min(to[r], was[r] + max(static_cast<int>(fminf(room, 300.f)), 0));
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            if (to[r] != was[r]) alpha[r] = fast_exp2(fall[r] + static_cast<float>(to[r] - was[r]));
+            up[r] = __uint_as_float(static_cast<uint32_t>(127 + to[r]) << 23);
+            vs[r] = tmax[r] == -INFINITY ? 0.f : vsc * up[r];
+          }
+        }
+      }
+      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {  // a row max (or its power) moved
         if constexpr (!C::FP8) {
 #pragma unroll
           for (int i2 = 0; i2 < D / 8; ++i2) {
@@ -417,8 +459,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           pa[kk][hf + 0] = pack_bf16(p0, p1);
           pa[kk][hf + 1] = pack_bf16(p2, p3);
         } else {
-          pa[kk][hf + 0] = pack_f16(p0 * vsc, p1 * vsc);
-          pa[kk][hf + 1] = pack_f16(p2 * vsc, p3 * vsc);
+          pa[kk][hf + 0] = pack_f16(p0 * vs[0], p1 * vs[0]);
+          pa[kk][hf + 1] = pack_f16(p2 * vs[1], p3 * vs[1]);
         }
       }
 
@@ -494,7 +536,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 #pragma unroll
       for (int w = 0; w < WN; ++w) L[r] += ml[(w * kRows + gq + 8 * r) * 2 + 1] * fast_exp2(ml[(w * kRows + gq + 8 * r) * 2] - base);
       f[r] = fast_exp2(mrun[r] - base);
-      if constexpr (C::FP8) f[r] *= ve == -200 ? 0.f : exp2f(static_cast<float>(ve));
+      if constexpr (C::FP8) f[r] *= __uint_as_float((254u << 23) - __float_as_uint(up[r]));  // 1 / up
       // (a warp without a tile has O = 0; 0 * 2^-inf = 0)
     }
     // the factor of each element: rows gq, gq + 8; fp8: O^T, rows 2tq, 2tq+1 (+8)
