@@ -60,6 +60,9 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;    // S_k (P_k over its first 64 columns) at kColS + 128 k
 constexpr uint32_t kColO = 256;  // O_k at kColO + 128 k
 constexpr float kTileSumLimit = 65536.0f;
+// Past this maximum (base 2) a score minus the maximum is taken after the score was rounded like it: the
+// fused form leaves up to half a unit of the maximum's last place, which an exponential past 2^30 cannot hold
+constexpr float kLargeScore = 4194304.0f;
 
 template <int D_, bool FP8_>
 struct TcCfg {
@@ -231,8 +234,8 @@ __device__ __noinline__ float first_max(uint32_t s_col, float m, float scale0, f
   return m == -INFINITY ? mx : m;
 }
 
-// A tile in which the p sum of some row of the warp (need) passed the limit: O and l rescaled to
-// the tile's true maximum, and its P again.  PV of the group's tile before ran before these scores,
+// A tile in which the p sum of some row of the warp (need) passed the limit, or whose scores are very
+// large: O and l rescaled to the tile's true maximum, and its P again.  PV of the group's tile before ran before these scores,
 // so O is final.  l comes back with the tile's sum.
 struct Redone {
   float m, l;
@@ -259,6 +262,7 @@ __device__ __noinline__ Redone redo_tile(uint32_t s_col, uint32_t o_col, bool ne
     l *= alpha;
   }
   const float base = (m_new == -INFINITY) ? 0.f : m_new;
+  const bool large = fabsf(base) > kLargeScore;
   uint64_t ls[2] = {0ull, 0ull};
 #pragma unroll 1
   for (int cc = 0; cc < kTN / 32; ++cc) {
@@ -270,7 +274,9 @@ __device__ __noinline__ Redone redo_tile(uint32_t s_col, uint32_t o_col, bool ne
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       float a0, a1;
-      fma_pair(__uint_as_float(x[e >> 3][(2 * e) & 15]), __uint_as_float(x[e >> 3][(2 * e + 1) & 15]), s2, -base, a0, a1);
+      const float x0 = __uint_as_float(x[e >> 3][(2 * e) & 15]), x1 = __uint_as_float(x[e >> 3][(2 * e + 1) & 15]);
+      fma_pair(x0, x1, s2, -base, a0, a1);
+      if (large) a0 = __fadd_rn(__fmul_rn(x0, s2), -base), a1 = __fadd_rn(__fmul_rn(x1, s2), -base);
       float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
       ls[e & 1] = add_f32x2(ls[e & 1], p0, p1);
       if constexpr (FP8) mul_pair(p0, p1, v2);
@@ -939,8 +945,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           if (__any_sync(0xffffffffu, m_used == -INFINITY)) m_used = first_max<C::FP8>(s_col, m_used, sl[0], sl[1]);
           uint32_t pk[kTN / 2];
           uint64_t ls[2] = {0ull, 0ull};  // fp32 pair sums of p
+          const float base0 = (m_used == -INFINITY) ? 0.f : m_used;
           {
-            const float base0 = (m_used == -INFINITY) ? 0.f : m_used;
 #pragma unroll
             for (int cc = 0; cc < kTN / 32; ++cc) {
               uint32_t x[2][16];
@@ -959,7 +965,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               }
             }
           }
-          const bool need = !(sum_f32x2(ls[0]) + sum_f32x2(ls[1]) <= kTileSumLimit);
+          const bool need = !(sum_f32x2(ls[0]) + sum_f32x2(ls[1]) <= kTileSumLimit) || fabsf(base0) > kLargeScore;
           if (__any_sync(0xffffffffu, need)) {
             const Redone again = redo_tile<D, C::FP8>(s_col, o_col, need, m_used, l_sum, sl[0], sl[1], vs[0], vs[1]);
             m_used = again.m;
