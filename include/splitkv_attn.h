@@ -412,7 +412,8 @@ skv_status gqa_decode_attn_passq(const skv_desc* desc, int32_t n_ranks, const vo
  * sees may also reach the rows of that row tile that do not see it.
  * Rounding: scores, sums and the weighted sum in fp32; the softmax weights once, to bf16 (fp8
  * pages: weight times V scale, to bf16, or with few rows to fp16), the output to bf16.  fp8 codes
- * are exact; of q what lies below 2^-18 of its row's largest magnitude may be lost with fp8 pages.
+ * are exact; with fp8 pages, of q what lies below 2^-17 of its row's (token's and head's) largest
+ * magnitude may be lost, and a row of q with an infinity or a NaN gives a row of NaN.
  * Errors: SKV_EINVAL, SKV_EUNSUPPORTED and SKV_EWORKSPACE as for gqa_decode_attn_paged, and
  * SKV_EINVAL for a softmax_scale that is not positive, a negative window or n_sink, and n_sink
  * without a window.  T = 0 does nothing.

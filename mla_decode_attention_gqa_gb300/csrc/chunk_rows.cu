@@ -58,9 +58,10 @@ struct RowsCfg {
   static constexpr int OFF_ML = OFF_O + ROWS * D * 4;          // (m, l) of each warp's rows
   static constexpr int OFF_QF = OFF_ML + WN * ROWS * 2 * 4;    // fp8: q fragments
   static constexpr int OFF_BAR = OFF_QF + (FP8 ? WM * (D / 16) * 32 * 16 : 0);
-  static constexpr int OFF_RUN = OFF_BAR + 256;                // each consumer warp's run and piece
+  static constexpr int OFF_QS = OFF_BAR + 256;                 // fp8: the score scale of each row
+  static constexpr int OFF_RUN = OFF_QS + (FP8 ? ROWS * 4 : 0);  // each consumer warp's run and piece
   static constexpr int SMEM = 1024 + OFF_RUN + WM * WN * 192;
-  static_assert((NFULL + NSTAGE) * 8 + WM * 4 <= 256, "barriers and the q scales");
+  static_assert((NFULL + NSTAGE) * 8 <= 256, "barriers");
   static_assert(CTAS * (SMEM + 1536) <= 227 * 1024, "CTAs an SM");
 };
 
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   const int gq = lane >> 2, tq = lane & 3;
   float* ml = reinterpret_cast<float*>(smem + C::OFF_ML) + wm * WN * kRows * 2;
   uint4* qfrag = reinterpret_cast<uint4*>(smem + C::OFF_QF) + wm * (D / 16) * 32;
-  float* q_scale = reinterpret_cast<float*>(empty + NSTAGE) + wm;
+  float* q_scale = reinterpret_cast<float*>(smem + C::OFF_QS) + wm * kRows;
   // the run and its piece wait in shared memory: the registers are full of scores and O
   static_assert(sizeof(ChunkRuns) <= 64 && sizeof(ChunkPiece) <= 128, "a warp's place");
   ChunkRuns* run = reinterpret_cast<ChunkRuns*>(smem + C::OFF_RUN + warp * 192);
@@ -209,13 +210,14 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           qa[ks][3] = v1 ? *reinterpret_cast<const uint32_t*>(q1 + d0 + 8) : 0u;
         }
       } else {
-        // The 16 rows times the power of two that puts their largest magnitude in [2^14, 2^15)
-        // convert to fp16 without overflow, exactly for every element within 2^-29 of the largest;
-        // the power goes back into the score scale
+        // A row times the power of two that puts its largest magnitude in [2^14, 2^15) converts to fp16
+        // without overflow, exactly for every element within 2^-31 of the largest; the power goes back
+        // into the row's score scale (NaN for a row with an infinity or a NaN, which says the same of the
+        // row and nothing of the others)
         consumers_sync<C>(wm);  // the fragments' readers of the piece before are done
         if (wn == 0) {
           uint2 u[2][D / 16];
-          uint32_t most = 0u;  // magnitudes order as their bits
+          uint32_t most[2] = {0u, 0u};  // magnitudes order as their bits
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             // k-slots (2tq, 2tq+1 | 2tq+8, 2tq+9) hold d = 16ks + 4tq + (0,1 | 2,3), the order in
@@ -226,19 +228,27 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 #pragma unroll
             for (int r = 0; r < 2; ++r)
 #pragma unroll
-              for (uint32_t w : {u[r][ks].x, u[r][ks].y}) most = max(most, max((w << 16) & 0x7FFF0000u, w & 0x7FFF0000u));
+              for (uint32_t w : {u[r][ks].x, u[r][ks].y})
+                most[r] = max(most[r], max((w << 16) & 0x7FFF0000u, w & 0x7FFF0000u));
           }
-          most = __reduce_max_sync(0xffffffffu, most);
-          int qe = 0;  // all-zero or non-finite rows keep their values
-          if (most != 0u && most < 0x7F800000u) qe = min(max(static_cast<int>(most >> 23) - 127 - 14, -100), 100);
-          const float down = __uint_as_float(static_cast<uint32_t>(127 - qe) << 23);
-          if (lane == 0) *q_scale = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + qe) << 23);
+          float down[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {  // a row's lanes: 4 gq .. 4 gq + 3
+            most[r] = max(most[r], __shfl_xor_sync(0xffffffffu, most[r], 1));
+            most[r] = max(most[r], __shfl_xor_sync(0xffffffffu, most[r], 2));
+            const bool finite = most[r] < 0x7F800000u;
+            const int qe = most[r] == 0u ? 0 : min(max(static_cast<int>(most[r] >> 23) - 127 - 14, -126), 126);
+            down[r] = __uint_as_float(static_cast<uint32_t>(127 - qe) << 23);
+            if (tq == 0)
+              q_scale[gq + 8 * r] =
+                  finite ? p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + qe) << 23) : __int_as_float(0x7fc00000);
+          }
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks)
-            qfrag[ks * 32 + lane] = make_uint4(pack_f16(bf16_lo(u[0][ks].x) * down, bf16_hi(u[0][ks].x) * down),
-                                               pack_f16(bf16_lo(u[1][ks].x) * down, bf16_hi(u[1][ks].x) * down),
-                                               pack_f16(bf16_lo(u[0][ks].y) * down, bf16_hi(u[0][ks].y) * down),
-                                               pack_f16(bf16_lo(u[1][ks].y) * down, bf16_hi(u[1][ks].y) * down));
+            qfrag[ks * 32 + lane] = make_uint4(pack_f16(bf16_lo(u[0][ks].x) * down[0], bf16_hi(u[0][ks].x) * down[0]),
+                                               pack_f16(bf16_lo(u[1][ks].x) * down[1], bf16_hi(u[1][ks].x) * down[1]),
+                                               pack_f16(bf16_lo(u[0][ks].y) * down[0], bf16_hi(u[0][ks].y) * down[0]),
+                                               pack_f16(bf16_lo(u[1][ks].y) * down[1], bf16_hi(u[1][ks].y) * down[1]));
         }
         consumers_sync<C>(wm);
       }
@@ -327,8 +337,11 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       }
 
       // ---- scale, mask, online softmax
-      float sl = p.scale_log2;
-      if constexpr (C::FP8) sl = *reinterpret_cast<volatile const float*>(q_scale) * ksc;
+      float sl[2] = {p.scale_log2, p.scale_log2};
+      if constexpr (C::FP8) {
+        sl[0] = reinterpret_cast<volatile const float*>(q_scale)[gq] * ksc;
+        sl[1] = reinterpret_cast<volatile const float*>(q_scale)[gq + 8] * ksc;
+      }
       // tokens of this tile that some row of the item sees / that every row of it sees
       const int r_lo = pc.tl.lo, r_hi = pc.tl.hi, sinks = pc.tl.sinks;
       const bool in_range = (t0 >= r_lo && t0 + TN <= r_hi) || t0 + TN <= sinks;
@@ -341,7 +354,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         for (int nt = 0; nt < TN / 8; ++nt) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float y = sc[nt][e] * sl;
+            float y = sc[nt][e] * sl[e >> 1];
             if constexpr (decltype(masked)::value) {
               const int tok = t0 + 8 * nt + 2 * tq + (e & 1);
               const bool seen = tok < r_hi && tok <= ((e < 2) ? hz0 : hz1) &&

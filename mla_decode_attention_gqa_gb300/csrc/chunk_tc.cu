@@ -741,8 +741,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const int row = (warp - 12) * 32 + lane;
       // Q for the products with e4m3 keys: a row times the power of two that puts its largest
       // magnitude in [2^7, 2^8) is the sum of two e4m3 values, the rounded one and the rest.  A bf16
-      // value's 8 bits are 4 and 4, so the sum is exact down to 2^-10 of the row's largest and off
-      // by 2^-18 of it at most below.  The rounded parts (128 bytes) go over the row's first 64
+      // value's 8 bits are 4 and 4, so the sum is exact down to 2^-9 of the row's largest and off
+      // by 2^-17 of it at most below (half the subnormal step, 2^-10, against 2^7).  The rounded parts (128 bytes) go over the row's first 64
       // values, the rests over its last 64, each after what it overwrites was read.
       auto split_q = [&](uint8_t* q) -> float {
         auto chunk = [&](int c) {

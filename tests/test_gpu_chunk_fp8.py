@@ -1,5 +1,5 @@
 """GPU tests of attn_chunk_paged over fp8 pages where the ranges of its roundings can go wrong: V
-scales that lie far apart, and how many bits the weights keep.
+scales that lie far apart, queries of very different size, and how many bits the weights keep.
 Every case runs on the kernel for 16 rows of a KV head, on the one for 32, and on the tensor cores."""
 
 import math
@@ -133,3 +133,73 @@ def test_bits_of_the_weights(kernel):
     tol = (WEIGHT[kernel] + 2.0 ** -18) * size + 2.0 ** -8 * ro.abs()
     assert ((out - ro).abs() <= tol).all()
     assert (lse - rl).abs().max() <= 2.0 ** -20
+
+
+# ------------------------------------------------------------------ queries
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_rows_of_very_different_size(kernel):
+    """A row 2^40 times another, a row of zeros and rows of ordinary size, in every place of a row
+    tile: each is as exact as alone."""
+    G, T = 4, 12
+    for seed in range(4):
+        c = R.make_case([T], [200], 2 * G, 2, 128, fp8=True, seed=30 + seed, device=DEV)
+        big = (torch.arange(T)[:, None] * 8 + torch.arange(2 * G)) % 7 == seed
+        zero = (torch.arange(T)[:, None] * 8 + torch.arange(2 * G)) % 11 == seed
+        q = c["q"].cpu().float()
+        q[big] *= 2.0 ** 40
+        q[zero & ~big] = 0.0
+        c["q"] = q.to(torch.bfloat16).to(DEV)
+        out, lse = run(c, kernel)
+        assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+        ro, rl, size = R.attend(c)
+        tol = (WEIGHT[kernel] + 2.0 ** -11) * size + 2.0 ** -8 * ro.abs() + 2.0 ** -20 * size.amax(-1, keepdim=True)
+        assert ((out - ro).abs() <= tol)[~big].all()
+        # a query's part below 2^-17 of its largest value may be lost: 2^-17 max|q| sum |k| / sqrt(d),
+        # below 2^-17 * 5 * 128 * 0.9 / 11.3 = 4e-4, beside 2.5e-4 of the sums
+        assert (lse - rl).abs()[~big].max() <= 6.5e-4
+        assert ((lse - rl).abs() <= 2.0 ** -16 * rl.abs() + 6.5e-4)[big].all()
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_a_query_that_is_no_number_spoils_its_own_row_only(kernel):
+    """Infinities and NaN in some rows, beside rows of values above fp16's largest."""
+    G, T = 4, 12
+    c = R.make_case([T], [200], 2 * G, 2, 128, fp8=True, seed=40, device=DEV)
+    q = c["q"].cpu().float() * 2.0 ** 17
+    bad = (torch.arange(T)[:, None] * 8 + torch.arange(2 * G)) % 9 == 2
+    q[..., 5][bad] = torch.tensor([math.inf, -math.inf, math.nan]).repeat(len(q))[: int(bad.sum())]
+    c["q"] = q.to(torch.bfloat16).to(DEV)
+    scale = 2.0 ** -17 / math.sqrt(128)
+    out, lse = run(c, kernel, softmax_scale=scale)
+    assert torch.isnan(out[bad]).all() and torch.isnan(lse[bad]).all()
+    c["q"] = torch.where(bad[..., None], 0.0, c["q"].cpu().float()).to(torch.bfloat16).to(DEV)
+    ro, rl, size = R.attend(c, scale=scale)
+    tol = (WEIGHT[kernel] + 2.0 ** -11) * size + 2.0 ** -8 * ro.abs() + 2.0 ** -20 * size.amax(-1, keepdim=True)
+    assert ((out - ro).abs() <= tol)[~bad].all()
+    assert (lse - rl).abs()[~bad].max() <= 6.5e-4
+
+
+@pytest.mark.parametrize("size", [1.0, 2.0 ** -100, 2.0 ** 126])
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_small_values_of_a_query(kernel, size):
+    """Row x has size at dim 0 and size 2^-x at dim 77, the only one where the keys are not zero: the
+    lse of a row that sees one token is 2^-x k.  Exact from 2^-9 on, else off by 2^-17 at most.  (The
+    size of the row does not count: the score scale takes it back.)"""
+    T, d, G = 40, 128, 1
+    q = torch.zeros(T, 1, d, dtype=torch.float64)
+    q[:, 0, 0] = size
+    q[:, 0, 77] = size * 2.0 ** -torch.arange(T, dtype=torch.float64)
+    k = torch.zeros(1, 1, L, d)
+    k[0, 0, :T, 77] = 96.0
+    c = dict(q=q.to(torch.bfloat16).to(DEV), k_pages=k.to(R.E4M3).to(DEV), v_pages=torch.ones(1, 1, L, d).to(R.E4M3).to(DEV),
+             k_scale=torch.ones(1, 1, 1, device=DEV), v_scale=torch.ones(1, 1, 1, device=DEV),
+             block_table=torch.zeros(1, 1, dtype=torch.int32, device=DEV),
+             seq_lens=torch.tensor([T], dtype=torch.int32, device=DEV), cu_q=torch.tensor([0, T], dtype=torch.int32, device=DEV))
+    scale = 1.0 / size if size < 2.0 ** 120 else 2.0 ** -126
+    _, lse = run(c, kernel, window=1, softmax_scale=scale)
+    x = torch.arange(T, dtype=torch.float64)
+    want = 96.0 * c["q"][:, 0, 77].cpu().double() * scale
+    lost = torch.where(x <= 9, 0.0, 96.0 * 2.0 ** -17)
+    assert ((lse[:, 0] - want).abs() <= lost + 2.0 ** -22 * want).all()
