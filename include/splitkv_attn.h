@@ -451,7 +451,8 @@ skv_status attn_chunk_paged(const skv_chunk_desc* desc, const skv_paged* paged, 
  * in fp32, rounded once at the store.
  *
  *   q, k, v    bf16, packed [T][H][d] with (token, head) strides, e.g. views of one fused
- *              projection;  q_out bf16 with its own strides (q itself is allowed: in place)
+ *              projection;  q_out bf16 with its own strides, a place of its own for
+ *              every row (q itself is allowed: in place)
  *   q_weight, k_weight  [d] (stride 0) or one row per head (stride in elements), bf16 or fp32
  *   cos, sin   fp32 [max_pos][rot / 2] contiguous
  *   positions  int32 [T]: the rows of the tables, or NULL: each token's place in its sequence.

@@ -1056,6 +1056,17 @@ skv_status chunk_desc(const skv_chunk_desc* c, const skv_paged* pg, skv_desc* d)
   return validate_paged(d, pg);
 }
 
+// Whether two of the rows of d elements at i a + j b (i < n, j < m; b >= d where m > 1) share an element.
+bool rows_overlap(__int128 a, int64_t n, __int128 b, int64_t m, int64_t d) {
+  if (a < d) return n > 1;
+  if (a >= b * (m - 1) + d || b >= a * (n - 1) + d) return false;  // one inside the other
+  for (int64_t j = 1; j < m; ++j) {  // else the multiples of a on either side of j b
+    const __int128 i = j * b / a;
+    if ((i >= 1 && i < n && j * b - i * a < d) || (i + 1 < n && (i + 1) * a - j * b < d)) return true;
+  }
+  return false;
+}
+
 // Rows of one token on the tensor-core kernel: the group padded to a power of two.
 int padded_group(int G) {
   int r = 1;
@@ -1222,6 +1233,8 @@ skv_status qk_norm_rope_append(const skv_append_desc* desc, const skv_paged* pag
   }
   if (desc->q_out_strides[1] < desc->d && desc->Hq > 1)
     return fail(SKV_EINVAL, "q_out head stride must cover a whole head row");
+  if (desc->T > 1 && rows_overlap(desc->q_out_strides[0], desc->T, desc->q_out_strides[1], desc->Hq, desc->d))
+    return fail(SKV_EINVAL, "q_out strides put the rows of several tokens in one place");
   if (!std::isfinite(desc->eps) || desc->eps < 0.f) return fail(SKV_EINVAL, "eps must be finite and not negative");
   const int step = desc->d / 8;  // a lane turns d / 16 values and its partner as many
   if (desc->rot < 0 || desc->rot > desc->d || desc->rot % step) {

@@ -200,3 +200,29 @@ def test_split_qkv_and_tables():
     assert cos.shape == sin.shape == (1000, 16) and cos.dtype == torch.float32
     angle = 777 * 10000.0 ** (-2 * 5 / 32)
     assert abs(cos[777, 5] - math.cos(angle)) <= 2 ** -24 and abs(sin[777, 5] - math.sin(angle)) <= 2 ** -24
+
+
+def _rows_meet(a, n, b, m, d):
+    seen = set()
+    for t in range(n):
+        for h in range(m):
+            row = set(range(t * a + h * b, t * a + h * b + d))
+            if row & seen:
+                return True
+            seen |= row
+    return False
+
+
+def test_queries_out_need_a_place_for_each_row():
+    """Token and head strides that put the rows of several tokens in one place; layouts that only
+    look like it, and a single token, are taken (and refused for the missing q behind that)."""
+    T, H, d = 4, 3, 64
+    for a in [0, 8, 32] + list(range(64, 420, 32)):
+        for b in range(64, 420, 32):
+            args = dict(T=T, Hq=H, Hkv=H, d=d, rot=64, q_strides=(9 * d, d), q_out_strides=(a, b),
+                        k_page_strides=(H * 64 * d, 64 * d, d), v_page_strides=(H * 64 * d, 64 * d, d))
+            assert _call_append(_append(**args), q=None) == skv.SKV_EINVAL
+            assert ("q_out strides" in skv.last_error()) == _rows_meet(a, T, b, H, d), (a, b, skv.last_error())
+            args["T"] = 1
+            assert _call_append(_append(**args), q=None) == skv.SKV_EINVAL
+            assert "strides" not in skv.last_error()
