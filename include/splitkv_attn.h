@@ -116,10 +116,10 @@ const char* splitkv_last_error(void);
 
 /*
  * Read and clear the device error word of the current device (blocking: waits for all
- * work on the device).  *code = 0 if no kernel gave up a bounded wait, else a bitmask
- * (1: a consumer waited too long for a tile, 2: the loader waited too long for a free
- * stage, 4: a final drain waited too long; 8: a position outside qk_norm_rope_append's
- * tables).  Every wait in the kernels has a time limit.
+ * work on the device).  *code = 0 if no kernel gave up a bounded wait and no position lay
+ * outside the tables, else a bitmask (1: a consumer waited too long for a tile, 2: the
+ * loader waited too long for a free stage, 4: a final drain waited too long; 8: a position
+ * outside qk_norm_rope_append's tables).  Every wait in the kernels has a time limit.
  */
 skv_status splitkv_device_error(uint32_t* code);
 
@@ -127,7 +127,7 @@ skv_status splitkv_device_error(uint32_t* code);
  * Read and clear the whole device error record (8 words, blocking): [0] the code as above,
  * [1] nonzero if the first failure was described, [2] its block index, [3] its thread
  * index, [4] the shared-memory address of the barrier it waited on, [5] the phase parity it
- * waited for | code << 8.  For diagnosing a wait that gave up.
+ * waited for | code << 8.  For diagnosing a wait that gave up ([1] = 0: none did).
  */
 skv_status splitkv_device_error_detail(uint32_t* record);
 

@@ -190,23 +190,29 @@ def last_error():
 
 
 last_device_error_detail = None
+_DEVICE_ERRORS = ((1, "a wait for a tile gave up"), (2, "a wait for a free stage gave up"), (4, "a final drain gave up"),
+                  (8, "a position outside the rotation tables"))
 
 
 def device_error():
-    """Read and clear the device error record (blocking); 0 means no kernel gave up a wait.
-    A nonzero code also leaves the record (block, thread, barrier, parity) in
-    ``last_device_error_detail`` and prints it to stderr."""
+    """Read and clear the device error record (blocking).  0: no kernel gave up a wait and no
+    token's position lay outside qk_norm_rope_append's tables; else the bits of
+    splitkv_device_error().  A nonzero code also leaves the record in ``last_device_error_detail``
+    (the code, and of the first wait that gave up the block, thread, barrier and parity) and prints
+    it to stderr."""
     global last_device_error_detail
     rec = (ctypes.c_uint32 * 8)()
     _check(_lib.splitkv_device_error_detail(rec))
     code = int(rec[0])
     if code:
-        last_device_error_detail = {"code": code, "block": int(rec[2]), "thread": int(rec[3]),
-                                    "barrier_smem_addr": int(rec[4]), "parity": int(rec[5]) & 0xFF,
-                                    "first_code": (int(rec[5]) >> 8) & 0xFF}
+        last_device_error_detail = {"code": code}
+        if rec[1]:  # a wait is described
+            last_device_error_detail.update(block=int(rec[2]), thread=int(rec[3]), barrier_smem_addr=int(rec[4]),
+                                            parity=int(rec[5]) & 0xFF, first_code=(int(rec[5]) >> 8) & 0xFF)
         import sys as _sys
 
-        print(f"device error record: {last_device_error_detail}", file=_sys.stderr)
+        what = ", ".join(text for bit, text in _DEVICE_ERRORS if code & bit)
+        print(f"device error ({what}): {last_device_error_detail}", file=_sys.stderr)
     return code
 
 

@@ -226,3 +226,28 @@ def test_queries_out_need_a_place_for_each_row():
             args["T"] = 1
             assert _call_append(_append(**args), q=None) == skv.SKV_EINVAL
             assert "strides" not in skv.last_error()
+
+
+@pytest.mark.parametrize("record,detail,words", [
+    ((0,) * 8, None, ""),
+    ((8,) + (0,) * 7, {"code": 8}, "a position outside the rotation tables"),
+    ((9, 1, 3, 64, 1024, 1 | 1 << 8, 0, 0),
+     {"code": 9, "block": 3, "thread": 64, "barrier_smem_addr": 1024, "parity": 1, "first_code": 1},
+     "a wait for a tile gave up, a position outside the rotation tables"),
+])
+def test_the_device_error_says_what_it_is(record, detail, words, monkeypatch, capsys):
+    """A position outside the tables is not a wait that gave up, and has no barrier to show."""
+    def fake(rec):
+        for i, x in enumerate(record):
+            rec[i] = x
+        return 0
+
+    class Lib:
+        splitkv_device_error_detail = staticmethod(fake)
+
+    monkeypatch.setattr(skv, "_lib", Lib())
+    monkeypatch.setattr(skv, "last_device_error_detail", None)
+    assert skv.device_error() == record[0]
+    assert skv.last_device_error_detail == detail
+    err = capsys.readouterr().err
+    assert words in err and (err == "") == (record[0] == 0)
