@@ -60,8 +60,8 @@ __device__ __forceinline__ ChunkTiles chunk_tiles(int window, int n_sink, int ca
   t.sinks = min(n_sink, t.hi);
   if (t.sinks >= t.lo) t.lo = 0;  // the sinks reach the window: one range
   t.n_first = t.lo > 0 ? (t.sinks + tile - 1) / tile : 0;
-  t.win = t.lo / tile;
   const int end = (t.hi + tile - 1) / tile;
+  t.win = min(t.lo / tile, end);  // (all rows far behind the last token: no block past the last one)
   if (t.lo > 0 && t.n_first > t.win) t.n_first = t.win;  // a block of both is the window's
   t.n = t.n_first + max(end - t.win, 0);
   return t;

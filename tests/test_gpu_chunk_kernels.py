@@ -57,3 +57,28 @@ def test_scores_of_any_size(kind, d, kernel, power):
     assert clear.double().mean() > 0.5
     tol = (WEIGHT[kernel] if kind == "fp8" else 2.0 ** -8) * size + 2.0 ** -8 * ro.abs()
     assert ((out - ro).abs() <= tol)[clear].all()
+
+
+# ------------------------------------------------------------------ edges, on each kernel
+
+
+def check(c, kernel, window=0, n_sink=0, **kw):
+    out, lse = run(c, kernel, window, n_sink, **kw)
+    R.check_attention(c, out, lse, window, n_sink, kw.get("softmax_scale"), q=kw.get("q"))
+    return out, lse
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("kind,d", TYPES)
+def test_rows_that_see_nothing(kind, d, kernel):
+    c = R.make_case([7, 4, 1, 3], [3, 0, 0, 64], 8, 2, d, fp8=kind == "fp8", seed=3, device=DEV)
+    check(c, kernel)
+    check(c, kernel, window=2, n_sink=1)
+    c["seq_lens"][1] = -5
+    check(c, kernel)
+    c["seq_lens"][3] = 64 + 7  # one page: tokens past it do not exist
+    check(c, kernel)
+    check(c, kernel, window=9, n_sink=1)
+    c["seq_lens"][3] = 2 ** 31 - 1  # all rows lie far behind the last token
+    check(c, kernel)
+    check(c, kernel, window=9, n_sink=1)
