@@ -251,3 +251,27 @@ def test_the_device_error_says_what_it_is(record, detail, words, monkeypatch, ca
     assert skv.last_device_error_detail == detail
     err = capsys.readouterr().err
     assert words in err and (err == "") == (record[0] == 0)
+
+
+@pytest.mark.parametrize("G", [1, 3, 4, 8, 16, 33, 128, 129, 200])
+def test_rows_of_a_kv_head_choose_the_kernel(G):
+    """Up to 32 rows of a KV head (chunk bound times group), or a group above 128 heads: the kernels
+    whose partials are two a CTA and row; more: the tensor cores, whose workspace counts 4 items of
+    up to 256 rows a CTA.  (Tests that name a kernel rely on it.)"""
+    lib = skv.load_library()
+
+    def size(T, longest):
+        n = ctypes.c_size_t(0)
+        d = _chunk(T=T, Hq=4 * G, max_q_len=longest, q_strides=(4 * G * 128, 128))
+        assert lib.attn_chunk_paged_workspace_size(ctypes.byref(d), ctypes.byref(_paged()), ctypes.byref(n)) == 0
+        return n.value
+
+    few = size(4096, 1) if G <= 32 or G > 128 else None
+    for longest in range(1, 60):
+        on_tc = longest * G > 32 and G <= 128
+        if on_tc:  # 608 items of 256 rows, heads of 128, in fp32
+            assert size(4096, longest) > 608 * 256 * 128 * 4
+        else:
+            assert size(4096, longest) == few and few < 608 * 256 * 128
+        assert size(4096, 0) == size(4096, 4096) == size(4096, 10 ** 6)  # no bound: T
+        assert size(longest, 0) == size(longest, longest)
