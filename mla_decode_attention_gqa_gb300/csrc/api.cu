@@ -1297,7 +1297,7 @@ skv_status qk_norm_rope_append(const skv_append_desc* desc, const skv_paged* pag
   a.max_blocks = paged->max_blocks;
   a.scale_block = d.kv_dtype == SKV_KV_FP8_E4M3 ? d.scale_block : kTileN;
   a.eps = desc->eps;
-  e = launch_append(a, desc->d, d.kv_dtype == SKV_KV_FP8_E4M3, static_cast<cudaStream_t>(stream));
+  e = launch_append(a, desc->d, d.kv_dtype == SKV_KV_FP8_E4M3, device_sm_count(), static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "append launch");
   return SKV_OK;
 }

@@ -419,11 +419,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(FP8)) append_kernel(cons
 }
 
 template <int D, bool FP8>
-cudaError_t launch(AppendArgs a, cudaStream_t stream) {
+cudaError_t launch(AppendArgs a, int sms, cudaStream_t stream) {
   const int64_t n_heads = a.Hq + 2 * a.Hkv, pairs = a.T * n_heads;
   // equal runs for the CTAs that are resident at once, of one stage at least; a run touches kMaxTokens tokens at most
-  constexpr int64_t kRuns = 152 * ctas_per_sm(FP8);
-  int64_t steps = (pairs + kGroups * kRuns - 1) / (kGroups * kRuns);
+  const int64_t runs = static_cast<int64_t>(sms) * ctas_per_sm(FP8);
+  int64_t steps = (pairs + kGroups * runs - 1) / (kGroups * runs);
   steps = std::min<int64_t>(steps, std::max<int64_t>(1, (kMaxTokens - 2) * n_heads / kGroups));
   a.steps = static_cast<int>(steps);
   a.fused = a.q_sh == D && a.k_st == a.q_st && a.v_st == a.q_st && a.k_sh == D && a.v_sh == D && a.k == a.q + a.Hq * D &&
@@ -452,9 +452,9 @@ cudaError_t launch(AppendArgs a, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_append(const AppendArgs& a, int32_t d, bool fp8, cudaStream_t stream) {
-  if (d == 64) return launch<64, false>(a, stream);
-  return fp8 ? launch<128, true>(a, stream) : launch<128, false>(a, stream);
+cudaError_t launch_append(const AppendArgs& a, int32_t d, bool fp8, int sms, cudaStream_t stream) {
+  if (d == 64) return launch<64, false>(a, sms, stream);
+  return fp8 ? launch<128, true>(a, sms, stream) : launch<128, false>(a, sms, stream);
 }
 
 }  // namespace skv

@@ -208,7 +208,7 @@ struct AppendArgs {
   float eps;
   unsigned int* err;
 };
-cudaError_t launch_append(const AppendArgs& a, int32_t d, bool fp8, cudaStream_t stream);
+cudaError_t launch_append(const AppendArgs& a, int32_t d, bool fp8, int sms, cudaStream_t stream);
 
 // MLA latent variant (dk = 576 latent+rope, dv = 512, one shared latent "head").
 // Tiles are 32 tokens; the tensor map's box is 64 elements x 32 tokens.
