@@ -405,13 +405,19 @@ skv_status gqa_decode_attn_passq(const skv_desc* desc, int32_t n_ranks, const vo
  *            the softmax denominator, so that results merge (attn_merge_lse).  A row that sees
  *            nothing (seq_lens[b] < n) gets out = 0, lse = -inf
  *   workspace  attn_chunk_paged_workspace_size() bytes, 256-byte aligned
- * desc->max_q_len bounds the sequences' new tokens (0: T): it chooses the kernel, the result
- * does not depend on it.  Shapes: bf16 pages with d = 64 or 128, fp8-e4m3 pages with d = 128; any
- * Hq multiple of Hkv.  A value that no row of a 64- or 128-token tile sees never counts, whatever
+ * desc->max_q_len bounds the sequences' new tokens (0: T): it chooses the kernel, and the result
+ * depends on it within the rounding below only.  Give it for decode steps and proposed tokens:
+ * without it they are taken for chunks of T (64 sequences of one token, 64 / 8 heads: 445 us
+ * instead of 373; 16 over fp8 pages, 128 / 8 heads: 488 instead of 216).  Shapes: bf16 pages
+ * with d = 64 or 128, fp8-e4m3 pages with d = 128; any Hq multiple of Hkv, but groups above 128
+ * heads have the kernel for few rows alone, which reads the pages once for 32 rows (prompts of up
+ * to 1000 tokens: 1110 us with 136 heads of one KV head, 194 with 128).  A value that no row of a 64- or 128-token tile sees never counts, whatever
  * it holds; a NaN or infinity in a V row, or in the scales of a block, that one row of a row tile
  * sees may also reach the rows of that row tile that do not see it.
  * Rounding: scores, sums and the weighted sum in fp32; the softmax weights once, to bf16 (fp8
- * pages: weight times V scale, to bf16, or with few rows to fp16), the output to bf16.  fp8 codes
+ * pages: weight times V scale, to bf16, or for up to 32 rows of a KV head to fp16, in which weights
+ * below 2^-18 of the largest of their 64 tokens may lose bits), the output to bf16.  Values of V
+ * are taken up to 2^100.  fp8 codes
  * are exact; with fp8 pages, of q what lies below 2^-17 of its row's (token's and head's) largest
  * magnitude may be lost, and a row of q with an infinity or a NaN gives a row of NaN.
  * Errors: SKV_EINVAL, SKV_EUNSUPPORTED and SKV_EWORKSPACE as for gqa_decode_attn_paged, and

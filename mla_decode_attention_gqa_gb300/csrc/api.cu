@@ -1090,9 +1090,9 @@ skv_status chunk_plan(const skv_chunk_desc* c, const skv_desc* d, ChunkPlan* pl)
   const int G = d->Hq / d->Hkv;
   // The caller's bound on the chunk lengths chooses the kernel (results do not depend on it): up
   // to 16 rows of a KV head fill an mma.sync tile, where the tensor cores' 128 are mostly padding
-  // (decode of 64 sequences, 64 / 8 heads: 377 us against 457, fp8 224 against 491), up to 32 two
-  // (24 sequences of 5 rows, 40 / 8 heads: 93 us against 115, fp8 92 against 154); a group above
-  // 128 heads has no query tile there.
+  // (decode of 64 sequences, 64 / 8 heads: 373 us against 445; 16 over fp8 pages, 128 / 8: 216 against
+  // 488), up to 32 two (24 sequences of 5 rows, 40 / 8 heads: 90 us against 112, fp8 90 against 153); a
+  // group above 128 heads has no query tile there.
   const int64_t longest = c->max_q_len > 0 ? std::min(c->max_q_len, c->T) : c->T;
   pl->tc = longest * G > 32 && G <= 128;
   pl->group_rows = pl->tc ? padded_group(G) : G;

@@ -187,7 +187,8 @@ __global__ void __launch_bounds__(32 * kRowsPerBlock)
   const int c = blockIdx.x + 1;
   ChunkRuns runs;
   ChunkShare sh;
-  // (reads lengths only: under the attention kernel's end)
+  // (reads lengths only, which were there before the attention kernel; its CTAs start as those of that
+  // kernel leave)
   const bool any = chunk_find_runs<32 * kRowsPerBlock>(a, a.n_wave, c, &runs, &sh);
   const int tile = any ? runs.s : 0;
   // the attention kernel before it on the stream is complete and its writes are visible (also where

@@ -633,8 +633,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   }
 }
 
-// (two sets with bf16 heads of 128: 5 warps a set have 168 registers each, too few: 126 us for 24
-// sequences of 5 rows, 40 / 8 heads, where 3 warps of 233 take 117; the other two fit, fp8 159 -> 137)
+// (two sets with bf16 heads of 128: 5 warps a set have 168 registers each, too few: 95 us for 24
+// sequences of 5 rows, 40 / 8 heads, where 3 warps of 233 take 90; the other two fit, fp8 104 -> 90)
 template <int WM>
 using CfgBf16D64 = RowsCfg<false, 64, WM, WM == 1 ? 4 : 5, WM == 1 ? 6 : 12>;
 template <int WM>

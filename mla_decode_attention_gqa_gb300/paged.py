@@ -36,7 +36,8 @@ def chunk_step(qkv, Hq, Hkv, k_pages, v_pages, seq_lens, cu_q, block_table, *, c
                k_scale=None, v_scale=None, softmax_scale=None, scale_block=64, out=None, lse=None):
     """Append the packed new tokens to the pages and attend: returns (out bf16 [T,Hq,d], lse
     fp32 [T,Hq]).  seq_lens counts the new tokens; the arguments are those of
-    qk_norm_rope_append and attn_chunk_paged."""
+    qk_norm_rope_append and attn_chunk_paged (max_q_len = 1 for a decode step: without it the
+    attention takes a kernel for long chunks)."""
     q, k, v = split_qkv(qkv, Hq, Hkv)
     q = qk_norm_rope_append(q, k, v, k_pages, v_pages, seq_lens, cu_q, block_table, cos=cos, sin=sin,
                             q_weight=q_weight, k_weight=k_weight, eps=eps, positions=positions,
