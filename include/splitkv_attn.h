@@ -86,7 +86,11 @@ typedef enum {
   SKV_EWORKSPACE = -4    /* workspace missing or smaller than the matching *_workspace_size */
 } skv_status;
 
-typedef enum { SKV_KV_BF16 = 0, SKV_KV_FP8_E4M3 = 1 } skv_kv_dtype;
+typedef enum {
+  SKV_KV_BF16 = 0,
+  SKV_KV_FP8_E4M3 = 1,
+  SKV_KV_FP4_E2M1 = 2 /* pages of the chunk calls that take skv_fp4_scales only */
+} skv_kv_dtype;
 
 /* causal_offset that masks nothing */
 #define SKV_NO_CAUSAL ((int64_t)1 << 62)
@@ -496,6 +500,107 @@ skv_status qk_norm_rope_append(const skv_append_desc* desc, const skv_paged* pag
                                const float* sin, const int32_t* positions, const int32_t* cu_q,
                                const int32_t* seq_lens, const float* k_scale, const float* v_scale, void* q_out,
                                void* k_pages, void* v_pages, void* stream);
+
+/*
+ * 4-bit pages (kv_dtype SKV_KV_FP4_E2M1, d = 128): 0.5625 bytes a value, quantised as they are
+ * written, with no calibration.  A page row of one KV head and token is d / 2 bytes of e2m1 codes
+ * (dim 2 i in the low half of byte i, dim 2 i + 1 in the high half; the values 0, 0.5, 1, 1.5, 2, 3, 4, 6
+ * and their negatives) with one e4m3 scale for each 16 dims, and a KV head may have an fp32 scale:
+ *   value = code * block scale * head scale.
+ * desc strides of such pages are in bytes.
+ *   k_block, v_block  e4m3 [num_blocks][Hkv][block_len][d / 16], contiguous, 16-byte aligned
+ *   k_head, v_head    fp32 [Hkv], or NULL: 1.  For heads whose magnitudes lie far from 1 (a block scale
+ *                     holds 2^-9 to 448); one outside [2^-64, 2^64] stands for zeros
+ * All pointers are device pointers; the struct itself is read by the host during the call.
+ */
+typedef struct {
+  void* k_block;
+  void* v_block;
+  const float* k_head;
+  const float* v_head;
+} skv_fp4_scales;
+
+/*
+ * qk_norm_rope_append_fp4 -- qk_norm_rope_append into 4-bit pages.  Of each 16 dims of a new token's
+ * key (after norm and rotation) or value y, with h the head's scale:
+ *   s = e4m3(max |y| / (6 h)),  code = e2m1(y / (s h)),
+ * to the nearest, ties to the even code; s saturates at 448 and a code at +-6; s = 0 stores zeros.  A
+ * NaN among the 16 makes s NaN, and all of them read as NaN.  Everything else as
+ * qk_norm_rope_append (the page strides, in bytes, are multiples of 16).
+ *
+ * attn_chunk_paged_fp4 -- attn_chunk_paged over 4-bit pages (attn_chunk_paged_workspace_size gives
+ * its workspace).  Codes times block scales are exact in the products; the head scales multiply
+ * scores and outputs in fp32.
+ */
+skv_status qk_norm_rope_append_fp4(const skv_append_desc* desc, const skv_paged* paged, const skv_fp4_scales* fp4,
+                                   const void* q, const void* k, const void* v, const void* q_weight,
+                                   const void* k_weight, const float* cos, const float* sin, const int32_t* positions,
+                                   const int32_t* cu_q, const int32_t* seq_lens, void* q_out, void* k_pages,
+                                   void* v_pages, void* stream);
+skv_status attn_chunk_paged_fp4(const skv_chunk_desc* desc, const skv_paged* paged, const skv_fp4_scales* fp4,
+                                const void* q, const void* k_pages, const void* v_pages, const int32_t* cu_q,
+                                const int32_t* seq_lens, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/*
+ * kv_read_paged -- tokens of a paged cache as packed bf16 rows, to go round a ring
+ * (attn_ring_step takes them as a block), to another cache or another rank.  Packed row
+ * cu_tokens[b] + i is token starts[b] + i of sequence b; all pages formats, dequantised in fp32 and
+ * rounded once (bf16 pages: copied).
+ *   k_pages, v_pages, k_scale, v_scale  as for attn_chunk_paged;  fp4: for 4-bit pages, else NULL
+ *   cu_tokens  int32 [B + 1], non-decreasing: rows at or past cu_tokens[B] and before cu_tokens[0]
+ *              are left as they were
+ *   starts     int32 [B], or NULL: 0
+ *   k_out, v_out  bf16 [T][Hkv][d] with (token, head) strides, a place of its own for every row,
+ *              strides multiples of 8 elements
+ * A token before 0 or past max_blocks * block_len, or whose table entry lies outside
+ * [0, num_blocks), reads as zeros.  T = 0 does nothing.  Errors as qk_norm_rope_append.
+ */
+typedef struct {
+  int32_t B, T, Hkv, d;
+  int32_t kv_dtype;        /* skv_kv_dtype of the pages */
+  int32_t scale_block;     /* fp8 only */
+  int64_t k_page_strides[3], v_page_strides[3]; /* (page, KV head, token) */
+  int64_t k_out_strides[2], v_out_strides[2];   /* (token, head) */
+} skv_read_desc;
+
+skv_status kv_read_paged(const skv_read_desc* desc, const skv_paged* paged, const skv_fp4_scales* fp4,
+                         const void* k_pages, const void* v_pages, const float* k_scale, const float* v_scale,
+                         const int32_t* cu_tokens, const int32_t* starts, void* k_out, void* v_out, void* stream);
+
+/*
+ * attn_shared_prefix_paged -- attn_chunk_paged for a batch whose sequences begin with the same pages
+ * (one system prompt or document, several samples of one prompt): the shared tokens are attended
+ * once for all rows of a group of sequences, the rest of each sequence by itself, and the two parts
+ * join exactly by their lse.  The result is that of attn_chunk_paged on the same arguments, within its
+ * rounding, whatever the groups are; only the time depends on them.
+ *   cu_groups    int32 [n_groups + 1], non-decreasing: group j is the sequences cu_groups[j] ..
+ *                cu_groups[j + 1] (none allowed); sequences of no group share nothing
+ *   prefix_lens  int32 [n_groups]: the first prefix_lens[j] tokens of the group's sequences lie in the
+ *                same pages, i.e. those entries of their block_table rows are the same (of sequences
+ *                with new tokens: others are not looked at).  The library shares them in whole tiles of
+ *                64 tokens, as far as every new token of the group sees them
+ *   max_group_rows  no group has more new tokens (0: T): chooses the kernel of the shared part, as
+ *                desc->max_q_len that of the rest
+ * The arrays are device memory, read by the kernels only, so that one captured graph serves any
+ * lengths and groups; the struct itself is read by the host during the call.  All page formats (fp4:
+ * the scales of 4-bit pages, else NULL).  desc->window and n_sink must be 0.  Errors otherwise as
+ * attn_chunk_paged.
+ */
+typedef struct {
+  int32_t n_groups;
+  int32_t max_group_rows;
+  const int32_t* cu_groups;
+  const int32_t* prefix_lens;
+} skv_shared_desc;
+
+skv_status attn_shared_prefix_paged_workspace_size(const skv_chunk_desc* desc, const skv_paged* paged,
+                                                   const skv_shared_desc* shared, size_t* bytes);
+skv_status attn_shared_prefix_paged(const skv_chunk_desc* desc, const skv_paged* paged, const skv_shared_desc* shared,
+                                    const skv_fp4_scales* fp4, const void* q, const void* k_pages, const void* v_pages,
+                                    const float* k_scale, const float* v_scale, const int32_t* cu_q,
+                                    const int32_t* seq_lens, void* out, float* lse, void* workspace,
+                                    size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -19,7 +19,15 @@ plus the position-masked (_pos), paged (_paged) and pass-KV ring-step variants, 
 ragged chunks of new tokens over a paged cache
   qk_norm_rope_append(q, k, v, k_pages, v_pages, seq_lens, cu_q, block_table, ...) -> q_out
   attn_chunk_paged(q, k_pages, v_pages, seq_lens, cu_q, block_table, ...) -> (out, lse)
-  (paged.chunk_step: both, from the fused projection's output)
+  attn_shared_prefix_paged(..., cu_groups, prefix_lens) -> (out, lse)   (sequences whose first pages
+                           are the same: those attended once a group)
+  kv_read_paged(k_pages, v_pages, cu_tokens, block_table, ...) -> (k, v)   (tokens back out of the pages)
+  (paged.chunk_step: append and attention, from the fused projection's output)
+
+Pages are bf16 [num_blocks,Hkv,block_len,d]; e4m3 codes of that shape with scales fp32
+[num_blocks,Hkv,block_len/scale_block]; or, for the paged chunk calls, 4-bit: uint8 (or
+float4_e2m1fn_x2) [num_blocks,Hkv,block_len,d/2], two e2m1 codes a byte, with e4m3 scales
+[num_blocks,Hkv,block_len,d/16] and optional fp32 scales [Hkv] (paged.fp4_pages makes them).
 """
 
 import ctypes
@@ -37,7 +45,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libsplitkv_attn.so")
 
 SKV_OK, SKV_EINVAL, SKV_EUNSUPPORTED, SKV_ECUDA, SKV_EWORKSPACE = 0, -1, -2, -3, -4
-SKV_KV_BF16, SKV_KV_FP8_E4M3 = 0, 1
+SKV_KV_BF16, SKV_KV_FP8_E4M3, SKV_KV_FP4_E2M1 = 0, 1, 2
 SKV_WEIGHT_BF16, SKV_WEIGHT_FP32 = 0, 1
 _STATUS = {0: "SKV_OK", -1: "SKV_EINVAL", -2: "SKV_EUNSUPPORTED", -3: "SKV_ECUDA", -4: "SKV_EWORKSPACE"}
 
@@ -66,6 +74,11 @@ EXPORTED_SYMBOLS = (
     "attn_chunk_paged_workspace_size",
     "attn_chunk_paged",
     "qk_norm_rope_append",
+    "qk_norm_rope_append_fp4",
+    "attn_chunk_paged_fp4",
+    "kv_read_paged",
+    "attn_shared_prefix_paged_workspace_size",
+    "attn_shared_prefix_paged",
 )
 
 # Every symbol declared in include/splitkv_attn_selftest.h (hardware self-tests).
@@ -154,6 +167,17 @@ def _load():
     lib.attn_chunk_paged.restype = I32
     lib.qk_norm_rope_append.argtypes = [ctypes.POINTER(SkvAppendDesc), PG] + [P] * 16
     lib.qk_norm_rope_append.restype = I32
+    F, S = ctypes.POINTER(SkvFp4Scales), ctypes.POINTER(SkvSharedDesc)
+    lib.qk_norm_rope_append_fp4.argtypes = [ctypes.POINTER(SkvAppendDesc), PG, F] + [P] * 14
+    lib.qk_norm_rope_append_fp4.restype = I32
+    lib.attn_chunk_paged_fp4.argtypes = [C, PG, F] + [P] * 8 + [SZ, P]
+    lib.attn_chunk_paged_fp4.restype = I32
+    lib.kv_read_paged.argtypes = [ctypes.POINTER(SkvReadDesc), PG, F] + [P] * 9
+    lib.kv_read_paged.restype = I32
+    lib.attn_shared_prefix_paged_workspace_size.argtypes = [C, PG, S, ctypes.POINTER(SZ)]
+    lib.attn_shared_prefix_paged_workspace_size.restype = I32
+    lib.attn_shared_prefix_paged.argtypes = [C, PG, S, F] + [P] * 10 + [SZ, P]
+    lib.attn_shared_prefix_paged.restype = I32
     return lib
 
 
@@ -261,8 +285,32 @@ class SkvAppendDesc(ctypes.Structure):
     ]
 
 
+class SkvFp4Scales(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_block", "v_block", "k_head", "v_head")]
+
+
+class SkvReadDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "Hkv", "d", "kv_dtype", "scale_block")] + [
+        ("k_page_strides", ctypes.c_int64 * 3),
+        ("v_page_strides", ctypes.c_int64 * 3),
+        ("k_out_strides", ctypes.c_int64 * 2),
+        ("v_out_strides", ctypes.c_int64 * 2),
+    ]
+
+
+class SkvSharedDesc(ctypes.Structure):
+    _fields_ = [
+        ("n_groups", ctypes.c_int32),
+        ("max_group_rows", ctypes.c_int32),
+        ("cu_groups", ctypes.c_void_p),
+        ("prefix_lens", ctypes.c_void_p),
+    ]
+
+
 _CHUNK_FIELDS = struct.Struct("@8if2i8q")
 _APPEND_FIELDS = struct.Struct("@10if17q")
+_READ_FIELDS = struct.Struct("@6i10q")
+_FP4_CODES = (torch.uint8, getattr(torch, "float4_e2m1fn_x2", torch.uint8))
 
 
 def _described(kind, fields, *values):
@@ -701,14 +749,15 @@ def _check_chunk(q, k_pages, v_pages, seq_lens, cu_q, block_table, k_scale, v_sc
         raise ValueError("the head dim must be unit-stride")
     T, Hq, hd = q.shape
     nb, Hkv, L, hd2 = k_pages.shape
-    if hd2 != hd or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
+    fp4 = 2 * hd2 == hd and k_pages.dtype in _FP4_CODES
+    if (hd2 != hd and not fp4) or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
         raise ValueError("q / k_pages / v_pages shapes or dtypes disagree")
     if block_table.dtype != torch.int32 or block_table.dim() != 2 or not block_table.is_contiguous():
         raise ValueError("block_table must be contiguous int32 [B, max_blocks]")
     B, max_blocks = block_table.shape
     _check_lens(seq_lens, B, "seq_lens")
     _check_lens(cu_q, B + 1, "cu_q")
-    kv = _kv_dtype(k_pages)
+    kv = SKV_KV_FP4_E2M1 if fp4 else _kv_dtype(k_pages)
     if kv == SKV_KV_FP8_E4M3:
         _elsewhere(q, k_scale, v_scale)
         if scale_block > 0:
@@ -716,23 +765,62 @@ def _check_chunk(q, k_pages, v_pages, seq_lens, cu_q, block_table, k_scale, v_sc
     return B, T, Hq, Hkv, hd, kv, SkvPaged(L, max_blocks, nb, block_table.data_ptr())
 
 
+def _fp4_scales(kv, pages, hd, k_scale, v_scale, k_head_scale, v_head_scale):
+    """The scales of 4-bit pages, checked: block scales e4m3 (or their bytes) [num_blocks, Hkv, block_len,
+    d / 16], head scales fp32 [Hkv] or None.  None for other pages, which have no head scales."""
+    if kv != SKV_KV_FP4_E2M1:
+        if k_head_scale is not None or v_head_scale is not None:
+            raise ValueError("k_head_scale and v_head_scale go with 4-bit pages")
+        return None
+    nb, Hkv, L, _ = pages.shape
+    shape, dev = (nb, Hkv, L, hd // 16), pages.device
+    for t in (k_scale, v_scale):
+        if t is None or t.device != dev or t.dtype not in (torch.float8_e4m3fn, torch.uint8) or t.shape != shape \
+                or not t.is_contiguous():
+            raise ValueError(f"4-bit pages need k_scale and v_scale: contiguous e4m3 [num_blocks, Hkv, block_len, d / 16] "
+                             f"= {shape} on {dev}")
+    for t in (k_head_scale, v_head_scale):
+        if t is not None and (t.device != dev or t.dtype != torch.float32 or t.shape != (Hkv,) or not t.is_contiguous()):
+            raise ValueError(f"head scales must be contiguous float32 ({Hkv},) on {dev}")
+    return SkvFp4Scales(k_scale.data_ptr(), v_scale.data_ptr(), _addr(k_head_scale), _addr(v_head_scale))
+
+
 @_on_tensor_device
 def attn_chunk_paged(q, k_pages, v_pages, seq_lens, cu_q, block_table, max_q_len=None, window=0, n_sink=0,
                      k_scale=None, v_scale=None, softmax_scale=None, scale_block=64, out=None, lse=None,
-                     workspace=None):
+                     workspace=None, k_head_scale=None, v_head_scale=None):
     """Attention of ragged chunks of new tokens over a paged cache: q packed [T,Hq,d], rows
     cu_q[b] .. cu_q[b+1] the last new tokens of sequence b's seq_lens[b] cached ones; causal, or
     with a sliding window of ``window`` tokens and the first ``n_sink`` tokens.  max_q_len (the
     longest chunk) chooses the kernel; results agree within their rounding.  Give it for decode
     steps (1) and proposed tokens: without it T stands in, and a decode step takes 1.2 times as
-    long, over fp8 pages 2.3 times.  Returns (out bf16 [T,Hq,d], lse fp32 [T,Hq]); rows of no
-    sequence are left as they were."""
+    long, over fp8 pages 2.3 times.  4-bit pages take their block scales as k_scale / v_scale, and
+    head scales.  Returns (out bf16 [T,Hq,d], lse fp32 [T,Hq]); rows of no sequence are left as they
+    were."""
     B, T, Hq, Hkv, hd, kv, pg = _check_chunk(q, k_pages, v_pages, seq_lens, cu_q, block_table, k_scale, v_scale,
                                              scale_block)
+    fp4 = _fp4_scales(kv, k_pages, hd, k_scale, v_scale, k_head_scale, v_head_scale)
     d = _described(SkvChunkDesc, _CHUNK_FIELDS, B, T, Hq, Hkv, hd, window, n_sink, max_q_len or 0,
                    1.0 / math.sqrt(hd) if softmax_scale is None else softmax_scale, kv, scale_block,
                    *q.stride()[:2], *k_pages.stride()[:3], *v_pages.stride()[:3])
     dev = q.device
+    out, lse = _chunk_out(out, lse, T, Hq, hd, dev)
+    n = ctypes.c_size_t(0)
+    _check(_lib.attn_chunk_paged_workspace_size(d, pg, n))
+    workspace, ws_bytes = _chunk_ws(workspace, n.value, dev)
+    if fp4 is not None:
+        _check(_lib.attn_chunk_paged_fp4(d, pg, fp4, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                                         cu_q.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                                         workspace.data_ptr(), ws_bytes, _raw_stream(dev)))
+        return out, lse
+    _check(_lib.attn_chunk_paged(d, pg, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _addr(k_scale),
+                                 _addr(v_scale), cu_q.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                                 workspace.data_ptr(), ws_bytes, _raw_stream(dev)))
+    return out, lse
+
+
+def _chunk_out(out, lse, T, Hq, hd, dev):
+    """The outputs of a chunk call: the caller's, checked, or new ones."""
     if out is None:
         out = torch.empty((T, Hq, hd), dtype=torch.bfloat16, device=dev)
     else:
@@ -741,18 +829,103 @@ def attn_chunk_paged(q, k_pages, v_pages, seq_lens, cu_q, block_table, max_q_len
         lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
     else:
         _out(lse, (T, Hq), torch.float32, dev, "lse")
-    n = ctypes.c_size_t(0)
-    _check(_lib.attn_chunk_paged_workspace_size(d, pg, n))
-    if workspace is None:
-        # from torch's stream-ordered allocator at each call (in a capture: the graph's own
-        # pool), so that neither two streams nor two graphs share it
-        workspace, ws_bytes = torch.empty(n.value, dtype=torch.uint8, device=dev), n.value
-    else:
-        workspace, ws_bytes = _ws_arg(workspace, n.value, dev)
-    _check(_lib.attn_chunk_paged(d, pg, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), _addr(k_scale),
-                                 _addr(v_scale), cu_q.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                                 workspace.data_ptr(), ws_bytes, _raw_stream(dev)))
     return out, lse
+
+
+def _chunk_ws(workspace, nbytes, dev):
+    """(buffer, bytes) of a chunk call's workspace: the caller's, or from torch's stream-ordered
+    allocator at each call (in a capture: the graph's own pool), so that neither two streams nor two
+    graphs share it."""
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev), nbytes
+    return _ws_arg(workspace, nbytes, dev)
+
+
+@_on_tensor_device
+def attn_shared_prefix_paged(q, k_pages, v_pages, seq_lens, cu_q, block_table, cu_groups, prefix_lens, max_q_len=None,
+                             max_group_rows=None, k_scale=None, v_scale=None, softmax_scale=None, scale_block=64,
+                             out=None, lse=None, workspace=None, k_head_scale=None, v_head_scale=None):
+    """attn_chunk_paged (causal) for a batch whose sequences begin with the same pages: those are
+    attended once for all rows of a group of sequences, and the rest of each sequence by itself.
+    cu_groups int32 [n_groups + 1]: group j is the sequences cu_groups[j] .. cu_groups[j+1];
+    prefix_lens int32 [n_groups]: its first prefix_lens[j] tokens lie in the same pages (the same
+    entries of block_table), which is the caller's word.  Any groups give the result of attn_chunk_paged,
+    within its rounding; only the time depends on them.  max_q_len and max_group_rows (the most
+    new tokens of a sequence, and of a group) choose the kernels.  Returns (out, lse)."""
+    B, T, Hq, Hkv, hd, kv, pg = _check_chunk(q, k_pages, v_pages, seq_lens, cu_q, block_table, k_scale, v_scale,
+                                             scale_block)
+    fp4 = _fp4_scales(kv, k_pages, hd, k_scale, v_scale, k_head_scale, v_head_scale)
+    _elsewhere(q, cu_groups, prefix_lens)
+    if prefix_lens.dim() != 1:
+        raise ValueError("prefix_lens must be int32 [n_groups]")
+    n_groups = prefix_lens.shape[0]
+    _check_lens(prefix_lens, n_groups, "prefix_lens")
+    _check_lens(cu_groups, n_groups + 1, "cu_groups")
+    d = _described(SkvChunkDesc, _CHUNK_FIELDS, B, T, Hq, Hkv, hd, 0, 0, max_q_len or 0,
+                   1.0 / math.sqrt(hd) if softmax_scale is None else softmax_scale, kv, scale_block,
+                   *q.stride()[:2], *k_pages.stride()[:3], *v_pages.stride()[:3])
+    group_rows = max_group_rows or 0
+    if not -(1 << 31) <= group_rows < 1 << 31:
+        raise ValueError("max_group_rows does not fit its field")
+    shared = SkvSharedDesc(n_groups, group_rows, cu_groups.data_ptr(), prefix_lens.data_ptr())
+    dev = q.device
+    out, lse = _chunk_out(out, lse, T, Hq, hd, dev)
+    n = ctypes.c_size_t(0)
+    _check(_lib.attn_shared_prefix_paged_workspace_size(d, pg, shared, n))
+    workspace, ws_bytes = _chunk_ws(workspace, n.value, dev)
+    block = fp4 is None
+    _check(_lib.attn_shared_prefix_paged(d, pg, shared, fp4, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                                         _addr(k_scale) if block else None, _addr(v_scale) if block else None,
+                                         cu_q.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                                         workspace.data_ptr(), ws_bytes, _raw_stream(dev)))
+    return out, lse
+
+
+@_on_tensor_device
+def kv_read_paged(k_pages, v_pages, cu_tokens, block_table, n_tokens=None, starts=None, k_scale=None, v_scale=None,
+                  scale_block=64, k_head_scale=None, v_head_scale=None, k_out=None, v_out=None):
+    """Tokens of a paged cache as packed bf16 rows [T,Hkv,d]: rows cu_tokens[b] .. cu_tokens[b+1] are
+    sequence b's tokens from starts[b] on (None: 0), dequantised from fp8 or 4-bit pages (scales as for
+    attn_chunk_paged).  T is n_tokens, or that of k_out and v_out (any token and head strides; rows
+    of no sequence are left as they were).  Returns (k, v): k.transpose(0, 1)[None] is a block of
+    attn_ring_step."""
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype:
+        raise ValueError("k_pages and v_pages must be [num_blocks,Hkv,block_len,..] of one shape and dtype")
+    if k_pages.stride(3) != 1 or v_pages.stride(3) != 1:
+        raise ValueError("the head dim must be unit-stride")
+    _elsewhere(k_pages, v_pages, cu_tokens, block_table, starts, k_scale, v_scale, k_out, v_out)
+    nb, Hkv, L, hd = k_pages.shape
+    if k_pages.dtype in _FP4_CODES and k_scale is not None and k_scale.dim() == 4:
+        kv, hd = SKV_KV_FP4_E2M1, 2 * hd
+    else:
+        kv = _kv_dtype(k_pages)
+        if kv == SKV_KV_FP8_E4M3 and scale_block > 0:
+            _check_scales((k_scale, v_scale), (nb, Hkv, L // scale_block), "[num_blocks, Hkv, block_len / scale_block]")
+    fp4 = _fp4_scales(kv, k_pages, hd, k_scale, v_scale, k_head_scale, v_head_scale)
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or not block_table.is_contiguous():
+        raise ValueError("block_table must be contiguous int32 [B, max_blocks]")
+    B, max_blocks = block_table.shape
+    _check_lens(cu_tokens, B + 1, "cu_tokens")
+    if starts is not None:
+        _check_lens(starts, B, "starts")
+    if (k_out is None) != (v_out is None):
+        raise ValueError("k_out and v_out go together")
+    dev = k_pages.device
+    if k_out is None:
+        if n_tokens is None:
+            raise ValueError("n_tokens (the packed rows) is needed without k_out and v_out")
+        k_out, v_out = (torch.empty((n_tokens, Hkv, hd), dtype=torch.bfloat16, device=dev) for _ in range(2))
+    T = k_out.shape[0] if n_tokens is None else n_tokens
+    for t in (k_out, v_out):
+        if t.dtype != torch.bfloat16 or t.shape != (T, Hkv, hd) or t.stride(2) != 1:
+            raise ValueError(f"k_out and v_out must be bf16 ({T}, {Hkv}, {hd}) with a unit-stride head dim")
+    d = _described(SkvReadDesc, _READ_FIELDS, B, T, Hkv, hd, kv, scale_block, *k_pages.stride()[:3],
+                   *v_pages.stride()[:3], *k_out.stride()[:2], *v_out.stride()[:2])
+    block = fp4 is None
+    _check(_lib.kv_read_paged(d, SkvPaged(L, max_blocks, nb, block_table.data_ptr()), fp4, k_pages.data_ptr(),
+                              v_pages.data_ptr(), _addr(k_scale) if block else None, _addr(v_scale) if block else None,
+                              cu_tokens.data_ptr(), _addr(starts), k_out.data_ptr(), v_out.data_ptr(), _raw_stream(dev)))
+    return k_out, v_out
 
 
 def _raw_stream(dev):
@@ -777,16 +950,19 @@ def _head_stride(w, heads, hd, dev, name):
 @_on_tensor_device
 def qk_norm_rope_append(q, k, v, k_pages, v_pages, seq_lens, cu_q, block_table, cos=None, sin=None, q_weight=None,
                         k_weight=None, eps=1e-6, positions=None, interleaved=False, k_scale=None, v_scale=None,
-                        scale_block=64, q_out=None):
+                        scale_block=64, q_out=None, k_head_scale=None, v_head_scale=None):
     """The new tokens on their way into the cache: RMS norm of every query and key head
     (weights [d] or [H,d], bf16 or fp32; None: no norm), rotation by the tables cos / sin fp32
     [max_pos, rot/2] (None: none; halves, or interleaved pairs), keys and values into the pages
     at each token's place in its sequence, queries to q_out (new, or the caller's strided bf16
     [T,Hq,d], q itself included).  q / k / v are packed [T,H,d] views, e.g. of one fused
     projection; positions int32 [T] replaces the place in the sequence as the tables' row; fp8
-    pages take codes by the scales already in k_scale / v_scale.  Returns q_out."""
+    pages take codes by the scales already in k_scale / v_scale; 4-bit pages take codes and, into
+    k_scale / v_scale, the scales of their blocks of 16 dims (times k_head_scale / v_head_scale fp32
+    [Hkv], where given).  Returns q_out."""
     B, T, Hq, Hkv, hd, kv, pg = _check_chunk(q, k_pages, v_pages, seq_lens, cu_q, block_table, k_scale, v_scale,
                                              scale_block)
+    fp4 = _fp4_scales(kv, k_pages, hd, k_scale, v_scale, k_head_scale, v_head_scale)
     dev = q.device
     i = q.get_device()
     if not i == k.get_device() == v.get_device():
@@ -824,6 +1000,12 @@ def qk_norm_rope_append(q, k, v, k_pages, v_pages, seq_lens, cu_q, block_table, 
                    SKV_WEIGHT_BF16 if wdtype == bf16 else SKV_WEIGHT_FP32, kv, scale_block, eps, max_pos,
                    *q.stride()[:2], *k.stride()[:2], *v.stride()[:2], *q_out.stride()[:2], q_ws, k_ws,
                    *k_pages.stride()[:3], *v_pages.stride()[:3])
+    if fp4 is not None:
+        _check(_lib.qk_norm_rope_append_fp4(d, pg, fp4, q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(q_weight),
+                                            _addr(k_weight), _addr(cos), _addr(sin), _addr(positions), cu_q.data_ptr(),
+                                            seq_lens.data_ptr(), q_out.data_ptr(), k_pages.data_ptr(),
+                                            v_pages.data_ptr(), _raw_stream(dev)))
+        return q_out
     _check(_lib.qk_norm_rope_append(d, pg, q.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(q_weight), _addr(k_weight),
                                     _addr(cos), _addr(sin), _addr(positions), cu_q.data_ptr(), seq_lens.data_ptr(),
                                     _addr(k_scale), _addr(v_scale), q_out.data_ptr(), k_pages.data_ptr(),
@@ -851,6 +1033,8 @@ __all__ = [
     "gqa_decode_attn_passq",
     "qk_norm_rope_append",
     "attn_chunk_paged",
+    "attn_shared_prefix_paged",
+    "kv_read_paged",
     "attn_partial",
     "attn_partial_paged",
     "gqa_decode_attn_paged",
@@ -868,6 +1052,9 @@ __all__ = [
     "SkvPaged",
     "SkvChunkDesc",
     "SkvAppendDesc",
+    "SkvFp4Scales",
+    "SkvReadDesc",
+    "SkvSharedDesc",
     "LIB_PATH",
     "load_library",
     "EXPORTED_SYMBOLS",

@@ -143,8 +143,8 @@ bool is_gqa_shape(const skv_desc* d) {
 }
 
 // Shape, dtype and stride checks of a call (the split bounds live in device memory and are
-// never read on the host).
-skv_status validate(const skv_desc* d, int32_t n_split) {
+// never read on the host).  fp4: the call takes 4-bit pages too, whose strides are in bytes.
+skv_status validate(const skv_desc* d, int32_t n_split, bool fp4 = false) {
   if (!d) return fail(SKV_EINVAL, "desc is NULL");
   if (d->B <= 0 || d->Tq <= 0 || d->Hq <= 0 || d->Hkv <= 0 || d->dk <= 0 || d->dv <= 0)
     return fail(SKV_EINVAL, "B, Tq, Hq, Hkv, dk, dv must be positive");
@@ -152,7 +152,9 @@ skv_status validate(const skv_desc* d, int32_t n_split) {
   if (d->S_max <= 0 || d->S_max >= (int64_t(1) << 31)) return fail(SKV_EINVAL, "S_max must be in [1, 2^31)");
   if (!std::isfinite(d->softmax_scale) || d->softmax_scale == 0.f)
     return fail(SKV_EINVAL, "softmax_scale must be finite and non-zero");
-  if (d->kv_dtype != SKV_KV_BF16 && d->kv_dtype != SKV_KV_FP8_E4M3) return fail(SKV_EINVAL, "unknown kv_dtype");
+  const bool is_fp4 = d->kv_dtype == SKV_KV_FP4_E2M1;
+  if (d->kv_dtype != SKV_KV_BF16 && d->kv_dtype != SKV_KV_FP8_E4M3 && !(fp4 && is_fp4))
+    return fail(SKV_EINVAL, "unknown kv_dtype");
   if (d->kv_dtype == SKV_KV_FP8_E4M3 && (d->scale_block <= 0 || d->scale_block % kTileN))
     return fail(SKV_EINVAL, "scale_block must be a positive multiple of 64 for fp8 KV");
   if (n_split < 1) return fail(SKV_EINVAL, "n_split must be >= 1");
@@ -163,16 +165,17 @@ skv_status validate(const skv_desc* d, int32_t n_split) {
       return fail(SKV_EINVAL, "strides must be non-negative");
     if (d->q_strides[i] % 8) return fail(SKV_EINVAL, "q strides must be multiples of 8 elements (16 bytes)");
   }
-  const int esz = d->kv_dtype == SKV_KV_FP8_E4M3 ? 1 : 2;
+  const int esz = d->kv_dtype == SKV_KV_BF16 ? 2 : 1;
   for (int i = 0; i < 3; ++i) {
     if ((d->k_strides[i] * esz) % 16 || (d->v_strides[i] * esz) % 16)
       return fail(SKV_EINVAL, "K/V strides must be multiples of 16 bytes");
   }
-  if (d->k_strides[2] < d->dk || d->v_strides[2] < d->dv)
+  if (d->k_strides[2] < (is_fp4 ? d->dk / 2 : d->dk) || d->v_strides[2] < (is_fp4 ? d->dv / 2 : d->dv))
     return fail(SKV_EINVAL, "K/V token stride must cover a whole head row");
   if (!is_gqa_shape(d) && !is_mla_shape(d)) {
     return fail(SKV_EUNSUPPORTED, "unsupported head dims / dtype: supported are bf16 dk=dv in {64,128}, "
-                                  "fp8-e4m3 dk=dv=128, and the bf16 MLA latent (Hkv=1, dk=576, dv=512)");
+                                  "fp8-e4m3 dk=dv=128, and the bf16 MLA latent (Hkv=1, dk=576, dv=512); "
+                                  "4-bit pages: d=128");
   }
   if (is_mla_shape(d)) {
     for (int i = 0; i < 3; ++i)
@@ -275,8 +278,9 @@ skv_status encode_kv_map(CUtensorMap* map, const void* base, const skv_desc* d, 
   cudaError_t e;
   auto encode = get_encode_fn(&e);
   if (!encode) return cuda_fail(e == cudaSuccess ? cudaErrorNotSupported : e, "cuTensorMapEncodeTiled lookup");
-  const bool fp8 = d->kv_dtype == SKV_KV_FP8_E4M3;
-  const int esz = fp8 ? 1 : 2;
+  const bool bf16 = d->kv_dtype == SKV_KV_BF16, fp4 = d->kv_dtype == SKV_KV_FP4_E2M1;
+  const int esz = bf16 ? 2 : 1;
+  if (fp4) dim /= 2;  // bytes
   // contiguous: (dim, token, head, sequence); paged: (dim, row in page, head, page)
   const int64_t rows = pg ? pg->block_len : d->S_max;
   const int64_t outer = pg ? pg->num_blocks : d->B;
@@ -289,15 +293,38 @@ skv_status encode_kv_map(CUtensorMap* map, const void* base, const skv_desc* d, 
   if (outer == 1 || batch_b == 0) batch_b = std::max<int64_t>(batch_b, head_b * d->Hkv);
   cuuint64_t gstride[3] = {static_cast<cuuint64_t>(tok_b), static_cast<cuuint64_t>(head_b),
                            static_cast<cuuint64_t>(batch_b)};
-  cuuint32_t box[4] = {static_cast<cuuint32_t>(128 / esz), static_cast<cuuint32_t>(box_rows), 1, 1};
+  // (4-bit rows: 64 bytes for heads of 128)
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(fp4 ? 64 : 128 / esz), static_cast<cuuint32_t>(box_rows), 1, 1};
   cuuint32_t estr[4] = {1, 1, 1, 1};
-  CUresult r = encode(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+  CUresult r = encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
                       const_cast<void*>(base), gdim, gstride, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      fp4 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) {
     char buf[160];
     snprintf(buf, sizeof buf, "cuTensorMapEncodeTiled failed (CUresult %d)", static_cast<int>(r));
+    return fail(SKV_ECUDA, buf);
+  }
+  return SKV_OK;
+}
+
+// The block scales of 4-bit pages, contiguous [num_blocks][Hkv][block_len][d / kFp4Block], as 32-bit
+// words (word of a head's rows, head, page, 1): a box holds the scales of box_rows rows.
+skv_status encode_fp4_scale_map(CUtensorMap* map, const void* base, const skv_desc* d, int box_rows, const skv_paged* pg) {
+  cudaError_t e;
+  auto encode = get_encode_fn(&e);
+  if (!encode) return cuda_fail(e == cudaSuccess ? cudaErrorNotSupported : e, "cuTensorMapEncodeTiled lookup");
+  const cuuint64_t row_b = d->dk / kFp4Block, head_b = row_b * pg->block_len, page_b = head_b * d->Hkv;
+  cuuint64_t gdim[4] = {head_b / 4, static_cast<cuuint64_t>(d->Hkv), static_cast<cuuint64_t>(pg->num_blocks), 1};
+  cuuint64_t gstride[3] = {head_b, page_b, page_b * pg->num_blocks};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(box_rows * row_b / 4), 1, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, const_cast<void*>(base), gdim, gstride, box, estr,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    char buf[160];
+    snprintf(buf, sizeof buf, "cuTensorMapEncodeTiled (block scales) failed (CUresult %d)", static_cast<int>(r));
     return fail(SKV_ECUDA, buf);
   }
   return SKV_OK;
@@ -1021,8 +1048,23 @@ skv_status gqa_decode_attn_passq(const skv_desc* desc, int32_t n_ranks, const vo
 
 namespace {
 
-// A chunk call's shape as the description the shared checks and tensor maps take.
-skv_status chunk_desc(const skv_chunk_desc* c, const skv_paged* pg, skv_desc* d) {
+PageFormat page_format(const skv_desc* d) {
+  return d->kv_dtype == SKV_KV_FP4_E2M1 ? kPagesFp4 : d->kv_dtype == SKV_KV_FP8_E4M3 ? kPagesFp8 : kPagesBf16;
+}
+
+// The scales of 4-bit pages: there for those, and for no others.
+skv_status validate_fp4(const skv_desc* d, const skv_fp4_scales* f) {
+  if (page_format(d) != kPagesFp4) return f ? fail(SKV_EINVAL, "fp4 scales go with SKV_KV_FP4_E2M1 pages") : SKV_OK;
+  if (!f) return fail(SKV_EINVAL, "4-bit pages need their scales (fp4 is NULL)");
+  if (!f->k_block || !f->v_block || !aligned(f->k_block, 16) || !aligned(f->v_block, 16))
+    return fail(SKV_EINVAL, "fp4 block scales must be non-NULL and 16-byte aligned");
+  if (!aligned(f->k_head, 4) || !aligned(f->v_head, 4)) return fail(SKV_EINVAL, "head scales must be 4-byte aligned");
+  return SKV_OK;
+}
+
+// A chunk call's shape as the description the shared checks and tensor maps take.  fp4: the call takes
+// 4-bit pages too.
+skv_status chunk_desc(const skv_chunk_desc* c, const skv_paged* pg, skv_desc* d, bool fp4 = false) {
   if (!c) return fail(SKV_EINVAL, "desc is NULL");
   if (!pg) return fail(SKV_EINVAL, "paged is NULL");
   if (c->T < 0) return fail(SKV_EINVAL, "T must not be negative");
@@ -1043,7 +1085,7 @@ skv_status chunk_desc(const skv_chunk_desc* c, const skv_paged* pg, skv_desc* d)
     d->k_strides[i] = c->k_strides[i];
     d->v_strides[i] = c->v_strides[i];
   }
-  skv_status st = validate(d, 1);
+  skv_status st = validate(d, 1, fp4);
   if (st != SKV_OK) return st;
   // (the kernels count in 32 bits up to a tile past the last token)
   if (d->S_max > (int64_t(1) << 31) - 4096) return fail(SKV_EINVAL, "max_blocks * block_len is too large");
@@ -1086,29 +1128,165 @@ struct ChunkPlan {
   size_t plan_bytes = 0, o_bytes = 0, lse_bytes = 0;
 };
 
-skv_status chunk_plan(const skv_chunk_desc* c, const skv_desc* d, ChunkPlan* pl) {
+// T packed rows of B sequences, of at most `longest` each (0: T).
+skv_status chunk_plan(const skv_desc* d, int32_t B, int32_t T, int32_t longest_or_0, ChunkPlan* pl) {
   const int G = d->Hq / d->Hkv;
   // The caller's bound on the chunk lengths chooses the kernel (results do not depend on it): up
   // to 16 rows of a KV head fill an mma.sync tile, where the tensor cores' 128 are mostly padding
   // (decode of 64 sequences, 64 / 8 heads: 373 us against 445; 16 over fp8 pages, 128 / 8: 216 against
   // 488), up to 32 two (24 sequences of 5 rows, 40 / 8 heads: 90 us against 112, fp8 90 against 153); a
   // group above 128 heads has no query tile there.
-  const int64_t longest = c->max_q_len > 0 ? std::min(c->max_q_len, c->T) : c->T;
-  pl->tc = longest * G > 32 && G <= 128;
+  const int64_t longest = longest_or_0 > 0 ? std::min(longest_or_0, T) : T;
+  pl->tc = longest * G > 32 && G <= 128 && page_format(d) != kPagesFp4;
   pl->group_rows = pl->tc ? padded_group(G) : G;
   pl->rows = pl->tc ? chunk_tc_rows() : longest * G <= 16 ? 16 : 32;
   pl->tile = pl->tc ? chunk_tc_kv_tile() : kTileN;
   pl->n_wave = static_cast<int64_t>(device_sm_count()) * (pl->tc ? 1 : chunk_rows_ctas_per_sm(pl->rows));
   pl->n_target = 4 * pl->n_wave;
-  const int64_t rows = static_cast<int64_t>(c->T) * pl->group_rows;
+  const int64_t rows = static_cast<int64_t>(T) * pl->group_rows;
   if (rows + pl->rows >= (int64_t(1) << 31)) return fail(SKV_EINVAL, "T * Hq / Hkv is too large for one call");
-  const int64_t row_tiles = rows / pl->rows + std::min(c->B, c->T);  // each sequence's last one may be short
+  const int64_t row_tiles = rows / pl->rows + std::min(B, T);  // each sequence's last one may be short
   pl->n_items = row_tiles * d->Hkv + pl->n_target;
   if (pl->n_items >= (int64_t(1) << 31)) return fail(SKV_EINVAL, "T * Hq is too large for one call");
   pl->part_rows = pl->tc ? pl->n_target * std::min<int64_t>(pl->rows, rows) : 2 * pl->n_wave * pl->rows;
-  pl->plan_bytes = align_up((kPlanHead + kPlanRow * static_cast<size_t>(c->B)) * 4, 256);
+  pl->plan_bytes = align_up((kPlanHead + kPlanRow * static_cast<size_t>(B)) * 4, 256);
   pl->o_bytes = align_up(static_cast<size_t>(pl->part_rows) * d->dv * 4, 256);
   pl->lse_bytes = align_up(static_cast<size_t>(pl->part_rows) * 4, 256);
+  return SKV_OK;
+}
+
+size_t chunk_ws_bytes(const ChunkPlan& pl) { return pl.plan_bytes + pl.o_bytes + pl.lse_bytes; }
+
+// What every pass of a chunk call shares: its parameters and the pages' maps.
+skv_status chunk_params(const skv_chunk_desc* desc, const skv_desc& d, const skv_paged* paged, const skv_fp4_scales* fp4,
+                        const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
+                        const float* v_scale, const int32_t* cu_q, const int32_t* seq_lens, void* out, float* lse,
+                        PartialParams* p, ChunkMaps* maps) {
+  Plan unused;
+  skv_status st = fill_params(p, &d, unused, q, k_scale, v_scale, seq_lens, nullptr, 1, 0, nullptr, nullptr, paged, nullptr,
+                              nullptr, false);
+  if (st != SKV_OK) return st;
+  p->ck.cu_q = cu_q;
+  p->ck.seq_lens = seq_lens;
+  p->ck.B = d.B;
+  p->ck.T = desc->T;
+  p->ck.Hkv = d.Hkv;
+  p->ck.G = d.Hq / d.Hkv;
+  p->ck.cap = static_cast<int32_t>(d.S_max);
+  p->ck.window = desc->window;
+  p->ck.n_sink = desc->n_sink;
+  p->ck.out = out;
+  p->ck.lse = lse;
+  // (both kernels take the pages in boxes of 64 tokens)
+  static_assert(kTileN == 64, "a page holds a multiple of it");
+  if ((st = encode_kv_map(&maps->k, k_pages, &d, d.k_strides, d.dk, kTileN, paged)) != SKV_OK) return st;
+  if ((st = encode_kv_map(&maps->v, v_pages, &d, d.v_strides, d.dv, kTileN, paged)) != SKV_OK) return st;
+  if (fp4) {
+    p->k_head = fp4->k_head;
+    p->v_head = fp4->v_head;
+    if ((st = encode_fp4_scale_map(&maps->k_block, fp4->k_block, &d, kTileN, paged)) != SKV_OK) return st;
+    if ((st = encode_fp4_scale_map(&maps->v_block, fp4->v_block, &d, kTileN, paged)) != SKV_OK) return st;
+  } else {
+    maps->k_block = maps->k;
+    maps->v_block = maps->v;
+  }
+  return SKV_OK;
+}
+
+// One pass of attention over pages, its partial rows in the workspace at ws: plan, attention, merge.
+skv_status chunk_pass(const skv_desc& d, const ChunkPlan& pl, PartialParams p, ChunkMaps* maps, char* ws, cudaStream_t s) {
+  const PageFormat pages = page_format(&d);
+  p.out_o = reinterpret_cast<float*>(ws + pl.plan_bytes);
+  p.out_lse = reinterpret_cast<float*>(ws + pl.plan_bytes + pl.o_bytes);
+  p.ck.group_rows = pl.group_rows;
+  p.ck.rows = pl.rows;
+  p.ck.tile = pl.tile;
+  p.ck.n_wave = static_cast<int32_t>(pl.n_wave);
+  p.ck.n_target = static_cast<int32_t>(pl.n_target);
+  // (with one KV tile at most no item is ever cut, and nothing merged)
+  p.ck.start = d.S_max <= pl.tile ? 0 : kChunkStart * (d.dk == 64 || pages != kPagesBf16 ? 2 : 1);
+  p.ck.plan = reinterpret_cast<int32_t*>(ws);
+  if (pl.tc) {
+    skv_desc dq = d;  // the packed rows as the query rows of one sequence
+    dq.B = 1;
+    dq.Tq = p.ck.T;
+    skv_status st = encode_q_map(&maps->q, p.q, &dq, pl.group_rows);
+    if (st != SKV_OK) return st;
+  }
+  cudaError_t e = cudaSuccess;
+  if (pl.tc) e = launch_chunk_plan(p.ck, s);
+  if (e == cudaSuccess) e = timing_mark(false, s);
+  if (e == cudaSuccess)
+    e = pl.tc ? launch_chunk_tc(p, d.dk, pages, *maps, pl.n_items, s) : launch_chunk_rows(p, d.dk, pages, *maps, s);
+  if (e == cudaSuccess) e = timing_mark(true, s);
+  if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
+  if (d.S_max <= pl.tile) return SKV_OK;  // one KV tile at most: never several chunks
+  // rows that can be in several chunks: no more than a partial row each
+  const int64_t rows = std::min<int64_t>(static_cast<int64_t>(p.ck.T) * d.Hq, pl.part_rows);
+  e = pl.tc ? launch_chunk_merge(p.ck, d.dv, p.out_o, p.out_lse, rows, s)
+            : launch_chunk_runs_merge(p.ck, d.dv, p.out_o, p.out_lse, s);
+  if (e != cudaSuccess) return cuda_fail(e, "chunk merge launch");
+  return SKV_OK;
+}
+
+// The checks that every attention call makes of its arguments, past the description.
+skv_status chunk_call_checks(const skv_chunk_desc* desc, const skv_desc& d, const skv_fp4_scales* fp4, const void* q,
+                             const void* k_pages, const void* v_pages, const float* k_scale, const float* v_scale,
+                             const int32_t* cu_q, const int32_t* seq_lens, void* out, float* lse) {
+  skv_status st;
+  if ((st = validate_ptrs(&d, q, k_pages, v_pages, k_scale, v_scale, seq_lens)) != SKV_OK) return st;
+  if ((st = validate_fp4(&d, fp4)) != SKV_OK) return st;
+  if (!cu_q || !aligned(cu_q, 4)) return fail(SKV_EINVAL, "cu_q NULL or misaligned");
+  if (!out || !lse) return fail(SKV_EINVAL, "out and lse must be non-NULL");
+  if (!aligned(out, 16) || !aligned(lse, 4)) return fail(SKV_EINVAL, "out must be 16-byte, lse 4-byte aligned");
+  return SKV_OK;
+}
+
+skv_status chunk_attention(const skv_chunk_desc* desc, const skv_paged* paged, bool fp4_call, const skv_fp4_scales* fp4,
+                           const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
+                           const float* v_scale, const int32_t* cu_q, const int32_t* seq_lens, void* out, float* lse,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  skv_desc d;
+  skv_status st = chunk_desc(desc, paged, &d, fp4_call);
+  if (st != SKV_OK) return st;
+  if (fp4_call && page_format(&d) != kPagesFp4) return fail(SKV_EINVAL, "kv_dtype must be SKV_KV_FP4_E2M1");
+  if (d.softmax_scale < 0.f) return fail(SKV_EINVAL, "softmax_scale must be positive");
+  if (desc->window < 0 || desc->n_sink < 0) return fail(SKV_EINVAL, "window and n_sink must not be negative");
+  if (desc->n_sink > 0 && desc->window == 0) return fail(SKV_EINVAL, "n_sink needs a window (window > 0)");
+  if (desc->T == 0) return SKV_OK;
+  st = chunk_call_checks(desc, d, fp4, q, k_pages, v_pages, k_scale, v_scale, cu_q, seq_lens, out, lse);
+  if (st != SKV_OK) return st;
+  ChunkPlan pl;
+  if ((st = chunk_plan(&d, d.B, desc->T, desc->max_q_len, &pl)) != SKV_OK) return st;
+  if (!workspace || workspace_bytes < chunk_ws_bytes(pl) || !aligned(workspace, 256))
+    return fail(SKV_EWORKSPACE, "workspace missing, misaligned or smaller than attn_chunk_paged_workspace_size()");
+  PartialParams p;
+  ChunkMaps maps;
+  st = chunk_params(desc, d, paged, fp4, q, k_pages, v_pages, k_scale, v_scale, cu_q, seq_lens, out, lse, &p, &maps);
+  if (st != SKV_OK) return st;
+  return chunk_pass(d, pl, p, &maps, static_cast<char*>(workspace), static_cast<cudaStream_t>(stream));
+}
+
+// The two passes of a shared prefix and their workspace: the groups' arrays, the prefixes' fp32 result,
+// and one pass's own, which the second takes over from the first.
+struct SharedPlan {
+  ChunkPlan prefix, rest;
+  size_t groups = 0, o = 0, lse = 0, pass = 0;
+  size_t bytes() const { return groups + o + lse + pass; }
+};
+
+skv_status shared_plan(const skv_chunk_desc* c, const skv_shared_desc* sh, const skv_desc* d, SharedPlan* pl) {
+  if (!sh) return fail(SKV_EINVAL, "shared is NULL");
+  if (c->window != 0 || c->n_sink != 0) return fail(SKV_EINVAL, "a shared prefix goes without window and n_sink");
+  if (sh->n_groups < 1) return fail(SKV_EINVAL, "n_groups must be positive");
+  skv_status st = chunk_plan(d, sh->n_groups, c->T, sh->max_group_rows, &pl->prefix);
+  if (st != SKV_OK) return st;
+  if ((st = chunk_plan(d, c->B, c->T, c->max_q_len, &pl->rest)) != SKV_OK) return st;
+  pl->groups = align_up((3 * static_cast<size_t>(sh->n_groups) + 1 + c->B) * 4, 256);
+  const size_t rows = static_cast<size_t>(c->T) * c->Hq;
+  pl->o = align_up(rows * d->dv * 4, 256);
+  pl->lse = align_up(rows * 4, 256);
+  pl->pass = std::max(chunk_ws_bytes(pl->prefix), chunk_ws_bytes(pl->rest));
   return SKV_OK;
 }
 
@@ -1119,11 +1297,11 @@ extern "C" {
 skv_status attn_chunk_paged_workspace_size(const skv_chunk_desc* desc, const skv_paged* paged, size_t* bytes) {
   if (!bytes) return fail(SKV_EINVAL, "bytes is NULL");
   skv_desc d;
-  skv_status st = chunk_desc(desc, paged, &d);
+  skv_status st = chunk_desc(desc, paged, &d, true);
   if (st != SKV_OK) return st;
   ChunkPlan pl;
-  if ((st = chunk_plan(desc, &d, &pl)) != SKV_OK) return st;
-  *bytes = desc->T == 0 ? 0 : pl.plan_bytes + pl.o_bytes + pl.lse_bytes;
+  if ((st = chunk_plan(&d, d.B, desc->T, desc->max_q_len, &pl)) != SKV_OK) return st;
+  *bytes = desc->T == 0 ? 0 : chunk_ws_bytes(pl);
   return SKV_OK;
 }
 
@@ -1131,81 +1309,97 @@ skv_status attn_chunk_paged(const skv_chunk_desc* desc, const skv_paged* paged, 
                             const void* v_pages, const float* k_scale, const float* v_scale, const int32_t* cu_q,
                             const int32_t* seq_lens, void* out, float* lse, void* workspace, size_t workspace_bytes,
                             void* stream) {
+  return chunk_attention(desc, paged, false, nullptr, q, k_pages, v_pages, k_scale, v_scale, cu_q, seq_lens, out, lse,
+                         workspace, workspace_bytes, stream);
+}
+
+skv_status attn_chunk_paged_fp4(const skv_chunk_desc* desc, const skv_paged* paged, const skv_fp4_scales* fp4,
+                                const void* q, const void* k_pages, const void* v_pages, const int32_t* cu_q,
+                                const int32_t* seq_lens, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+  return chunk_attention(desc, paged, true, fp4, q, k_pages, v_pages, nullptr, nullptr, cu_q, seq_lens, out, lse, workspace,
+                         workspace_bytes, stream);
+}
+
+skv_status attn_shared_prefix_paged_workspace_size(const skv_chunk_desc* desc, const skv_paged* paged,
+                                                   const skv_shared_desc* shared, size_t* bytes) {
+  if (!bytes) return fail(SKV_EINVAL, "bytes is NULL");
   skv_desc d;
-  skv_status st = chunk_desc(desc, paged, &d);
+  skv_status st = chunk_desc(desc, paged, &d, true);
   if (st != SKV_OK) return st;
-  if (d.softmax_scale < 0.f) return fail(SKV_EINVAL, "softmax_scale must be positive");
-  if (desc->window < 0 || desc->n_sink < 0) return fail(SKV_EINVAL, "window and n_sink must not be negative");
-  if (desc->n_sink > 0 && desc->window == 0) return fail(SKV_EINVAL, "n_sink needs a window (window > 0)");
-  if (desc->T == 0) return SKV_OK;
-  if ((st = validate_ptrs(&d, q, k_pages, v_pages, k_scale, v_scale, seq_lens)) != SKV_OK) return st;
-  if (!cu_q || !aligned(cu_q, 4)) return fail(SKV_EINVAL, "cu_q NULL or misaligned");
-  if (!out || !lse) return fail(SKV_EINVAL, "out and lse must be non-NULL");
-  if (!aligned(out, 16) || !aligned(lse, 4)) return fail(SKV_EINVAL, "out must be 16-byte, lse 4-byte aligned");
-  ChunkPlan pl;
-  if ((st = chunk_plan(desc, &d, &pl)) != SKV_OK) return st;
-  if (!workspace || workspace_bytes < pl.plan_bytes + pl.o_bytes + pl.lse_bytes || !aligned(workspace, 256))
-    return fail(SKV_EWORKSPACE, "workspace missing, misaligned or smaller than attn_chunk_paged_workspace_size()");
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  char* ws = static_cast<char*>(workspace);
-  float* part_o = reinterpret_cast<float*>(ws + pl.plan_bytes);
-  float* part_lse = reinterpret_cast<float*>(ws + pl.plan_bytes + pl.o_bytes);
-  PartialParams p;
-  Plan unused;
-  st = fill_params(&p, &d, unused, q, k_scale, v_scale, seq_lens, nullptr, 1, 0, nullptr, nullptr, paged, part_o,
-                   part_lse, false);
-  if (st != SKV_OK) return st;
-  p.ck.cu_q = cu_q;
-  p.ck.seq_lens = seq_lens;
-  p.ck.B = d.B;
-  p.ck.T = desc->T;
-  p.ck.Hkv = d.Hkv;
-  p.ck.G = d.Hq / d.Hkv;
-  p.ck.cap = static_cast<int32_t>(d.S_max);
-  p.ck.window = desc->window;
-  p.ck.n_sink = desc->n_sink;
-  p.ck.group_rows = pl.group_rows;
-  p.ck.rows = pl.rows;
-  p.ck.tile = pl.tile;
-  p.ck.n_wave = static_cast<int32_t>(pl.n_wave);
-  p.ck.n_target = static_cast<int32_t>(pl.n_target);
-  // (with one KV tile at most no item is ever cut, and nothing merged)
-  p.ck.start = d.S_max <= pl.tile ? 0 : kChunkStart * (d.dk == 64 || d.kv_dtype == SKV_KV_FP8_E4M3 ? 2 : 1);
-  p.ck.plan = reinterpret_cast<int32_t*>(ws);
-  p.ck.out = out;
-  p.ck.lse = lse;
-  CUtensorMap tmq, tmk, tmv;
-  const int box = pl.tc ? chunk_tc_kv_box() : kTileN;
-  if ((st = encode_kv_map(&tmk, k_pages, &d, d.k_strides, d.dk, box, paged)) != SKV_OK) return st;
-  if ((st = encode_kv_map(&tmv, v_pages, &d, d.v_strides, d.dv, box, paged)) != SKV_OK) return st;
-  if (pl.tc) {
-    skv_desc dq = d;  // the packed rows as the query rows of one sequence
-    dq.B = 1;
-    dq.Tq = desc->T;
-    if ((st = encode_q_map(&tmq, q, &dq, pl.group_rows)) != SKV_OK) return st;
-  }
-  cudaError_t e = cudaSuccess;
-  if (pl.tc) e = launch_chunk_plan(p.ck, s);
-  if (e == cudaSuccess) e = timing_mark(false, s);
-  if (e == cudaSuccess)
-    e = pl.tc ? launch_chunk_tc(p, d.dk, d.kv_dtype == SKV_KV_FP8_E4M3, tmq, tmk, tmv, pl.n_items, s)
-              : launch_chunk_rows(p, d.dk, d.kv_dtype == SKV_KV_FP8_E4M3, tmk, tmv, s);
-  if (e == cudaSuccess) e = timing_mark(true, s);
-  if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
-  if (d.S_max <= pl.tile) return SKV_OK;  // one KV tile at most: never several chunks
-  // rows that can be in several chunks: no more than a partial row each
-  const int64_t rows = std::min<int64_t>(static_cast<int64_t>(desc->T) * d.Hq, pl.part_rows);
-  e = pl.tc ? launch_chunk_merge(p.ck, d.dv, part_o, part_lse, rows, s)
-            : launch_chunk_runs_merge(p.ck, d.dv, part_o, part_lse, s);
-  if (e != cudaSuccess) return cuda_fail(e, "chunk merge launch");
+  SharedPlan pl;
+  if ((st = shared_plan(desc, shared, &d, &pl)) != SKV_OK) return st;
+  *bytes = desc->T == 0 ? 0 : pl.bytes();
   return SKV_OK;
 }
 
-skv_status qk_norm_rope_append(const skv_append_desc* desc, const skv_paged* paged, const void* q, const void* k,
-                               const void* v, const void* q_weight, const void* k_weight, const float* cos,
-                               const float* sin, const int32_t* positions, const int32_t* cu_q,
-                               const int32_t* seq_lens, const float* k_scale, const float* v_scale, void* q_out,
-                               void* k_pages, void* v_pages, void* stream) {
+skv_status attn_shared_prefix_paged(const skv_chunk_desc* desc, const skv_paged* paged, const skv_shared_desc* shared,
+                                    const skv_fp4_scales* fp4, const void* q, const void* k_pages, const void* v_pages,
+                                    const float* k_scale, const float* v_scale, const int32_t* cu_q,
+                                    const int32_t* seq_lens, void* out, float* lse, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+  skv_desc d;
+  skv_status st = chunk_desc(desc, paged, &d, true);
+  if (st != SKV_OK) return st;
+  if (d.softmax_scale < 0.f) return fail(SKV_EINVAL, "softmax_scale must be positive");
+  SharedPlan pl;
+  if ((st = shared_plan(desc, shared, &d, &pl)) != SKV_OK) return st;
+  if (desc->T == 0) return SKV_OK;
+  st = chunk_call_checks(desc, d, fp4, q, k_pages, v_pages, k_scale, v_scale, cu_q, seq_lens, out, lse);
+  if (st != SKV_OK) return st;
+  if (!shared->cu_groups || !shared->prefix_lens || !aligned(shared->cu_groups, 4) || !aligned(shared->prefix_lens, 4))
+    return fail(SKV_EINVAL, "cu_groups and prefix_lens must be non-NULL and 4-byte aligned");
+  if (!workspace || workspace_bytes < pl.bytes() || !aligned(workspace, 256))
+    return fail(SKV_EWORKSPACE, "workspace missing, misaligned or smaller than attn_shared_prefix_paged_workspace_size()");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  SharedArgs g;
+  g.cu_q = cu_q;
+  g.seq_lens = seq_lens;
+  g.cu_groups = shared->cu_groups;
+  g.prefix_lens = shared->prefix_lens;
+  g.B = d.B;
+  g.T = desc->T;
+  g.n_groups = shared->n_groups;
+  g.cap = static_cast<int32_t>(d.S_max);
+  g.group_rows_at = reinterpret_cast<int32_t*>(ws);
+  g.group_len = g.group_rows_at + g.n_groups + 1;
+  g.table_row = g.group_len + g.n_groups;
+  g.skip = g.table_row + g.n_groups;
+  float* prior_o = reinterpret_cast<float*>(ws + pl.groups);
+  float* prior_lse = reinterpret_cast<float*>(ws + pl.groups + pl.o);
+  char* pass_ws = ws + pl.groups + pl.o + pl.lse;
+  PartialParams p;
+  ChunkMaps maps;
+  st = chunk_params(desc, d, paged, fp4, q, k_pages, v_pages, k_scale, v_scale, cu_q, seq_lens, out, lse, &p, &maps);
+  if (st != SKV_OK) return st;
+  cudaError_t e = launch_shared_groups(g, s);
+  if (e != cudaSuccess) return cuda_fail(e, "shared prefix launch");
+  PartialParams first = p;  // the prefixes: groups in the place of sequences
+  first.ck.B = g.n_groups;
+  first.ck.seq_lens = g.group_len;
+  first.ck.group_rows_at = g.group_rows_at;
+  first.ck.table_row = g.table_row;
+  first.ck.whole = 1;
+  first.ck.out = prior_o;
+  first.ck.lse = prior_lse;
+  first.ck.out_f32 = 1;
+  if ((st = chunk_pass(d, pl.prefix, first, &maps, pass_ws, s)) != SKV_OK) return st;
+  p.ck.skip = g.skip;
+  p.ck.prior_o = prior_o;
+  p.ck.prior_lse = prior_lse;
+  return chunk_pass(d, pl.rest, p, &maps, pass_ws, s);
+}
+
+}  // extern "C"
+
+namespace {
+
+skv_status append_impl(const skv_append_desc* desc, const skv_paged* paged, bool fp4_call, const skv_fp4_scales* fp4,
+                       const void* q, const void* k, const void* v, const void* q_weight, const void* k_weight,
+                       const float* cos, const float* sin, const int32_t* positions, const int32_t* cu_q,
+                       const int32_t* seq_lens, const float* k_scale, const float* v_scale, void* q_out, void* k_pages,
+                       void* v_pages, void* stream) {
   if (!desc) return fail(SKV_EINVAL, "desc is NULL");
   // the pages' description, checked as the attention calls check it
   skv_chunk_desc c;
@@ -1224,8 +1418,9 @@ skv_status qk_norm_rope_append(const skv_append_desc* desc, const skv_paged* pag
     c.v_strides[i] = desc->v_page_strides[i];
   }
   skv_desc d;
-  skv_status st = chunk_desc(&c, paged, &d);
+  skv_status st = chunk_desc(&c, paged, &d, fp4_call);
   if (st != SKV_OK) return st;
+  if (fp4_call && page_format(&d) != kPagesFp4) return fail(SKV_EINVAL, "kv_dtype must be SKV_KV_FP4_E2M1");
   for (int i = 0; i < 2; ++i) {
     const int64_t all[3] = {desc->k_strides[i], desc->v_strides[i], desc->q_out_strides[i]};
     for (int64_t x : all)
@@ -1259,6 +1454,7 @@ skv_status qk_norm_rope_append(const skv_append_desc* desc, const skv_paged* pag
     return fail(SKV_EINVAL, "q, k, v and q_out must be non-NULL and 16-byte aligned");
   if (!cu_q || !aligned(cu_q, 4)) return fail(SKV_EINVAL, "cu_q NULL or misaligned");
   if ((st = validate_ptrs(&d, q, k_pages, v_pages, k_scale, v_scale, seq_lens)) != SKV_OK) return st;
+  if ((st = validate_fp4(&d, fp4)) != SKV_OK) return st;
   AppendArgs a;
   std::memset(&a, 0, sizeof(a));
   cudaError_t e;
@@ -1290,6 +1486,12 @@ skv_status qk_norm_rope_append(const skv_append_desc* desc, const skv_paged* pag
   a.vp_sb = d.v_strides[0], a.vp_sh = d.v_strides[1], a.vp_st = d.v_strides[2];
   a.k_scale = k_scale;
   a.v_scale = v_scale;
+  if (fp4) {
+    a.k_block = static_cast<uint8_t*>(fp4->k_block);
+    a.v_block = static_cast<uint8_t*>(fp4->v_block);
+    a.k_head = fp4->k_head;
+    a.v_head = fp4->v_head;
+  }
   a.num_blocks = paged->num_blocks;
   a.B = d.B, a.T = desc->T, a.Hq = d.Hq, a.Hkv = d.Hkv, a.rot = desc->rot;
   a.interleaved = desc->interleaved ? 1 : 0;
@@ -1297,8 +1499,97 @@ skv_status qk_norm_rope_append(const skv_append_desc* desc, const skv_paged* pag
   a.max_blocks = paged->max_blocks;
   a.scale_block = d.kv_dtype == SKV_KV_FP8_E4M3 ? d.scale_block : kTileN;
   a.eps = desc->eps;
-  e = launch_append(a, desc->d, d.kv_dtype == SKV_KV_FP8_E4M3, device_sm_count(), static_cast<cudaStream_t>(stream));
+  e = launch_append(a, desc->d, page_format(&d), device_sm_count(), static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "append launch");
+  return SKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+skv_status qk_norm_rope_append(const skv_append_desc* desc, const skv_paged* paged, const void* q, const void* k,
+                               const void* v, const void* q_weight, const void* k_weight, const float* cos,
+                               const float* sin, const int32_t* positions, const int32_t* cu_q,
+                               const int32_t* seq_lens, const float* k_scale, const float* v_scale, void* q_out,
+                               void* k_pages, void* v_pages, void* stream) {
+  return append_impl(desc, paged, false, nullptr, q, k, v, q_weight, k_weight, cos, sin, positions, cu_q, seq_lens, k_scale,
+                     v_scale, q_out, k_pages, v_pages, stream);
+}
+
+skv_status qk_norm_rope_append_fp4(const skv_append_desc* desc, const skv_paged* paged, const skv_fp4_scales* fp4,
+                                   const void* q, const void* k, const void* v, const void* q_weight,
+                                   const void* k_weight, const float* cos, const float* sin, const int32_t* positions,
+                                   const int32_t* cu_q, const int32_t* seq_lens, void* q_out, void* k_pages,
+                                   void* v_pages, void* stream) {
+  return append_impl(desc, paged, true, fp4, q, k, v, q_weight, k_weight, cos, sin, positions, cu_q, seq_lens, nullptr,
+                     nullptr, q_out, k_pages, v_pages, stream);
+}
+
+skv_status kv_read_paged(const skv_read_desc* desc, const skv_paged* paged, const skv_fp4_scales* fp4,
+                         const void* k_pages, const void* v_pages, const float* k_scale, const float* v_scale,
+                         const int32_t* cu_tokens, const int32_t* starts, void* k_out, void* v_out, void* stream) {
+  if (!desc) return fail(SKV_EINVAL, "desc is NULL");
+  // the pages' description, checked as the attention calls check it
+  skv_chunk_desc c;
+  std::memset(&c, 0, sizeof(c));
+  c.B = desc->B;
+  c.T = desc->T;
+  c.Hq = c.Hkv = desc->Hkv;
+  c.d = desc->d;
+  c.softmax_scale = 1.f;
+  c.kv_dtype = desc->kv_dtype;
+  c.scale_block = desc->scale_block;
+  c.q_strides[0] = c.q_strides[1] = 8;  // (there are no queries)
+  for (int i = 0; i < 3; ++i) {
+    c.k_strides[i] = desc->k_page_strides[i];
+    c.v_strides[i] = desc->v_page_strides[i];
+  }
+  skv_desc d;
+  skv_status st = chunk_desc(&c, paged, &d, true);
+  if (st != SKV_OK) return st;
+  for (const int64_t* o : {desc->k_out_strides, desc->v_out_strides}) {
+    if (o[0] < 0 || o[1] < 0 || o[0] % 8 || o[1] % 8)
+      return fail(SKV_EINVAL, "k_out and v_out strides must be non-negative multiples of 8 elements");
+    if ((desc->T > 1 && o[0] < desc->d) || (desc->Hkv > 1 && o[1] < desc->d) ||
+        (desc->T > 1 && desc->Hkv > 1 && rows_overlap(o[0], desc->T, o[1], desc->Hkv, desc->d)))
+      return fail(SKV_EINVAL, "k_out and v_out strides put several rows in one place");
+  }
+  if (desc->T == 0) return SKV_OK;
+  if (!k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16))
+    return fail(SKV_EINVAL, "k_out and v_out must be non-NULL and 16-byte aligned");
+  if (!cu_tokens || !aligned(cu_tokens, 4) || !aligned(starts, 4))
+    return fail(SKV_EINVAL, "cu_tokens must be non-NULL, cu_tokens and starts 4-byte aligned");
+  if ((st = validate_ptrs(&d, k_out, k_pages, v_pages, k_scale, v_scale, cu_tokens)) != SKV_OK) return st;
+  if ((st = validate_fp4(&d, fp4)) != SKV_OK) return st;
+  ReadArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.k_pages = k_pages;
+  a.v_pages = v_pages;
+  a.kp_sb = d.k_strides[0], a.kp_sh = d.k_strides[1], a.kp_st = d.k_strides[2];
+  a.vp_sb = d.v_strides[0], a.vp_sh = d.v_strides[1], a.vp_st = d.v_strides[2];
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  if (fp4) {
+    a.k_block = static_cast<const uint8_t*>(fp4->k_block);
+    a.v_block = static_cast<const uint8_t*>(fp4->v_block);
+    a.k_head = fp4->k_head;
+    a.v_head = fp4->v_head;
+  }
+  a.cu = cu_tokens;
+  a.starts = starts;
+  a.block_table = paged->block_table;
+  a.k_out = static_cast<__nv_bfloat16*>(k_out);
+  a.v_out = static_cast<__nv_bfloat16*>(v_out);
+  a.ko_st = desc->k_out_strides[0], a.ko_sh = desc->k_out_strides[1];
+  a.vo_st = desc->v_out_strides[0], a.vo_sh = desc->v_out_strides[1];
+  a.num_blocks = paged->num_blocks;
+  a.B = d.B, a.T = desc->T, a.Hkv = d.Hkv;
+  a.block_len = paged->block_len;
+  a.max_blocks = paged->max_blocks;
+  a.scale_block = page_format(&d) == kPagesFp8 ? d.scale_block : kTileN;
+  cudaError_t e = launch_kv_read(a, desc->d, page_format(&d), device_sm_count(), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "cache read launch");
   return SKV_OK;
 }
 

@@ -5,7 +5,8 @@
 //
 // For every such row, with k partials (o_c, lse_c): m = max lse_c, w_c = exp(lse_c - m),
 // out = sum w_c o_c / sum w_c in bf16, lse = m + ln sum w_c; all partials empty: out = 0,
-// lse = -inf.  Where they are stands in the plan (chunk_plan.cuh) of the call.
+// lse = -inf.  Where they are stands in the plan (chunk_plan.cuh) of the call.  Of a shared prefix the
+// result is fp32, and rows behind one are joined with it (ChunkArgs).
 //
 // Bound by the partials' bytes, which are mostly still in L2; what counts is how many loads
 // are in flight.  A block takes 8 rows: one warp each while k <= 16 (all partials of a row in
@@ -71,18 +72,35 @@ __device__ __forceinline__ Joined join(const float* part_o, const float* part_ls
   return j;
 }
 
+// (behind: the row's sequence has a prefix that another pass attended)
 template <int D>
-__device__ __forceinline__ void store_row(const ChunkArgs& a, int64_t row, const Joined& j, int lane) {
-  const float inv = j.den != 0.f ? 1.f / j.den : 0.f;
-  if (4 * lane < D) {
-    __nv_bfloat162 lo = __floats2bfloat162_rn(j.acc.x * inv, j.acc.y * inv);
-    __nv_bfloat162 hi = __floats2bfloat162_rn(j.acc.z * inv, j.acc.w * inv);
-    uint2 u;
-    u.x = *reinterpret_cast<uint32_t*>(&lo);
-    u.y = *reinterpret_cast<uint32_t*>(&hi);
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * D + 4 * lane) = u;
+__device__ __forceinline__ void store_row(const ChunkArgs& a, int64_t row, const Joined& j, int lane, bool behind) {
+  float inv = j.den != 0.f ? 1.f / j.den : 0.f;
+  float lse = j.den != 0.f ? j.m + logf(j.den) : -INFINITY;
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (behind) {
+    const ChunkJoin both = chunk_join(lse, __ldcg(a.prior_lse + row));
+    inv *= both.own;
+    lse = both.lse;
+    if (4 * lane < D && both.prior != 0.f) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(a.prior_o + row * D + 4 * lane));
+      y = make_float4(x.x * both.prior, x.y * both.prior, x.z * both.prior, x.w * both.prior);
+    }
   }
-  if (lane == 0) a.lse[row] = j.den != 0.f ? j.m + logf(j.den) : -INFINITY;
+  if (4 * lane < D) {
+    y = make_float4(fmaf(j.acc.x, inv, y.x), fmaf(j.acc.y, inv, y.y), fmaf(j.acc.z, inv, y.z), fmaf(j.acc.w, inv, y.w));
+    if (a.out_f32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * D + 4 * lane) = y;
+    } else {
+      __nv_bfloat162 lo = __floats2bfloat162_rn(y.x, y.y);
+      __nv_bfloat162 hi = __floats2bfloat162_rn(y.z, y.w);
+      uint2 u;
+      u.x = *reinterpret_cast<uint32_t*>(&lo);
+      u.y = *reinterpret_cast<uint32_t*>(&hi);
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * D + 4 * lane) = u;
+    }
+  }
+  if (lane == 0) a.lse[row] = lse;
 }
 
 // One row's partials dealt to the block's warps.
@@ -93,7 +111,7 @@ struct BlockJoin {
 };
 template <int D, class At>
 __device__ __forceinline__ void join_by_block(const ChunkArgs& a, BlockJoin<D>& sm, const float* part_o,
-                                              const float* part_lse, At&& at, int k, int64_t row) {
+                                              const float* part_lse, At&& at, int k, int64_t row, bool behind) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Joined j = join<D>(part_o, part_lse, at, warp, kRowsPerBlock, k, lane);
   __syncthreads();  // the sums before were read
@@ -119,14 +137,14 @@ __device__ __forceinline__ void join_by_block(const ChunkArgs& a, BlockJoin<D>& 
         s.acc.w += f * x.w;
       }
     }
-    store_row<D>(a, row, s, lane);
+    store_row<D>(a, row, s, lane, behind);
   }
 }
 
 template <int D>
 __global__ void __launch_bounds__(32 * kRowsPerBlock)
     chunk_merge_kernel(const __grid_constant__ ChunkArgs a, const float* part_o, const float* part_lse) {
-  __shared__ int sm_parts[kRowsPerBlock], sm_n[kRowsPerBlock];
+  __shared__ int sm_parts[kRowsPerBlock], sm_n[kRowsPerBlock], sm_skip[kRowsPerBlock];
   __shared__ int64_t sm_row[kRowsPerBlock], sm_part[kRowsPerBlock];
   __shared__ BlockJoin<D> sm_join;
   // the attention kernel before it on the stream is complete and its writes are visible
@@ -139,7 +157,7 @@ __global__ void __launch_bounds__(32 * kRowsPerBlock)
     const int r = r0 + warp;
     __syncthreads();  // the tables' earlier readers are done
     if (lane == 0) {
-      int k = 0, n = 0;
+      int k = 0, n = 0, skip = 0;
       int64_t row = 0, part = 0;
       if (r < rows) {
         int lo = 0, hi = a.B - 1;  // the last sequence whose first row is <= r
@@ -149,14 +167,15 @@ __global__ void __launch_bounds__(32 * kRowsPerBlock)
         }
         // sequences without rows to merge share the first row of the one after them
         const int in = r - __ldcg(plan + kPlanRow * lo + 1);
-        const int row0 = min(max(__ldg(a.cu_q + lo), 0), a.T);
-        n = max(min(max(__ldg(a.cu_q + lo + 1), 0), a.T) - row0, 0);
+        int row0, m;
+        chunk_lengths(a, lo, &row0, &n, &m, &skip);
         k = __ldcg(plan + kPlanRow * lo + 4);
         row = static_cast<int64_t>(row0) * Hq + in;
         part = static_cast<int64_t>(__ldcg(plan + kPlanRow * lo + 2)) + in;
       }
       sm_parts[warp] = k;
       sm_n[warp] = n;
+      sm_skip[warp] = skip;
       sm_row[warp] = row;
       sm_part[warp] = part;
     }
@@ -169,10 +188,11 @@ __global__ void __launch_bounds__(32 * kRowsPerBlock)
       return [first, stride](int c) -> int64_t { return first + c * stride; };
     };
     if (most <= kWarpParts) {
-      if (r < rows) store_row<D>(a, sm_row[warp], join<D>(part_o, part_lse, at(warp), 0, 1, sm_parts[warp], lane), lane);
+      if (r < rows)
+        store_row<D>(a, sm_row[warp], join<D>(part_o, part_lse, at(warp), 0, 1, sm_parts[warp], lane), lane, sm_skip[warp] > 0);
     } else {
       for (int w = 0; w < kRowsPerBlock && r0 + w < rows; ++w)
-        join_by_block<D>(a, sm_join, part_o, part_lse, at(w), sm_parts[w], sm_row[w]);
+        join_by_block<D>(a, sm_join, part_o, part_lse, at(w), sm_parts[w], sm_row[w], sm_skip[w] > 0);
     }
   }
 }
@@ -212,9 +232,10 @@ __global__ void __launch_bounds__(32 * kRowsPerBlock)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (k <= kWarpParts) {
     for (int r = mine * kRowsPerBlock + warp; r < rows; r += borders * kRowsPerBlock)
-      store_row<D>(a, out_row(r), join<D>(part_o, part_lse, at(r), 0, 1, k, lane), lane);
+      store_row<D>(a, out_row(r), join<D>(part_o, part_lse, at(r), 0, 1, k, lane), lane, runs.skip > 0);
   } else {
-    for (int r = mine; r < rows; r += borders) join_by_block<D>(a, sm_join, part_o, part_lse, at(r), k, out_row(r));
+    for (int r = mine; r < rows; r += borders)
+      join_by_block<D>(a, sm_join, part_o, part_lse, at(r), k, out_row(r), runs.skip > 0);
   }
 }
 

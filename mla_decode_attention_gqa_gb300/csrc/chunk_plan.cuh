@@ -33,14 +33,55 @@ struct ChunkItem {
   int row0;      // first packed row (cu_q[b])
   int n;         // new tokens
   int m;         // cached tokens with them
+  int skip;      // of those, the first ones that another pass attends
   int part_row;  // first partial row of the sequence (n_chunk > 1)
 };
 
-__device__ __forceinline__ void chunk_lengths(const ChunkArgs& a, int b, int* row0, int* n, int* m) {
-  const int lo = min(max(__ldg(a.cu_q + b), 0), a.T), hi = min(max(__ldg(a.cu_q + b + 1), 0), a.T);
+// (The arrays of a shared prefix are written by the kernel before, so they are not read through the
+// read-only path.)
+__device__ __forceinline__ void chunk_lengths(const ChunkArgs& a, int b, int* row0, int* n, int* m, int* skip) {
+  int lo, hi, len;
+  if (a.group_rows_at) {
+    lo = __ldcg(a.group_rows_at + b), hi = __ldcg(a.group_rows_at + b + 1);
+    len = __ldcg(a.seq_lens + b);
+  } else {
+    lo = __ldg(a.cu_q + b), hi = __ldg(a.cu_q + b + 1);
+    len = __ldg(a.seq_lens + b);
+  }
+  lo = min(max(lo, 0), a.T), hi = min(max(hi, 0), a.T);
   *row0 = lo;
-  *n = max(hi - lo, 0);
-  *m = max(__ldg(a.seq_lens + b), 0);
+  *m = max(len, 0);
+  *n = a.whole && *m == 0 ? 0 : max(hi - lo, 0);  // (nothing to do for a group without a prefix)
+  *skip = a.skip ? __ldcg(a.skip + b) : 0;
+}
+
+// Position of the first of n new tokens, and from each to the next.
+__device__ __forceinline__ int chunk_pos0(const ChunkArgs& a, int n, int m) { return a.whole ? m - 1 : m - n; }
+__device__ __forceinline__ int chunk_pos_step(const ChunkArgs& a) { return a.whole ? 0 : 1; }
+
+// A row's result over its own tokens (out, lse) joined with the one over its prefix: the weights of the
+// two, and the lse of both.  A part that saw nothing weighs nothing; a NaN on either side stays.
+struct ChunkJoin {
+  float own, prior, lse;
+};
+__device__ __forceinline__ ChunkJoin chunk_join(float lse, float prior_lse) {
+  const float m = fmaxf(lse, prior_lse);
+  ChunkJoin j;
+  if (m == -INFINITY) {
+    j.own = j.prior = 0.f;
+    j.lse = -INFINITY;
+    return j;
+  }
+  const float a = __expf(lse - m), b = __expf(prior_lse - m), sum = a + b;
+  j.own = a / sum;
+  j.prior = b / sum;
+  j.lse = m + logf(sum);
+  return j;
+}
+
+// Page of token `tok` of sequence (or group) b.
+__device__ __forceinline__ int chunk_page_of(const PartialParams& p, int b, int tok) {
+  return kv_page_of(p, p.ck.table_row ? __ldcg(p.ck.table_row + b) : b, tok);
 }
 
 // Blocks of kTileN tokens seen by the rows at positions [p0, p1] of a sequence with `cap` tokens
@@ -52,11 +93,11 @@ struct ChunkTiles {
   int n_first, win, n;
 };
 
-__device__ __forceinline__ ChunkTiles chunk_tiles(int window, int n_sink, int cap, int p0, int p1) {
+__device__ __forceinline__ ChunkTiles chunk_tiles(int window, int n_sink, int cap, int skip, int p0, int p1) {
   constexpr int tile = kTileN;
   ChunkTiles t;
   t.hi = min(max(p1 + 1, 0), cap);
-  t.lo = (window > 0 && p0 >= window) ? p0 - window + 1 : 0;
+  t.lo = (window > 0 && p0 >= window) ? p0 - window + 1 : skip;  // (a call with skips has no window)
   t.sinks = min(n_sink, t.hi);
   if (t.sinks >= t.lo) t.lo = 0;  // the sinks reach the window: one range
   t.n_first = t.lo > 0 ? (t.sinks + tile - 1) / tile : 0;
@@ -69,10 +110,10 @@ __device__ __forceinline__ ChunkTiles chunk_tiles(int window, int n_sink, int ca
 
 // Row tiles per KV head, and KV tiles of the row tile that has most: the last one; with a window, an
 // earlier one may touch a block more than the last, so there the bound is of their length alone.
-__device__ __forceinline__ void chunk_extent(const ChunkArgs& a, int n, int m, int* row_tiles, int* kv_tiles) {
+__device__ __forceinline__ void chunk_extent(const ChunkArgs& a, int n, int m, int skip, int* row_tiles, int* kv_tiles) {
   *row_tiles = static_cast<int>((static_cast<int64_t>(n) * a.group_rows + a.rows - 1) / a.rows);
   const int span = min(n, (a.rows + a.group_rows - 1) / a.group_rows + 1);
-  const ChunkTiles t = chunk_tiles(a.window, a.n_sink, a.cap, m - span, m - 1);
+  const ChunkTiles t = chunk_tiles(a.window, a.n_sink, a.cap, skip, a.whole ? m - 1 : m - span, m - 1);
   int blocks = t.n;
   if (a.window > 0 && *row_tiles > 1) {
     const int64_t seen = static_cast<int64_t>(a.window) - 1 + span;  // tokens of a row tile's window
@@ -140,9 +181,9 @@ __device__ __forceinline__ void chunk_make_plan(const ChunkArgs& a, int64_t* sm_
   const int tid = threadIdx.x;
   int64_t w = 0, zero = 0, total, unused;
   for (int b = tid; b < a.B; b += NT) {
-    int row0, n, m, rt, kt;
-    chunk_lengths(a, b, &row0, &n, &m);
-    chunk_extent(a, n, m, &rt, &kt);
+    int row0, n, m, skip, rt, kt;
+    chunk_lengths(a, b, &row0, &n, &m, &skip);
+    chunk_extent(a, n, m, skip, &rt, &kt);
     w += static_cast<int64_t>(rt) * a.Hkv * kt;
   }
   chunk_block_scan<NT>(w, zero, &total, &unused, sm_scan);
@@ -152,10 +193,10 @@ __device__ __forceinline__ void chunk_make_plan(const ChunkArgs& a, int64_t* sm_
   int64_t it0 = 0, part0 = 0, mr0 = 0;  // of the sequences before this pass
   for (int b0 = 0; b0 < a.B; b0 += NT) {
     const int b = b0 + tid;
-    int row0 = 0, n = 0, m = 0, rt = 0, kt = 1, k = 1;
+    int row0 = 0, n = 0, m = 0, skip = 0, rt = 0, kt = 1, k = 1;
     if (b < a.B) {
-      chunk_lengths(a, b, &row0, &n, &m);
-      chunk_extent(a, n, m, &rt, &kt);
+      chunk_lengths(a, b, &row0, &n, &m, &skip);
+      chunk_extent(a, n, m, skip, &rt, &kt);
       k = max(1, kt / L);
     }
     const int64_t mine = static_cast<int64_t>(rt) * a.Hkv * k;
@@ -180,7 +221,7 @@ __device__ __forceinline__ void chunk_make_plan(const ChunkArgs& a, int64_t* sm_
 __device__ __forceinline__ ChunkItem chunk_item_of(const ChunkArgs& a, int b, int r, int rt, int k, int part_row) {
   ChunkItem it;
   it.b = b;
-  chunk_lengths(a, b, &it.row0, &it.n, &it.m);
+  chunk_lengths(a, b, &it.row0, &it.n, &it.m, &it.skip);
   it.n_chunk = k;
   it.part_row = part_row;
   it.c = r % k;
@@ -229,6 +270,7 @@ struct ChunkShare {
 struct ChunkPiece {
   int b, g, mt;
   int row0, n, m;   // first packed row, new tokens, cached tokens with them
+  int skip;         // of those, the first ones that another pass attends
   ChunkTiles tl;
   int i0, n_tiles;  // its blocks in tl's run
   int slot;         // the partial's number, two of each CTA; < 0: the whole item, final
@@ -242,12 +284,12 @@ struct ChunkPiece {
 // before ends.)
 struct ChunkRuns {
   int64_t left;  // tiles left
-  int cta, b, row0, n, m, rt, kt;  // kt: with the start
+  int cta, b, row0, n, m, skip, rt, kt;  // kt: with the start
   int g, mt, s;  // the next piece's item, and its first tile there
   bool head;
   __device__ __forceinline__ void load(const ChunkArgs& a) {
-    chunk_lengths(a, b, &row0, &n, &m);
-    chunk_extent(a, n, m, &rt, &kt);
+    chunk_lengths(a, b, &row0, &n, &m, &skip);
+    chunk_extent(a, n, m, skip, &rt, &kt);
     kt += a.start;
   }
   // Tiles [at, at + count) of those from sequence `seq` on (which holds the first of them).
@@ -271,11 +313,12 @@ struct ChunkRuns {
       mt = rt - 1;
     }
     const int e = static_cast<int>(min(static_cast<int64_t>(kt), s + left));
-    pc->b = b, pc->row0 = row0, pc->n = n, pc->m = m;
+    pc->b = b, pc->row0 = row0, pc->n = n, pc->m = m, pc->skip = skip;
     pc->mt = mt;
     pc->g = g;
     const int m0 = mt * a.rows, m_last = min(m0 + a.rows, n * a.group_rows) - 1;
-    pc->tl = chunk_tiles(a.window, a.n_sink, a.cap, m - n + m0 / a.group_rows, m - n + m_last / a.group_rows);
+    const int pos0 = chunk_pos0(a, n, m), step = chunk_pos_step(a);
+    pc->tl = chunk_tiles(a.window, a.n_sink, a.cap, skip, pos0 + m0 / a.group_rows * step, pos0 + m_last / a.group_rows * step);
     pc->i0 = min(max(s - a.start, 0), pc->tl.n);
     pc->n_tiles = min(max(e - a.start, 0), pc->tl.n) - pc->i0;  // (an earlier row tile may see fewer than kt)
     pc->slot = (s == 0 && e == kt) ? -1 : 2 * cta + (head ? 0 : 1);
@@ -297,9 +340,9 @@ __device__ __forceinline__ bool chunk_find_runs(const ChunkArgs& a, int n_cta, i
   const int tid = threadIdx.x;
   int64_t w = 0, zero = 0, total, unused;
   for (int b = tid; b < a.B; b += NT) {
-    int row0, n, m, rt, kt;
-    chunk_lengths(a, b, &row0, &n, &m);
-    chunk_extent(a, n, m, &rt, &kt);
+    int row0, n, m, skip, rt, kt;
+    chunk_lengths(a, b, &row0, &n, &m, &skip);
+    chunk_extent(a, n, m, skip, &rt, &kt);
     w += static_cast<int64_t>(rt) * a.Hkv * (kt + a.start);
   }
   chunk_block_scan<NT>(w, zero, &total, &unused, sm_scan);
@@ -313,10 +356,10 @@ __device__ __forceinline__ bool chunk_find_runs(const ChunkArgs& a, int n_cta, i
   int64_t before = 0;
   for (int b0 = 0; b0 < a.B && before <= u; b0 += NT) {  // uniform in the block
     const int b = b0 + tid;
-    int row0, n, m, rt = 0, kt = 1;
+    int row0, n, m, skip, rt = 0, kt = 1;
     if (b < a.B) {
-      chunk_lengths(a, b, &row0, &n, &m);
-      chunk_extent(a, n, m, &rt, &kt);
+      chunk_lengths(a, b, &row0, &n, &m, &skip);
+      chunk_extent(a, n, m, skip, &rt, &kt);
     }
     const int64_t mine = static_cast<int64_t>(rt) * a.Hkv * (kt + a.start);
     int64_t x = mine, y = 0, tx, ty;

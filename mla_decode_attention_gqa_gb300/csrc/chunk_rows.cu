@@ -1,6 +1,7 @@
 // Attention of few new tokens over a paged cache (attn_chunk_paged): decode steps and proposed
 // tokens, 16 or 32 rows (new token, head of the group) of a KV head at a time, causal or with a
-// sliding window and sinks; bf16 pages, or fp8-e4m3 pages with block scales.
+// sliding window and sinks; bf16 pages, fp8-e4m3 pages with block scales, or 4-bit pages (e2m1 codes,
+// an e4m3 scale for each 16 dims of a token's head and an fp32 scale a head).
 //
 // For every row (new token at position p, query head h of KV head g): s_u = scale q.k_u over the
 // visible tokens u (u <= p and u > p - window or u < n_sink), out = softmax(s) V, lse = ln sum e^s,
@@ -33,9 +34,11 @@ namespace {
 
 constexpr int kRows = 16;  // rows of a warp
 
-template <bool FP8_, int D_, int WM_, int WN_, int NSTAGE_>
+template <PageFormat PAGES_, int D_, int WM_, int WN_, int NSTAGE_>
 struct RowsCfg {
-  static constexpr bool FP8 = FP8_;
+  static constexpr PageFormat PAGES = PAGES_;
+  static constexpr bool FP4 = PAGES == kPagesFp4;
+  static constexpr bool FP8 = PAGES != kPagesBf16;  // codes: the products run in fp16
   static constexpr int D = D_;
   static constexpr int WM = WM_;          // sets of 16 rows, which share the tiles
   static constexpr int WN = WN_;          // consumer warps of a set
@@ -44,11 +47,12 @@ struct RowsCfg {
   static constexpr int NSTAGE = NSTAGE_;  // tiles in the ring
   static constexpr int TN = kTileN;
   static constexpr int ESZ = FP8 ? 1 : 2;
-  static constexpr int NBOX = D * ESZ / 128;  // 128-byte boxes of a token row
+  static constexpr int NBOX = FP4 ? 1 : D * ESZ / 128;  // 128-byte boxes of a token row (4-bit: one of 64)
   static constexpr int BOX_ELEMS = 128 / ESZ;
-  static constexpr int BOX_BYTES = TN * 128;
+  static constexpr int BOX_BYTES = FP4 ? TN * (D / 2) : TN * 128;
   static constexpr int TILE = NBOX * BOX_BYTES;
-  static constexpr int STAGE = 2 * TILE;
+  static constexpr int SCALES = FP4 ? TN * (D / kFp4Block) : 0;  // 4-bit: the scales of a tile's blocks
+  static constexpr int STAGE = 2 * (TILE + SCALES);  // K, V, K's scales, V's
   static constexpr int THREADS = (WM * WN + 1) * 32;
   // Full barriers are per consumer warp (of each set), DW of them each: a warp's wait is then always for the
   // phase after the one it saw last, whatever the other warps' tiles do
@@ -77,6 +81,15 @@ template <class C>
 __device__ __forceinline__ uint32_t tile_off(uint32_t tok, uint32_t byte) {
   return (byte >> 7) * C::BOX_BYTES + swz128(tok, byte & 127u);
 }
+// Byte `byte` of token `tok`'s row of a 4-bit tile: 64-byte rows under the 64-byte swizzle.
+__device__ __forceinline__ uint32_t tile4_off(uint32_t tok, uint32_t byte) {
+  return tok * 64u + ((((byte >> 4) ^ ((tok >> 1) & 3u)) << 4) | (byte & 15u));
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 __device__ __forceinline__ uint32_t half_mask(bool lo, bool hi) {
   return (lo ? 0x0000FFFFu : 0u) | (hi ? 0xFFFF0000u : 0u);
 }
@@ -90,8 +103,8 @@ __device__ __forceinline__ void consumers_sync(int set) {  // the consumer warps
 
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, C::CTAS)
-    chunk_rows_kernel(const __grid_constant__ PartialParams p, const __grid_constant__ CUtensorMap tmk,
-                      const __grid_constant__ CUtensorMap tmv) {
+    chunk_rows_kernel(const __grid_constant__ PartialParams p, const __grid_constant__ ChunkMaps maps) {
+  const CUtensorMap &tmk = maps.k, &tmv = maps.v;
   constexpr int D = C::D, TN = C::TN, NSTAGE = C::NSTAGE, WN = C::WN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -124,7 +137,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         int pages = 0, rows = 0;
         if (i0 + lane < pc.n_tiles) {
           const int t = pc.token(i0 + lane);
-          pages = kv_page_of(p, pc.b, t);
+          pages = chunk_page_of(p, pc.b, t);
           rows = t % p.block_len;
         }
         const int n = min(32, pc.n_tiles - i0);
@@ -141,6 +154,10 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
               for (int bx = 0; bx < C::NBOX; ++bx) {
                 tma_load_4d(ks + bx * C::BOX_BYTES, &tmk, fb, bx * C::BOX_ELEMS, row, pc.g, page, pol);
                 tma_load_4d(ks + C::TILE + bx * C::BOX_BYTES, &tmv, fb, bx * C::BOX_ELEMS, row, pc.g, page, pol);
+              }
+              if constexpr (C::FP4) {
+                tma_load_4d(ks + 2 * C::TILE, &maps.k_block, fb, row * (D / kFp4Block / 4), pc.g, page, 0, pol);
+                tma_load_4d(ks + 2 * C::TILE + C::SCALES, &maps.v_block, fb, row * (D / kFp4Block / 4), pc.g, page, 0, pol);
               }
             }
           }
@@ -187,8 +204,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     const int tq0 = v0 ? mrow0 / p.G : 0, tq1 = v1 ? mrow1 / p.G : 0;
     const int h0 = pc.g * p.G + (v0 ? mrow0 % p.G : 0), h1 = pc.g * p.G + (v1 ? mrow1 % p.G : 0);
     // visible tokens of a row: [wl, hz] and below the sinks' end; all below the item's end
-    const int pos0 = pc.m - pc.n;
-    const int hz0 = pos0 + tq0, hz1 = pos0 + tq1, hz_min = pos0 + mset / p.G;
+    const int pos0 = chunk_pos0(p.ck, pc.n, pc.m), pos_step = chunk_pos_step(p.ck);
+    const int hz0 = pos0 + tq0 * pos_step, hz1 = pos0 + tq1 * pos_step, hz_min = pos0 + mset / p.G * pos_step;
     auto window_lo = [&](int pos) -> int { return p.ck.window > 0 && pos >= p.ck.window ? pos - p.ck.window + 1 : 0; };
     const int wl0 = window_lo(hz0), wl1 = window_lo(hz1);
     const int wl_max = window_lo(pos0 + min(mset + kRows - 1, rows_total - 1) / p.G);
@@ -222,7 +239,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           for (int ks = 0; ks < D / 16; ++ks) {
             // k-slots (2tq, 2tq+1 | 2tq+8, 2tq+9) hold d = 16ks + 4tq + (0,1 | 2,3), the order in
             // which ldmatrix delivers the e4m3 key bytes
-            const int d0 = 16 * ks + 4 * tq;
+            // (4-bit: of a chunk of 32 dims the lane has 8 tq .. 8 tq + 7, half for each step)
+            const int d0 = C::FP4 ? 32 * (ks >> 1) + 8 * tq + 4 * (ks & 1) : 16 * ks + 4 * tq;
             u[0][ks] = v0 ? *reinterpret_cast<const uint2*>(q0 + d0) : make_uint2(0u, 0u);
             u[1][ks] = v1 ? *reinterpret_cast<const uint2*>(q1 + d0) : make_uint2(0u, 0u);
 #pragma unroll
@@ -254,6 +272,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       }
     }
 
+    const float k_head = C::FP4 ? head_scale(p.k_head, pc.g) : 1.f;
     float o[D / 8][4];
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -272,9 +291,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       const int x = x0 + i, s = x % NSTAGE;
       const int t0 = pc.token(i);
       float ksc = 1.f, vsc = 1.f;
-      if constexpr (C::FP8) {
+      if constexpr (C::PAGES == kPagesFp8) {
         // a page outside the cache reads as zeros through TMA; its scale is never fetched
-        const int page = kv_page_of(p, pc.b, t0);
+        const int page = chunk_page_of(p, pc.b, t0);
         ksc = vsc = 0.f;
         if (page >= 0 && page < p.num_blocks) {
           const int per = p.block_len / p.scale_block;
@@ -310,6 +329,31 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             mma_bf16(sc[2 * np + 1], qa[ks], r2, r3);
           }
         }
+      } else if constexpr (C::FP4) {
+        // 8 tokens at a time: a lane has token gq, of each chunk of 32 dims 8 tq .. 8 tq + 7, which
+        // lie in one block.  Code times block scale is exact in fp16 (6 bits, 2^-10 to 2688)
+        const uint8_t* ksb = smem + s * C::STAGE + 2 * C::TILE;
+#pragma unroll
+        for (int nt = 0; nt < TN / 8; ++nt) {
+          uint32_t w[4];
+          ldsm_x4(kbase + tile4_off(8 * nt + (lane & 7), mi * 16), w[0], w[1], w[2], w[3]);
+          const uint2 sb = *reinterpret_cast<const uint2*>(ksb + (8 * nt + gq) * (D / kFp4Block));
+          // the scales of blocks (tq >> 1) + 2 c
+          uint32_t s01, s23;
+          e4m3x4_to_f16x2x2(prmt(sb.x, sb.y, (tq >> 1) ? 0x7531u : 0x6420u), s01, s23);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t by = prmt(c < 2 ? s01 : s23, 0u, (c & 1) ? 0x3232u : 0x1010u);
+            uint32_t k0, k1, k2, k3;
+            e2m1x8_to_f16x2x4(w[c], k0, k1, k2, k3);
+            const uint4 qv0 = qfrag[2 * c * 32 + lane];
+            const uint4 qv1 = qfrag[(2 * c + 1) * 32 + lane];
+            const uint32_t qa0[4] = {qv0.x, qv0.y, qv0.z, qv0.w};
+            const uint32_t qa1[4] = {qv1.x, qv1.y, qv1.z, qv1.w};
+            mma_f16(sc[nt], qa0, mul_f16x2(k0, by), mul_f16x2(k1, by));
+            mma_f16(sc[nt], qa1, mul_f16x2(k2, by), mul_f16x2(k3, by));
+          }
+        }
       } else {
 #pragma unroll
         for (int ks = 0; ks < D / 16; ks += 2) {
@@ -339,6 +383,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       // ---- scale, mask, online softmax
       float sl[2] = {p.scale_log2, p.scale_log2};
       if constexpr (C::FP8) {
+        if constexpr (C::FP4) ksc = k_head;
         sl[0] = reinterpret_cast<volatile const float*>(q_scale)[gq] * ksc;
         sl[1] = reinterpret_cast<volatile const float*>(q_scale)[gq + 8] * ksc;
       }
@@ -498,6 +543,48 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
               mma_bf16(o[2 * dp], pa[kk], r0, r1);
               mma_bf16(o[2 * dp + 1], pa[kk], r2, r3);
             }
+          } else if constexpr (C::FP4) {
+            // as below, 4 dims of two tokens a lane: of dims 32 c + 4 gq + i the nibbles of both tokens
+            // make one byte, and so one pair.  Row gq of the product's tiles 2 c and 2 c + 1 is
+            // dim 4 gq or 4 gq + 2, row gq + 8 the next one
+            const uint32_t b00 = pa[kk][0], b01 = pa[kk][2], b10 = pa[kk][1], b11 = pa[kk][3];
+            const uint8_t* vsb = smem + s * C::STAGE + 2 * C::TILE + C::SCALES + (16 * kk + 2 * tq) * (D / kFp4Block);
+            const uint4 sa = *reinterpret_cast<const uint4*>(vsb);  // two tokens' scales
+            const uint4 sb = *reinterpret_cast<const uint4*>(vsb + 8 * (D / kFp4Block));
+            uint32_t sv[2][4];  // scales of the pairs of tokens, blocks 2 c + (gq >> 2)
+            {
+              const uint32_t sel = (gq >> 2) ? 0x7351u : 0x6240u;  // (t0, t1) of a word's first, then second block
+              e4m3x4_to_f16x2x2(prmt(sa.x, sa.z, sel), sv[0][0], sv[0][1]);
+              e4m3x4_to_f16x2x2(prmt(sa.y, sa.w, sel), sv[0][2], sv[0][3]);
+              e4m3x4_to_f16x2x2(prmt(sb.x, sb.z, sel), sv[1][0], sv[1][1]);
+              e4m3x4_to_f16x2x2(prmt(sb.y, sb.w, sel), sv[1][2], sv[1][3]);
+            }
+            auto pairs = [](uint32_t w, uint32_t* f) {  // dims 0, 1, 2, 3 of both tokens
+              const uint32_t even = (w & 0x0F0Fu) | ((w >> 12) & 0xF0F0u);         // dims 0 and 2
+              const uint32_t odd = ((w >> 4) & 0x0F0Fu) | ((w >> 16) & 0xF0F0u);  // dims 1 and 3
+              e2m1x8_to_f16x2x4(even | (odd << 16), f[0], f[2], f[1], f[3]);
+            };
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              const uint32_t tok = 16 * kk + ((lane >> 3) & 1) * 8 + (lane & 7);
+              uint32_t r0, r1;
+              ldsm_x2_t(vbase + tile4_off(tok, c * 16), r0, r1);
+              uint32_t f[2][4];
+              pairs(r0, f[0]);
+              pairs(r1, f[1]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                f[0][i] = mul_f16x2(f[0][i], sv[0][c]);
+                f[1][i] = mul_f16x2(f[1][i], sv[1][c]);
+                if constexpr (decltype(vmasked)::value) f[0][i] &= mlo, f[1][i] &= mhi;  // (the scales may be anything too)
+              }
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const uint32_t a[4] = {f[0][2 * i], f[0][2 * i + 1], f[1][2 * i], f[1][2 * i + 1]};
+                mma_f16(o[2 * (2 * c + i)], a, b00, b01);
+                mma_f16(o[2 * (2 * c + i) + 1], a, b10, b11);
+              }
+            }
           } else {
             // O^T[dv x rows] += V^T[dv x tok] P^T[tok x rows]: ldmatrix.trans of the e4m3 tile
             // (16-bit view) gives each lane two tokens x two dims, one byte permute pairs them by
@@ -550,6 +637,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       for (int w = 0; w < WN; ++w) L[r] += ml[(w * kRows + gq + 8 * r) * 2 + 1] * fast_exp2(ml[(w * kRows + gq + 8 * r) * 2] - base);
       f[r] = fast_exp2(mrun[r] - base);
       if constexpr (C::FP8) f[r] *= __uint_as_float((254u << 23) - __float_as_uint(up[r]));  // 1 / up
+      if constexpr (C::FP4) f[r] *= head_scale(p.v_head, pc.g);
       // (a warp without a tile has O = 0; 0 * 2^-inf = 0)
     }
     // the factor of each element: rows gq, gq + 8; fp8: O^T, rows 2tq, 2tq+1 (+8)
@@ -589,24 +677,43 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       const int64_t row_a = direct ? (pc.row0 + static_cast<int64_t>(tq0)) * p.Hq + h0
                                    : static_cast<int64_t>(pc.slot) * C::ROWS + wm * kRows + gq;
       const int64_t row_b = direct ? (pc.row0 + static_cast<int64_t>(tq1)) * p.Hq + h1 : row_a + 8;
-      auto store2 = [&](int64_t row, int d, float y0, float y1) {
-        if (direct)
-          *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.ck.out) + row * D + d) = pack_bf16(y0, y1);
-        else
-          *reinterpret_cast<float2*>(p.out_o + row * D + d) = make_float2(y0, y1);
-      };
       const bool some0 = L[0] != 0.f, some1 = L[1] != 0.f;
-      const float inv0 = some0 ? 1.f / L[0] : 0.f, inv1 = some1 ? 1.f / L[1] : 0.f;
+      float inv0 = some0 ? 1.f / L[0] : 0.f, inv1 = some1 ? 1.f / L[1] : 0.f;
       const bool w0 = v0 && (some0 || direct), w1 = v1 && (some1 || direct);
+      float lse0 = some0 ? (M[0] + __log2f(L[0])) * kLn2 : -INFINITY, lse1 = some1 ? (M[1] + __log2f(L[1])) * kLn2 : -INFINITY;
+      float prior0 = 0.f, prior1 = 0.f;  // weights of the prefix's result
+      if (direct && pc.skip > 0) {
+        if (v0) {
+          const ChunkJoin j = chunk_join(lse0, __ldcg(p.ck.prior_lse + row_a));
+          inv0 *= j.own, prior0 = j.prior, lse0 = j.lse;
+        }
+        if (v1) {
+          const ChunkJoin j = chunk_join(lse1, __ldcg(p.ck.prior_lse + row_b));
+          inv1 *= j.own, prior1 = j.prior, lse1 = j.lse;
+        }
+      }
+      const bool f32 = !direct || p.ck.out_f32;
+      float* out_f = direct ? static_cast<float*>(p.ck.out) : p.out_o;
+      auto store2 = [&](int64_t row, int d, float y0, float y1, float prior) {
+        if (prior != 0.f) {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(p.ck.prior_o + row * D + d));
+          y0 = fmaf(x.x, prior, y0), y1 = fmaf(x.y, prior, y1);
+        }
+        if (f32)
+          *reinterpret_cast<float2*>(out_f + row * D + d) = make_float2(y0, y1);
+        else
+          *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.ck.out) + row * D + d) = pack_bf16(y0, y1);
+      };
       if constexpr (!C::FP8) {
 #pragma unroll
         for (int nt = 0; nt < D / 8; ++nt) {
           const int d = 8 * nt + 2 * tq;
-          if (w0) store2(row_a, d, o[nt][0] * inv0, o[nt][1] * inv0);
-          if (w1) store2(row_b, d, o[nt][2] * inv1, o[nt][3] * inv1);
+          if (w0) store2(row_a, d, o[nt][0] * inv0, o[nt][1] * inv0, prior0);
+          if (w1) store2(row_b, d, o[nt][2] * inv1, o[nt][3] * inv1, prior1);
         }
       } else {
         // O^T: this thread holds rows (8n + 2tq + {0,1}) at dv 16c + 2gq + {0,1}
+        // (4-bit: 32 (c >> 1) + 4 gq + 2 (c & 1) + {0,1})
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
 #pragma unroll
@@ -615,18 +722,20 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             const float inv = __shfl_sync(0xffffffffu, n ? inv1 : inv0, src);
             const bool wr = __shfl_sync(0xffffffffu, (n ? w1 : w0) ? 1 : 0, src) != 0;
             const int64_t row = __shfl_sync(0xffffffffu, n ? row_b : row_a, src);
+            const float prior = __shfl_sync(0xffffffffu, n ? prior1 : prior0, src);
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
               const float* ov = o[2 * c + n];
-              if (wr) store2(row, 16 * c + 2 * gq, ov[e] * inv, ov[2 + e] * inv);
+              const int d = C::FP4 ? 32 * (c >> 1) + 4 * gq + 2 * (c & 1) : 16 * c + 2 * gq;
+              if (wr) store2(row, d, ov[e] * inv, ov[2 + e] * inv, prior);
             }
           }
         }
       }
       if (tq == 0) {
         float* lse = direct ? p.ck.lse : p.out_lse;
-        if (v0) lse[row_a] = some0 ? (M[0] + __log2f(L[0])) * kLn2 : -INFINITY;
-        if (v1) lse[row_b] = some1 ? (M[1] + __log2f(L[1])) * kLn2 : -INFINITY;
+        if (v0) lse[row_a] = lse0;
+        if (v1) lse[row_b] = lse1;
       }
     }
     // (the next piece writes ml and obuf behind a sync that the first warp reaches after this)
@@ -636,38 +745,40 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 // (two sets with bf16 heads of 128: 5 warps a set have 168 registers each, too few: 95 us for 24
 // sequences of 5 rows, 40 / 8 heads, where 3 warps of 233 take 90; the other two fit, fp8 104 -> 90)
 template <int WM>
-using CfgBf16D64 = RowsCfg<false, 64, WM, WM == 1 ? 4 : 5, WM == 1 ? 6 : 12>;
+using CfgBf16D64 = RowsCfg<kPagesBf16, 64, WM, WM == 1 ? 4 : 5, WM == 1 ? 6 : 12>;
 template <int WM>
-using CfgBf16D128 = RowsCfg<false, 128, WM, 3, WM == 1 ? 3 : 6>;
+using CfgBf16D128 = RowsCfg<kPagesBf16, 128, WM, 3, WM == 1 ? 3 : 6>;
 template <int WM>
-using CfgFp8D128 = RowsCfg<true, 128, WM, WM == 1 ? 4 : 5, WM == 1 ? 6 : 12>;
+using CfgFp8D128 = RowsCfg<kPagesFp8, 128, WM, WM == 1 ? 4 : 5, WM == 1 ? 6 : 12>;
+template <int WM>
+using CfgFp4D128 = RowsCfg<kPagesFp4, 128, WM, WM == 1 ? 4 : 5, WM == 1 ? 8 : 15>;
 
 template <class C>
-cudaError_t launch_cfg(const PartialParams& p, const CUtensorMap& tmk, const CUtensorMap& tmv, cudaStream_t stream) {
+cudaError_t launch_cfg(const PartialParams& p, const ChunkMaps& maps, cudaStream_t stream) {
   static std::atomic<uint64_t> attr_done{0};  // per variant, per device
   cudaError_t e0 = once_per_device(attr_done, [] {
     return cudaFuncSetAttribute(chunk_rows_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   });
   if (e0 != cudaSuccess) return e0;
-  chunk_rows_kernel<C><<<static_cast<unsigned int>(p.ck.n_wave), C::THREADS, C::SMEM, stream>>>(p, tmk, tmv);
+  chunk_rows_kernel<C><<<static_cast<unsigned int>(p.ck.n_wave), C::THREADS, C::SMEM, stream>>>(p, maps);
   return cudaGetLastError();
 }
 
 template <int WM>
-cudaError_t launch_sets(const PartialParams& p, int32_t d, bool fp8, const CUtensorMap& tmk, const CUtensorMap& tmv,
-                        cudaStream_t stream) {
-  if (fp8) return launch_cfg<CfgFp8D128<WM>>(p, tmk, tmv, stream);
-  if (d == 64) return launch_cfg<CfgBf16D64<WM>>(p, tmk, tmv, stream);
-  return launch_cfg<CfgBf16D128<WM>>(p, tmk, tmv, stream);
+cudaError_t launch_sets(const PartialParams& p, int32_t d, PageFormat pages, const ChunkMaps& maps, cudaStream_t stream) {
+  if (pages == kPagesFp4) return launch_cfg<CfgFp4D128<WM>>(p, maps, stream);
+  if (pages == kPagesFp8) return launch_cfg<CfgFp8D128<WM>>(p, maps, stream);
+  if (d == 64) return launch_cfg<CfgBf16D64<WM>>(p, maps, stream);
+  return launch_cfg<CfgBf16D128<WM>>(p, maps, stream);
 }
 
 }  // namespace
 
 int chunk_rows_ctas_per_sm(int rows) { return rows == kRows ? 2 : 1; }
 
-cudaError_t launch_chunk_rows(const PartialParams& p, int32_t d, bool fp8, const CUtensorMap& tmk, const CUtensorMap& tmv,
+cudaError_t launch_chunk_rows(const PartialParams& p, int32_t d, PageFormat pages, const ChunkMaps& maps,
                               cudaStream_t stream) {
-  return p.ck.rows == kRows ? launch_sets<1>(p, d, fp8, tmk, tmv, stream) : launch_sets<2>(p, d, fp8, tmk, tmv, stream);
+  return p.ck.rows == kRows ? launch_sets<1>(p, d, pages, maps, stream) : launch_sets<2>(p, d, pages, maps, stream);
 }
 
 }  // namespace skv

@@ -293,10 +293,11 @@ __device__ __noinline__ Redone redo_tile(uint32_t s_col, uint32_t o_col, bool ne
 // The warp's 32 output rows (orow: this lane's; bit r of write: row r exists) from tensor memory:
 // w0 O_k, plus w1 O_1 where both groups worked for the row, as bf16 or fp32.  64 bytes of every row
 // at a time go through shared memory, so that a store instruction covers 8 rows x 64 bytes instead
-// of 16 bytes of 32 rows.
+// of 16 bytes of 32 rows.  prior_o (or NULL), prior: the prefix's result and this row's weight of it.
 template <int D>
 __device__ __noinline__ void store_rows(uint32_t o_col, bool has0, bool has1, float w0, bool some0, float w1, bool some1,
-                                        unsigned write, int64_t orow, void* out, bool bf16, uint32_t stage) {
+                                        unsigned write, int64_t orow, void* out, bool bf16, uint32_t stage,
+                                        const float* prior_o, float prior) {
   const int lane = threadIdx.x & 31;
   const int row_bytes = bf16 ? D * 2 : D * 4;
   uint8_t* to[4];  // this lane's stores: 16 bytes of rows lane / 4 + 8 i
@@ -341,6 +342,17 @@ __device__ __noinline__ void store_rows(uint32_t o_col, bool has0, bool has1, fl
       for (int e = 0; e < 32; ++e)
         x[e >> 4][e & 15] = some0 ? __float_as_uint(__uint_as_float(x[e >> 4][e & 15]) * w0) : 0u;
     }
+    if (prior_o != nullptr && prior != 0.f) {
+#pragma unroll
+      for (int e = 0; e < 32; e += 4) {
+        const float4 u = __ldcg(reinterpret_cast<const float4*>(prior_o + orow * D + c + e));
+        uint32_t* y = &x[e >> 4][e & 15];
+        y[0] = __float_as_uint(fmaf(u.x, prior, __uint_as_float(y[0])));
+        y[1] = __float_as_uint(fmaf(u.y, prior, __uint_as_float(y[1])));
+        y[2] = __float_as_uint(fmaf(u.z, prior, __uint_as_float(y[2])));
+        y[3] = __float_as_uint(fmaf(u.w, prior, __uint_as_float(y[3])));
+      }
+    }
     if (bf16) {
 #pragma unroll
       for (int e = 0; e < 16; ++e)
@@ -357,8 +369,8 @@ __device__ __noinline__ void store_rows(uint32_t o_col, bool has0, bool has1, fl
 // the next, so that loads and first scores of one item run under the epilogue of the one before.
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
-    chunk_tc_kernel(const __grid_constant__ PartialParams p, const __grid_constant__ CUtensorMap tmq,
-                    const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
+    chunk_tc_kernel(const __grid_constant__ PartialParams p, const __grid_constant__ ChunkMaps maps) {
+  const CUtensorMap &tmq = maps.q, &tmk = maps.k, &tmv = maps.v;
   constexpr int D = C::D, NST = C::NST, NB = C::NB;
   static_assert(sizeof(TcBars<C>) <= C::OFF_ML - C::OFF_BAR, "barriers");
   static_assert(2 * sizeof(TcItem) <= C::OFF_QS - C::OFF_ITEM, "items");
@@ -449,8 +461,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           t.m0 = t.it.mt * 2 * kRowsTile;
           const int m_last = min(t.m0 + 2 * kRowsTile, t.it.n * Gr) - 1;
           t.pair = m_last - t.m0 >= kRowsTile ? 1 : 0;
-          const int pos0 = t.it.m - t.it.n;
-          t.tl = chunk_tiles(p.ck.window, p.ck.n_sink, p.ck.cap, pos0 + (t.m0 >> gr_bits), pos0 + (m_last >> gr_bits));
+          const int pos0 = chunk_pos0(p.ck, t.it.n, t.it.m), step = chunk_pos_step(p.ck);
+          t.tl = chunk_tiles(p.ck.window, p.ck.n_sink, p.ck.cap, t.it.skip, pos0 + (t.m0 >> gr_bits) * step,
+                             pos0 + (m_last >> gr_bits) * step);
           const int tiles = (t.tl.n + 1) / 2, per = (tiles + t.it.n_chunk - 1) / t.it.n_chunk;
           const int i0 = min(t.it.c * per, tiles);
           t.h0 = 2 * i0;
@@ -497,8 +510,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           const int a = first[0], b = first[1] < p.ck.cap ? first[1] : a;
           at[0] = a % p.block_len;
           at[1] = b % p.block_len;
-          page[0] = kv_page_of(p, t.it.b, a);
-          page[1] = kv_page_of(p, t.it.b, b);
+          page[0] = chunk_page_of(p, t.it.b, a);
+          page[1] = chunk_page_of(p, t.it.b, b);
           if constexpr (C::FP8) {
             // the scales of both halves, a lane each (K, V, K, V).  Halves in which no row sees a token,
             // and pages outside the cache, take 0: their scales may be anything
@@ -894,7 +907,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int m = t.m0 + (pair ? k * kRowsTile : 0) + row;
         const int t_q = m >> gr_bits, hg = m & (Gr - 1);
         const bool valid = m < t.it.n * Gr && hg < G;
-        const int pos = t.it.m - t.it.n + t_q;
+        const int pos = chunk_pos0(p.ck, t.it.n, t.it.m) + t_q * chunk_pos_step(p.ck);
         // visible tokens of this row: [lo_row, hi_row) and [0, sink_row)
         const int hi_row = valid ? min(max(pos + 1, 0), p.ck.cap) : 0;
         const int lo_row = (valid && p.ck.window > 0 && pos >= p.ck.window) ? pos - p.ck.window + 1 : 0;
@@ -1038,22 +1051,29 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       if (both && !wait(&bars->pv_done[1], (np1 - 1) & 1, kDevErrFullWait)) break;
       tc::fence_after_sync();
       const bool some = some0 || some1;
-      const float inv = some ? 1.f / l_sum : 0.f;
-      a0 *= inv;
-      a1 *= inv;
+      float inv = some ? 1.f / l_sum : 0.f;
       constexpr float kLn2 = 0.6931471805599453f;
-      const float lse = some ? (m_used + __log2f(l_sum)) * kLn2 : -INFINITY;
+      float lse = some ? (m_used + __log2f(l_sum)) * kLn2 : -INFINITY;
       const bool direct = t.it.n_chunk == 1;
       const bool valid = mine->w != 0;
       const int m = t.m0 + (pair ? k * kRowsTile : 0) + row;
       const int t_q = m >> gr_bits, h = t.it.g * G + (m & (Gr - 1));
       const int64_t orow = direct ? (static_cast<int64_t>(t.it.row0) + t_q) * p.Hq + h
                                   : t.it.part_row + (static_cast<int64_t>(t.it.c) * t.it.n + t_q) * p.Hq + h;
+      float prior = 0.f;  // weight of the prefix's result
+      const bool behind = direct && t.it.skip > 0;
+      if (behind && valid) {
+        const ChunkJoin j = chunk_join(lse, __ldcg(p.ck.prior_lse + orow));
+        inv *= j.own, prior = j.prior, lse = j.lse;
+      }
+      a0 *= inv;
+      a1 *= inv;
       // an empty partial's o is never read
       const unsigned write_o = __ballot_sync(0xffffffffu, valid && (direct || some));
       if (write_o != 0u) {
         store_rows<D>(o_col, t.n_tiles > 0, both, some0 ? a0 : 0.f, some0, some1 ? a1 : 0.f, some1, write_o, orow,
-                      direct ? p.ck.out : p.out_o, direct, smem_u32(smem + C::OFF_OUT + (warp - 4) * (32 * 64)));
+                      direct ? p.ck.out : p.out_o, direct && !p.ck.out_f32,
+                      smem_u32(smem + C::OFF_OUT + (warp - 4) * (32 * 64)), behind ? p.ck.prior_o : nullptr, prior);
       }
       if (valid) (direct ? p.ck.lse : p.out_lse)[orow] = lse;
       // (the next tile's p_full arrival orders these TMEM reads before the next PV writes O)
@@ -1069,8 +1089,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 }
 
 template <class C>
-cudaError_t launch_cfg(const PartialParams& p, const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv,
-                       int64_t n_items, cudaStream_t stream) {
+cudaError_t launch_cfg(const PartialParams& p, const ChunkMaps& maps, int64_t n_items, cudaStream_t stream) {
   static std::atomic<uint64_t> attr_done{0};
   cudaError_t e0 = once_per_device(attr_done, [] {
     return cudaFuncSetAttribute(chunk_tc_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
@@ -1088,7 +1107,7 @@ cudaError_t launch_cfg(const PartialParams& p, const CUtensorMap& tmq, const CUt
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, chunk_tc_kernel<C>, p, tmq, tmk, tmv);
+  return cudaLaunchKernelEx(&cfg, chunk_tc_kernel<C>, p, maps);
 }
 
 }  // namespace
@@ -1097,11 +1116,11 @@ int chunk_tc_rows() { return 2 * kRowsTile; }
 int chunk_tc_kv_tile() { return kTN; }
 int chunk_tc_kv_box() { return kHalf; }
 
-cudaError_t launch_chunk_tc(const PartialParams& p, int32_t d, bool fp8, const CUtensorMap& tmq, const CUtensorMap& tmk,
-                            const CUtensorMap& tmv, int64_t n_items, cudaStream_t stream) {
-  if (fp8) return launch_cfg<TcCfg<128, true>>(p, tmq, tmk, tmv, n_items, stream);
-  if (d == 64) return launch_cfg<TcCfg<64, false>>(p, tmq, tmk, tmv, n_items, stream);
-  return launch_cfg<TcCfg<128, false>>(p, tmq, tmk, tmv, n_items, stream);
+cudaError_t launch_chunk_tc(const PartialParams& p, int32_t d, PageFormat pages, const ChunkMaps& maps, int64_t n_items,
+                            cudaStream_t stream) {
+  if (pages == kPagesFp8) return launch_cfg<TcCfg<128, true>>(p, maps, n_items, stream);
+  if (d == 64) return launch_cfg<TcCfg<64, false>>(p, maps, n_items, stream);
+  return launch_cfg<TcCfg<128, false>>(p, maps, n_items, stream);
 }
 
 }  // namespace skv

@@ -5,9 +5,9 @@
 //   (y_a, y_b) <- (y_a cos_j - y_b sin_j, y_b cos_j + y_a sin_j)   for j < rot / 2, with
 //   (a, b) = (j, j + rot/2), or (2j, 2j + 1) interleaved; cos_j, sin_j: the row of the token's
 //   position in the caller's tables.  The query goes out in bf16, the key to its page row in
-//   bf16 or as the e4m3 code of y / scale (the block scale that the cache holds), the value
-//   likewise without norm and rotation.  Everything between the loads and the one rounding at
-//   the store is in fp32.
+//   bf16, as the e4m3 code of y / scale (the block scale that the cache holds), or as 4-bit codes
+//   with scales made here (see store_fp4), the value likewise without norm and rotation.
+//   Everything between the loads and the one rounding at the store is in fp32.
 //
 // Bound by HBM: each input is read once and each output written once.  A warp copies the heads by
 // bulk copies into a ring, 32 heads a stage, so that 40 KB a CTA are on their way whatever the
@@ -36,7 +36,7 @@ constexpr int kStages = 5;             // 40 KB for heads of 128
 // CTAs an SM.  bf16: two, a token's rotation held in registers while its heads pass (4096 tokens of
 // 128 + 16 heads 53 us; three CTAs that read it from shared memory for each head 56).  fp8: three,
 // whose warps hide the conversions (6800 tokens of 64 + 16 heads 62 us against 70).
-constexpr int ctas_per_sm(bool fp8) { return fp8 ? 3 : 2; }
+constexpr int ctas_per_sm(PageFormat pages) { return pages == kPagesBf16 ? 2 : 3; }
 constexpr int kMaxTokens = 64;         // tokens a CTA's run may touch: 8 a warp
 constexpr int kScaleHeads = 16;        // KV heads whose scales wait in shared memory
 
@@ -120,6 +120,44 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, const uint64_t* x, float 
     *reinterpret_cast<uint32_t*>(p) = w[0];
 }
 
+// Where a head's chunk `id` (of H values) is: lane of its 8, and which of the lane's two chunks.
+struct ChunkAt {
+  int lane, second;
+};
+template <int H>
+__device__ __forceinline__ ChunkAt chunk_at(int id, bool inter, int rot) {
+  const int n = 16, half = inter ? 8 : rot / (2 * H), turned = inter ? n : rot / H, rest = (n - turned) / 2;
+  ChunkAt c;
+  if (id < turned) {
+    c.second = id >= half;
+    c.lane = c.second ? id - half : id;
+  } else {
+    c.second = id >= turned + rest;
+    c.lane = id - turned - (c.second ? rest : 0) + half;
+  }
+  return c;
+}
+
+// One of a lane's chunks as 4-bit codes: 8 of the block's 16 dims, whose largest magnitude is `most`.
+//   s = e4m3(most / (6 h)),  code = e2m1(y / (s h)),  h: the head's scale.
+// The block's first chunk stores s.  A NaN in the block makes s NaN, and so the block; a magnitude
+// past 2688 h saturates.
+__device__ __forceinline__ void store_fp4(uint8_t* codes, uint8_t* scale, const uint64_t* x, float most, float h) {
+  const uint32_t s = h > 0.f ? __nv_cvt_float_to_fp8(__fdiv_rn(most, 6.f * h), __NV_SATFINITE, __NV_E4M3) : 0u;
+  const uint32_t wide = e4m3x2_to_f16x2(static_cast<uint16_t>(s));
+  const float by = __low2float(*reinterpret_cast<const __half2*>(&wide)) * h;
+  float y[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    unpack2(x[j], y[2 * j], y[2 * j + 1]);
+    // (a division: values of few bits often lie just between two codes, where a product with the
+    // reciprocal would fall to either side)
+    y[2 * j] = __fdiv_rn(y[2 * j], by), y[2 * j + 1] = __fdiv_rn(y[2 * j + 1], by);
+  }
+  *reinterpret_cast<uint32_t*>(codes) = by > 0.f ? f32x8_to_e2m1x8(y) : 0u;
+  if (scale) *scale = static_cast<uint8_t>(s);
+}
+
 // H norm weights as packed pairs.
 template <int H>
 __device__ __forceinline__ void load_weight(const void* w, bool bf16, int64_t at, uint64_t* x) {
@@ -161,11 +199,13 @@ struct Place {
 };
 
 // INTER: pairs (2j, 2j + 1) instead of (j, j + rot / 2).
-template <int D, bool FP8, bool INTER>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(FP8)) append_kernel(const __grid_constant__ AppendArgs a) {
+template <int D, PageFormat PAGES, bool INTER>
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(PAGES)) append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int H = D / 16;  // values of a chunk
   constexpr uint32_t kRowBytes = D * 2;
-  constexpr bool kHoldTurns = !FP8;
+  constexpr bool FP8 = PAGES == kPagesFp8, FP4 = PAGES == kPagesFp4;
+  constexpr bool kHoldTurns = PAGES == kPagesBf16;
+  static_assert(!FP4 || H == 8, "a block is two chunks");
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t(*ring)[kGroups * kRowBytes] = reinterpret_cast<uint8_t(*)[kGroups * kRowBytes]>(smem);
   __shared__ uint64_t full[kStages], empty[kStages];
@@ -234,6 +274,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(FP8)) append_kernel(cons
   const int c0 = INTER || in_rot ? f : a.rot + f - half;
   const int c1 = INTER ? D / 2 + f : in_rot ? f + half : a.rot + (D - a.rot) / 2 + f - half;
   const bool turn0 = INTER ? c0 < a.rot : in_rot, turn1 = INTER ? c1 < a.rot : in_rot;
+
+  // fp4: where the other half of each chunk's block is
+  ChunkAt mate0 = {0, 0}, mate1 = {0, 0};
+  if constexpr (FP4) {
+    mate0 = chunk_at<H>((c0 / H) ^ 1, INTER, a.rot);
+    mate1 = chunk_at<H>((c1 / H) ^ 1, INTER, a.rot);
+  }
 
   // Places: a lane for each token, so that the chains of loads of all tokens run side by side
   {
@@ -382,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(FP8)) append_kernel(cons
       const uint64_t inv2 = pack2(inv, inv);
 #pragma unroll
       for (int j = 0; j < H; ++j) x[j] = mul2(x[j], inv2);
-      if (is_q || !FP8) {
+      if (is_q || PAGES == kPagesBf16) {
 #pragma unroll
         for (int j = 0; j < H; ++j) {
           float u, v;
@@ -409,6 +456,28 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(FP8)) append_kernel(cons
         uint8_t* o = static_cast<uint8_t*>(is_v ? a.v_pages : a.k_pages) + to;
         store_e4m3<H>(o + c0, x, scale);
         store_e4m3<H>(o + c1, x + H / 2, scale);
+      } else if constexpr (FP4) {
+        // magnitudes order as their bits, NaN above infinity
+        uint32_t most0 = 0u, most1 = 0u;
+#pragma unroll
+        for (int j = 0; j < H / 2; ++j) {
+          float u, v;
+          unpack2(x[j], u, v);
+          most0 = max(most0, max(__float_as_uint(u) & 0x7FFFFFFFu, __float_as_uint(v) & 0x7FFFFFFFu));
+          unpack2(x[H / 2 + j], u, v);
+          most1 = max(most1, max(__float_as_uint(u) & 0x7FFFFFFFu, __float_as_uint(v) & 0x7FFFFFFFu));
+        }
+        const unsigned eight = 0xFFu << (lane & 24);  // the head's lanes, which are all here
+        const uint32_t u0 = __shfl_sync(eight, most0, mate0.lane, 8), u1 = __shfl_sync(eight, most1, mate0.lane, 8);
+        const uint32_t v0 = __shfl_sync(eight, most0, mate1.lane, 8), v1 = __shfl_sync(eight, most1, mate1.lane, 8);
+        most0 = max(most0, mate0.second ? u1 : u0);
+        most1 = max(most1, mate1.second ? v1 : v0);
+        uint8_t* o = static_cast<uint8_t*>(is_v ? a.v_pages : a.k_pages) + to;
+        uint8_t* sc = (is_v ? a.v_block : a.k_block) +
+                      ((pl.page * a.Hkv + g) * a.block_len + pl.at) * static_cast<int64_t>(D / kFp4Block);
+        const float hs = head_scale(is_v ? a.v_head : a.k_head, g);
+        store_fp4(o + c0 / 2, (c0 & 8) ? nullptr : sc + c0 / kFp4Block, x, __uint_as_float(most0), hs);
+        store_fp4(o + c1 / 2, (c1 & 8) ? nullptr : sc + c1 / kFp4Block, x + H / 2, __uint_as_float(most1), hs);
       } else {
         __nv_bfloat16* o = static_cast<__nv_bfloat16*>(is_v ? a.v_pages : a.k_pages) + to;
         store_chunk<H>(o + c0, r);
@@ -418,11 +487,11 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(FP8)) append_kernel(cons
   }
 }
 
-template <int D, bool FP8>
+template <int D, PageFormat PAGES>
 cudaError_t launch(AppendArgs a, int sms, cudaStream_t stream) {
   const int64_t n_heads = a.Hq + 2 * a.Hkv, pairs = a.T * n_heads;
   // equal runs for the CTAs that are resident at once, of one stage at least; a run touches kMaxTokens tokens at most
-  const int64_t runs = static_cast<int64_t>(sms) * ctas_per_sm(FP8);
+  const int64_t runs = static_cast<int64_t>(sms) * ctas_per_sm(PAGES);
   int64_t steps = (pairs + kGroups * runs - 1) / (kGroups * runs);
   steps = std::min<int64_t>(steps, std::max<int64_t>(1, (kMaxTokens - 2) * n_heads / kGroups));
   a.steps = static_cast<int>(steps);
@@ -431,30 +500,31 @@ cudaError_t launch(AppendArgs a, int sms, cudaStream_t stream) {
   const unsigned int blocks = static_cast<unsigned int>((pairs + steps * kGroups - 1) / (steps * kGroups));
   a.run_tokens = static_cast<int>((steps * kGroups + n_heads - 2) / n_heads + 1);
   const auto bytes = [](int tokens, int rot) {
-    return kStages * kGroups * D * 2 + tokens * (rot / 2 * 3 + (FP8 ? 2 * kScaleHeads : 0)) * 4;
+    return kStages * kGroups * D * 2 + tokens * (rot / 2 * 3 + (PAGES == kPagesFp8 ? 2 * kScaleHeads : 0)) * 4;
   };
   static std::atomic<uint64_t> attr_done{0};
   cudaError_t e = once_per_device(attr_done, [&] {
-    cudaError_t x = cudaFuncSetAttribute(append_kernel<D, FP8, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t x = cudaFuncSetAttribute(append_kernel<D, PAGES, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          bytes(kMaxTokens, D));
     if (x != cudaSuccess) return x;
-    return cudaFuncSetAttribute(append_kernel<D, FP8, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(append_kernel<D, PAGES, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 bytes(kMaxTokens, D));
   });
   if (e != cudaSuccess) return e;
   const size_t smem = bytes(a.run_tokens, a.rot);
   if (a.interleaved)
-    append_kernel<D, FP8, true><<<blocks, kThreads, smem, stream>>>(a);
+    append_kernel<D, PAGES, true><<<blocks, kThreads, smem, stream>>>(a);
   else
-    append_kernel<D, FP8, false><<<blocks, kThreads, smem, stream>>>(a);
+    append_kernel<D, PAGES, false><<<blocks, kThreads, smem, stream>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_append(const AppendArgs& a, int32_t d, bool fp8, int sms, cudaStream_t stream) {
-  if (d == 64) return launch<64, false>(a, sms, stream);
-  return fp8 ? launch<128, true>(a, sms, stream) : launch<128, false>(a, sms, stream);
+cudaError_t launch_append(const AppendArgs& a, int32_t d, PageFormat pages, int sms, cudaStream_t stream) {
+  if (d == 64) return launch<64, kPagesBf16>(a, sms, stream);
+  if (pages == kPagesFp4) return launch<128, kPagesFp4>(a, sms, stream);
+  return pages == kPagesFp8 ? launch<128, kPagesFp8>(a, sms, stream) : launch<128, kPagesBf16>(a, sms, stream);
 }
 
 }  // namespace skv

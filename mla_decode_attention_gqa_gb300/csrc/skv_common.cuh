@@ -169,6 +169,40 @@ __device__ __forceinline__ void e4m3x4_to_f16x2x2(uint32_t w, uint32_t& lo, uint
       : "r"(w));
 }
 
+// Eight e2m1 codes (nibble j of w, from the lowest) -> fp16 pairs (0, 1), (2, 3), (4, 5), (6, 7), exactly.
+__device__ __forceinline__ void e2m1x8_to_f16x2x4(uint32_t w, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  asm("{\n\t.reg .b8 p, q, r, s;\n\t"
+      "mov.b32 {p, q, r, s}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, p;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, q;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, r;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, s;\n\t}"
+      : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+      : "r"(w));
+}
+
+// Eight values as e2m1 codes (value j in nibble j): to the nearest, ties to even, +-6 at most.
+__device__ __forceinline__ uint32_t f32x8_to_e2m1x8(const float* x) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 p, q, r, s;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 p, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 q, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 r, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 s, %8, %7;\n\t"
+      "mov.b32 %0, {p, q, r, s};\n\t}"
+      : "=r"(w)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+  return w;
+}
+
+// The scale of a KV head's 4-bit pages (NULL: 1).  One outside [2^-64, 2^64] stands for zeros, where it
+// is written and where it is read: inside, products with a block scale neither vanish nor overflow.
+__device__ __forceinline__ float head_scale(const float* scales, int head) {
+  if (!scales) return 1.f;
+  const float s = __ldg(scales + head);
+  return s >= 5.421010862e-20f && s <= 1.844674407e19f ? s : 0.f;
+}
+
 // Byte permute: result byte i = byte sel_i of {b, a} (a = bytes 0..3).
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t d;

@@ -13,6 +13,11 @@ namespace skv {
 // Tokens per KV tile of the GQA partial kernel (and the chunk granularity).
 constexpr int kTileN = 64;
 
+// What a KV page holds: bf16; e4m3 codes and an fp32 scale for each (page, head, scale_block tokens);
+// e2m1 codes, two a byte, an e4m3 scale for each kFp4Block dims of a token's head, and an fp32 scale a head.
+enum PageFormat : int { kPagesBf16 = 0, kPagesFp8 = 1, kPagesFp4 = 2 };
+constexpr int kFp4Block = 16;
+
 // Kernel attributes set with cudaFuncSetAttribute belong to the current device's context,
 // so a launcher applies them the first time it launches on each device: `done` keeps one
 // bit per device (devices past 63 set them on every launch).
@@ -44,8 +49,20 @@ struct ChunkArgs {
   int32_t n_target; // most work items with several chunks per row tile
   int32_t start;    // few rows: tiles that an item counts besides its own (chunk_plan.cuh)
   int32_t* plan;    // device [kPlanHead + kPlanRow B] (chunk_plan.cuh)
-  void* out;        // bf16 [T][Hq][d]
+  void* out;        // [T][Hq][d]: bf16, or fp32 (out_f32)
   float* lse;       // fp32 [T][Hq]
+  // A shared prefix (attn_shared_prefix_paged; see shared_prefix.cu) runs as two passes.  Over the prefixes
+  // a "sequence" is a group: its rows are those of its sequences, its length the prefix, all of which every
+  // row sees (seq_lens: the prefixes; first_row, table_row: device [B]), and the result is fp32.  Over the
+  // rest, sequence b's tokens from skip[b] on (a multiple of kTileN) are attended, and rows with
+  // skip[b] > 0 are joined with the prefix's result (prior_o fp32 [T][Hq][d], prior_lse [T][Hq]).
+  const int32_t* group_rows_at;  // device [B + 1]: first packed row of each group (NULL: cu_q)
+  const int32_t* table_row;      // device [B]: block-table row of each group (NULL: b)
+  const int32_t* skip;           // device [B] (NULL: 0)
+  const float* prior_o;
+  const float* prior_lse;
+  int32_t whole;    // every row sees all of its sequence's tokens
+  int32_t out_f32;
 };
 // The plan's words (see chunk_plan.cuh).
 enum ChunkPlanWord : int { kPlanItems = 0, kPlanMerged = 1, kPlanNext = 2, kPlanHead = 4, kPlanRow = 5 };
@@ -97,6 +114,8 @@ struct PartialParams {
   int32_t ring_n;      // pass-Q ring: ranks (0: off) and query rows each rank owns; B then
   int32_t ring_bq;     //   counts ring_n * ring_n * ring_bq work rows (rank, step, slot)
   const int32_t* bounds;  // device [B][n_split + 1], or NULL: one split [0, S_max) per row
+  const float* k_head;  // 4-bit pages: [Hkv], or NULL: 1
+  const float* v_head;
   ChunkArgs ck;  // ragged chunks only: replaces Tq, bounds, n_split, n_chunk and m_tiles
 };
 
@@ -158,24 +177,41 @@ cudaError_t launch_gqa_partial(GqaVariant v, const PartialParams& p, const CUten
 // Ragged chunks of new tokens (p.ck): items in one piece write p.ck.out / p.ck.lse, the others
 // partial rows to p.out_o / p.out_lse, which the merge of the kernel joins.
 // Few rows (see chunk_rows.cu): row tiles of 16 or 32, n_wave CTAs, two partials of a row tile each;
-// tmk / tmv: pages with kTileN rows a box.
+// maps: pages with kTileN rows a box.
+struct ChunkMaps {
+  CUtensorMap q, k, v;
+  CUtensorMap k_block, v_block;  // 4-bit pages: the block scales
+};
 int chunk_rows_ctas_per_sm(int rows);
-cudaError_t launch_chunk_rows(const PartialParams& p, int32_t d, bool fp8, const CUtensorMap& tmk, const CUtensorMap& tmv,
+cudaError_t launch_chunk_rows(const PartialParams& p, int32_t d, PageFormat pages, const ChunkMaps& maps,
                               cudaStream_t stream);
 cudaError_t launch_chunk_runs_merge(const ChunkArgs& a, int32_t d, const float* part_o, const float* part_lse,
                                     cudaStream_t stream);
-// On the tensor cores (see chunk_tc.cu), any G <= 128; tmq: q as (dim, head, packed
-// row) with 64 x group_rows x 128 / group_rows boxes, tmk / tmv: pages with chunk_tc_kv_box()
+// On the tensor cores (see chunk_tc.cu), any G <= 128; maps.q: q as (dim, head, packed
+// row) with 64 x group_rows x 128 / group_rows boxes, maps.k / v: pages with chunk_tc_kv_box()
 // rows a box.
 // launch_chunk_plan, directly before it on the stream, writes the plan that it takes its items from.
 cudaError_t launch_chunk_plan(const ChunkArgs& a, cudaStream_t stream);
 int chunk_tc_rows();
 int chunk_tc_kv_tile();
 int chunk_tc_kv_box();
-cudaError_t launch_chunk_tc(const PartialParams& p, int32_t d, bool fp8, const CUtensorMap& tmq,
-                            const CUtensorMap& tmk, const CUtensorMap& tmv, int64_t n_items, cudaStream_t stream);
+cudaError_t launch_chunk_tc(const PartialParams& p, int32_t d, PageFormat pages, const ChunkMaps& maps, int64_t n_items,
+                            cudaStream_t stream);
 cudaError_t launch_chunk_merge(const ChunkArgs& a, int32_t d, const float* part_o, const float* part_lse,
                                int64_t max_rows, cudaStream_t stream);
+// The groups of a shared prefix, ahead of its two passes (see shared_prefix.cu).
+struct SharedArgs {
+  const int32_t* cu_q;         // [B + 1]
+  const int32_t* seq_lens;     // [B]
+  const int32_t* cu_groups;    // [n_groups + 1]
+  const int32_t* prefix_lens;  // [n_groups]
+  int32_t B, T, n_groups, cap;
+  int32_t* group_rows_at;  // [n_groups + 1]
+  int32_t* group_len;      // [n_groups]
+  int32_t* table_row;      // [n_groups]
+  int32_t* skip;           // [B]
+};
+cudaError_t launch_shared_groups(const SharedArgs& a, cudaStream_t stream);
 
 // Norm, rotation and append of new tokens (see qk_norm_rope.cu).  Strides in elements.
 struct AppendArgs {
@@ -200,6 +236,10 @@ struct AppendArgs {
   const float* k_scale;  // fp8: [num_blocks][Hkv][block_len / scale_block]
   const float* v_scale;
   int64_t num_blocks;
+  uint8_t* k_block;  // fp4: e4m3 [num_blocks][Hkv][block_len][d / kFp4Block]
+  uint8_t* v_block;
+  const float* k_head;  // fp4: [Hkv], or NULL: 1
+  const float* v_head;
   int32_t B, T, Hq, Hkv, rot, interleaved, weight_bf16;
   int32_t block_len, max_blocks, scale_block;
   int32_t steps;  // stages of 32 heads of a CTA's run, and whether a token's q, k and v heads lie in
@@ -208,7 +248,29 @@ struct AppendArgs {
   float eps;
   unsigned int* err;
 };
-cudaError_t launch_append(const AppendArgs& a, int32_t d, bool fp8, int sms, cudaStream_t stream);
+cudaError_t launch_append(const AppendArgs& a, int32_t d, PageFormat pages, int sms, cudaStream_t stream);
+
+// Tokens of a paged cache as packed bf16 rows (see kv_read.cu).  Strides in elements.
+struct ReadArgs {
+  const void* k_pages;
+  const void* v_pages;
+  int64_t kp_sb, kp_sh, kp_st, vp_sb, vp_sh, vp_st;  // page, head, token (fp4: bytes)
+  const float* k_scale;  // fp8: [num_blocks][Hkv][block_len / scale_block]
+  const float* v_scale;
+  const uint8_t* k_block;  // fp4: e4m3 [num_blocks][Hkv][block_len][d / kFp4Block]
+  const uint8_t* v_block;
+  const float* k_head;  // fp4: [Hkv], or NULL: 1
+  const float* v_head;
+  const int32_t* cu;           // [B + 1]
+  const int32_t* starts;       // [B], or NULL: 0
+  const int32_t* block_table;  // [B][max_blocks]
+  __nv_bfloat16* k_out;
+  __nv_bfloat16* v_out;
+  int64_t ko_st, ko_sh, vo_st, vo_sh;
+  int64_t num_blocks;
+  int32_t B, T, Hkv, block_len, max_blocks, scale_block;
+};
+cudaError_t launch_kv_read(const ReadArgs& a, int32_t d, PageFormat pages, int sms, cudaStream_t stream);
 
 // MLA latent variant (dk = 576 latent+rope, dv = 512, one shared latent "head").
 // Tiles are 32 tokens; the tensor map's box is 64 elements x 32 tokens.
