@@ -1375,6 +1375,7 @@ skv_status attn_shared_prefix_paged(const skv_chunk_desc* desc, const skv_paged*
   if (st != SKV_OK) return st;
   cudaError_t e = launch_shared_groups(g, s);
   if (e != cudaSuccess) return cuda_fail(e, "shared prefix launch");
+  p.ck.shared = 1;
   PartialParams first = p;  // the prefixes: groups in the place of sequences
   first.ck.B = g.n_groups;
   first.ck.seq_lens = g.group_len;

@@ -73,12 +73,12 @@ __device__ __forceinline__ Joined join(const float* part_o, const float* part_ls
 }
 
 // (behind: the row's sequence has a prefix that another pass attended)
-template <int D>
+template <int D, bool SHARED>
 __device__ __forceinline__ void store_row(const ChunkArgs& a, int64_t row, const Joined& j, int lane, bool behind) {
   float inv = j.den != 0.f ? 1.f / j.den : 0.f;
   float lse = j.den != 0.f ? j.m + logf(j.den) : -INFINITY;
   float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (behind) {
+  if (SHARED && behind) {
     const ChunkJoin both = chunk_join(lse, __ldcg(a.prior_lse + row));
     inv *= both.own;
     lse = both.lse;
@@ -89,7 +89,7 @@ __device__ __forceinline__ void store_row(const ChunkArgs& a, int64_t row, const
   }
   if (4 * lane < D) {
     y = make_float4(fmaf(j.acc.x, inv, y.x), fmaf(j.acc.y, inv, y.y), fmaf(j.acc.z, inv, y.z), fmaf(j.acc.w, inv, y.w));
-    if (a.out_f32) {
+    if (SHARED && a.out_f32) {
       *reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * D + 4 * lane) = y;
     } else {
       __nv_bfloat162 lo = __floats2bfloat162_rn(y.x, y.y);
@@ -109,7 +109,7 @@ struct BlockJoin {
   float m[kRowsPerBlock], den[kRowsPerBlock];
   float4 acc[kRowsPerBlock][D / 4];
 };
-template <int D, class At>
+template <int D, bool SHARED, class At>
 __device__ __forceinline__ void join_by_block(const ChunkArgs& a, BlockJoin<D>& sm, const float* part_o,
                                               const float* part_lse, At&& at, int k, int64_t row, bool behind) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -137,11 +137,11 @@ __device__ __forceinline__ void join_by_block(const ChunkArgs& a, BlockJoin<D>& 
         s.acc.w += f * x.w;
       }
     }
-    store_row<D>(a, row, s, lane, behind);
+    store_row<D, SHARED>(a, row, s, lane, behind);
   }
 }
 
-template <int D>
+template <int D, bool SHARED>
 __global__ void __launch_bounds__(32 * kRowsPerBlock)
     chunk_merge_kernel(const __grid_constant__ ChunkArgs a, const float* part_o, const float* part_lse) {
   __shared__ int sm_parts[kRowsPerBlock], sm_n[kRowsPerBlock], sm_skip[kRowsPerBlock];
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(32 * kRowsPerBlock)
         // sequences without rows to merge share the first row of the one after them
         const int in = r - __ldcg(plan + kPlanRow * lo + 1);
         int row0, m;
-        chunk_lengths(a, lo, &row0, &n, &m, &skip);
+        chunk_lengths<SHARED>(a, lo, &row0, &n, &m, &skip);
         k = __ldcg(plan + kPlanRow * lo + 4);
         row = static_cast<int64_t>(row0) * Hq + in;
         part = static_cast<int64_t>(__ldcg(plan + kPlanRow * lo + 2)) + in;
@@ -189,10 +189,10 @@ __global__ void __launch_bounds__(32 * kRowsPerBlock)
     };
     if (most <= kWarpParts) {
       if (r < rows)
-        store_row<D>(a, sm_row[warp], join<D>(part_o, part_lse, at(warp), 0, 1, sm_parts[warp], lane), lane, sm_skip[warp] > 0);
+        store_row<D, SHARED>(a, sm_row[warp], join<D>(part_o, part_lse, at(warp), 0, 1, sm_parts[warp], lane), lane, sm_skip[warp] > 0);
     } else {
       for (int w = 0; w < kRowsPerBlock && r0 + w < rows; ++w)
-        join_by_block<D>(a, sm_join, part_o, part_lse, at(w), sm_parts[w], sm_row[w], sm_skip[w] > 0);
+        join_by_block<D, SHARED>(a, sm_join, part_o, part_lse, at(w), sm_parts[w], sm_row[w], sm_skip[w] > 0);
     }
   }
 }
@@ -200,16 +200,16 @@ __global__ void __launch_bounds__(32 * kRowsPerBlock)
 // The merge after the kernel for few rows: block c looks at the border between the runs of CTAs
 // c - 1 and c.  If it lies inside an item, that item's partials are those of the CTAs whose
 // runs reach into it, and the blocks of all its borders share its rows.
-template <int D>
+template <int D, bool SHARED>
 __global__ void __launch_bounds__(32 * kRowsPerBlock)
     chunk_runs_merge_kernel(const __grid_constant__ ChunkArgs a, const float* part_o, const float* part_lse) {
   __shared__ BlockJoin<D> sm_join;
   const int c = blockIdx.x + 1;
-  ChunkRuns runs;
+  ChunkRuns<SHARED> runs;
   ChunkShare sh;
   // (reads lengths only, which were there before the attention kernel; its CTAs start as those of that
   // kernel leave)
-  const bool any = chunk_find_runs<32 * kRowsPerBlock>(a, a.n_wave, c, &runs, &sh);
+  const bool any = chunk_find_runs<32 * kRowsPerBlock, SHARED>(a, a.n_wave, c, &runs, &sh);
   const int tile = any ? runs.s : 0;
   // the attention kernel before it on the stream is complete and its writes are visible (also where
   // there is nothing to do: what comes after this grid may rely on both)
@@ -232,10 +232,10 @@ __global__ void __launch_bounds__(32 * kRowsPerBlock)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (k <= kWarpParts) {
     for (int r = mine * kRowsPerBlock + warp; r < rows; r += borders * kRowsPerBlock)
-      store_row<D>(a, out_row(r), join<D>(part_o, part_lse, at(r), 0, 1, k, lane), lane, runs.skip > 0);
+      store_row<D, SHARED>(a, out_row(r), join<D>(part_o, part_lse, at(r), 0, 1, k, lane), lane, runs.skip > 0);
   } else {
     for (int r = mine; r < rows; r += borders)
-      join_by_block<D>(a, sm_join, part_o, part_lse, at(r), k, out_row(r), runs.skip > 0);
+      join_by_block<D, SHARED>(a, sm_join, part_o, part_lse, at(r), k, out_row(r), runs.skip > 0);
   }
 }
 
@@ -243,11 +243,12 @@ constexpr int kPlanThreads = 512;
 
 // The plan of a call, for the persistent attention kernel and the merge after it.  One block:
 // two loads and two scans a sequence, a few microseconds, under which the next grid starts.
+template <bool SHARED>
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_constant__ ChunkArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ int64_t sm_scan[2 * (kPlanThreads / 32)];
   int64_t items, merged;
-  chunk_make_plan<kPlanThreads>(a, sm_scan, &items, &merged,
+  chunk_make_plan<kPlanThreads, SHARED>(a, sm_scan, &items, &merged,
                                 [&](int b, int first, int rt, int k, int part_row, int merge_row) {
                                   chunk_write_plan(a, b, first, rt, k, part_row, merge_row);
                                 });
@@ -261,7 +262,10 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
 }  // namespace
 
 cudaError_t launch_chunk_plan(const ChunkArgs& a, cudaStream_t stream) {
-  chunk_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
+  if (a.shared)
+    chunk_plan_kernel<true><<<1, kPlanThreads, 0, stream>>>(a);
+  else
+    chunk_plan_kernel<false><<<1, kPlanThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -277,8 +281,9 @@ cudaError_t launch_chunk_runs_merge(const ChunkArgs& a, int32_t d, const float* 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (d == 64) return cudaLaunchKernelEx(&cfg, chunk_runs_merge_kernel<64>, a, part_o, part_lse);
-  return cudaLaunchKernelEx(&cfg, chunk_runs_merge_kernel<128>, a, part_o, part_lse);
+  const auto kernel = d == 64 ? (a.shared ? chunk_runs_merge_kernel<64, true> : chunk_runs_merge_kernel<64, false>)
+                              : (a.shared ? chunk_runs_merge_kernel<128, true> : chunk_runs_merge_kernel<128, false>);
+  return cudaLaunchKernelEx(&cfg, kernel, a, part_o, part_lse);
 }
 
 cudaError_t launch_chunk_merge(const ChunkArgs& a, int32_t d, const float* part_o, const float* part_lse,
@@ -296,8 +301,9 @@ cudaError_t launch_chunk_merge(const ChunkArgs& a, int32_t d, const float* part_
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (d == 64) return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<64>, a, part_o, part_lse);
-  return cudaLaunchKernelEx(&cfg, chunk_merge_kernel<128>, a, part_o, part_lse);
+  const auto kernel = d == 64 ? (a.shared ? chunk_merge_kernel<64, true> : chunk_merge_kernel<64, false>)
+                              : (a.shared ? chunk_merge_kernel<128, true> : chunk_merge_kernel<128, false>);
+  return cudaLaunchKernelEx(&cfg, kernel, a, part_o, part_lse);
 }
 
 }  // namespace skv

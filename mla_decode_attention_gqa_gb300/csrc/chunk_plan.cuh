@@ -37,11 +37,14 @@ struct ChunkItem {
   int part_row;  // first partial row of the sequence (n_chunk > 1)
 };
 
-// (The arrays of a shared prefix are written by the kernel before, so they are not read through the
-// read-only path.)
+// SHARED: a pass of a shared prefix, with the arrays that ChunkArgs lists for it.  A template argument
+// throughout, so that the other calls carry nothing of it (as tests of the arguments it took a call
+// of one token 1.5 us of 17, a windowed prompt 4 of 275).
+// (Those arrays are written by a kernel before, so they are not read through the read-only path.)
+template <bool SHARED>
 __device__ __forceinline__ void chunk_lengths(const ChunkArgs& a, int b, int* row0, int* n, int* m, int* skip) {
   int lo, hi, len;
-  if (a.group_rows_at) {
+  if (SHARED && a.group_rows_at) {
     lo = __ldcg(a.group_rows_at + b), hi = __ldcg(a.group_rows_at + b + 1);
     len = __ldcg(a.seq_lens + b);
   } else {
@@ -50,14 +53,24 @@ __device__ __forceinline__ void chunk_lengths(const ChunkArgs& a, int b, int* ro
   }
   lo = min(max(lo, 0), a.T), hi = min(max(hi, 0), a.T);
   *row0 = lo;
+  *n = max(hi - lo, 0);
   *m = max(len, 0);
-  *n = a.whole && *m == 0 ? 0 : max(hi - lo, 0);  // (nothing to do for a group without a prefix)
-  *skip = a.skip ? __ldcg(a.skip + b) : 0;
+  *skip = 0;
+  if constexpr (SHARED) {
+    if (a.whole && *m == 0) *n = 0;  // (nothing to do for a group without a prefix)
+    if (a.skip) *skip = __ldcg(a.skip + b);
+  }
 }
 
 // Position of the first of n new tokens, and from each to the next.
-__device__ __forceinline__ int chunk_pos0(const ChunkArgs& a, int n, int m) { return a.whole ? m - 1 : m - n; }
-__device__ __forceinline__ int chunk_pos_step(const ChunkArgs& a) { return a.whole ? 0 : 1; }
+template <bool SHARED>
+__device__ __forceinline__ int chunk_pos0(const ChunkArgs& a, int n, int m) {
+  return SHARED && a.whole ? m - 1 : m - n;
+}
+template <bool SHARED>
+__device__ __forceinline__ int chunk_pos_step(const ChunkArgs& a) {
+  return SHARED && a.whole ? 0 : 1;
+}
 
 // A row's result over its own tokens (out, lse) joined with the one over its prefix: the weights of the
 // two, and the lse of both.  A part that saw nothing weighs nothing; a NaN on either side stays.
@@ -80,8 +93,9 @@ __device__ __forceinline__ ChunkJoin chunk_join(float lse, float prior_lse) {
 }
 
 // Page of token `tok` of sequence (or group) b.
+template <bool SHARED>
 __device__ __forceinline__ int chunk_page_of(const PartialParams& p, int b, int tok) {
-  return kv_page_of(p, p.ck.table_row ? __ldcg(p.ck.table_row + b) : b, tok);
+  return kv_page_of(p, SHARED && p.ck.table_row ? __ldcg(p.ck.table_row + b) : b, tok);
 }
 
 // Blocks of kTileN tokens seen by the rows at positions [p0, p1] of a sequence with `cap` tokens
@@ -110,10 +124,11 @@ __device__ __forceinline__ ChunkTiles chunk_tiles(int window, int n_sink, int ca
 
 // Row tiles per KV head, and KV tiles of the row tile that has most: the last one; with a window, an
 // earlier one may touch a block more than the last, so there the bound is of their length alone.
+template <bool SHARED>
 __device__ __forceinline__ void chunk_extent(const ChunkArgs& a, int n, int m, int skip, int* row_tiles, int* kv_tiles) {
   *row_tiles = static_cast<int>((static_cast<int64_t>(n) * a.group_rows + a.rows - 1) / a.rows);
   const int span = min(n, (a.rows + a.group_rows - 1) / a.group_rows + 1);
-  const ChunkTiles t = chunk_tiles(a.window, a.n_sink, a.cap, skip, a.whole ? m - 1 : m - span, m - 1);
+  const ChunkTiles t = chunk_tiles(a.window, a.n_sink, a.cap, skip, SHARED && a.whole ? m - 1 : m - span, m - 1);
   int blocks = t.n;
   if (a.window > 0 && *row_tiles > 1) {
     const int64_t seen = static_cast<int64_t>(a.window) - 1 + span;  // tokens of a row tile's window
@@ -175,15 +190,15 @@ __device__ __forceinline__ void chunk_block_scan(int64_t& x, int64_t& y, int64_t
 // The plan of one call, computed by all NT threads of a block: `visit(b, first item, row tiles,
 // chunks, first partial row, first row to merge)` for every sequence, totals in *items and
 // *merged.  A visitor must not synchronise.
-template <int NT, class F>
+template <int NT, bool SHARED, class F>
 __device__ __forceinline__ void chunk_make_plan(const ChunkArgs& a, int64_t* sm_scan, int64_t* items, int64_t* merged,
                                                 F&& visit) {
   const int tid = threadIdx.x;
   int64_t w = 0, zero = 0, total, unused;
   for (int b = tid; b < a.B; b += NT) {
     int row0, n, m, skip, rt, kt;
-    chunk_lengths(a, b, &row0, &n, &m, &skip);
-    chunk_extent(a, n, m, skip, &rt, &kt);
+    chunk_lengths<SHARED>(a, b, &row0, &n, &m, &skip);
+    chunk_extent<SHARED>(a, n, m, skip, &rt, &kt);
     w += static_cast<int64_t>(rt) * a.Hkv * kt;
   }
   chunk_block_scan<NT>(w, zero, &total, &unused, sm_scan);
@@ -195,8 +210,8 @@ __device__ __forceinline__ void chunk_make_plan(const ChunkArgs& a, int64_t* sm_
     const int b = b0 + tid;
     int row0 = 0, n = 0, m = 0, skip = 0, rt = 0, kt = 1, k = 1;
     if (b < a.B) {
-      chunk_lengths(a, b, &row0, &n, &m, &skip);
-      chunk_extent(a, n, m, skip, &rt, &kt);
+      chunk_lengths<SHARED>(a, b, &row0, &n, &m, &skip);
+      chunk_extent<SHARED>(a, n, m, skip, &rt, &kt);
       k = max(1, kt / L);
     }
     const int64_t mine = static_cast<int64_t>(rt) * a.Hkv * k;
@@ -218,10 +233,11 @@ __device__ __forceinline__ void chunk_make_plan(const ChunkArgs& a, int64_t* sm_
 
 // Item number r of sequence b: later row tiles (which see more) first; a row tile's chunks and
 // heads side by side.
+template <bool SHARED>
 __device__ __forceinline__ ChunkItem chunk_item_of(const ChunkArgs& a, int b, int r, int rt, int k, int part_row) {
   ChunkItem it;
   it.b = b;
-  chunk_lengths(a, b, &it.row0, &it.n, &it.m, &it.skip);
+  chunk_lengths<SHARED>(a, b, &it.row0, &it.n, &it.m, &it.skip);
   it.n_chunk = k;
   it.part_row = part_row;
   it.c = r % k;
@@ -234,6 +250,7 @@ __device__ __forceinline__ ChunkItem chunk_item_of(const ChunkArgs& a, int b, in
 // Work item `idx` from the written plan (idx < its number of items).  Warp-collective: a
 // 32-way search for the last sequence whose first item is <= idx (sequences without items
 // share the first item of the one after them).
+template <bool SHARED>
 __device__ __forceinline__ ChunkItem chunk_item_at(const ChunkArgs& a, int idx) {
   const int lane = threadIdx.x & 31;
   int lo = 0, n = a.B;  // the answer lies in [lo, lo + n)
@@ -247,7 +264,7 @@ __device__ __forceinline__ ChunkItem chunk_item_at(const ChunkArgs& a, int idx) 
     n = min(step, n - skip);
   }
   const int32_t* e = a.plan + kPlanHead + static_cast<int64_t>(kPlanRow) * lo;
-  return chunk_item_of(a, lo, idx - __ldcg(e), __ldcg(e + 3), __ldcg(e + 4), __ldcg(e + 2));
+  return chunk_item_of<SHARED>(a, lo, idx - __ldcg(e), __ldcg(e + 3), __ldcg(e + 4), __ldcg(e + 2));
 }
 
 // ---- equal runs (the kernel for few rows): all items' KV tiles in one line -- sequence after
@@ -282,14 +299,15 @@ struct ChunkPiece {
 
 // A CTA's run, piece by piece.  (The divisions are done once, by find: a piece begins where the one
 // before ends.)
+template <bool SHARED>
 struct ChunkRuns {
   int64_t left;  // tiles left
   int cta, b, row0, n, m, skip, rt, kt;  // kt: with the start
   int g, mt, s;  // the next piece's item, and its first tile there
   bool head;
   __device__ __forceinline__ void load(const ChunkArgs& a) {
-    chunk_lengths(a, b, &row0, &n, &m, &skip);
-    chunk_extent(a, n, m, skip, &rt, &kt);
+    chunk_lengths<SHARED>(a, b, &row0, &n, &m, &skip);
+    chunk_extent<SHARED>(a, n, m, skip, &rt, &kt);
     kt += a.start;
   }
   // Tiles [at, at + count) of those from sequence `seq` on (which holds the first of them).
@@ -317,7 +335,7 @@ struct ChunkRuns {
     pc->mt = mt;
     pc->g = g;
     const int m0 = mt * a.rows, m_last = min(m0 + a.rows, n * a.group_rows) - 1;
-    const int pos0 = chunk_pos0(a, n, m), step = chunk_pos_step(a);
+    const int pos0 = chunk_pos0<SHARED>(a, n, m), step = chunk_pos_step<SHARED>(a);
     pc->tl = chunk_tiles(a.window, a.n_sink, a.cap, skip, pos0 + m0 / a.group_rows * step, pos0 + m_last / a.group_rows * step);
     pc->i0 = min(max(s - a.start, 0), pc->tl.n);
     pc->n_tiles = min(max(e - a.start, 0), pc->tl.n) - pc->i0;  // (an earlier row tile may see fewer than kt)
@@ -331,8 +349,8 @@ struct ChunkRuns {
 };
 
 // Run `cta` of at most n_cta; false if there is none.  Every thread of the block calls it.
-template <int NT>
-__device__ __forceinline__ bool chunk_find_runs(const ChunkArgs& a, int n_cta, int cta, ChunkRuns* runs,
+template <int NT, bool SHARED>
+__device__ __forceinline__ bool chunk_find_runs(const ChunkArgs& a, int n_cta, int cta, ChunkRuns<SHARED>* runs,
                                                 ChunkShare* share = nullptr) {
   __shared__ int64_t sm_scan[2 * (NT / 32)];
   __shared__ int64_t sm_first;
@@ -341,8 +359,8 @@ __device__ __forceinline__ bool chunk_find_runs(const ChunkArgs& a, int n_cta, i
   int64_t w = 0, zero = 0, total, unused;
   for (int b = tid; b < a.B; b += NT) {
     int row0, n, m, skip, rt, kt;
-    chunk_lengths(a, b, &row0, &n, &m, &skip);
-    chunk_extent(a, n, m, skip, &rt, &kt);
+    chunk_lengths<SHARED>(a, b, &row0, &n, &m, &skip);
+    chunk_extent<SHARED>(a, n, m, skip, &rt, &kt);
     w += static_cast<int64_t>(rt) * a.Hkv * (kt + a.start);
   }
   chunk_block_scan<NT>(w, zero, &total, &unused, sm_scan);
@@ -358,8 +376,8 @@ __device__ __forceinline__ bool chunk_find_runs(const ChunkArgs& a, int n_cta, i
     const int b = b0 + tid;
     int row0, n, m, skip, rt = 0, kt = 1;
     if (b < a.B) {
-      chunk_lengths(a, b, &row0, &n, &m, &skip);
-      chunk_extent(a, n, m, skip, &rt, &kt);
+      chunk_lengths<SHARED>(a, b, &row0, &n, &m, &skip);
+      chunk_extent<SHARED>(a, n, m, skip, &rt, &kt);
     }
     const int64_t mine = static_cast<int64_t>(rt) * a.Hkv * (kt + a.start);
     int64_t x = mine, y = 0, tx, ty;

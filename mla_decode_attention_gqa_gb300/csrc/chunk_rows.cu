@@ -34,11 +34,13 @@ namespace {
 
 constexpr int kRows = 16;  // rows of a warp
 
-template <PageFormat PAGES_, int D_, int WM_, int WN_, int NSTAGE_>
+template <PageFormat PAGES_, int D_, int WM_, int WN_, int NSTAGE_, bool SHARED_>
 struct RowsCfg {
   static constexpr PageFormat PAGES = PAGES_;
+  static constexpr bool SHARED = SHARED_;  // a pass of a shared prefix (ChunkArgs)
   static constexpr bool FP4 = PAGES == kPagesFp4;
-  static constexpr bool FP8 = PAGES != kPagesBf16;  // codes: the products run in fp16
+  static constexpr bool FP8 = PAGES == kPagesFp8;
+  static constexpr bool CODES = PAGES != kPagesBf16;  // the products run in fp16, P V as V^T P^T
   static constexpr int D = D_;
   static constexpr int WM = WM_;          // sets of 16 rows, which share the tiles
   static constexpr int WN = WN_;          // consumer warps of a set
@@ -46,7 +48,7 @@ struct RowsCfg {
   static constexpr int CTAS = WM == 1 ? 2 : 1;  // an SM
   static constexpr int NSTAGE = NSTAGE_;  // tiles in the ring
   static constexpr int TN = kTileN;
-  static constexpr int ESZ = FP8 ? 1 : 2;
+  static constexpr int ESZ = CODES ? 1 : 2;
   static constexpr int NBOX = FP4 ? 1 : D * ESZ / 128;  // 128-byte boxes of a token row (4-bit: one of 64)
   static constexpr int BOX_ELEMS = 128 / ESZ;
   static constexpr int BOX_BYTES = FP4 ? TN * (D / 2) : TN * 128;
@@ -60,10 +62,10 @@ struct RowsCfg {
   static constexpr int NFULL = WN * DW;
   static constexpr int OFF_O = NSTAGE * STAGE;                 // one warp's O of each set, to be joined
   static constexpr int OFF_ML = OFF_O + ROWS * D * 4;          // (m, l) of each warp's rows
-  static constexpr int OFF_QF = OFF_ML + WN * ROWS * 2 * 4;    // fp8: q fragments
-  static constexpr int OFF_BAR = OFF_QF + (FP8 ? WM * (D / 16) * 32 * 16 : 0);
-  static constexpr int OFF_QS = OFF_BAR + 256;                 // fp8: the score scale of each row
-  static constexpr int OFF_RUN = OFF_QS + (FP8 ? ROWS * 4 : 0);  // each consumer warp's run and piece
+  static constexpr int OFF_QF = OFF_ML + WN * ROWS * 2 * 4;    // codes: q fragments
+  static constexpr int OFF_BAR = OFF_QF + (CODES ? WM * (D / 16) * 32 * 16 : 0);
+  static constexpr int OFF_QS = OFF_BAR + 256;                 // codes: the score scale of each row
+  static constexpr int OFF_RUN = OFF_QS + (CODES ? ROWS * 4 : 0);  // each consumer warp's run and piece
   static constexpr int SMEM = 1024 + OFF_RUN + WM * WN * 192;
   static_assert((NFULL + NSTAGE) * 8 <= 256, "barriers");
   static_assert(CTAS * (SMEM + 1536) <= 227 * 1024, "CTAs an SM");
@@ -117,8 +119,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     for (int s = 0; s < NSTAGE; ++s) mbar_init(&empty[s], C::WM);
     fence_mbar_init();
   }
-  ChunkRuns runs;  // (synchronises the block)
-  if (!chunk_find_runs<C::THREADS>(p.ck, gridDim.x, blockIdx.x, &runs)) return;
+  using Runs = ChunkRuns<C::SHARED>;
+  Runs runs;  // (synchronises the block)
+  if (!chunk_find_runs<C::THREADS, C::SHARED>(p.ck, gridDim.x, blockIdx.x, &runs)) return;
 
   if (warp == C::WM * WN) {
     // ------------------------------------------------------------ producer warp
@@ -137,7 +140,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         int pages = 0, rows = 0;
         if (i0 + lane < pc.n_tiles) {
           const int t = pc.token(i0 + lane);
-          pages = chunk_page_of(p, pc.b, t);
+          pages = chunk_page_of<C::SHARED>(p, pc.b, t);
           rows = t % p.block_len;
         }
         const int n = min(32, pc.n_tiles - i0);
@@ -180,8 +183,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   uint4* qfrag = reinterpret_cast<uint4*>(smem + C::OFF_QF) + wm * (D / 16) * 32;
   float* q_scale = reinterpret_cast<float*>(smem + C::OFF_QS) + wm * kRows;
   // the run and its piece wait in shared memory: the registers are full of scores and O
-  static_assert(sizeof(ChunkRuns) <= 64 && sizeof(ChunkPiece) <= 128, "a warp's place");
-  ChunkRuns* run = reinterpret_cast<ChunkRuns*>(smem + C::OFF_RUN + warp * 192);
+  static_assert(sizeof(Runs) <= 64 && sizeof(ChunkPiece) <= 128, "a warp's place");
+  Runs* run = reinterpret_cast<Runs*>(smem + C::OFF_RUN + warp * 192);
   ChunkPiece& pc = *reinterpret_cast<ChunkPiece*>(smem + C::OFF_RUN + warp * 192 + 64);
   if (lane == 0) *run = runs;
   auto next_piece = [&]() -> bool {
@@ -204,7 +207,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     const int tq0 = v0 ? mrow0 / p.G : 0, tq1 = v1 ? mrow1 / p.G : 0;
     const int h0 = pc.g * p.G + (v0 ? mrow0 % p.G : 0), h1 = pc.g * p.G + (v1 ? mrow1 % p.G : 0);
     // visible tokens of a row: [wl, hz] and below the sinks' end; all below the item's end
-    const int pos0 = chunk_pos0(p.ck, pc.n, pc.m), pos_step = chunk_pos_step(p.ck);
+    const int pos0 = chunk_pos0<C::SHARED>(p.ck, pc.n, pc.m), pos_step = chunk_pos_step<C::SHARED>(p.ck);
     const int hz0 = pos0 + tq0 * pos_step, hz1 = pos0 + tq1 * pos_step, hz_min = pos0 + mset / p.G * pos_step;
     auto window_lo = [&](int pos) -> int { return p.ck.window > 0 && pos >= p.ck.window ? pos - p.ck.window + 1 : 0; };
     const int wl0 = window_lo(hz0), wl1 = window_lo(hz1);
@@ -212,12 +215,12 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     const bool idle = C::WM > 1 && mset >= rows_total;  // a set without rows only passes the tiles on
 
     // ---- Q fragments (A operand, 16 rows x D): registers for bf16, shared memory for fp8
-    uint32_t qa[C::FP8 ? 1 : D / 16][4];
+    uint32_t qa[C::CODES ? 1 : D / 16][4];
     {
       const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + pc.row0 * p.q_st;
       const __nv_bfloat16* q0 = q + tq0 * p.q_st + h0 * p.q_sh;
       const __nv_bfloat16* q1 = q + tq1 * p.q_st + h1 * p.q_sh;
-      if constexpr (!C::FP8) {
+      if constexpr (!C::CODES) {
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const int d0 = 16 * ks + 2 * tq;
@@ -282,6 +285,10 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     // power of two, up, by which its weights and its O are multiplied: the largest weight of a tile lies
     // between 2^4 and 2^15 then, and what is above 2^-28 of it (2^-18 where it lies lowest) keeps its
     // bits, however far apart the scales and the scores of the row's tiles are
+    // (4-bit pages: the scales are in V's own values, so the weights need no more than a power that puts
+    // the largest possible one, that of the running maximum, at 2^kUp4: a weight keeps all bits down to 2^-28 of
+    // it and counts down to 2^-38, so that even 2^20 tokens below that miss 2^-18)
+    constexpr float kUp4 = 14.f;
     constexpr int kMostUp = 124;  // (2^-kMostUp is a normal number)
     float up[2];
     up[0] = up[1] = __uint_as_float(static_cast<uint32_t>(127 + kMostUp) << 23);
@@ -291,9 +298,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       const int x = x0 + i, s = x % NSTAGE;
       const int t0 = pc.token(i);
       float ksc = 1.f, vsc = 1.f;
-      if constexpr (C::PAGES == kPagesFp8) {
+      if constexpr (C::FP8) {
         // a page outside the cache reads as zeros through TMA; its scale is never fetched
-        const int page = chunk_page_of(p, pc.b, t0);
+        const int page = chunk_page_of<C::SHARED>(p, pc.b, t0);
         ksc = vsc = 0.f;
         if (page >= 0 && page < p.num_blocks) {
           const int per = p.block_len / p.scale_block;
@@ -316,7 +323,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       float sc[TN / 8][4];
 #pragma unroll
       for (int i2 = 0; i2 < TN / 8; ++i2) sc[i2][0] = sc[i2][1] = sc[i2][2] = sc[i2][3] = 0.f;
-      if constexpr (!C::FP8) {
+      if constexpr (!C::CODES) {
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
 #pragma unroll
@@ -330,28 +337,36 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           }
         }
       } else if constexpr (C::FP4) {
-        // 8 tokens at a time: a lane has token gq, of each chunk of 32 dims 8 tq .. 8 tq + 7, which
-        // lie in one block.  Code times block scale is exact in fp16 (6 bits, 2^-10 to 2688)
-        const uint8_t* ksb = smem + s * C::STAGE + 2 * C::TILE;
+        // Of 8 tokens a lane has token gq, of each chunk of 32 dims 8 tq .. 8 tq + 7, which lie in one
+        // block.  Code times block scale is exact in fp16 (6 bits, 2^-10 to 2688).  Two chunks at a
+        // time: their queries stay in registers over the tile's tokens
+        const uint8_t* ksb = smem + s * C::STAGE + 2 * C::TILE + gq * (D / kFp4Block);
 #pragma unroll
-        for (int nt = 0; nt < TN / 8; ++nt) {
-          uint32_t w[4];
-          ldsm_x4(kbase + tile4_off(8 * nt + (lane & 7), mi * 16), w[0], w[1], w[2], w[3]);
-          const uint2 sb = *reinterpret_cast<const uint2*>(ksb + (8 * nt + gq) * (D / kFp4Block));
-          // the scales of blocks (tq >> 1) + 2 c
-          uint32_t s01, s23;
-          e4m3x4_to_f16x2x2(prmt(sb.x, sb.y, (tq >> 1) ? 0x7531u : 0x6420u), s01, s23);
+        for (int c2 = 0; c2 < D / 64; ++c2) {
+          uint4 qv[4];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t by = prmt(c < 2 ? s01 : s23, 0u, (c & 1) ? 0x3232u : 0x1010u);
-            uint32_t k0, k1, k2, k3;
-            e2m1x8_to_f16x2x4(w[c], k0, k1, k2, k3);
-            const uint4 qv0 = qfrag[2 * c * 32 + lane];
-            const uint4 qv1 = qfrag[(2 * c + 1) * 32 + lane];
-            const uint32_t qa0[4] = {qv0.x, qv0.y, qv0.z, qv0.w};
-            const uint32_t qa1[4] = {qv1.x, qv1.y, qv1.z, qv1.w};
-            mma_f16(sc[nt], qa0, mul_f16x2(k0, by), mul_f16x2(k1, by));
-            mma_f16(sc[nt], qa1, mul_f16x2(k2, by), mul_f16x2(k3, by));
+          for (int i = 0; i < 4; ++i) qv[i] = qfrag[(4 * c2 + i) * 32 + lane];
+#pragma unroll
+          for (int np = 0; np < TN / 16; ++np) {
+            uint32_t w[2][2];  // [8 tokens][chunk]
+            ldsm_x4(kbase + tile4_off(16 * np + (mi >> 1) * 8 + (lane & 7), (2 * c2 + (mi & 1)) * 16), w[0][0], w[0][1], w[1][0],
+                    w[1][1]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t sb = *reinterpret_cast<const uint32_t*>(ksb + (16 * np + 8 * h) * (D / kFp4Block) + 4 * c2);
+              uint32_t by, unused;  // the scales of the two chunks' blocks
+              e4m3x4_to_f16x2x2(prmt(sb, 0u, (tq >> 1) ? 0x4431u : 0x4420u), by, unused);
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const uint32_t b = prmt(by, 0u, c ? 0x3232u : 0x1010u);
+                uint32_t k0, k1, k2, k3;
+                e2m1x8_to_f16x2x4(w[h][c], k0, k1, k2, k3);
+                const uint32_t qa0[4] = {qv[2 * c].x, qv[2 * c].y, qv[2 * c].z, qv[2 * c].w};
+                const uint32_t qa1[4] = {qv[2 * c + 1].x, qv[2 * c + 1].y, qv[2 * c + 1].z, qv[2 * c + 1].w};
+                mma_f16(sc[2 * np + h], qa0, mul_f16x2(k0, b), mul_f16x2(k1, b));
+                mma_f16(sc[2 * np + h], qa1, mul_f16x2(k2, b), mul_f16x2(k3, b));
+              }
+            }
           }
         }
       } else {
@@ -382,7 +397,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 
       // ---- scale, mask, online softmax
       float sl[2] = {p.scale_log2, p.scale_log2};
-      if constexpr (C::FP8) {
+      if constexpr (C::CODES) {
         if constexpr (C::FP4) ksc = k_head;
         sl[0] = reinterpret_cast<volatile const float*>(q_scale)[gq] * ksc;
         sl[1] = reinterpret_cast<volatile const float*>(q_scale)[gq + 8] * ksc;
@@ -415,6 +430,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         scale_mask(std::true_type{});
       else
         scale_mask(std::false_type{});
+      // (base: what scores are taken against)
       float base[2], alpha[2], fall[2], vs[2] = {1.f, 1.f};
       bool other = false;  // fp8: a row's largest weight leaves its range
 #pragma unroll
@@ -427,6 +443,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         alpha[r] = fast_exp2(fall[r]);  // 0 when mrun = -inf
         mrun[r] = mnew;
         lrun[r] *= alpha[r];
+        if constexpr (C::FP4) base[r] -= kUp4;
         if constexpr (C::FP8) {
           vs[r] = vsc * up[r];
           const float most = fabsf(vs[r]) * fast_exp2(tmax[r] - base[r]);
@@ -478,7 +495,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         }
       }
       if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {  // a row max (or its power) moved
-        if constexpr (!C::FP8) {
+        if constexpr (!C::CODES) {
 #pragma unroll
           for (int i2 = 0; i2 < D / 8; ++i2) {
             o[i2][0] *= alpha[0];
@@ -513,9 +530,12 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         lrun[0] += p0 + p1;
         lrun[1] += p2 + p3;
         const int kk = nt >> 1, hf = (nt & 1) * 2;
-        if constexpr (!C::FP8) {
+        if constexpr (!C::CODES) {
           pa[kk][hf + 0] = pack_bf16(p0, p1);
           pa[kk][hf + 1] = pack_bf16(p2, p3);
+        } else if constexpr (C::FP4) {
+          pa[kk][hf + 0] = pack_f16(p0, p1);
+          pa[kk][hf + 1] = pack_f16(p2, p3);
         } else {
           pa[kk][hf + 0] = pack_f16(p0 * vs[0], p1 * vs[0]);
           pa[kk][hf + 1] = pack_f16(p2 * vs[1], p3 * vs[1]);
@@ -532,7 +552,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             mlo = half_mask(in_item(ta), in_item(ta + 1));
             mhi = half_mask(in_item(tb), in_item(tb + 1));
           }
-          if constexpr (!C::FP8) {
+          if constexpr (!C::CODES) {
 #pragma unroll
             for (int dp = 0; dp < D / 16; ++dp) {
               const uint32_t tok = 16 * kk + (mi & 1) * 8 + (lane & 7);
@@ -560,18 +580,21 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
               e4m3x4_to_f16x2x2(prmt(sb.y, sb.w, sel), sv[1][2], sv[1][3]);
             }
             auto pairs = [](uint32_t w, uint32_t* f) {  // dims 0, 1, 2, 3 of both tokens
-              const uint32_t even = (w & 0x0F0Fu) | ((w >> 12) & 0xF0F0u);         // dims 0 and 2
-              const uint32_t odd = ((w >> 4) & 0x0F0Fu) | ((w >> 16) & 0xF0F0u);  // dims 1 and 3
-              e2m1x8_to_f16x2x4(even | (odd << 16), f[0], f[2], f[1], f[3]);
+              // (the low halves: in a byte one token's nibble under the other's)
+              const uint32_t even = (w & 0x0F0F0F0Fu) | ((w >> 12) & 0xF0F0F0F0u);        // dims 0 and 2
+              const uint32_t odd = ((w >> 4) & 0x0F0F0F0Fu) | ((w >> 16) & 0xF0F0F0F0u);  // dims 1 and 3
+              e2m1x4_to_f16x2x2(even, f[0], f[2]);
+              e2m1x4_to_f16x2x2(odd, f[1], f[3]);
             };
+            uint32_t w[2][2];  // [chunk & 1][8 tokens]
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
-              const uint32_t tok = 16 * kk + ((lane >> 3) & 1) * 8 + (lane & 7);
-              uint32_t r0, r1;
-              ldsm_x2_t(vbase + tile4_off(tok, c * 16), r0, r1);
+              if ((c & 1) == 0)
+                ldsm_x4_t(vbase + tile4_off(16 * kk + (mi & 1) * 8 + (lane & 7), (c + (mi >> 1)) * 16), w[0][0], w[0][1], w[1][0],
+                          w[1][1]);
               uint32_t f[2][4];
-              pairs(r0, f[0]);
-              pairs(r1, f[1]);
+              pairs(w[c & 1][0], f[0]);
+              pairs(w[c & 1][1], f[1]);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 f[0][i] = mul_f16x2(f[0][i], sv[0][c]);
@@ -642,7 +665,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     }
     // the factor of each element: rows gq, gq + 8; fp8: O^T, rows 2tq, 2tq+1 (+8)
     float fr[4] = {f[0], f[0], f[1], f[1]};
-    if constexpr (C::FP8) {
+    if constexpr (C::CODES) {
       fr[0] = __shfl_sync(0xffffffffu, f[0], 8 * tq);
       fr[1] = __shfl_sync(0xffffffffu, f[0], 8 * tq + 4);
       fr[2] = __shfl_sync(0xffffffffu, f[1], 8 * tq);
@@ -651,7 +674,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 #pragma unroll
     for (int i2 = 0; i2 < D / 8; ++i2)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[i2][e] *= C::FP8 ? fr[2 * (i2 & 1) + (e & 1)] : fr[e];
+      for (int e = 0; e < 4; ++e) o[i2][e] *= C::CODES ? fr[2 * (i2 & 1) + (e & 1)] : fr[e];
     float4* obuf = reinterpret_cast<float4*>(smem + C::OFF_O) + wm * (D / 8) * 32;
 #pragma unroll 1
     for (int w = 1; w < WN; ++w) {
@@ -680,9 +703,11 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       const bool some0 = L[0] != 0.f, some1 = L[1] != 0.f;
       float inv0 = some0 ? 1.f / L[0] : 0.f, inv1 = some1 ? 1.f / L[1] : 0.f;
       const bool w0 = v0 && (some0 || direct), w1 = v1 && (some1 || direct);
-      float lse0 = some0 ? (M[0] + __log2f(L[0])) * kLn2 : -INFINITY, lse1 = some1 ? (M[1] + __log2f(L[1])) * kLn2 : -INFINITY;
+      constexpr float kUp = C::FP4 ? kUp4 : 0.f;
+      float lse0 = some0 ? (M[0] + (__log2f(L[0]) - kUp)) * kLn2 : -INFINITY;
+      float lse1 = some1 ? (M[1] + (__log2f(L[1]) - kUp)) * kLn2 : -INFINITY;
       float prior0 = 0.f, prior1 = 0.f;  // weights of the prefix's result
-      if (direct && pc.skip > 0) {
+      if (C::SHARED && direct && pc.skip > 0) {
         if (v0) {
           const ChunkJoin j = chunk_join(lse0, __ldcg(p.ck.prior_lse + row_a));
           inv0 *= j.own, prior0 = j.prior, lse0 = j.lse;
@@ -692,10 +717,10 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           inv1 *= j.own, prior1 = j.prior, lse1 = j.lse;
         }
       }
-      const bool f32 = !direct || p.ck.out_f32;
-      float* out_f = direct ? static_cast<float*>(p.ck.out) : p.out_o;
+      const bool f32 = !direct || (C::SHARED && p.ck.out_f32);
+      float* out_f = C::SHARED && direct ? static_cast<float*>(p.ck.out) : p.out_o;
       auto store2 = [&](int64_t row, int d, float y0, float y1, float prior) {
-        if (prior != 0.f) {
+        if (C::SHARED && prior != 0.f) {
           const float2 x = __ldcg(reinterpret_cast<const float2*>(p.ck.prior_o + row * D + d));
           y0 = fmaf(x.x, prior, y0), y1 = fmaf(x.y, prior, y1);
         }
@@ -704,7 +729,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         else
           *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.ck.out) + row * D + d) = pack_bf16(y0, y1);
       };
-      if constexpr (!C::FP8) {
+      if constexpr (!C::CODES) {
 #pragma unroll
         for (int nt = 0; nt < D / 8; ++nt) {
           const int d = 8 * nt + 2 * tq;
@@ -744,14 +769,14 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 
 // (two sets with bf16 heads of 128: 5 warps a set have 168 registers each, too few: 95 us for 24
 // sequences of 5 rows, 40 / 8 heads, where 3 warps of 233 take 90; the other two fit, fp8 104 -> 90)
-template <int WM>
-using CfgBf16D64 = RowsCfg<kPagesBf16, 64, WM, WM == 1 ? 4 : 5, WM == 1 ? 6 : 12>;
-template <int WM>
-using CfgBf16D128 = RowsCfg<kPagesBf16, 128, WM, 3, WM == 1 ? 3 : 6>;
-template <int WM>
-using CfgFp8D128 = RowsCfg<kPagesFp8, 128, WM, WM == 1 ? 4 : 5, WM == 1 ? 6 : 12>;
-template <int WM>
-using CfgFp4D128 = RowsCfg<kPagesFp4, 128, WM, WM == 1 ? 4 : 5, WM == 1 ? 8 : 15>;
+template <int WM, bool SHARED>
+using CfgBf16D64 = RowsCfg<kPagesBf16, 64, WM, WM == 1 ? 4 : 5, WM == 1 ? 6 : 12, SHARED>;
+template <int WM, bool SHARED>
+using CfgBf16D128 = RowsCfg<kPagesBf16, 128, WM, 3, WM == 1 ? 3 : 6, SHARED>;
+template <int WM, bool SHARED>
+using CfgFp8D128 = RowsCfg<kPagesFp8, 128, WM, WM == 1 ? 4 : 5, WM == 1 ? 6 : 12, SHARED>;
+template <int WM, bool SHARED>
+using CfgFp4D128 = RowsCfg<kPagesFp4, 128, WM, 5, WM == 1 ? 9 : 15, SHARED>;
 
 template <class C>
 cudaError_t launch_cfg(const PartialParams& p, const ChunkMaps& maps, cudaStream_t stream) {
@@ -764,21 +789,30 @@ cudaError_t launch_cfg(const PartialParams& p, const ChunkMaps& maps, cudaStream
   return cudaGetLastError();
 }
 
-template <int WM>
+template <int WM, bool SHARED>
 cudaError_t launch_sets(const PartialParams& p, int32_t d, PageFormat pages, const ChunkMaps& maps, cudaStream_t stream) {
-  if (pages == kPagesFp4) return launch_cfg<CfgFp4D128<WM>>(p, maps, stream);
-  if (pages == kPagesFp8) return launch_cfg<CfgFp8D128<WM>>(p, maps, stream);
-  if (d == 64) return launch_cfg<CfgBf16D64<WM>>(p, maps, stream);
-  return launch_cfg<CfgBf16D128<WM>>(p, maps, stream);
+  if (pages == kPagesFp4) return launch_cfg<CfgFp4D128<WM, SHARED>>(p, maps, stream);
+  if (pages == kPagesFp8) return launch_cfg<CfgFp8D128<WM, SHARED>>(p, maps, stream);
+  if (d == 64) return launch_cfg<CfgBf16D64<WM, SHARED>>(p, maps, stream);
+  return launch_cfg<CfgBf16D128<WM, SHARED>>(p, maps, stream);
 }
 
 }  // namespace
 
+// (the passes of a shared prefix are compiled in a unit of their own, side by side with the others)
+#ifdef SKV_CHUNK_SHARED
+cudaError_t launch_chunk_rows_shared(const PartialParams& p, int32_t d, PageFormat pages, const ChunkMaps& maps,
+                                     cudaStream_t stream) {
+  return p.ck.rows == kRows ? launch_sets<1, true>(p, d, pages, maps, stream) : launch_sets<2, true>(p, d, pages, maps, stream);
+}
+#else
 int chunk_rows_ctas_per_sm(int rows) { return rows == kRows ? 2 : 1; }
 
 cudaError_t launch_chunk_rows(const PartialParams& p, int32_t d, PageFormat pages, const ChunkMaps& maps,
                               cudaStream_t stream) {
-  return p.ck.rows == kRows ? launch_sets<1>(p, d, pages, maps, stream) : launch_sets<2>(p, d, pages, maps, stream);
+  if (p.ck.shared) return launch_chunk_rows_shared(p, d, pages, maps, stream);
+  return p.ck.rows == kRows ? launch_sets<1, false>(p, d, pages, maps, stream) : launch_sets<2, false>(p, d, pages, maps, stream);
 }
+#endif
 
 }  // namespace skv

@@ -64,10 +64,11 @@ constexpr float kTileSumLimit = 65536.0f;
 // fused form leaves up to half a unit of the maximum's last place, which an exponential past 2^30 cannot hold
 constexpr float kLargeScore = 4194304.0f;
 
-template <int D_, bool FP8_>
+template <int D_, bool FP8_, bool SHARED_>
 struct TcCfg {
   static constexpr int D = D_;
   static constexpr bool FP8 = FP8_;
+  static constexpr bool SHARED = SHARED_;  // a pass of a shared prefix (ChunkArgs)
   static constexpr int THREADS = (FP8 ? 16 : 12) * 32;
   static constexpr int READERS = FP8 ? 15 : 11;      // warps that read the work items
   static constexpr int NB = D / 64;                  // 128-byte boxes of a row of 16-bit values
@@ -294,7 +295,7 @@ __device__ __noinline__ Redone redo_tile(uint32_t s_col, uint32_t o_col, bool ne
 // w0 O_k, plus w1 O_1 where both groups worked for the row, as bf16 or fp32.  64 bytes of every row
 // at a time go through shared memory, so that a store instruction covers 8 rows x 64 bytes instead
 // of 16 bytes of 32 rows.  prior_o (or NULL), prior: the prefix's result and this row's weight of it.
-template <int D>
+template <int D, bool SHARED>
 __device__ __noinline__ void store_rows(uint32_t o_col, bool has0, bool has1, float w0, bool some0, float w1, bool some1,
                                         unsigned write, int64_t orow, void* out, bool bf16, uint32_t stage,
                                         const float* prior_o, float prior) {
@@ -342,7 +343,7 @@ __device__ __noinline__ void store_rows(uint32_t o_col, bool has0, bool has1, fl
       for (int e = 0; e < 32; ++e)
         x[e >> 4][e & 15] = some0 ? __float_as_uint(__uint_as_float(x[e >> 4][e & 15]) * w0) : 0u;
     }
-    if (prior_o != nullptr && prior != 0.f) {
+    if (SHARED && prior_o != nullptr && prior != 0.f) {
 #pragma unroll
       for (int e = 0; e < 32; e += 4) {
         const float4 u = __ldcg(reinterpret_cast<const float4*>(prior_o + orow * D + c + e));
@@ -457,11 +458,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         TcItem t;
         t.it.b = -1;
         if (idx < total) {
-          t.it = chunk_item_at(p.ck, idx);
+          t.it = chunk_item_at<C::SHARED>(p.ck, idx);
           t.m0 = t.it.mt * 2 * kRowsTile;
           const int m_last = min(t.m0 + 2 * kRowsTile, t.it.n * Gr) - 1;
           t.pair = m_last - t.m0 >= kRowsTile ? 1 : 0;
-          const int pos0 = chunk_pos0(p.ck, t.it.n, t.it.m), step = chunk_pos_step(p.ck);
+          const int pos0 = chunk_pos0<C::SHARED>(p.ck, t.it.n, t.it.m), step = chunk_pos_step<C::SHARED>(p.ck);
           t.tl = chunk_tiles(p.ck.window, p.ck.n_sink, p.ck.cap, t.it.skip, pos0 + (t.m0 >> gr_bits) * step,
                              pos0 + (m_last >> gr_bits) * step);
           const int tiles = (t.tl.n + 1) / 2, per = (tiles + t.it.n_chunk - 1) / t.it.n_chunk;
@@ -510,8 +511,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           const int a = first[0], b = first[1] < p.ck.cap ? first[1] : a;
           at[0] = a % p.block_len;
           at[1] = b % p.block_len;
-          page[0] = chunk_page_of(p, t.it.b, a);
-          page[1] = chunk_page_of(p, t.it.b, b);
+          page[0] = chunk_page_of<C::SHARED>(p, t.it.b, a);
+          page[1] = chunk_page_of<C::SHARED>(p, t.it.b, b);
           if constexpr (C::FP8) {
             // the scales of both halves, a lane each (K, V, K, V).  Halves in which no row sees a token,
             // and pages outside the cache, take 0: their scales may be anything
@@ -907,7 +908,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int m = t.m0 + (pair ? k * kRowsTile : 0) + row;
         const int t_q = m >> gr_bits, hg = m & (Gr - 1);
         const bool valid = m < t.it.n * Gr && hg < G;
-        const int pos = chunk_pos0(p.ck, t.it.n, t.it.m) + t_q * chunk_pos_step(p.ck);
+        const int pos = chunk_pos0<C::SHARED>(p.ck, t.it.n, t.it.m) + t_q * chunk_pos_step<C::SHARED>(p.ck);
         // visible tokens of this row: [lo_row, hi_row) and [0, sink_row)
         const int hi_row = valid ? min(max(pos + 1, 0), p.ck.cap) : 0;
         const int lo_row = (valid && p.ck.window > 0 && pos >= p.ck.window) ? pos - p.ck.window + 1 : 0;
@@ -1061,7 +1062,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const int64_t orow = direct ? (static_cast<int64_t>(t.it.row0) + t_q) * p.Hq + h
                                   : t.it.part_row + (static_cast<int64_t>(t.it.c) * t.it.n + t_q) * p.Hq + h;
       float prior = 0.f;  // weight of the prefix's result
-      const bool behind = direct && t.it.skip > 0;
+      const bool behind = C::SHARED && direct && t.it.skip > 0;
       if (behind && valid) {
         const ChunkJoin j = chunk_join(lse, __ldcg(p.ck.prior_lse + orow));
         inv *= j.own, prior = j.prior, lse = j.lse;
@@ -1071,8 +1072,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       // an empty partial's o is never read
       const unsigned write_o = __ballot_sync(0xffffffffu, valid && (direct || some));
       if (write_o != 0u) {
-        store_rows<D>(o_col, t.n_tiles > 0, both, some0 ? a0 : 0.f, some0, some1 ? a1 : 0.f, some1, write_o, orow,
-                      direct ? p.ck.out : p.out_o, direct && !p.ck.out_f32,
+        store_rows<D, C::SHARED>(o_col, t.n_tiles > 0, both, some0 ? a0 : 0.f, some0, some1 ? a1 : 0.f, some1, write_o, orow,
+                      direct ? p.ck.out : p.out_o, direct && !(C::SHARED && p.ck.out_f32),
                       smem_u32(smem + C::OFF_OUT + (warp - 4) * (32 * 64)), behind ? p.ck.prior_o : nullptr, prior);
       }
       if (valid) (direct ? p.ck.lse : p.out_lse)[orow] = lse;
@@ -1110,17 +1111,31 @@ cudaError_t launch_cfg(const PartialParams& p, const ChunkMaps& maps, int64_t n_
   return cudaLaunchKernelEx(&cfg, chunk_tc_kernel<C>, p, maps);
 }
 
+template <bool SHARED>
+cudaError_t launch(const PartialParams& p, int32_t d, PageFormat pages, const ChunkMaps& maps, int64_t n_items,
+                   cudaStream_t stream) {
+  if (pages == kPagesFp8) return launch_cfg<TcCfg<128, true, SHARED>>(p, maps, n_items, stream);
+  if (d == 64) return launch_cfg<TcCfg<64, false, SHARED>>(p, maps, n_items, stream);
+  return launch_cfg<TcCfg<128, false, SHARED>>(p, maps, n_items, stream);
+}
+
 }  // namespace
 
+// (the passes of a shared prefix are compiled in a unit of their own, side by side with the others)
+#ifdef SKV_CHUNK_SHARED
+cudaError_t launch_chunk_tc_shared(const PartialParams& p, int32_t d, PageFormat pages, const ChunkMaps& maps,
+                                   int64_t n_items, cudaStream_t stream) {
+  return launch<true>(p, d, pages, maps, n_items, stream);
+}
+#else
 int chunk_tc_rows() { return 2 * kRowsTile; }
 int chunk_tc_kv_tile() { return kTN; }
-int chunk_tc_kv_box() { return kHalf; }
 
 cudaError_t launch_chunk_tc(const PartialParams& p, int32_t d, PageFormat pages, const ChunkMaps& maps, int64_t n_items,
                             cudaStream_t stream) {
-  if (pages == kPagesFp8) return launch_cfg<TcCfg<128, true>>(p, maps, n_items, stream);
-  if (d == 64) return launch_cfg<TcCfg<64, false>>(p, maps, n_items, stream);
-  return launch_cfg<TcCfg<128, false>>(p, maps, n_items, stream);
+  return p.ck.shared ? launch_chunk_tc_shared(p, d, pages, maps, n_items, stream)
+                     : launch<false>(p, d, pages, maps, n_items, stream);
 }
+#endif
 
 }  // namespace skv

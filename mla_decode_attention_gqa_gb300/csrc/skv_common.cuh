@@ -181,6 +181,16 @@ __device__ __forceinline__ void e2m1x8_to_f16x2x4(uint32_t w, uint32_t& a, uint3
       : "r"(w));
 }
 
+// The codes of the low two bytes of w.
+__device__ __forceinline__ void e2m1x4_to_f16x2x2(uint32_t w, uint32_t& a, uint32_t& b) {
+  asm("{\n\t.reg .b8 p, q, r, s;\n\t"
+      "mov.b32 {p, q, r, s}, %2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, p;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, q;\n\t}"
+      : "=r"(a), "=r"(b)
+      : "r"(w));
+}
+
 // Eight values as e2m1 codes (value j in nibble j): to the nearest, ties to even, +-6 at most.
 __device__ __forceinline__ uint32_t f32x8_to_e2m1x8(const float* x) {
   uint32_t w;

@@ -56,6 +56,7 @@ struct ChunkArgs {
   // row sees (seq_lens: the prefixes; first_row, table_row: device [B]), and the result is fp32.  Over the
   // rest, sequence b's tokens from skip[b] on (a multiple of kTileN) are attended, and rows with
   // skip[b] > 0 are joined with the prefix's result (prior_o fp32 [T][Hq][d], prior_lse [T][Hq]).
+  int32_t shared;   // one of these passes
   const int32_t* group_rows_at;  // device [B + 1]: first packed row of each group (NULL: cu_q)
   const int32_t* table_row;      // device [B]: block-table row of each group (NULL: b)
   const int32_t* skip;           // device [B] (NULL: 0)
@@ -185,18 +186,20 @@ struct ChunkMaps {
 int chunk_rows_ctas_per_sm(int rows);
 cudaError_t launch_chunk_rows(const PartialParams& p, int32_t d, PageFormat pages, const ChunkMaps& maps,
                               cudaStream_t stream);
+cudaError_t launch_chunk_rows_shared(const PartialParams& p, int32_t d, PageFormat pages, const ChunkMaps& maps,
+                                     cudaStream_t stream);
 cudaError_t launch_chunk_runs_merge(const ChunkArgs& a, int32_t d, const float* part_o, const float* part_lse,
                                     cudaStream_t stream);
 // On the tensor cores (see chunk_tc.cu), any G <= 128; maps.q: q as (dim, head, packed
-// row) with 64 x group_rows x 128 / group_rows boxes, maps.k / v: pages with chunk_tc_kv_box()
-// rows a box.
+// row) with 64 x group_rows x 128 / group_rows boxes, maps.k / v: pages with kTileN rows a box.
 // launch_chunk_plan, directly before it on the stream, writes the plan that it takes its items from.
 cudaError_t launch_chunk_plan(const ChunkArgs& a, cudaStream_t stream);
 int chunk_tc_rows();
 int chunk_tc_kv_tile();
-int chunk_tc_kv_box();
 cudaError_t launch_chunk_tc(const PartialParams& p, int32_t d, PageFormat pages, const ChunkMaps& maps, int64_t n_items,
                             cudaStream_t stream);
+cudaError_t launch_chunk_tc_shared(const PartialParams& p, int32_t d, PageFormat pages, const ChunkMaps& maps,
+                                   int64_t n_items, cudaStream_t stream);
 cudaError_t launch_chunk_merge(const ChunkArgs& a, int32_t d, const float* part_o, const float* part_lse,
                                int64_t max_rows, cudaStream_t stream);
 // The groups of a shared prefix, ahead of its two passes (see shared_prefix.cu).
