@@ -1137,7 +1137,7 @@ skv_status chunk_plan(const skv_desc* d, int32_t B, int32_t T, int32_t longest_o
   // 488), up to 32 two (24 sequences of 5 rows, 40 / 8 heads: 90 us against 112, fp8 90 against 153); a
   // group above 128 heads has no query tile there.
   const int64_t longest = longest_or_0 > 0 ? std::min(longest_or_0, T) : T;
-  pl->tc = longest * G > 32 && G <= 128 && page_format(d) != kPagesFp4;
+  pl->tc = longest * G > 32 && G <= 128;
   pl->group_rows = pl->tc ? padded_group(G) : G;
   pl->rows = pl->tc ? chunk_tc_rows() : longest * G <= 16 ? 16 : 32;
   pl->tile = pl->tc ? chunk_tc_kv_tile() : kTileN;
@@ -1184,6 +1184,12 @@ skv_status chunk_params(const skv_chunk_desc* desc, const skv_desc& d, const skv
   if (fp4) {
     p->k_head = fp4->k_head;
     p->v_head = fp4->v_head;
+    for (int x = 0; x < 2; ++x) {
+      const int64_t* st = x ? d.v_strides : d.k_strides;
+      p->codes[x] = static_cast<const uint8_t*>(x ? v_pages : k_pages);
+      p->code_sb[x] = st[0], p->code_sh[x] = st[1], p->code_st[x] = st[2];
+      p->block_scales[x] = static_cast<const uint8_t*>(x ? fp4->v_block : fp4->k_block);
+    }
     if ((st = encode_fp4_scale_map(&maps->k_block, fp4->k_block, &d, kTileN, paged)) != SKV_OK) return st;
     if ((st = encode_fp4_scale_map(&maps->v_block, fp4->v_block, &d, kTileN, paged)) != SKV_OK) return st;
   } else {

@@ -87,11 +87,6 @@ __device__ __forceinline__ uint32_t tile_off(uint32_t tok, uint32_t byte) {
 __device__ __forceinline__ uint32_t tile4_off(uint32_t tok, uint32_t byte) {
   return tok * 64u + ((((byte >> 4) ^ ((tok >> 1) & 3u)) << 4) | (byte & 15u));
 }
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 __device__ __forceinline__ uint32_t half_mask(bool lo, bool hi) {
   return (lo ? 0x0000FFFFu : 0u) | (hi ? 0xFFFF0000u : 0u);
 }
@@ -776,7 +771,7 @@ using CfgBf16D128 = RowsCfg<kPagesBf16, 128, WM, 3, WM == 1 ? 3 : 6, SHARED>;
 template <int WM, bool SHARED>
 using CfgFp8D128 = RowsCfg<kPagesFp8, 128, WM, WM == 1 ? 4 : 5, WM == 1 ? 6 : 12, SHARED>;
 template <int WM, bool SHARED>
-using CfgFp4D128 = RowsCfg<kPagesFp4, 128, WM, 5, WM == 1 ? 9 : 15, SHARED>;
+using CfgFp4D128 = RowsCfg<kPagesFp4, 128, WM, WM == 1 ? 4 : 5, WM == 1 ? 8 : 15, SHARED>;
 
 template <class C>
 cudaError_t launch_cfg(const PartialParams& p, const ChunkMaps& maps, cudaStream_t stream) {

@@ -1,6 +1,6 @@
 // Tensor-core (tcgen05) attention of ragged chunks of new tokens over a paged cache
 // (attn_chunk_paged): prompt chunks, proposed tokens and decode tokens of one packed batch,
-// causal or with a sliding window and sinks; bf16 pages, or fp8-e4m3 pages with block scales.
+// causal or with a sliding window and sinks; bf16 pages, fp8-e4m3 pages with block scales, or 4-bit pages.
 //
 // For every row (new token at position p, query head h of KV head g): s_u = scale q.k_u over
 // the visible tokens u (u <= p and u > p - window or u < n_sink), out = softmax(s) V, lse =
@@ -34,6 +34,11 @@
 //     (exact) for P V; the K block scale goes into the score's scale, the V block scale into p
 //     before its rounding.  (Widening K as well made the converters the bound: 554 us for ragged
 //     prompts over an fp8 cache that take 329 this way);
+//   * 4-bit: four converter warps, a token row a thread, load codes and block scales from the pages a tile
+//     ahead, and write K and V tiles in fp16 (code times block scale, exact); they also turn Q to fp16, a
+//     row times a power of two.  Both products run in fp16, p against a maximum that lies kUp4 powers
+//     of two lower, so that fp16 holds all bits of weights down to 2^-22 of the largest and
+//     something of those down to 2^-33;
 //   * optimistic softmax: p = 2^(s - m) against the maximum so far; only a row's first visible
 //     tile takes a maximum (of 32 columns) beforehand, and a tile whose p sum passes 2^16 its true
 //     one, with O rescaled, and its p again.
@@ -64,13 +69,19 @@ constexpr float kTileSumLimit = 65536.0f;
 // fused form leaves up to half a unit of the maximum's last place, which an exponential past 2^30 cannot hold
 constexpr float kLargeScore = 4194304.0f;
 
-template <int D_, bool FP8_, bool SHARED_>
+// 4-bit pages: p is at most 2^kUp4 where the maximum is a true one (128 of them sum to 2^15), and no tile's
+// sum passes kTileSumLimit4, so that no p leaves fp16
+constexpr float kUp4 = 8.f;
+constexpr float kTileSumLimit4 = 65000.0f;
+
+template <int D_, PageFormat PAGES_, bool SHARED_>
 struct TcCfg {
   static constexpr int D = D_;
-  static constexpr bool FP8 = FP8_;
+  static constexpr bool FP8 = PAGES_ == kPagesFp8, FP4 = PAGES_ == kPagesFp4;
+  static constexpr bool CODES = FP8 || FP4;  // converter warps
   static constexpr bool SHARED = SHARED_;  // a pass of a shared prefix (ChunkArgs)
-  static constexpr int THREADS = (FP8 ? 16 : 12) * 32;
-  static constexpr int READERS = FP8 ? 15 : 11;      // warps that read the work items
+  static constexpr int THREADS = (CODES ? 16 : 12) * 32;
+  static constexpr int READERS = FP8 ? 15 : FP4 ? 14 : 11;  // warps that read the work items
   static constexpr int NB = D / 64;                  // 128-byte boxes of a row of 16-bit values
   static constexpr int NST = D == 64 ? 4 : 2;        // ring depth, tiles
   static constexpr int BOX = kTN * 128;              // one box column of a tile: 128 rows x 128 bytes
@@ -85,11 +96,11 @@ struct TcCfg {
   static constexpr int OFF_ML = OFF_BAR + 768;       // solo: group 1's (m, l) per row
   static constexpr int OFF_ITEM = OFF_ML + kRowsTile * 8;
   static constexpr int OFF_QS = OFF_ITEM + 256;      // fp8: Q's row scales [item & 1][query tile][row]
-  static constexpr int OFF_OUT = OFF_QS + (FP8 ? 4 * kRowsTile * 4 : 0);  // 64 bytes of each output row
+  static constexpr int OFF_OUT = OFF_QS + (CODES ? 4 * kRowsTile * 4 : 0);  // 64 bytes of each output row
   static constexpr int OFF_ROW = OFF_OUT + 2 * kRowsTile * 64;            // what each softmax thread's row sees
   static constexpr int SMEM = 1024 + OFF_ROW + 2 * kRowsTile * 16;
   static_assert(kHalf == kTileN, "the plan counts in halves");
-  static_assert(!FP8 || D == 128, "e4m3 rows are one 128-byte box");
+  static_assert(!CODES || D == 128, "e4m3 rows are one 128-byte box, e2m1 rows half of one");
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
 };
 
@@ -241,13 +252,13 @@ __device__ __noinline__ float first_max(uint32_t s_col, float m, float scale0, f
 struct Redone {
   float m, l;
 };
-template <int D, bool FP8>
+template <int D, bool FP8, bool FP4>
 __device__ __noinline__ Redone redo_tile(uint32_t s_col, uint32_t o_col, bool need, float m, float l, float scale0,
                                          float scale1, float v0, float v1) {
-  float mx = m;
+  float mx = -INFINITY;
 #pragma unroll 1
   for (int cc = 0; cc < kTN / 32; ++cc) mx = fmaxf(mx, largest<FP8>(s_col + 32 * cc, cc < 2 ? scale0 : scale1));
-  const float m_new = need ? mx : m;
+  const float m_new = need ? fmaxf(m, FP4 ? mx - kUp4 : mx) : m;
   const float alpha = (need && l != 0.f) ? fast_exp2(m - m_new) : 1.f;
   if (__any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
@@ -281,7 +292,7 @@ __device__ __noinline__ Redone redo_tile(uint32_t s_col, uint32_t o_col, bool ne
       float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
       ls[e & 1] = add_f32x2(ls[e & 1], p0, p1);
       if constexpr (FP8) mul_pair(p0, p1, v2);
-      w[e] = pack_bf16(p0, p1);
+      w[e] = FP4 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
     }
     tc::tmem_st16(s_col + 16 * cc, w);  // S columns 32 cc.. were read before P 16 cc.. is written
   }
@@ -393,9 +404,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 1);
     for (int s = 0; s < NST; ++s) {
-      mbar_init(&bars->k_full[s], 1);
+      mbar_init(&bars->k_full[s], C::FP4 ? 128 : 1);
       mbar_init(&bars->k_empty[s], 1);
-      mbar_init(&bars->v_full[s], C::FP8 ? 128 : 1);
+      mbar_init(&bars->v_full[s], C::CODES ? 128 : 1);
       mbar_init(&bars->v_empty[s], 1);
       mbar_init(&bars->v8_full[s], 1);
       mbar_init(&bars->v8_empty[s], 128);
@@ -434,9 +445,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     return true;
   };
 
-  // fp8: the launch's 512 threads x 128 registers as 128 x (88 + 72 + 176 + 176)
+  // codes: the launch's 512 threads x 128 registers as 128 x (88 + 72 + 176 + 176), 4-bit: (80 + 80 + ..)
   if (warp < 4) {
-    if constexpr (C::FP8)
+    if constexpr (C::FP4)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    else if constexpr (C::FP8)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     else
       asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
@@ -477,6 +490,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         __syncwarp();
         if (t.it.b < 0) break;
       }
+    } else if (C::FP4 && warp == 2) {
+      // (nothing: the converter warps load K and V)
     } else if (warp != 1) {
       // ------------------------------------------------------------ TMA producers: 0 Q and K, 2 V
       // A warp each, so that neither waits for the other's ring; the pages and rows of the next
@@ -490,7 +505,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       uint64_t* empty = is_k ? bars->k_empty : C::FP8 ? bars->v8_empty : bars->v_empty;
       uint8_t* ring = smem + (is_k ? C::OFF_K : C::FP8 ? C::OFF_V8 : C::OFF_V);
       if (tc::elect_one()) {
-        tma_prefetch_desc(map);
+        if (!C::FP4) tma_prefetch_desc(map);
         if (is_k) tma_prefetch_desc(&tmq);
       }
       __syncwarp();
@@ -526,7 +541,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
           }
         };
-        look_up(0);
+        if (!C::FP4) look_up(0);
         if (is_k) {
           // the item before has no scores left to compute
           if (nq > 0 && !wait_all(&bars->q_empty, (nq - 1) & 1)) break;
@@ -540,7 +555,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           __syncwarp();
           ++nq;
         }
-        for (int i = 0; i < t.n_tiles; ++i) {
+        for (int i = 0; !C::FP4 && i < t.n_tiles; ++i) {
           const int s = done % NST;
           ok = done < NST || wait_all(&empty[s], ((done / NST) - 1) & 1);
           if (!ok) break;
@@ -577,8 +592,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       // The whole warp waits, one elected lane issues; a tile's stage is a compile-time constant,
       // so every operand is a constant offset.
       // (format 0 of kind::f8f6f4 is e4m3, as 0 of kind::f16 is fp16)
-      const uint32_t idesc_s = tc::idesc_f16(128, kTN, !C::FP8, false, false);
-      const uint32_t idesc_pv = tc::idesc_f16(128, D, true, false, true);
+      const uint32_t idesc_s = tc::idesc_f16(128, kTN, !C::CODES, false, false);
+      const uint32_t idesc_pv = tc::idesc_f16(128, D, !C::FP4, false, true);
       const uint64_t qd = tc::smem_desc_sw128(smem_u32(smem), 16, 1024);
       const uint64_t kd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
       const uint64_t vd = tc::smem_desc_sw128(smem_u32(smem + C::OFF_V), C::BOX, 1024);
@@ -634,7 +649,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       for (int r = 0; ok && next_item(r, &t); ++r) {
         const int n = t.n_tiles;
         if (n == 0) continue;
-        ok = C::FP8 ? wait_all(&bars->q8_full[nq & 1], (nq >> 1) & 1) : wait_all(&bars->q_full, nq & 1);
+        ok = C::CODES ? wait_all(&bars->q8_full[nq & 1], (nq >> 1) & 1) : wait_all(&bars->q_full, nq & 1);
         if (!ok) break;
         ++nq;
         // scores of tile x (both groups, or group x & 1 in solo mode); the last ones free Q
@@ -746,6 +761,125 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
         }
         base += n;
+      }
+    }
+  } else if (C::FP4 && warp >= 12) {
+    // ------------------------------------------------------------ 4-bit: Q, K and V to fp16
+    if constexpr (C::FP4) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+      const int row = (warp - 12) * 32 + lane;
+      // A row of Q times the power of two that puts its largest magnitude in [2^14, 2^15): exact in fp16
+      // for every value within 2^-31 of the largest.  An infinity or a NaN makes the row's scores NaN
+      auto narrow_q = [&](uint8_t* q) -> float {
+        auto chunk = [&](int c) {
+          return reinterpret_cast<uint4*>(q + (c >> 3) * C::BOX + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+        };
+        uint32_t most = 0u;  // magnitudes order as their bits; a NaN is above infinity
+#pragma unroll 4
+        for (int c = 0; c < 16; ++c) {
+          const uint4 u = *chunk(c);
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) most = max(most, max((w[j] << 16) & 0x7FFF0000u, w[j] & 0x7FFF0000u));
+        }
+        const bool finite = most < 0x7F800000u;
+        const int e = most == 0u ? 0 : min(max(static_cast<int>(most >> 23) - 127 - 14, -126), 126);
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        auto narrow = [&](uint32_t w) { return pack_f16(bf16_lo(w) * down, bf16_hi(w) * down); };
+#pragma unroll 2
+        for (int c = 0; c < 16; ++c) {
+          const uint4 u = *chunk(c);
+          *chunk(c) = make_uint4(narrow(u.x), narrow(u.y), narrow(u.z), narrow(u.w));
+        }
+        return finite ? __uint_as_float(static_cast<uint32_t>(127 + e) << 23) : __int_as_float(0x7fc00000);
+      };
+      // Where this thread's token of tile i lies: its row of the pages' rows (page < 0: zeros)
+      struct Place {
+        int64_t page;
+        int at;
+      };
+      auto place_of = [&](const TcItem& t, int i) -> Place {
+        const int first = t.token(2 * i), second = t.token(2 * i + 1);
+        // a second half at or past the capacity holds no token: it takes the first one's page instead of
+        // an entry behind the table's row
+        const int tok = row < kHalf || second >= p.ck.cap ? first : second;
+        Place pl;
+        pl.page = chunk_page_of<C::SHARED>(p, t.it.b, tok);
+        pl.at = tok % p.block_len + (row & (kHalf - 1));
+        if (pl.page >= p.num_blocks) pl.page = -1;
+        return pl;
+      };
+      struct Row {
+        uint4 codes[4];
+        uint2 scales;
+      };
+      auto load = [&](int x, int g, const Place& pl) -> Row {  // x: 0 K, 1 V
+        Row r;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r.codes[j] = make_uint4(0u, 0u, 0u, 0u);
+        r.scales = make_uint2(0u, 0u);
+        if (pl.page >= 0) {
+          const uint4* from = reinterpret_cast<const uint4*>(p.codes[x] + pl.page * p.code_sb[x] + g * p.code_sh[x] + pl.at * p.code_st[x]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) r.codes[j] = __ldg(from + j);
+          r.scales = __ldg(reinterpret_cast<const uint2*>(p.block_scales[x]) + (pl.page * p.Hkv + g) * p.block_len + pl.at);
+        }
+        return r;
+      };
+      // 8 codes at a time to 16 bytes of the 128-byte-swizzled tile (conflict-free: eight rows, eight chunks)
+      auto convert = [&](const Row& r, uint8_t* to) {
+        uint32_t sc[4];  // pairs of blocks
+        e4m3x4_to_f16x2x2(r.scales.x, sc[0], sc[1]);
+        e4m3x4_to_f16x2x2(r.scales.y, sc[2], sc[3]);
+        uint8_t* d = to + row * 128;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const uint4& u = r.codes[j >> 2];
+          const uint32_t w = (j & 3) == 0 ? u.x : (j & 3) == 1 ? u.y : (j & 3) == 2 ? u.z : u.w;
+          const uint32_t by = prmt(sc[j >> 2], 0u, ((j >> 1) & 1) ? 0x3232u : 0x1010u);
+          uint32_t a, b, c, e;
+          e2m1x8_to_f16x2x4(w, a, b, c, e);
+          st_shared_v4(smem_u32(d + (j >> 3) * C::BOX + (((j & 7) ^ (row & 7)) << 4)), mul_f16x2(a, by), mul_f16x2(b, by),
+                       mul_f16x2(c, by), mul_f16x2(e, by));
+        }
+      };
+      int done = 0, nq = 0;  // tiles and query tiles so far
+      bool ok = true;
+      auto wait_all = [&](uint64_t* bar, uint32_t parity, unsigned int code) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, p.err, code)) != 0;
+      };
+      TcItem t;
+      for (int r = 0; ok && next_item(r, &t); ++r) {
+        const int n = t.n_tiles, g = t.it.g;
+        if (n == 0) continue;
+        Place pl = place_of(t, 0);
+        Row k = load(0, g, pl);
+        ok = wait_all(&bars->q_full, nq & 1, kDevErrFullWait);
+        if (!ok) break;
+        float* qs = reinterpret_cast<float*>(smem + C::OFF_QS) + (nq & 1) * 2 * kRowsTile;
+        for (int x = 0; x <= t.pair; ++x) qs[x * kRowsTile + row] = narrow_q(smem + x * C::TILE);
+        fence_proxy_async_smem();
+        mbar_arrive(&bars->q8_full[nq & 1]);
+        ++nq;
+        for (int i = 0; i < n; ++i, ++done) {
+          const int s = done % NST;
+          const uint32_t parity = ((done / NST) - 1) & 1;
+          const Row v = load(1, g, pl);  // under K's conversion
+          ok = done < NST || wait_all(&bars->k_empty[s], parity, kDevErrEmptyWait);
+          if (!ok) break;
+          convert(k, smem + C::OFF_K + s * C::TILE);
+          fence_proxy_async_smem();
+          mbar_arrive(&bars->k_full[s]);
+          if (i + 1 < n) {  // the next tile's K under V's
+            pl = place_of(t, i + 1);
+            k = load(0, g, pl);
+          }
+          ok = done < NST || wait_all(&bars->v_empty[s], parity, kDevErrEmptyWait);
+          if (!ok) break;
+          convert(v, smem + C::OFF_V + s * C::TILE);
+          fence_proxy_async_smem();
+          mbar_arrive(&bars->v_full[s]);
+        }
       }
     }
   } else if (warp >= 12) {  // (fp8 only: no such warps otherwise)
@@ -881,7 +1015,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
   } else {
     // ------------------------------------------------------------ softmax groups
-    if constexpr (C::FP8)
+    if constexpr (C::CODES)
       asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     else
       asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
@@ -920,7 +1054,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         *mine = make_int4(hi_row, lo_row, sink_row, valid ? 1 : 0);
       }
       float m_used = -INFINITY, l_sum = 0.f;
-      float q_scale = 0.f;  // fp8: the score scale times the row's own
+      float q_scale = 0.f;  // codes: the score scale times the row's own (4-bit: and K's head's)
       const int step = pair ? 1 : 2;  // this group's tiles: all, or every other
 
       int j = 0;  // tiles of the item done
@@ -947,7 +1081,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
             sl[0] = q_scale * sc.x, vs[0] = sc.y, sl[1] = q_scale * sc.z, vs[1] = sc.w;
           }
-          if constexpr (C::FP8) {  // a masked score is an infinity that the scale makes -inf
+          if constexpr (C::FP4) {
+            if (j == 0) {  // (as above)
+              if (!wait(&bars->q8_full[nq & 1], (nq >> 1) & 1, kDevErrFullWait)) break;
+              q_scale = p.scale_log2 * head_scale(p.k_head, t.it.g) *
+                        reinterpret_cast<const float*>(smem + C::OFF_QS)[((nq & 1) * 2 + (pair ? k : 0)) * kRowsTile + row];
+            }
+            sl[0] = sl[1] = q_scale;
+          }
+          if constexpr (C::CODES) {  // a masked score is an infinity that the scale makes -inf
             sl[0] = sl[0] == 0.f ? 1e-37f : sl[0];
             sl[1] = sl[1] == 0.f ? 1e-37f : sl[1];
           }
@@ -956,7 +1098,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             hide_scores(s_col, ta, tb, *mine, hi_min, lo_max, sink_min, C::FP8 && sl[0] < 0.f ? -inf : inf,
                         C::FP8 && sl[1] < 0.f ? -inf : inf);
           }
-          if (__any_sync(0xffffffffu, m_used == -INFINITY)) m_used = first_max<C::FP8>(s_col, m_used, sl[0], sl[1]);
+          if (__any_sync(0xffffffffu, m_used == -INFINITY)) {
+            const float first = first_max<C::FP8>(s_col, m_used, sl[0], sl[1]);
+            m_used = C::FP4 && m_used == -INFINITY ? first - kUp4 : first;
+          }
           uint32_t pk[kTN / 2];
           uint64_t ls[2] = {0ull, 0ull};  // fp32 pair sums of p
           const float base0 = (m_used == -INFINITY) ? 0.f : m_used;
@@ -975,13 +1120,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 float p0 = fast_exp2(a0), p1 = fast_exp2(a1);
                 ls[e & 1] = add_f32x2(ls[e & 1], p0, p1);
                 if constexpr (C::FP8) mul_pair(p0, p1, vs[cc >> 1]);  // V = code * scale
-                pk[16 * cc + e] = pack_bf16(p0, p1);
+                pk[16 * cc + e] = C::FP4 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
               }
             }
           }
-          const bool need = !(sum_f32x2(ls[0]) + sum_f32x2(ls[1]) <= kTileSumLimit) || fabsf(base0) > kLargeScore;
+          const bool need = !(sum_f32x2(ls[0]) + sum_f32x2(ls[1]) <= (C::FP4 ? kTileSumLimit4 : kTileSumLimit)) || fabsf(base0) > kLargeScore;
           if (__any_sync(0xffffffffu, need)) {
-            const Redone again = redo_tile<D, C::FP8>(s_col, o_col, need, m_used, l_sum, sl[0], sl[1], vs[0], vs[1]);
+            const Redone again = redo_tile<D, C::FP8, C::FP4>(s_col, o_col, need, m_used, l_sum, sl[0], sl[1], vs[0], vs[1]);
             m_used = again.m;
             l_sum = again.l;
           } else {
@@ -1053,6 +1198,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       tc::fence_after_sync();
       const bool some = some0 || some1;
       float inv = some ? 1.f / l_sum : 0.f;
+      if constexpr (C::FP4) inv *= head_scale(p.v_head, t.it.g);
       constexpr float kLn2 = 0.6931471805599453f;
       float lse = some ? (m_used + __log2f(l_sum)) * kLn2 : -INFINITY;
       const bool direct = t.it.n_chunk == 1;
@@ -1114,9 +1260,10 @@ cudaError_t launch_cfg(const PartialParams& p, const ChunkMaps& maps, int64_t n_
 template <bool SHARED>
 cudaError_t launch(const PartialParams& p, int32_t d, PageFormat pages, const ChunkMaps& maps, int64_t n_items,
                    cudaStream_t stream) {
-  if (pages == kPagesFp8) return launch_cfg<TcCfg<128, true, SHARED>>(p, maps, n_items, stream);
-  if (d == 64) return launch_cfg<TcCfg<64, false, SHARED>>(p, maps, n_items, stream);
-  return launch_cfg<TcCfg<128, false, SHARED>>(p, maps, n_items, stream);
+  if (pages == kPagesFp4) return launch_cfg<TcCfg<128, kPagesFp4, SHARED>>(p, maps, n_items, stream);
+  if (pages == kPagesFp8) return launch_cfg<TcCfg<128, kPagesFp8, SHARED>>(p, maps, n_items, stream);
+  if (d == 64) return launch_cfg<TcCfg<64, kPagesBf16, SHARED>>(p, maps, n_items, stream);
+  return launch_cfg<TcCfg<128, kPagesBf16, SHARED>>(p, maps, n_items, stream);
 }
 
 }  // namespace

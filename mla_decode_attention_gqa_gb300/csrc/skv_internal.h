@@ -117,6 +117,10 @@ struct PartialParams {
   const int32_t* bounds;  // device [B][n_split + 1], or NULL: one split [0, S_max) per row
   const float* k_head;  // 4-bit pages: [Hkv], or NULL: 1
   const float* v_head;
+  // 4-bit pages: K's and V's codes, their strides in bytes (page, head, token), and block scales
+  const uint8_t* codes[2];
+  int64_t code_sb[2], code_sh[2], code_st[2];
+  const uint8_t* block_scales[2];
   ChunkArgs ck;  // ragged chunks only: replaces Tq, bounds, n_split, n_chunk and m_tiles
 };
 
