@@ -246,6 +246,8 @@ constexpr int kPlanThreads = 512;
 template <bool SHARED>
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_constant__ ChunkArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // a pass of a shared prefix: the groups' arrays are there, and the pass before has left the workspace
+  if constexpr (SHARED) asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ int64_t sm_scan[2 * (kPlanThreads / 32)];
   int64_t items, merged;
   chunk_make_plan<kPlanThreads, SHARED>(a, sm_scan, &items, &merged,
@@ -262,10 +264,19 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const __grid_c
 }  // namespace
 
 cudaError_t launch_chunk_plan(const ChunkArgs& a, cudaStream_t stream) {
-  if (a.shared)
-    chunk_plan_kernel<true><<<1, kPlanThreads, 0, stream>>>(a);
-  else
-    chunk_plan_kernel<false><<<1, kPlanThreads, 0, stream>>>(a);
+  if (a.shared) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, chunk_plan_kernel<true>, a);
+  }
+  chunk_plan_kernel<false><<<1, kPlanThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -202,7 +202,11 @@ __device__ __forceinline__ void chunk_make_plan(const ChunkArgs& a, int64_t* sm_
     w += static_cast<int64_t>(rt) * a.Hkv * kt;
   }
   chunk_block_scan<NT>(w, zero, &total, &unused, sm_scan);
-  const int64_t target = total <= a.n_wave * static_cast<int64_t>(kChunkShortTiles) ? a.n_wave : a.n_target;
+  // (prefixes: one wave of items, with chunks rounded to the nearest number instead of down, since every one
+  // writes fp32 rows that the merge reads again; 4/3 of W / L at most.  64 rows of 64 / 8 heads behind 32768
+  // tokens: 9 chunks a row tile where four waves made 36, 60 us and 8 of merge for 81 and 27)
+  const bool whole = SHARED && a.whole;
+  const int64_t target = whole || total <= a.n_wave * static_cast<int64_t>(kChunkShortTiles) ? a.n_wave : a.n_target;
   const int L = static_cast<int>(min(max((total + target - 1) / target, (int64_t)1), (int64_t)1 << 30));
   const int Hq = a.Hkv * a.G;
   int64_t it0 = 0, part0 = 0, mr0 = 0;  // of the sequences before this pass
@@ -212,7 +216,7 @@ __device__ __forceinline__ void chunk_make_plan(const ChunkArgs& a, int64_t* sm_
     if (b < a.B) {
       chunk_lengths<SHARED>(a, b, &row0, &n, &m, &skip);
       chunk_extent<SHARED>(a, n, m, skip, &rt, &kt);
-      k = max(1, kt / L);
+      k = max(1, static_cast<int>((kt + (whole ? static_cast<int64_t>(L / 2) : 0)) / L));
     }
     const int64_t mine = static_cast<int64_t>(rt) * a.Hkv * k;
     const int64_t rows = k > 1 ? static_cast<int64_t>(n) * Hq : 0;

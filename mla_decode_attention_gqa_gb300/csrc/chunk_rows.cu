@@ -114,6 +114,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     for (int s = 0; s < NSTAGE; ++s) mbar_init(&empty[s], C::WM);
     fence_mbar_init();
   }
+  // a pass of a shared prefix: the groups' arrays are there, and the pass before has left the workspace
+  if constexpr (C::SHARED) asm volatile("griddepcontrol.wait;" ::: "memory");
   using Runs = ChunkRuns<C::SHARED>;
   Runs runs;  // (synchronises the block)
   if (!chunk_find_runs<C::THREADS, C::SHARED>(p.ck, gridDim.x, blockIdx.x, &runs)) return;
@@ -342,25 +344,34 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 #pragma unroll
           for (int i = 0; i < 4; ++i) qv[i] = qfrag[(4 * c2 + i) * 32 + lane];
 #pragma unroll
-          for (int np = 0; np < TN / 16; ++np) {
-            uint32_t w[2][2];  // [8 tokens][chunk]
-            ldsm_x4(kbase + tile4_off(16 * np + (mi >> 1) * 8 + (lane & 7), (2 * c2 + (mi & 1)) * 16), w[0][0], w[0][1], w[1][0],
-                    w[1][1]);
+          for (int np = 0; np < TN / 16; np += 2) {
+            uint32_t w[4][2];  // [8 tokens][chunk]
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t sb = *reinterpret_cast<const uint32_t*>(ksb + (16 * np + 8 * h) * (D / kFp4Block) + 4 * c2);
-              uint32_t by, unused;  // the scales of the two chunks' blocks
-              e4m3x4_to_f16x2x2(prmt(sb, 0u, (tq >> 1) ? 0x4431u : 0x4420u), by, unused);
+            for (int h = 0; h < 4; h += 2)
+              ldsm_x4(kbase + tile4_off(16 * np + (h + (mi >> 1)) * 8 + (lane & 7), (2 * c2 + (mi & 1)) * 16), w[h][0], w[h][1],
+                      w[h + 1][0], w[h + 1][1]);
+            uint32_t by[4];  // the scales of the two chunks' blocks
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                const uint32_t b = prmt(by, 0u, c ? 0x3232u : 0x1010u);
-                uint32_t k0, k1, k2, k3;
-                e2m1x8_to_f16x2x4(w[h][c], k0, k1, k2, k3);
-                const uint32_t qa0[4] = {qv[2 * c].x, qv[2 * c].y, qv[2 * c].z, qv[2 * c].w};
-                const uint32_t qa1[4] = {qv[2 * c + 1].x, qv[2 * c + 1].y, qv[2 * c + 1].z, qv[2 * c + 1].w};
-                mma_f16(sc[2 * np + h], qa0, mul_f16x2(k0, b), mul_f16x2(k1, b));
-                mma_f16(sc[2 * np + h], qa1, mul_f16x2(k2, b), mul_f16x2(k3, b));
+            for (int h = 0; h < 4; ++h)
+              by[h] = e4m3x2_low_to_f16x2(prmt(
+                  *reinterpret_cast<const uint32_t*>(ksb + (16 * np + 8 * h) * (D / kFp4Block) + 4 * c2), 0u, (tq >> 1) ? 0x31u : 0x20u));
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t qa0[4] = {qv[2 * c].x, qv[2 * c].y, qv[2 * c].z, qv[2 * c].w};
+              const uint32_t qa1[4] = {qv[2 * c + 1].x, qv[2 * c + 1].y, qv[2 * c + 1].z, qv[2 * c + 1].w};
+              uint32_t k[4][4];
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {
+                const uint32_t b = prmt(by[h], 0u, c ? 0x3232u : 0x1010u);
+                e2m1x8_to_f16x2x4(w[h][c], k[h][0], k[h][1], k[h][2], k[h][3]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) k[h][j] = mul_f16x2(k[h][j], b);
               }
+              // (four independent products between two into the same scores)
+#pragma unroll
+              for (int h = 0; h < 4; ++h) mma_f16(sc[2 * np + h], qa0, k[h][0], k[h][1]);
+#pragma unroll
+              for (int h = 0; h < 4; ++h) mma_f16(sc[2 * np + h], qa1, k[h][2], k[h][3]);
             }
           }
         }
@@ -404,6 +415,16 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       auto in_item = [&](int tok) -> bool { return (tok >= r_lo && tok < r_hi) || tok < sinks; };
       float tmax[2] = {-INFINITY, -INFINITY};
       // an instantiation per mask mode: most tiles carry no test
+      // (4-bit: packed arithmetic, here and below)
+      auto scale_all = [&]() {
+#pragma unroll
+        for (int nt = 0; nt < TN / 8; ++nt) {
+          mul_pair(sc[nt][0], sc[nt][1], sl[0]);
+          mul_pair(sc[nt][2], sc[nt][3], sl[1]);
+          tmax[0] = fmax3(tmax[0], sc[nt][0], sc[nt][1]);
+          tmax[1] = fmax3(tmax[1], sc[nt][2], sc[nt][3]);
+        }
+      };
       auto scale_mask = [&](auto masked) {
 #pragma unroll
         for (int nt = 0; nt < TN / 8; ++nt) {
@@ -423,6 +444,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       };
       if (need_mask)
         scale_mask(std::true_type{});
+      else if constexpr (C::FP4)
+        scale_all();
       else
         scale_mask(std::false_type{});
       // (base: what scores are taken against)
@@ -516,8 +539,22 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         }
       }
       uint32_t pa[TN / 16][4];
+      if constexpr (C::FP4) {
+        uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-      for (int nt = 0; nt < TN / 8; ++nt) {
+        for (int nt = 0; nt < TN / 8; ++nt)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            add_pair(sc[nt][2 * r], sc[nt][2 * r + 1], -base[r]);
+            const float p0 = fast_exp2(sc[nt][2 * r]), p1 = fast_exp2(sc[nt][2 * r + 1]);
+            sum[r] = add_f32x2(sum[r], p0, p1);
+            pa[nt >> 1][(nt & 1) * 2 + r] = pack_f16(p0, p1);
+          }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) lrun[r] += sum_f32x2(sum[r]);
+      }
+#pragma unroll
+      for (int nt = 0; nt < (C::FP4 ? 0 : TN / 8); ++nt) {
         const float p0 = fast_exp2(sc[nt][0] - base[0]);
         const float p1 = fast_exp2(sc[nt][1] - base[0]);
         const float p2 = fast_exp2(sc[nt][2] - base[1]);
@@ -528,9 +565,6 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         if constexpr (!C::CODES) {
           pa[kk][hf + 0] = pack_bf16(p0, p1);
           pa[kk][hf + 1] = pack_bf16(p2, p3);
-        } else if constexpr (C::FP4) {
-          pa[kk][hf + 0] = pack_f16(p0, p1);
-          pa[kk][hf + 1] = pack_f16(p2, p3);
         } else {
           pa[kk][hf + 0] = pack_f16(p0 * vs[0], p1 * vs[0]);
           pa[kk][hf + 1] = pack_f16(p2 * vs[1], p3 * vs[1]);
@@ -575,11 +609,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
               e4m3x4_to_f16x2x2(prmt(sb.y, sb.w, sel), sv[1][2], sv[1][3]);
             }
             auto pairs = [](uint32_t w, uint32_t* f) {  // dims 0, 1, 2, 3 of both tokens
-              // (the low halves: in a byte one token's nibble under the other's)
-              const uint32_t even = (w & 0x0F0F0F0Fu) | ((w >> 12) & 0xF0F0F0F0u);        // dims 0 and 2
-              const uint32_t odd = ((w >> 4) & 0x0F0F0F0Fu) | ((w >> 16) & 0xF0F0F0F0u);  // dims 1 and 3
-              e2m1x4_to_f16x2x2(even, f[0], f[2]);
-              e2m1x4_to_f16x2x2(odd, f[1], f[3]);
+              // one token's nibble under the other's: dims 0 and 2 in the low half, 1 and 3 in the high one
+              const uint32_t moved = prmt(w >> 12, w << 12, 0x7610u);
+              e2m1x8_to_f16x2x4((w & 0xF0F00F0Fu) | (moved & 0x0F0FF0F0u), f[0], f[2], f[1], f[3]);
             };
             uint32_t w[2][2];  // [chunk & 1][8 tokens]
 #pragma unroll
@@ -780,6 +812,19 @@ cudaError_t launch_cfg(const PartialParams& p, const ChunkMaps& maps, cudaStream
     return cudaFuncSetAttribute(chunk_rows_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   });
   if (e0 != cudaSuccess) return e0;
+  if constexpr (C::SHARED) {  // a programmatic dependent of the kernel before, which it waits for
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned int>(p.ck.n_wave));
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, chunk_rows_kernel<C>, p, maps);
+  }
   chunk_rows_kernel<C><<<static_cast<unsigned int>(p.ck.n_wave), C::THREADS, C::SMEM, stream>>>(p, maps);
   return cudaGetLastError();
 }

@@ -173,14 +173,6 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t at) {
   return u;
 }
 
-// (x0, x1) * s for a pair in one packed instruction.
-__device__ __forceinline__ void mul_pair(float& x0, float& x1, float s) {
-  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\tmul.rn.f32x2 a, a, b;\n\t"
-      "mov.b64 {%0, %1}, a;\n\t}"
-      : "+f"(x0), "+f"(x1)
-      : "f"(s));
-}
-
 // An edge tile: the scores that this thread's row does not see (row: its end, the start of its
 // window, the end of its sinks) become out0 (first half) or out1 in tensor memory, so that
 // the passes over the scores carry no test.  hi_min, lo_max, sink_min: columns that the whole warp

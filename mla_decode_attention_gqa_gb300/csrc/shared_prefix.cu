@@ -22,6 +22,7 @@ namespace {
 constexpr int kThreads = 256;
 
 __global__ void __launch_bounds__(kThreads) shared_groups_kernel(const __grid_constant__ SharedArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // (the next kernel sets itself up meanwhile)
   __shared__ int sm_len[kThreads / 32], sm_first[kThreads / 32];
   const int j = blockIdx.x;
   auto bound = [&](int i) { return min(max(__ldg(a.cu_groups + i), 0), a.B); };

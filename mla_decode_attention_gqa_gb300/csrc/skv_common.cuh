@@ -181,16 +181,6 @@ __device__ __forceinline__ void e2m1x8_to_f16x2x4(uint32_t w, uint32_t& a, uint3
       : "r"(w));
 }
 
-// The codes of the low two bytes of w.
-__device__ __forceinline__ void e2m1x4_to_f16x2x2(uint32_t w, uint32_t& a, uint32_t& b) {
-  asm("{\n\t.reg .b8 p, q, r, s;\n\t"
-      "mov.b32 {p, q, r, s}, %2;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, p;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, q;\n\t}"
-      : "=r"(a), "=r"(b)
-      : "r"(w));
-}
-
 // Eight values as e2m1 codes (value j in nibble j): to the nearest, ties to even, +-6 at most.
 __device__ __forceinline__ uint32_t f32x8_to_e2m1x8(const float* x) {
   uint32_t w;
@@ -211,6 +201,13 @@ __device__ __forceinline__ float head_scale(const float* scales, int head) {
   if (!scales) return 1.f;
   const float s = __ldg(scales + head);
   return s >= 5.421010862e-20f && s <= 1.844674407e19f ? s : 0.f;
+}
+
+// Two e4m3 codes in the low half of w -> an fp16 pair.
+__device__ __forceinline__ uint32_t e4m3x2_low_to_f16x2(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
+  return r;
 }
 
 // Byte permute: result byte i = byte sel_i of {b, a} (a = bytes 0..3).
@@ -297,6 +294,20 @@ __device__ __forceinline__ void fma_pair(float x0, float x1, float s, float c, f
   asm("mov.b64 %0, {%1, %1};" : "=l"(cv) : "f"(c));
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(sv), "l"(cv));
   asm("mov.b64 {%0, %1}, %2;" : "=f"(r0), "=f"(r1) : "l"(r));
+}
+// (x0, x1) * s for a pair in one packed instruction.
+__device__ __forceinline__ void mul_pair(float& x0, float& x1, float s) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\tmul.rn.f32x2 a, a, b;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(s));
+}
+// (x0, x1) + c, likewise.
+__device__ __forceinline__ void add_pair(float& x0, float& x1, float c) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\tadd.rn.f32x2 a, a, b;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(x0), "+f"(x1)
+      : "f"(c));
 }
 __device__ __forceinline__ float sum_f32x2(uint64_t acc) {
   float x, y;
