@@ -746,22 +746,42 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       }
       const bool f32 = !direct || (C::SHARED && p.ck.out_f32);
       float* out_f = C::SHARED && direct ? static_cast<float*>(p.ck.out) : p.out_o;
-      auto store2 = [&](int64_t row, int d, float y0, float y1, float prior) {
-        if (C::SHARED && prior != 0.f) {
-          const float2 x = __ldcg(reinterpret_cast<const float2*>(p.ck.prior_o + row * D + d));
-          y0 = fmaf(x.x, prior, y0), y1 = fmaf(x.y, prior, y1);
-        }
+      auto store2 = [&](int64_t row, int d, float y0, float y1) {
         if (f32)
           *reinterpret_cast<float2*>(out_f + row * D + d) = make_float2(y0, y1);
         else
           *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.ck.out) + row * D + d) = pack_bf16(y0, y1);
       };
       if constexpr (!C::CODES) {
+        if constexpr (C::SHARED) {  // (loads in batches ahead of the stores: one after the other took 15 us an item)
+#pragma unroll
+          for (int nt = 0; nt < D / 8; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nt][e] *= e < 2 ? inv0 : inv1;
+#pragma unroll
+          for (int n0 = 0; n0 < D / 8; n0 += 8) {
+            float2 x[8], y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int d = 8 * (n0 + i) + 2 * tq;
+              x[i] = y[i] = make_float2(0.f, 0.f);
+              if (prior0 != 0.f) x[i] = __ldcg(reinterpret_cast<const float2*>(p.ck.prior_o + row_a * D + d));
+              if (prior1 != 0.f) y[i] = __ldcg(reinterpret_cast<const float2*>(p.ck.prior_o + row_b * D + d));
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float* z = o[n0 + i];
+              z[0] = fmaf(x[i].x, prior0, z[0]), z[1] = fmaf(x[i].y, prior0, z[1]);
+              z[2] = fmaf(y[i].x, prior1, z[2]), z[3] = fmaf(y[i].y, prior1, z[3]);
+            }
+          }
+          inv0 = inv1 = 1.f;
+        }
 #pragma unroll
         for (int nt = 0; nt < D / 8; ++nt) {
           const int d = 8 * nt + 2 * tq;
-          if (w0) store2(row_a, d, o[nt][0] * inv0, o[nt][1] * inv0, prior0);
-          if (w1) store2(row_b, d, o[nt][2] * inv1, o[nt][3] * inv1, prior1);
+          if (w0) store2(row_a, d, o[nt][0] * inv0, o[nt][1] * inv0);
+          if (w1) store2(row_b, d, o[nt][2] * inv1, o[nt][3] * inv1);
         }
       } else {
         // O^T: this thread holds rows (8n + 2tq + {0,1}) at dv 16c + 2gq + {0,1}
@@ -774,12 +794,27 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             const float inv = __shfl_sync(0xffffffffu, n ? inv1 : inv0, src);
             const bool wr = __shfl_sync(0xffffffffu, (n ? w1 : w0) ? 1 : 0, src) != 0;
             const int64_t row = __shfl_sync(0xffffffffu, n ? row_b : row_a, src);
-            const float prior = __shfl_sync(0xffffffffu, n ? prior1 : prior0, src);
+            float2 x[D / 16];  // of the prefix, all loaded ahead of the stores
+            if constexpr (C::SHARED) {
+              const float prior = __shfl_sync(0xffffffffu, n ? prior1 : prior0, src);
+#pragma unroll
+              for (int c = 0; c < D / 16; ++c) {
+                const int d = C::FP4 ? 32 * (c >> 1) + 4 * gq + 2 * (c & 1) : 16 * c + 2 * gq;
+                x[c] = make_float2(0.f, 0.f);
+                if (prior != 0.f) x[c] = __ldcg(reinterpret_cast<const float2*>(p.ck.prior_o + row * D + d));
+              }
+#pragma unroll
+              for (int c = 0; c < D / 16; ++c) x[c] = make_float2(x[c].x * prior, x[c].y * prior);
+            }
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
               const float* ov = o[2 * c + n];
               const int d = C::FP4 ? 32 * (c >> 1) + 4 * gq + 2 * (c & 1) : 16 * c + 2 * gq;
-              if (wr) store2(row, d, ov[e] * inv, ov[2 + e] * inv, prior);
+              if (!wr) continue;
+              if constexpr (C::SHARED)
+                store2(row, d, fmaf(ov[e], inv, x[c].x), fmaf(ov[2 + e], inv, x[c].y));
+              else
+                store2(row, d, ov[e] * inv, ov[2 + e] * inv);
             }
           }
         }

@@ -818,6 +818,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
         return r;
       };
+      // A tile's codes on their way into L2: what a thread can hold in registers covers L2's latency, not
+      // the memory's
+      auto ahead = [&](int g, const Place& pl) {
+        if (pl.page < 0) return;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(p.codes[x] + pl.page * p.code_sb[x] + g * p.code_sh[x] + pl.at * p.code_st[x]));
+          if ((row & 3) == 0)  // 32 bytes of scales
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.block_scales[x] +
+                                                        ((pl.page * p.Hkv + g) * p.block_len + pl.at) * (D / kFp4Block)));
+        }
+      };
       // 8 codes at a time to 16 bytes of the 128-byte-swizzled tile (conflict-free: eight rows, eight chunks)
       auto convert = [&](const Row& r, uint8_t* to) {
         uint32_t sc[4];  // pairs of blocks
@@ -844,8 +856,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       for (int r = 0; ok && next_item(r, &t); ++r) {
         const int n = t.n_tiles, g = t.it.g;
         if (n == 0) continue;
-        Place pl = place_of(t, 0);
+        Place pl = place_of(t, 0), next = pl, after = pl;  // of tiles i, i + 1 and i + 2
         Row k = load(0, g, pl);
+        if (n > 1) ahead(g, next = place_of(t, 1));
         ok = wait_all(&bars->q_full, nq & 1, kDevErrFullWait);
         if (!ok) break;
         float* qs = reinterpret_cast<float*>(smem + C::OFF_QS) + (nq & 1) * 2 * kRowsTile;
@@ -857,15 +870,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           const int s = done % NST;
           const uint32_t parity = ((done / NST) - 1) & 1;
           const Row v = load(1, g, pl);  // under K's conversion
+          if (i + 2 < n) after = place_of(t, i + 2);
           ok = done < NST || wait_all(&bars->k_empty[s], parity, kDevErrEmptyWait);
           if (!ok) break;
           convert(k, smem + C::OFF_K + s * C::TILE);
           fence_proxy_async_smem();
           mbar_arrive(&bars->k_full[s]);
-          if (i + 1 < n) {  // the next tile's K under V's
-            pl = place_of(t, i + 1);
-            k = load(0, g, pl);
-          }
+          pl = next;
+          next = after;
+          if (i + 1 < n) k = load(0, g, pl);  // under V's
+          if (i + 2 < n) ahead(g, next);
           ok = done < NST || wait_all(&bars->v_empty[s], parity, kDevErrEmptyWait);
           if (!ok) break;
           convert(v, smem + C::OFF_V + s * C::TILE);
