@@ -785,20 +785,21 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
         return finite ? __uint_as_float(static_cast<uint32_t>(127 + e) << 23) : __int_as_float(0x7fc00000);
       };
-      // Where this thread's token of tile i lies: its row of the pages' rows (page < 0: zeros)
+      // Where this thread's token of tile i lies.  (The table's entry is not looked at before it is used, a
+      // tile or two later: a look here would wait for it)
       struct Place {
-        int64_t page;
-        int at;
+        int page, at;
+        __device__ __forceinline__ bool in(const PartialParams& p) const { return page >= 0 && page < p.num_blocks; }
       };
-      auto place_of = [&](const TcItem& t, int i) -> Place {
+      auto place_of = [&](const TcItem& t, int table_row, int i) -> Place {
         const int first = t.token(2 * i), second = t.token(2 * i + 1);
         // a second half at or past the capacity holds no token: it takes the first one's page instead of
         // an entry behind the table's row
         const int tok = row < kHalf || second >= p.ck.cap ? first : second;
+        const int block = tok / p.block_len;
         Place pl;
-        pl.page = chunk_page_of<C::SHARED>(p, t.it.b, tok);
-        pl.at = tok % p.block_len + (row & (kHalf - 1));
-        if (pl.page >= p.num_blocks) pl.page = -1;
+        pl.page = __ldg(p.block_table + static_cast<int64_t>(table_row) * p.max_blocks + block);
+        pl.at = tok - block * p.block_len + (row & (kHalf - 1));
         return pl;
       };
       struct Row {
@@ -810,24 +811,26 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j) r.codes[j] = make_uint4(0u, 0u, 0u, 0u);
         r.scales = make_uint2(0u, 0u);
-        if (pl.page >= 0) {
+        if (pl.in(p)) {
           const uint4* from = reinterpret_cast<const uint4*>(p.codes[x] + pl.page * p.code_sb[x] + g * p.code_sh[x] + pl.at * p.code_st[x]);
 #pragma unroll
           for (int j = 0; j < 4; ++j) r.codes[j] = __ldg(from + j);
-          r.scales = __ldg(reinterpret_cast<const uint2*>(p.block_scales[x]) + (pl.page * p.Hkv + g) * p.block_len + pl.at);
+          r.scales = __ldg(reinterpret_cast<const uint2*>(p.block_scales[x]) +
+                           (static_cast<int64_t>(pl.page) * p.Hkv + g) * p.block_len + pl.at);
         }
         return r;
       };
       // A tile's codes on their way into L2: what a thread can hold in registers covers L2's latency, not
       // the memory's
       auto ahead = [&](int g, const Place& pl) {
-        if (pl.page < 0) return;
+        if (!pl.in(p)) return;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           asm volatile("prefetch.global.L2 [%0];" ::"l"(p.codes[x] + pl.page * p.code_sb[x] + g * p.code_sh[x] + pl.at * p.code_st[x]));
           if ((row & 3) == 0)  // 32 bytes of scales
             asm volatile("prefetch.global.L2 [%0];" ::"l"(p.block_scales[x] +
-                                                        ((pl.page * p.Hkv + g) * p.block_len + pl.at) * (D / kFp4Block)));
+                                                        ((static_cast<int64_t>(pl.page) * p.Hkv + g) * p.block_len + pl.at) *
+                                                            (D / kFp4Block)));
         }
       };
       // 8 codes at a time to 16 bytes of the 128-byte-swizzled tile (conflict-free: eight rows, eight chunks)
@@ -856,9 +859,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       for (int r = 0; ok && next_item(r, &t); ++r) {
         const int n = t.n_tiles, g = t.it.g;
         if (n == 0) continue;
-        Place pl = place_of(t, 0), next = pl, after = pl;  // of tiles i, i + 1 and i + 2
+        const int table_row = C::SHARED && p.ck.table_row ? __ldcg(p.ck.table_row + t.it.b) : t.it.b;
+        Place pl = place_of(t, table_row, 0), next = pl, after = pl;  // of tiles i, i + 1 and i + 2
+        if (n > 1) next = place_of(t, table_row, 1);
         Row k = load(0, g, pl);
-        if (n > 1) ahead(g, next = place_of(t, 1));
+        if (n > 1) ahead(g, next);
         ok = wait_all(&bars->q_full, nq & 1, kDevErrFullWait);
         if (!ok) break;
         float* qs = reinterpret_cast<float*>(smem + C::OFF_QS) + (nq & 1) * 2 * kRowsTile;
@@ -870,7 +875,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           const int s = done % NST;
           const uint32_t parity = ((done / NST) - 1) & 1;
           const Row v = load(1, g, pl);  // under K's conversion
-          if (i + 2 < n) after = place_of(t, i + 2);
+          if (i + 2 < n) after = place_of(t, table_row, i + 2);
           ok = done < NST || wait_all(&bars->k_empty[s], parity, kDevErrEmptyWait);
           if (!ok) break;
           convert(k, smem + C::OFF_K + s * C::TILE);
