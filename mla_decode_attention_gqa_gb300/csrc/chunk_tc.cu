@@ -322,6 +322,58 @@ __device__ __noinline__ void store_rows(uint32_t o_col, bool has0, bool has1, fl
     }
     __syncwarp();
   };
+  if constexpr (SHARED) {
+    if (prior_o != nullptr) {
+      // the rows go through shared memory in fp32, 16 columns at a time, so that the prefix's rows are read as
+      // the output's are written, 8 rows x 64 bytes an instruction, and a step ahead (read by each row's own
+      // lane, 16 bytes of 32 rows at once, they took half of the epilogue)
+      const float* from[4];
+      float weight[4];
+      float4 next[4];
+      bool mine[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2);
+        from[i] = prior_o + __shfl_sync(0xffffffffu, orow, r) * D + (lane & 3) * 4;
+        weight[i] = __shfl_sync(0xffffffffu, prior, r);
+        mine[i] = ((write >> r) & 1u) && weight[i] != 0.f;
+        next[i] = mine[i] ? __ldcg(reinterpret_cast<const float4*>(from[i])) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll 1
+      for (int c = 0; c < D; c += 16) {
+        uint32_t x[16], y[16];
+        if (has0) tc::tmem_ld16(o_col + c, x);
+        if (has1) tc::tmem_ld16(o_col + 128 + c, y);
+        float4 cur[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          cur[i] = next[i];
+          if (mine[i] && c + 16 < D) next[i] = __ldcg(reinterpret_cast<const float4*>(from[i] + c + 16));
+        }
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float v = some0 ? __uint_as_float(x[e]) * w0 : 0.f;
+          if (has1 && some1) v = fmaf(__uint_as_float(y[e]), w1, v);
+          x[e] = __float_as_uint(v);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) st_shared_v4(at_w + ((q ^ swz_w) << 4), x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 u = ld_shared_v4(at_r + 512 * i);
+          uint2 z;
+          z.x = pack_bf16(fmaf(cur[i].x, weight[i], __uint_as_float(u.x)), fmaf(cur[i].y, weight[i], __uint_as_float(u.y)));
+          z.y = pack_bf16(fmaf(cur[i].z, weight[i], __uint_as_float(u.z)), fmaf(cur[i].w, weight[i], __uint_as_float(u.w)));
+          if ((write >> (8 * i + (lane >> 2))) & 1u)
+            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(out) + (from[i] - prior_o + c) * 2) = z;
+        }
+        __syncwarp();
+      }
+      return;
+    }
+  }
 #pragma unroll 1
   for (int c = 0; c < D; c += 32) {
     uint32_t x[2][16], w[16];
@@ -345,17 +397,6 @@ __device__ __noinline__ void store_rows(uint32_t o_col, bool has0, bool has1, fl
 #pragma unroll
       for (int e = 0; e < 32; ++e)
         x[e >> 4][e & 15] = some0 ? __float_as_uint(__uint_as_float(x[e >> 4][e & 15]) * w0) : 0u;
-    }
-    if (SHARED && prior_o != nullptr && prior != 0.f) {
-#pragma unroll
-      for (int e = 0; e < 32; e += 4) {
-        const float4 u = __ldcg(reinterpret_cast<const float4*>(prior_o + orow * D + c + e));
-        uint32_t* y = &x[e >> 4][e & 15];
-        y[0] = __float_as_uint(fmaf(u.x, prior, __uint_as_float(y[0])));
-        y[1] = __float_as_uint(fmaf(u.y, prior, __uint_as_float(y[1])));
-        y[2] = __float_as_uint(fmaf(u.z, prior, __uint_as_float(y[2])));
-        y[3] = __float_as_uint(fmaf(u.w, prior, __uint_as_float(y[3])));
-      }
     }
     if (bf16) {
 #pragma unroll

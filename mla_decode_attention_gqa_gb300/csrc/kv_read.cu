@@ -21,7 +21,7 @@ namespace skv {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 64;
 constexpr int kAhead = 4;  // rows that a lane loads before it stores the first
 
 // Where a packed row comes from.
