@@ -1128,8 +1128,9 @@ struct ChunkPlan {
   size_t plan_bytes = 0, o_bytes = 0, lse_bytes = 0;
 };
 
-// T packed rows of B sequences, of at most `longest` each (0: T).
-skv_status chunk_plan(const skv_desc* d, int32_t B, int32_t T, int32_t longest_or_0, ChunkPlan* pl) {
+// T packed rows of B sequences, of at most `longest` each (0: T); waves: of items of sequences that are cut,
+// tensor cores only.
+skv_status chunk_plan(const skv_desc* d, int32_t B, int32_t T, int32_t longest_or_0, ChunkPlan* pl, int waves = 4) {
   const int G = d->Hq / d->Hkv;
   // The caller's bound on the chunk lengths chooses the kernel (results do not depend on it): up
   // to 16 rows of a KV head fill an mma.sync tile, where the tensor cores' 128 are mostly padding
@@ -1142,7 +1143,7 @@ skv_status chunk_plan(const skv_desc* d, int32_t B, int32_t T, int32_t longest_o
   pl->rows = pl->tc ? chunk_tc_rows() : longest * G <= 16 ? 16 : 32;
   pl->tile = pl->tc ? chunk_tc_kv_tile() : kTileN;
   pl->n_wave = static_cast<int64_t>(device_sm_count()) * (pl->tc ? 1 : chunk_rows_ctas_per_sm(pl->rows));
-  pl->n_target = 4 * pl->n_wave;
+  pl->n_target = waves * pl->n_wave;
   const int64_t rows = static_cast<int64_t>(T) * pl->group_rows;
   if (rows + pl->rows >= (int64_t(1) << 31)) return fail(SKV_EINVAL, "T * Hq / Hkv is too large for one call");
   const int64_t row_tiles = rows / pl->rows + std::min(B, T);  // each sequence's last one may be short
@@ -1274,25 +1275,24 @@ skv_status chunk_attention(const skv_chunk_desc* desc, const skv_paged* paged, b
 }
 
 // The two passes of a shared prefix and their workspace: the groups' arrays, the prefixes' fp32 result,
-// and one pass's own, which the second takes over from the first.
+// and each pass's own (the second begins under the end of the first).
 struct SharedPlan {
   ChunkPlan prefix, rest;
-  size_t groups = 0, o = 0, lse = 0, pass = 0;
-  size_t bytes() const { return groups + o + lse + pass; }
+  size_t groups = 0, o = 0, lse = 0;
+  size_t bytes() const { return groups + o + lse + chunk_ws_bytes(prefix) + chunk_ws_bytes(rest); }
 };
 
 skv_status shared_plan(const skv_chunk_desc* c, const skv_shared_desc* sh, const skv_desc* d, SharedPlan* pl) {
   if (!sh) return fail(SKV_EINVAL, "shared is NULL");
   if (c->window != 0 || c->n_sink != 0) return fail(SKV_EINVAL, "a shared prefix goes without window and n_sink");
   if (sh->n_groups < 1) return fail(SKV_EINVAL, "n_groups must be positive");
-  skv_status st = chunk_plan(d, sh->n_groups, c->T, sh->max_group_rows, &pl->prefix);
+  skv_status st = chunk_plan(d, sh->n_groups, c->T, sh->max_group_rows, &pl->prefix, 2);  // (4 / 3 waves at most)
   if (st != SKV_OK) return st;
   if ((st = chunk_plan(d, c->B, c->T, c->max_q_len, &pl->rest)) != SKV_OK) return st;
   pl->groups = align_up((3 * static_cast<size_t>(sh->n_groups) + 1 + c->B) * 4, 256);
   const size_t rows = static_cast<size_t>(c->T) * c->Hq;
   pl->o = align_up(rows * d->dv * 4, 256);
   pl->lse = align_up(rows * 4, 256);
-  pl->pass = std::max(chunk_ws_bytes(pl->prefix), chunk_ws_bytes(pl->rest));
   return SKV_OK;
 }
 
@@ -1392,6 +1392,7 @@ skv_status attn_shared_prefix_paged(const skv_chunk_desc* desc, const skv_paged*
   first.ck.lse = prior_lse;
   first.ck.out_f32 = 1;
   if ((st = chunk_pass(d, pl.prefix, first, &maps, pass_ws, s)) != SKV_OK) return st;
+  pass_ws += chunk_ws_bytes(pl.prefix);
   p.ck.skip = g.skip;
   p.ck.prior_o = prior_o;
   p.ck.prior_lse = prior_lse;

@@ -147,6 +147,8 @@ __global__ void __launch_bounds__(32 * kRowsPerBlock)
   __shared__ int sm_parts[kRowsPerBlock], sm_n[kRowsPerBlock], sm_skip[kRowsPerBlock];
   __shared__ int64_t sm_row[kRowsPerBlock], sm_part[kRowsPerBlock];
   __shared__ BlockJoin<D> sm_join;
+  // (the second pass of a shared prefix may start)
+  if constexpr (SHARED) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // the attention kernel before it on the stream is complete and its writes are visible
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -204,6 +206,8 @@ template <int D, bool SHARED>
 __global__ void __launch_bounds__(32 * kRowsPerBlock)
     chunk_runs_merge_kernel(const __grid_constant__ ChunkArgs a, const float* part_o, const float* part_lse) {
   __shared__ BlockJoin<D> sm_join;
+  // (the second pass of a shared prefix may start)
+  if constexpr (SHARED) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int c = blockIdx.x + 1;
   ChunkRuns<SHARED> runs;
   ChunkShare sh;

@@ -114,11 +114,20 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     for (int s = 0; s < NSTAGE; ++s) mbar_init(&empty[s], C::WM);
     fence_mbar_init();
   }
-  // a pass of a shared prefix: the groups' arrays are there, and the pass before has left the workspace
-  if constexpr (C::SHARED) asm volatile("griddepcontrol.wait;" ::: "memory");
+  // The second pass of a shared prefix starts under the end of the first (its merge), whose result it reads
+  // at the end of an item only; the groups' arrays were complete before the first pass's attention
+  // kernel began.  Every thread waits before it leaves, so that what comes after this grid may rely on the first
+  // pass as well.
+  auto first_pass_done = [&]() {
+    if constexpr (C::SHARED) asm volatile("griddepcontrol.wait;" ::: "memory");
+  };
+  if (C::SHARED && p.ck.whole) first_pass_done();  // (the first pass itself: the groups' arrays)
   using Runs = ChunkRuns<C::SHARED>;
   Runs runs;  // (synchronises the block)
-  if (!chunk_find_runs<C::THREADS, C::SHARED>(p.ck, gridDim.x, blockIdx.x, &runs)) return;
+  if (!chunk_find_runs<C::THREADS, C::SHARED>(p.ck, gridDim.x, blockIdx.x, &runs)) {
+    first_pass_done();
+    return;
+  }
 
   if (warp == C::WM * WN) {
     // ------------------------------------------------------------ producer warp
@@ -170,6 +179,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     // every issued copy lands before the CTA may exit
     for (int y = max(0, x - NSTAGE); y < x; ++y)
       if (!mbar_wait(&full[full_slot<C>(y)], full_parity<C>(y), p.err, kDevErrDrainWait)) break;
+    first_pass_done();
     return;
   }
 
@@ -735,6 +745,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       float lse1 = some1 ? (M[1] + (__log2f(L[1]) - kUp)) * kLn2 : -INFINITY;
       float prior0 = 0.f, prior1 = 0.f;  // weights of the prefix's result
       if (C::SHARED && direct && pc.skip > 0) {
+        first_pass_done();
         if (v0) {
           const ChunkJoin j = chunk_join(lse0, __ldcg(p.ck.prior_lse + row_a));
           inv0 *= j.own, prior0 = j.prior, lse0 = j.lse;
@@ -827,6 +838,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     }
     // (the next piece writes ml and obuf behind a sync that the first warp reaches after this)
   }
+  first_pass_done();
 }
 
 // (two sets with bf16 heads of 128: 5 warps a set have 168 registers each, too few: 95 us for 24
