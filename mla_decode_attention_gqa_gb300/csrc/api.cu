@@ -1211,7 +1211,7 @@ skv_status chunk_pass(const skv_desc& d, const ChunkPlan& pl, PartialParams p, C
   p.ck.n_wave = static_cast<int32_t>(pl.n_wave);
   p.ck.n_target = static_cast<int32_t>(pl.n_target);
   // (with one KV tile at most no item is ever cut, and nothing merged)
-  p.ck.start = d.S_max <= pl.tile ? 0 : kChunkStart * (d.dk == 64 || pages != kPagesBf16 ? 2 : 1);
+  p.ck.start = d.S_max <= pl.tile ? 0 : (p.ck.skip ? kChunkStartBehind : kChunkStart) * (d.dk == 64 || pages != kPagesBf16 ? 2 : 1);
   p.ck.plan = reinterpret_cast<int32_t*>(ws);
   if (pl.tc) {
     skv_desc dq = d;  // the packed rows as the query rows of one sequence

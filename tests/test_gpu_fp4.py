@@ -250,6 +250,59 @@ def test_attention_flat_after_a_spike():
         R.check_attention(c["dense"], out, lse, scale=scale)
 
 
+@pytest.mark.parametrize("max_q_len", [1, 2, None])
+@pytest.mark.parametrize("step", [0.02, 0.5])
+def test_attention_scores_that_rise(max_q_len, step):
+    """Scores that grow from token to token, slowly or by more than fp16's range within a tile: the maximum
+    moves in every tile."""
+    n = 700
+    c = F.make_case("fp4", (1, 1), (n, 300), 8, 2, 128, seed=15, device=DEV)
+    q = torch.zeros(2, 8, 128)
+    q[..., 0] = 1.0
+    q[..., 16] = 1.0
+    c["q"] = q.bfloat16().to(DEV)
+    # dim 0: code 1.0 times a scale, so that the score is the token's scale: the nearest e4m3 of step * t
+    c["k_pages"].zero_()
+    c["k_pages"][..., 0] = 2
+    s = torch.zeros(c["k_scale"].shape)
+    for b, m in enumerate((n, 300)):
+        t = torch.arange(m)
+        s[c["block_table"][b].cpu().long()[t // 64], :, t % 64, 0] = (step * t)[:, None].float()
+    c["k_scale"] = s.to(torch.float8_e4m3fn).to(DEV)
+    c["k_head_scale"] = None
+    F.with_dense(c)
+    out, lse = skv.attn_chunk_paged(c["q"], c["k_pages"], c["v_pages"], c["seq_lens"], c["cu_q"], c["block_table"],
+                                    max_q_len=max_q_len, softmax_scale=1.0, **F.pages_of(c))
+    ro, rl, size = R.attend(c["dense"], scale=1.0)
+    # scores up to 448 in base 2 up to 2^10: each off by 2^-23 of that at most, and so a weight by 2^-13
+    assert ((lse.cpu().double() - rl).abs() <= 2.0 ** -22 * rl.abs() + 2.5e-4).all()
+    assert ((out.cpu().double() - ro).abs() <= 2.0 ** -8 * (ro.abs() + size) + 2.0 ** -11 * size).all()
+
+
+@pytest.mark.parametrize("n", [1, 5, 20])
+def test_attention_cut_in_chunks(n):
+    """Few rows over many tokens: on the tensor cores every row's tokens are dealt to several items."""
+    c = F.make_case("fp4", (n, 3), (20000, 9000), 16, 2, 128, block_len=128, seed=16, device=DEV)
+    for max_q_len in (n, None):
+        out, lse = skv.attn_chunk_paged(c["q"], c["k_pages"], c["v_pages"], c["seq_lens"], c["cu_q"], c["block_table"],
+                                        max_q_len=max(max_q_len, 3) if max_q_len else None, **F.pages_of(c))
+        R.check_attention(c["dense"], out, lse)
+
+
+def test_queries_with_infinities_spoil_their_rows_only():
+    c = F.make_case("fp4", (4,), (300,), 8, 2, 128, seed=17, device=DEV)
+    want, _ = skv.attn_chunk_paged(c["q"], c["k_pages"], c["v_pages"], c["seq_lens"], c["cu_q"], c["block_table"], **F.pages_of(c))
+    c["q"][1, 3, 7] = math.inf
+    c["q"][2, 0, 100] = math.nan
+    for max_q_len in (4, None):
+        out, lse = skv.attn_chunk_paged(c["q"], c["k_pages"], c["v_pages"], c["seq_lens"], c["cu_q"], c["block_table"],
+                                        max_q_len=max_q_len, **F.pages_of(c))
+        bad = torch.zeros(4, 8, dtype=torch.bool, device=DEV)
+        bad[1, 3] = bad[2, 0] = True
+        assert torch.equal(torch.isnan(out).all(-1), bad) and torch.equal(torch.isnan(lse), bad)
+        assert ((out.float() - want.float())[~bad].abs() <= 2.0 ** -7 * want.float()[~bad].abs() + 2.0 ** -7).all()
+
+
 def test_strided_pages_and_float4_dtype():
     """Pages as every other token row, page and head of a larger buffer; codes as float4_e2m1fn_x2."""
     c = F.make_case("fp4", (1, 2), (300, 130), 8, 2, 128, seed=11, device=DEV)
