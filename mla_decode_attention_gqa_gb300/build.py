@@ -20,7 +20,8 @@ BUILD_DIR = os.path.join(HERE, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "gqa_partial.cu", "mla_partial.cu", "merge_lse.cu", "umma_selftest.cu", "attn_tc.cu", "mla_tc.cu",
            "chunk_tc.cu", "chunk_rows.cu", "chunk_merge.cu", "qk_norm_rope.cu", "kv_read.cu",
-           "shared_prefix.cu", "chunk_tc_shared.cu", "chunk_rows_shared.cu"]
+           "shared_prefix.cu", "chunk_tc_shared.cu", "chunk_rows_shared.cu",
+           "chunk_rows4.cu"]
 
 
 def _nvcc():

@@ -1140,9 +1140,11 @@ skv_status chunk_plan(const skv_desc* d, int32_t B, int32_t T, int32_t longest_o
   const int64_t longest = longest_or_0 > 0 ? std::min(longest_or_0, T) : T;
   pl->tc = longest * G > 32 && G <= 128;
   pl->group_rows = pl->tc ? padded_group(G) : G;
-  pl->rows = pl->tc ? chunk_tc_rows() : longest * G <= 16 ? 16 : 32;
+  // (4-bit pages: up to 8 rows have a kernel whose products take 8 columns)
+  const bool few4 = page_format(d) == kPagesFp4 && longest * G <= chunk_rows4_rows();
+  pl->rows = pl->tc ? chunk_tc_rows() : few4 ? chunk_rows4_rows() : longest * G <= 16 ? 16 : 32;
   pl->tile = pl->tc ? chunk_tc_kv_tile() : kTileN;
-  pl->n_wave = static_cast<int64_t>(device_sm_count()) * (pl->tc ? 1 : chunk_rows_ctas_per_sm(pl->rows));
+  pl->n_wave = static_cast<int64_t>(device_sm_count()) * (pl->tc ? 1 : few4 ? chunk_rows4_ctas_per_sm() : chunk_rows_ctas_per_sm(pl->rows));
   pl->n_target = waves * pl->n_wave;
   const int64_t rows = static_cast<int64_t>(T) * pl->group_rows;
   if (rows + pl->rows >= (int64_t(1) << 31)) return fail(SKV_EINVAL, "T * Hq / Hkv is too large for one call");
@@ -1224,7 +1226,9 @@ skv_status chunk_pass(const skv_desc& d, const ChunkPlan& pl, PartialParams p, C
   if (pl.tc) e = launch_chunk_plan(p.ck, s);
   if (e == cudaSuccess) e = timing_mark(false, s);
   if (e == cudaSuccess)
-    e = pl.tc ? launch_chunk_tc(p, d.dk, pages, *maps, pl.n_items, s) : launch_chunk_rows(p, d.dk, pages, *maps, s);
+    e = pl.tc                               ? launch_chunk_tc(p, d.dk, pages, *maps, pl.n_items, s)
+        : pl.rows == chunk_rows4_rows() ? launch_chunk_rows4(p, *maps, s)
+                                            : launch_chunk_rows(p, d.dk, pages, *maps, s);
   if (e == cudaSuccess) e = timing_mark(true, s);
   if (e != cudaSuccess) return cuda_fail(e, "chunk attention launch");
   if (d.S_max <= pl.tile) return SKV_OK;  // one KV tile at most: never several chunks

@@ -195,6 +195,10 @@ cudaError_t launch_chunk_rows(const PartialParams& p, int32_t d, PageFormat page
                               cudaStream_t stream);
 cudaError_t launch_chunk_rows_shared(const PartialParams& p, int32_t d, PageFormat pages, const ChunkMaps& maps,
                                      cudaStream_t stream);
+// The same for up to 8 rows over 4-bit pages (see chunk_rows4.cu): row tiles of 8.
+int chunk_rows4_rows();
+int chunk_rows4_ctas_per_sm();
+cudaError_t launch_chunk_rows4(const PartialParams& p, const ChunkMaps& maps, cudaStream_t stream);
 cudaError_t launch_chunk_runs_merge(const ChunkArgs& a, int32_t d, const float* part_o, const float* part_lse,
                                     cudaStream_t stream);
 // On the tensor cores (see chunk_tc.cu), any G <= 128; maps.q: q as (dim, head, packed

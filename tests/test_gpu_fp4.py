@@ -187,7 +187,29 @@ def test_attention_window(window, n_sink, max_q_len):
     R.check_attention(c["dense"], out, lse, window=window, n_sink=n_sink)
 
 
-@pytest.mark.parametrize("max_q_len", [3, 12, None])
+@pytest.mark.parametrize("window,n_sink", [(1, 0), (2, 1), (64, 4), (100, 70), (500, 1)])
+@pytest.mark.parametrize("Hq,Hkv,q_lens", [(8, 2, (2, 1, 2)), (8, 1, (1, 1, 1)), (3, 3, (8, 1, 7)), (6, 2, (2, 2, 0))])
+def test_attention_window_few_rows(window, n_sink, Hq, Hkv, q_lens):
+    """Up to 8 rows of a KV head."""
+    c = F.make_case("fp4", q_lens, (900, 70, 333), Hq, Hkv, 128, seed=14, device=DEV)
+    out, lse = skv.attn_chunk_paged(c["q"], c["k_pages"], c["v_pages"], c["seq_lens"], c["cu_q"], c["block_table"],
+                                    max_q_len=max(q_lens), window=window, n_sink=n_sink, **F.pages_of(c))
+    assert skv.device_error() == 0
+    R.check_attention(c["dense"], out, lse, window=window, n_sink=n_sink)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (5, 1), (8, 8), (64, 8)])
+def test_attention_few_rows_many_sequences(Hq, Hkv):
+    """More items than CTAs, some of them empty or of one token: runs that begin and end inside items."""
+    lens = [1 + (i * 977) % 1500 for i in range(60)] + [0, 1, 64]
+    q_lens = [1] * 60 + [0, 1, 1]
+    c = F.make_case("fp4", q_lens, lens, Hq, Hkv, 128, seed=18, device=DEV)
+    out, lse = skv.attn_chunk_paged(c["q"], c["k_pages"], c["v_pages"], c["seq_lens"], c["cu_q"], c["block_table"],
+                                    max_q_len=1, **F.pages_of(c))
+    R.check_attention(c["dense"], out, lse)
+
+
+@pytest.mark.parametrize("max_q_len", [2, 3, 12, None])
 def test_attention_unseen_and_missing_pages(max_q_len):
     """NaN scales behind the last token and in pages of nobody change nothing; entries outside the cache
     read as zeros."""
