@@ -529,8 +529,13 @@ typedef struct {
  * qk_norm_rope_append (the page strides, in bytes, are multiples of 16).
  *
  * attn_chunk_paged_fp4 -- attn_chunk_paged over 4-bit pages (attn_chunk_paged_workspace_size gives
- * its workspace).  Codes times block scales are exact in the products; the head scales multiply
- * scores and outputs in fp32.
+ * its workspace).  Codes times block scales are exact in the products, which run in fp16; the head
+ * scales multiply scores and outputs in fp32.  The softmax weights are rounded once, to fp16 (2^-11 of
+ * each) times a power of two: all bits of weights down to 2^-28 (more than 32 rows of a KV head:
+ * 2^-22) of the largest so far, something of those down to 2^-38 (2^-33).  Of q what lies below 2^-29 of its
+ * row's (token's and head's) largest magnitude may lose bits; a row of q with an infinity or a NaN
+ * gives a row of NaN.  max_q_len matters as for fp8 pages: up to 8 rows of a KV head (new tokens times the
+ * group's heads) have a kernel of their own, up to 32 another, more the tensor cores.
  */
 skv_status qk_norm_rope_append_fp4(const skv_append_desc* desc, const skv_paged* paged, const skv_fp4_scales* fp4,
                                    const void* q, const void* k, const void* v, const void* q_weight,

@@ -21,6 +21,11 @@
 // 404 us, in equal runs 374: the rate of a plain copy).
 // A run may begin and end inside an item: those two pieces go out as partial rows, at most
 // two a CTA, which chunk_runs_merge joins; the items between are final.
+//
+// 4-bit pages are bound by the instructions that widen them (see chunk_rows4.cu, which takes up to 8 rows):
+// decode of 8 sequences of 65536 to 131072 tokens, 128 / 8 heads, 234 us, 0.55 of the measured copy rate.  Queries in
+// registers for two chunks of 32 dims, four independent products between two into the same scores, both tokens'
+// nibbles of V brought into one byte by four operations for 8 codes: 252 -> 234.
 #include <cuda_runtime.h>
 
 #include "chunk_plan.cuh"
@@ -841,6 +846,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   first_pass_done();
 }
 
+// (4-bit, 16 rows: 5 warps 276 us for the 8 long sequences above where 4 took 252, 3 285)
 // (two sets with bf16 heads of 128: 5 warps a set have 168 registers each, too few: 95 us for 24
 // sequences of 5 rows, 40 / 8 heads, where 3 warps of 233 take 90; the other two fit, fp8 104 -> 90)
 template <int WM, bool SHARED>

@@ -9,7 +9,8 @@
 // of codes, a scale, 32 bytes out), so that 8 lanes (heads of 64: 4) read a row and a warp reads the
 // rows of neighbouring tokens, which lie side by side in the page, and writes whole rows.  Each
 // lane has kAhead rows of its token on their way, K and V of some heads; the places of a
-// block's tokens are found once, a lane each.
+// block's tokens are found once, a lane each.  Measured: 8 histories of 20000 to 65536 4-bit tokens, 8 heads, 342 us
+// (5.8 TB/s, 0.85 of the measured copy rate); blocks of 128 threads 350, of 256 369, of 512 432; 8 rows ahead 430.
 #include <cuda_runtime.h>
 
 #include <algorithm>

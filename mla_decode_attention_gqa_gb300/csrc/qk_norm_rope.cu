@@ -35,7 +35,10 @@ constexpr int kGroups = kWarps * 4;    // heads of a stage
 constexpr int kStages = 5;             // 40 KB for heads of 128
 // CTAs an SM.  bf16: two, a token's rotation held in registers while its heads pass (4096 tokens of
 // 128 + 16 heads 53 us; three CTAs that read it from shared memory for each head 56).  fp8: three,
-// whose warps hide the conversions (6800 tokens of 64 + 16 heads 62 us against 70).
+// whose warps hide the conversions (6800 tokens of 64 + 16 heads 62 us against 70).  4-bit: three as well (8192
+// tokens of 64 + 16 heads 73 us, 0.64 of the measured copy rate, against 75; the instructions of the key and value
+// heads, 16 divisions a lane among them, which products with a reciprocal would do in 4 us less, but on the
+// wrong side of a middle between two codes).
 constexpr int ctas_per_sm(PageFormat pages) { return pages == kPagesBf16 ? 2 : 3; }
 constexpr int kMaxTokens = 64;         // tokens a CTA's run may touch: 8 a warp
 constexpr int kScaleHeads = 16;        // KV heads whose scales wait in shared memory

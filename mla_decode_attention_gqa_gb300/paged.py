@@ -5,8 +5,9 @@ tokens and single decode tokens side by side) and runs the layer's attention: no
 rotation of the new queries and keys and the write of keys and values into their pages
 (``qk_norm_rope_append``), then the attention of every new token over its sequence's pages
 (``attn_chunk_paged``; ``attn_shared_prefix_paged`` where groups of sequences begin with the same
-pages).  ``fp4_pages`` makes an empty 4-bit cache for it.  Nothing is copied to the host and no length is read there, so a step
-can be captured into a CUDA graph and replayed after the arrays of lengths were rewritten.
+pages).  ``fp4_pages`` makes an empty 4-bit cache for it.  Nothing is copied to the host and no
+length is read there, so a step can be captured into a CUDA graph and replayed after the arrays of
+lengths were rewritten.
 """
 
 import torch
