@@ -799,15 +799,29 @@ def attn_chunk_paged(q, k_pages, v_pages, seq_lens, cu_q, block_table, max_q_len
     were."""
     B, T, Hq, Hkv, hd, kv, pg = _check_chunk(q, k_pages, v_pages, seq_lens, cu_q, block_table, k_scale, v_scale,
                                              scale_block)
-    fp4 = _fp4_scales(kv, k_pages, hd, k_scale, v_scale, k_head_scale, v_head_scale)
+    # (host time counts in a decode step: bf16 and fp8 pages pass by what is for 4-bit ones, and what the
+    # calls share is written out here)
+    fp4 = None
+    if kv == SKV_KV_FP4_E2M1 or k_head_scale is not None or v_head_scale is not None:
+        fp4 = _fp4_scales(kv, k_pages, hd, k_scale, v_scale, k_head_scale, v_head_scale)
     d = _described(SkvChunkDesc, _CHUNK_FIELDS, B, T, Hq, Hkv, hd, window, n_sink, max_q_len or 0,
                    1.0 / math.sqrt(hd) if softmax_scale is None else softmax_scale, kv, scale_block,
                    *q.stride()[:2], *k_pages.stride()[:3], *v_pages.stride()[:3])
     dev = q.device
-    out, lse = _chunk_out(out, lse, T, Hq, hd, dev)
+    if out is None:
+        out = torch.empty((T, Hq, hd), dtype=torch.bfloat16, device=dev)
+    else:
+        _out(out, (T, Hq, hd), torch.bfloat16, dev, "out")
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    else:
+        _out(lse, (T, Hq), torch.float32, dev, "lse")
     n = ctypes.c_size_t(0)
     _check(_lib.attn_chunk_paged_workspace_size(d, pg, n))
-    workspace, ws_bytes = _chunk_ws(workspace, n.value, dev)
+    if workspace is None:  # (as _chunk_ws)
+        workspace, ws_bytes = torch.empty(n.value, dtype=torch.uint8, device=dev), n.value
+    else:
+        workspace, ws_bytes = _ws_arg(workspace, n.value, dev)
     if fp4 is not None:
         _check(_lib.attn_chunk_paged_fp4(d, pg, fp4, q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
                                          cu_q.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), lse.data_ptr(),
@@ -962,7 +976,9 @@ def qk_norm_rope_append(q, k, v, k_pages, v_pages, seq_lens, cu_q, block_table, 
     [Hkv], where given).  Returns q_out."""
     B, T, Hq, Hkv, hd, kv, pg = _check_chunk(q, k_pages, v_pages, seq_lens, cu_q, block_table, k_scale, v_scale,
                                              scale_block)
-    fp4 = _fp4_scales(kv, k_pages, hd, k_scale, v_scale, k_head_scale, v_head_scale)
+    fp4 = None
+    if kv == SKV_KV_FP4_E2M1 or k_head_scale is not None or v_head_scale is not None:
+        fp4 = _fp4_scales(kv, k_pages, hd, k_scale, v_scale, k_head_scale, v_head_scale)
     dev = q.device
     i = q.get_device()
     if not i == k.get_device() == v.get_device():
