@@ -476,7 +476,6 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         alpha[r] = fast_exp2(fall[r]);  // 0 when mrun = -inf
         mrun[r] = mnew;
         lrun[r] *= alpha[r];
-        if constexpr (C::FP4) base[r] -= kUp4;
         if constexpr (C::FP8) {
           vs[r] = vsc * up[r];
           const float most = fabsf(vs[r]) * fast_exp2(tmax[r] - base[r]);
@@ -560,7 +559,9 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         for (int nt = 0; nt < TN / 8; ++nt)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
+            // (two steps: a very large maximum less kUp4 would be rounded, and not alike in all warps)
             add_pair(sc[nt][2 * r], sc[nt][2 * r + 1], -base[r]);
+            add_pair(sc[nt][2 * r], sc[nt][2 * r + 1], kUp4);
             const float p0 = fast_exp2(sc[nt][2 * r]), p1 = fast_exp2(sc[nt][2 * r + 1]);
             sum[r] = add_f32x2(sum[r], p0, p1);
             pa[nt >> 1][(nt & 1) * 2 + r] = pack_f16(p0, p1);

@@ -309,7 +309,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
           mul2(o[j][2], o[j][3], a2);
         }
       }
-      const uint64_t less = pack2(kUp - base[0], kUp - base[1]);
+      // (two steps: a very large maximum less kUp would be rounded, and not alike in all warps)
+      const uint64_t less = pack2(-base[0], -base[1]), up = pack2(kUp, kUp);
       uint64_t sum = 0ull;
       uint32_t pt[TN / 16][2];
 #pragma unroll
@@ -317,6 +318,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           add2(st[np][2 * h], st[np][2 * h + 1], less);
+          add2(st[np][2 * h], st[np][2 * h + 1], up);
           const float p0 = fast_exp2(st[np][2 * h]), p1 = fast_exp2(st[np][2 * h + 1]);
           sum = add_f32x2(sum, p0, p1);
           pt[np][h] = movmatrix_t(pack_f16(p0, p1));

@@ -75,6 +75,13 @@ constexpr float kLargeScore = 4194304.0f;
 constexpr float kUp4 = 8.f;
 constexpr float kTileSumLimit4 = 65000.0f;
 
+// What scores are taken against: kUp4 less than their maximum, or the maximum itself where it is so large that
+// the difference is rounded to more.
+__device__ __forceinline__ float below4(float m) {
+  const float r = m - kUp4;
+  return m - r > kUp4 ? m : r;
+}
+
 template <int D_, PageFormat PAGES_, bool SHARED_>
 struct TcCfg {
   static constexpr int D = D_;
@@ -251,7 +258,7 @@ __device__ __noinline__ Redone redo_tile(uint32_t s_col, uint32_t o_col, bool ne
   float mx = -INFINITY;
 #pragma unroll 1
   for (int cc = 0; cc < kTN / 32; ++cc) mx = fmaxf(mx, largest<FP8>(s_col + 32 * cc, cc < 2 ? scale0 : scale1));
-  const float m_new = need ? fmaxf(m, FP4 ? mx - kUp4 : mx) : m;
+  const float m_new = need ? fmaxf(m, FP4 ? below4(mx) : mx) : m;
   const float alpha = (need && l != 0.f) ? fast_exp2(m - m_new) : 1.f;
   if (__any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
@@ -1153,7 +1160,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
           if (__any_sync(0xffffffffu, m_used == -INFINITY)) {
             const float first = first_max<C::FP8>(s_col, m_used, sl[0], sl[1]);
-            m_used = C::FP4 && m_used == -INFINITY ? first - kUp4 : first;
+            m_used = C::FP4 && m_used == -INFINITY ? below4(first) : first;
           }
           uint32_t pk[kTN / 2];
           uint64_t ls[2] = {0ull, 0ull};  // fp32 pair sums of p

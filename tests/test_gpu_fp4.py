@@ -301,6 +301,39 @@ def test_attention_scores_that_rise(max_q_len, step):
     assert ((out.cpu().double() - ro).abs() <= 2.0 ** -8 * (ro.abs() + size) + 2.0 ** -11 * size).all()
 
 
+@pytest.mark.parametrize("max_q_len", [1, 2, None])
+@pytest.mark.parametrize("gain", [2.0 ** 18, 2.0 ** 24, 2.0 ** 27])
+@pytest.mark.parametrize("Hq", [8, 32])
+@pytest.mark.parametrize("n", [64, 900])
+def test_attention_huge_scores(n, gain, max_q_len, Hq):
+    """Scores up to 6 * 2^27 (base 2: past 2^29, where neighbouring numbers are 64 apart): tokens with the largest
+    score share the weight, and nothing overflows.  Rows of several items are joined by their lse, which 32 bits
+    hold to 2^-24 of itself: there (n = 900) a weight is off by 2^-22 |lse| of itself, and where that is more than
+    all of it the output is still a mean of the rows that share the largest score."""
+    c = F.make_case("fp4", (1, 1), (n, min(n, 300)), Hq, 2, 128, seed=19, device=DEV)
+    q = torch.zeros(2, Hq, 128)
+    q[..., 0] = 1.0
+    c["q"] = q.bfloat16().to(DEV)
+    g = torch.Generator().manual_seed(3)
+    c["k_pages"].zero_()
+    c["k_pages"][..., 0] = torch.randint(0, 8, c["k_pages"].shape[:3], generator=g, dtype=torch.uint8).to(DEV)
+    c["k_scale"] = torch.full_like(c["k_scale"].view(torch.uint8), 0x38).view(torch.float8_e4m3fn)  # 1.0
+    c["k_head_scale"] = None
+    F.with_dense(c)
+    c["dense"]["q"] = c["q"]
+    out, lse = skv.attn_chunk_paged(c["q"], c["k_pages"], c["v_pages"], c["seq_lens"], c["cu_q"], c["block_table"],
+                                    max_q_len=max_q_len, softmax_scale=gain, **F.pages_of(c))
+    ro, rl, size = R.attend(c["dense"], scale=gain)
+    # equal scores are equal in 32 bits too; others lie 2^17 and more lower
+    out, lse = out.cpu().double(), lse.cpu().double()
+    assert ((lse - rl).abs() <= 2.0 ** -21 * rl.abs()).all()
+    tol = 2.0 ** -8 * (ro.abs() + size) + 2.0 ** -12 * size
+    if n > 64:
+        most = c["dense"]["v_pages"].abs().amax()
+        tol += torch.clamp(2.0 ** -22 * rl.abs()[..., None] * size, max=2 * most)
+    assert torch.isfinite(out).all() and ((out - ro).abs() <= tol).all()
+
+
 @pytest.mark.parametrize("n", [1, 5, 20])
 def test_attention_cut_in_chunks(n):
     """Few rows over many tokens: on the tensor cores every row's tokens are dealt to several items."""
