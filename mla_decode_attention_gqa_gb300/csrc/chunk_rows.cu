@@ -98,9 +98,9 @@ __device__ __forceinline__ uint32_t half_mask(bool lo, bool hi) {
 template <class C>
 __device__ __forceinline__ void consumers_sync(int set) {  // the consumer warps of a set
   if (C::WM == 1 || set == 0)
-    asm volatile("bar.sync 1, %0;" ::"n"(C::WN * 32) : "memory");
+    named_barrier(1, C::WN * 32);
   else
-    asm volatile("bar.sync 2, %0;" ::"n"(C::WN * 32) : "memory");
+    named_barrier(2, C::WN * 32);
 }
 
 template <class C>

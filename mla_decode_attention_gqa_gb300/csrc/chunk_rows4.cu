@@ -70,7 +70,7 @@ __device__ __forceinline__ void mul2(float& x0, float& x1, uint64_t s) {
 __device__ __forceinline__ void add2(float& x0, float& x1, uint64_t s) {
   asm("{\n\t.reg .b64 a;\n\tmov.b64 a, {%0, %1};\n\tadd.rn.f32x2 a, a, %2;\n\tmov.b64 {%0, %1}, a;\n\t}" : "+f"(x0), "+f"(x1) : "l"(s));
 }
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(WN * 32) : "memory"); }
+__device__ __forceinline__ void consumers_sync() { named_barrier(1, WN * 32); }
 
 template <bool SHARED>
 __global__ void __launch_bounds__(kThreads, kCtas)

@@ -86,7 +86,7 @@ struct GqaCfg {
 };
 
 __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+  named_barrier(id, nthreads);
 }
 
 // Byte offset of (token row, byte in the row) in a K or V tile of the ring.

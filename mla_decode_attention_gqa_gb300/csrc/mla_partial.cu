@@ -48,7 +48,7 @@ static_assert(kDk % 64 == 0, "latent rows are whole 128-byte boxes");
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
 
 __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+  named_barrier(id, nthreads);
 }
 
 __device__ __forceinline__ uint32_t lat_off(uint32_t tok, uint32_t byte) {

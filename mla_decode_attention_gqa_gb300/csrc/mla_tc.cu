@@ -124,6 +124,7 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t smem_addr, uint32_t ran
 }
 
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();  // (as named_barrier)
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 

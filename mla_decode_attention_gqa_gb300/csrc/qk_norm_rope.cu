@@ -76,6 +76,19 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
+// Arrival once `sum`, a sum of squares, is there.  An arrival after the loads in the program alone let the next
+// copy into the stage overtake some of them: in the first launch of a process, whose warps wait for
+// their instructions, 5 of 90 had a head or two of the first stage read after its refill.  The sum is tested
+// against a value that it cannot have, so the arrival needs it, and it needs what was loaded.
+__device__ __forceinline__ void arrive_after(uint64_t* bar, float sum) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %1, 0x80000001;\n\t"
+      "@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(__float_as_uint(sum))
+      : "memory");
+}
+
 // H bf16 values as packed words.
 template <int H>
 __device__ __forceinline__ void load_chunk(const __nv_bfloat16* p, uint32_t* w) {
@@ -229,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(PAGES)) append_kernel(co
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], kWarps);
+      mbar_init(&empty[s], kGroups);
     }
     fence_mbar_init();
   }
@@ -332,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(PAGES)) append_kernel(co
       }
     }
   }
-  asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");  // (the copying warp goes its own way)
+  named_barrier(1, kWarps * 32);  // (the copying warp goes its own way)
 
   Place pl;
   pl.live = 0;
@@ -372,8 +385,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(PAGES)) append_kernel(co
       load_chunk<H>(reinterpret_cast<const __nv_bfloat16*>(row) + c0, r);
       load_chunk<H>(reinterpret_cast<const __nv_bfloat16*>(row) + c1, r + H / 2);
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&empty[s]);
     const bool here = pair0 + static_cast<uint32_t>(n * kGroups + (threadIdx.x >> 3)) < pair1;
     if (here && t != have_t) {  // a new token
       have_t = t;
@@ -392,6 +403,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(PAGES)) append_kernel(co
     float ss = sum_f32x2(acc);
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    // the head is read: the sum that says so holds all its values
+    if (l8 == 0) arrive_after(&empty[s], ss);
     if (!here || !pl.live) continue;  // (no shuffle below)
     if (!is_v) {
       const void* wp = is_q ? a.q_weight : a.k_weight;

@@ -41,6 +41,17 @@ __device__ __forceinline__ unsigned long long globaltimer_ns() {
   return t;
 }
 
+// ----------------------------------------------------------------- barriers
+
+// Barrier `id` among `threads` threads (whole warps).  bar.sync counts a warp as it comes: from one whose
+// lanes have parted, say behind a search of different length in each, the first lanes would answer for
+// the others, whose writes the block then reads too early.  So the warp comes together first, and no
+// kernel uses the instruction but through this function.
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+  __syncwarp();
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
 // ----------------------------------------------------------------- mbarrier
 
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
