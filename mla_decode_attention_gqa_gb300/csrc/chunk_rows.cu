@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 #pragma unroll
             for (int h = 0; h < 4; ++h)
               by[h] = e4m3x2_low_to_f16x2(prmt(
-                  *reinterpret_cast<const uint32_t*>(ksb + (16 * np + 8 * h) * (D / kFp4Block) + 4 * c2), 0u, (tq >> 1) ? 0x31u : 0x20u));
+                  ring_load(ksb + (16 * np + 8 * h) * (D / kFp4Block) + 4 * c2), 0u, (tq >> 1) ? 0x31u : 0x20u));
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const uint32_t qa0[4] = {qv[2 * c].x, qv[2 * c].y, qv[2 * c].z, qv[2 * c].w};
@@ -614,8 +614,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             // dim 4 gq or 4 gq + 2, row gq + 8 the next one
             const uint32_t b00 = pa[kk][0], b01 = pa[kk][2], b10 = pa[kk][1], b11 = pa[kk][3];
             const uint8_t* vsb = smem + s * C::STAGE + 2 * C::TILE + C::SCALES + (16 * kk + 2 * tq) * (D / kFp4Block);
-            const uint4 sa = *reinterpret_cast<const uint4*>(vsb);  // two tokens' scales
-            const uint4 sb = *reinterpret_cast<const uint4*>(vsb + 8 * (D / kFp4Block));
+            const uint4 sa = ring_load_v4(vsb);  // two tokens' scales
+            const uint4 sb = ring_load_v4(vsb + 8 * (D / kFp4Block));
             uint32_t sv[2][4];  // scales of the pairs of tokens, blocks 2 c + (gq >> 2)
             {
               const uint32_t sel = (gq >> 2) ? 0x7351u : 0x6240u;  // (t0, t1) of a word's first, then second block

@@ -170,6 +170,19 @@ __device__ __forceinline__ void ldsm_x2_t(uint32_t addr, uint32_t& r0, uint32_t&
   asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(addr));
 }
 
+// Shared memory that a copy will write again once its readers have arrived: loads that stay where they are
+// written (a plain one may be taken for one of memory that nothing changes, and moved behind the arrival).
+__device__ __forceinline__ uint32_t ring_load(const void* p) {
+  uint32_t r;
+  asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(r) : "r"(smem_u32(p)));
+  return r;
+}
+__device__ __forceinline__ uint4 ring_load_v4(const void* p) {
+  uint4 r;
+  asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(smem_u32(p)));
+  return r;
+}
+
 // Four e4m3 codes (bytes b0..b3 of w) -> two fp16 pairs: lo = (b0, b1), hi = (b2, b3).
 __device__ __forceinline__ void e4m3x4_to_f16x2x2(uint32_t w, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 l, h;\n\t"
