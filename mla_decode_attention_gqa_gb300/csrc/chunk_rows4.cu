@@ -12,9 +12,10 @@
 //   chains of conversions, and they join at the end of an item all at once, each thread summing 4 columns of a
 //   row over the warps.
 //
-// Measured: decode of 64 sequences of 4096 to 16384 tokens, 64 / 8 heads, 160 us (0.64 of the measured copy
-// rate; 203 on the kernel of 16 rows; 8 instructions for 8 codes of K, 13 for 8 of V, at 2.1 a cycle).  5 warps a
-// CTA 171, 6 176, 4 with ten stages 163; rings of their own for K and V, with K's freed after the scores, 171.
+// Measured: decode of 64 sequences of 4096 to 16384 tokens, 64 / 8 heads, 166 us (0.62 of the measured copy
+// rate; 203 on the kernel of 16 rows; 8 instructions for 8 codes of K, 13 for 8 of V, at 2.1 a cycle).  Before the
+// scales' loads were held ahead of the arrival (160): 5 warps a CTA 171, 6 176, 4 with ten stages 163; rings of their
+// own for K and V, with K's freed after the scores, 171.
 #include <cuda_runtime.h>
 
 #include "chunk_plan.cuh"
