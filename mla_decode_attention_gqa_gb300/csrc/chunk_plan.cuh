@@ -73,13 +73,18 @@ __device__ __forceinline__ int chunk_pos_step(const ChunkArgs& a) {
 }
 
 // A row's result over its own tokens (out, lse) joined with the one over its prefix: the weights of the
-// two, and the lse of both.  A part that saw nothing weighs nothing; a NaN on either side stays.
+// two, and the lse of both.  A part that saw nothing weighs nothing; a NaN on either side stays, also beside a
+// part of -inf, where fmaxf would drop it.
 struct ChunkJoin {
   float own, prior, lse;
 };
 __device__ __forceinline__ ChunkJoin chunk_join(float lse, float prior_lse) {
   const float m = fmaxf(lse, prior_lse);
   ChunkJoin j;
+  if (lse != lse || prior_lse != prior_lse) {
+    j.own = j.prior = j.lse = __int_as_float(0x7fc00000);
+    return j;
+  }
   if (m == -INFINITY) {
     j.own = j.prior = 0.f;
     j.lse = -INFINITY;
