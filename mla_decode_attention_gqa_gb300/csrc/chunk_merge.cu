@@ -82,7 +82,7 @@ __device__ __forceinline__ void store_row(const ChunkArgs& a, int64_t row, const
     const ChunkJoin both = chunk_join(lse, __ldcg(a.prior_lse + row));
     inv *= both.own;
     lse = both.lse;
-    if (4 * lane < D && both.prior != 0.f) {
+    if (4 * lane < D) {
       const float4 x = __ldcg(reinterpret_cast<const float4*>(a.prior_o + row * D + 4 * lane));
       y = make_float4(x.x * both.prior, x.y * both.prior, x.z * both.prior, x.w * both.prior);
     }

@@ -74,7 +74,8 @@ __device__ __forceinline__ int chunk_pos_step(const ChunkArgs& a) {
 
 // A row's result over its own tokens (out, lse) joined with the one over its prefix: the weights of the
 // two, and the lse of both.  A part that saw nothing weighs nothing; a NaN on either side stays, also beside a
-// part of -inf, where fmaxf would drop it.
+// part of -inf, where fmaxf would drop it.  (Both rows are multiplied by their weights, zero or not: 0 times a NaN or
+// an infinity, that of a value which a softmax over all tokens would have multiplied by 0 as well, is NaN.)
 struct ChunkJoin {
   float own, prior, lse;
 };

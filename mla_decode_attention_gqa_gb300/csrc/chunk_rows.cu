@@ -750,7 +750,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       float lse0 = some0 ? (M[0] + (__log2f(L[0]) - kUp)) * kLn2 : -INFINITY;
       float lse1 = some1 ? (M[1] + (__log2f(L[1]) - kUp)) * kLn2 : -INFINITY;
       float prior0 = 0.f, prior1 = 0.f;  // weights of the prefix's result
-      if (C::SHARED && direct && pc.skip > 0) {
+      const bool behind = C::SHARED && direct && pc.skip > 0;
+      if (behind) {
         first_pass_done();
         if (v0) {
           const ChunkJoin j = chunk_join(lse0, __ldcg(p.ck.prior_lse + row_a));
@@ -782,8 +783,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
             for (int i = 0; i < 8; ++i) {
               const int d = 8 * (n0 + i) + 2 * tq;
               x[i] = y[i] = make_float2(0.f, 0.f);
-              if (prior0 != 0.f) x[i] = __ldcg(reinterpret_cast<const float2*>(p.ck.prior_o + row_a * D + d));
-              if (prior1 != 0.f) y[i] = __ldcg(reinterpret_cast<const float2*>(p.ck.prior_o + row_b * D + d));
+              if (behind && v0) x[i] = __ldcg(reinterpret_cast<const float2*>(p.ck.prior_o + row_a * D + d));
+              if (behind && v1) y[i] = __ldcg(reinterpret_cast<const float2*>(p.ck.prior_o + row_b * D + d));
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -818,7 +819,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
               for (int c = 0; c < D / 16; ++c) {
                 const int d = C::FP4 ? 32 * (c >> 1) + 4 * gq + 2 * (c & 1) : 16 * c + 2 * gq;
                 x[c] = make_float2(0.f, 0.f);
-                if (prior != 0.f) x[c] = __ldcg(reinterpret_cast<const float2*>(p.ck.prior_o + row * D + d));
+                if (behind && wr) x[c] = __ldcg(reinterpret_cast<const float2*>(p.ck.prior_o + row * D + d));
               }
 #pragma unroll
               for (int c = 0; c < D / 16; ++c) x[c] = make_float2(x[c].x * prior, x[c].y * prior);

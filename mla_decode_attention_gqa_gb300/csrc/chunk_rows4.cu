@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       }
       const float2 by = info[row];
       u.x *= by.x, u.y *= by.x, u.z *= by.x, u.w *= by.x;
-      if (SHARED && by.y != 0.f) {  // (a weight of zero counts nothing, whatever the prefix's row holds)
+      if (behind) {
         u.x = fmaf(before[y].x, by.y, u.x), u.y = fmaf(before[y].y, by.y, u.y);
         u.z = fmaf(before[y].z, by.y, u.z), u.w = fmaf(before[y].w, by.y, u.w);
       }

@@ -344,7 +344,7 @@ __device__ __noinline__ void store_rows(uint32_t o_col, bool has0, bool has1, fl
         const int r = 8 * i + (lane >> 2);
         from[i] = prior_o + __shfl_sync(0xffffffffu, orow, r) * D + (lane & 3) * 4;
         weight[i] = __shfl_sync(0xffffffffu, prior, r);
-        mine[i] = ((write >> r) & 1u) && weight[i] != 0.f;
+        mine[i] = (write >> r) & 1u;
         next[i] = mine[i] ? __ldcg(reinterpret_cast<const float4*>(from[i])) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll 1

@@ -82,3 +82,45 @@ def test_nan_in_the_prefix_of_rows_without_own_tokens(fmt, d, rows):
         c["k_scale"].view(torch.uint8)[page, 1, 5, 2] = 0x7F
         F.with_dense(c)
     same_as_definition(c, *run(c, max_q_len=rows, max_group_rows=rows + 1))
+
+
+@pytest.mark.parametrize("fmt,d", FORMATS)
+@pytest.mark.parametrize("name", ["few rows", "two sets of rows", "tensor cores", "few rows, cut", "tensor cores, cut"])
+@pytest.mark.parametrize("heavy", ["prefix", "own"])
+def test_values_that_are_no_numbers_under_weights_of_zero(fmt, d, name, heavy):
+    """A NaN or an infinity among the values of the part that the other one outweighs by all that fp32 can tell: the
+    row holds no number there, as attn_chunk_paged's, and the dims beside it do."""
+    members, kw = CASES[name]
+    c = shared_case(fmt, d, [(P, members)], 4, 2, seed=23)
+    # one key in four dims for each part: scores +-200 apart whatever the rest of the row adds
+    c["q"].zero_()
+    c["q"][..., :4] = 30.0 * math.sqrt(d) / 4
+    table, L = c["block_table"].cpu(), 64
+    for b, (_, m) in enumerate(members):
+        for i in range(-(-(P + m) // L)):
+            page, up = int(table[b, i]), (i * L < P) == (heavy == "prefix")
+            if fmt == "bf16":
+                c["k_pages"][page, ..., :4] = 4.0 if up else -4.0
+            elif fmt == "fp8":
+                c["k_pages"].view(torch.uint8)[page, ..., :4] = 0x48 if up else 0xC8  # +-4
+                c["k_scale"][page] = 1.0
+            else:
+                c["k_pages"].view(torch.uint8)[page, ..., :2] = 0x66 if up else 0xEE  # +-4
+                c["k_scale"].view(torch.uint8)[page] = 0x38  # 1
+    light = int(table[0, 0 if heavy == "own" else P // L])
+    if fmt == "bf16":
+        c["v_pages"][light, 0, 0, 7] = NAN
+        c["v_pages"][light, 1, 0, 9] = math.inf
+    elif fmt == "fp8":
+        c["v_pages"].view(torch.uint8)[light, :, 0, 7] = 0x7F
+    else:
+        c["v_scale"].view(torch.uint8)[light, :, 0, 0] = 0x7F
+    out, lse = run(c, **kw)
+    want, want_lse = skv.attn_chunk_paged(c["q"], c["k_pages"], c["v_pages"], c["seq_lens"], c["cu_q"], c["block_table"],
+                                          max_q_len=kw.get("max_q_len"), **F.pages_of(c))
+    first = slice(0, members[0][0])
+    n = members[0][0] if heavy == "own" else 1  # the light token is the prefix's first, or the first own one
+    assert not torch.isfinite(want[:n]).all(-1).any(), "attn_chunk_paged"
+    assert torch.equal(torch.isfinite(out[first]), torch.isfinite(want[first]))
+    # five roundings of numbers of the lse's size a side: the score's two, the sum's logarithm added, ln 2, the join
+    assert torch.isfinite(lse).all() and ((lse - want_lse).abs() <= 10 * 2.0 ** -24 * want_lse.abs()).all()
