@@ -528,8 +528,8 @@ typedef struct {
  * NaN among the 16 makes s NaN, and all of them read as NaN.  Everything else as
  * qk_norm_rope_append (the page strides, in bytes, are multiples of 16).
  *
- * attn_chunk_paged_fp4 -- attn_chunk_paged over 4-bit pages (attn_chunk_paged_workspace_size gives
- * its workspace).  Codes times block scales are exact in the products, which run in fp16; the head
+ * attn_chunk_paged_fp4 -- attn_chunk_paged over 4-bit pages of up to 2^30 tokens each
+ * (attn_chunk_paged_workspace_size gives its workspace).  Codes times block scales are exact in the products, which run in fp16; the head
  * scales multiply scores and outputs in fp32.  The softmax weights are rounded once, to fp16 (2^-11 of
  * each) times a power of two: all bits of weights down to 2^-28 (more than 32 rows of a KV head:
  * 2^-22) of the largest so far, something of those down to 2^-38 (2^-33).  Of q what lies below 2^-29 of its

@@ -1098,6 +1098,14 @@ skv_status chunk_desc(const skv_chunk_desc* c, const skv_paged* pg, skv_desc* d,
   return validate_paged(d, pg);
 }
 
+// Pages that attention can address: a copy's coordinates are 32-bit numbers, and those of 4-bit block
+// scales count words, two a token.
+skv_status attended_pages(const skv_desc* d, const skv_paged* pg) {
+  if (page_format(d) == kPagesFp4 && pg->block_len > (1 << 30))
+    return fail(SKV_EINVAL, "attention over 4-bit pages takes pages of 2^30 tokens at most");
+  return SKV_OK;
+}
+
 // Whether two of the rows of d elements at i a + j b (i < n, j < m; b >= d where m > 1) share an element.
 bool rows_overlap(__int128 a, int64_t n, __int128 b, int64_t m, int64_t d) {
   if (a < d) return n > 1;
@@ -1259,7 +1267,7 @@ skv_status chunk_attention(const skv_chunk_desc* desc, const skv_paged* paged, b
                            void* workspace, size_t workspace_bytes, void* stream) {
   skv_desc d;
   skv_status st = chunk_desc(desc, paged, &d, fp4_call);
-  if (st != SKV_OK) return st;
+  if (st != SKV_OK || (st = attended_pages(&d, paged)) != SKV_OK) return st;
   if (fp4_call && page_format(&d) != kPagesFp4) return fail(SKV_EINVAL, "kv_dtype must be SKV_KV_FP4_E2M1");
   if (d.softmax_scale < 0.f) return fail(SKV_EINVAL, "softmax_scale must be positive");
   if (desc->window < 0 || desc->n_sink < 0) return fail(SKV_EINVAL, "window and n_sink must not be negative");
@@ -1308,7 +1316,7 @@ skv_status attn_chunk_paged_workspace_size(const skv_chunk_desc* desc, const skv
   if (!bytes) return fail(SKV_EINVAL, "bytes is NULL");
   skv_desc d;
   skv_status st = chunk_desc(desc, paged, &d, true);
-  if (st != SKV_OK) return st;
+  if (st != SKV_OK || (st = attended_pages(&d, paged)) != SKV_OK) return st;
   ChunkPlan pl;
   if ((st = chunk_plan(&d, d.B, desc->T, desc->max_q_len, &pl)) != SKV_OK) return st;
   *bytes = desc->T == 0 ? 0 : chunk_ws_bytes(pl);
@@ -1336,7 +1344,7 @@ skv_status attn_shared_prefix_paged_workspace_size(const skv_chunk_desc* desc, c
   if (!bytes) return fail(SKV_EINVAL, "bytes is NULL");
   skv_desc d;
   skv_status st = chunk_desc(desc, paged, &d, true);
-  if (st != SKV_OK) return st;
+  if (st != SKV_OK || (st = attended_pages(&d, paged)) != SKV_OK) return st;
   SharedPlan pl;
   if ((st = shared_plan(desc, shared, &d, &pl)) != SKV_OK) return st;
   *bytes = desc->T == 0 ? 0 : pl.bytes();
@@ -1350,7 +1358,7 @@ skv_status attn_shared_prefix_paged(const skv_chunk_desc* desc, const skv_paged*
                                     size_t workspace_bytes, void* stream) {
   skv_desc d;
   skv_status st = chunk_desc(desc, paged, &d, true);
-  if (st != SKV_OK) return st;
+  if (st != SKV_OK || (st = attended_pages(&d, paged)) != SKV_OK) return st;
   if (d.softmax_scale < 0.f) return fail(SKV_EINVAL, "softmax_scale must be positive");
   SharedPlan pl;
   if ((st = shared_plan(desc, shared, &d, &pl)) != SKV_OK) return st;
