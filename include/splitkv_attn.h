@@ -577,8 +577,14 @@ skv_status kv_read_paged(const skv_read_desc* desc, const skv_paged* paged, cons
  * attn_shared_prefix_paged -- attn_chunk_paged for a batch whose sequences begin with the same pages
  * (one system prompt or document, several samples of one prompt): the shared tokens are attended
  * once for all rows of a group of sequences, the rest of each sequence by itself, and the two parts
- * join exactly by their lse.  The result is that of attn_chunk_paged on the same arguments, within its
- * rounding, whatever the groups are; only the time depends on them.
+ * join by their lse.  The result is that of attn_chunk_paged on the same arguments, within its
+ * rounding, whatever the groups are; only the time depends on them.  (The join is exact but for the lse's own
+ * rounding: the weight of each part is off by about |lse| 2^-23 of itself.  A NaN on either side stays.)
+ * It pays where shared pages are read many times for few rows each: decode steps and proposed tokens of
+ * about 2^20 (sequence, KV head, shared token) and more (8 KV heads, one token each: 16 sequences behind 8192
+ * tokens 49 us against 55, 64 behind 32768 114 against 648; 16 behind 2048 45 against 30).  Chunks of some
+ * tens of tokens and more, whose products are the work either way, take as long with attn_chunk_paged (16 chunks of
+ * up to 301 tokens behind 16384: bf16 894 against 942 us, fp8 1376 against 1241, 4-bit 1036 against 1117).
  *   cu_groups    int32 [n_groups + 1], non-decreasing: group j is the sequences cu_groups[j] ..
  *                cu_groups[j + 1] (none allowed); sequences of no group share nothing
  *   prefix_lens  int32 [n_groups]: the first prefix_lens[j] tokens of the group's sequences lie in the
@@ -590,7 +596,8 @@ skv_status kv_read_paged(const skv_read_desc* desc, const skv_paged* paged, cons
  * The arrays are device memory, read by the kernels only, so that one captured graph serves any
  * lengths and groups; the struct itself is read by the host during the call.  All page formats (fp4:
  * the scales of 4-bit pages, else NULL).  desc->window and n_sink must be 0.  Errors otherwise as
- * attn_chunk_paged.
+ * attn_chunk_paged.  The workspace holds, beside both passes' own, the first one's result in fp32: (d + 1) * 4 bytes
+ * for each of the T * Hq rows, whether or not they stand behind a prefix.
  */
 typedef struct {
   int32_t n_groups;

@@ -864,7 +864,8 @@ def attn_shared_prefix_paged(q, k_pages, v_pages, seq_lens, cu_q, block_table, c
     cu_groups int32 [n_groups + 1]: group j is the sequences cu_groups[j] .. cu_groups[j+1];
     prefix_lens int32 [n_groups]: its first prefix_lens[j] tokens lie in the same pages (the same
     entries of block_table), which is the caller's word.  Any groups give the result of attn_chunk_paged,
-    within its rounding; only the time depends on them.  max_q_len and max_group_rows (the most
+    within its rounding; only the time depends on them: it pays for decode steps and proposed tokens
+    from about 2^20 (sequence, KV head, shared token) on, and not for chunks of tens of tokens.  max_q_len and max_group_rows (the most
     new tokens of a sequence, and of a group) choose the kernels.  Returns (out, lse)."""
     B, T, Hq, Hkv, hd, kv, pg = _check_chunk(q, k_pages, v_pages, seq_lens, cu_q, block_table, k_scale, v_scale,
                                              scale_block)

@@ -1249,7 +1249,7 @@ skv_status chunk_pass(const skv_desc& d, const ChunkPlan& pl, PartialParams p, C
 }
 
 // The checks that every attention call makes of its arguments, past the description.
-skv_status chunk_call_checks(const skv_chunk_desc* desc, const skv_desc& d, const skv_fp4_scales* fp4, const void* q,
+skv_status chunk_call_checks(const skv_desc& d, const skv_fp4_scales* fp4, const void* q,
                              const void* k_pages, const void* v_pages, const float* k_scale, const float* v_scale,
                              const int32_t* cu_q, const int32_t* seq_lens, void* out, float* lse) {
   skv_status st;
@@ -1273,7 +1273,7 @@ skv_status chunk_attention(const skv_chunk_desc* desc, const skv_paged* paged, b
   if (desc->window < 0 || desc->n_sink < 0) return fail(SKV_EINVAL, "window and n_sink must not be negative");
   if (desc->n_sink > 0 && desc->window == 0) return fail(SKV_EINVAL, "n_sink needs a window (window > 0)");
   if (desc->T == 0) return SKV_OK;
-  st = chunk_call_checks(desc, d, fp4, q, k_pages, v_pages, k_scale, v_scale, cu_q, seq_lens, out, lse);
+  st = chunk_call_checks(d, fp4, q, k_pages, v_pages, k_scale, v_scale, cu_q, seq_lens, out, lse);
   if (st != SKV_OK) return st;
   ChunkPlan pl;
   if ((st = chunk_plan(&d, d.B, desc->T, desc->max_q_len, &pl)) != SKV_OK) return st;
@@ -1363,7 +1363,7 @@ skv_status attn_shared_prefix_paged(const skv_chunk_desc* desc, const skv_paged*
   SharedPlan pl;
   if ((st = shared_plan(desc, shared, &d, &pl)) != SKV_OK) return st;
   if (desc->T == 0) return SKV_OK;
-  st = chunk_call_checks(desc, d, fp4, q, k_pages, v_pages, k_scale, v_scale, cu_q, seq_lens, out, lse);
+  st = chunk_call_checks(d, fp4, q, k_pages, v_pages, k_scale, v_scale, cu_q, seq_lens, out, lse);
   if (st != SKV_OK) return st;
   if (!shared->cu_groups || !shared->prefix_lens || !aligned(shared->cu_groups, 4) || !aligned(shared->prefix_lens, 4))
     return fail(SKV_EINVAL, "cu_groups and prefix_lens must be non-NULL and 4-byte aligned");

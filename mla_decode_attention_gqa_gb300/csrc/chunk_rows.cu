@@ -22,8 +22,9 @@
 // A run may begin and end inside an item: those two pieces go out as partial rows, at most
 // two a CTA, which chunk_runs_merge joins; the items between are final.
 //
-// 4-bit pages are bound by the instructions that widen them (see chunk_rows4.cu, which takes up to 8 rows):
-// decode of 8 sequences of 65536 to 131072 tokens, 128 / 8 heads, 225 us, 0.57 of the measured copy rate.  Queries in
+// 4-bit pages are bound by the instructions that widen them, at 1.9 a cycle of the 10 warps that 168 registers leave
+// (see chunk_rows4.cu, which takes up to 8 rows): decode of 8 sequences of 65536 to 131072 tokens, 128 / 8 heads,
+// 223 us, 0.57 of the measured copy rate.  Queries in
 // registers for two chunks of 32 dims, four independent products between two into the same scores, both tokens'
 // nibbles of V brought into one byte by four operations for 8 codes: 252 -> 234.
 #include <cuda_runtime.h>

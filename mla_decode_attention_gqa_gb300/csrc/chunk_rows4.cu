@@ -1,9 +1,9 @@
 // Attention of up to 8 rows (new token, head of the group) of a KV head over 4-bit pages: a decode step
 // of groups of 8 heads or fewer (attn_chunk_paged, both passes of attn_shared_prefix_paged).
 //
-// The mathematics and the equal runs of KV tiles are those of chunk_rows.cu.  What differs: 4-bit tiles are
-// bound by the instructions that widen them (1500 a warp and tile with 16 rows, where HBM brings a
-// tile every 390 cycles an SM), so the rows lie on the 8 columns of the products, not on their 16 rows:
+// The mathematics and the equal runs of KV tiles are those of chunk_rows.cu.  What differs: 4-bit tiles take
+// the instructions that widen them (1500 a warp and tile with 16 rows, where HBM brings a tile every 390 cycles
+// an SM), in chains that the warps have to cover, so the rows lie on the 8 columns of the products, not on their 16 rows:
 //   S^T = K Q^T (16 tokens x 8 rows a product) and O^T = V^T P^T (16 dims x 8 rows), half the products, scores and
 //   sums of O of a tile of 16 rows, half of which would be padding;
 //   S^T's fragments, packed in pairs and turned by movmatrix, are P^T's operand;
@@ -13,7 +13,8 @@
 //   row over the warps.
 //
 // Measured: decode of 64 sequences of 4096 to 16384 tokens, 64 / 8 heads, 166 us (0.62 of the measured copy
-// rate; 203 on the kernel of 16 rows; 8 instructions for 8 codes of K, 13 for 8 of V, at 2.1 a cycle).  Before the
+// rate; 203 on the kernel of 16 rows; 8 instructions for 8 codes of K, 13 for 8 of V, at 2.1 a cycle: issue slots
+// and the fullest pipe are half busy, so what bounds it is the latency of the chains beside the instructions' number).  Before the
 // scales' loads were held ahead of the arrival (160): 5 warps a CTA 171, 6 176, 4 with ten stages 163; rings of their
 // own for K and V, with K's freed after the scores, 171.
 #include <cuda_runtime.h>

@@ -12,7 +12,7 @@
 // Bound by HBM: each input is read once and each output written once.  A warp copies the heads by
 // bulk copies into a ring, 32 heads a stage, so that 40 KB a CTA are on their way whatever the
 // others wait for (heads loaded to registers ahead of their use: 68 us for 4096 tokens of
-// 128 + 16 heads, this way 53: 5.7 TB/s of the 6.8 that a copy reaches).  8 lanes take one head, as
+// 128 + 16 heads, this way 54: 5.7 TB/s of the 6.8 that a copy reaches).  8 lanes take one head, as
 // two chunks of d / 16 values that the rotation pairs, so that it needs no exchange between lanes,
 // the sum of squares is three shuffles for four heads, and the arithmetic runs on packed pairs.
 // The chains token -> sequence -> position -> page and table row of all tokens of a CTA's run go
@@ -34,7 +34,7 @@ constexpr int kThreads = kWarps * 32 + 32;
 constexpr int kGroups = kWarps * 4;    // heads of a stage
 constexpr int kStages = 5;             // 40 KB for heads of 128
 // CTAs an SM.  bf16: two, a token's rotation held in registers while its heads pass (4096 tokens of
-// 128 + 16 heads 53 us; three CTAs that read it from shared memory for each head 56).  fp8: three,
+// 128 + 16 heads 54 us; three CTAs that read it from shared memory for each head 56).  fp8: three,
 // whose warps hide the conversions (6800 tokens of 64 + 16 heads 62 us against 70).  4-bit: three as well (8192
 // tokens of 64 + 16 heads 73 us, 0.64 of the measured copy rate, against 75; the instructions of the key and value
 // heads, 16 divisions a lane among them, which products with a reciprocal would do in 4 us less, but on the
@@ -76,10 +76,12 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
-// Arrival once `sum`, a sum of squares, is there.  An arrival after the loads in the program alone let the next
-// copy into the stage overtake some of them: in the first launch of a process, whose warps wait for
-// their instructions, 5 of 90 had a head or two of the first stage read after its refill.  The sum is tested
-// against a value that it cannot have, so the arrival needs it, and it needs what was loaded.
+// Arrival once `sum`, a sum of squares, is there.  One lane arrives for the loads of eight: behind them in the
+// program alone, with neither a __syncwarp() nor a use of what they bring between, the arrival does not say that the
+// other lanes' are done, and the next copy into the stage overtook some of them (in the first launch of a process, whose
+// warps wait for their instructions, 5 of 90 had a head or two of the first stage read after its refill).
+// The sum holds all values of the eight lanes.  It is tested against a value that it cannot have, so the arrival
+// needs it, and it needs what was loaded.
 __device__ __forceinline__ void arrive_after(uint64_t* bar, float sum) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -405,7 +407,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(PAGES)) append_kernel(co
     for (int o = 4; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     // the head is read: the sum that says so holds all its values
     if (l8 == 0) arrive_after(&empty[s], ss);
-    if (!here || !pl.live) continue;  // (no shuffle below)
+    // (shuffles below stay within the 8 lanes of a head, which leave here together or not at all)
+    if (!here || !pl.live) continue;
     if (!is_v) {
       const void* wp = is_q ? a.q_weight : a.k_weight;
       const int64_t w_sh = is_q ? a.q_weight_sh : a.k_weight_sh;

@@ -10,9 +10,11 @@
 // whatever lengths it is given, a sequence's own pass covers the rest.  One block a group, and one for
 // the sequences of no group; a few loads a sequence.
 //
-// Measured: 64 sequences of 100 to 1000 tokens behind one document of 32768, 64 / 8 heads, one token each: 116 us
-// where attn_chunk_paged over the same pages reads the document 64 times (1.3 ms); 58 of them the tensor cores over
-// the prefix (29 tiles a CTA of 1.4 us), 10 its merge, 36 the rest of the sequences.
+// Measured: 64 sequences of 100 to 1000 tokens behind one document of 32768, 64 / 8 heads, one token each: 115 us
+// where attn_chunk_paged over the same pages takes 630 to 670 (more than half of its reads come from L2: HBM alone would
+// take 1290); 58 of the 115 the tensor cores over the prefix (29 tiles a CTA of 1.4 us), 10 its merge, 36 the rest of
+// the sequences.  The five launches and the second pass's starts cost 10 to 30 us, which about 2^20 (sequence, KV head,
+// prefix token) win back: 16 sequences behind 2048 tokens, 8 KV heads, 45 us against 30, behind 8192 49 against 55.
 #include <cuda_runtime.h>
 
 #include <climits>

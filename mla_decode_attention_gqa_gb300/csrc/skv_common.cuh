@@ -170,8 +170,11 @@ __device__ __forceinline__ void ldsm_x2_t(uint32_t addr, uint32_t& r0, uint32_t&
   asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(addr));
 }
 
-// Shared memory that a copy will write again once its readers have arrived: loads that stay where they are
-// written (a plain one may be taken for one of memory that nothing changes, and moved behind the arrival).
+// Shared memory that a copy will write again once its readers have arrived.  Two things keep a warp's loads ahead of
+// that: they stand before the arrival (volatile, as ldmatrix is, so that the compiler leaves them there), and what
+// they brought is there by then, since every word goes into a matrix product (volatile too) that stands before the
+// __syncwarp() ahead of lane 0's arrival, and a product is not issued before its operands are there.  Where no
+// product and no __syncwarp() stands between, the arrival takes what was read as an operand (qk_norm_rope.cu).
 __device__ __forceinline__ uint32_t ring_load(const void* p) {
   uint32_t r;
   asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(r) : "r"(smem_u32(p)));

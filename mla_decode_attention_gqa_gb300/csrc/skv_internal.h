@@ -53,9 +53,9 @@ struct ChunkArgs {
   float* lse;       // fp32 [T][Hq]
   // A shared prefix (attn_shared_prefix_paged; see shared_prefix.cu) runs as two passes.  Over the prefixes
   // a "sequence" is a group: its rows are those of its sequences, its length the prefix, all of which every
-  // row sees (seq_lens: the prefixes; first_row, table_row: device [B]), and the result is fp32.  Over the
-  // rest, sequence b's tokens from skip[b] on (a multiple of kTileN) are attended, and rows with
-  // skip[b] > 0 are joined with the prefix's result (prior_o fp32 [T][Hq][d], prior_lse [T][Hq]).
+  // row sees (seq_lens: the prefixes; group_rows_at, table_row), and the result is fp32.  Over the rest, sequence
+  // b's tokens from skip[b] on (a multiple of kTileN) are attended, and rows with skip[b] > 0 are joined with the
+  // prefix's result (prior_o fp32 [T][Hq][d], prior_lse [T][Hq]).
   int32_t shared;   // one of these passes
   const int32_t* group_rows_at;  // device [B + 1]: first packed row of each group (NULL: cu_q)
   const int32_t* table_row;      // device [B]: block-table row of each group (NULL: b)
